@@ -35,6 +35,12 @@ class GdnError(RuntimeError):
         super().__init__(f"{fn}: {STATUS.get(status, status)}: {detail}")
 
 
+class gdn_kv_cache(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("format", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
 class gdn_dims(ctypes.Structure):
     _fields_ = [("hk", ctypes.c_int32), ("hv", ctypes.c_int32), ("dk", ctypes.c_int32),
                 ("dv", ctypes.c_int32), ("eps", ctypes.c_float)]
@@ -97,6 +103,17 @@ def lib():
             L.gdn_layer_selftest_stages.argtypes = [D, _i32, _i32] + [_p] * 13 + [_i32, _p, _p, _sz, _i32, _i32, _p]
             L.gdn_step.restype = ctypes.c_int
             L.gdn_step.argtypes = [D, _i32] + [_p] * 12 + [_i32, _p, _p]
+            K, _i64 = ctypes.POINTER(gdn_kv_cache), ctypes.c_int64
+            L.gdn_kv_append.restype = ctypes.c_int
+            L.gdn_kv_append.argtypes = ([K, _i32, _i32, _i32, _p, _p, _p, _i64, _i32, _i32] + [_p, _i64] * 3 +
+                                        [_p, _p, _i32, _i32, _i32, _p, _p])
+            L.gdn_kv_attn_workspace_bytes.restype = _sz
+            L.gdn_kv_attn_workspace_bytes.argtypes = [K, _i32, _i32, _i32, _i32]
+            L.gdn_kv_attn.restype = ctypes.c_int
+            L.gdn_kv_attn.argtypes = [K, _i32, _i32, _i32, _p, _p, _p, _i64, _i32, _i32, _p, _i64, ctypes.c_float,
+                                      _p, _p, _sz, _p]
+            L.gdn_draft_verify.restype = ctypes.c_int
+            L.gdn_draft_verify.argtypes = [_i32, _i32, _i32, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p]
             _lib = L
     return _lib
 
@@ -341,3 +358,131 @@ def gdn_scan_selftest_withhold_flag(d: gdn_dims, cu_seqlens, total_tokens, qn, k
         _ptr(workspace, "workspace", torch.uint8), workspace.numel() if workspace is not None else 0,
         _stream(stream))
     _check("gdn_scan_selftest_withhold_flag", st)
+
+
+# ---- attention layers: the 8-bit paged cache, attention over it, the check of drafted tokens ----
+_KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
+_ACT_TYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def kv_cache(k, v, k_scale, v_scale) -> gdn_kv_cache:
+    """One layer's pool of pages: k, v [n_pages, heads, page_tokens, head_dim] of torch.int8 or
+    torch.float8_e4m3fn, k_scale, v_scale float32 [n_pages, heads].  Keeps the tensors alive."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a tensor [n_pages, heads, page_tokens, head_dim]")
+    if k.dtype not in _KV_FORMATS:
+        raise TypeError(f"k must be torch.int8 or torch.float8_e4m3fn, got {k.dtype}")
+    n_pages, heads, page, dim = k.shape
+    f32 = torch.float32
+    c = gdn_kv_cache(heads, dim, page, n_pages, _KV_FORMATS[k.dtype], _ptr(k, "k", k.dtype),
+                     _ptr(v, "v", k.dtype, k.shape), _ptr(k_scale, "k_scale", f32, (n_pages, heads)),
+                     _ptr(v_scale, "v_scale", f32, (n_pages, heads)))
+    c.tensors = (k, v, k_scale, v_scale)
+    return c
+
+
+def _rows16(t, name: str, dtype, T: int, heads: int, dim: int):
+    """Device pointer and token stride of an activation tensor [T, heads, dim] whose token rows are
+    contiguous (a slice of a packed projection will do)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape != (T, heads, dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, heads, dim)}")
+    st, sh, sd = t.stride()
+    row = heads * dim
+    if T and ((sd != 1 and dim > 1) or (sh != dim and heads > 1)):
+        raise ValueError(f"{name}'s token rows must be contiguous")
+    return (t.data_ptr() if T else None), (st if T > 1 else row)
+
+
+def _kv_batch(cu_seqlens, past, page_table):
+    if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous 1-D int32 CUDA tensor")
+    n = cu_seqlens.shape[0] - 1
+    if page_table.dtype != torch.int32 or not page_table.is_cuda or page_table.dim() != 2 or page_table.shape[0] != n:
+        raise ValueError("page_table must be an int32 CUDA tensor [n_seq, max_pages]")
+    width = page_table.shape[1]
+    if width > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table's rows must be contiguous")
+    stride = page_table.stride(0) if n > 1 else width
+    return n, cu_seqlens.data_ptr(), _ptr(past, "past", torch.int32, (n,)), \
+        (page_table.data_ptr() if n and width else None), stride, width
+
+
+def gdn_kv_append(cache: gdn_kv_cache, cu_seqlens, total_tokens, past, page_table, q, k, v, cos, sin,
+                  interleaved: bool, q_out, stream=None):
+    """Store the new tokens' keys and values in the cache, rotated by their positions and quantised to 8
+    bits; rotate q into q_out (both None: keys and values only).  cos, sin [n_pos, rot_dim / 2] or None."""
+    T = int(total_tokens)
+    n, cu, pst, table, table_stride, width = _kv_batch(cu_seqlens, past, page_table)
+    dt, dim = k.dtype, cache.head_dim
+    if dt not in _ACT_TYPES:
+        raise TypeError(f"k must be torch.float16 or torch.bfloat16, got {dt}")
+    kp, ks = _rows16(k, "k", dt, T, cache.heads, dim)
+    vp, vs = _rows16(v, "v", dt, T, cache.heads, dim)
+    hq, qp, qs, qo = 0, None, 0, None
+    if q is not None:
+        hq = q.shape[1]
+        qp, qs = _rows16(q, "q", dt, T, hq, dim)
+        qo = _ptr(q_out, "q_out", dt, (T, hq, dim))
+    n_pos = half = 0
+    cp = sp = None
+    if cos is not None:
+        n_pos, half = cos.shape
+        cp = _ptr(cos, "cos", torch.float32, (n_pos, half))
+        sp = _ptr(sin, "sin", torch.float32, (n_pos, half))
+    st = lib().gdn_kv_append(ctypes.byref(cache), _ACT_TYPES[dt], n, T, cu, pst, table, table_stride, width, hq, qp, qs,
+                             kp, ks, vp, vs, cp, sp, 2 * half, n_pos, 1 if interleaved else 0, qo, _stream(stream))
+    _check("gdn_kv_append", st)
+
+
+def gdn_kv_attn_workspace_bytes(cache: gdn_kv_cache, n_seq: int, total_tokens: int, hq: int, max_pages: int) -> int:
+    return int(lib().gdn_kv_attn_workspace_bytes(ctypes.byref(cache), n_seq, total_tokens, hq, max_pages))
+
+
+def gdn_kv_attn(cache: gdn_kv_cache, cu_seqlens, total_tokens, past, page_table, q, softmax_scale: float, y,
+                workspace, stream=None):
+    """Causal attention of the new tokens over the cache, their own keys and values included."""
+    T = int(total_tokens)
+    n, cu, pst, table, table_stride, width = _kv_batch(cu_seqlens, past, page_table)
+    dt, hq = q.dtype, q.shape[1]
+    if dt not in _ACT_TYPES:
+        raise TypeError(f"q must be torch.float16 or torch.bfloat16, got {dt}")
+    qp, qs = _rows16(q, "q", dt, T, hq, cache.head_dim)
+    wp, wb = None, 0
+    if workspace is not None:
+        wp, wb = _ptr(workspace, "workspace", torch.uint8), workspace.numel()
+    st = lib().gdn_kv_attn(ctypes.byref(cache), _ACT_TYPES[dt], n, T, cu, pst, table, table_stride, width, hq, qp, qs,
+                           softmax_scale, _ptr(y, "y", dt, (T, hq, cache.head_dim)), wp, wb, _stream(stream))
+    _check("gdn_kv_attn", st)
+
+
+def _prob_rows(t, name: str, n: int, rows: int, vocab: int):
+    """Device pointer and row stride of float32 [n, rows, vocab] whose rows are evenly spaced."""
+    if t.dtype != torch.float32 or not t.is_cuda:
+        raise TypeError(f"{name} must be a float32 CUDA tensor")
+    if t.shape != (n, rows, vocab):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, rows, vocab)}")
+    sn, sr, sv = t.stride()
+    stride = sr if rows > 1 else (sn if n > 1 else vocab)
+    if t.numel() and ((sv != 1 and vocab > 1) or (n > 1 and sn != rows * stride)):
+        raise ValueError(f"{name}'s rows must be contiguous and evenly spaced")
+    return (t.data_ptr() if t.numel() else None), stride
+
+
+def gdn_draft_verify(p, q, draft, n_draft, u, accepted, next_token, stream=None):
+    """Check drafted tokens: p [n, d + 1, vocab], q [n, d, vocab] float32, draft int32 [n, d], n_draft int32
+    [n] or None (all d), u float32 [n, d + 1]; writes accepted and next_token, int32 [n]."""
+    n, d1, vocab = p.shape
+    d, i32 = d1 - 1, torch.int32
+    pp, ps = _prob_rows(p, "p", n, d1, vocab)
+    qp, qs = _prob_rows(q, "q", n, d, vocab) if d else (None, vocab)
+    st = lib().gdn_draft_verify(n, d, vocab, pp, ps, qp, qs, _ptr(draft, "draft", i32, (n, d)) if d else None,
+                                _ptr(n_draft, "n_draft", i32, (n,)), _ptr(u, "u", torch.float32, (n, d1)),
+                                _ptr(accepted, "accepted", i32, (n,)), _ptr(next_token, "next_token", i32, (n,)),
+                                _stream(stream))
+    _check("gdn_draft_verify", st)

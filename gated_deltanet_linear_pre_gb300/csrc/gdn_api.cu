@@ -10,23 +10,12 @@
 
 #include "gdn.h"
 #include "gdn_testing.h"
+#include "gdn_host.cuh"
 #include "gdn_internal.cuh"
 
 namespace {
 
 thread_local std::string g_last_error;
-
-gdn_status fail(gdn_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-gdn_status fail(gdn_status s, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return s;
-}
 
 // First CUDA error the library has seen that leaves the context unusable (a fault of an earlier
 // kernel, which every later launch and copy reports), kept for gdn_last_async_error; 0 = none yet.
@@ -59,25 +48,26 @@ void note_cuda_error(cudaError_t e)
     if (context_fatal(e)) g_sticky_error.compare_exchange_strong(none, (int)e);
 }
 
+}  // namespace
+
+namespace gdn {
+namespace host {
+
+gdn_status fail(gdn_status s, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return s;
+}
+
 gdn_status cuda_fail(cudaError_t e, const char* what)
 {
     note_cuda_error(e);
     return fail(GDN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-gdn_status check_dims(const gdn_dims* d)
-{
-    if (!d) return fail(GDN_ERR_INVALID_ARG, "dims is NULL");
-    if (d->hk < 1 || d->hv < 1 || d->hv % d->hk != 0)
-        return fail(GDN_ERR_INVALID_ARG, "need hk >= 1 and hv a multiple of hk (hk=%d hv=%d)", d->hk, d->hv);
-    if (d->dk != gdn::kHeadDim || d->dv != gdn::kHeadDim)
-        return fail(GDN_ERR_UNSUPPORTED, "only dk = dv = 128 is implemented (dk=%d dv=%d)", d->dk, d->dv);
-    if (d->hv > 4096) return fail(GDN_ERR_UNSUPPORTED, "hv=%d above 4096", d->hv);
-    if (!(d->eps > 0.0f) || !std::isfinite(d->eps))
-        return fail(GDN_ERR_INVALID_ARG, "eps must be finite and > 0");
-    return GDN_OK;
 }
 
 gdn_status check_batch(int32_t n_seq, int32_t T, const int32_t* cu)
@@ -89,12 +79,6 @@ gdn_status check_batch(int32_t n_seq, int32_t T, const int32_t* cu)
     if (cu && (reinterpret_cast<uintptr_t>(cu) & 3u)) return fail(GDN_ERR_ALIGNMENT, "cu_seqlens not 4-byte aligned");
     return GDN_OK;
 }
-
-struct Buf {
-    const void* p;
-    size_t bytes;
-    const char* name;
-};
 
 // every non-empty buffer present and 16-byte aligned
 gdn_status check_bufs(const Buf* b, int n)
@@ -128,7 +112,25 @@ gdn_status check_disjoint(const Buf* outs, int n_out, const Buf* ins, int n_in)
     return GDN_OK;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+}  // namespace host
+}  // namespace gdn
+
+using namespace gdn::host;
+
+namespace {
+
+gdn_status check_dims(const gdn_dims* d)
+{
+    if (!d) return fail(GDN_ERR_INVALID_ARG, "dims is NULL");
+    if (d->hk < 1 || d->hv < 1 || d->hv % d->hk != 0)
+        return fail(GDN_ERR_INVALID_ARG, "need hk >= 1 and hv a multiple of hk (hk=%d hv=%d)", d->hk, d->hv);
+    if (d->dk != gdn::kHeadDim || d->dv != gdn::kHeadDim)
+        return fail(GDN_ERR_UNSUPPORTED, "only dk = dv = 128 is implemented (dk=%d dv=%d)", d->dk, d->dv);
+    if (d->hv > 4096) return fail(GDN_ERR_UNSUPPORTED, "hv=%d above 4096", d->hv);
+    if (!(d->eps > 0.0f) || !std::isfinite(d->eps))
+        return fail(GDN_ERR_INVALID_ARG, "eps must be finite and > 0");
+    return GDN_OK;
+}
 
 int channels(const gdn_dims* d) { return 2 * d->hk * d->dk + d->hv * d->dv; }
 

@@ -97,6 +97,56 @@ struct StepParams {
     void* y;                // [n_seq][hv][dv]
 };
 
+// one layer's paged 8-bit cache and the batch that appends to it or reads it
+struct KvBatch {
+    int heads, dim, page, n_pages, format;  // page: tokens per page, a power of two
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int n_seq, T, hq, max_pages;
+    const int32_t* cu_seqlens;
+    const int32_t* past;
+    const int32_t* table;
+    int64_t table_stride;
+    const uint16_t* q;
+    int64_t q_stride;
+    int bf16;  // activations: bf16, else fp16
+};
+
+struct AppendParams : KvBatch {
+    const uint16_t* k_new;
+    const uint16_t* v_new;
+    int64_t k_stride, v_stride;
+    const float* cos;
+    const float* sin;
+    int rot, n_pos, interleaved;
+    uint16_t* q_out;
+};
+
+struct AttnParams : KvBatch {
+    float scale;
+    uint16_t* y;
+    void* workspace;
+};
+
+struct VerifyParams {
+    int n_seq, max_draft, vocab;
+    const float* p;
+    const float* q;
+    int64_t p_stride, q_stride;
+    const int32_t* draft;
+    const int32_t* n_draft;
+    const float* u;
+    int32_t* accepted;
+    int32_t* next;
+};
+
+cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
+size_t kv_attn_workspace_bytes(const KvBatch& b);
+cudaError_t launch_kv_attn(const AttnParams& p, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);
+
 cudaError_t launch_pre(const PreParams& p, cudaStream_t stream);
 cudaError_t launch_step(const StepParams& p, cudaStream_t stream);
 size_t scan_workspace_bytes(int hk, int hv, int n_seq, int T);

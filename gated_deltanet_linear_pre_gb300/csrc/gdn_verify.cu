@@ -1,0 +1,208 @@
+// gdn_verify.cu -- the check of drafted tokens against the target's probabilities.
+//
+// Mathematics.  Leading drafts are accepted while u q(x) < p(x); the token after them is drawn from
+// the normalised positive part of p - q (from p after the last draft) by inverting its running sum at
+// u W.  Weights are whole multiples of 2^-43 of a probability, so their sums are exact in 64 bits and
+// do not depend on the order in which threads form them: the drawn index is the one that a sequential
+// sum would give.  At most 2^19 weights of at most 2^43 stay below 2^63.
+//
+// Layout.  The call reads one row of p and one of q per sequence, once: HBM-bound for large batches and
+// bound by latency for one sequence.  A cluster of 8 CTAs shares a sequence (one CTA per sequence
+// would leave most SMs idle in small batches); each sums its part of the row in segments of 512
+// weights, the CTAs exchange their totals through distributed shared memory, and the one CTA whose part
+// holds the threshold finds its segment from the sums and reads those 512 weights again.
+#include <cooperative_groups.h>
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCtas = 8;          // CTAs a sequence (the portable cluster size)
+constexpr int kSegment = 512;     // weights a segment: 16 a lane
+constexpr int kMaxSegments = ((1 << 19) / kCtas + kSegment - 1) / kSegment;
+
+__device__ __forceinline__ uint64_t weight(float x)
+{
+    // NaN and negative values give 0; the product is exact (a power of two) and below 2^44
+    return (uint64_t)__float2ll_rz(fminf(fmaxf(x, 0.0f), 1.0f) * 8796093022208.0f);
+}
+
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+struct Row {
+    const float* p;
+    const float* q;  // NULL: the weights are p's alone
+    bool vec;        // both rows 16-byte aligned
+    // 4 weights at i .. i + 3 (0 from `end` on)
+    __device__ __forceinline__ void four(int i, int end, uint64_t (&w)[4]) const
+    {
+        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (vec && i + 4 <= end) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
+            a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
+            if (q) {
+                const float4 y = __ldg(reinterpret_cast<const float4*>(q + i));
+                b[0] = y.x; b[1] = y.y; b[2] = y.z; b[3] = y.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < end) {
+                    a[e] = __ldg(p + i + e);
+                    if (q) b[e] = __ldg(q + i + e);
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = weight(q ? __fsub_rn(a[e], b[e]) : a[e]);
+    }
+};
+
+struct Shared {
+    uint64_t seg[kMaxSegments];
+    uint64_t total;
+    int accepted;
+};
+
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) verify_kernel(VerifyParams p)
+{
+    __shared__ Shared sm;
+    cg::cluster_group cluster = cg::this_cluster();
+    pdl_wait();
+    pdl_launch_dependents();
+    const int s = blockIdx.y, rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int count = p.n_draft ? min(max(__ldg(p.n_draft + s), 0), p.max_draft) : p.max_draft;
+    const float* const u = p.u + (size_t)s * (p.max_draft + 1);
+    const float* const p0 = p.p + (size_t)s * (p.max_draft + 1) * p.p_stride;
+    const float* const q0 = p.q + (size_t)s * p.max_draft * p.q_stride;
+    if (warp == 0) {  // every CTA finds the first draft that is not accepted, 32 drafts at a time
+        int accepted = count;
+        for (int i0 = 0; i0 < count; i0 += 32) {
+            const int i = i0 + lane;
+            bool ok = true;
+            if (i < count) {
+                const int x = __ldg(p.draft + (size_t)s * p.max_draft + i);
+                ok = x >= 0 && x < p.vocab &&
+                     __fmul_rn(__ldg(u + i), __ldg(q0 + (size_t)i * p.q_stride + x)) < __ldg(p0 + (size_t)i * p.p_stride + x);
+            }
+            const uint32_t bad = __ballot_sync(0xffffffffu, !ok);
+            if (bad) {
+                accepted = i0 + __ffs(bad) - 1;
+                break;
+            }
+        }
+        if (lane == 0) sm.accepted = accepted;
+    }
+    __syncthreads();
+    const int accepted = sm.accepted;
+    Row row;
+    row.p = p0 + (size_t)accepted * p.p_stride;
+    row.q = accepted < count ? q0 + (size_t)accepted * p.q_stride : nullptr;
+    // this CTA's part of the vocabulary, a whole number of segments
+    const int per = ((p.vocab + kCtas * kSegment - 1) / (kCtas * kSegment)) * kSegment;
+    const int lo = min(rank * per, p.vocab), hi = min(lo + per, p.vocab), segments = (hi - lo + kSegment - 1) / kSegment;
+    int token = -1;
+    uint64_t before = 0, total = 0;
+    for (int pass = 0; pass < 2; ++pass) {  // the second one where the residual has no mass: p itself
+        row.vec = ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) & 15u) == 0;
+        for (int g = warp; g < segments; g += kWarps) {
+            uint64_t sum = 0;
+#pragma unroll
+            for (int j = 0; j < kSegment / 128; ++j) {
+                uint64_t w[4];
+                row.four(lo + g * kSegment + j * 128 + lane * 4, hi, w);
+                sum += (w[0] + w[1]) + (w[2] + w[3]);
+            }
+            sum = warp_sum64(sum);
+            if (lane == 0) sm.seg[g] = sum;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            uint64_t sum = 0;
+            for (int g = lane; g < segments; g += 32) sum += sm.seg[g];
+            sum = warp_sum64(sum);
+            if (lane == 0) sm.total = sum;
+        }
+        cluster.sync();
+        before = total = 0;
+        for (int r = 0; r < kCtas; ++r) {
+            const uint64_t t = *cluster.map_shared_rank(&sm.total, r);
+            if (r < rank) before += t;
+            total += t;
+        }
+        cluster.sync();  // totals read before they are written again, or their CTA leaves
+        if (total != 0 || row.q == nullptr) break;
+        row.q = nullptr;
+    }
+    if (tid == 0 && rank == 0) p.accepted[s] = accepted;
+    if (total == 0) {
+        if (tid == 0 && rank == 0) p.next[s] = -1;
+        return;
+    }
+    // u outside [0, 1] or NaN counts as the nearest of 0 and 1
+    const double x = __dmul_rn((double)fminf(fmaxf(__ldg(u + p.max_draft), 0.0f), 1.0f), __ull2double_rn(total));
+    const uint64_t limit = min((uint64_t)__double2ull_rd(x), total - 1);
+    if (warp != 0 || limit < before || limit >= before + sm.total) return;
+    // the first segment whose running sum exceeds the limit, then the first weight in it
+    uint64_t run = before;
+    int g0 = 0;
+    for (;; g0 += 32) {
+        const uint64_t v = g0 + lane < segments ? sm.seg[g0 + lane] : 0;
+        uint64_t incl = v;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        const uint32_t over = __ballot_sync(0xffffffffu, run + incl > limit);
+        if (over || g0 + 32 >= segments) {
+            const int f = over ? __ffs(over) - 1 : 31;
+            run += __shfl_sync(0xffffffffu, incl - v, f);
+            g0 += f;
+            break;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    for (int j = 0; j < kSegment / 128; ++j) {
+        const int i = lo + g0 * kSegment + j * 128 + lane * 4;
+        uint64_t w[4];
+        row.four(i, hi, w);
+        uint64_t incl = (w[0] + w[1]) + (w[2] + w[3]);
+        const uint64_t v = incl;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        const uint32_t over = __ballot_sync(0xffffffffu, run + incl > limit);
+        if (over) {
+            if (lane == __ffs(over) - 1) {
+                uint64_t at = run + incl - v;
+                int e = 0;
+                while (e < 3 && (at += w[e]) <= limit) ++e;
+                token = i + e;
+                p.next[s] = token;
+            }
+            return;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream)
+{
+    return launch_k(verify_kernel, dim3(kCtas, (unsigned)p.n_seq), dim3(kThreads), 0, stream, true, p);
+}
+
+}  // namespace gdn

@@ -319,6 +319,146 @@ GDN_API gdn_status gdn_step(const gdn_dims* dims, int32_t n_seq, const uint16_t*
                             const float* dt_bias, const float* gamma, const float* S_in, float* S_out,
                             int32_t out_f32, void* y, struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention layers between GDN layers: an 8-bit paged cache of keys and
+ * values, the append that fills it, the attention that reads it, and the
+ * check of drafted tokens.  The pages have no counterpart to these.
+ * ------------------------------------------------------------------------ */
+
+/* activation type of q, k, v and the attention's output */
+typedef enum gdn_dtype { GDN_FP16 = 0, GDN_BF16 = 1 } gdn_dtype;
+
+/* what a cache byte holds: a two's complement integer in [-127, 127], or a
+ * 4-bit-exponent, 3-bit-mantissa float (largest value 448, no infinities) */
+typedef enum gdn_kv_format { GDN_KV_INT8 = 0, GDN_KV_E4M3 = 1 } gdn_kv_format;
+
+/*
+ * gdn_kv_cache -- one layer's pool of pages.  A page holds page_tokens
+ * consecutive positions of one sequence for every kv head; which page holds
+ * which positions is the page table's affair:
+ *   page_table  int32 [n_seq] rows of max_pages entries, page_table_stride
+ *               entries apart: entry j of row s is the pool page of positions
+ *               [j * page_tokens, (j + 1) * page_tokens) of sequence s.
+ * A value is its code times the scale of its (page, head), one scale for k and
+ * one for v.  Scales are 0 (every value 0), a power of two, or NaN (a value
+ * that was not finite was stored: everything read from that page and head is
+ * NaN).  Fresh pages need no initialisation: the call that stores a page's
+ * first position ignores what the page held.
+ */
+typedef struct gdn_kv_cache {
+    int32_t heads;       /* kv heads, 1..1024                              */
+    int32_t head_dim;    /* 64 or 128                                      */
+    int32_t page_tokens; /* 16, 32, 64 or 128                              */
+    int32_t n_pages;     /* pages in the pool                              */
+    int32_t format;      /* gdn_kv_format                                  */
+    uint8_t* k;          /* [n_pages][heads][page_tokens][head_dim]        */
+    uint8_t* v;          /* [n_pages][heads][page_tokens][head_dim]        */
+    float* k_scale;      /* [n_pages][heads]                               */
+    float* v_scale;      /* [n_pages][heads]                               */
+} gdn_kv_cache;
+
+/*
+ * gdn_kv_append -- stores the new tokens' keys and values, rotating keys (and
+ * queries) by their positions on the way.
+ *
+ * Token i of sequence s has position past[s] + i, past[s] being the tokens
+ * that the sequence already holds.
+ *
+ * In:  past     int32 [n_seq] (device)
+ *      q        [T][hq][head_dim], k, v [T][heads][head_dim] of `dtype`; tokens
+ *               are q_stride, k_stride, v_stride elements apart (multiples of
+ *               8: the three may be slices of one packed projection).  q may be
+ *               NULL (hq 0): only k and v are stored.
+ *      cos, sin fp32 [n_pos][rot_dim / 2], the rotation of each position
+ *               (positions past the table take its last row); NULL with
+ *               rot_dim 0 for none.  rot_dim: a multiple of 16 up to head_dim;
+ *               the channels behind it are left as they are.  Channel pairs
+ *               (a, b) are (j, j + rot_dim/2) when interleaved == 0, (2j, 2j + 1)
+ *               when 1, and turn to (a c - b s, b c + a s), each product and sum
+ *               rounded to fp32.
+ * Out: q_out    [T][hq][head_dim] dense, of `dtype`; overlaps no input
+ *      the cache: with x the rotated k (or v) in fp32, a page and head's scale
+ *      becomes the larger of its own and the smallest power of two (at least
+ *      2^-100) not below max|x| / 127 (int8) or max|x| / 448 (e4m3) over its new
+ *      tokens, its own counting as 0 when this call stores the page's first
+ *      position.  New codes are x / scale to nearest even; where the scale grew,
+ *      the codes of the page's earlier positions are divided by the growth and
+ *      rounded again.  The error of a value is therefore below one code step
+ *      of its page, however its page was filled.
+ * A position that is negative, past the table row or whose entry is outside
+ * [0, n_pages) is not stored (its query is still rotated).  Going back to an
+ * earlier length needs no call: append again from there.  Two sequences of
+ * one call must not store into the same page.
+ */
+GDN_API gdn_status gdn_kv_append(const gdn_kv_cache* cache, int32_t dtype, int32_t n_seq,
+                                 int32_t total_tokens, const int32_t* cu_seqlens, const int32_t* past,
+                                 const int32_t* page_table, int64_t page_table_stride,
+                                 int32_t max_pages, int32_t hq, const uint16_t* q, int64_t q_stride,
+                                 const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                 int64_t v_stride, const float* cos, const float* sin,
+                                 int32_t rot_dim, int32_t n_pos, int32_t interleaved,
+                                 uint16_t* q_out, struct CUstream_st* stream);
+
+/* Workspace bytes gdn_kv_attn needs for this batch shape. */
+GDN_API size_t gdn_kv_attn_workspace_bytes(const gdn_kv_cache* cache, int32_t n_seq,
+                                           int32_t total_tokens, int32_t hq, int32_t max_pages);
+
+/*
+ * gdn_kv_attn -- causal attention of the new tokens over the cache (after
+ * their own gdn_kv_append): for query head h and its kv head h / (hq / heads),
+ *   y = sum_j softmax_j(softmax_scale * q . k_j) v_j   over positions
+ *   j <= past[s] + i.
+ * A position whose table entry is outside [0, n_pages), or past the table row,
+ * is not seen; a token that sees none (past[s] + i < 0, say, for an idle slot
+ * of a captured batch) gives zeros.
+ *
+ * In:  q        [T][hq][head_dim] of `dtype`, tokens q_stride elements apart (a
+ *               multiple of 8); hq a multiple of heads, at most 64 per kv head
+ * Out: y        [T][hq][head_dim] dense, of `dtype`
+ * workspace: device scratch of at least gdn_kv_attn_workspace_bytes() bytes;
+ *            contents on entry are ignored.  Calls sharing one must not overlap
+ *            on the GPU.
+ * Scores, softmax statistics and sums are fp32; the softmax weights are
+ * rounded to fp16 for their product with v.  A call may be captured into a CUDA
+ * graph; the lengths in `past` may change between replays.
+ */
+GDN_API gdn_status gdn_kv_attn(const gdn_kv_cache* cache, int32_t dtype, int32_t n_seq,
+                               int32_t total_tokens, const int32_t* cu_seqlens, const int32_t* past,
+                               const int32_t* page_table, int64_t page_table_stride,
+                               int32_t max_pages, int32_t hq, const uint16_t* q, int64_t q_stride,
+                               float softmax_scale, uint16_t* y, void* workspace,
+                               size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * gdn_draft_verify -- accepts or replaces drafted tokens so that the tokens
+ * kept are distributed as the target's.
+ *
+ * Sequence s has n_draft[s] drafts (n_draft NULL: max_draft; clamped to
+ * [0, max_draft]), drawn from the rows q; row i of p is the target's
+ * distribution at draft i, row n_draft[s] the one after the last draft.
+ *   accepted[s] = the number of leading drafts i with u[s][i] q_i(x_i) < p_i(x_i)
+ *                 (fp32 product; a draft outside [0, vocab) is not accepted)
+ *   next[s]     = the token after them: the first index whose running sum of
+ *                 weights exceeds floor(u[s][max_draft] W), W the sum of all.
+ *                 The weight of a token is floor(min(max(x, 0), 1) 2^43), NaN
+ *                 counting as 0, with x = p - q (fp32) at the first draft not
+ *                 accepted, x = p after the last draft.  If W = 0, x = p; if W is
+ *                 still 0, next[s] = -1.
+ * The sums are of whole numbers, so the result does not depend on their order.
+ *
+ * In:  p        fp32 [n_seq][max_draft + 1] rows of vocab, p_stride apart
+ *      q        fp32 [n_seq][max_draft] rows of vocab, q_stride apart
+ *               (NULL when max_draft is 0)
+ *      draft    int32 [n_seq][max_draft];  n_draft int32 [n_seq] or NULL
+ *      u        fp32 [n_seq][max_draft + 1], uniform in [0, 1)
+ * Out: accepted, next  int32 [n_seq]
+ * vocab: 1..2^19.  These arrays need 4-byte alignment only.
+ */
+GDN_API gdn_status gdn_draft_verify(int32_t n_seq, int32_t max_draft, int32_t vocab, const float* p,
+                                    int64_t p_stride, const float* q, int64_t q_stride,
+                                    const int32_t* draft, const int32_t* n_draft, const float* u,
+                                    int32_t* accepted, int32_t* next, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif
