@@ -112,6 +112,8 @@ def lib():
             L.gdn_kv_attn.restype = ctypes.c_int
             L.gdn_kv_attn.argtypes = [K, _i32, _i32, _i32, _p, _p, _p, _i64, _i32, _i32, _p, _i64, ctypes.c_float,
                                       _p, _p, _sz, _p]
+            L.gdn_kv_attn_check.restype = ctypes.c_int
+            L.gdn_kv_attn_check.argtypes = [_p, _p]
             L.gdn_draft_verify.restype = ctypes.c_int
             L.gdn_draft_verify.argtypes = [_i32, _i32, _i32, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p]
             _lib = L
@@ -459,6 +461,12 @@ def gdn_kv_attn(cache: gdn_kv_cache, cu_seqlens, total_tokens, past, page_table,
     st = lib().gdn_kv_attn(ctypes.byref(cache), _ACT_TYPES[dt], n, T, cu, pst, table, table_stride, width, hq, qp, qs,
                            softmax_scale, _ptr(y, "y", dt, (T, hq, cache.head_dim)), wp, wb, _stream(stream))
     _check("gdn_kv_attn", st)
+
+
+def gdn_kv_attn_check(workspace, stream=None):
+    """Raise GdnError (GDN_ERR_TIMEOUT) if the last gdn_kv_attn on this workspace reported an expired wait;
+    synchronises the stream."""
+    _check("gdn_kv_attn_check", lib().gdn_kv_attn_check(_ptr(workspace, "workspace", torch.uint8), _stream(stream)))
 
 
 def _prob_rows(t, name: str, n: int, rows: int, vocab: int):

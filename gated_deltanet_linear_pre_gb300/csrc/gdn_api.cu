@@ -112,6 +112,18 @@ gdn_status check_disjoint(const Buf* outs, int n_out, const Buf* ins, int n_in)
     return GDN_OK;
 }
 
+gdn_status read_failure_word(const void* word, struct CUstream_st* stream)
+{
+    if (!word) return fail(GDN_ERR_INVALID_ARG, "workspace is NULL");
+    uint32_t h = 0;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(&h, word, sizeof h, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "reading the failure record");
+    if (h) return fail(GDN_ERR_TIMEOUT, "a bounded wait in the kernels expired (record 0x%x); outputs are invalid", h);
+    return GDN_OK;
+}
+
 }  // namespace host
 }  // namespace gdn
 
@@ -270,19 +282,6 @@ gdn_status run_scan(const gdn::ScanParams& p, struct CUstream_st* stream)
     }
     cudaError_t e = gdn::launch_scan(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_scan launch");
-}
-
-// the scan's failure record: the first 4 bytes of its workspace
-gdn_status read_failure_word(const void* word, struct CUstream_st* stream)
-{
-    if (!word) return fail(GDN_ERR_INVALID_ARG, "workspace is NULL");
-    uint32_t h = 0;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemcpyAsync(&h, word, sizeof h, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return cuda_fail(e, "reading the scan's failure record");
-    if (h) return fail(GDN_ERR_TIMEOUT, "a bounded wait in the scan kernels expired (record 0x%x); outputs are invalid", h);
-    return GDN_OK;
 }
 
 // offset of the scan workspace inside a gdn_layer workspace (the stage tensors vc, o, glog and beta

@@ -32,5 +32,8 @@ bool overlap(const Buf& a, const Buf& b);
 // no output may overlap another output or any input
 gdn_status check_disjoint(const Buf* outs, int n_out, const Buf* ins, int n_in);
 
+// a workspace's failure record, its first 4 bytes (synchronises the stream)
+gdn_status read_failure_word(const void* word, struct CUstream_st* stream);
+
 }  // namespace host
 }  // namespace gdn

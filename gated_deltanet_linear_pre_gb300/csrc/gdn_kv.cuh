@@ -13,7 +13,7 @@ namespace gdn {
 // Largest s in [0, n) with base(s) <= x, for a non-decreasing base with base(0) <= x; a whole warp
 // searches 32-way, so a batch of 1024 sequences takes two dependent loads instead of ten.
 template <typename F>
-__device__ __forceinline__ int warp_find(int n, int x, F base)
+__device__ __forceinline__ int warp_find(int n, int64_t x, F base)
 {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = n;

@@ -140,13 +140,18 @@ gdn_status gdn_kv_attn(const gdn_kv_cache* cache, int32_t dtype, int32_t n_seq, 
     if ((st = check_bufs(ins, 1)) != GDN_OK) return st;
     if ((st = check_bufs(outs, 2)) != GDN_OK) return st;
     if ((st = check_disjoint(outs, 2, ins, 5)) != GDN_OK) return st;
-    if (T == 0) return GDN_OK;
+    if (T == 0) {  // nothing to compute; a failure record still starts clean
+        cudaError_t e = workspace && workspace_bytes >= 4 ? cudaMemsetAsync(workspace, 0, 4, reinterpret_cast<cudaStream_t>(stream)) : cudaSuccess;
+        return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_kv_attn workspace clear");
+    }
     gdn::AttnParams p{};
     fill(p, cache, dtype, n_seq, T, cu_seqlens, past, page_table, page_table_stride, max_pages, hq, q, q_stride);
     p.scale = softmax_scale; p.y = y; p.workspace = workspace;
     cudaError_t e = gdn::launch_kv_attn(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_kv_attn launch");
 }
+
+gdn_status gdn_kv_attn_check(const void* workspace, struct CUstream_st* stream) { return read_failure_word(workspace, stream); }
 
 gdn_status gdn_draft_verify(int32_t n_seq, int32_t max_draft, int32_t vocab, const float* p, int64_t p_stride, const float* q,
                             int64_t q_stride, const int32_t* draft, const int32_t* n_draft, const float* u, int32_t* accepted,

@@ -1,22 +1,33 @@
-// gdn_kv_attn.cuh -- what the attention's kernels share: the split of a ragged
-// batch into equal shares of work, and the workspace.
+// gdn_kv_attn.cuh -- what the attention's kernels share: which sequences go which
+// way, the split of a ragged batch into equal shares of work, and the workspace.
 //
-// Work is counted in key tiles: a unit is (sequence, kv head, group of query rows) and costs the
-// sequence's tiles.  The units of a batch, end to end, are cut into equal ranges, one per worker (CTA),
-// so that one long sequence and many short ones load the GPU alike, whatever the lengths; the cuts come
-// from the device's own lengths and change with them between replays of a captured call.  A unit that
-// lies in one range is finished by its worker; one that is cut leaves a partial (maximum, sum, output)
-// per worker, and a last kernel joins them in order.
+// Two ways through the cache.  Sequences with few query rows (tokens times query heads per kv head, up
+// to kLongRows) go to the step kernel, which reads the codes themselves; the others are long: their
+// cache is unpacked once to fp16 operand images, which the prompt kernel then reads for every 256 query
+// rows.  The choice is made per sequence on the device, so one call serves a batch that mixes prompts
+// and single tokens, and a captured call follows its lengths.
+//
+// Work is counted in key tiles: a unit is (sequence, kv head, group of query rows) and costs the tiles
+// that it sees.  The units of a batch, end to end, are cut into equal ranges, one per worker (CTA), so
+// that one long sequence and many short ones load the GPU alike.  A unit that lies in one range is
+// finished by its worker; one that is cut leaves a partial (maximum, sum, output) per worker, and a last
+// kernel joins them in the order of the ranges.
 #pragma once
 
 #include "gdn_kv.cuh"
 
 namespace gdn {
 
-constexpr int kStepThreads = 256;
-constexpr int kSub = 16;              // positions of one step tile (a page holds whole ones)
-constexpr int kStepMaxRows = 32;      // query rows of a step unit, at most
+constexpr int kSub = 16;               // positions of a step tile (a page holds whole ones)
+constexpr int kStepMaxRows = 32;       // query rows of a step unit, at most
 constexpr int kStepMaxWorkers = 512;
+constexpr int kKeys = 128;             // positions of a prompt tile
+constexpr int kUnitRows = 256;         // query rows of a prompt unit: two halves of 128
+constexpr int kPromptMaxWorkers = 160;
+constexpr int kLongRows = 64;
+constexpr size_t kImageCap = (size_t)2 << 30;  // bytes of images; sequences past it take the step kernel
+
+constexpr uint32_t kAttnTimeout = 1u;  // failure record: a bounded wait expired
 
 // a sequence as the attention sees it
 struct SeqView {
@@ -34,42 +45,123 @@ __device__ __forceinline__ SeqView seq_view(const KvBatch& p, int s)
     return v;
 }
 
-// the cut of `total` tiles into `workers` ranges: start of range w, and the range that holds tile x
-__host__ __device__ __forceinline__ int64_t cut_start(int64_t total, int workers, int w) { return total * w / workers; }
-__host__ __device__ __forceinline__ int cut_of(int64_t total, int workers, int64_t x) { return (int)(((x + 1) * workers - 1) / total); }
+// where the range of a worker begins: tile j0 of a unit of `tiles`
+struct Cut {
+    int s, head, unit, j0, tiles;  // unit: the step unit's first row, the prompt unit's index
+};
 
-// workspace: header, first tile of every sequence, partial statistics and outputs (two per worker: the
-// range's first unit and its last)
-struct StepHeader {
-    int64_t total;
-    int workers;
+struct AttnHeader {
+    uint32_t error;
+    int step_workers, prompt_workers;
+    int64_t step_total, prompt_total;
 };
-constexpr size_t kStepHeader = 256;
-struct StepSpace {
-    StepHeader* head;
-    int64_t* base;  // [n_seq]
-    float2* stat;   // [2 * kStepMaxWorkers][kStepMaxRows]: maximum (base 2), sum
-    float* out;     // [2 * kStepMaxWorkers][kStepMaxRows][dim]
+
+// the workspace's parts (kv_attn.cu lays them out)
+struct AttnSpace {
+    AttnHeader* head;
+    Cut* step_cut;         // [kStepMaxWorkers]
+    float2* step_stat;     // [2 kStepMaxWorkers][kStepMaxRows]: maximum (base 2), sum; two per worker, the
+    float* step_out;       //   range's first unit and its last;  [..][kStepMaxRows][dim]
+    // the rest is there only where the batch may hold a long sequence (image_tiles > 0)
+    int* ok;               // [n_seq] a candidate whose images are written
+    int* image_base;       // [n_seq] its first image tile
+    float2* norm;          // [image_tiles][heads], at the sequence's first tile: largest k and v scale
+    Cut* prompt_cut;       // [kPromptMaxWorkers]
+    float2* prompt_stat;   // [2 kPromptMaxWorkers][kUnitRows]
+    float4* prompt_out;    // [2 kPromptMaxWorkers][dim / 4][kUnitRows]
+    unsigned char* images; // [image_tiles][heads][2]: K and V operand images of 128 positions
+    int image_tiles;
+    int most_rows;         // sequences with more query rows are candidates for the prompt way
 };
-__host__ __device__ __forceinline__ size_t step_base_bytes(int n_seq) { return ((size_t)n_seq * 8 + 255) & ~size_t(255); }
-__host__ __device__ __forceinline__ StepSpace step_space(void* ws, int n_seq)
+
+__device__ __forceinline__ bool candidate(const KvBatch& p, const AttnSpace& a, const SeqView& v)
 {
-    unsigned char* w = static_cast<unsigned char*>(ws);
-    StepSpace s;
-    s.head = reinterpret_cast<StepHeader*>(w);
-    s.base = reinterpret_cast<int64_t*>(w + kStepHeader);
-    s.stat = reinterpret_cast<float2*>(w + kStepHeader + step_base_bytes(n_seq));
-    s.out = reinterpret_cast<float*>(s.stat + 2 * kStepMaxWorkers * kStepMaxRows);
-    return s;
+    // (negative positions and positions past the table take the step kernel, which sees to them)
+    return (int64_t)v.n * (p.hq / p.heads) > a.most_rows && v.first >= 0 && v.first + v.n <= p.max_pages * p.page;
 }
-__host__ __device__ __forceinline__ size_t step_space_bytes(int n_seq, int dim)
+__device__ __forceinline__ bool is_long(const KvBatch& p, const AttnSpace& a, int s, const SeqView& v) { return candidate(p, a, v) && a.ok[s]; }
+
+// the cut of `total` tiles into `workers` ranges: start of range w, and the range that holds tile x
+__device__ __forceinline__ int64_t cut_start(int64_t total, int workers, int w) { return total * w / workers; }
+__device__ __forceinline__ int cut_of(int64_t total, int workers, int64_t x) { return (int)(((x + 1) * workers - 1) / total); }
+
+// ---- where a worker's range begins -------------------------------------------------
+template <int THREADS>
+struct ScanSmem {
+    int64_t chunk[256];  // sums over every THREADS sequences (at most 65535 of them)
+    int64_t prefix[THREADS + 1], warp_sum[THREADS / 32];
+    int found;
+};
+
+// exclusive scan over the block; `total` for all
+template <int THREADS>
+__device__ __forceinline__ int64_t block_scan(int64_t mine, ScanSmem<THREADS>& sm, int64_t& total)
 {
-    return kStepHeader + step_base_bytes(n_seq) + (size_t)2 * kStepMaxWorkers * kStepMaxRows * (8 + (size_t)dim * 4);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t v = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += o;
+    }
+    __syncthreads();  // warp_sum free
+    if (lane == 31) sm.warp_sum[warp] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) v += sm.warp_sum[w];
+        total += sm.warp_sum[w];
+    }
+    return v - mine;
+}
+
+// the sum of weight(s) over all sequences
+template <int THREADS, typename F>
+__device__ __forceinline__ int64_t scan_total(int n_seq, F weight, ScanSmem<THREADS>& sm)
+{
+    int64_t total = 0;
+    for (int c = 0; c * THREADS < n_seq; ++c) {
+        const int s = c * THREADS + threadIdx.x;
+        int64_t sum;
+        const int64_t before = block_scan<THREADS>(s < n_seq ? weight(s) : 0, sm, sum);
+        if (c == 0) sm.prefix[threadIdx.x] = before;  // a single chunk needs no second look
+        if (threadIdx.x == 0) sm.chunk[c] = sum;
+        total += sum;
+    }
+    return total;
+}
+
+// the sequence that holds x (0 <= x < scan_total's result), and the sum before it
+template <int THREADS, typename F>
+__device__ __forceinline__ int scan_find(int n_seq, int64_t x, F weight, ScanSmem<THREADS>& sm, int64_t& before)
+{
+    __syncthreads();
+    const int chunks = (n_seq + THREADS - 1) / THREADS;
+    int64_t base = 0;
+    int c = 0;
+    while (c + 1 < chunks && base + sm.chunk[c] <= x) base += sm.chunk[c++];
+    if (c > 0) {
+        const int s = c * THREADS + threadIdx.x;
+        int64_t sum;
+        const int64_t b = block_scan<THREADS>(s < n_seq ? weight(s) : 0, sm, sum);
+        sm.prefix[threadIdx.x] = b;
+    }
+    if (threadIdx.x == 0) {
+        sm.prefix[THREADS] = sm.chunk[c];
+        sm.found = 0;
+    }
+    __syncthreads();
+    if (base + sm.prefix[threadIdx.x] <= x && x < base + sm.prefix[threadIdx.x + 1]) sm.found = threadIdx.x;
+    __syncthreads();
+    before = base + sm.prefix[sm.found];
+    return c * THREADS + sm.found;
 }
 
 // ---- 8-bit codes to fp16 ------------------------------------------------------------
-// Two codes, bytes LO of y, to a pair of fp16 values.  Both conversions are exact and give finite
-// values for every byte, so what lies behind a sequence's end in its last page can do no harm:
+// Two codes, bytes 0 and 1 (HIGH: 2 and 3) of y, to a pair of fp16 values.  Both conversions are exact
+// and give finite values for every byte, so what lies behind a sequence's end in its last page can do no
+// harm:
 //   int8: 1024 + (code + 128) assembled as fp16 bits, less 1152;
 //   e4m3: the sign, exponent and mantissa bits moved to their fp16 places, which is the value / 256
 //         (subnormals included); the byte pattern of NaN, which no append writes, reads as 480 / 256.
@@ -87,5 +179,22 @@ __device__ __forceinline__ uint32_t codes2(uint32_t y)
 
 template <bool E4M3>
 constexpr float kCodeUnit = E4M3 ? 256.0f : 1.0f;  // value of a converted code of 1.0
+
+// Power of two that brings a query row (the bits of its largest magnitude) to [2^14, 2^15), and its
+// inverse: fp16 then holds a row of either type, exactly for fp16 and, less what is 2^-29 of the row's
+// largest, for bf16.  Rows of zeros, infinities or NaN stay as they are.
+__device__ __forceinline__ void row_unit(uint32_t amax, float& mul, float& back)
+{
+    const int e = (int)(amax >> 23);
+    const int up = amax != 0 && e < 255 ? 141 - max(e, 41) : 0;
+    mul = __uint_as_float((uint32_t)(127 + up) << 23);
+    back = __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// the kernels' launches (gdn_kv_step.cu, gdn_kv_prompt.cu)
+cudaError_t launch_kv_step(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream);
+cudaError_t launch_kv_prompt(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream);
 
 }  // namespace gdn

@@ -1,0 +1,687 @@
+// gdn_kv_prompt.cu -- attention of many query rows over the 8-bit paged cache, on
+// the tcgen05 tensor cores.
+//
+// Mathematics.  One pass over the keys per 128 query rows with the softmax's running maximum and sum:
+// S = Q K^T and O += P V are 128 x 128 (x head_dim) products with fp32 accumulators in TMEM; a thread
+// owns a query row.  P = 2^(x - m + 7), x = scale log2(e) q.k; the reference m moves, and O and l are
+// rescaled, only where a tile's maximum passes it by 8 (a factor of 256): P stays below 2^15, and what is
+// lost to fp16's smallest step is 2^-31 of the largest weight.  Weights are rounded to fp16 (11 bits),
+// sums and statistics are fp32.  Queries are scaled to fp16 by a power of two per row (row_unit).
+//
+// Layout.  The tensor cores read 16-bit operands from shared memory, so the codes have to be unpacked
+// somewhere.  Done by every CTA for itself, a 128-position tile would cost each about as many issue slots
+// as a third of its softmax; instead one kernel unpacks each long sequence's cache once into images, in
+// the no-swizzle core-matrix order, that a single bulk copy brings in: 4 bytes moved per code byte, a few
+// per cent of a prompt's time.  An image holds code * (page scale / largest scale of the sequence and
+// head) * 2^kUp, exact for pages whose scale is at least 2^-15 (e4m3) or 2^-24 (int8) of the largest after
+// the shift; the largest scale itself goes into the scores' unit and the outputs'.
+//
+// A CTA (320 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
+// other's products: warps 0-3 and 4-7 the rows, warp 8 the copies, warp 9 the products.  TMEM: S (later
+// the fp16 P in its place) and O of each half, 512 columns at head_dim 128.  Rows are (token, query head
+// of the kv head): floor(128 / group) tokens a half.
+#include "gdn_kv_attn.cuh"
+#include "umma.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kImageThreads = 256;
+constexpr int kThreads = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr float kWeightShift = 7.0f;
+constexpr float kLazy = 8.0f;
+
+// images hold code2 values times 2^kUp: up to 127 x 2^8 and 1.75 x 2^14
+template <bool E4M3> constexpr float kUp = E4M3 ? 16384.0f : 256.0f;
+template <bool E4M3> constexpr float kImageUnit = kCodeUnit<E4M3> / kUp<E4M3>;  // value of an image's 1.0 per unit scale
+
+template <int D> constexpr uint32_t kTileBytes = kKeys * D * 2;
+
+// byte offset of (position, channels 8 c8 .. + 7) in an image: core matrices of 8 positions x 16 bytes
+template <int D>
+__device__ __forceinline__ int image_off(int pos, int c8) { return ((pos >> 3) * (D / 8) + c8) * 128 + (pos & 7) * 16; }
+
+// ---- unpacking ------------------------------------------------------------------------
+__device__ __forceinline__ int key_tiles(int kv) { return (kv + kKeys - 1) / kKeys; }
+
+template <bool E4M3>
+__device__ __forceinline__ uint4 unpack8(uint2 w, __half2 f)
+{
+    uint32_t r[4] = {codes2<E4M3, false>(w.x), codes2<E4M3, true>(w.x), codes2<E4M3, false>(w.y), codes2<E4M3, true>(w.y)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&r[i]), f);
+        r[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Each block takes an equal range of the (tile, kv head) items of all candidates, head fastest.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kImageThreads) kv_image_kernel(AttnParams p, AttnSpace a)
+{
+    __shared__ ScanSmem<kImageThreads> scan;
+    __shared__ float top_k[kImageThreads / 32], top_v[kImageThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, shift = 31 - __clz(p.page);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.x == 0 && tid == 0) a.head->error = 0u;
+    auto weight = [&](int s) {
+        const SeqView v = seq_view(p, s);
+        return candidate(p, a, v) ? (int64_t)key_tiles(v.kv) : 0;
+    };
+    const int64_t tiles = scan_total<kImageThreads>(p.n_seq, weight, scan), items = tiles * p.heads;
+    const int64_t lo = cut_start(items, gridDim.x, blockIdx.x), hi = cut_start(items, gridDim.x, blockIdx.x + 1);
+    if (lo >= hi) return;
+    int64_t before;
+    int s = scan_find<kImageThreads>(p.n_seq, lo / p.heads, weight, scan, before);
+    int64_t at = lo / p.heads - before;  // tile within the sequence
+    int head = (int)(lo % p.heads);
+    for (int64_t x = lo; x < hi && s < p.n_seq;) {
+        const SeqView v = seq_view(p, s);
+        const int n = candidate(p, a, v) ? key_tiles(v.kv) : 0;
+        if (at >= n) {
+            before += n;
+            at = 0;
+            ++s;
+            continue;
+        }
+        // the sequence's images fit, every page is there; its largest scales (NaN ones apart)
+        const int pages = (v.kv + p.page - 1) >> shift;
+        float mk = 0.0f, mv = 0.0f;
+        bool there = before + n <= a.image_tiles;
+        for (int i = tid; i < pages; i += kImageThreads) {
+            const int page = page_at(p, s, i);
+            if (page < 0) {
+                there = false;
+            } else {
+                mk = fmaxf(mk, __ldg(p.k_scale + (size_t)page * p.heads + head));
+                mv = fmaxf(mv, __ldg(p.v_scale + (size_t)page * p.heads + head));
+            }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
+            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
+        }
+        if (lane == 0) {
+            top_k[warp] = mk;
+            top_v[warp] = mv;
+        }
+        there = __syncthreads_and(there);
+#pragma unroll
+        for (int w = 0; w < kImageThreads / 32; ++w) {
+            mk = fmaxf(mk, top_k[w]);
+            mv = fmaxf(mv, top_v[w]);
+        }
+        if (at == 0 && tid == 0) {
+            if (head == 0) {
+                a.ok[s] = there;
+                a.image_base[s] = there ? (int)before : 0;
+            }
+            if (there) a.norm[(size_t)before * p.heads + head] = make_float2(mk, mv);
+        }
+        if (there) {
+            unsigned char* const img = a.images + ((size_t)(before + at) * p.heads + head) * (2 * kTileBytes<D>);
+            // a lane's place: 8 positions x 4 groups of 8 channels a warp, 512 contiguous image bytes
+            for (int i = tid; i < kKeys * (D / 8); i += kImageThreads) {
+                const int pos = ((i >> 5) / (D / 32)) * 8 + (i & 7), c8 = ((i >> 5) % (D / 32)) * 4 + ((i >> 3) & 3);
+                const int at_pos = (int)at * kKeys + pos;
+                uint4 wk = make_uint4(0u, 0u, 0u, 0u), wv = wk;
+                if (at_pos < v.kv) {
+                    const size_t row = (size_t)page_at(p, s, at_pos >> shift) * p.heads + head;
+                    const size_t src = (row * p.page + (at_pos & (p.page - 1))) * D + 8 * c8;
+                    const float ks = __ldg(p.k_scale + row), vs = __ldg(p.v_scale + row);
+                    // (a scale of 0 may meet a largest one of 0; NaN scales stay NaN)
+                    const float fk = ks == 0.0f ? 0.0f : ks / mk * kUp<E4M3>, fv = vs == 0.0f ? 0.0f : vs / mv * kUp<E4M3>;
+                    wk = unpack8<E4M3>(__ldg(reinterpret_cast<const uint2*>(p.k + src)), __float2half2_rn(fk));
+                    wv = unpack8<E4M3>(__ldg(reinterpret_cast<const uint2*>(p.v + src)), __float2half2_rn(fv));
+                }
+                *reinterpret_cast<uint4*>(img + image_off<D>(pos, c8)) = wk;
+                *reinterpret_cast<uint4*>(img + kTileBytes<D> + image_off<D>(pos, c8)) = wv;
+            }
+        }
+        __syncthreads();  // top_k, top_v read
+        ++x;
+        if (++head == p.heads) {
+            head = 0;
+            ++at;
+        }
+    }
+}
+
+// ---- the units of long sequences -----------------------------------------------------
+// sum over i < n of floor((a i + b) / m), by exchanging the roles of a and m as in Euclid's algorithm
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b)
+{
+    int64_t sum = 0;
+    while (n > 0) {
+        sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const int64_t y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const int64_t t = a;
+        a = m;
+        m = t;
+    }
+    return sum;
+}
+
+// tokens of a unit: two halves of floor(128 / group)
+__device__ __forceinline__ int half_tokens(int group) { return (kUnitRows / 2) / group; }
+// key tiles that units before unit i of a (sequence, head) see together (none of them the last one)
+__device__ __forceinline__ int64_t unit_prefix(const SeqView& v, int span, int i) { return floor_sum(i, kKeys, span, (int64_t)v.first + span + kKeys - 1); }
+__device__ __forceinline__ int unit_tiles(const SeqView& v, int span, int i) { return (v.first + min((i + 1) * span, v.n) + kKeys - 1) / kKeys; }
+
+// A worker's units in order; every role of the CTA walks the same ones.
+struct Walk {
+    const AttnParams& p;
+    const AttnSpace& a;
+    int span;                 // tokens a unit
+    int s, head, i, units;    // sequence, kv head, unit
+    int j0, j1, tiles;        // this worker's tiles of the unit
+    int64_t left;             // tiles of the range from here on
+    int64_t image;            // image tile of the sequence's first positions
+    SeqView v;
+    bool first;
+
+    __device__ __forceinline__ Walk(const AttnParams& p_, const AttnSpace& a_, const Cut& c, int64_t tiles_) : p(p_), a(a_), left(tiles_), first(true)
+    {
+        span = 2 * half_tokens(p.hq / p.heads);
+        s = c.s;
+        head = c.head;
+        i = c.unit;
+        j0 = c.j0;
+        enter();
+        here();
+    }
+    __device__ __forceinline__ void enter()
+    {
+        v = seq_view(p, s);
+        units = (v.n + span - 1) / span;
+        image = a.image_base[s];
+    }
+    __device__ __forceinline__ void here()
+    {
+        tiles = unit_tiles(v, span, i);
+        j1 = (int)min((int64_t)tiles, j0 + left);
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next()
+    {
+        left -= j1 - j0;
+        first = false;
+        j0 = 0;
+        if (left <= 0) return;
+        if (++i == units) {
+            i = 0;
+            if (++head == p.heads) {
+                head = 0;
+                do {
+                    if (++s >= p.n_seq) {
+                        left = 0;
+                        return;
+                    }
+                } while (!is_long(p, a, s, seq_view(p, s)));
+                enter();
+            }
+        }
+        here();
+    }
+};
+
+template <int D>
+struct PromptSmem {
+    static constexpr int kSlots = D == 128 ? 5 : 8;
+    unsigned char q[2][kTileBytes<D>];
+    unsigned char kv[kSlots][kTileBytes<D>];   // K and V images in turn
+    uint64_t kv_full[kSlots], kv_empty[kSlots];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    Cut start;
+};
+// the search for the range's start is over before the first copy lands where it keeps its sums
+static_assert(sizeof(ScanSmem<kThreads>) <= kTileBytes<64>, "scan fits a ring slot");
+static_assert(sizeof(PromptSmem<128>) <= 232448 && sizeof(PromptSmem<64>) <= 232448, "shared memory");
+
+// Bounded wait (about two seconds of SM clock; abandoned once another warp of the CTA has given up); the
+// warp agrees on the outcome and stays converged.
+__device__ __forceinline__ bool wait_for(uint64_t* mbar, uint32_t parity, const volatile int* abort_flag)
+{
+    bool ok = umma::mbar_try_wait(mbar, parity);
+    if (!ok) {
+        const long long start = clock64();
+        while (!(ok = umma::mbar_try_wait_suspend(mbar, parity, 20000u)))
+            if (*abort_flag || clock64() - start > (4ll << 30)) break;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D, bool BF16, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, AttnSpace a)
+{
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    using Smem = PromptSmem<D>;
+    Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+    constexpr int kSlots = Smem::kSlots;
+    constexpr uint32_t kTile = kTileBytes<D>;
+    constexpr uint32_t kColS = 128, kColO = 256, kTmemCols = 512;  // S of half h at 128 h, O at 256 + D h
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = p.hq / p.heads, tokens = half_tokens(group), span = 2 * tokens;
+    ScanSmem<kThreads>& scan = *reinterpret_cast<ScanSmem<kThreads>*>(sm.kv[0]);
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // ---- this worker's range ----
+    auto weight = [&](int s) {
+        const SeqView v = seq_view(p, s);
+        if (!is_long(p, a, s, v)) return (int64_t)0;
+        const int last = (v.n + span - 1) / span - 1;
+        return p.heads * (unit_prefix(v, span, last) + unit_tiles(v, span, last));
+    };
+    const int64_t total = scan_total<kThreads>(p.n_seq, weight, scan);
+    const int workers = (int)min((int64_t)gridDim.x, total);
+    if (blockIdx.x == 0 && tid == 0) {
+        a.head->prompt_total = total;
+        a.head->prompt_workers = workers;
+    }
+    if ((int)blockIdx.x >= workers) return;
+    const int64_t lo = cut_start(total, workers, blockIdx.x), hi = cut_start(total, workers, blockIdx.x + 1);
+    {
+        int64_t before;
+        const int s = scan_find<kThreads>(p.n_seq, lo, weight, scan, before);
+        if (warp == 0) {
+            const SeqView v = seq_view(p, s);
+            const int units = (v.n + span - 1) / span;
+            const int64_t per_head = unit_prefix(v, span, units - 1) + unit_tiles(v, span, units - 1);
+            const int head = (int)((lo - before) / per_head);
+            const int64_t rest = lo - before - head * per_head;
+            const int i = warp_find(units, rest, [&](int u) { return unit_prefix(v, span, u); });
+            if (lane == 0) {
+                sm.start = Cut{s, head, i, (int)(rest - unit_prefix(v, span, i)), unit_tiles(v, span, i)};
+                a.prompt_cut[blockIdx.x] = sm.start;
+            }
+        }
+    }
+    if (warp == kMmaWarp) umma::tmem_alloc(&sm.tmem_base, kTmemCols);
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            umma::mbar_init(&sm.kv_full[i], 1);
+            umma::mbar_init(&sm.kv_empty[i], 1);
+        }
+        for (int h = 0; h < 2; ++h) {
+            umma::mbar_init(&sm.q_full[h], 128);
+            umma::mbar_init(&sm.s_full[h], 1);
+            umma::mbar_init(&sm.p_full[h], 128);
+            umma::mbar_init(&sm.o_full[h], 1);
+        }
+        umma::mbar_init(&sm.drain, 1);
+        sm.abort_flag = 0;
+    }
+    umma::fence_proxy_async();  // the scan's shared memory goes to the copies
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = sm.tmem_base;
+    const volatile int* abort_flag = &sm.abort_flag;
+    Walk w(p, a, sm.start, hi - lo);
+
+#define GDN_KV_WAIT(mbar, parity)                         \
+    do {                                                  \
+        if (!wait_for((mbar), (parity), abort_flag)) {    \
+            if (lane == 0) {                              \
+                sm.abort_flag = 1;                        \
+                atomicOr(&a.head->error, kAttnTimeout);   \
+            }                                             \
+            goto done;                                    \
+        }                                                 \
+    } while (0)
+
+    if (warp == kLoadWarp) {
+        // ---- copies: K and V of each tile in turn through the ring ----
+        uint32_t n = 0;  // copies issued
+        for (; w.more(); w.next()) {
+            for (int j = w.j0; j < w.j1; ++j) {
+                const unsigned char* src = a.images + ((size_t)(w.image + j) * p.heads + w.head) * (2 * kTile);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const uint32_t slot = n % kSlots;
+                    if (n >= kSlots) {
+                        if (!wait_for(&sm.kv_empty[slot], (n / kSlots - 1) & 1, abort_flag)) {
+                            if (lane == 0) {
+                                sm.abort_flag = 1;
+                                atomicOr(&a.head->error, kAttnTimeout);
+                            }
+                            goto copies_done;
+                        }
+                    }
+                    if (lane == 0) {
+                        umma::mbar_arrive_expect_tx(&sm.kv_full[slot], kTile);
+                        umma::bulk_g2s(sm.kv[slot], src + kv * kTile, kTile, &sm.kv_full[slot]);
+                    }
+                }
+            }
+        }
+    copies_done:
+        // no copy may be in flight when the CTA leaves (copies end by themselves; the limit is a formality)
+        for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i)
+            for (int k = 0; k < 1 << 20 && !umma::mbar_try_wait(&sm.kv_full[i % kSlots], (i / kSlots) & 1); ++k) {}
+        goto done;
+    }
+    if (warp == kMmaWarp) {
+        // ---- products, issued by lane 0 ----
+        constexpr uint32_t id_s = umma::idesc_f16(128, kKeys, false, false);
+        constexpr uint32_t id_o = umma::idesc_f16(128, D, false, true);  // V: channels (N) contiguous
+        uint32_t n = 0;         // ring position of the current tile's K
+        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        auto scores = [&](int h, uint32_t at) {
+            if (lane == 0) {
+                const uint64_t da = umma::desc(umma::smem_u32(sm.q[h]), 128, (D / 8) * 128);
+                const uint64_t db = umma::desc(umma::smem_u32(sm.kv[at % kSlots]), 128, (D / 8) * 128);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) umma::mma_bf16(tmem + h * kColS, da + ks * 16, db + ks * 16, id_s, ks != 0);
+                umma::commit(&sm.s_full[h]);
+            }
+            __syncwarp();
+        };
+        auto outputs = [&](int h, uint32_t at, bool start) {
+            if (lane == 0) {
+                const uint64_t db = umma::desc(umma::smem_u32(sm.kv[at % kSlots]), (D / 8) * 128, 128);
+#pragma unroll
+                for (int ks = 0; ks < kKeys / 16; ++ks)
+                    umma::mma_ts(tmem + kColO + h * D, tmem + h * kColS + 8 * ks, db + ks * (2 * (D / 8) * 128 >> 4), id_o, !(start && ks == 0));
+                umma::commit(&sm.o_full[h]);
+            }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t at) {
+            if (lane == 0) umma::commit(&sm.kv_empty[at % kSlots]);
+            __syncwarp();
+        };
+        for (; w.more(); w.next()) {
+            const bool both = (2 * w.i + 1) * tokens < w.v.n;  // the second half has rows
+            GDN_KV_WAIT(&sm.kv_full[n % kSlots], (n / kSlots) & 1);
+            GDN_KV_WAIT(&sm.q_full[0], q_phase[0]);
+            q_phase[0] ^= 1u;
+            umma::fence_after_sync();
+            scores(0, n);
+            if (both) {
+                GDN_KV_WAIT(&sm.q_full[1], q_phase[1]);
+                q_phase[1] ^= 1u;
+                umma::fence_after_sync();
+                scores(1, n);
+            }
+            release(n);
+            for (int j = w.j0; j < w.j1; ++j, n += 2) {
+                const bool again = j + 1 < w.j1;
+                GDN_KV_WAIT(&sm.kv_full[(n + 1) % kSlots], ((n + 1) / kSlots) & 1);
+                GDN_KV_WAIT(&sm.p_full[0], p_phase[0]);
+                p_phase[0] ^= 1u;
+                umma::fence_after_sync();
+                outputs(0, n + 1, j == w.j0);
+                if (again) {
+                    GDN_KV_WAIT(&sm.kv_full[(n + 2) % kSlots], ((n + 2) / kSlots) & 1);
+                    scores(0, n + 2);
+                }
+                if (both) {
+                    GDN_KV_WAIT(&sm.p_full[1], p_phase[1]);
+                    p_phase[1] ^= 1u;
+                    umma::fence_after_sync();
+                    outputs(1, n + 1, j == w.j0);
+                }
+                release(n + 1);
+                if (again) {
+                    if (both) scores(1, n + 2);
+                    release(n + 2);
+                }
+            }
+        }
+        goto done;
+    }
+    {
+        // ---- softmax: a thread owns a query row ----
+        const int h = warp >> 2, r = tid & 127;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lane_off + h * kColS, t_o = tmem + lane_off + kColO + h * D;
+        const int i_tok = r / group, qh = r - i_tok * group;
+        uint32_t s_phase = 0, o_phase = 0;  // o_phase: parity of the next PV product's completion
+        for (; w.more(); w.next()) {
+            const int tok = (2 * w.i + h) * tokens + i_tok;
+            if ((2 * w.i + h) * tokens >= w.v.n) continue;  // a second half without rows
+            const bool valid = i_tok < tokens && tok < w.v.n;
+            // the row to shared memory in fp16
+            float coef;
+            {
+                const uint16_t* src = p.q + (int64_t)(w.v.t0 + tok) * p.q_stride + (w.head * group + qh) * D;
+                uint4 raw[D / 8];
+                uint32_t amax = 0;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    raw[c] = valid ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+                    float x[8];
+                    widen8<BF16>(raw[c], x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+                }
+                float mul, back;
+                row_unit(amax, mul, back);
+                if (p.scale < 0.0f) mul = -mul;  // scores times |scale|: a row's largest is its maximum's
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    float x[8];
+                    widen8<BF16>(raw[c], x);
+                    *reinterpret_cast<uint4*>(sm.q[h] + image_off<D>(r, c)) =
+                        make_uint4(narrow2<false>(x[0] * mul, x[1] * mul), narrow2<false>(x[2] * mul, x[3] * mul),
+                                   narrow2<false>(x[4] * mul, x[5] * mul), narrow2<false>(x[6] * mul, x[7] * mul));
+                }
+                umma::fence_proxy_async();
+                umma::mbar_arrive(&sm.q_full[h]);
+                const float2 norm = a.norm[(size_t)w.image * p.heads + w.head];
+                // (above 0, so that a masked score of -infinity stays one whatever the scale)
+                coef = fmaxf(back * (fabsf(p.scale) * kLog2e) * (norm.x * kImageUnit<E4M3>), 1e-35f);
+            }
+            const int limit = valid ? w.v.first + tok : -1;
+            const int first_limit = w.v.first + (2 * w.i + h) * tokens;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = w.j0; j < w.j1; ++j) {
+                GDN_KV_WAIT(&sm.s_full[h], s_phase);
+                s_phase ^= 1u;
+                umma::fence_after_sync();
+                float x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) umma::tmem_ld32(t_s + 32 * c, x[c]);
+                umma::tmem_wait_ld();
+                if (j * kKeys + kKeys - 1 > first_limit) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (j * kKeys + 32 * c + e > limit) x[c][e] = -INFINITY;
+                }
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = x[c][0];
+#pragma unroll
+                    for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], x[c][e]);
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * coef;
+                const bool moves = top > m + kLazy;
+                if (__any_sync(0xffffffffu, moves)) {
+                    float f = 1.0f;
+                    if (moves) {
+                        f = ex2(m - top);
+                        m = top;
+                        l *= f;
+                    }
+                    if (j > w.j0) {  // O holds the products up to tile j - 1
+                        GDN_KV_WAIT(&sm.o_full[h], o_phase ^ 1u);
+                        umma::fence_after_sync();
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            uint32_t u[32];
+                            umma::tmem_ld32(t_o + 32 * c, o);
+                            umma::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+                            umma::tmem_st32(t_o + 32 * c, u);
+                        }
+                    }
+                }
+                const float off = kWeightShift - (m == -INFINITY ? 0.0f : m);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t u[32];
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float w0 = ex2(fmaf(x[2 * c + (e >> 4)][(2 * e) & 31], coef, off));
+                        const float w1 = ex2(fmaf(x[2 * c + (e >> 4)][(2 * e + 1) & 31], coef, off));
+                        sum += w0 + w1;
+                        u[e] = narrow2<false>(w0, w1);
+                    }
+                    l += sum;
+                    umma::tmem_st32(t_s + 32 * c, u);
+                }
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                umma::mbar_arrive(&sm.p_full[h]);
+                o_phase ^= 1u;
+            }
+            GDN_KV_WAIT(&sm.o_full[h], o_phase ^ 1u);
+            umma::fence_after_sync();
+            const float unit = a.norm[(size_t)w.image * p.heads + w.head].y * kImageUnit<E4M3>;
+            const bool whole = w.j0 == 0 && w.j1 == w.tiles;
+            const int slot = 2 * blockIdx.x + (w.first ? 0 : 1), row = 128 * h + r;
+            const float scale = whole ? (l == 0.0f ? 0.0f : unit / l) : unit;
+            uint16_t* const dst = p.y + ((int64_t)(w.v.t0 + tok) * p.hq + w.head * group + qh) * D;
+            if (!whole) a.prompt_stat[(size_t)slot * kUnitRows + row] = make_float2(m, l);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                umma::tmem_ld32(t_o + 32 * c, o);
+                umma::tmem_wait_ld();
+                if (whole) {
+                    if (valid)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(dst + 32 * c + e) =
+                                make_uint4(narrow2<BF16>(o[e] * scale, o[e + 1] * scale), narrow2<BF16>(o[e + 2] * scale, o[e + 3] * scale),
+                                           narrow2<BF16>(o[e + 4] * scale, o[e + 5] * scale), narrow2<BF16>(o[e + 6] * scale, o[e + 7] * scale));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        a.prompt_out[((size_t)slot * (D / 4) + 8 * c + e / 4) * kUnitRows + row] =
+                            make_float4(o[e] * scale, o[e + 1] * scale, o[e + 2] * scale, o[e + 3] * scale);
+                }
+            }
+            umma::fence_before_sync();  // O read before the next unit's products (which wait for this thread's weights)
+        }
+    }
+done:
+    // every product issued has ended before TMEM and shared memory go
+    __syncwarp();
+    if (warp == kMmaWarp) {
+        if (lane == 0) {
+            umma::commit(&sm.drain);
+            for (int k = 0; k < 1 << 20 && !umma::mbar_try_wait(&sm.drain, 0); ++k) {}
+        }
+        __syncwarp();
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) umma::tmem_dealloc(tmem, kTmemCols);
+#undef GDN_KV_WAIT
+}
+
+// Block (w, 32 rows): where range w is the first that begins inside a unit, joins that unit's parts.  Four
+// threads share a row's channels.
+constexpr int kJoinThreads = 128;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) kv_prompt_join_kernel(AttnParams p, AttnSpace a)
+{
+    const int group = p.hq / p.heads, tokens = half_tokens(group);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int w = (int)blockIdx.x + 1, workers = a.head->prompt_workers;
+    if (w >= workers) return;
+    const Cut cut = a.prompt_cut[w];
+    if (cut.j0 == 0) return;
+    const int64_t total = a.head->prompt_total, begin = cut_start(total, workers, w) - cut.j0;
+    if (cut_start(total, workers, w - 1) > begin) return;
+    const int last = cut_of(total, workers, begin + cut.tiles - 1);
+    const int row = blockIdx.y * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+    const int h = row >> 7, r = row & 127, i_tok = r / group, qh = r - i_tok * group;
+    const int t0 = cu_at(p.cu_seqlens, cut.s, p.T), n = cu_at(p.cu_seqlens, cut.s + 1, p.T) - t0;
+    const int tok = (2 * cut.unit + h) * tokens + i_tok;
+    if (i_tok >= tokens || tok >= n) return;
+    constexpr int E = D / 16;  // float4s a thread
+    float top = -INFINITY, sum = 0.0f;
+    float4 acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = w - 1; i <= last; ++i) {
+        const int slot = 2 * i + (cut_start(total, workers, i) >= begin ? 0 : 1);
+        const float2 st = a.prompt_stat[(size_t)slot * kUnitRows + row];
+        const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.0f : next;
+        const float f0 = exp2f(top - ref), f1 = exp2f(st.x - ref);
+        sum = sum * f0 + st.y * f1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float4 o = a.prompt_out[((size_t)slot * (D / 4) + part * E + e) * kUnitRows + row];
+            acc[e].x = acc[e].x * f0 + o.x * f1;
+            acc[e].y = acc[e].y * f0 + o.y * f1;
+            acc[e].z = acc[e].z * f0 + o.z * f1;
+            acc[e].w = acc[e].w * f0 + o.w * f1;
+        }
+        top = next;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint2* dst = reinterpret_cast<uint2*>(p.y + ((int64_t)(t0 + tok) * p.hq + cut.head * group + qh) * D) + part * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) dst[e] = make_uint2(narrow2<BF16>(acc[e].x * inv, acc[e].y * inv), narrow2<BF16>(acc[e].z * inv, acc[e].w * inv));
+}
+
+template <int D, bool BF16, bool E4M3>
+cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
+{
+    const int64_t items = (int64_t)a.image_tiles * p.heads;
+    cudaError_t e = launch_k(kv_image_kernel<D, E4M3>, dim3((unsigned)(items < sms * 8 ? items : sms * 8)), dim3(kImageThreads), 0, stream, true, p, a);
+    if (e != cudaSuccess) return e;
+    auto kernel = kv_prompt_kernel<D, BF16, E4M3>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PromptSmem<D>));
+    if (e != cudaSuccess) return e;
+    const int grid = sms < kPromptMaxWorkers ? sms : kPromptMaxWorkers;
+    e = launch_k(kernel, dim3(grid), dim3(kThreads), sizeof(PromptSmem<D>), stream, true, p, a);
+    if (e != cudaSuccess || grid == 1) return e;
+    return launch_k(kv_prompt_join_kernel<D, BF16>, dim3(grid - 1, kUnitRows / 32), dim3(kJoinThreads), 0, stream, true, p, a);
+}
+
+template <int D>
+cudaError_t launch_types(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
+{
+    if (p.format == 1) return p.bf16 ? launch<D, true, true>(p, a, sms, stream) : launch<D, false, true>(p, a, sms, stream);
+    return p.bf16 ? launch<D, true, false>(p, a, sms, stream) : launch<D, false, false>(p, a, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_prompt(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
+{
+    return p.dim == 64 ? launch_types<64>(p, a, sms, stream) : launch_types<128>(p, a, sms, stream);
+}
+
+}  // namespace gdn

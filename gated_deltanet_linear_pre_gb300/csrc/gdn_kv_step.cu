@@ -22,6 +22,7 @@
 namespace gdn {
 namespace {
 
+constexpr int kStepThreads = 256;
 constexpr int kWarps = kStepThreads / 32;
 constexpr float kWeightUnit = 16384.0f;  // 2^14
 
@@ -88,44 +89,21 @@ struct StepSmem {
     static constexpr int R = 8 * NT, kStride = D + 4;
     float o[kWarps][R][kStride];
     float m[kWarps][R], l[kWarps][R], unit[kWarps];
-    int64_t chunk[256];   // tiles of every 256 sequences
-    int64_t prefix[kStepThreads + 1];
-    int64_t warp_sum[kWarps];
-    int found;
+    ScanSmem<kStepThreads> scan;
 };
 
-// inclusive scan over the block's 256 threads
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sum, int64_t& total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += o;
-    }
-    __syncthreads();  // warp_sum free
-    if (lane == 31) warp_sum[warp] = v;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) v += warp_sum[w];
-        total += warp_sum[w];
-    }
-    return v;
-}
-
+// row groups and key tiles of a sequence (a unit that sees nothing still writes its zeros: one tile)
 template <int NT>
-__device__ __forceinline__ void step_units(const KvBatch& p, const SeqView& v, int group, int most_rows, int& groups, int& tiles)
+__device__ __forceinline__ void step_units(const KvBatch& p, const AttnSpace& a, int s, const SeqView& v, int& groups, int& tiles)
 {
     constexpr int R = 8 * NT;
-    const int64_t rows = (int64_t)v.n * group;
-    groups = rows > most_rows ? 0 : (int)((rows + R - 1) / R);
-    tiles = max((v.kv + kSub - 1) / kSub, 1);  // a unit that sees nothing still writes its zeros
+    const int64_t rows = (int64_t)v.n * (p.hq / p.heads);
+    groups = is_long(p, a, s, v) ? 0 : (int)((rows + R - 1) / R);
+    tiles = max((v.kv + kSub - 1) / kSub, 1);
 }
 
 template <int D, bool BF16, bool E4M3, int NT>
-__global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(AttnParams p, int most_rows)
+__global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(AttnParams p, AttnSpace a)
 {
     constexpr int R = 8 * NT, KS = D / 16, MT = D / 16;
     using Smem = StepSmem<D, NT>;
@@ -137,59 +115,31 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
     pdl_launch_dependents();
 
     // ---- this worker's range of the batch's tiles ----
-    const StepSpace ws = step_space(p.workspace, p.n_seq);
-    const int chunks = (p.n_seq + kStepThreads - 1) / kStepThreads;
-    int64_t total = 0;
-    for (int c = 0; c < chunks; ++c) {
-        const int s = c * kStepThreads + tid;
-        int64_t mine = 0, sum;
-        if (s < p.n_seq) {
-            int groups, tiles;
-            step_units<NT>(p, seq_view(p, s), group, most_rows, groups, tiles);
-            mine = (int64_t)p.heads * groups * tiles;
-        }
-        const int64_t incl = block_scan(mine, sm.warp_sum, sum);
-        if (c == 0) sm.prefix[tid] = incl - mine;  // a single chunk needs no second look
-        if (tid == 0) sm.chunk[c] = sum;
-        if (blockIdx.x == 0 && s < p.n_seq) ws.base[s] = total + incl - mine;
-        total += sum;
-    }
+    auto weight = [&](int s) {
+        int groups, tiles;
+        step_units<NT>(p, a, s, seq_view(p, s), groups, tiles);
+        return (int64_t)p.heads * groups * tiles;
+    };
+    const int64_t total = scan_total<kStepThreads>(p.n_seq, weight, sm.scan);
     // at least two tiles a warp and worker: shorter ranges cost more to join than they save
     const int workers = (int)min((int64_t)gridDim.x, (total + 2 * kWarps - 1) / (2 * kWarps));
     if (blockIdx.x == 0 && tid == 0) {
-        ws.head->total = total;
-        ws.head->workers = workers;
+        a.head->step_total = total;
+        a.head->step_workers = workers;
+        if (a.image_tiles == 0) a.head->error = 0u;  // else the image kernel cleared it
     }
     if ((int)blockIdx.x >= workers) return;
     const int64_t lo = cut_start(total, workers, blockIdx.x), hi = cut_start(total, workers, blockIdx.x + 1);
-    int64_t before = 0;
-    int c0 = 0;
-    __syncthreads();
-    while (c0 + 1 < chunks && before + sm.chunk[c0] <= lo) before += sm.chunk[c0++];
-    if (c0 > 0) {
-        const int s = c0 * kStepThreads + tid;
-        int64_t mine = 0, sum;
-        if (s < p.n_seq) {
-            int groups, tiles;
-            step_units<NT>(p, seq_view(p, s), group, most_rows, groups, tiles);
-            mine = (int64_t)p.heads * groups * tiles;
-        }
-        const int64_t incl = block_scan(mine, sm.warp_sum, sum);
-        sm.prefix[tid] = incl - mine;
-    }
-    if (tid == 0) sm.prefix[kStepThreads] = sm.chunk[c0];
-    __syncthreads();
-    if (before + sm.prefix[tid] <= lo && lo < before + sm.prefix[tid + 1]) sm.found = tid;
-    __syncthreads();
-    int s = c0 * kStepThreads + sm.found;
-    int64_t at = lo - (before + sm.prefix[sm.found]);  // tiles into sequence s
+    int64_t before;
+    int s = scan_find<kStepThreads>(p.n_seq, lo, weight, sm.scan, before);
+    int64_t at = lo - before;  // tiles into sequence s
 
     // ---- the units of the range ----
     bool first_unit = true;
     for (int64_t x = lo; x < hi && s < p.n_seq; ++s) {
         const SeqView v = seq_view(p, s);
         int groups, tiles;
-        step_units<NT>(p, v, group, most_rows, groups, tiles);
+        step_units<NT>(p, a, s, v, groups, tiles);
         const int64_t units = (int64_t)p.heads * groups;
         for (int64_t unit = tiles ? at / tiles : 0; unit < units && x < hi; ++unit) {
             const int j0 = (int)(at - unit * tiles), j1 = (int)min((int64_t)tiles, j0 + (hi - x));
@@ -197,6 +147,7 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
             x += j1 - j0;
             const int head = (int)(unit / groups), row0 = (int)(unit - (int64_t)head * groups) * R;
             const int rows = v.n * group;
+            if (first_unit && tid == 0) a.step_cut[blockIdx.x] = Cut{s, head, row0, j0, tiles};
 
             // queries: B operands (row g of each 8), scaled per row; the factor goes into the row's score unit
             uint32_t qf[NT][KS][2];
@@ -232,17 +183,14 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
                 }
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // 2^(14 - exponent of the largest); rows of zeros, infinities or NaN stay as they are
-                const int e8 = (int)(amax >> 23);
-                const bool scaled = amax != 0 && e8 < 255;
-                const int up = scaled ? 141 - max(e8, 41) : 0;
-                const float mul = __uint_as_float((uint32_t)(127 + up) << 23), back = __uint_as_float((uint32_t)(127 - up) << 23);
+                float mul, back;
+                row_unit(amax, mul, back);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     qf[nt][ks][0] = narrow2<false>(f[ks][0] * mul, f[ks][1] * mul);
                     qf[nt][ks][1] = narrow2<false>(f[ks][2] * mul, f[ks][3] * mul);
                 }
-                const float unit_of = back * (p.scale * 1.4426950408889634f) * kCodeUnit<E4M3>;
+                const float unit_of = back * (p.scale * kLog2e) * kCodeUnit<E4M3>;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     coef[nt][e] = __shfl_sync(0xffffffffu, unit_of, (2 * t + e) * 4);
@@ -349,18 +297,18 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
             const int in_mask = p.page - 1;
             int j = j0 + warp;
             if (j < j1) {
-                Tile<D> a, b;
-                a.load(p, page_of(j), head, (j * kSub) & in_mask, lane);
+                Tile<D> t0, t1;
+                t0.load(p, page_of(j), head, (j * kSub) & in_mask, lane);
                 int next = page_of(j + kWarps);
                 while (true) {
-                    if (j + kWarps < j1) b.load(p, next, head, ((j + kWarps) * kSub) & in_mask, lane);
+                    if (j + kWarps < j1) t1.load(p, next, head, ((j + kWarps) * kSub) & in_mask, lane);
                     next = page_of(j + 2 * kWarps);
-                    work(a, j);
+                    work(t0, j);
                     j += kWarps;
                     if (j >= j1) break;
-                    if (j + kWarps < j1) a.load(p, next, head, ((j + kWarps) * kSub) & in_mask, lane);
+                    if (j + kWarps < j1) t0.load(p, next, head, ((j + kWarps) * kSub) & in_mask, lane);
                     next = page_of(j + 2 * kWarps);
-                    work(b, j);
+                    work(t1, j);
                     j += kWarps;
                     if (j >= j1) break;
                 }
@@ -416,8 +364,8 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
 #pragma unroll
                     for (int e = 0; e < E; e += 2) dst[e / 2] = narrow2<BF16>(acc[e] * inv, acc[e + 1] * inv);
                 } else {
-                    if (lane == 0) ws.stat[(size_t)slot * kStepMaxRows + row] = make_float2(top, sum);
-                    float* dst = ws.out + ((size_t)slot * kStepMaxRows + row) * D + lane * E;
+                    if (lane == 0) a.step_stat[(size_t)slot * kStepMaxRows + row] = make_float2(top, sum);
+                    float* dst = a.step_out + ((size_t)slot * kStepMaxRows + row) * D + lane * E;
 #pragma unroll
                     for (int e = 0; e < E; ++e) dst[e] = acc[e];
                 }
@@ -428,37 +376,36 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
     }
 }
 
-// One block per (token, query head): the parts of its unit, in the order of their ranges.
+// Block (w, row): where range w is the first that begins inside a unit, joins that unit's parts for one
+// query row, in the order of their ranges.
 constexpr int kJoinThreads = 128;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttnParams p, int most_rows, int R)
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttnParams p, AttnSpace a)
 {
     constexpr int E = D / 32, W = kJoinThreads / 32;
     __shared__ float part[W][D], part_l[W], part_m[W];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = p.hq / p.heads;
     pdl_wait();
     pdl_launch_dependents();
-    const int token = (int)blockIdx.x, hq = blockIdx.y, group = p.hq / p.heads, head = hq / group;
-    const StepSpace ws = step_space(p.workspace, p.n_seq);
-    const int s = warp_find(p.n_seq, token, [&](int i) { return cu_at(p.cu_seqlens, i, p.T); });
-    const SeqView v = seq_view(p, s);
-    const int64_t all = (int64_t)v.n * group;
-    if (all > most_rows || token - v.t0 >= v.n) return;
-    const int row = (token - v.t0) * group + hq - head * group;
-    const int groups = (int)((all + R - 1) / R), tiles = max((v.kv + kSub - 1) / kSub, 1);
-    const int64_t total = ws.head->total;
-    const int workers = ws.head->workers;
-    const int64_t a = ws.base[s] + ((int64_t)head * groups + row / R) * tiles;
-    const int w0 = cut_of(total, workers, a), w1 = cut_of(total, workers, a + tiles - 1);
-    if (w0 == w1) return;  // finished by its worker
+    const int w = (int)blockIdx.x + 1, row = blockIdx.y;
+    const int workers = a.head->step_workers;
+    if (w >= workers) return;
+    const Cut cut = a.step_cut[w];
+    if (cut.j0 == 0) return;
+    const int64_t total = a.head->step_total, begin = cut_start(total, workers, w) - cut.j0;
+    if (cut_start(total, workers, w - 1) > begin) return;
+    const int t0 = cu_at(p.cu_seqlens, cut.s, p.T), n = cu_at(p.cu_seqlens, cut.s + 1, p.T) - t0;
+    if (cut.unit + row >= n * group) return;
+    const int last = cut_of(total, workers, begin + cut.tiles - 1);
     float top = -INFINITY, sum = 0.0f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int w = w0 + warp; w <= w1; w += W) {
-        // the unit is the last of the range that it begins in the middle of, the first of the others
-        const int slot = 2 * w + (cut_start(total, workers, w) >= a ? 0 : 1);
-        const float2 st = ws.stat[(size_t)slot * kStepMaxRows + row % R];
-        const float* src = ws.out + ((size_t)slot * kStepMaxRows + row % R) * D + lane * E;
+#pragma unroll 4
+    for (int i = w - 1 + warp; i <= last; i += W) {
+        // the unit is the first of every range but the one that it begins in the middle of
+        const int slot = 2 * i + (cut_start(total, workers, i) >= begin ? 0 : 1);
+        const float2 st = a.step_stat[(size_t)slot * kStepMaxRows + row];
+        const float* src = a.step_out + ((size_t)slot * kStepMaxRows + row) * D + lane * E;
         const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.0f : next;
         const float f0 = exp2f(top - ref), f1 = exp2f(st.x - ref);
         sum = sum * f0 + st.y * f1;
@@ -476,61 +423,57 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttnParams p, int
     if (tid >= D / 2) return;
     float m = -INFINITY, l = 0.0f, x0 = 0.0f, x1 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) m = fmaxf(m, part_m[w]);
+    for (int i = 0; i < W; ++i) m = fmaxf(m, part_m[i]);
     const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        const float f = exp2f(part_m[w] - ref);
-        l += f * part_l[w];
-        x0 += f * part[w][2 * tid];
-        x1 += f * part[w][2 * tid + 1];
+    for (int i = 0; i < W; ++i) {
+        const float f = exp2f(part_m[i] - ref);
+        l += f * part_l[i];
+        x0 += f * part[i][2 * tid];
+        x1 += f * part[i][2 * tid + 1];
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    reinterpret_cast<uint32_t*>(p.y + ((int64_t)token * p.hq + hq) * D)[tid] = narrow2<BF16>(x0 * inv, x1 * inv);
+    const int i = (cut.unit + row) / group, qh = cut.unit + row - i * group;
+    reinterpret_cast<uint32_t*>(p.y + ((int64_t)(t0 + i) * p.hq + cut.head * group + qh) * D)[tid] = narrow2<BF16>(x0 * inv, x1 * inv);
 }
 
 template <int D, bool BF16, bool E4M3, int NT>
-cudaError_t launch(const AttnParams& p, int sms, int most_rows, cudaStream_t stream)
+cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
     auto kernel = kv_step_kernel<D, BF16, E4M3, NT>;
     const size_t smem = sizeof(StepSmem<D, NT>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int grid = min(sms * (NT == 1 ? 2 : 1), kStepMaxWorkers);
-    e = launch_k(kernel, dim3(grid), dim3(kStepThreads), smem, stream, true, p, most_rows);
+    e = launch_k(kernel, dim3(grid), dim3(kStepThreads), smem, stream, true, p, a);
     if (e != cudaSuccess) return e;
-    return launch_k(kv_join_kernel<D, BF16>, dim3(p.T, p.hq), dim3(kJoinThreads), 0, stream, true, p, most_rows, 8 * NT);
+    if (grid == 1) return cudaSuccess;
+    return launch_k(kv_join_kernel<D, BF16>, dim3(grid - 1, 8 * NT), dim3(kJoinThreads), 0, stream, true, p, a);
 }
 
 template <int D, bool BF16, bool E4M3>
-cudaError_t launch_rows(const AttnParams& p, int sms, int most_rows, cudaStream_t stream)
+cudaError_t launch_rows(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
     // query rows of an average sequence decide the tile: 8 rows as long as they hold them (two blocks an
     // SM), else 16 or 32 (a warp's codes serve more rows, at one block an SM)
     const int64_t rows = ((int64_t)p.T * (p.hq / p.heads) + p.n_seq - 1) / p.n_seq;
-    if (rows <= 8) return launch<D, BF16, E4M3, 1>(p, sms, most_rows, stream);
-    if (rows <= 16) return launch<D, BF16, E4M3, 2>(p, sms, most_rows, stream);
-    return launch<D, BF16, E4M3, 4>(p, sms, most_rows, stream);
+    if (rows <= 8) return launch<D, BF16, E4M3, 1>(p, a, sms, stream);
+    if (rows <= 16) return launch<D, BF16, E4M3, 2>(p, a, sms, stream);
+    return launch<D, BF16, E4M3, 4>(p, a, sms, stream);
 }
 
 template <int D>
-cudaError_t launch_types(const AttnParams& p, int sms, int most_rows, cudaStream_t stream)
+cudaError_t launch_types(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
-    if (p.format == 1) return p.bf16 ? launch_rows<D, true, true>(p, sms, most_rows, stream) : launch_rows<D, false, true>(p, sms, most_rows, stream);
-    return p.bf16 ? launch_rows<D, true, false>(p, sms, most_rows, stream) : launch_rows<D, false, false>(p, sms, most_rows, stream);
+    if (p.format == 1) return p.bf16 ? launch_rows<D, true, true>(p, a, sms, stream) : launch_rows<D, false, true>(p, a, sms, stream);
+    return p.bf16 ? launch_rows<D, true, false>(p, a, sms, stream) : launch_rows<D, false, false>(p, a, sms, stream);
 }
 
 }  // namespace
 
-size_t kv_attn_workspace_bytes(const KvBatch& b) { return b.T > 0 ? step_space_bytes(b.n_seq, b.dim) : 0; }
-
-cudaError_t launch_kv_attn(const AttnParams& p, cudaStream_t stream)
+cudaError_t launch_kv_step(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    return p.dim == 64 ? launch_types<64>(p, sms, 0x7fffffff, stream) : launch_types<128>(p, sms, 0x7fffffff, stream);
+    return p.dim == 64 ? launch_types<64>(p, a, sms, stream) : launch_types<128>(p, a, sms, stream);
 }
 
 }  // namespace gdn

@@ -430,6 +430,15 @@ GDN_API gdn_status gdn_kv_attn(const gdn_kv_cache* cache, int32_t dtype, int32_t
                                size_t workspace_bytes, struct CUstream_st* stream);
 
 /*
+ * gdn_kv_attn_check -- the failure report of the last gdn_kv_attn on this
+ * workspace: every wait inside its kernels is bounded (about two seconds), and
+ * one that expires ends its CTA and is recorded, as for the scan.  Enqueues a
+ * 4-byte device-to-host copy on `stream`, SYNCHRONISES it and returns GDN_OK or
+ * GDN_ERR_TIMEOUT (that call's outputs are invalid).
+ */
+GDN_API gdn_status gdn_kv_attn_check(const void* workspace, struct CUstream_st* stream);
+
+/*
  * gdn_draft_verify -- accepts or replaces drafted tokens so that the tokens
  * kept are distributed as the target's.
  *

@@ -82,6 +82,8 @@ class Batch:
         y = buf[guard:buf.numel() - guard].view(self.T, self.hq, self.dim)
         gdn.gdn_kv_attn(self.cache, self.cu, self.T, self.past, self.table, q,
                         self.dim ** -0.5 if softmax_scale is None else softmax_scale, y, ws[:size])
+        if size:
+            gdn.gdn_kv_attn_check(ws)
         torch.cuda.synchronize()
         assert bool((buf[:guard] == 7).all()) and bool((buf[-guard:] == 7).all()), "output written outside y"
         if workspace is None:
@@ -270,6 +272,9 @@ CASES = [  # new, past, hq, heads, dim, page
     ([130, 7], [0, 259], 3, 1, 128, 32),
     ([97], [4], 4, 4, 64, 16),
     ([1], [5000], 64, 1, 128, 64),
+    ([300, 1, 2, 200], [0, 900, 40, 1000], 8, 2, 128, 64),
+    ([260, 129], [130, 0], 4, 4, 64, 128),
+    ([70, 5, 90], [513, 1200, 126], 48, 1, 128, 16),
 ]
 
 

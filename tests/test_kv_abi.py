@@ -80,6 +80,7 @@ def test_attention_refusals(L):
     assert attn(L, c, wb=need - 1) == 4
     assert L.gdn_kv_attn_workspace_bytes(None, 2, 6, 4, 8) == 0
     assert L.gdn_kv_attn_workspace_bytes(ctypes.byref(c), 2, 0, 4, 8) == 0
+    assert L.gdn_kv_attn_check(None, None) == 1
 
 
 def test_verify_refusals(L):
