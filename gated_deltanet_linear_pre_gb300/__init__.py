@@ -23,5 +23,6 @@ def __getattr__(name):
     # the binding (and torch) load on first use, so `inputs` stays light
     if name in _BINDING:
         from . import _native
-        return getattr(_native, name)
+        value = globals()[name] = getattr(_native, name)  # later uses find it without coming here
+        return value
     raise AttributeError(name)

@@ -57,6 +57,8 @@ def library_path() -> str:
 def lib():
     """Load libgdn.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -126,8 +128,8 @@ def _check(fn: str, status: int):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -363,8 +365,26 @@ def gdn_scan_selftest_withhold_flag(d: gdn_dims, cu_seqlens, total_tokens, qn, k
 
 
 # ---- attention layers: the 8-bit paged cache, attention over it, the check of drafted tokens ----
+# One token's step through these calls takes a few microseconds on the GPU, so their checks are kept to
+# one pass over each tensor; a tensor that fails one goes to a function that says why.
 _KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
 _ACT_TYPES = {torch.float16: 0, torch.bfloat16: 1}
+_I32, _F32 = torch.int32, torch.float32
+
+
+def _refuse(t, name, dtype, shape):
+    _ptr(t, name, dtype, shape)  # says what is wrong with it, unless it is the missing tensor
+    raise TypeError(f"{name} must be a torch.Tensor")
+
+
+def _dense(t, name, dtype, shape):
+    """Device pointer of a contiguous CUDA tensor of this dtype and shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape)
 
 
 def kv_cache(k, v, k_scale, v_scale) -> gdn_kv_cache:
@@ -375,44 +395,50 @@ def kv_cache(k, v, k_scale, v_scale) -> gdn_kv_cache:
     if k.dtype not in _KV_FORMATS:
         raise TypeError(f"k must be torch.int8 or torch.float8_e4m3fn, got {k.dtype}")
     n_pages, heads, page, dim = k.shape
-    f32 = torch.float32
     c = gdn_kv_cache(heads, dim, page, n_pages, _KV_FORMATS[k.dtype], _ptr(k, "k", k.dtype),
-                     _ptr(v, "v", k.dtype, k.shape), _ptr(k_scale, "k_scale", f32, (n_pages, heads)),
-                     _ptr(v_scale, "v_scale", f32, (n_pages, heads)))
+                     _ptr(v, "v", k.dtype, k.shape), _ptr(k_scale, "k_scale", _F32, (n_pages, heads)),
+                     _ptr(v_scale, "v_scale", _F32, (n_pages, heads)))
     c.tensors = (k, v, k_scale, v_scale)
     return c
 
 
-def _rows16(t, name: str, dtype, T: int, heads: int, dim: int):
+def _rows16(t, name: str, dtype, shape):
     """Device pointer and token stride of an activation tensor [T, heads, dim] whose token rows are
     contiguous (a slice of a packed projection will do)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.shape != (T, heads, dim):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, heads, dim)}")
-    st, sh, sd = t.stride()
-    row = heads * dim
-    if T and ((sd != 1 and dim > 1) or (sh != dim and heads > 1)):
-        raise ValueError(f"{name}'s token rows must be contiguous")
-    return (t.data_ptr() if T else None), (st if T > 1 else row)
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda:
+            st, sh, sd = t.stride()
+            T, heads, dim = shape
+            if T == 0:
+                return None, heads * dim
+            if sd == 1 and (sh == dim or heads == 1):
+                return t.data_ptr(), (st if T > 1 else heads * dim)
+            raise ValueError(f"{name}'s token rows must be contiguous")
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor):
+        _ptr(t.contiguous() if t.dtype is dtype and t.is_cuda else t, name, dtype, shape)
+    raise TypeError(f"{name} must be a torch.Tensor")
+
+
+def _act(t, name: str) -> int:
+    act = _ACT_TYPES.get(getattr(t, "dtype", None))
+    if act is None or t.dim() != 3:
+        raise TypeError(f"{name} must be a torch.float16 or torch.bfloat16 tensor [T, heads, head_dim]")
+    return act
 
 
 def _kv_batch(cu_seqlens, past, page_table):
-    if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be a contiguous 1-D int32 CUDA tensor")
-    n = cu_seqlens.shape[0] - 1
-    if page_table.dtype != torch.int32 or not page_table.is_cuda or page_table.dim() != 2 or page_table.shape[0] != n:
+    n = page_table.shape[0]
+    cu = _dense(cu_seqlens, "cu_seqlens", _I32, (n + 1,))
+    if page_table.dtype is not _I32 or page_table.dim() != 2 or not page_table.is_cuda:
         raise ValueError("page_table must be an int32 CUDA tensor [n_seq, max_pages]")
     width = page_table.shape[1]
-    if width > 1 and page_table.stride(1) != 1:
+    stride, one = page_table.stride()
+    if one != 1 and width > 1:
         raise ValueError("page_table's rows must be contiguous")
-    stride = page_table.stride(0) if n > 1 else width
-    return n, cu_seqlens.data_ptr(), _ptr(past, "past", torch.int32, (n,)), \
-        (page_table.data_ptr() if n and width else None), stride, width
+    return (n, cu, _dense(past, "past", _I32, (n,)), (page_table.data_ptr() if n and width else None),
+            (stride if n > 1 else width), width)
 
 
 def gdn_kv_append(cache: gdn_kv_cache, cu_seqlens, total_tokens, past, page_table, q, k, v, cos, sin,
@@ -421,25 +447,25 @@ def gdn_kv_append(cache: gdn_kv_cache, cu_seqlens, total_tokens, past, page_tabl
     bits; rotate q into q_out (both None: keys and values only).  cos, sin [n_pos, rot_dim / 2] or None."""
     T = int(total_tokens)
     n, cu, pst, table, table_stride, width = _kv_batch(cu_seqlens, past, page_table)
-    dt, dim = k.dtype, cache.head_dim
-    if dt not in _ACT_TYPES:
-        raise TypeError(f"k must be torch.float16 or torch.bfloat16, got {dt}")
-    kp, ks = _rows16(k, "k", dt, T, cache.heads, dim)
-    vp, vs = _rows16(v, "v", dt, T, cache.heads, dim)
+    act, dt, shape = _act(k, "k"), k.dtype, (T, cache.heads, cache.head_dim)
+    kp, ks = _rows16(k, "k", dt, shape)
+    vp, vs = _rows16(v, "v", dt, shape)
     hq, qp, qs, qo = 0, None, 0, None
     if q is not None:
         hq = q.shape[1]
-        qp, qs = _rows16(q, "q", dt, T, hq, dim)
-        qo = _ptr(q_out, "q_out", dt, (T, hq, dim))
+        shape = (T, hq, shape[2])
+        qp, qs = _rows16(q, "q", dt, shape)
+        qo = _dense(q_out, "q_out", dt, shape)
     n_pos = half = 0
     cp = sp = None
     if cos is not None:
-        n_pos, half = cos.shape
-        cp = _ptr(cos, "cos", torch.float32, (n_pos, half))
-        sp = _ptr(sin, "sin", torch.float32, (n_pos, half))
-    st = lib().gdn_kv_append(ctypes.byref(cache), _ACT_TYPES[dt], n, T, cu, pst, table, table_stride, width, hq, qp, qs,
+        n_pos, half = shape = cos.shape
+        cp = _dense(cos, "cos", _F32, shape)
+        sp = _dense(sin, "sin", _F32, shape)
+    st = lib().gdn_kv_append(ctypes.byref(cache), act, n, T, cu, pst, table, table_stride, width, hq, qp, qs,
                              kp, ks, vp, vs, cp, sp, 2 * half, n_pos, 1 if interleaved else 0, qo, _stream(stream))
-    _check("gdn_kv_append", st)
+    if st:
+        _check("gdn_kv_append", st)
 
 
 def gdn_kv_attn_workspace_bytes(cache: gdn_kv_cache, n_seq: int, total_tokens: int, hq: int, max_pages: int) -> int:
@@ -451,16 +477,17 @@ def gdn_kv_attn(cache: gdn_kv_cache, cu_seqlens, total_tokens, past, page_table,
     """Causal attention of the new tokens over the cache, their own keys and values included."""
     T = int(total_tokens)
     n, cu, pst, table, table_stride, width = _kv_batch(cu_seqlens, past, page_table)
-    dt, hq = q.dtype, q.shape[1]
-    if dt not in _ACT_TYPES:
-        raise TypeError(f"q must be torch.float16 or torch.bfloat16, got {dt}")
-    qp, qs = _rows16(q, "q", dt, T, hq, cache.head_dim)
+    act, dt, hq = _act(q, "q"), q.dtype, q.shape[1]
+    shape = (T, hq, cache.head_dim)
+    qp, qs = _rows16(q, "q", dt, shape)
     wp, wb = None, 0
     if workspace is not None:
-        wp, wb = _ptr(workspace, "workspace", torch.uint8), workspace.numel()
-    st = lib().gdn_kv_attn(ctypes.byref(cache), _ACT_TYPES[dt], n, T, cu, pst, table, table_stride, width, hq, qp, qs,
-                           softmax_scale, _ptr(y, "y", dt, (T, hq, cache.head_dim)), wp, wb, _stream(stream))
-    _check("gdn_kv_attn", st)
+        wb = workspace.numel()
+        wp = _ptr(workspace, "workspace", torch.uint8)
+    st = lib().gdn_kv_attn(ctypes.byref(cache), act, n, T, cu, pst, table, table_stride, width, hq, qp, qs,
+                           softmax_scale, _dense(y, "y", dt, shape), wp, wb, _stream(stream))
+    if st:
+        _check("gdn_kv_attn", st)
 
 
 def gdn_kv_attn_check(workspace, stream=None):
@@ -469,28 +496,33 @@ def gdn_kv_attn_check(workspace, stream=None):
     _check("gdn_kv_attn_check", lib().gdn_kv_attn_check(_ptr(workspace, "workspace", torch.uint8), _stream(stream)))
 
 
-def _prob_rows(t, name: str, n: int, rows: int, vocab: int):
+def _prob_rows(t, name: str, shape):
     """Device pointer and row stride of float32 [n, rows, vocab] whose rows are evenly spaced."""
-    if t.dtype != torch.float32 or not t.is_cuda:
+    if t.dtype is not _F32 or not t.is_cuda:
         raise TypeError(f"{name} must be a float32 CUDA tensor")
-    if t.shape != (n, rows, vocab):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, rows, vocab)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    n, rows, vocab = shape
     sn, sr, sv = t.stride()
     stride = sr if rows > 1 else (sn if n > 1 else vocab)
-    if t.numel() and ((sv != 1 and vocab > 1) or (n > 1 and sn != rows * stride)):
+    if n and ((sv != 1 and vocab > 1) or (n > 1 and sn != rows * stride)):
         raise ValueError(f"{name}'s rows must be contiguous and evenly spaced")
-    return (t.data_ptr() if t.numel() else None), stride
+    return (t.data_ptr() if n else None), stride
 
 
 def gdn_draft_verify(p, q, draft, n_draft, u, accepted, next_token, stream=None):
     """Check drafted tokens: p [n, d + 1, vocab], q [n, d, vocab] float32, draft int32 [n, d], n_draft int32
     [n] or None (all d), u float32 [n, d + 1]; writes accepted and next_token, int32 [n]."""
     n, d1, vocab = p.shape
-    d, i32 = d1 - 1, torch.int32
-    pp, ps = _prob_rows(p, "p", n, d1, vocab)
-    qp, qs = _prob_rows(q, "q", n, d, vocab) if d else (None, vocab)
-    st = lib().gdn_draft_verify(n, d, vocab, pp, ps, qp, qs, _ptr(draft, "draft", i32, (n, d)) if d else None,
-                                _ptr(n_draft, "n_draft", i32, (n,)), _ptr(u, "u", torch.float32, (n, d1)),
-                                _ptr(accepted, "accepted", i32, (n,)), _ptr(next_token, "next_token", i32, (n,)),
-                                _stream(stream))
-    _check("gdn_draft_verify", st)
+    d, per_seq = d1 - 1, (n,)
+    pp, ps = _prob_rows(p, "p", (n, d1, vocab))
+    qp, qs, dp = None, vocab, None
+    if d:
+        qp, qs = _prob_rows(q, "q", (n, d, vocab))
+        dp = _dense(draft, "draft", _I32, (n, d))
+    st = lib().gdn_draft_verify(n, d, vocab, pp, ps, qp, qs, dp,
+                                None if n_draft is None else _dense(n_draft, "n_draft", _I32, per_seq),
+                                _dense(u, "u", _F32, (n, d1)), _dense(accepted, "accepted", _I32, per_seq),
+                                _dense(next_token, "next_token", _I32, per_seq), _stream(stream))
+    if st:
+        _check("gdn_draft_verify", st)

@@ -11,7 +11,8 @@
 // Layout.  The unit of work is (page touched by a sequence, kv head, k or v): its scale is one maximum
 // over the unit's rows, so no unit needs another's result and the call is one launch without
 // atomics.  16 bytes per thread: D / 8 threads hold a row, and the partner channels of a rotation
-// half a head apart come from another lane of the row by shuffles.  A sequence's pages get
+// half a head apart come from another lane of the row by shuffles.  Queries go by (token, 8 heads): a
+// lane's eight loads are in flight together and share the angles it holds.  A sequence's pages get
 // slots floor(cu[s] / P) + 2 s onwards: n tokens touch at most floor((n - 1) / P) + 2 pages, so
 // floor(T / P) + 2 n_seq slots hold any batch without a prefix sum on the host.
 #include "gdn_kv.cuh"
@@ -19,52 +20,74 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
-
-// Rotates the 8 channels 8c .. 8c+7 that this lane holds of a row (lanes of a row are adjacent).
-// `cs`, `sn`: the position's table rows.  Every product and sum is rounded to fp32 on its own: the
+// The angles of the 8 channels 8c .. 8c+7 that this lane holds of a row at one position, and their
+// rotation (lanes of a row are adjacent).  Every product and sum is rounded to fp32 on its own: the
 // result does not depend on how a compiler would contract them.
-template <bool BF16>
-__device__ __forceinline__ void rotate8(const uint4& raw, float (&x)[8], int c, int rot, int interleaved, const float* cs, const float* sn)
-{
-    if (rot == 0) return;
-    const int half = rot >> 1;
-    if (interleaved) {
-        if (8 * c >= rot) return;
-        const float4 co = __ldg(reinterpret_cast<const float4*>(cs) + c), si = __ldg(reinterpret_cast<const float4*>(sn) + c);
-        const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float a = x[2 * e], b = x[2 * e + 1];
-            x[2 * e] = __fsub_rn(__fmul_rn(a, cc[e]), __fmul_rn(b, ss[e]));
-            x[2 * e + 1] = __fadd_rn(__fmul_rn(b, cc[e]), __fmul_rn(a, ss[e]));
+struct Angles {
+    float c[8], s[8];
+    int from;      // lane of the partner channels (rotations of halves)
+    bool turned, first;
+
+    __device__ __forceinline__ Angles(const AppendParams& p, int lane8, int pos)
+    {
+        const int half = p.rot >> 1, lane = threadIdx.x & 31;
+        const int64_t at = (int64_t)min(max(pos, 0), p.n_pos - 1) * half;
+        if (p.interleaved) {  // 4 angles
+            turned = 8 * lane8 < p.rot;
+            first = true;
+            from = lane;
+            if (turned) {
+                load4(p.cos + at + 4 * lane8, c);
+                load4(p.sin + at + 4 * lane8, s);
+            }
+        } else {
+            const int shift = half >> 3;  // lanes between the two channels of a pair
+            first = lane8 < shift;
+            turned = lane8 < 2 * shift;
+            from = turned ? (first ? lane + shift : lane - shift) : lane;
+            if (turned) {
+                const int64_t j = at + 8 * (first ? lane8 : lane8 - shift);
+                load4(p.cos + j, c);
+                load4(p.cos + j + 4, c + 4);
+                load4(p.sin + j, s);
+                load4(p.sin + j + 4, s + 4);
+            }
         }
-        return;
     }
-    const int shift = half >> 3;  // lanes between the two channels of a pair
-    const bool first = c < shift, turned = c < 2 * shift;
-    const int lane = threadIdx.x & 31;
-    const int from = turned ? (first ? lane + shift : lane - shift) : lane;
-    uint4 o;
-    o.x = __shfl_sync(0xffffffffu, raw.x, from);
-    o.y = __shfl_sync(0xffffffffu, raw.y, from);
-    o.z = __shfl_sync(0xffffffffu, raw.z, from);
-    o.w = __shfl_sync(0xffffffffu, raw.w, from);
-    if (!turned) return;
-    float other[8];
-    widen8<BF16>(o, other);
-    const int j = 8 * (first ? c : c - shift);
-    const float4* cp = reinterpret_cast<const float4*>(cs + j);
-    const float4* sp = reinterpret_cast<const float4*>(sn + j);
-    const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
-    const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-    const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    static __device__ __forceinline__ void load4(const float* a, float* x)
+    {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(a));
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    }
+    // x: the row's values of this lane, raw their bits (whole warps call this together)
+    template <bool BF16>
+    __device__ __forceinline__ void turn(const uint4& raw, float (&x)[8], int interleaved) const
+    {
+        if (interleaved) {
+            if (!turned) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float own = __fmul_rn(x[e], cc[e]), cross = __fmul_rn(other[e], ss[e]);
-        x[e] = first ? __fsub_rn(own, cross) : __fadd_rn(own, cross);
+            for (int e = 0; e < 4; ++e) {
+                const float a = x[2 * e], b = x[2 * e + 1];
+                x[2 * e] = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
+                x[2 * e + 1] = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
+            }
+            return;
+        }
+        uint4 o;
+        o.x = __shfl_sync(0xffffffffu, raw.x, from);
+        o.y = __shfl_sync(0xffffffffu, raw.y, from);
+        o.z = __shfl_sync(0xffffffffu, raw.z, from);
+        o.w = __shfl_sync(0xffffffffu, raw.w, from);
+        if (!turned) return;
+        float other[8];
+        widen8<BF16>(o, other);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float own = __fmul_rn(x[e], c[e]), cross = __fmul_rn(other[e], s[e]);
+            x[e] = first ? __fsub_rn(own, cross) : __fadd_rn(own, cross);
+        }
     }
-}
+};
 
 // Smallest power of two not below amax / qmax, at least 2^-100; 0 for 0 and NaN for an infinity or NaN.
 // 127 = 1.984375 x 2^6 and 448 = 1.75 x 2^8: the exponent is amax's less 6 or 8, one more where amax's
@@ -112,17 +135,17 @@ __device__ __forceinline__ void decode8(const uint2& w, float (&x)[8])
     }
 }
 
-// One unit with UNIT threads (32: a warp; 256: the block).  The block form holds every row of a page in
-// registers between the maximum and the codes (8 rows a thread at P = 128, D = 128); the warp form reads
-// its rows twice, the second time from the first-level cache.
-template <bool BF16, bool E4M3, int D, int UNIT>
+// One unit.  THREADS = 32: a warp, which reads its few rows twice, the second time from the first-level
+// cache.  Else a block, which holds a page's rows in registers (HELD a thread) between the maximum and
+// the codes.
+template <bool BF16, bool E4M3, int D, int THREADS, int HELD>
 __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
 {
-    constexpr int kRowLanes = D / 8, kRows = UNIT / kRowLanes;      // threads a row, rows a pass
-    constexpr int kHeld = UNIT == 32 ? 1 : 128 / kRows;             // rows a thread holds (block form)
-    const int tid = threadIdx.x % UNIT, c = tid % kRowLanes, r0 = tid / kRowLanes;
+    constexpr bool kWarp = THREADS == 32;
+    constexpr int kRowLanes = D / 8, kRows = THREADS / kRowLanes;  // threads a row, rows a pass
+    const int tid = threadIdx.x % THREADS, c = tid % kRowLanes, r0 = tid / kRowLanes;
     const int slot = unit / (2 * p.heads), rest = unit - slot * 2 * p.heads;
-    const int head = rest >> 1, is_v = rest & 1;
+    const int is_v = rest >= p.heads, head = is_v ? rest - p.heads : rest;
     const int shift = 31 - __clz(p.page);
     auto base = [&](int s) { return (cu_at(p.cu_seqlens, s, p.T) >> shift) + 2 * s; };
     const int s = warp_find(p.n_seq, slot, base);
@@ -135,47 +158,49 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
     if (page < 0) return;
     float* const scale_at = (is_v ? p.v_scale : p.k_scale) + (size_t)page * p.heads + head;
     uint8_t* const codes = (is_v ? p.v : p.k) + ((size_t)page * p.heads + head) * p.page * D + 8 * c;
-    const uint16_t* const src = (is_v ? p.v_new : p.k_new) + (int64_t)(t0 + at * p.page - first) * (is_v ? p.v_stride : p.k_stride) + head * D + 8 * c;
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
-    const int rot = is_v ? 0 : p.rot, half = p.rot >> 1;
+    const uint16_t* const src = (is_v ? p.v_new : p.k_new) + (int64_t)(t0 + at * p.page - first) * stride + head * D + 8 * c;
+    const bool rotated = !is_v && p.rot > 0;
     const float before = lo > 0 ? *scale_at : 0.0f;
 
-    // the rotated row `row` (valid where lo <= row < hi; other lanes of a warp take part in the shuffles)
-    auto load = [&](int row, float (&x)[8]) {
-        const bool mine = row >= lo && row < hi;
-        const uint4 raw = mine ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * stride)) : make_uint4(0, 0, 0, 0);
+    auto fetch = [&](int row) {
+        return row >= lo && row < hi ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * stride)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto value = [&](int row, const uint4& raw, float (&x)[8]) {  // rows outside [lo, hi) come out as zeros
         widen8<BF16>(raw, x);
-        const int64_t at_pos = rot ? (int64_t)min(at * p.page + min(row, p.page - 1), p.n_pos - 1) * half : 0;
-        rotate8<BF16>(raw, x, c, rot, p.interleaved, p.cos + at_pos, p.sin + at_pos);
-        return mine;
+        if (rotated) Angles(p, c, at * p.page + row).turn<BF16>(raw, x, p.interleaved);
+    };
+    auto largest = [](uint32_t amax, const float (&x)[8]) {  // as bits: infinities and NaN come out largest
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+        return amax;
     };
 
-    float held[kHeld][8];
-    uint32_t amax = 0;  // as bits: infinities and NaN come out largest
-    const int rows = UNIT == 32 ? (hi - lo + kRows - 1) / kRows : kHeld;
-    const int start = UNIT == 32 ? lo : 0;
+    float held[HELD][8];
+    uint32_t amax = 0;
+    if constexpr (kWarp) {
+        for (int row = lo + r0; row - r0 < hi; row += kRows) {
+            float x[8];
+            value(row, fetch(row), x);
+            amax = largest(amax, x);
+        }
+    } else {
+        uint4 raw[HELD];
 #pragma unroll
-    for (int i = 0; i < (UNIT == 32 ? 1 : kHeld); ++i) {
-        if (UNIT == 32) {
-            for (int j = 0; j < rows; ++j) {
-                float x[8];
-                if (load(start + j * kRows + r0, x))
+        for (int i = 0; i < HELD; ++i) raw[i] = fetch(i * kRows + r0);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
-            }
-        } else if (i * kRows < p.page) {
-            if (load(i * kRows + r0, held[i]))
-#pragma unroll
-                for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(held[i][e]) & 0x7fffffffu);
+        for (int i = 0; i < HELD; ++i) {
+            value(i * kRows + r0, raw[i], held[i]);
+            amax = largest(amax, held[i]);
         }
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
-    if (UNIT > 32) {
-        __shared__ uint32_t part[kThreads / 32];
+    if constexpr (!kWarp) {
+        __shared__ uint32_t part[THREADS / 32];
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) amax = max(amax, part[w]);
+        for (int w = 0; w < THREADS / 32; ++w) amax = max(amax, part[w]);
     }
     const float need = scale_for<E4M3>(amax);
     const float scale = (before != before || need != need) ? __uint_as_float(0x7fc00000u) : fmaxf(before, need);
@@ -189,76 +214,106 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
             *w = encode8<E4M3>(x, ratio);
         }
     }
-#pragma unroll
-    for (int i = 0; i < (UNIT == 32 ? 1 : kHeld); ++i) {
-        if (UNIT == 32) {
-            for (int j = 0; j < rows; ++j) {
-                float x[8];
-                const int row = start + j * kRows + r0;
-                if (load(row, x)) *reinterpret_cast<uint2*>(codes + (size_t)row * D) = scale > 0.0f ? encode8<E4M3>(x, inv) : make_uint2(0u, 0u);
-            }
-        } else if (i * kRows < p.page) {
-            const int row = i * kRows + r0;
-            if (row >= lo && row < hi) *reinterpret_cast<uint2*>(codes + (size_t)row * D) = scale > 0.0f ? encode8<E4M3>(held[i], inv) : make_uint2(0u, 0u);
+    auto put = [&](int row, const float (&x)[8]) {
+        if (row >= lo && row < hi)
+            *reinterpret_cast<uint2*>(codes + (size_t)row * D) = scale > 0.0f ? encode8<E4M3>(x, inv) : make_uint2(0u, 0u);
+    };
+    if constexpr (kWarp) {
+        for (int row = lo + r0; row - r0 < hi; row += kRows) {
+            float x[8];
+            value(row, fetch(row), x);
+            put(row, x);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) put(i * kRows + r0, held[i]);
     }
     if (tid == 0) *scale_at = scale;
 }
 
-// blocks [0, unit_blocks) store pages; the others rotate queries, 16 bytes a thread
-template <bool BF16, bool E4M3, int D, int UNIT>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p, int units, int unit_blocks)
+// (token, kQueryHeads heads) by D / 8 lanes
+constexpr int kQueryHeads = 8;
+template <bool BF16, int D>
+__device__ __forceinline__ void rotate_queries(const AppendParams& p, int64_t item, int64_t items, int chunks)
+{
+    constexpr int kRowLanes = D / 8;
+    const int c = threadIdx.x % kRowLanes;
+    const int64_t mine = min(item, items - 1);  // lanes past the end take part in shuffles
+    const int t = (int)(mine / chunks), h0 = (int)(mine - (int64_t)t * chunks) * kQueryHeads;
+    int pos = 0;
+    if (p.rot > 0) {
+        // the warp looks for its first token; the others are the same or follow it
+        int s = warp_find(p.n_seq, __shfl_sync(0xffffffffu, t, 0), [&](int i) { return cu_at(p.cu_seqlens, i, p.T); });
+        while (s + 1 < p.n_seq && cu_at(p.cu_seqlens, s + 1, p.T) <= t) ++s;
+        pos = past_at(p.past, s) + t - cu_at(p.cu_seqlens, s, p.T);
+    }
+    const uint16_t* src = p.q + (int64_t)t * p.q_stride + 8 * c;
+    uint16_t* dst = p.q_out + (int64_t)t * p.hq * D + 8 * c;
+    uint4 raw[kQueryHeads];
+#pragma unroll
+    for (int i = 0; i < kQueryHeads; ++i) raw[i] = h0 + i < p.hq ? __ldg(reinterpret_cast<const uint4*>(src + (h0 + i) * D)) : make_uint4(0u, 0u, 0u, 0u);
+    if (p.rot > 0) {
+        const Angles angles(p, c, pos);
+#pragma unroll
+        for (int i = 0; i < kQueryHeads; ++i) {
+            float x[8];
+            widen8<BF16>(raw[i], x);
+            angles.turn<BF16>(raw[i], x, p.interleaved);
+            raw[i] = make_uint4(narrow2<BF16>(x[0], x[1]), narrow2<BF16>(x[2], x[3]), narrow2<BF16>(x[4], x[5]), narrow2<BF16>(x[6], x[7]));
+        }
+    }
+    if (item < items)
+#pragma unroll
+        for (int i = 0; i < kQueryHeads; ++i)
+            if (h0 + i < p.hq) *reinterpret_cast<uint4*>(dst + (h0 + i) * D) = raw[i];
+}
+
+// blocks [0, unit_blocks) store pages, the others rotate queries
+template <bool BF16, bool E4M3, int D, int THREADS, int UNIT, int HELD>
+__global__ void __launch_bounds__(THREADS) kv_append_kernel(AppendParams p, int units, int unit_blocks)
 {
     pdl_wait();
     pdl_launch_dependents();
     if ((int)blockIdx.x < unit_blocks) {
-        const int unit = blockIdx.x * (kThreads / UNIT) + threadIdx.x / UNIT;
-        if (unit < units) store_unit<BF16, E4M3, D, UNIT>(p, unit);
+        const int unit = blockIdx.x * (THREADS / UNIT) + threadIdx.x / UNIT;
+        if (unit < units) store_unit<BF16, E4M3, D, UNIT, HELD>(p, unit);
         return;
     }
-    constexpr int kRowLanes = D / 8, kRows = kThreads / kRowLanes;
-    const int64_t row = (int64_t)(blockIdx.x - unit_blocks) * kRows + threadIdx.x / kRowLanes;
-    const int64_t last = (int64_t)p.T * p.hq - 1;
-    const int64_t mine = min(row, last);  // lanes past the end repeat the last row: they take part in shuffles
-    const int t = (int)(mine / p.hq), head = (int)(mine - (int64_t)t * p.hq), c = threadIdx.x % kRowLanes;
-    // a warp's rows may belong to two sequences: each lane looks for its own
-    int lo = 0, hi = p.n_seq;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu_at(p.cu_seqlens, mid, p.T) <= t) lo = mid; else hi = mid;
-    }
-    const int pos = past_at(p.past, lo) + t - cu_at(p.cu_seqlens, lo, p.T);
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)t * p.q_stride + head * D + 8 * c));
-    float x[8];
-    widen8<BF16>(raw, x);
-    const int64_t at_pos = p.rot ? (int64_t)min(max(pos, 0), p.n_pos - 1) * (p.rot >> 1) : 0;
-    rotate8<BF16>(raw, x, c, p.rot, p.interleaved, p.cos + at_pos, p.sin + at_pos);
-    if (row <= last) {
-        const uint4 w = make_uint4(narrow2<BF16>(x[0], x[1]), narrow2<BF16>(x[2], x[3]), narrow2<BF16>(x[4], x[5]), narrow2<BF16>(x[6], x[7]));
-        *reinterpret_cast<uint4*>(p.q_out + (mine * D + 8 * c)) = w;
-    }
+    const int chunks = (p.hq + kQueryHeads - 1) / kQueryHeads;
+    const int64_t item = (int64_t)(blockIdx.x - unit_blocks) * (THREADS / (D / 8)) + threadIdx.x / (D / 8);
+    rotate_queries<BF16, D>(p, item, (int64_t)p.T * chunks, chunks);
+}
+
+template <bool BF16, bool E4M3, int D, int THREADS, int UNIT, int HELD>
+cudaError_t launch(const AppendParams& p, cudaStream_t stream)
+{
+    const int64_t units = ((int64_t)p.T / p.page + 2 * (int64_t)p.n_seq) * p.heads * 2;
+    const int64_t unit_blocks = (units + THREADS / UNIT - 1) / (THREADS / UNIT);
+    const int64_t items = (int64_t)p.T * ((p.hq + kQueryHeads - 1) / kQueryHeads), per_block = THREADS / (D / 8);
+    const int64_t q_blocks = (items + per_block - 1) / per_block;
+    if (units > 0x7fffffff || unit_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    return launch_k(kv_append_kernel<BF16, E4M3, D, THREADS, UNIT, HELD>, dim3((unsigned)(unit_blocks + q_blocks)), dim3(THREADS), 0, stream, true, p,
+                    (int)units, (int)unit_blocks);
 }
 
 template <bool BF16, bool E4M3, int D>
-cudaError_t launch(const AppendParams& p, cudaStream_t stream)
+cudaError_t launch_page(const AppendParams& p, cudaStream_t stream)
 {
-    // A warp per unit where sequences bring a few tokens each (a block would leave most of its
-    // threads without a row), a block per unit where they fill pages.
-    const bool warp_units = (int64_t)p.T <= 8 * (int64_t)p.n_seq;
-    const int64_t units = ((int64_t)p.T / p.page + 2 * (int64_t)p.n_seq) * p.heads * 2;
-    const int64_t per_block = warp_units ? kThreads / 32 : 1;
-    const int64_t unit_blocks = (units + per_block - 1) / per_block;
-    const int64_t q_blocks = ((int64_t)p.T * p.hq * (D / 8) + kThreads - 1) / kThreads;
-    if (units > 0x7fffffff || unit_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(unit_blocks + q_blocks));
-    if (warp_units) return launch_k(kv_append_kernel<BF16, E4M3, D, 32>, grid, dim3(kThreads), 0, stream, true, p, (int)units, (int)unit_blocks);
-    return launch_k(kv_append_kernel<BF16, E4M3, D, kThreads>, grid, dim3(kThreads), 0, stream, true, p, (int)units, (int)unit_blocks);
+    // A warp per unit where sequences bring a few tokens each (a block would leave most of its threads
+    // without a row), a block per unit where they fill pages: 256 threads with up to 4 rows each, 512
+    // for pages of 16 Ki values.
+    if ((int64_t)p.T <= 8 * (int64_t)p.n_seq) return launch<BF16, E4M3, D, 256, 32, 1>(p, stream);
+    const int lanes = p.page * (D / 8);
+    if (lanes <= 256) return launch<BF16, E4M3, D, 256, 256, 1>(p, stream);
+    if (lanes == 512) return launch<BF16, E4M3, D, 256, 256, 2>(p, stream);
+    if (lanes == 1024) return launch<BF16, E4M3, D, 256, 256, 4>(p, stream);
+    return launch<BF16, E4M3, D, 512, 512, 4>(p, stream);
 }
 
 template <bool BF16, bool E4M3>
 cudaError_t launch_dim(const AppendParams& p, cudaStream_t stream)
 {
-    return p.dim == 64 ? launch<BF16, E4M3, 64>(p, stream) : launch<BF16, E4M3, 128>(p, stream);
+    return p.dim == 64 ? launch_page<BF16, E4M3, 64>(p, stream) : launch_page<BF16, E4M3, 128>(p, stream);
 }
 
 }  // namespace

@@ -25,10 +25,14 @@ constexpr int kCtas = 8;          // CTAs a sequence (the portable cluster size)
 constexpr int kSegment = 512;     // weights a segment: 16 a lane
 constexpr int kMaxSegments = ((1 << 19) / kCtas + kSegment - 1) / kSegment;
 
+// floor(x 2^43) for x in [0, 1], from the number's bits: its 24-bit mantissa times or over a power of
+// two (one 32 x 32 -> 64 multiply-add to a sum; a float-to-64-bit conversion runs at a fraction of that
+// rate).  Below 2^-126 the mantissa's hidden bit is wrong, and shifted out.
 __device__ __forceinline__ uint64_t weight(float x)
 {
-    // NaN and negative values give 0; the product is exact (a power of two) and below 2^44
-    return (uint64_t)__float2ll_rz(fminf(fmaxf(x, 0.0f), 1.0f) * 8796093022208.0f);
+    const uint32_t bits = __float_as_uint(x), mantissa = (bits & 0x7fffffu) | 0x800000u;
+    const int up = (int)(bits >> 23) - 107;  // 2^43 / 2^23 against the exponent's bias of 127
+    return (uint64_t)(mantissa >> min(max(-up, 0), 31)) * (1u << max(up, 0));
 }
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v)
@@ -62,7 +66,7 @@ struct Row {
                 }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = weight(q ? __fsub_rn(a[e], b[e]) : a[e]);
+        for (int e = 0; e < 4; ++e) w[e] = weight(__saturatef(__fsub_rn(a[e], b[e])));  // NaN saturates to 0
     }
 };
 
