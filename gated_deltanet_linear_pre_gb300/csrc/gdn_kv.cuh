@@ -31,6 +31,8 @@ __device__ __forceinline__ int warp_find(int n, int64_t x, F base)
 // past[s], kept where position arithmetic cannot leave 31 bits
 __device__ __forceinline__ int past_at(const int32_t* past, int s) { return min(max(__ldg(past + s), -(1 << 30)), 1 << 30); }
 
+__device__ __forceinline__ int page_shift(const KvBatch& p) { return 31 - __clz(p.page); }
+
 // pool page of table entry `at` of sequence s, or -1 where there is none
 __device__ __forceinline__ int page_at(const KvBatch& p, int s, int at)
 {

@@ -146,7 +146,7 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
     const int tid = threadIdx.x % THREADS, c = tid % kRowLanes, r0 = tid / kRowLanes;
     const int slot = unit / (2 * p.heads), rest = unit - slot * 2 * p.heads;
     const int is_v = rest >= p.heads, head = is_v ? rest - p.heads : rest;
-    const int shift = 31 - __clz(p.page);
+    const int shift = page_shift(p);
     auto base = [&](int s) { return (cu_at(p.cu_seqlens, s, p.T) >> shift) + 2 * s; };
     const int s = warp_find(p.n_seq, slot, base);
     const int t0 = cu_at(p.cu_seqlens, s, p.T), n = cu_at(p.cu_seqlens, s + 1, p.T) - t0, first = past_at(p.past, s);

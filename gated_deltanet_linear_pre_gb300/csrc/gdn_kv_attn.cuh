@@ -18,7 +18,8 @@
 
 namespace gdn {
 
-constexpr int kSub = 16;               // positions of a step tile (a page holds whole ones)
+constexpr int kSub = 16;               // positions of a step tile's part (a page holds whole ones)
+template <int D> constexpr int kStepTile = D == 128 ? kSub : 2 * kSub;  // positions of a step tile: 4 KB of codes
 constexpr int kStepMaxRows = 32;       // query rows of a step unit, at most
 constexpr int kStepMaxWorkers = 512;
 constexpr int kKeys = 128;             // positions of a prompt tile
@@ -159,26 +160,29 @@ __device__ __forceinline__ int scan_find(int n_seq, int64_t x, F weight, ScanSme
 }
 
 // ---- 8-bit codes to fp16 ------------------------------------------------------------
-// Two codes, bytes 0 and 1 (HIGH: 2 and 3) of y, to a pair of fp16 values.  Both conversions are exact
-// and give finite values for every byte, so what lies behind a sequence's end in its last page can do no
-// harm:
+// Two codes, bytes 0 and 1 (HIGH: 2 and 3) of y, to a pair of fp16 values, exactly:
 //   int8: 1024 + (code + 128) assembled as fp16 bits, less 1152;
-//   e4m3: the sign, exponent and mantissa bits moved to their fp16 places, which is the value / 256
-//         (subnormals included); the byte pattern of NaN, which no append writes, reads as 480 / 256.
+//   e4m3: the hardware's conversion.
 template <bool E4M3, bool HIGH>
 __device__ __forceinline__ uint32_t codes2(uint32_t y)
 {
     if (E4M3) {
-        const uint32_t x = __byte_perm(y, 0u, HIGH ? 0x3424 : 0x1404);
-        return ((x >> 1) & 0x3f803f80u) | (x & 0x80008000u);
+        uint32_t h;
+        if (HIGH) asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(h) : "r"(y));
+        else asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(y));
+        return h;
     }
     const uint32_t x = __byte_perm(y ^ 0x80808080u, 0x64646464u, HIGH ? 0x4342 : 0x4140);
     const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half((unsigned short)0x6480)));
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool E4M3>
-constexpr float kCodeUnit = E4M3 ? 256.0f : 1.0f;  // value of a converted code of 1.0
+__device__ __forceinline__ float ex2(float x)  // 2^x; results below 2^-126 are 0
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Power of two that brings a query row (the bits of its largest magnitude) to [2^14, 2^15), and its
 // inverse: fp16 then holds a row of either type, exactly for fp16 and, less what is 2^-29 of the row's

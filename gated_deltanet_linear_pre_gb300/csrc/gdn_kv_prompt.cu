@@ -13,7 +13,7 @@
 // as a third of its softmax; instead one kernel unpacks each long sequence's cache once into images, in
 // the no-swizzle core-matrix order, that a single bulk copy brings in: 4 bytes moved per code byte, a few
 // per cent of a prompt's time.  An image holds code * (page scale / largest scale of the sequence and
-// head) * 2^kUp, exact for pages whose scale is at least 2^-15 (e4m3) or 2^-24 (int8) of the largest after
+// head) * kUp, exact for pages whose scale is at least 2^-15 (e4m3) or 2^-24 (int8) of the largest after
 // the shift; the largest scale itself goes into the scores' unit and the outputs'.
 //
 // A CTA (320 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
@@ -32,9 +32,8 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr float kWeightShift = 7.0f;
 constexpr float kLazy = 8.0f;
 
-// images hold code2 values times 2^kUp: up to 127 x 2^8 and 1.75 x 2^14
-template <bool E4M3> constexpr float kUp = E4M3 ? 16384.0f : 256.0f;
-template <bool E4M3> constexpr float kImageUnit = kCodeUnit<E4M3> / kUp<E4M3>;  // value of an image's 1.0 per unit scale
+// images hold codes times kUp: up to 127 x 2^8 and 448 x 2^6
+template <bool E4M3> constexpr float kUp = E4M3 ? 64.0f : 256.0f;
 
 template <int D> constexpr uint32_t kTileBytes = kKeys * D * 2;
 
@@ -63,7 +62,7 @@ __global__ void __launch_bounds__(kImageThreads) kv_image_kernel(AttnParams p, A
 {
     __shared__ ScanSmem<kImageThreads> scan;
     __shared__ float top_k[kImageThreads / 32], top_v[kImageThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, shift = 31 - __clz(p.page);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, shift = page_shift(p);
     pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == 0 && tid == 0) a.head->error = 0u;
@@ -260,13 +259,6 @@ __device__ __forceinline__ bool wait_for(uint64_t* mbar, uint32_t parity, const 
             if (*abort_flag || clock64() - start > (4ll << 30)) break;
     }
     return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 template <int D, bool BF16, bool E4M3>
@@ -490,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 umma::mbar_arrive(&sm.q_full[h]);
                 const float2 norm = a.norm[(size_t)w.image * p.heads + w.head];
                 // (above 0, so that a masked score of -infinity stays one whatever the scale)
-                coef = fmaxf(back * (fabsf(p.scale) * kLog2e) * (norm.x * kImageUnit<E4M3>), 1e-35f);
+                coef = fmaxf(back * (fabsf(p.scale) * kLog2e) * (norm.x * (1.0f / kUp<E4M3>)), 1e-35f);
             }
             const int limit = valid ? w.v.first + tok : -1;
             const int first_limit = w.v.first + (2 * w.i + h) * tokens;
@@ -563,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
             }
             GDN_KV_WAIT(&sm.o_full[h], o_phase ^ 1u);
             umma::fence_after_sync();
-            const float unit = a.norm[(size_t)w.image * p.heads + w.head].y * kImageUnit<E4M3>;
+            const float unit = a.norm[(size_t)w.image * p.heads + w.head].y * (1.0f / kUp<E4M3>);
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
             const int slot = 2 * blockIdx.x + (w.first ? 0 : 1), row = 128 * h + r;
             const float scale = whole ? (l == 0.0f ? 0.0f : unit / l) : unit;

@@ -7,16 +7,17 @@
 // O^T = V^T P^T (m16n8k16, fp16 operands, fp32 accumulators): keys and channels fill the 16-row side
 // and 8 query rows the other, so 8 rows (a kv head's query heads, times drafted tokens) cost no more
 // than one.  Codes become fp16 exactly (codes2); a page's k scale multiplies its scores in fp32 and its
-// v scale its weights p.  The weights are rounded to fp16 as p r 2^14, r the page's v scale over the
-// largest met so far: 11 bits down to weights 2^-28 of the largest, below which the error stays under
-// 2^-39 of the largest v.  Queries are scaled by a power of two per row to below 2^15: exact for fp16
-// and, less what is 2^-29 of the row's largest, for bf16.
+// v scale its weights p.  The reference m moves only where a score passes it by 8, so most tiles need no
+// exchange between lanes: p stays below 2^8.  The weights are rounded to fp16 as p r 2^7, r the page's v
+// scale over the largest met so far: 11 bits down to 2^-21 of the largest weight, below which the error
+// stays under 2^-32 of the largest v.  Queries are scaled to fp16 by a power of two per row (row_unit).
 //
-// Bound.  HBM: every code is read once.  A warp takes 16 positions at a time straight from global memory
-// into its registers (16-byte loads, whole 128-byte lines), the next 16 in flight while it works on
-// these: the layout of the loads is chosen so that a lane's bytes are the operands it needs (K: 16
-// channels of a row feed 4 K steps; V: the same 16 channels of 4 positions, whose byte pairs one
-// byte permute interleaves), so nothing passes through shared memory.
+// Bound.  HBM: every code is read once.  A warp takes 4 KB of codes at a time; a lane copies (cp.async)
+// exactly the bytes that it will turn into its operands, into shared memory that only it reads, so the
+// ring needs no barrier, the codes in flight cost no registers, and every copy of a warp covers whole
+// 128-byte lines.  The bytes are chosen so that no exchange between lanes is needed: K, 16 channels of
+// a row feed 4 K steps; V, the same 16 channels of 4 positions, whose byte pairs one byte permute
+// interleaves.
 #include "gdn_kv_attn.cuh"
 
 namespace gdn {
@@ -24,7 +25,9 @@ namespace {
 
 constexpr int kStepThreads = 256;
 constexpr int kWarps = kStepThreads / 32;
-constexpr float kWeightUnit = 16384.0f;  // 2^14
+constexpr int kStages = 3;             // tiles of a warp in its ring
+constexpr float kWeightUnit = 128.0f;  // 2^7
+constexpr float kLazy = 8.0f;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -41,83 +44,122 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return y;
 }
 
-// streaming 16- or 8-byte loads of codes (read once)
-__device__ __forceinline__ uint4 ld16(const uint8_t* a) { return __ldcs(reinterpret_cast<const uint4*>(a)); }
-__device__ __forceinline__ uint2 ld8(const uint8_t* a) { return __ldcs(reinterpret_cast<const uint2*>(a)); }
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src)
+{
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
-// 16 positions of a kv head as one lane holds them: K rows g and g + 8, 16-byte chunks t (and t + 4);
-// V rows 2t, 2t + 1, 2t + 8, 2t + 9, channels g (D / 8) onwards
+// A tile of a kv head in a warp's ring, in parts of 16 positions, every lane's bytes at [..][lane]:
+// K rows g and g + 8, 16-byte chunks t (and t + 4); V rows 2t, 2t + 1, 2t + 8, 2t + 9, channels g (D / 8)
+// onwards
 template <int D>
 struct Tile {
-    uint32_t k[D / 64][2][4];
-    uint32_t v[4][D / 32];
-    float ks, vs;  // the page's scales
-    int page;      // -1: not there, nothing is seen
+    static constexpr int kParts = kStepTile<D> / kSub;
+    uint4 k[kParts][D / 64][2][32];
+    uint32_t v[kParts][4][32][D / 32];
+};
 
-    __device__ __forceinline__ void load(const KvBatch& p, int page_, int head, int in_page, int lane)
+// what a lane keeps of a tile on its way: each part's page (-1: not there) and scales
+template <int D>
+struct Pages {
+    int page[Tile<D>::kParts];
+    float ks[Tile<D>::kParts], vs[Tile<D>::kParts];
+};
+
+// a unit's cache as a lane reads it
+template <int D>
+struct Source {
+    const uint8_t *k, *v;        // its bytes of row 0 of page 0
+    const float *ks, *vs;
+    const int32_t* table;
+    int64_t page_bytes;
+    int heads, n_pages, shift, mask;
+
+    __device__ __forceinline__ Source(const KvBatch& p, int s, int head, int lane)
+        : table(p.table + (size_t)s * p.table_stride), page_bytes((int64_t)p.heads * p.page * D), heads(p.heads), n_pages(p.n_pages),
+          shift(page_shift(p)), mask(p.page - 1)
     {
-        page = page_;
-        const size_t at = (size_t)max(page_, 0) * p.heads + head;
-        ks = __ldg(p.k_scale + at);
-        vs = __ldg(p.v_scale + at);
-        const size_t base = (at * p.page + in_page) * D;
-        const int g = lane >> 2, t = lane & 3;
+        const int g = lane >> 2, t = lane & 3, at = head * p.page * D;
+        k = p.k + at + g * D + 16 * t;
+        v = p.v + at + 2 * t * D + g * (D / 8);
+        ks = p.k_scale + head;
+        vs = p.v_scale + head;
+    }
+    // the pages of tile j (pos < kv <= max_pages * page: the entries exist)
+    __device__ __forceinline__ void look(int j, int kv, int (&page)[Tile<D>::kParts]) const
+    {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int i = 0; i < Tile<D>::kParts; ++i) {
+            const int pos = j * kStepTile<D> + i * kSub;
+            const int x = pos < kv ? __ldg(table + (pos >> shift)) : -1;
+            page[i] = x < n_pages ? x : -1;
+        }
+    }
+    __device__ __forceinline__ void load(Tile<D>& tile, Pages<D>& pages, const int (&page)[Tile<D>::kParts], int j, int lane) const
+    {
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                const uint4 w = ld16(p.k + base + (g + 8 * r) * D + 64 * h + 16 * t);
-                k[h][r][0] = w.x; k[h][r][1] = w.y; k[h][r][2] = w.z; k[h][r][3] = w.w;
-            }
+        for (int i = 0; i < Tile<D>::kParts; ++i) {
+            pages.page[i] = page[i];
+            const int x = max(page[i], 0);  // (a missing page: any, its scores are masked)
+            pages.ks[i] = __ldg(ks + (int64_t)x * heads);
+            pages.vs[i] = __ldg(vs + (int64_t)x * heads);
+            const int64_t at = x * page_bytes + ((j * kStepTile<D> + i * kSub) & mask) * D;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint8_t* a = p.v + base + (2 * t + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8);
-            if constexpr (D == 128) {
-                const uint4 w = ld16(a);
-                v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
-            } else {
-                const uint2 w = ld8(a);
-                v[i][0] = w.x; v[i][1] = w.y;
-            }
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) copy_async<16>(&tile.k[i][h][r][lane], k + at + 8 * r * D + 64 * h);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) copy_async<D / 8>(&tile.v[i][r][lane][0], v + at + ((r & 1) + 8 * (r >> 1)) * D);
         }
     }
 };
 
-// shared memory: each warp's statistics and output of the unit in hand
 template <int D, int NT>
 struct StepSmem {
     static constexpr int R = 8 * NT, kStride = D + 4;
-    float o[kWarps][R][kStride];
+    union {
+        Tile<D> ring[kWarps][kStages];
+        float o[kWarps][R][kStride];  // each warp's output of the unit in hand, once its keys are done
+        ScanSmem<kStepThreads> scan;  // before the first unit
+    };
+    uint2 q[NT][D / 16][32];          // queries as B operands: row g of each 8, K step, lane
+    float coef[R];                    // a row's score unit
+    int limit[R];                     // last position it sees
     float m[kWarps][R], l[kWarps][R], unit[kWarps];
-    ScanSmem<kStepThreads> scan;
 };
 
 // row groups and key tiles of a sequence (a unit that sees nothing still writes its zeros: one tile)
-template <int NT>
+template <int D, int NT>
 __device__ __forceinline__ void step_units(const KvBatch& p, const AttnSpace& a, int s, const SeqView& v, int& groups, int& tiles)
 {
     constexpr int R = 8 * NT;
     const int64_t rows = (int64_t)v.n * (p.hq / p.heads);
     groups = is_long(p, a, s, v) ? 0 : (int)((rows + R - 1) / R);
-    tiles = max((v.kv + kSub - 1) / kSub, 1);
+    tiles = max((v.kv + kStepTile<D> - 1) / kStepTile<D>, 1);
 }
 
 template <int D, bool BF16, bool E4M3, int NT>
-__global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(AttnParams p, AttnSpace a)
+__global__ void __launch_bounds__(kStepThreads, NT == 4 ? 1 : 2) kv_step_kernel(AttnParams p, AttnSpace a)
 {
     constexpr int R = 8 * NT, KS = D / 16, MT = D / 16;
     using Smem = StepSmem<D, NT>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int group = p.hq / p.heads, shift = 31 - __clz(p.page);
+    const int group = p.hq / p.heads;
     pdl_wait();
     pdl_launch_dependents();
 
     // ---- this worker's range of the batch's tiles ----
     auto weight = [&](int s) {
         int groups, tiles;
-        step_units<NT>(p, a, s, seq_view(p, s), groups, tiles);
+        step_units<D, NT>(p, a, s, seq_view(p, s), groups, tiles);
         return (int64_t)p.heads * groups * tiles;
     };
     const int64_t total = scan_total<kStepThreads>(p.n_seq, weight, sm.scan);
@@ -139,9 +181,9 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
     for (int64_t x = lo; x < hi && s < p.n_seq; ++s) {
         const SeqView v = seq_view(p, s);
         int groups, tiles;
-        step_units<NT>(p, a, s, v, groups, tiles);
+        step_units<D, NT>(p, a, s, v, groups, tiles);
         const int64_t units = (int64_t)p.heads * groups;
-        for (int64_t unit = tiles ? at / tiles : 0; unit < units && x < hi; ++unit) {
+        for (int64_t unit = at / tiles; unit < units && x < hi; ++unit) {
             const int j0 = (int)(at - unit * tiles), j1 = (int)min((int64_t)tiles, j0 + (hi - x));
             at = (unit + 1) * tiles;
             x += j1 - j0;
@@ -149,173 +191,199 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
             const int rows = v.n * group;
             if (first_unit && tid == 0) a.step_cut[blockIdx.x] = Cut{s, head, row0, j0, tiles};
 
-            // queries: B operands (row g of each 8), scaled per row; the factor goes into the row's score unit
-            uint32_t qf[NT][KS][2];
-            float coef[NT][2];
-            int limit[NT][2];
+            // the warp's first tiles on their way
+            constexpr int kParts = Tile<D>::kParts;
+            const Source<D> src(p, s, head, lane);
+            Tile<D>* const ring = sm.ring[warp];
+            Pages<D> pages[kStages];
+            int j = j0 + warp, next_page[kParts];
+            src.look(j, j < j1 ? v.kv : 0, next_page);
+            __syncthreads();  // the last unit's outputs and queries are read
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int row = row0 + 8 * nt + g;
+            for (int i = 0; i < kStages - 1; ++i) {
+                if (j + i * kWarps < j1) src.load(ring[i], pages[i], next_page, j + i * kWarps, lane);
+                copy_commit();
+                src.look(j + (i + 1) * kWarps, j + (i + 1) * kWarps < j1 ? v.kv : 0, next_page);
+            }
+
+            // queries as B operands, scaled per row; the factor goes into the row's score unit
+            for (int nt = warp; nt < NT; nt += kWarps) {
+                const int row = row0 + 8 * nt + g, i = row / group, qh = row - i * group;
+                const uint16_t* from = p.q + (int64_t)(v.t0 + i) * p.q_stride + (head * group + qh) * D;
                 uint2 raw[KS];
-                uint32_t amax = 0;
-                const int i = row / group, qh = row - i * group;
-                const uint16_t* src = p.q + (int64_t)(v.t0 + i) * p.q_stride + (head * group + qh) * D;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-                    raw[ks] = row < rows ? __ldg(reinterpret_cast<const uint2*>(src + 64 * (ks >> 2) + 16 * t + 4 * (ks & 3))) : make_uint2(0u, 0u);
+                    raw[ks] = row < rows ? __ldg(reinterpret_cast<const uint2*>(from + 64 * (ks >> 2) + 16 * t + 4 * (ks & 3))) : make_uint2(0u, 0u);
                 float f[KS][4];
+                uint32_t amax = 0;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const uint32_t r2[2] = {raw[ks].x, raw[ks].y};
+                for (int ks = 0; ks < KS; ks += 2) {
+                    float y[8];
+                    widen8<BF16>(make_uint4(raw[ks].x, raw[ks].y, raw[ks + 1].x, raw[ks + 1].y), y);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (BF16) {
-                            f[ks][2 * e] = __uint_as_float(r2[e] << 16);
-                            f[ks][2 * e + 1] = __uint_as_float(r2[e] & 0xffff0000u);
-                        } else {
-                            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&r2[e]));
-                            f[ks][2 * e] = h.x;
-                            f[ks][2 * e + 1] = h.y;
-                        }
+                    for (int e = 0; e < 8; ++e) {
+                        f[ks + (e >> 2)][e & 3] = y[e];
+                        amax = max(amax, __float_as_uint(y[e]) & 0x7fffffffu);
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) amax = max(amax, __float_as_uint(f[ks][e]) & 0x7fffffffu);
                 }
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 float mul, back;
                 row_unit(amax, mul, back);
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    qf[nt][ks][0] = narrow2<false>(f[ks][0] * mul, f[ks][1] * mul);
-                    qf[nt][ks][1] = narrow2<false>(f[ks][2] * mul, f[ks][3] * mul);
-                }
-                const float unit_of = back * (p.scale * kLog2e) * kCodeUnit<E4M3>;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    coef[nt][e] = __shfl_sync(0xffffffffu, unit_of, (2 * t + e) * 4);
-                    const int col = row0 + 8 * nt + 2 * t + e;
-                    limit[nt][e] = col < rows ? v.first + col / group : -1;
+                for (int ks = 0; ks < KS; ++ks)
+                    sm.q[nt][ks][lane] = make_uint2(narrow2<false>(f[ks][0] * mul, f[ks][1] * mul), narrow2<false>(f[ks][2] * mul, f[ks][3] * mul));
+                if (t == 0) {
+                    sm.coef[8 * nt + g] = back * (p.scale * kLog2e);
+                    sm.limit[8 * nt + g] = row < rows ? v.first + i : -1;
                 }
             }
+            __syncthreads();
+            float coef[NT][2];
+            int limit[NT][2];
             const int first_limit = v.first + row0 / group;  // the smallest of the unit's rows
-
-            float o[NT][MT][4], m[NT][2], l[NT][2], unit_v = 0.0f;
+            bool seen = false;                               // the warp has met a score
+            float o[NT][MT][4], m[NT][2], l[NT][2], unit_v = 0.0f, inv_v = 0.0f;  // inv_v: kWeightUnit / unit_v
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.0f;
-                m[nt][0] = m[nt][1] = -INFINITY;
-                l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    m[nt][e] = 0.0f;
+                    l[nt][e] = 0.0f;
+                    coef[nt][e] = sm.coef[8 * nt + 2 * t + e];
+                    limit[nt][e] = sm.limit[8 * nt + 2 * t + e];
+                }
             }
 
-            auto work = [&](const Tile<D>& tile, int j) {
-                float x2[NT][4];
+            // part `i` of a tile: positions pos onwards
+            auto work = [&](const Tile<D>& tile, const Pages<D>& pg, int i, int pos) {
+                float x[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) x2[nt][0] = x2[nt][1] = x2[nt][2] = x2[nt][3] = 0.0f;
+                for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const uint32_t r0 = tile.k[ks >> 2][0][ks & 3], r1 = tile.k[ks >> 2][1][ks & 3];
-                    const uint32_t a[4] = {codes2<E4M3, false>(r0), codes2<E4M3, false>(r1), codes2<E4M3, true>(r0), codes2<E4M3, true>(r1)};
+                for (int h = 0; h < D / 64; ++h) {
+                    const uint4 w0 = tile.k[i][h][0][lane], w1 = tile.k[i][h][1][lane];
+                    const uint32_t r0[4] = {w0.x, w0.y, w0.z, w0.w}, r1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(x2[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-                }
-                const bool masked = j * kSub + kSub - 1 > first_limit || tile.page < 0;
-                bool grew = false;
-                float keep[NT][2];
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t ka[4] = {codes2<E4M3, false>(r0[c]), codes2<E4M3, false>(r1[c]), codes2<E4M3, true>(r0[c]), codes2<E4M3, true>(r1[c])};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x2[nt][e] *= coef[nt][e & 1] * tile.ks;
-                        if (masked && (tile.page < 0 || j * kSub + g + 8 * (e >> 1) > limit[nt][e & 1])) x2[nt][e] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(x2[nt][e], x2[nt][2 + e]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        keep[nt][e] = 1.0f;
-                        if (mx > m[nt][e]) {
-                            keep[nt][e] = exp2f(m[nt][e] - mx);
-                            m[nt][e] = mx;
-                            grew = true;
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint2 b = sm.q[nt][4 * h + c][lane];
+                            mma16816(x[nt], ka, b.x, b.y);
                         }
                     }
                 }
-                // the v unit: the largest page scale met so far (a power of two)
-                float up = 1.0f;
-                if (tile.vs > unit_v) {
-                    up = unit_v / tile.vs;
-                    unit_v = tile.vs;
-                    grew = true;
+                const float vs = pg.vs[i];
+                const bool there = pg.page[i] >= 0, masked = pos + kSub - 1 > first_limit || !there;
+                float top = -INFINITY;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float c2[2] = {coef[nt][0] * pg.ks[i], coef[nt][1] * pg.ks[i]};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[nt][e] = fmaf(x[nt][e], c2[e & 1], -m[nt][e & 1]);  // m: 0 until the first score is seen
+                        if (masked && (!there || pos + g + 8 * (e >> 1) > limit[nt][e & 1])) x[nt][e] = -INFINITY;
+                        top = fmaxf(top, x[nt][e]);
+                    }
                 }
-                if (__any_sync(0xffffffffu, grew)) {
+                // a score passes its row's reference by kLazy, or is the warp's first (a row that the first tile
+                // with any score leaves out sees none of the later ones either): references move to the maxima
+                const bool first = !seen && __any_sync(0xffffffffu, top > -INFINITY);
+                const bool grows = there && vs > unit_v;
+                if (__any_sync(0xffffffffu, top > kLazy) || first || grows) {
+                    float up = 1.0f;
+                    if (grows) {  // the v unit: the largest page scale met so far (a power of two)
+                        up = unit_v * __frcp_rn(vs);
+                        unit_v = vs;
+                        inv_v = kWeightUnit * __frcp_rn(vs);
+                    }
+                    seen = seen || first;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
+                        float keep[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) l[nt][e] *= keep[nt][e];
+                        for (int e = 0; e < 2; ++e) {
+                            float mx = fmaxf(x[nt][e], x[nt][2 + e]);
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                            // by how much the reference moves (with the first scores, down as well as up)
+                            const float by = mx > 0.0f || (first && mx > -INFINITY) ? mx : 0.0f;
+                            keep[e] = first ? 1.0f : ex2(-by);
+                            m[nt][e] += by;
+                            l[nt][e] *= keep[e];
+                            x[nt][e] -= by;
+                            x[nt][2 + e] -= by;
+                        }
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= keep[nt][e & 1] * up;
+                            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= keep[e & 1] * up;
                     }
                 }
                 // (a page whose v are all 0 has scale 0; a NaN scale makes every weight NaN)
-                const float r = unit_v > 0.0f ? tile.vs / unit_v * kWeightUnit : tile.vs;
+                const float r = unit_v > 0.0f ? vs * inv_v : vs;
                 uint32_t b[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float mm = m[nt][e & 1];
-                        w[e] = exp2f(x2[nt][e] - (mm == -INFINITY ? 0.0f : mm));
+                        w[e] = ex2(x[nt][e]);
                         l[nt][e & 1] += w[e];
+                        w[e] *= r;
                         // a masked position has weight 0 even where its page's scale is NaN
-                        w[e] = x2[nt][e] == -INFINITY ? 0.0f : w[e] * r;
+                        if (masked && x[nt][e] == -INFINITY) w[e] = 0.0f;
                     }
                     b[nt][0] = transpose8x8(narrow2<false>(w[0], w[1]));
                     b[nt][1] = transpose8x8(narrow2<false>(w[2], w[3]));
                 }
+                constexpr int W = D / 32;
+                uint32_t vw[4][W];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                    for (int y = 0; y < W; ++y) vw[c][y] = tile.v[i][c][lane][y];
+                    // positions past the sequence's end hold anything: their codes count as 0
+                    if (masked && (!there || pos + 2 * t + (c & 1) + 8 * (c >> 1) >= v.kv))
+#pragma unroll
+                        for (int y = 0; y < W; ++y) vw[c][y] = 0u;
+                }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const uint32_t sel = mt & 1 ? 0x7362 : 0x5140;
-                    const uint32_t y0 = __byte_perm(tile.v[0][mt >> 1], tile.v[1][mt >> 1], sel);
-                    const uint32_t y1 = __byte_perm(tile.v[2][mt >> 1], tile.v[3][mt >> 1], sel);
-                    const uint32_t a[4] = {codes2<E4M3, false>(y0), codes2<E4M3, true>(y0), codes2<E4M3, false>(y1), codes2<E4M3, true>(y1)};
+                    const uint32_t y0 = __byte_perm(vw[0][mt >> 1], vw[1][mt >> 1], sel);
+                    const uint32_t y1 = __byte_perm(vw[2][mt >> 1], vw[3][mt >> 1], sel);
+                    const uint32_t va[4] = {codes2<E4M3, false>(y0), codes2<E4M3, true>(y0), codes2<E4M3, false>(y1), codes2<E4M3, true>(y1)};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][mt], a, b[nt][0], b[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][mt], va, b[nt][0], b[nt][1]);
                 }
             };
 
-            // the warp's tiles of the unit, the next one's codes in flight and the page after that looked up
-            auto page_of = [&](int j) { return j < j1 ? page_at(p, s, (j * kSub) >> shift) : -1; };
-            const int in_mask = p.page - 1;
-            int j = j0 + warp;
-            if (j < j1) {
-                Tile<D> t0, t1;
-                t0.load(p, page_of(j), head, (j * kSub) & in_mask, lane);
-                int next = page_of(j + kWarps);
-                while (true) {
-                    if (j + kWarps < j1) t1.load(p, next, head, ((j + kWarps) * kSub) & in_mask, lane);
-                    next = page_of(j + 2 * kWarps);
-                    work(t0, j);
-                    j += kWarps;
-                    if (j >= j1) break;
-                    if (j + kWarps < j1) t0.load(p, next, head, ((j + kWarps) * kSub) & in_mask, lane);
-                    next = page_of(j + 2 * kWarps);
-                    work(t1, j);
+            // the warp's tiles of the unit: kStages - 1 ahead in flight, the pages of the next one looked up
+            while (j < j1) {
+#pragma unroll
+                for (int i = 0; i < kStages; ++i) {
+                    constexpr int ahead = kStages - 1;
+                    const int to = (i + ahead) % kStages;
+                    if (j + ahead * kWarps < j1) src.load(ring[to], pages[to], next_page, j + ahead * kWarps, lane);
+                    copy_commit();
+                    src.look(j + kStages * kWarps, j + kStages * kWarps < j1 ? v.kv : 0, next_page);
+                    copy_wait<ahead>();
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part) work(ring[i], pages[i], part, j * kStepTile<D> + part * kSub);
                     j += kWarps;
                     if (j >= j1) break;
                 }
             }
 
             // ---- join the warps ----
-            __syncthreads();  // the last unit's values are read
+            __syncthreads();  // every ring is done with
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -326,7 +394,7 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
                     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                     const int row = 8 * nt + 2 * t + e;
                     if (g == 0) {
-                        sm.m[warp][row] = m[nt][e];
+                        sm.m[warp][row] = sum == 0.0f ? -INFINITY : m[nt][e];
                         sm.l[warp][row] = sum;
                     }
 #pragma unroll
@@ -351,9 +419,9 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
                 for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float f = exp2f(sm.m[w][row] - ref);
+                    const float f = ex2(sm.m[w][row] - ref);
                     sum += f * sm.l[w][row];
-                    const float fo = f * (sm.unit[w] > 0.0f ? sm.unit[w] * (kCodeUnit<E4M3> / kWeightUnit) : 1.0f);
+                    const float fo = f * (sm.unit[w] > 0.0f ? sm.unit[w] * (1.0f / kWeightUnit) : 1.0f);
 #pragma unroll
                     for (int e = 0; e < E; ++e) acc[e] += fo * sm.o[w][row][lane * E + e];
                 }
@@ -378,7 +446,7 @@ __global__ void __launch_bounds__(kStepThreads, NT == 1 ? 2 : 1) kv_step_kernel(
 
 // Block (w, row): where range w is the first that begins inside a unit, joins that unit's parts for one
 // query row, in the order of their ranges.
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttnParams p, AttnSpace a)
 {
@@ -389,11 +457,12 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttnParams p, Att
     pdl_launch_dependents();
     const int w = (int)blockIdx.x + 1, row = blockIdx.y;
     const int workers = a.head->step_workers;
+    const int64_t total = a.head->step_total;
     if (w >= workers) return;
     const Cut cut = a.step_cut[w];
     if (cut.j0 == 0) return;
-    const int64_t total = a.head->step_total, begin = cut_start(total, workers, w) - cut.j0;
-    if (cut_start(total, workers, w - 1) > begin) return;
+    const int64_t begin = cut_start(total, workers, w) - cut.j0, prev = cut_start(total, workers, w - 1);
+    if (prev > begin) return;
     const int t0 = cu_at(p.cu_seqlens, cut.s, p.T), n = cu_at(p.cu_seqlens, cut.s + 1, p.T) - t0;
     if (cut.unit + row >= n * group) return;
     const int last = cut_of(total, workers, begin + cut.tiles - 1);
@@ -403,11 +472,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttnParams p, Att
 #pragma unroll 4
     for (int i = w - 1 + warp; i <= last; i += W) {
         // the unit is the first of every range but the one that it begins in the middle of
-        const int slot = 2 * i + (cut_start(total, workers, i) >= begin ? 0 : 1);
+        const int slot = 2 * i + (i == w - 1 && prev < begin ? 1 : 0);
         const float2 st = a.step_stat[(size_t)slot * kStepMaxRows + row];
         const float* src = a.step_out + ((size_t)slot * kStepMaxRows + row) * D + lane * E;
         const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.0f : next;
-        const float f0 = exp2f(top - ref), f1 = exp2f(st.x - ref);
+        const float f0 = ex2(top - ref), f1 = ex2(st.x - ref);
         sum = sum * f0 + st.y * f1;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + src[e] * f1;
@@ -427,7 +496,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttnParams p, Att
     const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        const float f = exp2f(part_m[i] - ref);
+        const float f = ex2(part_m[i] - ref);
         l += f * part_l[i];
         x0 += f * part[i][2 * tid];
         x1 += f * part[i][2 * tid + 1];
@@ -442,20 +511,20 @@ cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_
 {
     auto kernel = kv_step_kernel<D, BF16, E4M3, NT>;
     const size_t smem = sizeof(StepSmem<D, NT>);
+    static_assert(sizeof(StepSmem<D, NT>) <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int grid = min(sms * (NT == 1 ? 2 : 1), kStepMaxWorkers);
+    const int grid = min(sms * (NT == 4 ? 1 : 2), kStepMaxWorkers);
     e = launch_k(kernel, dim3(grid), dim3(kStepThreads), smem, stream, true, p, a);
-    if (e != cudaSuccess) return e;
-    if (grid == 1) return cudaSuccess;
+    if (e != cudaSuccess || grid == 1) return e;
     return launch_k(kv_join_kernel<D, BF16>, dim3(grid - 1, 8 * NT), dim3(kJoinThreads), 0, stream, true, p, a);
 }
 
 template <int D, bool BF16, bool E4M3>
 cudaError_t launch_rows(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
-    // query rows of an average sequence decide the tile: 8 rows as long as they hold them (two blocks an
-    // SM), else 16 or 32 (a warp's codes serve more rows, at one block an SM)
+    // query rows of an average sequence decide the tile: 8 rows as long as they hold them, else 16 or 32
+    // (a warp's codes serve more rows)
     const int64_t rows = ((int64_t)p.T * (p.hq / p.heads) + p.n_seq - 1) / p.n_seq;
     if (rows <= 8) return launch<D, BF16, E4M3, 1>(p, a, sms, stream);
     if (rows <= 16) return launch<D, BF16, E4M3, 2>(p, a, sms, stream);
