@@ -8,10 +8,11 @@
 // and single tokens, and a captured call follows its lengths.
 //
 // Work is counted in key tiles: a unit is (sequence, kv head, group of query rows) and costs the tiles
-// that it sees.  The units of a batch, end to end, are cut into equal ranges, one per worker (CTA), so
-// that one long sequence and many short ones load the GPU alike.  A unit that lies in one range is
-// finished by its worker; one that is cut leaves a partial (maximum, sum, output) per worker, and a last
-// kernel joins them in the order of the ranges.
+// that it sees and a constant for its beginning and end.  The units of a batch, end to end, are cut into
+// equal ranges, one per worker (CTA), so that one long sequence and many short ones load the GPU alike.  A
+// unit whose tiles lie in one range is finished by its worker; one that is cut leaves a partial (maximum,
+// sum, output) per worker, and a last kernel joins them in the order of the ranges.  A range that ends
+// within a unit's constant has none of its tiles.
 #pragma once
 
 #include "gdn_kv.cuh"
@@ -21,7 +22,9 @@ namespace gdn {
 constexpr int kSub = 16;               // positions of a step tile's part (a page holds whole ones)
 template <int D> constexpr int kStepTile = D == 128 ? kSub : 2 * kSub;  // positions of a step tile: 4 KB of codes
 constexpr int kStepMaxRows = 32;       // query rows of a step unit, at most
-constexpr int kStepMaxWorkers = 512;
+constexpr int kStepMaxWorkers = 640;
+constexpr int kStepUnitCost = 16;      // a step unit's beginning and end, in tiles
+constexpr int kPromptUnitCost = 1;     // a prompt unit's
 constexpr int kKeys = 128;             // positions of a prompt tile
 constexpr int kUnitRows = 256;         // query rows of a prompt unit: two halves of 128
 constexpr int kPromptMaxWorkers = 160;
@@ -49,6 +52,8 @@ __device__ __forceinline__ SeqView seq_view(const KvBatch& p, int s)
 // where the range of a worker begins: tile j0 of a unit of `tiles`
 struct Cut {
     int s, head, unit, j0, tiles;  // unit: the step unit's first row, the prompt unit's index
+    int from;                      // cost of the unit that lies before the range
+    int64_t lo;                    // cost of all units that does
 };
 
 struct AttnHeader {
@@ -89,7 +94,7 @@ __device__ __forceinline__ int cut_of(int64_t total, int workers, int64_t x) { r
 // ---- where a worker's range begins -------------------------------------------------
 template <int THREADS>
 struct ScanSmem {
-    int64_t chunk[256];  // sums over every THREADS sequences (at most 65535 of them)
+    int64_t chunk[65536 / THREADS + 1];  // sums over every THREADS sequences (at most 65535 of them)
     int64_t prefix[THREADS + 1], warp_sum[THREADS / 32];
     int found;
 };

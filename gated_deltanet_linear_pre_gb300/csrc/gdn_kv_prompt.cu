@@ -172,8 +172,11 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 
 // tokens of a unit: two halves of floor(128 / group)
 __device__ __forceinline__ int half_tokens(int group) { return (kUnitRows / 2) / group; }
-// key tiles that units before unit i of a (sequence, head) see together (none of them the last one)
-__device__ __forceinline__ int64_t unit_prefix(const SeqView& v, int span, int i) { return floor_sum(i, kKeys, span, (int64_t)v.first + span + kKeys - 1); }
+// cost of the units before unit i of a (sequence, head) (none of them the last one)
+__device__ __forceinline__ int64_t unit_prefix(const SeqView& v, int span, int i)
+{
+    return floor_sum(i, kKeys, span, (int64_t)v.first + span + kKeys - 1) + (int64_t)i * kPromptUnitCost;
+}
 __device__ __forceinline__ int unit_tiles(const SeqView& v, int span, int i) { return (v.first + min((i + 1) * span, v.n) + kKeys - 1) / kKeys; }
 
 // A worker's units in order; every role of the CTA walks the same ones.
@@ -183,7 +186,8 @@ struct Walk {
     int span;                 // tokens a unit
     int s, head, i, units;    // sequence, kv head, unit
     int j0, j1, tiles;        // this worker's tiles of the unit
-    int64_t left;             // tiles of the range from here on
+    int from, to;             // and costs
+    int64_t left;             // cost of the range from here on
     int64_t image;            // image tile of the sequence's first positions
     SeqView v;
     bool first;
@@ -194,7 +198,7 @@ struct Walk {
         s = c.s;
         head = c.head;
         i = c.unit;
-        j0 = c.j0;
+        from = c.from;
         enter();
         here();
     }
@@ -207,14 +211,17 @@ struct Walk {
     __device__ __forceinline__ void here()
     {
         tiles = unit_tiles(v, span, i);
-        j1 = (int)min((int64_t)tiles, j0 + left);
+        to = (int)min((int64_t)tiles + kPromptUnitCost, from + left);
+        j0 = max(from - kPromptUnitCost, 0);
+        j1 = to - kPromptUnitCost;
+        if (j1 <= 0) left = 0;  // the range ends within the unit's constant
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
     __device__ __forceinline__ void next()
     {
-        left -= j1 - j0;
+        left -= to - from;
         first = false;
-        j0 = 0;
+        from = 0;
         if (left <= 0) return;
         if (++i == units) {
             i = 0;
@@ -281,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         const SeqView v = seq_view(p, s);
         if (!is_long(p, a, s, v)) return (int64_t)0;
         const int last = (v.n + span - 1) / span - 1;
-        return p.heads * (unit_prefix(v, span, last) + unit_tiles(v, span, last));
+        return p.heads * (unit_prefix(v, span, last) + unit_tiles(v, span, last) + kPromptUnitCost);
     };
     const int64_t total = scan_total<kThreads>(p.n_seq, weight, scan);
     const int workers = (int)min((int64_t)gridDim.x, total);
@@ -297,12 +304,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         if (warp == 0) {
             const SeqView v = seq_view(p, s);
             const int units = (v.n + span - 1) / span;
-            const int64_t per_head = unit_prefix(v, span, units - 1) + unit_tiles(v, span, units - 1);
+            const int64_t per_head = unit_prefix(v, span, units - 1) + unit_tiles(v, span, units - 1) + kPromptUnitCost;
             const int head = (int)((lo - before) / per_head);
             const int64_t rest = lo - before - head * per_head;
             const int i = warp_find(units, rest, [&](int u) { return unit_prefix(v, span, u); });
             if (lane == 0) {
-                sm.start = Cut{s, head, i, (int)(rest - unit_prefix(v, span, i)), unit_tiles(v, span, i)};
+                const int from = (int)(rest - unit_prefix(v, span, i));
+                sm.start = Cut{s, head, i, max(from - kPromptUnitCost, 0), unit_tiles(v, span, i), from, lo};
                 a.prompt_cut[blockIdx.x] = sm.start;
             }
         }
@@ -611,10 +619,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_prompt_join_kernel(AttnParams
     const int w = (int)blockIdx.x + 1, workers = a.head->prompt_workers;
     if (w >= workers) return;
     const Cut cut = a.prompt_cut[w];
-    if (cut.j0 == 0) return;
-    const int64_t total = a.head->prompt_total, begin = cut_start(total, workers, w) - cut.j0;
-    if (cut_start(total, workers, w - 1) > begin) return;
-    const int last = cut_of(total, workers, begin + cut.tiles - 1);
+    const int64_t total = a.head->prompt_total, begin = cut.lo - cut.from, prev = a.prompt_cut[w - 1].lo;
+    if (cut.j0 == 0 || prev > begin + kPromptUnitCost) return;
+    const int last = cut_of(total, workers, begin + kPromptUnitCost + cut.tiles - 1);
     const int row = blockIdx.y * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
     const int h = row >> 7, r = row & 127, i_tok = r / group, qh = r - i_tok * group;
     const int t0 = cu_at(p.cu_seqlens, cut.s, p.T), n = cu_at(p.cu_seqlens, cut.s + 1, p.T) - t0;
@@ -626,7 +633,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_prompt_join_kernel(AttnParams
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int i = w - 1; i <= last; ++i) {
-        const int slot = 2 * i + (cut_start(total, workers, i) >= begin ? 0 : 1);
+        const int slot = 2 * i + (i == w - 1 && prev < begin ? 1 : 0);
         const float2 st = a.prompt_stat[(size_t)slot * kUnitRows + row];
         const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.0f : next;
         const float f0 = exp2f(top - ref), f1 = exp2f(st.x - ref);

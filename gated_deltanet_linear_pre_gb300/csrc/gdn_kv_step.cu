@@ -23,7 +23,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 128;
 constexpr int kWarps = kStepThreads / 32;
 constexpr int kStages = 3;             // tiles of a warp in its ring
 constexpr float kWeightUnit = 128.0f;  // 2^7
@@ -145,7 +145,7 @@ __device__ __forceinline__ void step_units(const KvBatch& p, const AttnSpace& a,
 }
 
 template <int D, bool BF16, bool E4M3, int NT>
-__global__ void __launch_bounds__(kStepThreads, NT == 4 ? 1 : 2) kv_step_kernel(AttnParams p, AttnSpace a)
+__global__ void __launch_bounds__(kStepThreads, NT == 4 ? 2 : 4) kv_step_kernel(AttnParams p, AttnSpace a)
 {
     constexpr int R = 8 * NT, KS = D / 16, MT = D / 16;
     using Smem = StepSmem<D, NT>;
@@ -160,11 +160,12 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 1 : 2) kv_step_kernel(
     auto weight = [&](int s) {
         int groups, tiles;
         step_units<D, NT>(p, a, s, seq_view(p, s), groups, tiles);
-        return (int64_t)p.heads * groups * tiles;
+        return (int64_t)p.heads * groups * (tiles + kStepUnitCost);
     };
     const int64_t total = scan_total<kStepThreads>(p.n_seq, weight, sm.scan);
-    // at least two tiles a warp and worker: shorter ranges cost more to join than they save
-    const int workers = (int)min((int64_t)gridDim.x, (total + 2 * kWarps - 1) / (2 * kWarps));
+    // at least two tiles a warp beside a unit's constant: shorter ranges cost more to join than they save
+    constexpr int kLeast = kStepUnitCost + 2 * kWarps;
+    const int workers = (int)min((int64_t)gridDim.x, (total + kLeast - 1) / kLeast);
     if (blockIdx.x == 0 && tid == 0) {
         a.head->step_total = total;
         a.head->step_workers = workers;
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 1 : 2) kv_step_kernel(
     const int64_t lo = cut_start(total, workers, blockIdx.x), hi = cut_start(total, workers, blockIdx.x + 1);
     int64_t before;
     int s = scan_find<kStepThreads>(p.n_seq, lo, weight, sm.scan, before);
-    int64_t at = lo - before;  // tiles into sequence s
+    int64_t at = lo - before;  // cost into sequence s
 
     // ---- the units of the range ----
     bool first_unit = true;
@@ -183,13 +184,16 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 1 : 2) kv_step_kernel(
         int groups, tiles;
         step_units<D, NT>(p, a, s, v, groups, tiles);
         const int64_t units = (int64_t)p.heads * groups;
-        for (int64_t unit = at / tiles; unit < units && x < hi; ++unit) {
-            const int j0 = (int)(at - unit * tiles), j1 = (int)min((int64_t)tiles, j0 + (hi - x));
-            at = (unit + 1) * tiles;
-            x += j1 - j0;
+        const int cost = tiles + kStepUnitCost;
+        for (int64_t unit = at / cost; unit < units && x < hi; ++unit) {
+            const int from = (int)(at - unit * cost), to = (int)min((int64_t)cost, from + (hi - x));
+            const int j0 = max(from - kStepUnitCost, 0), j1 = to - kStepUnitCost;
+            at = (unit + 1) * cost;
+            x += to - from;
             const int head = (int)(unit / groups), row0 = (int)(unit - (int64_t)head * groups) * R;
             const int rows = v.n * group;
-            if (first_unit && tid == 0) a.step_cut[blockIdx.x] = Cut{s, head, row0, j0, tiles};
+            if (first_unit && tid == 0) a.step_cut[blockIdx.x] = Cut{s, head, row0, j0, tiles, from, lo};
+            if (j1 <= 0) break;  // the range ends within the unit's constant
 
             // the warp's first tiles on their way
             constexpr int kParts = Tile<D>::kParts;
@@ -444,66 +448,108 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 1 : 2) kv_step_kernel(
     }
 }
 
-// Block (w, row): where range w is the first that begins inside a unit, joins that unit's parts for one
-// query row, in the order of their ranges.
-constexpr int kJoinThreads = 256;
-template <int D, bool BF16>
+// Joins the parts of the units that the ranges cut, in the order of the ranges.  Every block lists the cut
+// units (where a range is the first that begins inside a unit's tiles) and takes its share of their rows;
+// the fewer rows there are (one long sequence: few rows of many parts), the more warps share a row's parts.
+constexpr int kJoinThreads = 512;
+template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttnParams p, AttnSpace a)
 {
-    constexpr int E = D / 32, W = kJoinThreads / 32;
+    constexpr int E = D / 32, W = kJoinThreads / 32, R = 8 * NT;
+    struct Joint {
+        int s, head, unit;
+        int from, last, slot;  // its first and last range, the slot of the first part
+    };
+    __shared__ Joint joints[kStepMaxWorkers];
+    __shared__ int counts[W];
     __shared__ float part[W][D], part_l[W], part_m[W];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = p.hq / p.heads;
     pdl_wait();
     pdl_launch_dependents();
-    const int w = (int)blockIdx.x + 1, row = blockIdx.y;
     const int workers = a.head->step_workers;
     const int64_t total = a.head->step_total;
-    if (w >= workers) return;
-    const Cut cut = a.step_cut[w];
-    if (cut.j0 == 0) return;
-    const int64_t begin = cut_start(total, workers, w) - cut.j0, prev = cut_start(total, workers, w - 1);
-    if (prev > begin) return;
-    const int t0 = cu_at(p.cu_seqlens, cut.s, p.T), n = cu_at(p.cu_seqlens, cut.s + 1, p.T) - t0;
-    if (cut.unit + row >= n * group) return;
-    const int last = cut_of(total, workers, begin + cut.tiles - 1);
-    float top = -INFINITY, sum = 0.0f, acc[E];
+    int n = 0;
+    for (int w0 = 1; w0 < workers; w0 += kJoinThreads) {
+        const int w = w0 + tid;
+        Cut cut{};
+        int64_t begin = 0, prev = 0;
+        bool is_first = false;
+        if (w < workers) {
+            cut = a.step_cut[w];
+            begin = cut.lo - cut.from;
+            prev = a.step_cut[w - 1].lo;
+            is_first = cut.j0 > 0 && prev <= begin + kStepUnitCost;
+        }
+        const uint32_t vote = __ballot_sync(0xffffffffu, is_first);
+        if (lane == 0) counts[warp] = __popc(vote);
+        __syncthreads();
+        int at = n + __popc(vote & ((1u << lane) - 1u));
+        for (int i = 0; i < W; ++i) {
+            if (i < warp) at += counts[i];
+            n += counts[i];
+        }
+        if (is_first)
+            // the unit is the first of every range but the one that it begins in the middle of
+            joints[at] = Joint{cut.s, cut.head, cut.unit, w - 1, cut_of(total, workers, begin + kStepUnitCost + cut.tiles - 1),
+                               2 * (w - 1) + (prev < begin ? 1 : 0)};
+        __syncthreads();
+    }
+    const int items = n * R, per_block = (items + (int)gridDim.x - 1) / (int)gridDim.x;
+    int share = W;  // warps a row
+    while (share > 1 && share * per_block > W) share >>= 1;
+    for (int k0 = blockIdx.x * per_block; k0 < min((int)(blockIdx.x + 1) * per_block, items); k0 += W / share) {
+        const int k = k0 + warp / share, in_row = warp % share;
+        bool mine = k < min((int)(blockIdx.x + 1) * per_block, items);
+        const Joint u = joints[mine ? k / R : 0];
+        const int row = k % R, t0 = cu_at(p.cu_seqlens, u.s, p.T);
+        mine = mine && u.unit + row < (cu_at(p.cu_seqlens, u.s + 1, p.T) - t0) * group;
+        float top = -INFINITY, sum = 0.0f, acc[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        if (mine)
 #pragma unroll 4
-    for (int i = w - 1 + warp; i <= last; i += W) {
-        // the unit is the first of every range but the one that it begins in the middle of
-        const int slot = 2 * i + (i == w - 1 && prev < begin ? 1 : 0);
-        const float2 st = a.step_stat[(size_t)slot * kStepMaxRows + row];
-        const float* src = a.step_out + ((size_t)slot * kStepMaxRows + row) * D + lane * E;
-        const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.0f : next;
-        const float f0 = ex2(top - ref), f1 = ex2(st.x - ref);
-        sum = sum * f0 + st.y * f1;
+            for (int i = u.from + in_row; i <= u.last; i += share) {
+                const int slot = i == u.from ? u.slot : 2 * i;
+                const float2 st = a.step_stat[(size_t)slot * kStepMaxRows + row];
+                const float* src = a.step_out + ((size_t)slot * kStepMaxRows + row) * D + lane * E;
+                const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.0f : next;
+                const float f0 = ex2(top - ref), f1 = ex2(st.x - ref);
+                sum = sum * f0 + st.y * f1;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + src[e] * f1;
-        top = next;
+                for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + src[e] * f1;
+                top = next;
+            }
+        if (share > 1) {  // uniform over the block
+            __syncthreads();  // the last round's parts are read
+#pragma unroll
+            for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+            if (lane == 0) {
+                part_m[warp] = top;
+                part_l[warp] = sum;
+            }
+            __syncthreads();
+            if (in_row == 0) {
+                float m = top;
+                for (int i = 1; i < share; ++i) m = fmaxf(m, part_m[warp + i]);
+                const float ref = m == -INFINITY ? 0.0f : m, f0 = ex2(top - ref);
+                sum *= f0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] *= f0;
+                for (int i = 1; i < share; ++i) {
+                    const float f = ex2(part_m[warp + i] - ref);
+                    sum += f * part_l[warp + i];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += f * part[warp + i][lane * E + e];
+                }
+            }
+        }
+        if (!mine || in_row != 0) continue;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int i = (u.unit + row) / group, qh = u.unit + row - i * group;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.y + ((int64_t)(t0 + i) * p.hq + u.head * group + qh) * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) dst[e / 2] = narrow2<BF16>(acc[e] * inv, acc[e + 1] * inv);
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-    if (lane == 0) {
-        part_m[warp] = top;
-        part_l[warp] = sum;
-    }
-    __syncthreads();
-    if (tid >= D / 2) return;
-    float m = -INFINITY, l = 0.0f, x0 = 0.0f, x1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) m = fmaxf(m, part_m[i]);
-    const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const float f = ex2(part_m[i] - ref);
-        l += f * part_l[i];
-        x0 += f * part[i][2 * tid];
-        x1 += f * part[i][2 * tid + 1];
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int i = (cut.unit + row) / group, qh = cut.unit + row - i * group;
-    reinterpret_cast<uint32_t*>(p.y + ((int64_t)(t0 + i) * p.hq + cut.head * group + qh) * D)[tid] = narrow2<BF16>(x0 * inv, x1 * inv);
 }
 
 template <int D, bool BF16, bool E4M3, int NT>
@@ -514,10 +560,10 @@ cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_
     static_assert(sizeof(StepSmem<D, NT>) <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int grid = min(sms * (NT == 4 ? 1 : 2), kStepMaxWorkers);
+    const int grid = min(sms * (NT == 4 ? 2 : 4), kStepMaxWorkers);
     e = launch_k(kernel, dim3(grid), dim3(kStepThreads), smem, stream, true, p, a);
     if (e != cudaSuccess || grid == 1) return e;
-    return launch_k(kv_join_kernel<D, BF16>, dim3(grid - 1, 8 * NT), dim3(kJoinThreads), 0, stream, true, p, a);
+    return launch_k(kv_join_kernel<D, BF16, NT>, dim3(min(grid, 2 * sms)), dim3(kJoinThreads), 0, stream, true, p, a);
 }
 
 template <int D, bool BF16, bool E4M3>
