@@ -16,8 +16,9 @@
 // head) * kUp, exact for pages whose scale is at least 2^-15 (e4m3) or 2^-24 (int8) of the largest after
 // the shift; the largest scale itself goes into the scores' unit and the outputs'.
 //
-// A CTA (320 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
-// other's products: warps 0-3 and 4-7 the rows, warp 8 the copies, warp 9 the products.  TMEM: S (later
+// A CTA (384 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
+// other's products: warps 0-3 and 4-7 the rows, warp 8 the copies, warp 9 the products (10 and 11 only
+// make up the warpgroup whose registers the rows' threads get).  TMEM: S (later
 // the fp16 P in its place) and O of each half, 512 columns at head_dim 128.  Rows are (token, query head
 // of the kv head): floor(128 / group) tokens a half.
 #include "gdn_kv_attn.cuh"
@@ -27,8 +28,10 @@ namespace gdn {
 namespace {
 
 constexpr int kImageThreads = 256;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
+// registers a thread, of the 168 that 384 threads are launched with: 2 x 128 x 208 + 128 x 88 = 384 x 168
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr float kWeightShift = 7.0f;
 constexpr float kLazy = 8.0f;
 
@@ -268,6 +271,27 @@ __device__ __forceinline__ bool wait_for(uint64_t* mbar, uint32_t parity, const 
     return __all_sync(0xffffffffu, ok);
 }
 
+// two fp32 operations an instruction
+__device__ __forceinline__ uint64_t pair2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <int D, bool BF16, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, AttnSpace a)
 {
@@ -349,6 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         }                                                 \
     } while (0)
 
+    if (warp >= kLoadWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp > kMmaWarp) goto done;
     if (warp == kLoadWarp) {
         // ---- copies: K and V of each tile in turn through the ring ----
         uint32_t n = 0;  // copies issued
@@ -450,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         }
         goto done;
     }
-    {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---- softmax: a thread owns a query row ----
         const int h = warp >> 2, r = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -513,9 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 float mx[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    mx[c] = x[c][0];
+                    mx[c] = fmaxf(x[c][0], x[c][1]);
 #pragma unroll
-                    for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], x[c][e]);
+                    for (int e = 2; e < 32; e += 2) mx[c] = fmaxf(mx[c], fmaxf(x[c][e], x[c][e + 1]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * coef;
                 const bool moves = top > m + kLazy;
@@ -542,19 +570,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                     }
                 }
                 const float off = kWeightShift - (m == -INFINITY ? 0.0f : m);
+                const uint64_t coef2 = pair2(coef, coef), off2 = pair2(off, off);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t u[32];
-                    float sum = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const float w0 = ex2(fmaf(x[2 * c + (e >> 4)][(2 * e) & 31], coef, off));
-                        const float w1 = ex2(fmaf(x[2 * c + (e >> 4)][(2 * e + 1) & 31], coef, off));
-                        sum += w0 + w1;
+                        const uint64_t y = fma2(pair2(x[2 * c + (e >> 4)][(2 * e) & 31], x[2 * c + (e >> 4)][(2 * e + 1) & 31]), coef2, off2);
+                        float w0, w1;
+                        unpair2(y, w0, w1);
+                        w0 = ex2(w0);
+                        w1 = ex2(w1);
+                        sum[e & 1] = add2(sum[e & 1], pair2(w0, w1));
                         u[e] = narrow2<false>(w0, w1);
                     }
-                    l += sum;
                     umma::tmem_st32(t_s + 32 * c, u);
+                }
+                {
+                    float s0, s1;
+                    unpair2(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
                 }
                 umma::tmem_wait_st();
                 umma::fence_before_sync();
