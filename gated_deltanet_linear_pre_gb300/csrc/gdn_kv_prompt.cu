@@ -16,11 +16,13 @@
 // head) * kUp, exact for pages whose scale is at least 2^-15 (e4m3) or 2^-24 (int8) of the largest after
 // the shift; the largest scale itself goes into the scores' unit and the outputs'.
 //
-// A CTA (384 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
-// other's products: warps 0-3 and 4-7 the rows, warp 8 the copies, warp 9 the products (10 and 11 only
-// make up the warpgroup whose registers the rows' threads get).  TMEM: S (later
-// the fp16 P in its place) and O of each half, 512 columns at head_dim 128.  Rows are (token, query head
-// of the kv head): floor(128 / group) tokens a half.
+// A CTA (640 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
+// other's products: warps 0-7 and 8-15 the rows (two threads a row, each half of a tile's columns: a tile's
+// softmax takes less than the other half's 1024 tensor cycles only with four warps a scheduler), warp 16
+// the copies, warp 17 the products (18 and 19 only make up the warpgroup whose registers the rows'
+// threads get).  TMEM: S and O of each half, 512 columns at head_dim 128; the fp16 P of 64 keys takes the
+// first 32 of their 64 score columns.
+// Rows are (token, query head of the kv head): floor(128 / group) tokens a half.
 #include "gdn_kv_attn.cuh"
 #include "umma.cuh"
 
@@ -28,10 +30,10 @@ namespace gdn {
 namespace {
 
 constexpr int kImageThreads = 256;
-constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
-// registers a thread, of the 168 that 384 threads are launched with: 2 x 128 x 208 + 128 x 88 = 384 x 168
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kThreads = 640;
+constexpr int kLoadWarp = 16, kMmaWarp = 17;
+// registers a thread, of the 96 that 640 threads are launched with: 512 x 104 + 128 x 64 = 640 x 96
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr float kWeightShift = 7.0f;
 constexpr float kLazy = 8.0f;
 
@@ -180,50 +182,51 @@ __device__ __forceinline__ int64_t unit_prefix(const SeqView& v, int span, int i
 {
     return floor_sum(i, kKeys, span, (int64_t)v.first + span + kKeys - 1) + (int64_t)i * kPromptUnitCost;
 }
-__device__ __forceinline__ int unit_tiles(const SeqView& v, int span, int i) { return (v.first + min((i + 1) * span, v.n) + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int unit_tiles(int first, int n, int span, int i) { return (first + min((i + 1) * span, n) + kKeys - 1) / kKeys; }
 
-// A worker's units in order; every role of the CTA walks the same ones.
+// A worker's units in order.  Each role walks them for itself, in shared memory: what a unit needs now and
+// then is read where it is needed, and the registers of the tile loops hold none of it.
 struct Walk {
-    const AttnParams& p;
-    const AttnSpace& a;
-    int span;                 // tokens a unit
-    int s, head, i, units;    // sequence, kv head, unit
-    int j0, j1, tiles;        // this worker's tiles of the unit
-    int from, to;             // and costs
-    int64_t left;             // cost of the range from here on
-    int64_t image;            // image tile of the sequence's first positions
-    SeqView v;
-    bool first;
+    int s, head, i, units;    // sequence, kv head, unit; units of a (sequence, head)
+    int t0, n, first;         // the sequence's tokens, its first one's position
+    int image;                // image tile of its first positions
+    int from, to;             // this worker's cost of the unit
+    int j0, j1, tiles;        // and its tiles
+    int opening;              // the range's first unit
+    int64_t left;             // cost of the range from here on (0: no more units)
 
-    __device__ __forceinline__ Walk(const AttnParams& p_, const AttnSpace& a_, const Cut& c, int64_t tiles_) : p(p_), a(a_), left(tiles_), first(true)
+    __device__ void begin(const AttnParams& p, const AttnSpace& a, const Cut& c, int64_t cost, int span)
     {
-        span = 2 * half_tokens(p.hq / p.heads);
         s = c.s;
         head = c.head;
         i = c.unit;
         from = c.from;
-        enter();
-        here();
+        left = cost;
+        opening = 1;
+        enter(p, a, span);
+        here(span);
     }
-    __device__ __forceinline__ void enter()
+    __device__ void enter(const AttnParams& p, const AttnSpace& a, int span)
     {
-        v = seq_view(p, s);
-        units = (v.n + span - 1) / span;
+        const SeqView v = seq_view(p, s);
+        t0 = v.t0;
+        n = v.n;
+        first = v.first;
+        units = (n + span - 1) / span;
         image = a.image_base[s];
     }
-    __device__ __forceinline__ void here()
+    __device__ void here(int span)
     {
-        tiles = unit_tiles(v, span, i);
+        tiles = unit_tiles(first, n, span, i);
         to = (int)min((int64_t)tiles + kPromptUnitCost, from + left);
         j0 = max(from - kPromptUnitCost, 0);
         j1 = to - kPromptUnitCost;
         if (j1 <= 0) left = 0;  // the range ends within the unit's constant
     }
-    __device__ __forceinline__ bool more() const { return left > 0; }
-    __device__ __forceinline__ void next()
+    __device__ void next(const AttnParams& p, const AttnSpace& a, int span)
     {
         left -= to - from;
-        first = false;
+        opening = 0;
         from = 0;
         if (left <= 0) return;
         if (++i == units) {
@@ -236,10 +239,10 @@ struct Walk {
                         return;
                     }
                 } while (!is_long(p, a, s, seq_view(p, s)));
-                enter();
+                enter(p, a, span);
             }
         }
-        here();
+        here(span);
     }
 };
 
@@ -253,10 +256,30 @@ struct PromptSmem {
     uint32_t tmem_base;
     int abort_flag;
     Cut start;
+    Walk walk[4];                              // of the two halves, the copies and the products
+    float other[2][2][128];                    // what a row's two threads tell each other
 };
 // the search for the range's start is over before the first copy lands where it keeps its sums
 static_assert(sizeof(ScanSmem<kThreads>) <= kTileBytes<64>, "scan fits a ring slot");
 static_assert(sizeof(PromptSmem<128>) <= 232448 && sizeof(PromptSmem<64>) <= 232448, "shared memory");
+
+// barriers: of the two warps that hold the two halves of the same rows' columns (64 threads, ids 1-8), of a
+// half's 256 threads (ids 9, 10)
+__device__ __forceinline__ bool pair_any(int id, bool say)  // whether any of them says so
+{
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)say), "r"(id)
+        : "memory");
+    return any != 0;
+}
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void half_sync(int h) { asm volatile("barrier.cta.sync %0, 256;" ::"r"(9 + h) : "memory"); }
 
 // Bounded wait (about two seconds of SM clock; abandoned once another warp of the CTA has given up); the
 // warp agrees on the outcome and stays converged.
@@ -312,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         const SeqView v = seq_view(p, s);
         if (!is_long(p, a, s, v)) return (int64_t)0;
         const int last = (v.n + span - 1) / span - 1;
-        return p.heads * (unit_prefix(v, span, last) + unit_tiles(v, span, last) + kPromptUnitCost);
+        return p.heads * (unit_prefix(v, span, last) + unit_tiles(v.first, v.n, span, last) + kPromptUnitCost);
     };
     const int64_t total = scan_total<kThreads>(p.n_seq, weight, scan);
     const int workers = (int)min((int64_t)gridDim.x, total);
@@ -328,13 +351,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         if (warp == 0) {
             const SeqView v = seq_view(p, s);
             const int units = (v.n + span - 1) / span;
-            const int64_t per_head = unit_prefix(v, span, units - 1) + unit_tiles(v, span, units - 1) + kPromptUnitCost;
+            const int64_t per_head = unit_prefix(v, span, units - 1) + unit_tiles(v.first, v.n, span, units - 1) + kPromptUnitCost;
             const int head = (int)((lo - before) / per_head);
             const int64_t rest = lo - before - head * per_head;
             const int i = warp_find(units, rest, [&](int u) { return unit_prefix(v, span, u); });
             if (lane == 0) {
                 const int from = (int)(rest - unit_prefix(v, span, i));
-                sm.start = Cut{s, head, i, max(from - kPromptUnitCost, 0), unit_tiles(v, span, i), from, lo};
+                sm.start = Cut{s, head, i, max(from - kPromptUnitCost, 0), unit_tiles(v.first, v.n, span, i), from, lo};
                 a.prompt_cut[blockIdx.x] = sm.start;
             }
         }
@@ -346,21 +369,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
             umma::mbar_init(&sm.kv_empty[i], 1);
         }
         for (int h = 0; h < 2; ++h) {
-            umma::mbar_init(&sm.q_full[h], 128);
+            umma::mbar_init(&sm.q_full[h], 256);
             umma::mbar_init(&sm.s_full[h], 1);
-            umma::mbar_init(&sm.p_full[h], 128);
+            umma::mbar_init(&sm.p_full[h], 256);
             umma::mbar_init(&sm.o_full[h], 1);
         }
         umma::mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
     }
+    __syncthreads();  // the range's start
+    if (tid < 4) sm.walk[tid].begin(p, a, sm.start, hi - lo, span);
     umma::fence_proxy_async();  // the scan's shared memory goes to the copies
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
     const volatile int* abort_flag = &sm.abort_flag;
-    Walk w(p, a, sm.start, hi - lo);
 
 #define GDN_KV_WAIT(mbar, parity)                         \
     do {                                                  \
@@ -378,28 +402,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         if (warp > kMmaWarp) goto done;
     if (warp == kLoadWarp) {
         // ---- copies: K and V of each tile in turn through the ring ----
+        Walk& w = sm.walk[2];
         uint32_t n = 0;  // copies issued
-        for (; w.more(); w.next()) {
-            for (int j = w.j0; j < w.j1; ++j) {
-                const unsigned char* src = a.images + ((size_t)(w.image + j) * p.heads + w.head) * (2 * kTile);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const uint32_t slot = n % kSlots;
-                    if (n >= kSlots) {
-                        if (!wait_for(&sm.kv_empty[slot], (n / kSlots - 1) & 1, abort_flag)) {
-                            if (lane == 0) {
-                                sm.abort_flag = 1;
-                                atomicOr(&a.head->error, kAttnTimeout);
-                            }
-                            goto copies_done;
-                        }
-                    }
+        while (w.left > 0) {
+            const unsigned char* src = a.images + ((size_t)(w.image + w.j0) * p.heads + w.head) * (2 * kTile);
+            const size_t stride = (size_t)p.heads * (2 * kTile);
+            for (int j = 2 * (w.j1 - w.j0); j > 0; --j, ++n) {
+                const uint32_t slot = n % kSlots;
+                if (n >= kSlots && !wait_for(&sm.kv_empty[slot], (n / kSlots - 1) & 1, abort_flag)) {
                     if (lane == 0) {
-                        umma::mbar_arrive_expect_tx(&sm.kv_full[slot], kTile);
-                        umma::bulk_g2s(sm.kv[slot], src + kv * kTile, kTile, &sm.kv_full[slot]);
+                        sm.abort_flag = 1;
+                        atomicOr(&a.head->error, kAttnTimeout);
                     }
+                    goto copies_done;
                 }
+                if (lane == 0) {
+                    umma::mbar_arrive_expect_tx(&sm.kv_full[slot], kTile);
+                    umma::bulk_g2s(sm.kv[slot], j & 1 ? src + kTile : src, kTile, &sm.kv_full[slot]);
+                }
+                if (j & 1) src += stride;
             }
+            __syncwarp();
+            if (lane == 0) w.next(p, a, span);
+            __syncwarp();
         }
     copies_done:
         // no copy may be in flight when the CTA leaves (copies end by themselves; the limit is a formality)
@@ -411,24 +436,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         // ---- products, issued by lane 0 ----
         constexpr uint32_t id_s = umma::idesc_f16(128, kKeys, false, false);
         constexpr uint32_t id_o = umma::idesc_f16(128, D, false, true);  // V: channels (N) contiguous
+        Walk& w = sm.walk[3];
         uint32_t n = 0;         // ring position of the current tile's K
         uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        // descriptors of the first tiles; the others lie a whole number of tiles behind them
+        const uint64_t q_desc = umma::desc(umma::smem_u32(sm.q[0]), 128, (D / 8) * 128);
+        const uint64_t k_desc = umma::desc(umma::smem_u32(sm.kv[0]), 128, (D / 8) * 128);
+        const uint64_t v_desc = umma::desc(umma::smem_u32(sm.kv[0]), (D / 8) * 128, 128);
         auto scores = [&](int h, uint32_t at) {
             if (lane == 0) {
-                const uint64_t da = umma::desc(umma::smem_u32(sm.q[h]), 128, (D / 8) * 128);
-                const uint64_t db = umma::desc(umma::smem_u32(sm.kv[at % kSlots]), 128, (D / 8) * 128);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) umma::mma_bf16(tmem + h * kColS, da + ks * 16, db + ks * 16, id_s, ks != 0);
+                uint64_t da = q_desc + h * (kTile >> 4), db = k_desc + (at % kSlots) * (kTile >> 4);
+#pragma unroll 2
+                for (int ks = 0; ks < D / 16; ++ks, da += 16, db += 16) umma::mma_bf16(tmem + h * kColS, da, db, id_s, ks != 0);
                 umma::commit(&sm.s_full[h]);
             }
             __syncwarp();
         };
         auto outputs = [&](int h, uint32_t at, bool start) {
             if (lane == 0) {
-                const uint64_t db = umma::desc(umma::smem_u32(sm.kv[at % kSlots]), (D / 8) * 128, 128);
-#pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
-                    umma::mma_ts(tmem + kColO + h * D, tmem + h * kColS + 8 * ks, db + ks * (2 * (D / 8) * 128 >> 4), id_o, !(start && ks == 0));
+                uint64_t db = v_desc + (at % kSlots) * (kTile >> 4);
+#pragma unroll 2
+                for (int ks = 0; ks < kKeys / 16; ++ks, db += 2 * (D / 8) * 128 >> 4)
+                    umma::mma_ts(tmem + kColO + h * D, tmem + h * kColS + 64 * (ks >> 2) + 8 * (ks & 3), db, id_o, !(start && ks == 0));
                 umma::commit(&sm.o_full[h]);
             }
             __syncwarp();
@@ -437,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
             if (lane == 0) umma::commit(&sm.kv_empty[at % kSlots]);
             __syncwarp();
         };
-        for (; w.more(); w.next()) {
-            const bool both = (2 * w.i + 1) * tokens < w.v.n;  // the second half has rows
+        while (w.left > 0) {
+            const bool both = (2 * w.i + 1) * tokens < w.n;  // the second half has rows
             GDN_KV_WAIT(&sm.kv_full[n % kSlots], (n / kSlots) & 1);
             GDN_KV_WAIT(&sm.q_full[0], q_phase[0]);
             q_phase[0] ^= 1u;
@@ -451,13 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 scores(1, n);
             }
             release(n);
-            for (int j = w.j0; j < w.j1; ++j, n += 2) {
-                const bool again = j + 1 < w.j1;
+            const int count = w.j1 - w.j0;
+            for (int j = 0; j < count; ++j, n += 2) {
+                const bool again = j + 1 < count;
                 GDN_KV_WAIT(&sm.kv_full[(n + 1) % kSlots], ((n + 1) / kSlots) & 1);
                 GDN_KV_WAIT(&sm.p_full[0], p_phase[0]);
                 p_phase[0] ^= 1u;
                 umma::fence_after_sync();
-                outputs(0, n + 1, j == w.j0);
+                outputs(0, n + 1, j == 0);
                 if (again) {
                     GDN_KV_WAIT(&sm.kv_full[(n + 2) % kSlots], ((n + 2) / kSlots) & 1);
                     scores(0, n + 2);
@@ -466,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                     GDN_KV_WAIT(&sm.p_full[1], p_phase[1]);
                     p_phase[1] ^= 1u;
                     umma::fence_after_sync();
-                    outputs(1, n + 1, j == w.j0);
+                    outputs(1, n + 1, j == 0);
                 }
                 release(n + 1);
                 if (again) {
@@ -474,43 +504,71 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                     release(n + 2);
                 }
             }
+            __syncwarp();
+            if (lane == 0) w.next(p, a, span);
+            __syncwarp();
         }
         goto done;
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        // ---- softmax: a thread owns a query row ----
-        const int h = warp >> 2, r = tid & 127;
+        // ---- softmax: a row's two threads share a tile's columns ----
+        // A wait that expires is recorded and its warp goes on, with waits that no longer wait: a half's warps
+        // meet at barriers, and every loop ends by itself.
+        auto await = [&](uint64_t* mbar, uint32_t parity) {
+            if (!wait_for(mbar, parity, abort_flag) && lane == 0) {
+                sm.abort_flag = 1;
+                atomicOr(&a.head->error, kAttnTimeout);
+            }
+        };
+        const int h = warp >> 3, part = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, pair = 1 + 4 * h + (warp & 3);
+        Walk& w = sm.walk[h];
+        float* const mine = &sm.other[h][part][r];
+        const float* const others = &sm.other[h][part ^ 1][r];
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lane_off + h * kColS, t_o = tmem + lane_off + kColO + h * D;
+        const uint32_t t_s = tmem + lane_off + h * kColS + 64 * part, t_o = tmem + lane_off + kColO + h * D + part * (D / 2);
         const int i_tok = r / group, qh = r - i_tok * group;
         uint32_t s_phase = 0, o_phase = 0;  // o_phase: parity of the next PV product's completion
-        for (; w.more(); w.next()) {
+        // 32 of the thread's scores, -infinity from the column after `last` on
+        auto scores = [&](int c, bool ends, int last, float (&x)[32]) {
+            umma::tmem_ld32(t_s + 32 * c, x);
+            umma::tmem_wait_ld();
+            if (ends)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (32 * c + e > last) x[e] = -INFINITY;
+        };
+        for (; w.left > 0; half_sync(h)) {
+            // (a second half without rows does nothing)
+            if ((2 * w.i + h) * tokens < w.n) {
             const int tok = (2 * w.i + h) * tokens + i_tok;
-            if ((2 * w.i + h) * tokens >= w.v.n) continue;  // a second half without rows
-            const bool valid = i_tok < tokens && tok < w.v.n;
-            // the row to shared memory in fp16
+            const bool valid = i_tok < tokens && tok < w.n;
+            // the row's channels to shared memory in fp16
             float coef;
             {
-                const uint16_t* src = p.q + (int64_t)(w.v.t0 + tok) * p.q_stride + (w.head * group + qh) * D;
-                uint4 raw[D / 8];
+                constexpr int C = D / 16;  // 16-byte pieces a thread
+                const uint16_t* src = p.q + (int64_t)(w.t0 + tok) * p.q_stride + (w.head * group + qh) * D + part * (D / 2);
+                uint4 raw[C];
                 uint32_t amax = 0;
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
+                for (int c = 0; c < C; ++c) {
                     raw[c] = valid ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
                     float x[8];
                     widen8<BF16>(raw[c], x);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
                 }
+                *mine = __uint_as_float(amax);
+                pair_sync(pair);
+                amax = max(amax, __float_as_uint(*others));
                 float mul, back;
                 row_unit(amax, mul, back);
                 if (p.scale < 0.0f) mul = -mul;  // scores times |scale|: a row's largest is its maximum's
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
+                for (int c = 0; c < C; ++c) {
                     float x[8];
                     widen8<BF16>(raw[c], x);
-                    *reinterpret_cast<uint4*>(sm.q[h] + image_off<D>(r, c)) =
+                    *reinterpret_cast<uint4*>(sm.q[h] + image_off<D>(r, part * C + c)) =
                         make_uint4(narrow2<false>(x[0] * mul, x[1] * mul), narrow2<false>(x[2] * mul, x[3] * mul),
                                    narrow2<false>(x[4] * mul, x[5] * mul), narrow2<false>(x[6] * mul, x[7] * mul));
                 }
@@ -520,93 +578,96 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 // (above 0, so that a masked score of -infinity stays one whatever the scale)
                 coef = fmaxf(back * (fabsf(p.scale) * kLog2e) * (norm.x * (1.0f / kUp<E4M3>)), 1e-35f);
             }
-            const int limit = valid ? w.v.first + tok : -1;
-            const int first_limit = w.v.first + (2 * w.i + h) * tokens;
+            // the last of the thread's columns that the row sees, in the tile in hand, and whether a tile ends
+            // before the half's first row does
+            int last = (valid ? w.first + tok : -1) - (w.j0 * kKeys + 64 * part);
+            int spare = w.first + (2 * w.i + h) * tokens - (w.j0 * kKeys + kKeys - 1);
             float m = -INFINITY, l = 0.0f;
-            for (int j = w.j0; j < w.j1; ++j) {
-                GDN_KV_WAIT(&sm.s_full[h], s_phase);
+            const int count = w.j1 - w.j0;
+#pragma unroll 1
+            for (int j = 0; j < count; ++j, last -= kKeys, spare -= kKeys) {
+                await(&sm.s_full[h], s_phase);
                 s_phase ^= 1u;
                 umma::fence_after_sync();
-                float x[4][32];
+                // (32 of the thread's 64 scores at a time: all of them and their weights do not fit its registers)
+                const bool ends = spare < 0;
+                float x[32], top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) umma::tmem_ld32(t_s + 32 * c, x[c]);
-                umma::tmem_wait_ld();
-                if (j * kKeys + kKeys - 1 > first_limit) {
+                for (int c = 0; c < 2; ++c) {
+                    scores(c, ends, last, x);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (j * kKeys + 32 * c + e > limit) x[c][e] = -INFINITY;
+                    for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
                 }
-                float mx[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mx[c] = fmaxf(x[c][0], x[c][1]);
-#pragma unroll
-                    for (int e = 2; e < 32; e += 2) mx[c] = fmaxf(mx[c], fmaxf(x[c][e], x[c][e + 1]));
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * coef;
-                const bool moves = top > m + kLazy;
-                if (__any_sync(0xffffffffu, moves)) {
+                top *= coef;
+                if (pair_any(pair, top > m + kLazy)) {
+                    *mine = top;
+                    pair_sync(pair);
+                    top = fmaxf(top, *others);
                     float f = 1.0f;
-                    if (moves) {
+                    if (top > m + kLazy) {
                         f = ex2(m - top);
                         m = top;
                         l *= f;
                     }
-                    if (j > w.j0) {  // O holds the products up to tile j - 1
-                        GDN_KV_WAIT(&sm.o_full[h], o_phase ^ 1u);
+                    if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {  // O holds the products up to tile j - 1
+                        await(&sm.o_full[h], o_phase ^ 1u);
                         umma::fence_after_sync();
 #pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-                            uint32_t u[32];
-                            umma::tmem_ld32(t_o + 32 * c, o);
+                            float o[16];
+                            uint32_t u[16];
+                            umma::tmem_ld16(t_o + 16 * c, o);
                             umma::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
-                            umma::tmem_st32(t_o + 32 * c, u);
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
+                            umma::tmem_st16(t_o + 16 * c, u);
                         }
                     }
                 }
                 const float off = kWeightShift - (m == -INFINITY ? 0.0f : m);
                 const uint64_t coef2 = pair2(coef, coef), off2 = pair2(off, off);
                 uint64_t sum[2] = {0, 0};
+                uint32_t u[16], u1[16];
+                auto weights = [&](uint32_t (&to)[16]) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t u[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const uint64_t y = fma2(pair2(x[2 * c + (e >> 4)][(2 * e) & 31], x[2 * c + (e >> 4)][(2 * e + 1) & 31]), coef2, off2);
+                    for (int e = 0; e < 16; ++e) {
                         float w0, w1;
-                        unpair2(y, w0, w1);
+                        unpair2(fma2(pair2(x[2 * e], x[2 * e + 1]), coef2, off2), w0, w1);
                         w0 = ex2(w0);
                         w1 = ex2(w1);
                         sum[e & 1] = add2(sum[e & 1], pair2(w0, w1));
-                        u[e] = narrow2<false>(w0, w1);
+                        to[e] = narrow2<false>(w0, w1);
                     }
-                    umma::tmem_st32(t_s + 32 * c, u);
-                }
-                {
-                    float s0, s1;
-                    unpair2(add2(sum[0], sum[1]), s0, s1);
-                    l += s0 + s1;
-                }
+                };
+                // the second 32 are still there; the first ones come again, then both go where those were
+                weights(u1);
+                scores(0, ends, last, x);
+                umma::tmem_st16(t_s + 16, u1);
+                weights(u);
+                umma::tmem_st16(t_s, u);
                 umma::tmem_wait_st();
                 umma::fence_before_sync();
                 umma::mbar_arrive(&sm.p_full[h]);
+                float s0, s1;
+                unpair2(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
                 o_phase ^= 1u;
             }
-            GDN_KV_WAIT(&sm.o_full[h], o_phase ^ 1u);
+            pair_sync(pair);  // the last tile's maxima are read
+            *mine = l;
+            pair_sync(pair);
+            l += *others;
+            pair_sync(pair);  // the sums are read
+            await(&sm.o_full[h], o_phase ^ 1u);
             umma::fence_after_sync();
             const float unit = a.norm[(size_t)w.image * p.heads + w.head].y * (1.0f / kUp<E4M3>);
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
-            const int slot = 2 * blockIdx.x + (w.first ? 0 : 1), row = 128 * h + r;
+            const int slot = 2 * blockIdx.x + (w.opening ? 0 : 1), row = 128 * h + r;
             const float scale = whole ? (l == 0.0f ? 0.0f : unit / l) : unit;
-            uint16_t* const dst = p.y + ((int64_t)(w.v.t0 + tok) * p.hq + w.head * group + qh) * D;
-            if (!whole) a.prompt_stat[(size_t)slot * kUnitRows + row] = make_float2(m, l);
+            uint16_t* const dst = p.y + ((int64_t)(w.t0 + tok) * p.hq + w.head * group + qh) * D + part * (D / 2);
+            if (!whole && part == 0) a.prompt_stat[(size_t)slot * kUnitRows + row] = make_float2(m, l);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < D / 64; ++c) {
                 float o[32];
                 umma::tmem_ld32(t_o + 32 * c, o);
                 umma::tmem_wait_ld();
@@ -620,11 +681,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        a.prompt_out[((size_t)slot * (D / 4) + 8 * c + e / 4) * kUnitRows + row] =
+                        a.prompt_out[((size_t)slot * (D / 4) + part * (D / 8) + 8 * c + e / 4) * kUnitRows + row] =
                             make_float4(o[e] * scale, o[e + 1] * scale, o[e + 2] * scale, o[e + 3] * scale);
                 }
             }
             umma::fence_before_sync();  // O read before the next unit's products (which wait for this thread's weights)
+            }
+            half_sync(h);  // the unit is read
+            if (part == 0 && r == 0) w.next(p, a, span);
         }
     }
 done:
