@@ -11,7 +11,8 @@
 // Layout.  The tensor cores read 16-bit operands from shared memory, so the codes have to be unpacked
 // somewhere.  Done by every CTA for itself, a 128-position tile would cost each about as many issue slots
 // as a third of its softmax; instead one kernel unpacks each long sequence's cache once into images, in
-// the no-swizzle core-matrix order, that a single bulk copy brings in: 4 bytes moved per code byte, a few
+// the 128-byte swizzled order (without swizzle the products run at two thirds of their rate), that a single
+// bulk copy brings in: 4 bytes moved per code byte, a few
 // per cent of a prompt's time.  An image holds code * (page scale / largest scale of the sequence and
 // head) * kUp, exact for pages whose scale is at least 2^-15 (e4m3) or 2^-24 (int8) of the largest after
 // the shift; the largest scale itself goes into the scores' unit and the outputs'.
@@ -42,9 +43,10 @@ template <bool E4M3> constexpr float kUp = E4M3 ? 64.0f : 256.0f;
 
 template <int D> constexpr uint32_t kTileBytes = kKeys * D * 2;
 
-// byte offset of (position, channels 8 c8 .. + 7) in an image: core matrices of 8 positions x 16 bytes
-template <int D>
-__device__ __forceinline__ int image_off(int pos, int c8) { return ((pos >> 3) * (D / 8) + c8) * 128 + (pos & 7) * 16; }
+// byte offset of (position, channels 8 c8 .. + 7) in an image: planes of 64 channels, a position's 128 bytes
+// of a plane a row, its 16-byte pieces swizzled
+constexpr uint32_t kPlane = kKeys * 128;
+__device__ __forceinline__ int image_off(int pos, int c8) { return (c8 >> 3) * (int)kPlane + pos * 128 + (((c8 & 7) ^ (pos & 7)) << 4); }
 
 // ---- unpacking ------------------------------------------------------------------------
 __device__ __forceinline__ int key_tiles(int kv) { return (kv + kKeys - 1) / kKeys; }
@@ -128,9 +130,9 @@ __global__ void __launch_bounds__(kImageThreads) kv_image_kernel(AttnParams p, A
         }
         if (there) {
             unsigned char* const img = a.images + ((size_t)(before + at) * p.heads + head) * (2 * kTileBytes<D>);
-            // a lane's place: 8 positions x 4 groups of 8 channels a warp, 512 contiguous image bytes
+            // neighbouring lanes take neighbouring channels: whole rows of codes and of an image's planes
             for (int i = tid; i < kKeys * (D / 8); i += kImageThreads) {
-                const int pos = ((i >> 5) / (D / 32)) * 8 + (i & 7), c8 = ((i >> 5) % (D / 32)) * 4 + ((i >> 3) & 3);
+                const int pos = i / (D / 8), c8 = i % (D / 8);
                 const int at_pos = (int)at * kKeys + pos;
                 uint4 wk = make_uint4(0u, 0u, 0u, 0u), wv = wk;
                 if (at_pos < v.kv) {
@@ -142,8 +144,8 @@ __global__ void __launch_bounds__(kImageThreads) kv_image_kernel(AttnParams p, A
                     wk = unpack8<E4M3>(__ldg(reinterpret_cast<const uint2*>(p.k + src)), __float2half2_rn(fk));
                     wv = unpack8<E4M3>(__ldg(reinterpret_cast<const uint2*>(p.v + src)), __float2half2_rn(fv));
                 }
-                *reinterpret_cast<uint4*>(img + image_off<D>(pos, c8)) = wk;
-                *reinterpret_cast<uint4*>(img + kTileBytes<D> + image_off<D>(pos, c8)) = wv;
+                *reinterpret_cast<uint4*>(img + image_off(pos, c8)) = wk;
+                *reinterpret_cast<uint4*>(img + kTileBytes<D> + image_off(pos, c8)) = wv;
             }
         }
         __syncthreads();  // top_k, top_v read
@@ -440,24 +442,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         uint32_t n = 0;         // ring position of the current tile's K
         uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
         // descriptors of the first tiles; the others lie a whole number of tiles behind them
-        const uint64_t q_desc = umma::desc(umma::smem_u32(sm.q[0]), 128, (D / 8) * 128);
-        const uint64_t k_desc = umma::desc(umma::smem_u32(sm.kv[0]), 128, (D / 8) * 128);
-        const uint64_t v_desc = umma::desc(umma::smem_u32(sm.kv[0]), (D / 8) * 128, 128);
+        const uint64_t q_desc = umma::desc_sw128(umma::smem_u32(sm.q[0]), 16, 1024);
+        const uint64_t k_desc = umma::desc_sw128(umma::smem_u32(sm.kv[0]), 16, 1024);
+        const uint64_t v_desc = umma::desc_sw128(umma::smem_u32(sm.kv[0]), kPlane, 1024);
         auto scores = [&](int h, uint32_t at) {
             if (lane == 0) {
-                uint64_t da = q_desc + h * (kTile >> 4), db = k_desc + (at % kSlots) * (kTile >> 4);
-#pragma unroll 2
-                for (int ks = 0; ks < D / 16; ++ks, da += 16, db += 16) umma::mma_bf16(tmem + h * kColS, da, db, id_s, ks != 0);
+                const uint64_t da = q_desc + h * (kTile >> 4), db = k_desc + (at % kSlots) * (kTile >> 4);
+#pragma unroll 4
+                for (int ks = 0; ks < D / 16; ++ks) {  // 16 channels: 32 bytes of a plane's rows
+                    const uint32_t step = (ks >> 2) * (kPlane >> 4) + 2 * (ks & 3);
+                    umma::mma_bf16(tmem + h * kColS, da + step, db + step, id_s, ks != 0);
+                }
                 umma::commit(&sm.s_full[h]);
             }
             __syncwarp();
         };
         auto outputs = [&](int h, uint32_t at, bool start) {
             if (lane == 0) {
-                uint64_t db = v_desc + (at % kSlots) * (kTile >> 4);
-#pragma unroll 2
-                for (int ks = 0; ks < kKeys / 16; ++ks, db += 2 * (D / 8) * 128 >> 4)
-                    umma::mma_ts(tmem + kColO + h * D, tmem + h * kColS + 64 * (ks >> 2) + 8 * (ks & 3), db, id_o, !(start && ks == 0));
+                const uint64_t db = v_desc + (at % kSlots) * (kTile >> 4);
+#pragma unroll 4
+                for (int ks = 0; ks < kKeys / 16; ++ks)  // 16 keys: two atoms of 8 rows
+                    umma::mma_ts(tmem + kColO + h * D, tmem + h * kColS + 64 * (ks >> 2) + 8 * (ks & 3), db + ks * (2048 >> 4), id_o, !(start && ks == 0));
                 umma::commit(&sm.o_full[h]);
             }
             __syncwarp();
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 for (int c = 0; c < C; ++c) {
                     float x[8];
                     widen8<BF16>(raw[c], x);
-                    *reinterpret_cast<uint4*>(sm.q[h] + image_off<D>(r, part * C + c)) =
+                    *reinterpret_cast<uint4*>(sm.q[h] + image_off(r, part * C + c)) =
                         make_uint4(narrow2<false>(x[0] * mul, x[1] * mul), narrow2<false>(x[2] * mul, x[3] * mul),
                                    narrow2<false>(x[4] * mul, x[5] * mul), narrow2<false>(x[6] * mul, x[7] * mul));
                 }

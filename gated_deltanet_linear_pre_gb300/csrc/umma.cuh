@@ -35,6 +35,15 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo_bytes, uin
     return d;                 // base offset 0, absolute LBO mode, layout 0 = no swizzle
 }
 
+// the same for 128-byte swizzled tiles: rows of 128 bytes (64 16-bit elements), 8 of them an atom of 1024
+// bytes on a 1024-byte boundary, the 16-byte piece c of row r at c ^ (r & 7).  K-major (a row's elements
+// along K): sbo = distance of 8-row atoms along M/N, lbo unused.  MN-major (a row's elements along M/N, a
+// row per K index): sbo = distance of atoms along K, lbo = of the next 64 elements along M/N.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes)
+{
+    return desc(saddr, lbo_bytes, sbo_bytes) | ((uint64_t)2u << 61);
+}
+
 // instruction descriptor, kind::f16 with bf16 inputs and fp32 accumulation
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major)
 {
