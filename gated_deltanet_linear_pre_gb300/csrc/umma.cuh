@@ -66,6 +66,19 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, 
            | ((uint32_t)(M >> 4) << 24);      // M / 16
 }
 
+// true in one lane of a converged warp, always the same one.  Unlike a comparison of lane numbers it tells the
+// compiler that a single thread goes on, so that operands which all lanes agree on stay in uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit operands: row m of A in lane m, its K elements 2c, 2c + 1 in
 // column a_tmem + c; issued by a single thread
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
