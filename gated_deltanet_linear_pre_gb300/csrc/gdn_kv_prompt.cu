@@ -126,8 +126,8 @@ __device__ __forceinline__ void plan(const AttnParams& p, const AttnSpace& a, in
             const int head = (int)(rest / per_head), units = (v.n + span - 1) / span;
             rest -= head * per_head;
             // the unit: about half a tile's rounding a unit makes the prefix a quadratic, whose root is near
-            const double qa = span / (2.0 * kKeys), qb = (v.first + 0.5 * span) / kKeys + 0.5 + kPromptUnitCost;
-            int i = min(max((int)((sqrt(qb * qb + 4.0 * qa * (double)rest) - qb) / (2.0 * qa)), 0), units - 1);
+            const float qa = span / (2.0f * kKeys), qb = (v.first + 0.5f * span) / kKeys + 0.5f + kPromptUnitCost;
+            int i = min(max((int)((sqrtf(qb * qb + 4.0f * qa * (float)rest) - qb) / (2.0f * qa)), 0), units - 1);
             int64_t at = unit_prefix(v.first, span, i);
             while (at > rest) at -= unit_tiles(v.first, v.n, span, --i) + kPromptUnitCost;
             while (i + 1 < units) {
@@ -338,17 +338,19 @@ __device__ __forceinline__ bool pair_any(int id, bool say)  // whether any of th
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void half_sync(int h) { asm volatile("barrier.cta.sync %0, 256;" ::"r"(9 + h) : "memory"); }
 
-// Bounded wait (about two seconds of SM clock; abandoned once another warp of the CTA has given up); the
+// Bounded wait (about two seconds of SM clock; abandoned once another warp of the CTA has given up).  The
 // warp agrees on the outcome and stays converged.
+__device__ __noinline__ bool wait_long(uint64_t* mbar, uint32_t parity, const volatile int* abort_flag)
+{
+    bool ok = false;
+    const long long start = clock64();
+    while (!(ok = umma::mbar_try_wait_suspend(mbar, parity, 20000u)))
+        if (*abort_flag || clock64() - start > (4ll << 30)) break;
+    return __all_sync(0xffffffffu, ok);
+}
 __device__ __forceinline__ bool wait_for(uint64_t* mbar, uint32_t parity, const volatile int* abort_flag)
 {
-    bool ok = umma::mbar_try_wait(mbar, parity);
-    if (!ok) {
-        const long long start = clock64();
-        while (!(ok = umma::mbar_try_wait_suspend(mbar, parity, 20000u)))
-            if (*abort_flag || clock64() - start > (4ll << 30)) break;
-    }
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, umma::mbar_try_wait(mbar, parity)) || wait_long(mbar, parity, abort_flag);
 }
 
 // two fp32 operations an instruction
@@ -546,32 +548,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
             const uint64_t v_desc = umma::desc_sw128(umma::smem_u32(sm.kv[0]), kPlane, 1024);
             uint32_t n = 0;  // ring position of the current tile's K
             uint32_t p_phase[2] = {0, 0};
+            // (one lane, in a converged warp)
             auto scores = [&](int h, uint32_t at, bool last) {
-                if (umma::elect_one()) {
-                    const uint64_t da = q_desc + h * (kTile >> 4), db = k_desc + (at % kSlots) * (kTile >> 4);
+                const uint64_t da = q_desc + h * (kTile >> 4), db = k_desc + (at % kSlots) * (kTile >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {  // 16 channels: 32 bytes of a plane's rows
-                        const uint32_t step = (ks >> 2) * (kPlane >> 4) + 2 * (ks & 3);
-                        umma::mma_bf16(tmem + h * kColS, da + step, db + step, id_s, ks != 0);
-                    }
-                    umma::commit(&sm.s_full[h]);
-                    if (last) umma::commit(&sm.q_empty[h]);
+                for (int ks = 0; ks < D / 16; ++ks) {  // 16 channels: 32 bytes of a plane's rows
+                    const uint32_t step = (ks >> 2) * (kPlane >> 4) + 2 * (ks & 3);
+                    umma::mma_bf16(tmem + h * kColS, da + step, db + step, id_s, ks != 0);
                 }
-                __syncwarp();
+                umma::commit(&sm.s_full[h]);
+                if (last) umma::commit(&sm.q_empty[h]);
             };
-            auto outputs = [&](int h, uint32_t at, bool start) {
-                if (umma::elect_one()) {
-                    const uint64_t db = v_desc + (at % kSlots) * (kTile >> 4);
+            auto outputs = [&](int h, uint32_t at, bool start, bool last) {
+                const uint64_t db = v_desc + (at % kSlots) * (kTile >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)  // 16 keys: two atoms of 8 rows
-                        umma::mma_ts(tmem + kColO + h * kColS, tmem + h * kColS + 64 * (ks >> 2) + 8 * (ks & 3), db + ks * (2048 >> 4), id_o, !(start && ks == 0));
-                    umma::commit(&sm.o_full[h]);
-                }
-                __syncwarp();
-            };
-            auto release = [&](uint32_t at) {
-                if (umma::elect_one()) umma::commit(&sm.kv_empty[at % kSlots]);
-                __syncwarp();
+                for (int ks = 0; ks < kKeys / 16; ++ks)  // 16 keys: two atoms of 8 rows
+                    umma::mma_ts(tmem + kColO + h * kColS, tmem + h * kColS + 64 * (ks >> 2) + 8 * (ks & 3), db + ks * (2048 >> 4), id_o, !(start && ks == 0));
+                if (last) umma::commit(&sm.o_full[h]);
             };
             for (uint32_t x = 0; unit_ready(x); ++x) {
                 const Unit& u = sm.unit[x % kUnits];
@@ -581,35 +574,47 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 GDN_KV_WAIT(&sm.kv_full[n % kSlots], (n / kSlots) & 1);
                 GDN_KV_WAIT(&sm.q_full[x % kUnits][0], (x / kUnits) & 1);
                 umma::fence_after_sync();
-                scores(0, n, count == 1);
+                if (umma::elect_one()) scores(0, n, count == 1);
+                __syncwarp();
                 if (both) {
                     GDN_KV_WAIT(&sm.q_full[x % kUnits][1], (x / kUnits) & 1);
                     umma::fence_after_sync();
-                    scores(1, n, count == 1);
+                }
+                if (umma::elect_one()) {
+                    if (both) scores(1, n, count == 1);
+                    umma::commit(&sm.kv_empty[n % kSlots]);
                 }
                 unit_done(x);
-                release(n);
+                // the copies that a tile's products read are waited for a tile ahead, while the tensor cores have work
+                GDN_KV_WAIT(&sm.kv_full[(n + 1) % kSlots], ((n + 1) / kSlots) & 1);
+                if (count > 1) GDN_KV_WAIT(&sm.kv_full[(n + 2) % kSlots], ((n + 2) / kSlots) & 1);
                 for (int j = 0; j < count; ++j, n += 2) {
-                    const bool again = j + 1 < count;
-                    GDN_KV_WAIT(&sm.kv_full[(n + 1) % kSlots], ((n + 1) / kSlots) & 1);
+                    const bool last = j + 1 == count;
                     GDN_KV_WAIT(&sm.p_full[0], p_phase[0]);
                     p_phase[0] ^= 1u;
                     umma::fence_after_sync();
-                    outputs(0, n + 1, j == 0);
-                    if (again) {
-                        GDN_KV_WAIT(&sm.kv_full[(n + 2) % kSlots], ((n + 2) / kSlots) & 1);
-                        scores(0, n + 2, j + 2 == count);
+                    if (umma::elect_one()) {
+                        outputs(0, n + 1, j == 0, last);
+                        if (!last) scores(0, n + 2, j + 2 == count);
                     }
+                    __syncwarp();
                     if (both) {
                         GDN_KV_WAIT(&sm.p_full[1], p_phase[1]);
                         p_phase[1] ^= 1u;
                         umma::fence_after_sync();
-                        outputs(1, n + 1, j == 0);
                     }
-                    release(n + 1);
-                    if (again) {
-                        if (both) scores(1, n + 2, j + 2 == count);
-                        release(n + 2);
+                    if (umma::elect_one()) {
+                        if (both) outputs(1, n + 1, j == 0, last);
+                        umma::commit(&sm.kv_empty[(n + 1) % kSlots]);
+                        if (!last) {
+                            if (both) scores(1, n + 2, j + 2 == count);
+                            umma::commit(&sm.kv_empty[(n + 2) % kSlots]);
+                        }
+                    }
+                    __syncwarp();
+                    if (!last) {
+                        GDN_KV_WAIT(&sm.kv_full[(n + 3) % kSlots], ((n + 3) / kSlots) & 1);
+                        if (j + 2 < count) GDN_KV_WAIT(&sm.kv_full[(n + 4) % kSlots], ((n + 4) / kSlots) & 1);
                     }
                 }
             }
@@ -621,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         const int h = warp >> 3, part = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, pair = 1 + 4 * h + (warp & 3);
         // this thread's score columns, and half of its row's outputs
         const uint32_t t_s = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * kColS + 64 * part, t_o = t_s + kColO - part * (64 - D / 2);
-        uint32_t phase = 0;  // parity of the next scores' completion; the outputs' follows it by one tile
+        uint32_t phase = 0, units = 0;  // parity of the next scores' completion; units whose output was waited for
         // 32 of the thread's scores, -infinity from the column after `last` on
         auto scores = [&](int c, int last, float (&x)[32]) {
             umma::tmem_ld32(t_s + 32 * c, x);
@@ -671,9 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                             m = top;
                             l *= f;
                         }
-                        if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {  // O holds the products up to tile j - 1
-                            await(&sm.o_full[h], phase);
-                            umma::fence_after_sync();
+                        // O holds the products up to tile j - 1, which ended before this tile's scores
+                        if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll
                             for (int c = 0; c < D / 32; ++c) {
                                 float o[16];
@@ -718,7 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 sm.other[h][part][r] = l;
                 pair_sync(pair);
                 l += sm.other[h][part ^ 1][r];
-                await(&sm.o_full[h], phase ^ 1u);
+                await(&sm.o_full[h], units & 1);
+                ++units;
                 umma::fence_after_sync();
                 const int i_tok = r / group, tok = token0 + i_tok, qh = r - i_tok * group;
                 const bool whole = u.whole, valid = i_tok < tokens && tok < u.n;
@@ -766,7 +771,7 @@ done:
 #undef GDN_KV_WAIT
 }
 
-// Block (w, 32 rows): where range w is the first that begins inside a unit, joins that unit's parts.  16
+// Block (w, half): where range w is the first that begins inside a unit, joins that unit's parts.  Four
 // threads share a row's channels.
 constexpr int kJoinThreads = 512;
 template <int D, bool BF16>
@@ -781,17 +786,17 @@ __global__ void __launch_bounds__(kJoinThreads) kv_prompt_join_kernel(AttnParams
     const int64_t total = a.head->prompt_total, begin = cut.lo - cut.from, prev = a.prompt_cut[w - 1].lo;
     if (cut.j0 == 0 || prev > begin + kPromptUnitCost || !a.ok[cut.s]) return;
     const int last = cut_of(total, workers, begin + kPromptUnitCost + cut.tiles - 1);
-    const int row = blockIdx.y * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+    const int row = blockIdx.y * 128 + (threadIdx.x & 127), part = threadIdx.x >> 7;
     const int h = row >> 7, r = row & 127, i_tok = r / group, qh = r - i_tok * group;
     const int t0 = cu_at(p.cu_seqlens, cut.s, p.T), n = cu_at(p.cu_seqlens, cut.s + 1, p.T) - t0;
     const int tok = (2 * cut.unit + h) * tokens + i_tok;
     if (i_tok >= tokens || tok >= n) return;
-    constexpr int E = D / 64;  // float4s a thread
+    constexpr int E = D / 16;  // float4s a thread
     float top = -INFINITY, sum = 0.0f;
     float4 acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 2
     for (int i = w - 1; i <= last; ++i) {
         const int slot = 2 * i + (i == w - 1 && prev < begin ? 1 : 0);
         const float2 st = a.prompt_stat[(size_t)slot * kUnitRows + row];
@@ -826,7 +831,7 @@ cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_
     if (e != cudaSuccess) return e;
     e = launch_k(kernel, dim3(grid), dim3(kThreads), sizeof(PromptSmem<D>), stream, true, p, a);
     if (e != cudaSuccess || grid == 1) return e;
-    return launch_k(kv_prompt_join_kernel<D, BF16>, dim3(grid - 1, kUnitRows / 32), dim3(kJoinThreads), 0, stream, true, p, a);
+    return launch_k(kv_prompt_join_kernel<D, BF16>, dim3(grid - 1, 2), dim3(kJoinThreads), 0, stream, true, p, a);
 }
 
 template <int D>

@@ -570,8 +570,11 @@ template <int D, bool BF16, bool E4M3>
 cudaError_t launch_rows(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
     // query rows of an average sequence decide the tile: 8 rows as long as they hold them, else 16 or 32
-    // (a warp's codes serve more rows)
-    const int64_t rows = ((int64_t)p.T * (p.hq / p.heads) + p.n_seq - 1) / p.n_seq;
+    // (a warp's codes serve more rows).  An average above kLongRows says that there are long sequences, which
+    // the prompt kernel takes; those left here are then taken to bring single tokens.
+    const int group = p.hq / p.heads;
+    int64_t rows = ((int64_t)p.T * group + p.n_seq - 1) / p.n_seq;
+    if (rows > a.most_rows) rows = group;
     if (rows <= 8) return launch<D, BF16, E4M3, 1>(p, a, sms, stream);
     if (rows <= 16) return launch<D, BF16, E4M3, 2>(p, a, sms, stream);
     return launch<D, BF16, E4M3, 4>(p, a, sms, stream);
