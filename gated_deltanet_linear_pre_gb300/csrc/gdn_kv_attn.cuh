@@ -54,6 +54,7 @@ struct Cut {
     int s, head, unit, j0, tiles;  // unit: the step unit's first row, the prompt unit's index
     int from;                      // cost of the unit that lies before the range
     int64_t lo;                    // cost of all units that does
+    int t0, n, first, image;       // (prompt) the sequence's tokens, first position and image tile
 };
 
 struct AttnHeader {

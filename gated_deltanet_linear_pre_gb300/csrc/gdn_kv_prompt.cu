@@ -20,10 +20,15 @@
 // A CTA (640 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
 // other's products: warps 0-7 and 8-15 the rows (two threads a row, each half of a tile's columns: a tile's
 // softmax takes less than the other half's 1024 tensor cycles only with four warps a scheduler), warp 16
-// the copies, warp 17 the products, warps 18 and 19 the queries of the next unit, which they bring in as
-// soon as the unit's last scores are issued, under its softmax and its output.  TMEM: S and O of each half,
+// the copies, warp 17 the products, warp 18 the units ahead and their queries, which it brings in as soon as
+// the last scores of the unit before are issued, under its softmax and its output (a tensor map's box of
+// floor(128 / group) tokens by group heads by 64 channels is 128 swizzled rows as the products read them).
+// TMEM: S and O of each half,
 // 512 columns at head_dim 128; the fp16 P of 64 keys takes the first 32 of their 64 score columns.
 // Rows are (token, query head of the kv head): floor(128 / group) tokens a half.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "gdn_kv_attn.cuh"
 #include "umma.cuh"
 
@@ -31,8 +36,8 @@ namespace gdn {
 namespace {
 
 constexpr int kImageThreads = 256;
-constexpr int kThreads = 640;
-constexpr int kLoadWarp = 16, kMmaWarp = 17, kQueryWarp = 18;  // 18 and 19
+constexpr int kThreads = 608;
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kQueryWarp = 18;
 constexpr float kWeightShift = 7.0f;
 constexpr float kLazy = 8.0f;
 
@@ -102,8 +107,20 @@ __device__ __forceinline__ void plan(const AttnParams& p, const AttnSpace& a, in
         a.head->prompt_total = total;
         a.head->prompt_workers = workers;
     }
-    int64_t base = 0;
+    int64_t base = 0, tiles = 0;
+    __shared__ int image[THREADS];  // image tiles before each of the chunk's sequences
     for (int c = 0; c * THREADS < p.n_seq; ++c) {
+        {
+            const int s = c * THREADS + tid;
+            int64_t mine = 0, sum;
+            if (s < p.n_seq) {
+                const SeqView v = seq_view(p, s);
+                mine = candidate(p, a, v) ? key_tiles(v.kv) : 0;
+            }
+            const int64_t before = tiles + block_scan<THREADS>(mine, scan, sum);
+            image[tid] = (int)min(before, (int64_t)a.image_tiles);
+            tiles += sum;
+        }
         if (c > 0) {
             const int s = c * THREADS + tid;
             int64_t sum;
@@ -137,27 +154,21 @@ __device__ __forceinline__ void plan(const AttnParams& p, const AttnSpace& a, in
                 ++i;
             }
             const int from = (int)(rest - at);
-            a.prompt_cut[w] = Cut{s, head, i, max(from - kPromptUnitCost, 0), unit_tiles(v.first, v.n, span, i), from, lo};
+            a.prompt_cut[w] = Cut{s, head, i, max(from - kPromptUnitCost, 0), unit_tiles(v.first, v.n, span, i), from, lo, v.t0, v.n, v.first, image[s - c * THREADS]};
         }
         base = end;
         __syncthreads();
     }
 }
 
-// A worker's units in order, as the query warps walk them.
+// A worker's units in order.
 struct Walk {
     int s, head, i, units;  // sequence, kv head, unit; units of a (sequence, head)
-    SeqView v;
-    int image;              // image tile of the sequence's first positions (-1: not a long sequence after all)
+    int t0, n, first;       // the sequence's tokens, its first one's position
+    int image;              // image tile of its first positions (-1: not a long sequence after all)
     int from;               // cost of the unit before the range
     int64_t left;           // cost of the range from here on
 
-    __device__ __forceinline__ void enter(const AttnParams& p, const AttnSpace& a, int span)
-    {
-        v = seq_view(p, s);
-        units = (v.n + span - 1) / span;
-        image = candidate(p, a, v) && a.ok[s] ? a.image_base[s] : -1;
-    }
     // to the next unit, having used `cost` of this one; false at the range's end
     __device__ __forceinline__ bool next(const AttnParams& p, const AttnSpace& a, int span, int cost)
     {
@@ -168,15 +179,21 @@ struct Walk {
         i = 0;
         if (++head < p.heads) return true;
         head = 0;
-        do {  // (a candidate that has turned out otherwise keeps its place in the ranges)
+        for (;;) {  // (a candidate that has turned out otherwise keeps its place in the ranges)
             if (++s >= p.n_seq) return false;
-            enter(p, a, span);
-        } while (!candidate(p, a, v));
-        return true;
+            const SeqView v = seq_view(p, s);
+            if (!candidate(p, a, v)) continue;
+            t0 = v.t0;
+            n = v.n;
+            first = v.first;
+            units = (n + span - 1) / span;
+            image = a.ok[s] ? a.image_base[s] : -1;
+            return true;
+        }
     }
 };
 
-// What the CTA's roles need of a unit; the query warps write it ahead, into a ring.
+// What the CTA's roles need of a unit; written ahead, into a ring.
 constexpr int kUnits = 4;
 struct Unit {
     int count;         // tiles (0: no more units)
@@ -375,7 +392,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 }
 
 template <int D, bool BF16, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, AttnSpace a)
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, AttnSpace a, const __grid_constant__ CUtensorMap q_map)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     using Smem = PromptSmem<D>;
@@ -392,10 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
             umma::mbar_init(&sm.kv_empty[i], 1);
         }
         for (int i = 0; i < kUnits; ++i) {
-            umma::mbar_init(&sm.unit_full[i], 64);
+            umma::mbar_init(&sm.unit_full[i], 1);
             umma::mbar_init(&sm.unit_empty[i], 18);  // the softmax warps, the copies and the products
-            umma::mbar_init(&sm.q_full[i][0], 64);
-            umma::mbar_init(&sm.q_full[i][1], 64);
+            umma::mbar_init(&sm.q_full[i][0], 1);
+            umma::mbar_init(&sm.q_full[i][1], 1);
         }
         for (int h = 0; h < 2; ++h) {
             umma::mbar_init(&sm.q_empty[h], 1);
@@ -438,82 +455,77 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
     if (warp >= kLoadWarp) {
         if (warp >= kQueryWarp) {
             // ---- units and queries ----
-            const int workers = a.head->prompt_workers, span = 2 * tokens;
-            uint32_t x = 0, q_use[2] = {0, 0};
-            Walk w;
+            const int span = 2 * tokens, workers = a.head->prompt_workers;
+            const Cut c = a.prompt_cut[blockIdx.x];  // (nothing of it is used past the plan's workers)
+            const int64_t end = (int)blockIdx.x + 1 < workers ? a.prompt_cut[blockIdx.x + 1].lo : a.head->prompt_total;
+            uint32_t x = 0, q_use[2] = {0, 0};  // units, and queries of each half, brought in
             bool more = (int)blockIdx.x < workers;
+            Walk w;
             if (more) {
-                const Cut c = a.prompt_cut[blockIdx.x];
-                const int64_t end = (int)blockIdx.x + 1 < workers ? a.prompt_cut[blockIdx.x + 1].lo : a.head->prompt_total;
                 w.s = c.s;
                 w.head = c.head;
                 w.i = c.unit;
+                w.t0 = c.t0;
+                w.n = c.n;
+                w.first = c.first;
+                w.units = (c.n + span - 1) / span;
+                w.image = a.ok[c.s] ? c.image : -1;
                 w.from = c.from;
                 w.left = end - c.lo;
-                w.enter(p, a, span);
             }
-            for (int opening = 1; more; ) {
-                const int tiles = unit_tiles(w.v.first, w.v.n, span, w.i);
+            while (more) {
+                const int tiles = unit_tiles(w.first, w.n, span, w.i);
                 const int to = (int)min((int64_t)tiles + kPromptUnitCost, w.from + w.left);
                 const int j0 = max(w.from - kPromptUnitCost, 0), count = to - kPromptUnitCost - j0;
-                const bool use = count > 0 && w.image >= 0;  // (a range may end within a unit's constant)
-                if (use) {
+                if (count > 0 && w.image >= 0) {  // (a range may end within a unit's constant)
                     if (x >= kUnits) GDN_KV_WAIT(&sm.unit_empty[x % kUnits], (x / kUnits - 1) & 1);
-                    Unit& u = sm.unit[x % kUnits];
                     const float2 norm = a.norm[(size_t)w.image * p.heads + w.head];
                     const int token = w.i * span;
-                    if (warp == kQueryWarp && lane == 0) {
+                    if (lane == 0) {
+                        Unit& u = sm.unit[x % kUnits];
                         u.count = count;
                         u.tile = w.image + j0;
                         u.j0 = j0;
                         u.head = w.head;
-                        u.first = w.v.first;
-                        u.t0 = w.v.t0;
-                        u.n = w.v.n;
+                        u.first = w.first;
+                        u.t0 = w.t0;
+                        u.n = w.n;
                         u.token = token;
                         u.whole = count == tiles;
-                        u.slot = 2 * blockIdx.x + (opening ? 0 : 1);
+                        u.slot = 2 * blockIdx.x + (x == 0 ? 0 : 1);
                         // (above 0, so that a masked score of -infinity stays one whatever the scale)
                         u.score_unit = fmaxf(fabsf(p.scale) * kLog2e * (BF16 ? 1.0f : norm.x * (1.0f / kUp<E4M3>)), 1e-35f);
                         u.v_unit = norm.y * (1.0f / kUp<E4M3>);
+                        umma::mbar_arrive(&sm.unit_full[x % kUnits]);
                     }
-                    umma::mbar_arrive(&sm.unit_full[x % kUnits]);
-                    // 16 bytes a lane, D / 8 lanes a row; all of a half's rows are in flight together
-                    constexpr int kLanes = D / 8, kPass = 64 / kLanes;
-                    const int c = lane % kLanes, inv = (65536 + group - 1) / group;  // r * inv >> 16 = r / group for r < 128
-#pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         const int token0 = token + h * tokens;
-                        if (token0 < w.v.n) {  // (else a second half without rows)
+                        const bool rows = token0 < w.n;  // (else a second half without rows)
+                        if (rows) {
                             if (q_use[h] > 0) GDN_KV_WAIT(&sm.q_empty[h], (q_use[h] - 1) & 1);
                             ++q_use[h];
-                            const uint16_t* const src = p.q + (int64_t)(w.v.t0 + token0) * p.q_stride + (w.head * group) * D + 8 * c;
-                            const int most = min(tokens, w.v.n - token0);
-#pragma unroll 4
-                            for (int r = (tid & 63) / kLanes; r < 128; r += kPass) {
-                                const int i_tok = r * inv >> 16;
-                                unsigned char* const dst = sm.q[h] + image_off(r, c);
-                                if (i_tok < most)
-                                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(umma::smem_u32(dst)),
-                                                 "l"(src + (int64_t)i_tok * p.q_stride + (r - i_tok * group) * D)
-                                                 : "memory");
-                                else
-                                    *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
-                            }
-                            asm volatile("cp.async.wait_all;" ::: "memory");
-                            umma::fence_proxy_async();
                         }
-                        umma::mbar_arrive(&sm.q_full[x % kUnits][h]);
+                        if (lane == 0) {
+                            uint64_t* const full = &sm.q_full[x % kUnits][h];
+                            if (rows) {
+                                // (rows past the sequence's end are another's or zeros; what comes of them is not written)
+                                umma::mbar_arrive_expect_tx(full, tokens * group * D * 2);
+                                for (int plane = 0; plane < D / 64; ++plane)
+                                    umma::tensor_g2s_3d(sm.q[h] + plane * kPlane, &q_map, 64 * plane, w.head * group, w.t0 + token0, full);
+                            } else {
+                                umma::mbar_arrive(full);
+                            }
+                        }
                     }
                     ++x;
-                    opening = 0;
                 }
                 more = w.next(p, a, span, to - w.from);
             }
             if (x >= kUnits) GDN_KV_WAIT(&sm.unit_empty[x % kUnits], (x / kUnits - 1) & 1);
-            if (warp == kQueryWarp && lane == 0) sm.unit[x % kUnits].count = 0;
-            __syncwarp();
-            umma::mbar_arrive(&sm.unit_full[x % kUnits]);
+            if (lane == 0) {
+                sm.unit[x % kUnits].count = 0;
+                umma::mbar_arrive(&sm.unit_full[x % kUnits]);
+            }
         } else if (warp == kLoadWarp) {
             // ---- copies: K and V of each tile in turn through the ring ----
             uint32_t n = 0;  // copies issued
@@ -819,6 +831,18 @@ __global__ void __launch_bounds__(kJoinThreads) kv_prompt_join_kernel(AttnParams
     for (int e = 0; e < E; ++e) dst[e] = make_uint2(narrow2<BF16>(acc[e].x * inv, acc[e].y * inv), narrow2<BF16>(acc[e].z * inv, acc[e].w * inv));
 }
 
+// the driver's tensor map encoder, looked up once (the library links the runtime alone)
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(e == cudaSuccess && found == cudaDriverEntryPointSuccess ? f : nullptr);
+    }();
+    return encode;
+}
+
 template <int D, bool BF16, bool E4M3>
 cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
@@ -829,7 +853,17 @@ cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_
     auto kernel = kv_prompt_kernel<D, BF16, E4M3>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PromptSmem<D>));
     if (e != cudaSuccess) return e;
-    e = launch_k(kernel, dim3(grid), dim3(kThreads), sizeof(PromptSmem<D>), stream, true, p, a);
+    // queries as [token][head][channel]; a box is the tokens of half a unit, one kv head's heads, 64 channels
+    const auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    CUtensorMap q_map;
+    const int group = p.hq / p.heads;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.hq, (cuuint64_t)p.T}, strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(kUnitRows / 2 / group)}, ones[3] = {1, 1, 1};
+    if (encode(&q_map, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    e = launch_k(kernel, dim3(grid), dim3(kThreads), sizeof(PromptSmem<D>), stream, true, p, a, q_map);
     if (e != cudaSuccess || grid == 1) return e;
     return launch_k(kv_prompt_join_kernel<D, BF16>, dim3(grid - 1, 2), dim3(kJoinThreads), 0, stream, true, p, a);
 }

@@ -274,6 +274,17 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
                  : "memory");
 }
 
+// one box of a 3-D tensor map -> shared memory (dst on a 1024-byte boundary for a 128-byte swizzle); x times
+// the element size a multiple of 16 bytes; places outside the tensor are zeros
+__device__ __forceinline__ void tensor_g2s_3d(void* dst, const void* map, int x, int y, int z, uint64_t* mbar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        :
+        : "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(mbar))
+        : "memory");
+}
+
 // global -> L2 only (no completion tracking); src 16-byte aligned, bytes a multiple of 16
 __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes)
 {
