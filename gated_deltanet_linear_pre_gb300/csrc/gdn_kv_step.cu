@@ -200,14 +200,15 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 2 : 4) kv_step_kernel(
             const Source<D> src(p, s, head, lane);
             Tile<D>* const ring = sm.ring[warp];
             Pages<D> pages[kStages];
-            int j = j0 + warp, next_page[kParts];
-            src.look(j, j < j1 ? v.kv : 0, next_page);
+            int j = j0 + warp, look[kStages][kParts];  // pages looked up ahead of their tiles
+#pragma unroll
+            for (int i = 0; i < kStages; ++i) src.look(j + i * kWarps, j + i * kWarps < j1 ? v.kv : 0, look[i]);
+            int(&next_page)[kParts] = look[kStages - 1];
             __syncthreads();  // the last unit's outputs and queries are read
 #pragma unroll
             for (int i = 0; i < kStages - 1; ++i) {
-                if (j + i * kWarps < j1) src.load(ring[i], pages[i], next_page, j + i * kWarps, lane);
+                if (j + i * kWarps < j1) src.load(ring[i], pages[i], look[i], j + i * kWarps, lane);
                 copy_commit();
-                src.look(j + (i + 1) * kWarps, j + (i + 1) * kWarps < j1 ? v.kv : 0, next_page);
             }
 
             // queries as B operands, scaled per row; the factor goes into the row's score unit
