@@ -59,7 +59,8 @@ cudaError_t launch_kv_attn(const AttnParams& p, cudaStream_t stream)
     AttnSpace a;
     layout(p, p.workspace, a);
     if (a.image_tiles > 0 && (e = launch_kv_prompt(p, a, sms, stream)) != cudaSuccess) return e;
-    return launch_kv_step(p, a, sms, stream);
+    if ((e = launch_kv_step(p, a, sms, stream)) != cudaSuccess) return e;
+    return launch_kv_join(p, a, sms, stream);
 }
 
 }  // namespace gdn

@@ -92,6 +92,9 @@ __device__ __forceinline__ bool is_long(const KvBatch& p, const AttnSpace& a, in
 __device__ __forceinline__ int64_t cut_start(int64_t total, int workers, int w) { return total * w / workers; }
 __device__ __forceinline__ int cut_of(int64_t total, int workers, int64_t x) { return (int)(((x + 1) * workers - 1) / total); }
 
+// tokens of half a prompt unit: as many as fit 128 rows of (token, query head of the kv head)
+__device__ __forceinline__ int half_tokens(int group) { return (kUnitRows / 2) / group; }
+
 // ---- where a worker's range begins -------------------------------------------------
 template <int THREADS>
 struct ScanSmem {
@@ -203,7 +206,11 @@ __device__ __forceinline__ void row_unit(uint32_t amax, float& mul, float& back)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// the kernels' launches (gdn_kv_step.cu, gdn_kv_prompt.cu)
+inline int prompt_grid(int sms) { return sms < kPromptMaxWorkers ? sms : kPromptMaxWorkers; }
+
+// the kernels' launches (gdn_kv_step.cu, gdn_kv_prompt.cu, gdn_kv_join.cu)
+int step_rows(const AttnParams& p, const AttnSpace& a);  // query rows of a step unit
+cudaError_t launch_kv_join(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream);
 cudaError_t launch_kv_step(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream);
 cudaError_t launch_kv_prompt(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream);
 

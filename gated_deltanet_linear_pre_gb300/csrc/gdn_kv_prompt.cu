@@ -68,9 +68,6 @@ __device__ __forceinline__ uint4 unpack8(uint2 w, __half2 f)
 }
 
 // ---- the units of long sequences -----------------------------------------------------
-// tokens of a unit: two halves of floor(128 / group)
-__device__ __forceinline__ int half_tokens(int group) { return (kUnitRows / 2) / group; }
-
 // Sum over k < i of ceil((first + (k + 1) span) / 128): the sum of the numerators, rounded up, less the sum
 // of their residues, which repeat with a period of at most 128.
 __device__ __forceinline__ int64_t tiles_before(int first, int span, int i)
@@ -430,6 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
     const volatile int* abort_flag = &sm.abort_flag;
     pdl_wait();
     pdl_launch_dependents();
+    if ((int)blockIdx.x >= a.head->prompt_workers) {  // nothing to do
+        if (warp == kMmaWarp) umma::tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
 
     // A wait that expires is recorded; its warp goes on or ends as its role allows.
     auto await = [&](uint64_t* mbar, uint32_t parity) {
@@ -456,12 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         if (warp >= kQueryWarp) {
             // ---- units and queries ----
             const int span = 2 * tokens, workers = a.head->prompt_workers;
-            const Cut c = a.prompt_cut[blockIdx.x];  // (nothing of it is used past the plan's workers)
+            const Cut c = a.prompt_cut[blockIdx.x];
             const int64_t end = (int)blockIdx.x + 1 < workers ? a.prompt_cut[blockIdx.x + 1].lo : a.head->prompt_total;
             uint32_t x = 0, q_use[2] = {0, 0};  // units, and queries of each half, brought in
-            bool more = (int)blockIdx.x < workers;
+            bool more = true;
             Walk w;
-            if (more) {
+            {
                 w.s = c.s;
                 w.head = c.head;
                 w.i = c.unit;
@@ -783,54 +784,6 @@ done:
 #undef GDN_KV_WAIT
 }
 
-// Block (w, half): where range w is the first that begins inside a unit, joins that unit's parts.  Four
-// threads share a row's channels.
-constexpr int kJoinThreads = 512;
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinThreads) kv_prompt_join_kernel(AttnParams p, AttnSpace a)
-{
-    const int group = p.hq / p.heads, tokens = half_tokens(group);
-    pdl_wait();
-    pdl_launch_dependents();
-    const int w = (int)blockIdx.x + 1, workers = a.head->prompt_workers;
-    if (w >= workers) return;
-    const Cut cut = a.prompt_cut[w];
-    const int64_t total = a.head->prompt_total, begin = cut.lo - cut.from, prev = a.prompt_cut[w - 1].lo;
-    if (cut.j0 == 0 || prev > begin + kPromptUnitCost || !a.ok[cut.s]) return;
-    const int last = cut_of(total, workers, begin + kPromptUnitCost + cut.tiles - 1);
-    const int row = blockIdx.y * 128 + (threadIdx.x & 127), part = threadIdx.x >> 7;
-    const int h = row >> 7, r = row & 127, i_tok = r / group, qh = r - i_tok * group;
-    const int t0 = cu_at(p.cu_seqlens, cut.s, p.T), n = cu_at(p.cu_seqlens, cut.s + 1, p.T) - t0;
-    const int tok = (2 * cut.unit + h) * tokens + i_tok;
-    if (i_tok >= tokens || tok >= n) return;
-    constexpr int E = D / 16;  // float4s a thread
-    float top = -INFINITY, sum = 0.0f;
-    float4 acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-    for (int i = w - 1; i <= last; ++i) {
-        const int slot = 2 * i + (i == w - 1 && prev < begin ? 1 : 0);
-        const float2 st = a.prompt_stat[(size_t)slot * kUnitRows + row];
-        const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.0f : next;
-        const float f0 = ex2(top - ref), f1 = ex2(st.x - ref);
-        sum = sum * f0 + st.y * f1;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float4 o = a.prompt_out[((size_t)slot * (D / 4) + part * E + e) * kUnitRows + row];
-            acc[e].x = acc[e].x * f0 + o.x * f1;
-            acc[e].y = acc[e].y * f0 + o.y * f1;
-            acc[e].z = acc[e].z * f0 + o.z * f1;
-            acc[e].w = acc[e].w * f0 + o.w * f1;
-        }
-        top = next;
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint2* dst = reinterpret_cast<uint2*>(p.y + ((int64_t)(t0 + tok) * p.hq + cut.head * group + qh) * D) + part * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) dst[e] = make_uint2(narrow2<BF16>(acc[e].x * inv, acc[e].y * inv), narrow2<BF16>(acc[e].z * inv, acc[e].w * inv));
-}
-
 // the driver's tensor map encoder, looked up once (the library links the runtime alone)
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
@@ -847,8 +800,8 @@ template <int D, bool BF16, bool E4M3>
 cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
     const int64_t items = (int64_t)a.image_tiles * p.heads;
-    const int grid = sms < kPromptMaxWorkers ? sms : kPromptMaxWorkers;
-    cudaError_t e = launch_k(kv_image_kernel<D, BF16, E4M3>, dim3((unsigned)(items < sms * 8 ? items + 1 : sms * 8)), dim3(kImageThreads), 0, stream, true, p, a, grid);
+    const int grid = prompt_grid(sms);
+    cudaError_t e = launch_k(kv_image_kernel<D, BF16, E4M3>, dim3((unsigned)(items < sms * 6 ? items + 1 : sms * 6)), dim3(kImageThreads), 0, stream, true, p, a, grid);
     if (e != cudaSuccess) return e;
     auto kernel = kv_prompt_kernel<D, BF16, E4M3>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PromptSmem<D>));
@@ -863,9 +816,7 @@ cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_
     if (encode(&q_map, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, ones,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    e = launch_k(kernel, dim3(grid), dim3(kThreads), sizeof(PromptSmem<D>), stream, true, p, a, q_map);
-    if (e != cudaSuccess || grid == 1) return e;
-    return launch_k(kv_prompt_join_kernel<D, BF16>, dim3(grid - 1, 2), dim3(kJoinThreads), 0, stream, true, p, a);
+    return launch_k(kernel, dim3(grid), dim3(kThreads), sizeof(PromptSmem<D>), stream, true, p, a, q_map);
 }
 
 template <int D>

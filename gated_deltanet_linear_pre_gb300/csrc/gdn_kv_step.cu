@@ -1,5 +1,5 @@
 // gdn_kv_step.cu -- attention of few query rows over the 8-bit paged cache (single
-// tokens, drafted tokens), split over the key axis, and the join of its parts.
+// tokens, drafted tokens), split over the key axis.
 //
 // Mathematics.  One pass over the keys with the softmax's running maximum m and sum l (base 2):
 // p = 2^(x - m) with x = scale log2(e) q.k, o = sum p v, and o, l scaled by 2^(m_old - m_new) where a
@@ -449,110 +449,6 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 2 : 4) kv_step_kernel(
     }
 }
 
-// Joins the parts of the units that the ranges cut, in the order of the ranges.  Every block lists the cut
-// units (where a range is the first that begins inside a unit's tiles) and takes its share of their rows;
-// the fewer rows there are (one long sequence: few rows of many parts), the more warps share a row's parts.
-constexpr int kJoinThreads = 512;
-template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttnParams p, AttnSpace a)
-{
-    constexpr int E = D / 32, W = kJoinThreads / 32, R = 8 * NT;
-    struct Joint {
-        int s, head, unit;
-        int from, last, slot;  // its first and last range, the slot of the first part
-    };
-    __shared__ Joint joints[kStepMaxWorkers];
-    __shared__ int counts[W];
-    __shared__ float part[W][D], part_l[W], part_m[W];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = p.hq / p.heads;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int workers = a.head->step_workers;
-    const int64_t total = a.head->step_total;
-    int n = 0;
-    for (int w0 = 1; w0 < workers; w0 += kJoinThreads) {
-        const int w = w0 + tid;
-        Cut cut{};
-        int64_t begin = 0, prev = 0;
-        bool is_first = false;
-        if (w < workers) {
-            cut = a.step_cut[w];
-            begin = cut.lo - cut.from;
-            prev = a.step_cut[w - 1].lo;
-            is_first = cut.j0 > 0 && prev <= begin + kStepUnitCost;
-        }
-        const uint32_t vote = __ballot_sync(0xffffffffu, is_first);
-        if (lane == 0) counts[warp] = __popc(vote);
-        __syncthreads();
-        int at = n + __popc(vote & ((1u << lane) - 1u));
-        for (int i = 0; i < W; ++i) {
-            if (i < warp) at += counts[i];
-            n += counts[i];
-        }
-        if (is_first)
-            // the unit is the first of every range but the one that it begins in the middle of
-            joints[at] = Joint{cut.s, cut.head, cut.unit, w - 1, cut_of(total, workers, begin + kStepUnitCost + cut.tiles - 1),
-                               2 * (w - 1) + (prev < begin ? 1 : 0)};
-        __syncthreads();
-    }
-    const int items = n * R, per_block = (items + (int)gridDim.x - 1) / (int)gridDim.x;
-    int share = W;  // warps a row
-    while (share > 1 && share * per_block > W) share >>= 1;
-    for (int k0 = blockIdx.x * per_block; k0 < min((int)(blockIdx.x + 1) * per_block, items); k0 += W / share) {
-        const int k = k0 + warp / share, in_row = warp % share;
-        bool mine = k < min((int)(blockIdx.x + 1) * per_block, items);
-        const Joint u = joints[mine ? k / R : 0];
-        const int row = k % R, t0 = cu_at(p.cu_seqlens, u.s, p.T);
-        mine = mine && u.unit + row < (cu_at(p.cu_seqlens, u.s + 1, p.T) - t0) * group;
-        float top = -INFINITY, sum = 0.0f, acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-        if (mine)
-#pragma unroll 4
-            for (int i = u.from + in_row; i <= u.last; i += share) {
-                const int slot = i == u.from ? u.slot : 2 * i;
-                const float2 st = a.step_stat[(size_t)slot * kStepMaxRows + row];
-                const float* src = a.step_out + ((size_t)slot * kStepMaxRows + row) * D + lane * E;
-                const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.0f : next;
-                const float f0 = ex2(top - ref), f1 = ex2(st.x - ref);
-                sum = sum * f0 + st.y * f1;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + src[e] * f1;
-                top = next;
-            }
-        if (share > 1) {  // uniform over the block
-            __syncthreads();  // the last round's parts are read
-#pragma unroll
-            for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-            if (lane == 0) {
-                part_m[warp] = top;
-                part_l[warp] = sum;
-            }
-            __syncthreads();
-            if (in_row == 0) {
-                float m = top;
-                for (int i = 1; i < share; ++i) m = fmaxf(m, part_m[warp + i]);
-                const float ref = m == -INFINITY ? 0.0f : m, f0 = ex2(top - ref);
-                sum *= f0;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] *= f0;
-                for (int i = 1; i < share; ++i) {
-                    const float f = ex2(part_m[warp + i] - ref);
-                    sum += f * part_l[warp + i];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += f * part[warp + i][lane * E + e];
-                }
-            }
-        }
-        if (!mine || in_row != 0) continue;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int i = (u.unit + row) / group, qh = u.unit + row - i * group;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.y + ((int64_t)(t0 + i) * p.hq + u.head * group + qh) * D + lane * E);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) dst[e / 2] = narrow2<BF16>(acc[e] * inv, acc[e + 1] * inv);
-    }
-}
-
 template <int D, bool BF16, bool E4M3, int NT>
 cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
@@ -562,22 +458,15 @@ cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int grid = min(sms * (NT == 4 ? 2 : 4), kStepMaxWorkers);
-    e = launch_k(kernel, dim3(grid), dim3(kStepThreads), smem, stream, true, p, a);
-    if (e != cudaSuccess || grid == 1) return e;
-    return launch_k(kv_join_kernel<D, BF16, NT>, dim3(min(grid, 2 * sms)), dim3(kJoinThreads), 0, stream, true, p, a);
+    return launch_k(kernel, dim3(grid), dim3(kStepThreads), smem, stream, true, p, a);
 }
 
 template <int D, bool BF16, bool E4M3>
 cudaError_t launch_rows(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
-    // query rows of an average sequence decide the tile: 8 rows as long as they hold them, else 16 or 32
-    // (a warp's codes serve more rows).  An average above kLongRows says that there are long sequences, which
-    // the prompt kernel takes; those left here are then taken to bring single tokens.
-    const int group = p.hq / p.heads;
-    int64_t rows = ((int64_t)p.T * group + p.n_seq - 1) / p.n_seq;
-    if (rows > a.most_rows) rows = group;
-    if (rows <= 8) return launch<D, BF16, E4M3, 1>(p, a, sms, stream);
-    if (rows <= 16) return launch<D, BF16, E4M3, 2>(p, a, sms, stream);
+    const int rows = step_rows(p, a);
+    if (rows == 8) return launch<D, BF16, E4M3, 1>(p, a, sms, stream);
+    if (rows == 16) return launch<D, BF16, E4M3, 2>(p, a, sms, stream);
     return launch<D, BF16, E4M3, 4>(p, a, sms, stream);
 }
 
@@ -589,6 +478,17 @@ cudaError_t launch_types(const AttnParams& p, const AttnSpace& a, int sms, cudaS
 }
 
 }  // namespace
+
+int step_rows(const AttnParams& p, const AttnSpace& a)
+{
+    // query rows of an average sequence decide the tile: 8 rows as long as they hold them, else 16 or 32
+    // (a warp's codes serve more rows).  An average above kLongRows says that there are long sequences, which
+    // the prompt kernel takes; those left here are then taken to bring single tokens.
+    const int group = p.hq / p.heads;
+    int64_t rows = ((int64_t)p.T * group + p.n_seq - 1) / p.n_seq;
+    if (rows > a.most_rows) rows = group;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : kStepMaxRows;
+}
 
 cudaError_t launch_kv_step(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_t stream)
 {
