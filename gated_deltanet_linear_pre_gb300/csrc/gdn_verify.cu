@@ -10,7 +10,9 @@
 // bound by latency for one sequence.  A cluster of 8 CTAs shares a sequence (one CTA per sequence
 // would leave most SMs idle in small batches); each sums its part of the row in segments of 512
 // weights, the CTAs exchange their totals through distributed shared memory, and the one CTA whose part
-// holds the threshold finds its segment from the sums and reads those 512 weights again.
+// holds the threshold finds its segment from the sums and reads those 512 weights again.  CTAs of 256
+// threads: six share an SM, so that one's search for the first rejected draft and its exchange run under
+// the others' loads.
 #include <cooperative_groups.h>
 
 #include "gdn_internal.cuh"
@@ -20,7 +22,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtas = 8;          // CTAs a sequence (the portable cluster size)
 constexpr int kSegment = 512;     // weights a segment: 16 a lane
 constexpr int kMaxSegments = ((1 << 19) / kCtas + kSegment - 1) / kSegment;
@@ -46,27 +48,38 @@ struct Row {
     const float* p;
     const float* q;  // NULL: the weights are p's alone
     bool vec;        // both rows 16-byte aligned
-    // 4 weights at i .. i + 3 (0 from `end` on)
-    __device__ __forceinline__ void four(int i, int end, uint64_t (&w)[4]) const
+    __device__ __forceinline__ uint64_t one(int i) const
     {
-        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (vec && i + 4 <= end) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
-            a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
-            if (q) {
-                const float4 y = __ldg(reinterpret_cast<const float4*>(q + i));
-                b[0] = y.x; b[1] = y.y; b[2] = y.z; b[3] = y.w;
+        return weight(__saturatef(__fsub_rn(__ldg(p + i), q ? __ldg(q + i) : 0.0f)));  // NaN saturates to 0
+    }
+    // the sum of a segment's weights from i on (0 from `end` on); a lane's own share of it
+    __device__ __forceinline__ uint64_t share(int i, int end, int lane) const
+    {
+        uint64_t sum = 0;
+        if (i + kSegment > end) {
+            for (int k = i + lane; k < end; k += 32) sum += one(k);
+        } else if (vec) {
+            float4 a[kSegment / 128], b[kSegment / 128];
+#pragma unroll
+            for (int j = 0; j < kSegment / 128; ++j) {
+                a[j] = __ldcs(reinterpret_cast<const float4*>(p + i + j * 128) + lane);
+                b[j] = q ? __ldcs(reinterpret_cast<const float4*>(q + i + j * 128) + lane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
+#pragma unroll
+            for (int j = 0; j < kSegment / 128; ++j)
+                sum += (weight(__saturatef(__fsub_rn(a[j].x, b[j].x))) + weight(__saturatef(__fsub_rn(a[j].y, b[j].y)))) +
+                       (weight(__saturatef(__fsub_rn(a[j].z, b[j].z))) + weight(__saturatef(__fsub_rn(a[j].w, b[j].w))));
         } else {
+            float a[kSegment / 32], b[kSegment / 32];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (i + e < end) {
-                    a[e] = __ldg(p + i + e);
-                    if (q) b[e] = __ldg(q + i + e);
-                }
+            for (int j = 0; j < kSegment / 32; ++j) {
+                a[j] = __ldcs(p + i + j * 32 + lane);
+                b[j] = q ? __ldcs(q + i + j * 32 + lane) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < kSegment / 32; ++j) sum += weight(__saturatef(__fsub_rn(a[j], b[j])));
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = weight(__saturatef(__fsub_rn(a[e], b[e])));  // NaN saturates to 0
+        return sum;
     }
 };
 
@@ -89,14 +102,17 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) verify
     const float* const p0 = p.p + (size_t)s * (p.max_draft + 1) * p.p_stride;
     const float* const q0 = p.q + (size_t)s * p.max_draft * p.q_stride;
     if (warp == 0) {  // every CTA finds the first draft that is not accepted, 32 drafts at a time
-        int accepted = count;
-        for (int i0 = 0; i0 < count; i0 += 32) {
+        // (a draft, its random number and the count are loaded together; then the two probabilities)
+        int accepted = p.max_draft;
+        for (int i0 = 0; i0 < p.max_draft; i0 += 32) {
             const int i = i0 + lane;
             bool ok = true;
-            if (i < count) {
+            if (i < p.max_draft) {
                 const int x = __ldg(p.draft + (size_t)s * p.max_draft + i);
-                ok = x >= 0 && x < p.vocab &&
-                     __fmul_rn(__ldg(u + i), __ldg(q0 + (size_t)i * p.q_stride + x)) < __ldg(p0 + (size_t)i * p.p_stride + x);
+                const float r = __ldg(u + i);
+                const bool there = x >= 0 && x < p.vocab;
+                const size_t at = there ? x : 0;
+                ok = there && __fmul_rn(r, __ldg(q0 + (size_t)i * p.q_stride + at)) < __ldg(p0 + (size_t)i * p.p_stride + at);
             }
             const uint32_t bad = __ballot_sync(0xffffffffu, !ok);
             if (bad) {
@@ -104,6 +120,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) verify
                 break;
             }
         }
+        accepted = min(accepted, count);
         if (lane == 0) sm.accepted = accepted;
     }
     __syncthreads();
@@ -119,14 +136,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) verify
     for (int pass = 0; pass < 2; ++pass) {  // the second one where the residual has no mass: p itself
         row.vec = ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) & 15u) == 0;
         for (int g = warp; g < segments; g += kWarps) {
-            uint64_t sum = 0;
-#pragma unroll
-            for (int j = 0; j < kSegment / 128; ++j) {
-                uint64_t w[4];
-                row.four(lo + g * kSegment + j * 128 + lane * 4, hi, w);
-                sum += (w[0] + w[1]) + (w[2] + w[3]);
-            }
-            sum = warp_sum64(sum);
+            const uint64_t sum = warp_sum64(row.share(lo + g * kSegment, hi, lane));
             if (lane == 0) sm.seg[g] = sum;
         }
         __syncthreads();
@@ -179,7 +189,8 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) verify
     for (int j = 0; j < kSegment / 128; ++j) {
         const int i = lo + g0 * kSegment + j * 128 + lane * 4;
         uint64_t w[4];
-        row.four(i, hi, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = i + e < hi ? row.one(i + e) : 0;
         uint64_t incl = (w[0] + w[1]) + (w[2] + w[3]);
         const uint64_t v = incl;
 #pragma unroll
