@@ -11,8 +11,8 @@
 // Layout.  The unit of work is (page touched by a sequence, kv head, k or v): its scale is one maximum
 // over the unit's rows, so no unit needs another's result and the call is one launch without
 // atomics.  16 bytes per thread: D / 8 threads hold a row, and the partner channels of a rotation
-// half a head apart come from another lane of the row by shuffles.  Queries go by (token, 8 heads): a
-// lane's eight loads are in flight together and share the angles it holds.  A sequence's pages get
+// half a head apart come from another lane of the row by shuffles.  Queries go by (token, 4 heads): a
+// lane's four loads are in flight together and share the angles it holds.  A sequence's pages get
 // slots floor(cu[s] / P) + 2 s onwards: n tokens touch at most floor((n - 1) / P) + 2 pages, so
 // floor(T / P) + 2 n_seq slots hold any batch without a prefix sum on the host.
 #include "gdn_kv.cuh"
@@ -232,7 +232,7 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
 }
 
 // (token, kQueryHeads heads) by D / 8 lanes
-constexpr int kQueryHeads = 8;
+constexpr int kQueryHeads = 4;
 template <bool BF16, int D>
 __device__ __forceinline__ void rotate_queries(const AppendParams& p, int64_t item, int64_t items, int chunks)
 {
@@ -240,20 +240,16 @@ __device__ __forceinline__ void rotate_queries(const AppendParams& p, int64_t it
     const int c = threadIdx.x % kRowLanes;
     const int64_t mine = min(item, items - 1);  // lanes past the end take part in shuffles
     const int t = (int)(mine / chunks), h0 = (int)(mine - (int64_t)t * chunks) * kQueryHeads;
-    int pos = 0;
-    if (p.rot > 0) {
-        // the warp looks for its first token; the others are the same or follow it
-        int s = warp_find(p.n_seq, __shfl_sync(0xffffffffu, t, 0), [&](int i) { return cu_at(p.cu_seqlens, i, p.T); });
-        while (s + 1 < p.n_seq && cu_at(p.cu_seqlens, s + 1, p.T) <= t) ++s;
-        pos = past_at(p.past, s) + t - cu_at(p.cu_seqlens, s, p.T);
-    }
     const uint16_t* src = p.q + (int64_t)t * p.q_stride + 8 * c;
     uint16_t* dst = p.q_out + (int64_t)t * p.hq * D + 8 * c;
     uint4 raw[kQueryHeads];
 #pragma unroll
-    for (int i = 0; i < kQueryHeads; ++i) raw[i] = h0 + i < p.hq ? __ldg(reinterpret_cast<const uint4*>(src + (h0 + i) * D)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kQueryHeads; ++i) raw[i] = h0 + i < p.hq ? __ldcs(reinterpret_cast<const uint4*>(src + (h0 + i) * D)) : make_uint4(0u, 0u, 0u, 0u);
     if (p.rot > 0) {
-        const Angles angles(p, c, pos);
+        // the warp looks for its first token; the others are the same or follow it
+        int s = warp_find(p.n_seq, __shfl_sync(0xffffffffu, t, 0), [&](int i) { return cu_at(p.cu_seqlens, i, p.T); });
+        while (s + 1 < p.n_seq && cu_at(p.cu_seqlens, s + 1, p.T) <= t) ++s;
+        const Angles angles(p, c, past_at(p.past, s) + t - cu_at(p.cu_seqlens, s, p.T));
 #pragma unroll
         for (int i = 0; i < kQueryHeads; ++i) {
             float x[8];
@@ -265,12 +261,12 @@ __device__ __forceinline__ void rotate_queries(const AppendParams& p, int64_t it
     if (item < items)
 #pragma unroll
         for (int i = 0; i < kQueryHeads; ++i)
-            if (h0 + i < p.hq) *reinterpret_cast<uint4*>(dst + (h0 + i) * D) = raw[i];
+            if (h0 + i < p.hq) __stcs(reinterpret_cast<uint4*>(dst + (h0 + i) * D), raw[i]);
 }
 
 // blocks [0, unit_blocks) store pages, the others rotate queries
 template <bool BF16, bool E4M3, int D, int THREADS, int UNIT, int HELD>
-__global__ void __launch_bounds__(THREADS) kv_append_kernel(AppendParams p, int units, int unit_blocks)
+__global__ void __launch_bounds__(THREADS, UNIT == 32 ? 1 : 1024 / THREADS) kv_append_kernel(AppendParams p, int units, int unit_blocks)
 {
     pdl_wait();
     pdl_launch_dependents();
