@@ -24,11 +24,13 @@ template <int D> constexpr int kStepTile = D == 128 ? kSub : 2 * kSub;  // posit
 constexpr int kStepMaxRows = 32;       // query rows of a step unit, at most
 constexpr int kStepMaxWorkers = 640;
 constexpr int kStepUnitCost = 16;      // a step unit's beginning and end, in tiles
-constexpr int kPromptUnitCost = 1;     // a prompt unit's
+constexpr int kPromptUnitCost = 2;     // a prompt unit's
 constexpr int kKeys = 128;             // positions of a prompt tile
 constexpr int kUnitRows = 256;         // query rows of a prompt unit: two halves of 128
 constexpr int kPromptMaxWorkers = 160;
-constexpr int kLongRows = 64;
+// Above this many query rows the prompt way is faster: 16 sequences of 8K positions (4 heads, e4m3) took
+// 162 us by steps at 128 rows and 234 at 192, 180 and 185 us by images.
+constexpr int kLongRows = 128;
 constexpr size_t kImageCap = (size_t)2 << 30;  // bytes of images; sequences past it take the step kernel
 
 constexpr uint32_t kAttnTimeout = 1u;  // failure record: a bounded wait expired

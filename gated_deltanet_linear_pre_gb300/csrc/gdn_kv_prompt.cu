@@ -217,8 +217,8 @@ __device__ __forceinline__ uint4 unpack8_bf16(uint2 w, float f)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Block 0 makes the prompt kernel's plan; each of the others takes an equal range of the (tile, kv head)
-// items of all candidates, head fastest.
+// Block 0 makes the prompt kernel's plan; each of the others takes an equal range of the (kv head, tile)
+// items of all candidates, tiles fastest: the largest scales are looked for once a (sequence, head).
 template <int D, bool BF16, bool E4M3>
 __global__ void __launch_bounds__(kImageThreads) kv_image_kernel(AttnParams p, AttnSpace a, int prompt_grid)
 {
@@ -234,88 +234,85 @@ __global__ void __launch_bounds__(kImageThreads) kv_image_kernel(AttnParams p, A
     }
     auto weight = [&](int s) {
         const SeqView v = seq_view(p, s);
-        return candidate(p, a, v) ? (int64_t)key_tiles(v.kv) : 0;
+        return candidate(p, a, v) ? (int64_t)p.heads * key_tiles(v.kv) : 0;
     };
-    const int64_t tiles = scan_total<kImageThreads>(p.n_seq, weight, scan), items = tiles * p.heads;
+    const int64_t items = scan_total<kImageThreads>(p.n_seq, weight, scan);
     const int64_t lo = cut_start(items, gridDim.x - 1, blockIdx.x - 1), hi = cut_start(items, gridDim.x - 1, blockIdx.x);
     if (lo >= hi) return;
     int64_t before;
-    int s = scan_find<kImageThreads>(p.n_seq, lo / p.heads, weight, scan, before);
-    int64_t at = lo / p.heads - before;  // tile within the sequence
-    int head = (int)(lo % p.heads);
-    for (int64_t x = lo; x < hi && s < p.n_seq;) {
+    int s = scan_find<kImageThreads>(p.n_seq, lo, weight, scan, before);
+    const float sign = p.scale < 0.0f ? -1.0f : 1.0f;  // scores times |scale|: a row's largest is its maximum's
+    int64_t at = lo - before;                          // item within the sequence
+    for (int64_t x = lo; x < hi && s < p.n_seq; ++s) {
         const SeqView v = seq_view(p, s);
-        const int n = candidate(p, a, v) ? key_tiles(v.kv) : 0;
-        if (at >= n) {
-            before += n;
-            at = 0;
-            ++s;
-            continue;
-        }
-        // the sequence's images fit, every page is there; its largest scales (NaN ones apart)
-        const int pages = (v.kv + p.page - 1) >> shift;
-        float mk = 0.0f, mv = 0.0f;
-        bool there = before + n <= a.image_tiles;
-        for (int i = tid; i < pages; i += kImageThreads) {
-            const int page = page_at(p, s, i);
-            if (page < 0) {
-                there = false;
-            } else {
-                mk = fmaxf(mk, __ldg(p.k_scale + (size_t)page * p.heads + head));
-                mv = fmaxf(mv, __ldg(p.v_scale + (size_t)page * p.heads + head));
-            }
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
-            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
-        }
-        if (lane == 0) {
-            top_k[warp] = mk;
-            top_v[warp] = mv;
-        }
-        there = __syncthreads_and(there);
-#pragma unroll
-        for (int w = 0; w < kImageThreads / 32; ++w) {
-            mk = fmaxf(mk, top_k[w]);
-            mv = fmaxf(mv, top_v[w]);
-        }
-        if (at == 0 && tid == 0) {
-            if (head == 0) {
-                a.ok[s] = there;
-                a.image_base[s] = there ? (int)before : 0;
-            }
-            if (there) a.norm[(size_t)before * p.heads + head] = make_float2(mk, mv);
-        }
-        if (there) {
-            const float sign = p.scale < 0.0f ? -1.0f : 1.0f;  // scores times |scale|: a row's largest is its maximum's
-            unsigned char* const img = a.images + ((size_t)(before + at) * p.heads + head) * (2 * kTileBytes<D>);
-            // neighbouring lanes take neighbouring channels: whole rows of codes and of an image's planes
-#pragma unroll 4
-            for (int i = tid; i < kKeys * (D / 8); i += kImageThreads) {
-                const int pos = i / (D / 8), c8 = i % (D / 8);
-                const int at_pos = (int)at * kKeys + pos;
-                uint4 wk = make_uint4(0u, 0u, 0u, 0u), wv = wk;
-                if (at_pos < v.kv) {
-                    const size_t row = (size_t)page_at(p, s, at_pos >> shift) * p.heads + head;
-                    const size_t src = (row * p.page + (at_pos & (p.page - 1))) * D + 8 * c8;
-                    const float ks = __ldg(p.k_scale + row), vs = __ldg(p.v_scale + row);
-                    // (a scale of 0 may meet a largest one of 0; NaN scales stay NaN)
-                    const float fk = (ks == 0.0f ? 0.0f : BF16 ? ks : ks / mk * kUp<E4M3>) * sign, fv = vs == 0.0f ? 0.0f : vs / mv * kUp<E4M3>;
-                    const uint2 ck = __ldg(reinterpret_cast<const uint2*>(p.k + src));
-                    wk = BF16 ? unpack8_bf16<E4M3>(ck, fk) : unpack8<E4M3>(ck, __float2half2_rn(fk));
-                    wv = unpack8<E4M3>(__ldg(reinterpret_cast<const uint2*>(p.v + src)), __float2half2_rn(fv));
+        if (!candidate(p, a, v)) continue;
+        const int n = key_tiles(v.kv), pages = (v.kv + p.page - 1) >> shift;
+        const int64_t base = before / p.heads;         // image tiles before the sequence's
+        before += (int64_t)p.heads * n;
+        for (int head = (int)(at / n); head < p.heads && x < hi; ++head) {
+            // whether the sequence's images fit and every page is there; its largest scales (NaN ones apart)
+            float mk = 0.0f, mv = 0.0f;
+            bool there = base + n <= a.image_tiles;
+            for (int i = tid; i < pages; i += kImageThreads) {
+                const int page = page_at(p, s, i);
+                if (page < 0) {
+                    there = false;
+                } else {
+                    mk = fmaxf(mk, __ldg(p.k_scale + (size_t)page * p.heads + head));
+                    mv = fmaxf(mv, __ldg(p.v_scale + (size_t)page * p.heads + head));
                 }
-                *reinterpret_cast<uint4*>(img + image_off(pos, c8)) = wk;
-                *reinterpret_cast<uint4*>(img + kTileBytes<D> + image_off(pos, c8)) = wv;
             }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
+                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
+            }
+            if (lane == 0) {
+                top_k[warp] = mk;
+                top_v[warp] = mv;
+            }
+            there = __syncthreads_and(there);
+#pragma unroll
+            for (int w = 0; w < kImageThreads / 32; ++w) {
+                mk = fmaxf(mk, top_k[w]);
+                mv = fmaxf(mv, top_v[w]);
+            }
+            const int first = (int)(at - (int64_t)head * n);
+            if (first == 0 && tid == 0) {
+                if (head == 0) {
+                    a.ok[s] = there;
+                    a.image_base[s] = there ? (int)base : 0;
+                }
+                if (there) a.norm[(size_t)base * p.heads + head] = make_float2(mk, mv);
+            }
+            const int last = (int)min((int64_t)n, first + (hi - x));
+            x += last - first;
+            at = (int64_t)(head + 1) * n;
+            for (int tile = first; there && tile < last; ++tile) {
+                unsigned char* const img = a.images + ((size_t)(base + tile) * p.heads + head) * (2 * kTileBytes<D>);
+                // neighbouring lanes take neighbouring channels: whole rows of codes and of an image's planes
+#pragma unroll 4
+                for (int i = tid; i < kKeys * (D / 8); i += kImageThreads) {
+                    const int pos = i / (D / 8), c8 = i % (D / 8);
+                    const int at_pos = tile * kKeys + pos;
+                    uint4 wk = make_uint4(0u, 0u, 0u, 0u), wv = wk;
+                    if (at_pos < v.kv) {
+                        const size_t row = (size_t)page_at(p, s, at_pos >> shift) * p.heads + head;
+                        const size_t src = (row * p.page + (at_pos & (p.page - 1))) * D + 8 * c8;
+                        const float ks = __ldg(p.k_scale + row), vs = __ldg(p.v_scale + row);
+                        // (a scale of 0 may meet a largest one of 0; NaN scales stay NaN)
+                        const float fk = (ks == 0.0f ? 0.0f : BF16 ? ks : ks / mk * kUp<E4M3>) * sign, fv = vs == 0.0f ? 0.0f : vs / mv * kUp<E4M3>;
+                        const uint2 ck = __ldg(reinterpret_cast<const uint2*>(p.k + src));
+                        wk = BF16 ? unpack8_bf16<E4M3>(ck, fk) : unpack8<E4M3>(ck, __float2half2_rn(fk));
+                        wv = unpack8<E4M3>(__ldg(reinterpret_cast<const uint2*>(p.v + src)), __float2half2_rn(fv));
+                    }
+                    *reinterpret_cast<uint4*>(img + image_off(pos, c8)) = wk;
+                    *reinterpret_cast<uint4*>(img + kTileBytes<D> + image_off(pos, c8)) = wv;
+                }
+            }
+            __syncthreads();  // top_k, top_v read
         }
-        __syncthreads();  // top_k, top_v read
-        ++x;
-        if (++head == p.heads) {
-            head = 0;
-            ++at;
-        }
+        at = 0;
     }
 }
 
