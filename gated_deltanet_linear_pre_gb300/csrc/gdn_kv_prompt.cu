@@ -220,10 +220,15 @@ __device__ __forceinline__ uint4 unpack8_bf16(uint2 w, float f)
 // Block 0 makes the prompt kernel's plan; each of the others takes an equal range of the (kv head, tile)
 // items of all candidates, tiles fastest: the largest scales are looked for once a (sequence, head).
 template <int D, bool BF16, bool E4M3>
-__global__ void __launch_bounds__(kImageThreads) kv_image_kernel(AttnParams p, AttnSpace a, int prompt_grid)
+__global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p, AttnSpace a, int prompt_grid)
 {
     __shared__ ScanSmem<kImageThreads> scan;
     __shared__ float top_k[kImageThreads / 32], top_v[kImageThreads / 32];
+    struct Part {
+        int64_t at;  // byte of its first code
+        float k, v;
+    };
+    __shared__ Part parts[kKeys / kSub];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, shift = page_shift(p);
     pdl_wait();
     pdl_launch_dependents();
@@ -289,26 +294,44 @@ __global__ void __launch_bounds__(kImageThreads) kv_image_kernel(AttnParams p, A
             x += last - first;
             at = (int64_t)(head + 1) * n;
             for (int tile = first; there && tile < last; ++tile) {
-                unsigned char* const img = a.images + ((size_t)(base + tile) * p.heads + head) * (2 * kTileBytes<D>);
-                // neighbouring lanes take neighbouring channels: whole rows of codes and of an image's planes
-#pragma unroll 4
-                for (int i = tid; i < kKeys * (D / 8); i += kImageThreads) {
-                    const int pos = i / (D / 8), c8 = i % (D / 8);
-                    const int at_pos = tile * kKeys + pos;
-                    uint4 wk = make_uint4(0u, 0u, 0u, 0u), wv = wk;
-                    if (at_pos < v.kv) {
-                        const size_t row = (size_t)page_at(p, s, at_pos >> shift) * p.heads + head;
-                        const size_t src = (row * p.page + (at_pos & (p.page - 1))) * D + 8 * c8;
+                // where the tile's 16-position parts lie and their factors
+                if (tid < kKeys / kSub) {
+                    const int pos = tile * kKeys + tid * kSub;
+                    Part part{-1, 0.0f, 0.0f};
+                    if (pos < v.kv) {
+                        const int64_t row = (int64_t)page_at(p, s, pos >> shift) * p.heads + head;
                         const float ks = __ldg(p.k_scale + row), vs = __ldg(p.v_scale + row);
+                        part.at = (row * p.page + (pos & (p.page - 1))) * D;
                         // (a scale of 0 may meet a largest one of 0; NaN scales stay NaN)
-                        const float fk = (ks == 0.0f ? 0.0f : BF16 ? ks : ks / mk * kUp<E4M3>) * sign, fv = vs == 0.0f ? 0.0f : vs / mv * kUp<E4M3>;
-                        const uint2 ck = __ldg(reinterpret_cast<const uint2*>(p.k + src));
-                        wk = BF16 ? unpack8_bf16<E4M3>(ck, fk) : unpack8<E4M3>(ck, __float2half2_rn(fk));
-                        wv = unpack8<E4M3>(__ldg(reinterpret_cast<const uint2*>(p.v + src)), __float2half2_rn(fv));
+                        part.k = (ks == 0.0f ? 0.0f : BF16 ? ks : ks / mk * kUp<E4M3>) * sign;
+                        part.v = vs == 0.0f ? 0.0f : vs / mv * kUp<E4M3>;
                     }
-                    *reinterpret_cast<uint4*>(img + image_off(pos, c8)) = wk;
-                    *reinterpret_cast<uint4*>(img + kTileBytes<D> + image_off(pos, c8)) = wv;
+                    parts[tid] = part;
                 }
+                __syncthreads();
+                // neighbouring lanes take neighbouring channels: whole rows of codes and of an image's planes; a
+                // thread's codes are all on their way before the first is unpacked
+                constexpr int kTimes = kKeys * (D / 8) / kImageThreads, kStep = kImageThreads / (D / 8);
+                const int pos0 = tid / (D / 8), c8 = tid % (D / 8);
+                uint2 ck[kTimes], cv[kTimes];
+#pragma unroll
+                for (int i = 0; i < kTimes; ++i) {
+                    const int pos = pos0 + i * kStep;
+                    const int64_t src = parts[pos / kSub].at + (pos % kSub) * D + 8 * c8;
+                    const bool in = tile * kKeys + pos < v.kv;
+                    ck[i] = in ? __ldcs(reinterpret_cast<const uint2*>(p.k + src)) : make_uint2(0u, 0u);
+                    cv[i] = in ? __ldcs(reinterpret_cast<const uint2*>(p.v + src)) : make_uint2(0u, 0u);
+                }
+                unsigned char* const img = a.images + ((size_t)(base + tile) * p.heads + head) * (2 * kTileBytes<D>);
+#pragma unroll
+                for (int i = 0; i < kTimes; ++i) {
+                    const int pos = pos0 + i * kStep;
+                    const bool in = tile * kKeys + pos < v.kv;  // (a NaN factor leaves what lies behind at 0)
+                    const float fk = in ? parts[pos / kSub].k : 0.0f, fv = in ? parts[pos / kSub].v : 0.0f;
+                    *reinterpret_cast<uint4*>(img + image_off(pos, c8)) = BF16 ? unpack8_bf16<E4M3>(ck[i], fk) : unpack8<E4M3>(ck[i], __float2half2_rn(fk));
+                    *reinterpret_cast<uint4*>(img + kTileBytes<D> + image_off(pos, c8)) = unpack8<E4M3>(cv[i], __float2half2_rn(fv));
+                }
+                __syncthreads();  // parts read
             }
             __syncthreads();  // top_k, top_v read
         }
@@ -798,7 +821,7 @@ cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_
 {
     const int64_t items = (int64_t)a.image_tiles * p.heads;
     const int grid = prompt_grid(sms);
-    cudaError_t e = launch_k(kv_image_kernel<D, BF16, E4M3>, dim3((unsigned)(items < sms * 6 ? items + 1 : sms * 6)), dim3(kImageThreads), 0, stream, true, p, a, grid);
+    cudaError_t e = launch_k(kv_image_kernel<D, BF16, E4M3>, dim3((unsigned)(items < sms * 3 ? items + 1 : sms * 3)), dim3(kImageThreads), 0, stream, true, p, a, grid);
     if (e != cudaSuccess) return e;
     auto kernel = kv_prompt_kernel<D, BF16, E4M3>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PromptSmem<D>));
