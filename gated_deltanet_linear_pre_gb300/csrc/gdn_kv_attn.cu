@@ -23,8 +23,12 @@ size_t layout(const KvBatch& b, void* ws, AttnSpace& a)
     a.step_stat = reinterpret_cast<float2*>(take((size_t)2 * kStepMaxWorkers * kStepMaxRows * 8));
     a.step_out = reinterpret_cast<float*>(take((size_t)2 * kStepMaxWorkers * kStepMaxRows * dim * 4));
     a.most_rows = 0x7fffffff;
-    // as many long sequences as the batch's tokens allow, each as long as the page table allows
-    const size_t long_seqs = (size_t)b.T * group / (kLongRows + 1);
+    a.whole_units = (int64_t)b.max_pages * b.page <= (int64_t)kWholePositions * (128 / b.dim);
+    // As many long sequences as the batch's tokens allow where every sequence has one at least, each as long as
+    // the page table allows.  In a batch with many empty sequences there may be more: those without room for
+    // images take the step kernel.  (Counting on empty ones would launch the prompt way's kernels, some 8 us, in
+    // every decode step of a large batch.)
+    const size_t extra = (size_t)b.T > n ? (size_t)b.T - n : 0, long_seqs = extra / (kLongRows / group);
     const size_t per_seq = ((size_t)b.max_pages * b.page + kKeys - 1) / kKeys;
     const size_t tile_bytes = (size_t)b.heads * 2 * kKeys * dim * 2;
     size_t tiles = (long_seqs < n ? long_seqs : n) * per_seq;
@@ -60,7 +64,7 @@ cudaError_t launch_kv_attn(const AttnParams& p, cudaStream_t stream)
     layout(p, p.workspace, a);
     if (a.image_tiles > 0 && (e = launch_kv_prompt(p, a, sms, stream)) != cudaSuccess) return e;
     if ((e = launch_kv_step(p, a, sms, stream)) != cudaSuccess) return e;
-    return launch_kv_join(p, a, sms, stream);
+    return a.whole_units && a.image_tiles == 0 ? cudaSuccess : launch_kv_join(p, a, sms, stream);
 }
 
 }  // namespace gdn

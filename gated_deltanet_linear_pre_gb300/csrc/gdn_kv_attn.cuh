@@ -31,6 +31,9 @@ constexpr int kPromptMaxWorkers = 160;
 // Above this many query rows the prompt way is faster: 16 sequences of 8K positions (4 heads, e4m3) took
 // 162 us by steps at 128 rows and 234 at 192, 180 and 185 us by images.
 constexpr int kLongRows = 128;
+// Where the page table holds at most this many positions (times 128 / head_dim) step units stay whole, and no
+// kernel joins them: a unit's last tiles take less than a second launch.
+constexpr int kWholePositions = 512;
 constexpr size_t kImageCap = (size_t)2 << 30;  // bytes of images; sequences past it take the step kernel
 
 constexpr uint32_t kAttnTimeout = 1u;  // failure record: a bounded wait expired
@@ -81,6 +84,7 @@ struct AttnSpace {
     unsigned char* images; // [image_tiles][heads][2]: K and V operand images of 128 positions
     int image_tiles;
     int most_rows;         // sequences with more query rows are candidates for the prompt way
+    int whole_units;       // step units are not cut: ranges of units, not of tiles
 };
 
 __device__ __forceinline__ bool candidate(const KvBatch& p, const AttnSpace& a, const SeqView& v)

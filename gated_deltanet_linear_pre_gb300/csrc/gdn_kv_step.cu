@@ -160,12 +160,12 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 2 : 4) kv_step_kernel(
     auto weight = [&](int s) {
         int groups, tiles;
         step_units<D, NT>(p, a, s, seq_view(p, s), groups, tiles);
-        return (int64_t)p.heads * groups * (tiles + kStepUnitCost);
+        return (int64_t)p.heads * groups * (a.whole_units ? 1 : tiles + kStepUnitCost);
     };
     const int64_t total = scan_total<kStepThreads>(p.n_seq, weight, sm.scan);
     // at least two tiles a warp beside a unit's constant: shorter ranges cost more to join than they save
-    constexpr int kLeast = kStepUnitCost + 2 * kWarps;
-    const int workers = (int)min((int64_t)gridDim.x, (total + kLeast - 1) / kLeast);
+    const int least = a.whole_units ? 1 : kStepUnitCost + 2 * kWarps;
+    const int workers = (int)min((int64_t)gridDim.x, (total + least - 1) / least);
     if (blockIdx.x == 0 && tid == 0) {
         a.head->step_total = total;
         a.head->step_workers = workers;
@@ -184,10 +184,10 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 2 : 4) kv_step_kernel(
         int groups, tiles;
         step_units<D, NT>(p, a, s, v, groups, tiles);
         const int64_t units = (int64_t)p.heads * groups;
-        const int cost = tiles + kStepUnitCost;
+        const int cost = a.whole_units ? 1 : tiles + kStepUnitCost;
         for (int64_t unit = at / cost; unit < units && x < hi; ++unit) {
             const int from = (int)(at - unit * cost), to = (int)min((int64_t)cost, from + (hi - x));
-            const int j0 = max(from - kStepUnitCost, 0), j1 = to - kStepUnitCost;
+            const int j0 = a.whole_units ? 0 : max(from - kStepUnitCost, 0), j1 = a.whole_units ? tiles : to - kStepUnitCost;
             at = (unit + 1) * cost;
             x += to - from;
             const int head = (int)(unit / groups), row0 = (int)(unit - (int64_t)head * groups) * R;
