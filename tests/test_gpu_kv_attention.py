@@ -333,6 +333,86 @@ def test_attention_bf16_queries_beyond_fp16():
     check_attention(b, q=q, softmax_scale=1e-30)
 
 
+# ---- the prompt way: sequences of more than 128 query rows ------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_scales_of_either_sign_and_uneven_pages(fmt, dtype, dim):
+    """Pages whose k and v differ by 2^8 in size, scores of several hundred, scales of 0 and below."""
+    b = Batch([70, 1, 150], [100, 600, 0], 8, 2, dim, 32, fmt, dtype, seed=2, scale=6.0)
+    b.fill_past()
+    b.append()
+    g = torch.Generator("cuda").manual_seed(1)
+    for scales in (b.ks, b.vs):
+        scales.mul_(torch.exp2(torch.randint(-8, 1, scales.shape, device="cuda", generator=g).float()))
+    for softmax_scale in (0.1, -0.1, 0.0):
+        check_attention(b, softmax_scale=softmax_scale)
+
+
+def test_prompt_pages_that_are_missing_zero_or_not_finite():
+    """A hole in the table, a page of zeros, and a NaN page: only rows that see it are NaN."""
+    import kv_util as u
+    b = Batch([80, 80, 80], [300, 300, 300], 4, 2, 128, 64, "int8", "fp16", seed=4)
+    b.fill_past()
+    b.append()
+    b.table_h[0, 1] = -1
+    b.table_h[0, 3] = 10 ** 6
+    b.table.copy_(torch.tensor(b.table_h))
+    zero, bad = int(b.table_h[1, 2]), int(b.table_h[2, 5])
+    for t in (b.k, b.v, b.ks, b.vs):
+        t[zero] = 0
+    check_attention(b)
+    b.vs[bad, 1] = float("nan")                       # positions 320 onwards of the last sequence
+    y = u.values(b.attend())
+    assert np.isnan(y[160 + 20:, 2:]).all() and not np.isnan(y[:, :2]).any() and not np.isnan(y[:160]).any()
+
+
+def test_prompt_queries_at_the_ends_of_their_types():
+    for dtype, size, softmax_scale in (("bf16", 1e30, 1e-30), ("bf16", 1e-30, 1e30), ("fp16", 3e4, 1e-5)):
+        b = Batch([90], [40], 4, 2, 64, 16, "e4m3", dtype, seed=6, rot=0)
+        b.fill_past()
+        b.append()
+        q = torch.randn(b.q.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).clamp(-2, 2)
+        check_attention(b, q=(q * size).to(b.q.dtype), softmax_scale=softmax_scale)
+
+
+def test_prompts_among_empty_and_single_token_sequences():
+    """More long sequences than a batch without empty ones could hold: some take the step kernel."""
+    new = [0] * 60 + [40, 0, 200, 1, 1, 0, 180, 33] + [0] * 60
+    past = [7] * len(new)
+    past[62] = -30                                    # begins before position 0
+    b = Batch(new, past, 16, 2, 128, 32, "e4m3", "bf16", seed=8)
+    b.fill_past()
+    b.append()
+    check_attention(b)
+
+
+def test_prompts_repeat_exactly_and_follow_their_lengths_in_a_graph():
+    import gated_deltanet_linear_pre_gb300 as gdn
+    b = Batch([150, 1, 90], [700, 300, 10], 8, 2, 128, 64, "int8", "bf16", seed=7)
+    b.fill_past()
+    b.append()
+    size = gdn.gdn_kv_attn_workspace_bytes(b.cache, 3, b.T, b.hq, b.table.shape[1])
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    y = torch.empty(b.q.shape, dtype=b.q.dtype, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    call = lambda: gdn.gdn_kv_attn(b.cache, b.cu, b.T, b.past, b.table, b.q, 0.1, y, ws)
+    call()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        call()
+    for cuts, past in (([150, 1, 90], [700, 300, 10]), ([1, 239, 1], [849, 62, 99]), ([80, 81, 80], [0, 0, 20]), ([0, 0, 241], [9, 9, -141])):
+        b.new, b.past_h, b.cu_h = cuts, past, np.concatenate([[0], np.cumsum(cuts)])
+        b.cu.copy_(torch.tensor(b.cu_h))
+        b.past.copy_(torch.tensor(past))
+        graph.replay()
+        gdn.gdn_kv_attn_check(ws)
+        replayed = y.clone()
+        assert torch.equal(b.attend(softmax_scale=0.1), replayed)
+        check_attention(b, softmax_scale=0.1)
+
+
 def test_attention_ignores_what_no_query_sees():
     """Scales and codes of unused pages and of rows past the end are whatever they were."""
     b = Batch([1, 2], [37, 130], 4, 1, 128, 64, "e4m3", "bf16", seed=8)
