@@ -19,13 +19,20 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // bytes from the first element of a strided [T][row] array of 16-bit values to its last
 size_t span16(int32_t T, int64_t stride, size_t row) { return T > 0 ? ((size_t)(T - 1) * (size_t)stride + row) * 2 : 0; }
 
+bool known_dim(const gdn_kv_cache* c) { return c->head_dim == 64 || c->head_dim == 128; }
+
+bool known_page(const gdn_kv_cache* c)
+{
+    return c->page_tokens == 16 || c->page_tokens == 32 || c->page_tokens == 64 || c->page_tokens == 128;
+}
+
 gdn_status check_cache(const gdn_kv_cache* c)
 {
     if (!c) return fail(GDN_ERR_INVALID_ARG, "cache is NULL");
     if (c->heads < 1 || c->n_pages < 1) return fail(GDN_ERR_INVALID_ARG, "need heads >= 1 and n_pages >= 1 (heads=%d n_pages=%d)", c->heads, c->n_pages);
     if (c->heads > 1024) return fail(GDN_ERR_UNSUPPORTED, "heads=%d above 1024", c->heads);
-    if (c->head_dim != 64 && c->head_dim != 128) return fail(GDN_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", c->head_dim);
-    if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
+    if (!known_dim(c)) return fail(GDN_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", c->head_dim);
+    if (!known_page(c))
         return fail(GDN_ERR_UNSUPPORTED, "page_tokens must be 16, 32, 64 or 128 (got %d)", c->page_tokens);
     if (c->format != GDN_KV_INT8 && c->format != GDN_KV_E4M3) return fail(GDN_ERR_INVALID_ARG, "unknown cache format %d", c->format);
     const size_t codes = (size_t)c->n_pages * c->heads * c->page_tokens * c->head_dim, scales = (size_t)c->n_pages * c->heads * 4;
@@ -111,7 +118,9 @@ gdn_status gdn_kv_append(const gdn_kv_cache* cache, int32_t dtype, int32_t n_seq
 
 size_t gdn_kv_attn_workspace_bytes(const gdn_kv_cache* cache, int32_t n_seq, int32_t T, int32_t hq, int32_t max_pages)
 {
-    if (!cache || cache->heads < 1 || hq < cache->heads || n_seq < 0 || T < 0 || max_pages < 0) return 0;
+    // shapes that gdn_kv_attn refuses have no layout
+    if (!cache || cache->heads < 1 || !known_dim(cache) || !known_page(cache) || n_seq < 0 || T < 0) return 0;
+    if (hq < cache->heads || hq % cache->heads || hq / cache->heads > kMaxGroup || max_pages < 0) return 0;
     gdn::KvBatch b{};
     fill(b, cache, GDN_FP16, n_seq, T, nullptr, nullptr, nullptr, 0, max_pages, hq, nullptr, 0);
     return gdn::kv_attn_workspace_bytes(b);

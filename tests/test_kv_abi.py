@@ -105,3 +105,18 @@ def test_binding_refuses_cpu_tensors():
         N.kv_cache(k, k, torch.zeros(2, 1), torch.zeros(2, 1))
     with pytest.raises(TypeError):
         N.gdn_draft_verify(torch.zeros(1, 2, 4), torch.zeros(1, 1, 4), None, None, None, None, None)
+
+
+def test_workspace_of_refused_shapes_is_nothing(L):
+    def need(hq=4, width=8, n=2, T=300, **over):
+        return L.gdn_kv_attn_workspace_bytes(ctypes.byref(cache(**over)), n, T, hq, width)
+
+    assert need() > 0
+    assert need(hq=2 * 64) > 0
+    for dim in (0, 1, 96, 256, -128):
+        assert need(head_dim=dim) == 0, dim
+    for page in (0, 8, 48, 256, -16):
+        assert need(page_tokens=page) == 0, page
+    for hq in (-4, 0, 1, 3, 2 * 65, 2 * 129, 2 * 4000):
+        assert need(hq=hq) == 0, hq
+    assert need(heads=0) == need(heads=-2) == need(width=-1) == need(n=-1) == need(T=-1) == 0
