@@ -135,13 +135,13 @@ __device__ __forceinline__ void decode8(const uint2& w, float (&x)[8])
     }
 }
 
-// One unit.  THREADS = 32: a warp, which reads its few rows twice, the second time from the first-level
-// cache.  Else a block, which holds a page's rows in registers (HELD a thread) between the maximum and
-// the codes.
+// One unit, by a warp or a block (THREADS).  The page's rows stay in registers (HELD a thread) between the
+// maximum and the codes, or, HELD = 0, the call's few rows are read twice, the second time from the
+// first-level cache.
 template <bool BF16, bool E4M3, int D, int THREADS, int HELD>
 __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
 {
-    constexpr bool kWarp = THREADS == 32;
+    constexpr bool kTwice = HELD == 0;
     constexpr int kRowLanes = D / 8, kRows = THREADS / kRowLanes;  // threads a row, rows a pass
     const int tid = threadIdx.x % THREADS, c = tid % kRowLanes, r0 = tid / kRowLanes;
     const int slot = unit / (2 * p.heads), rest = unit - slot * 2 * p.heads;
@@ -176,9 +176,9 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
         return amax;
     };
 
-    float held[HELD][8];
+    float held[kTwice ? 1 : HELD][8];
     uint32_t amax = 0;
-    if constexpr (kWarp) {
+    if constexpr (kTwice) {
         for (int row = lo + r0; row - r0 < hi; row += kRows) {
             float x[8];
             value(row, fetch(row), x);
@@ -195,7 +195,7 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
         }
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
-    if constexpr (!kWarp) {
+    if constexpr (THREADS > 32) {
         __shared__ uint32_t part[THREADS / 32];
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
         __syncthreads();
@@ -218,7 +218,7 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
         if (row >= lo && row < hi)
             *reinterpret_cast<uint2*>(codes + (size_t)row * D) = scale > 0.0f ? encode8<E4M3>(x, inv) : make_uint2(0u, 0u);
     };
-    if constexpr (kWarp) {
+    if constexpr (kTwice) {
         for (int row = lo + r0; row - r0 < hi; row += kRows) {
             float x[8];
             value(row, fetch(row), x);
@@ -280,11 +280,14 @@ __global__ void __launch_bounds__(THREADS, UNIT == 32 ? 1 : 1024 / THREADS) kv_a
     rotate_queries<BF16, D>(p, item, (int64_t)p.T * chunks, chunks);
 }
 
+int64_t unit_count(const AppendParams& p) { return ((int64_t)p.T / p.page + 2 * (int64_t)p.n_seq) * p.heads * 2; }
+
+constexpr int64_t kFewUnits = 8 * 152;  // a wave of blocks
+
 template <bool BF16, bool E4M3, int D, int THREADS, int UNIT, int HELD>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream)
 {
-    const int64_t units = ((int64_t)p.T / p.page + 2 * (int64_t)p.n_seq) * p.heads * 2;
-    const int64_t unit_blocks = (units + THREADS / UNIT - 1) / (THREADS / UNIT);
+    const int64_t units = unit_count(p), unit_blocks = (units + THREADS / UNIT - 1) / (THREADS / UNIT);
     const int64_t items = (int64_t)p.T * ((p.hq + kQueryHeads - 1) / kQueryHeads), per_block = THREADS / (D / 8);
     const int64_t q_blocks = (items + per_block - 1) / per_block;
     if (units > 0x7fffffff || unit_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -295,12 +298,20 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream)
 template <bool BF16, bool E4M3, int D>
 cudaError_t launch_page(const AppendParams& p, cudaStream_t stream)
 {
-    // A warp per unit where sequences bring a few tokens each (a block would leave most of its threads
-    // without a row), a block per unit where they fill pages: 256 threads with up to 4 rows each, 512
-    // for pages of 16 Ki values.
-    if ((int64_t)p.T <= 8 * (int64_t)p.n_seq) return launch<BF16, E4M3, D, 256, 32, 1>(p, stream);
+    // Up to kFewUnits the units fit the SMs at once as blocks of 256, and a call takes as long as one unit;
+    // above, as long as all units together.
+    //   Sequences that bring a few tokens: a warp per unit, which looks at those rows only.  64 sequences of 12
+    //   tokens (pages of 64, 8 heads of 128) took 9.5 us by warps and 11.2 by blocks, of 16 11.8 and 12.0, of 32
+    //   17.2 and 18.3; 8 sequences of 1 token 3.2 and 4.2, of 4 the same, of 8 5.5 and 4.0.
+    //   Small pages, many units: again a warp, its lanes holding the whole page.  64 sequences of 1024 tokens in
+    //   pages of 16 took 349 us by warps, 407 by blocks (366 with rows read twice), 8 of 16 tokens 5.7 and 3.6.
+    //   Else a block, 256 threads with up to 4 rows each, 512 for pages of 16 Ki values.
+    const bool few = unit_count(p) <= kFewUnits;
+    if ((int64_t)p.T <= (few ? 4 : 16) * (int64_t)p.n_seq) return launch<BF16, E4M3, D, 256, 32, 0>(p, stream);
     const int lanes = p.page * (D / 8);
-    if (lanes <= 256) return launch<BF16, E4M3, D, 256, 256, 1>(p, stream);
+    if (lanes <= 256 && few) return launch<BF16, E4M3, D, 256, 256, 1>(p, stream);
+    if (lanes == 128) return launch<BF16, E4M3, D, 256, 32, 4>(p, stream);
+    if (lanes == 256) return launch<BF16, E4M3, D, 256, 32, 8>(p, stream);
     if (lanes == 512) return launch<BF16, E4M3, D, 256, 256, 2>(p, stream);
     if (lanes == 1024) return launch<BF16, E4M3, D, 256, 256, 4>(p, stream);
     return launch<BF16, E4M3, D, 512, 512, 4>(p, stream);

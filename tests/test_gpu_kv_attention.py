@@ -169,6 +169,34 @@ def test_append_from_empty(new, hq, heads, dim, page, fmt, dtype, rot, interleav
             assert np.all(np.abs(got - x) <= step * (1 + 2.0 ** -6) + np.abs(x).max(initial=0) * 2.0 ** -21)
 
 
+MANY = [400, 1, 333, 0, 390, 17, 256]  # more pages and heads than a wave of blocks, as one call
+
+
+@pytest.mark.parametrize("dim,page", [(128, 16), (64, 16), (64, 32), (128, 32), (64, 128)])
+@pytest.mark.parametrize("fmt,dtype,rot,interleaved", [("int8", "bf16", None, False), ("e4m3", "fp16", 32, True)])
+def test_append_many_pages(dim, page, fmt, dtype, rot, interleaved):
+    """A large call's pages against the definitions; the same tokens stored a sequence at a time, behind
+    pages that are partly filled, give the same codes and scales bit for bit."""
+    test_append_from_empty(MANY, 16, 16, dim, page, fmt, dtype, rot, interleaved)
+    import gated_deltanet_linear_pre_gb300 as gdn
+    one, each = (Batch(MANY, [5, 0, 1000, 3, 16, 31, 127], 16, 16, dim, page, fmt, dtype, seed=9, rot=rot, interleaved=interleaved)
+                 for _ in range(2))
+    for b in (one, each):
+        b.fill_past()
+    q_out = one.append()
+    q_each = torch.full_like(q_out, float("nan"))
+    for s, n in enumerate(MANY):
+        rows = slice(int(each.cu_h[s]), int(each.cu_h[s + 1]))
+        cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        gdn.gdn_kv_append(each.cache, cu, n, each.past[s:s + 1], each.table[s:s + 1], each.q[rows], each.kn[rows], each.vn[rows],
+                          each.cos, each.sin, interleaved, q_each[rows])
+    assert torch.equal(q_out, q_each)
+    for a, b in ((one.k, each.k), (one.v, each.v)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    for a, b in ((one.ks, each.ks), (one.vs, each.vs)):
+        assert torch.equal(a.nan_to_num(3), b.nan_to_num(3))
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("dim,page", [(128, 16), (64, 64)])
 def test_append_in_pieces_stays_below_one_step(fmt, dim, page):
