@@ -25,6 +25,8 @@ constexpr int kStepMaxRows = 32;       // query rows of a step unit, at most
 constexpr int kStepMaxWorkers = 640;
 constexpr int kStepUnitCost = 16;      // a step unit's beginning and end, in tiles
 constexpr int kPromptUnitCost = 2;     // a prompt unit's
+constexpr int kPromptCutCost = 6;      // what cutting the prompt units costs a worker, beside a sixteenth of
+                                       // its share (whole_units)
 constexpr int kKeys = 128;             // positions of a prompt tile
 constexpr int kUnitRows = 256;         // query rows of a prompt unit: two halves of 128
 constexpr int kPromptMaxWorkers = 160;
@@ -65,6 +67,7 @@ struct Cut {
 struct AttnHeader {
     uint32_t error;
     int step_workers, prompt_workers;
+    int prompt_whole, prompt_next;  // prompt units are not cut but handed out one by one; the next one
     int64_t step_total, prompt_total;
 };
 

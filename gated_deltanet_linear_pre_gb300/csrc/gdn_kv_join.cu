@@ -20,7 +20,7 @@ __device__ __forceinline__ void join_prompt(const AttnParams& p, const AttnSpace
 {
     const int group = p.hq / p.heads, tokens = half_tokens(group);
     const int workers = a.head->prompt_workers;
-    if (w >= workers) return;
+    if (w >= workers || a.head->prompt_whole) return;
     const Cut cut = a.prompt_cut[w];
     const int64_t total = a.head->prompt_total, begin = cut.lo - cut.from, prev = a.prompt_cut[w - 1].lo;
     if (cut.j0 == 0 || prev > begin + kPromptUnitCost || !a.ok[cut.s]) return;

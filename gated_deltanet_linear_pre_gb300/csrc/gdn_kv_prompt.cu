@@ -89,6 +89,34 @@ __device__ __forceinline__ int64_t head_cost(const SeqView& v, int span)
     return unit_prefix(v.first, span, last) + unit_tiles(v.first, v.n, span, last) + kPromptUnitCost;
 }
 
+// Whether the units are not cut but handed out one by one, sequence after sequence, each with its longest
+// units first.  A unit then begins, at the latest, when all before it have taken every worker's time, so the
+// last one ends by the largest of (cost of the units before it) / workers + its own.  Within a sequence that
+// is a concave function of the unit, with its largest value where a unit's cost is what the following
+// unit's is less, times workers / heads.  Against it stands an equal share of a cut batch, with one more unit
+// begun and ended, its parts and their join.  Cut and whole took (48 query heads over 16, e4m3, from empty)
+// 44 and 35 us for 1024 tokens, 83 and 72 for 2048, 717 and 675 for 8192 (a share of 358 tiles); 1186 and 1113
+// for 8 prompts of 1 to 4096; 788 and 861 for 4001 tokens behind 16500 (16 over 4), whose 500 equal units
+// make 4 rounds of 152 CTAs out of 3.3, and which the bound leaves cut.
+template <int THREADS>
+__device__ __forceinline__ bool whole_units(const AttnParams& p, const AttnSpace& a, int span, int64_t total, int workers, ScanSmem<THREADS>& scan)
+{
+    if (p.n_seq > THREADS) return false;  // (scan.prefix holds the costs before the sequences of one chunk)
+    const int64_t share = (total + workers - 1) / workers, most = share + share / 16 + kPromptCutCost;
+    bool late = false;
+    if ((int)threadIdx.x < p.n_seq) {
+        const SeqView v = seq_view(p, threadIdx.x);
+        if (candidate(p, a, v)) {
+            const int units = (v.n + span - 1) / span;
+            const int64_t at = (int64_t)span * workers / p.heads - kPromptUnitCost * kKeys - v.first;
+            const int i = (int)max(min(at / span - 1, (int64_t)units - 1), (int64_t)0);
+            const int64_t rest = p.heads * (head_cost(v, span) - unit_prefix(v.first, span, i));  // of unit i and the longer ones
+            late = (scan.prefix[threadIdx.x] + rest) / workers + unit_tiles(v.first, v.n, span, i) + kPromptUnitCost > most;
+        }
+    }
+    return !__syncthreads_or(late);
+}
+
 // The plan: the total cost of all candidates, and where each worker's range begins in it.  One block.
 template <int THREADS>
 __device__ __forceinline__ void plan(const AttnParams& p, const AttnSpace& a, int grid, ScanSmem<THREADS>& scan)
@@ -99,10 +127,24 @@ __device__ __forceinline__ void plan(const AttnParams& p, const AttnSpace& a, in
         return candidate(p, a, v) ? p.heads * head_cost(v, span) : 0;
     };
     const int64_t total = scan_total<THREADS>(p.n_seq, weight, scan);
-    const int workers = (int)min((int64_t)grid, total);
+    int workers = (int)min((int64_t)grid, total);
+    const bool whole = total > 0 && whole_units(p, a, span, total, workers, scan);
+    if (whole) {  // units in the place of costs
+        int64_t mine = 0, jobs;
+        if (tid < p.n_seq) {
+            const SeqView v = seq_view(p, tid);
+            if (candidate(p, a, v)) mine = (int64_t)((v.n + span - 1) / span) * p.heads;
+        }
+        const int64_t before = block_scan<THREADS>(mine, scan, jobs);
+        scan.prefix[tid] = before;
+        if (tid == 0) scan.chunk[0] = jobs;
+        workers = (int)min((int64_t)grid, jobs);
+    }
     if (tid == 0) {
         a.head->prompt_total = total;
         a.head->prompt_workers = workers;
+        a.head->prompt_whole = whole;
+        a.head->prompt_next = workers;
     }
     int64_t base = 0, tiles = 0;
     __shared__ int image[THREADS];  // image tiles before each of the chunk's sequences
@@ -128,7 +170,7 @@ __device__ __forceinline__ void plan(const AttnParams& p, const AttnSpace& a, in
         __syncthreads();
         const int64_t end = base + scan.chunk[c];
         for (int w = tid; w < workers; w += THREADS) {  // the workers whose range begins in this chunk
-            const int64_t lo = cut_start(total, workers, w);
+            const int64_t lo = whole ? w : cut_start(total, workers, w);
             if (lo < base || lo >= end) continue;
             int s = 0;
             for (int step = THREADS / 2; step > 0; step >>= 1)
@@ -136,8 +178,14 @@ __device__ __forceinline__ void plan(const AttnParams& p, const AttnSpace& a, in
             int64_t rest = lo - (base + scan.prefix[s]);
             s += c * THREADS;
             const SeqView v = seq_view(p, s);
+            const int units = (v.n + span - 1) / span;
+            if (whole) {
+                const int i = units - 1 - (int)(rest / p.heads);
+                a.prompt_cut[w] = Cut{s, (int)(rest % p.heads), i, 0, unit_tiles(v.first, v.n, span, i), 0, lo - rest, v.t0, v.n, v.first, image[s]};
+                continue;
+            }
             const int64_t per_head = head_cost(v, span);
-            const int head = (int)(rest / per_head), units = (v.n + span - 1) / span;
+            const int head = (int)(rest / per_head);
             rest -= head * per_head;
             // the unit: about half a tile's rounding a unit makes the prefix a quadratic, whose root is near
             const float qa = span / (2.0f * kKeys), qb = (v.first + 0.5f * span) / kKeys + 0.5f + kPromptUnitCost;
@@ -158,13 +206,14 @@ __device__ __forceinline__ void plan(const AttnParams& p, const AttnSpace& a, in
     }
 }
 
-// A worker's units in order.
+// A worker's units in order: those of its range, or, where units are handed out, one by one.
 struct Walk {
     int s, head, i, units;  // sequence, kv head, unit; units of a (sequence, head)
     int t0, n, first;       // the sequence's tokens, its first one's position
-    int image;              // image tile of its first positions (-1: not a long sequence after all)
+    int image, ok;          // image tile of its first positions; 0: not a long sequence after all
     int from;               // cost of the unit before the range
     int64_t left;           // cost of the range from here on
+    int64_t jobs;           // (handed out) units of the sequences before s
 
     // to the next unit, having used `cost` of this one; false at the range's end
     __device__ __forceinline__ bool next(const AttnParams& p, const AttnSpace& a, int span, int cost)
@@ -184,9 +233,53 @@ struct Walk {
             n = v.n;
             first = v.first;
             units = (n + span - 1) / span;
-            image = a.ok[s] ? a.image_base[s] : -1;
+            ok = a.ok[s];
+            image = ok ? a.image_base[s] : 0;
             return true;
         }
+    }
+    // to unit `job` of those handed out, at or behind the one in hand; the whole warp calls it
+    __device__ __forceinline__ bool take(const AttnParams& p, const AttnSpace& a, int span, int64_t job)
+    {
+        const int lane = threadIdx.x & 31;
+        while (job >= jobs + (int64_t)units * p.heads) {  // 32 sequences at a time
+            jobs += (int64_t)units * p.heads;
+            const int at = s + 1 + lane;
+            int64_t mine = 0;
+            if (at < p.n_seq) {
+                const SeqView v = seq_view(p, at);
+                if (candidate(p, a, v)) mine = (int64_t)((v.n + span - 1) / span) * p.heads;
+            }
+            int64_t upto = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += o;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, job < jobs + upto);
+            if (past == 0) {
+                if (s + 33 >= p.n_seq) return false;
+                jobs += __shfl_sync(0xffffffffu, upto, 31);
+                s += 32;
+                units = 0;
+                continue;
+            }
+            const int found = __ffs(past) - 1;
+            jobs += __shfl_sync(0xffffffffu, upto - mine, found);
+            s += 1 + found;
+            const SeqView v = seq_view(p, s);
+            t0 = v.t0;
+            n = v.n;
+            first = v.first;
+            units = (n + span - 1) / span;
+            ok = a.ok[s];
+            image = ok ? a.image_base[s] : 0;
+        }
+        const int64_t in = job - jobs;
+        i = units - 1 - (int)(in / p.heads);
+        head = (int)(in % p.heads);
+        from = 0;
+        return true;
     }
 };
 
@@ -354,8 +447,7 @@ struct PromptSmem {
 };
 static_assert(sizeof(PromptSmem<128>) <= 232448 && sizeof(PromptSmem<64>) <= 232448, "shared memory");
 
-// barriers: of the two warps that hold the two halves of the same rows' columns (64 threads, ids 1-8), of a
-// half's 256 threads (ids 9, 10)
+// barriers of the two warps that hold the two halves of the same rows' columns (64 threads, ids 1-8)
 __device__ __forceinline__ bool pair_any(int id, bool say)  // whether any of them says so
 {
     uint32_t any;
@@ -370,7 +462,6 @@ __device__ __forceinline__ bool pair_any(int id, bool say)  // whether any of th
     return any != 0;
 }
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void half_sync(int h) { asm volatile("barrier.cta.sync %0, 256;" ::"r"(9 + h) : "memory"); }
 
 // Bounded wait (about two seconds of SM clock; abandoned once another warp of the CTA has given up).  The
 // warp agrees on the outcome and stays converged.
@@ -420,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int group = p.hq / p.heads, tokens = half_tokens(group);
     if (warp == kMmaWarp) umma::tmem_alloc(&sm.tmem_base, kTmemCols);
+    if (warp == kQueryWarp && lane == 0) umma::prefetch_map(&q_map);
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             umma::mbar_init(&sm.kv_full[i], 1);
@@ -447,10 +539,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
     const volatile int* abort_flag = &sm.abort_flag;
     pdl_wait();
     pdl_launch_dependents();
-    if ((int)blockIdx.x >= a.head->prompt_workers) {  // nothing to do
-        if (warp == kMmaWarp) umma::tmem_dealloc(tmem, kTmemCols);
-        return;
-    }
 
     // A wait that expires is recorded; its warp goes on or ends as its role allows.
     auto await = [&](uint64_t* mbar, uint32_t parity) {
@@ -477,12 +565,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
         if (warp >= kQueryWarp) {
             // ---- units and queries ----
             const int span = 2 * tokens, workers = a.head->prompt_workers;
-            const Cut c = a.prompt_cut[blockIdx.x];
-            const int64_t end = (int)blockIdx.x + 1 < workers ? a.prompt_cut[blockIdx.x + 1].lo : a.head->prompt_total;
+            const bool handed = a.head->prompt_whole;
+            const int64_t total = a.head->prompt_total;
+            const Cut c = a.prompt_cut[blockIdx.x];  // (all these loads at once: what lies past the workers is not used)
+            const int64_t next_lo = a.prompt_cut[min(blockIdx.x + 1, kPromptMaxWorkers - 1)].lo;
             uint32_t x = 0, q_use[2] = {0, 0};  // units, and queries of each half, brought in
-            bool more = true;
+            bool more = (int)blockIdx.x < workers;
             Walk w;
-            {
+            if (more) {
                 w.s = c.s;
                 w.head = c.head;
                 w.i = c.unit;
@@ -490,17 +580,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 w.n = c.n;
                 w.first = c.first;
                 w.units = (c.n + span - 1) / span;
-                w.image = a.ok[c.s] ? c.image : -1;
+                w.ok = a.ok[c.s];
+                w.image = min(c.image, a.image_tiles - 1);
                 w.from = c.from;
-                w.left = end - c.lo;
+                w.left = handed ? (int64_t)1 << 62 : ((int)blockIdx.x + 1 < workers ? next_lo : total) - c.lo;
+                w.jobs = c.lo;  // (handed out)
             }
             while (more) {
                 const int tiles = unit_tiles(w.first, w.n, span, w.i);
                 const int to = (int)min((int64_t)tiles + kPromptUnitCost, w.from + w.left);
                 const int j0 = max(w.from - kPromptUnitCost, 0), count = to - kPromptUnitCost - j0;
-                if (count > 0 && w.image >= 0) {  // (a range may end within a unit's constant)
+                const float2 norm = a.norm[(size_t)w.image * p.heads + w.head];
+                if (count > 0 && w.ok) {  // (a range may end within a unit's constant)
                     if (x >= kUnits) GDN_KV_WAIT(&sm.unit_empty[x % kUnits], (x / kUnits - 1) & 1);
-                    const float2 norm = a.norm[(size_t)w.image * p.heads + w.head];
                     const int token = w.i * span;
                     if (lane == 0) {
                         Unit& u = sm.unit[x % kUnits];
@@ -540,7 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                     }
                     ++x;
                 }
-                more = w.next(p, a, span, to - w.from);
+                if (handed) {
+                    // the next one once the last scores of this are under way: sooner would leave it to a busy CTA
+                    if (q_use[0] > 0) GDN_KV_WAIT(&sm.q_empty[0], (q_use[0] - 1) & 1);
+                    int job = lane == 0 ? atomicAdd(&a.head->prompt_next, 1) : 0;
+                    more = w.take(p, a, span, __shfl_sync(0xffffffffu, job, 0));
+                } else {
+                    more = w.next(p, a, span, to - w.from);
+                }
             }
             if (x >= kUnits) GDN_KV_WAIT(&sm.unit_empty[x % kUnits], (x / kUnits - 1) & 1);
             if (lane == 0) {

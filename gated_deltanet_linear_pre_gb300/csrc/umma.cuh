@@ -274,6 +274,8 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
                  : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const void* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
+
 // one box of a 3-D tensor map -> shared memory (dst on a 1024-byte boundary for a 128-byte swizzle); x times
 // the element size a multiple of 16 bytes; places outside the tensor are zeros
 __device__ __forceinline__ void tensor_g2s_3d(void* dst, const void* map, int x, int y, int z, uint64_t* mbar)

@@ -416,6 +416,38 @@ def test_prompts_among_empty_and_single_token_sequences():
     check_attention(b)
 
 
+@pytest.mark.parametrize("new,past,hq,heads,dim,page", [
+    # more units than CTAs: handed out one by one
+    ([700, 333], [0, 0], 64, 16, 64, 64),
+    ([333, 40, 1, 300], [30, 0, 500, 100], 128, 32, 64, 16),
+    # the next prompt is many sequences away, single tokens and none between
+    ([70] + [1] * 33 + [0, 1, 90] + [1] * 70 + [45], [100] + [9] * 107, 8, 2, 128, 32),
+    # more sequences than a block has threads
+    ([1] * 290 + [60] * 4, [3] * 294, 4, 1, 64, 16),
+    # a few long units: cut
+    ([40, 1, 90], [9000, 5, 4000], 8, 2, 128, 64),
+    ([140], [3000], 16, 1, 64, 128),
+])
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("e4m3", "fp16")])
+def test_prompt_units_handed_out_or_cut(new, past, hq, heads, dim, page, fmt, dtype):
+    b = Batch(new, past, hq, heads, dim, page, fmt, dtype, seed=len(new))
+    b.fill_past()
+    b.append()
+    check_attention(b)
+    again = b.attend().clone()
+    assert torch.equal(b.attend(), again)             # whichever CTA takes a unit
+
+
+def test_prompt_units_handed_out_past_one_without_images():
+    """The middle prompt has a hole in its table and takes the other way; its place is passed over."""
+    b = Batch([200, 300, 250], [0, 60, 0], 32, 8, 128, 32, "e4m3", "bf16", seed=2)
+    b.fill_past()
+    b.append()
+    b.table_h[1, 2] = -1
+    b.table.copy_(torch.tensor(b.table_h))
+    check_attention(b)
+
+
 def test_prompts_repeat_exactly_and_follow_their_lengths_in_a_graph():
     import gated_deltanet_linear_pre_gb300 as gdn
     b = Batch([150, 1, 90], [700, 300, 10], 8, 2, 128, 64, "int8", "bf16", seed=7)
