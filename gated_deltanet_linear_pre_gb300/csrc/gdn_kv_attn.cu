@@ -23,7 +23,8 @@ size_t layout(const KvBatch& b, void* ws, AttnSpace& a)
     a.step_stat = reinterpret_cast<float2*>(take((size_t)2 * kStepMaxWorkers * kStepMaxRows * 8));
     a.step_out = reinterpret_cast<float*>(take((size_t)2 * kStepMaxWorkers * kStepMaxRows * dim * 4));
     a.most_rows = 0x7fffffff;
-    a.whole_units = (int64_t)b.max_pages * b.page <= (int64_t)kWholePositions * (128 / b.dim);
+    const int64_t whole = (int64_t)kWholePositions * (128 / b.dim) * ((int64_t)b.heads * b.n_seq <= kWholeUnits ? 2 : 1);
+    a.whole_units = (int64_t)b.max_pages * b.page <= whole;
     // As many long sequences as the batch's tokens allow where every sequence has one at least, each as long as
     // the page table allows.  In a batch with many empty sequences there may be more: those without room for
     // images take the step kernel.  (Counting on empty ones would launch the prompt way's kernels, some 8 us, in

@@ -22,7 +22,7 @@ namespace gdn {
 constexpr int kSub = 16;               // positions of a step tile's part (a page holds whole ones)
 template <int D> constexpr int kStepTile = D == 128 ? kSub : 2 * kSub;  // positions of a step tile: 4 KB of codes
 constexpr int kStepMaxRows = 32;       // query rows of a step unit, at most
-constexpr int kStepMaxWorkers = 640;
+constexpr int kStepMaxWorkers = 480;
 constexpr int kStepUnitCost = 16;      // a step unit's beginning and end, in tiles
 constexpr int kPromptUnitCost = 2;     // a prompt unit's
 constexpr int kPromptCutCost = 6;      // what cutting the prompt units costs a worker, beside a sixteenth of
@@ -34,8 +34,12 @@ constexpr int kPromptMaxWorkers = 160;
 // 162 us by steps at 128 rows and 234 at 192, 180 and 185 us by images.
 constexpr int kLongRows = 128;
 // Where the page table holds at most this many positions (times 128 / head_dim) step units stay whole, and no
-// kernel joins them: a unit's last tiles take less than a second launch.
+// kernel joins them: a unit's last tiles take less than a second launch (64 sequences of 490 positions, 4 heads,
+// 15.1 us whole and 18.1 cut; 16 heads 38.3 and 38.4, of lengths up to 500 30.1 and 27.6).  Twice as many where
+// the (sequence, kv head) pairs are few (kWholeUnits): 16 sequences of 900 positions, 4 heads, 12.8 us whole and
+// 16.7 cut, 38 of 1000 15.5 and 18.5; but 64 of lengths up to 1000 20.4 and 18.6.
 constexpr int kWholePositions = 512;
+constexpr int kWholeUnits = 152;
 constexpr size_t kImageCap = (size_t)2 << 30;  // bytes of images; sequences past it take the step kernel
 
 constexpr uint32_t kAttnTimeout = 1u;  // failure record: a bounded wait expired

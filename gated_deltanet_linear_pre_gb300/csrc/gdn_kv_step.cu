@@ -25,7 +25,12 @@ namespace {
 
 constexpr int kStepThreads = 128;
 constexpr int kWarps = kStepThreads / 32;
-constexpr int kStages = 3;             // tiles of a warp in its ring
+constexpr int kStages = 2;             // tiles of a warp in its ring
+// CTAs an SM.  Three of two tiles a warp keep some 48 KB in flight beside the tiles in work, which is enough:
+// with four of three tiles requests only waited for one another (64 sequences of up to 8192 positions 71.2 ->
+// 68.1 us, 3 of 131000 50.0 -> 45.5, 37 sequences of drafts 88.8 -> 81.6; two of four: 66.4, 69.3 and 89.8), and
+// three leave the registers for the queries.
+template <int NT> constexpr int kCtas = NT == 4 ? 2 : 3;
 constexpr float kWeightUnit = 128.0f;  // 2^7
 constexpr float kLazy = 8.0f;
 
@@ -145,7 +150,7 @@ __device__ __forceinline__ void step_units(const KvBatch& p, const AttnSpace& a,
 }
 
 template <int D, bool BF16, bool E4M3, int NT>
-__global__ void __launch_bounds__(kStepThreads, NT == 4 ? 2 : 4) kv_step_kernel(AttnParams p, AttnSpace a)
+__global__ void __launch_bounds__(kStepThreads, kCtas<NT>) kv_step_kernel(AttnParams p, AttnSpace a)
 {
     constexpr int R = 8 * NT, KS = D / 16, MT = D / 16;
     using Smem = StepSmem<D, NT>;
@@ -244,6 +249,14 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 2 : 4) kv_step_kernel(
                 }
             }
             __syncthreads();
+            // up to 16 rows are held in registers (shared memory reads bound the kernel with the conversions)
+            constexpr bool kHeld = NT <= 2;
+            uint2 qb[kHeld ? NT : 1][kHeld ? KS : 1];
+            if constexpr (kHeld)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) qb[nt][ks] = sm.q[nt][ks][lane];
             float coef[NT][2];
             int limit[NT][2];
             const int first_limit = v.first + row0 / group;  // the smallest of the unit's rows
@@ -278,7 +291,9 @@ __global__ void __launch_bounds__(kStepThreads, NT == 4 ? 2 : 4) kv_step_kernel(
                         const uint32_t ka[4] = {codes2<E4M3, false>(r0[c]), codes2<E4M3, false>(r1[c]), codes2<E4M3, true>(r0[c]), codes2<E4M3, true>(r1[c])};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const uint2 b = sm.q[nt][4 * h + c][lane];
+                            uint2 b;
+                            if constexpr (kHeld) b = qb[nt][4 * h + c];
+                            else b = sm.q[nt][4 * h + c][lane];
                             mma16816(x[nt], ka, b.x, b.y);
                         }
                     }
@@ -457,7 +472,11 @@ cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_
     static_assert(sizeof(StepSmem<D, NT>) <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int grid = min(sms * (NT == 4 ? 2 : 4), kStepMaxWorkers);
+    // no more workers than the call can have ranges: those without one would only look for it (one sequence of
+    // 301 positions 10.8 -> 7.5 us)
+    const double units = ((double)p.T * (p.hq / p.heads) / (8 * NT) + p.n_seq) * p.heads, tiles = (double)p.max_pages * p.page / kStepTile<D> + 1;
+    const double most = a.whole_units ? units : units * (tiles + kStepUnitCost) / (kStepUnitCost + 2 * kWarps) + 1;
+    const int grid = (int)min((double)min(sms * kCtas<NT>, kStepMaxWorkers), ceil(most));
     return launch_k(kernel, dim3(grid), dim3(kStepThreads), smem, stream, true, p, a);
 }
 
