@@ -31,8 +31,8 @@ constexpr int kKeys = 128;             // positions of a prompt tile
 constexpr int kUnitRows = 256;         // query rows of a prompt unit: two halves of 128
 constexpr int kPromptMaxWorkers = 160;
 // Above this many query rows the prompt way is faster: 16 sequences of 8K positions (4 heads, e4m3) took
-// 162 us by steps at 128 rows and 234 at 192, 180 and 185 us by images.
-constexpr int kLongRows = 128;
+// 127 us by steps at 96 rows and 161 at 128, 137 and 135 us by images; 4 of 2000 26.7 and 29.5, 26.9 and 27.2.
+constexpr int kLongRows = 96;
 // Where the page table holds at most this many positions (times 128 / head_dim) step units stay whole, and no
 // kernel joins them: a unit's last tiles take less than a second launch (64 sequences of 490 positions, 4 heads,
 // 15.1 us whole and 18.1 cut; 16 heads 38.3 and 38.4, of lengths up to 500 30.1 and 27.6).  Twice as many where
