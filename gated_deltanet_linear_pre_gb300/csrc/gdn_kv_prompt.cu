@@ -11,13 +11,13 @@
 // somewhere.  Done by every CTA for itself, a 128-position tile would cost each about as many issue slots
 // as a third of its softmax; instead one kernel unpacks each long sequence's cache once into images, in
 // the 128-byte swizzled order (without swizzle the products ran 7% slower), that a single bulk copy brings
-// in: 4 bytes moved per code byte, a few per cent of a prompt's time.  K takes the activations' type (both
+// in: 4 bytes moved per code byte, some 5% of a prompt's time (16 us of 72 with its launch at 2048 tokens).  K takes the activations' type (both
 // operands of a product have one), so queries go to shared memory as they are.  A bf16 image holds code *
 // scale, exactly.  An fp16 image (V always) holds code * (page scale / largest scale of the sequence and
 // head) * kUp, exact for pages whose scale is at least 2^-21 (e4m3) or 2^-32 (int8) of the largest; the
 // largest scale itself goes into the scores' unit and the outputs'.
 //
-// A CTA (640 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
+// A CTA (608 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
 // other's products: warps 0-7 and 8-15 the rows (two threads a row, each half of a tile's columns: a tile's
 // softmax takes less than the other half's 1024 tensor cycles only with four warps a scheduler), warp 16
 // the copies, warp 17 the products, warp 18 the units ahead and their queries, which it brings in as soon as
@@ -26,6 +26,14 @@
 // TMEM: S and O of each half,
 // 512 columns at head_dim 128; the fp16 P of 64 keys takes the first 32 of their 64 score columns.
 // Rows are (token, query head of the kv head): floor(128 / group) tokens a half.
+//
+// Bound and measured.  By the tensor cores and what feeds them together: a tile of both halves is 2048 cycles of
+// products, reads shared memory at its full 128 bytes a cycle for as long, and has 1024 cycles of exponentials a
+// half.  A 4001-token chunk behind 16500 tokens (32 query heads over 4 of 128, beside three single tokens) takes
+// 745 us, 1.6 PFLOP/s, 83% of the measured dense rate; 2048 tokens from nothing (48 over 16) 60 us, of which a
+// CTA's start takes 6 and each of its units 3 between the last tile of one and the first of the next.  Tried and
+// left out: 8 softmax warps of 208 registers (1090 us for the chunk's call, 790), a warp of products for each
+// half (830), waits that spin (829 and more).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -12,7 +12,10 @@
 // weights, the CTAs exchange their totals through distributed shared memory, and the one CTA whose part
 // holds the threshold finds its segment from the sums and reads those 512 weights again.  CTAs of 256
 // threads: six share an SM, so that one's search for the first rejected draft and its exchange run under
-// the others' loads.
+// the others' loads (512 threads: 63 us where 256 take 47).
+//
+// Measured: 256 sequences of 131072 weights, 220 MB that no cache holds, 47 us, 4.7 TB/s (the floor is 39.5 us
+// for what the call must read); one sequence 5.8 us: four dependent loads, two exchanges and the launch.
 #include <cooperative_groups.h>
 
 #include "gdn_internal.cuh"

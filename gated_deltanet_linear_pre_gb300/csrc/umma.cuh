@@ -1,9 +1,10 @@
 // umma.cuh -- thin inline-PTX wrappers for the sm_100-family 5th-generation
 // tensor core (tcgen05), tensor memory (TMEM) and shared-memory mbarriers.
 //
-// Layout conventions used by this library (all operand tiles are bf16 in
-// shared memory, no swizzle, "core matrix" = 8 rows x 16 bytes stored as 128
-// contiguous bytes):
+// Layout conventions used by this library (operand tiles are 16-bit, in
+// shared memory; the attention's are swizzled over 128 bytes (desc_sw128), the
+// others are not: "core matrix" = 8 rows x 16 bytes stored as 128 contiguous
+// bytes):
 //   K-major tile (K contiguous within a core-matrix row): core matrix (mg, kg)
 //     covers rows [8mg, 8mg+8) x K [8kg, 8kg+8); LBO = byte distance between
 //     core matrices adjacent along K, SBO = along M/N.

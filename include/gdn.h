@@ -399,7 +399,11 @@ GDN_API gdn_status gdn_kv_append(const gdn_kv_cache* cache, int32_t dtype, int32
                                  int32_t rot_dim, int32_t n_pos, int32_t interleaved,
                                  uint16_t* q_out, struct CUstream_st* stream);
 
-/* Workspace bytes gdn_kv_attn needs for this batch shape. */
+/* Workspace bytes gdn_kv_attn needs for this batch shape (0 for one that it
+ * refuses): parts of outputs, some 16 MB at head_dim 128, and where the batch
+ * can hold a sequence of more than 96 query rows per kv head, 40 MB more and
+ * unpacked copies of such sequences' caches, 4 bytes per code byte up to 2 GB
+ * (sequences that find no room are attended to without). */
 GDN_API size_t gdn_kv_attn_workspace_bytes(const gdn_kv_cache* cache, int32_t n_seq,
                                            int32_t total_tokens, int32_t hq, int32_t max_pages);
 
