@@ -11,7 +11,7 @@
 // would leave most SMs idle in small batches); each sums its part of the row in segments of 512
 // weights, the CTAs exchange their totals through distributed shared memory, and the one CTA whose part
 // holds the threshold finds its segment from the sums and reads those 512 weights again.  CTAs of 256
-// threads: six share an SM, so that one's search for the first rejected draft and its exchange run under
+// threads: five share an SM, so that one's search for the first rejected draft and its exchange run under
 // the others' loads (512 threads: 63 us where 256 take 47).
 //
 // Measured: 256 sequences of 131072 weights, 220 MB that no cache holds, 47 us, 4.7 TB/s (the floor is 39.5 us
