@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
             const Cut c = a.prompt_cut[blockIdx.x];  // (all these loads at once: what lies past the workers is not used)
             const int64_t next_lo = a.prompt_cut[min(blockIdx.x + 1, kPromptMaxWorkers - 1)].lo;
             uint32_t x = 0, q_use[2] = {0, 0};  // units, and queries of each half, brought in
-            bool more = (int)blockIdx.x < workers;
+            bool more = (int)blockIdx.x < workers, first_unit = true;
             Walk w;
             if (more) {
                 w.s = c.s;
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                         u.n = w.n;
                         u.token = token;
                         u.whole = count == tiles;
-                        u.slot = 2 * blockIdx.x + (x == 0 ? 0 : 1);
+                        u.slot = 2 * blockIdx.x + (first_unit ? 0 : 1);  // (the range's first, were it one without images)
                         // (above 0, so that a masked score of -infinity stays one whatever the scale)
                         u.score_unit = fmaxf(fabsf(p.scale) * kLog2e * (BF16 ? 1.0f : norm.x * (1.0f / kUp<E4M3>)), 1e-35f);
                         u.v_unit = norm.y * (1.0f / kUp<E4M3>);
@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                     }
                     ++x;
                 }
+                first_unit = false;
                 if (handed) {
                     // the next one once the last scores of this are under way: sooner would leave it to a busy CTA
                     if (q_use[0] > 0) GDN_KV_WAIT(&sm.q_empty[0], (q_use[0] - 1) & 1);

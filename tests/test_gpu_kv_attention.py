@@ -448,6 +448,18 @@ def test_prompt_units_handed_out_past_one_without_images():
     check_attention(b)
 
 
+@pytest.mark.parametrize("hole", [0, 1, 2, 3])
+def test_prompt_ranges_that_begin_in_a_sequence_without_images(hole):
+    """A range of cut units may begin with units that have no images: what it has of the next sequence's
+    first unit is still its second part."""
+    b = Batch([192, 378, 35, 106, 1], [1167, 0, 214, 15, 127], 28, 4, 128, 16, "int8", "bf16", seed=7)
+    b.fill_past()
+    b.append()
+    b.table_h[hole, 5] = -1
+    b.table.copy_(torch.tensor(b.table_h))
+    check_attention(b)
+
+
 def test_prompts_repeat_exactly_and_follow_their_lengths_in_a_graph():
     import gated_deltanet_linear_pre_gb300 as gdn
     b = Batch([150, 1, 90], [700, 300, 10], 8, 2, 128, 64, "int8", "bf16", seed=7)
