@@ -369,7 +369,7 @@ def gdn_scan_selftest_withhold_flag(d: gdn_dims, cu_seqlens, total_tokens, qn, k
 # one pass over each tensor; a tensor that fails one goes to a function that says why.
 _KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
 _ACT_TYPES = {torch.float16: 0, torch.bfloat16: 1}
-_I32, _F32 = torch.int32, torch.float32
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
 def _refuse(t, name, dtype, shape):
@@ -429,11 +429,10 @@ def _act(t, name: str) -> int:
 
 
 def _kv_batch(cu_seqlens, past, page_table):
-    n = page_table.shape[0]
-    cu = _dense(cu_seqlens, "cu_seqlens", _I32, (n + 1,))
     if page_table.dtype is not _I32 or page_table.dim() != 2 or not page_table.is_cuda:
         raise ValueError("page_table must be an int32 CUDA tensor [n_seq, max_pages]")
-    width = page_table.shape[1]
+    n, width = page_table.shape
+    cu = _dense(cu_seqlens, "cu_seqlens", _I32, (n + 1,))
     stride, one = page_table.stride()
     if one != 1 and width > 1:
         raise ValueError("page_table's rows must be contiguous")
@@ -483,7 +482,10 @@ def gdn_kv_attn(cache: gdn_kv_cache, cu_seqlens, total_tokens, past, page_table,
     wp, wb = None, 0
     if workspace is not None:
         wb = workspace.numel()
-        wp = _ptr(workspace, "workspace", torch.uint8)
+        if workspace.dtype is _U8 and workspace.is_cuda and workspace.is_contiguous():
+            wp = workspace.data_ptr()
+        else:
+            _refuse(workspace, "workspace", _U8, None)
     st = lib().gdn_kv_attn(ctypes.byref(cache), act, n, T, cu, pst, table, table_stride, width, hq, qp, qs,
                            softmax_scale, _dense(y, "y", dt, shape), wp, wb, _stream(stream))
     if st:
