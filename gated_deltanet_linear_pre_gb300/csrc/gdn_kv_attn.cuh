@@ -65,7 +65,8 @@ struct Cut {
     int s, head, unit, j0, tiles;  // unit: the step unit's first row, the prompt unit's index
     int from;                      // cost of the unit that lies before the range
     int64_t lo;                    // cost of all units that does
-    int t0, n, first, image;       // (prompt) the sequence's tokens, first position and image tile
+    int t0, n;                     // the sequence's tokens
+    int first, image;              // (prompt) its first position and image tile
 };
 
 struct AttnHeader {
@@ -219,6 +220,12 @@ __device__ __forceinline__ void row_unit(uint32_t amax, float& mul, float& back)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// CTAs an SM of the step kernel, and its CTAs.  Three of two tiles a warp keep some 48 KB in flight beside the tiles in work, which is enough:
+// with four of three tiles requests only waited for one another (64 sequences of up to 8192 positions 71.2 ->
+// 68.1 us, 3 of 131000 50.0 -> 45.5, 37 sequences of drafts 88.8 -> 81.6; two of four: 66.4, 69.3 and 89.8), and
+// three leave the registers for the queries.
+constexpr int step_ctas(int rows) { return rows == kStepMaxRows ? 2 : 3; }
+inline int step_grid(int sms, int rows) { return sms * step_ctas(rows) < kStepMaxWorkers ? sms * step_ctas(rows) : kStepMaxWorkers; }
 inline int prompt_grid(int sms) { return sms < kPromptMaxWorkers ? sms : kPromptMaxWorkers; }
 
 // the kernels' launches (gdn_kv_step.cu, gdn_kv_prompt.cu, gdn_kv_join.cu)

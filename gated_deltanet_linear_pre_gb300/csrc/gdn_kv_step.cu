@@ -34,11 +34,6 @@ namespace {
 constexpr int kStepThreads = 128;
 constexpr int kWarps = kStepThreads / 32;
 constexpr int kStages = 2;             // tiles of a warp in its ring
-// CTAs an SM.  Three of two tiles a warp keep some 48 KB in flight beside the tiles in work, which is enough:
-// with four of three tiles requests only waited for one another (64 sequences of up to 8192 positions 71.2 ->
-// 68.1 us, 3 of 131000 50.0 -> 45.5, 37 sequences of drafts 88.8 -> 81.6; two of four: 66.4, 69.3 and 89.8), and
-// three leave the registers for the queries.
-template <int NT> constexpr int kCtas = NT == 4 ? 2 : 3;
 constexpr float kWeightUnit = 128.0f;  // 2^7
 constexpr float kLazy = 8.0f;
 
@@ -158,7 +153,7 @@ __device__ __forceinline__ void step_units(const KvBatch& p, const AttnSpace& a,
 }
 
 template <int D, bool BF16, bool E4M3, int NT>
-__global__ void __launch_bounds__(kStepThreads, kCtas<NT>) kv_step_kernel(AttnParams p, AttnSpace a)
+__global__ void __launch_bounds__(kStepThreads, step_ctas(8 * NT)) kv_step_kernel(AttnParams p, AttnSpace a)
 {
     constexpr int R = 8 * NT, KS = D / 16, MT = D / 16;
     using Smem = StepSmem<D, NT>;
@@ -205,7 +200,7 @@ __global__ void __launch_bounds__(kStepThreads, kCtas<NT>) kv_step_kernel(AttnPa
             x += to - from;
             const int head = (int)(unit / groups), row0 = (int)(unit - (int64_t)head * groups) * R;
             const int rows = v.n * group;
-            if (first_unit && tid == 0) a.step_cut[blockIdx.x] = Cut{s, head, row0, j0, tiles, from, lo};
+            if (first_unit && tid == 0) a.step_cut[blockIdx.x] = Cut{s, head, row0, j0, tiles, from, lo, v.t0, v.n, 0, 0};
             if (j1 <= 0) break;  // the range ends within the unit's constant
 
             // the warp's first tiles on their way
@@ -484,7 +479,7 @@ cudaError_t launch(const AttnParams& p, const AttnSpace& a, int sms, cudaStream_
     // 301 positions 10.8 -> 7.5 us)
     const double units = ((double)p.T * (p.hq / p.heads) / (8 * NT) + p.n_seq) * p.heads, tiles = (double)p.max_pages * p.page / kStepTile<D> + 1;
     const double most = a.whole_units ? units : units * (tiles + kStepUnitCost) / (kStepUnitCost + 2 * kWarps) + 1;
-    const int grid = (int)min((double)min(sms * kCtas<NT>, kStepMaxWorkers), ceil(most));
+    const int grid = (int)min((double)step_grid(sms, 8 * NT), ceil(most));
     return launch_k(kernel, dim3(grid), dim3(kStepThreads), smem, stream, true, p, a);
 }
 
