@@ -220,10 +220,10 @@ __device__ __forceinline__ void row_unit(uint32_t amax, float& mul, float& back)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// CTAs an SM of the step kernel, and its CTAs.  Three of two tiles a warp keep some 48 KB in flight beside the tiles in work, which is enough:
-// with four of three tiles requests only waited for one another (64 sequences of up to 8192 positions 71.2 ->
-// 68.1 us, 3 of 131000 50.0 -> 45.5, 37 sequences of drafts 88.8 -> 81.6; two of four: 66.4, 69.3 and 89.8), and
-// three leave the registers for the queries.
+// CTAs an SM of the step kernel, and its CTAs.  Three with rings of two tiles a warp keep some 48 KB in flight
+// beside the tiles in work, which is enough: with four and rings of three, requests only waited for one another
+// (64 sequences of up to 8192 positions 71.2 -> 68.1 us, 3 of 131000 50.0 -> 45.5, 37 sequences of drafts 88.8 ->
+// 81.6; two and rings of four: 66.4, 69.3 and 89.8), and three leave the registers for the queries.
 constexpr int step_ctas(int rows) { return rows == kStepMaxRows ? 2 : 3; }
 inline int step_grid(int sms, int rows) { return sms * step_ctas(rows) < kStepMaxWorkers ? sms * step_ctas(rows) : kStepMaxWorkers; }
 inline int prompt_grid(int sms) { return sms < kPromptMaxWorkers ? sms : kPromptMaxWorkers; }
