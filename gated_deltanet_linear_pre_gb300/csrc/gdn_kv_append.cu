@@ -171,11 +171,14 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
     auto fetch = [&](int row) {
         return row >= lo && row < hi ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * stride)) : make_uint4(0u, 0u, 0u, 0u);
     };
-    auto value = [&](int row, const uint4& raw, float (&x)[8]) {  // rows outside [lo, hi) come out as zeros
+    auto value = [&](int row, const uint4& raw, float (&x)[8]) {
         widen8<BF16>(raw, x);
         if (rotated) Angles(p, c, at * p.page + row).turn<BF16>(raw, x, p.interleaved);
     };
-    auto largest = [](uint32_t amax, const float (&x)[8]) {  // as bits: infinities and NaN come out largest
+    // as bits: infinities and NaN come out largest.  Rows outside [lo, hi) do not count: the table's angles at
+    // their positions may be anything, and make NaN of their zeros.
+    auto largest = [&](uint32_t amax, int row, const float (&x)[8]) {
+        if (row < lo || row >= hi) return amax;
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
         return amax;
@@ -187,7 +190,7 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
         for (int row = lo + r0; row - r0 < hi; row += kRows) {
             float x[8];
             value(row, fetch(row), x);
-            amax = largest(amax, x);
+            amax = largest(amax, row, x);
         }
     } else {
         uint4 raw[HELD];
@@ -196,7 +199,7 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             value(i * kRows + r0, raw[i], held[i]);
-            amax = largest(amax, held[i]);
+            amax = largest(amax, i * kRows + r0, held[i]);
         }
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
