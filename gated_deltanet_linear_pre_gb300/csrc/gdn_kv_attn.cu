@@ -39,7 +39,7 @@ size_t layout(const KvBatch& b, void* ws, AttnSpace& a)
     a.most_rows = kLongRows;
     a.ok = reinterpret_cast<int*>(take(n * 4));
     a.image_base = reinterpret_cast<int*>(take(n * 4));
-    a.norm = reinterpret_cast<float2*>(take(tiles * b.heads * 8));
+    a.units = reinterpret_cast<HeadUnits*>(take(tiles * b.heads * sizeof(HeadUnits)));
     a.prompt_cut = reinterpret_cast<Cut*>(take(kPromptMaxWorkers * sizeof(Cut)));
     a.prompt_stat = reinterpret_cast<float2*>(take((size_t)2 * kPromptMaxWorkers * kUnitRows * 8));
     a.prompt_out = reinterpret_cast<float4*>(take((size_t)2 * kPromptMaxWorkers * kUnitRows * dim * 4));

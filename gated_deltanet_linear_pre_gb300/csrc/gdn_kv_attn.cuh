@@ -69,6 +69,13 @@ struct Cut {
     int first, image;              // (prompt) its first position and image tile
 };
 
+// what the images of a (sequence, kv head) leave out
+struct alignas(16) HeadUnits {
+    float k, v;    // largest scales
+    int nan_from;  // first position of a page whose v scale is NaN: rows that see it are NaN
+    int unused;
+};
+
 struct AttnHeader {
     uint32_t error;
     int step_workers, prompt_workers;
@@ -85,7 +92,7 @@ struct AttnSpace {
     // the rest is there only where the batch may hold a long sequence (image_tiles > 0)
     int* ok;               // [n_seq] a candidate whose images are written
     int* image_base;       // [n_seq] its first image tile
-    float2* norm;          // [image_tiles][heads], at the sequence's first tile: largest k and v scale
+    HeadUnits* units;      // [image_tiles][heads], at the sequence's first tile
     Cut* prompt_cut;       // [kPromptMaxWorkers]
     float2* prompt_stat;   // [2 kPromptMaxWorkers][kUnitRows]
     float4* prompt_out;    // [2 kPromptMaxWorkers][dim / 4][kUnitRows]

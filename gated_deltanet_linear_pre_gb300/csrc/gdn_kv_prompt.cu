@@ -15,7 +15,9 @@
 // operands of a product have one), so queries go to shared memory as they are.  A bf16 image holds code *
 // scale, exactly.  An fp16 image (V always) holds code * (page scale / largest scale of the sequence and
 // head) * kUp, exact for pages whose scale is at least 2^-21 (e4m3) or 2^-32 (int8) of the largest; the
-// largest scale itself goes into the scores' unit and the outputs'.
+// largest scale itself goes into the scores' unit and the outputs'.  A page whose v scale is NaN has an image of
+// zeros, since a weight of 0 times NaN would reach the rows that do not see it: the output code makes the rows
+// that do see it NaN.  (A NaN k scale makes a column of scores NaN, which the mask replaces.)
 //
 // A CTA (608 threads, one per SM) holds two 128-row halves, so that one half's softmax runs under the
 // other's products: warps 0-7 and 8-15 the rows (two threads a row, each half of a tile's columns: a tile's
@@ -303,6 +305,7 @@ struct Unit {
     int token;         // the unit's first one in the sequence
     int whole, slot;   // all of the unit's tiles; else where its part goes
     float score_unit, v_unit;  // value of a score's unit (base 2) and of an output's
+    int nan_from;      // first position of a page whose v are NaN
 };
 
 // and in bf16
@@ -324,7 +327,7 @@ template <int D, bool BF16, bool E4M3>
 __global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p, AttnSpace a, int prompt_grid)
 {
     __shared__ ScanSmem<kImageThreads> scan;
-    __shared__ float top_k[kImageThreads / 32], top_v[kImageThreads / 32];
+    __shared__ uint32_t top_k[kImageThreads / 32], top_v[kImageThreads / 32], first_nan[kImageThreads / 32];
     struct Part {
         int64_t at;  // byte of its first code
         float k, v;
@@ -356,40 +359,44 @@ __global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p
         const int64_t base = before / p.heads;         // image tiles before the sequence's
         before += (int64_t)p.heads * n;
         for (int head = (int)(at / n); head < p.heads && x < hi; ++head) {
-            // whether the sequence's images fit and every page is there; its largest scales (NaN ones apart)
-            float mk = 0.0f, mv = 0.0f;
+            // whether the sequence's images fit and every page is there; its largest scales (NaN ones apart, as
+            // bits: they are not below 0) and the first page whose v scale is NaN
+            uint32_t k_bits = 0u, v_bits = 0u, nan_page = 0x7fffffffu;
             bool there = base + n <= a.image_tiles;
             for (int i = tid; i < pages; i += kImageThreads) {
                 const int page = page_at(p, s, i);
                 if (page < 0) {
                     there = false;
                 } else {
-                    mk = fmaxf(mk, __ldg(p.k_scale + (size_t)page * p.heads + head));
-                    mv = fmaxf(mv, __ldg(p.v_scale + (size_t)page * p.heads + head));
+                    const float ks = __ldg(p.k_scale + (size_t)page * p.heads + head), vs = __ldg(p.v_scale + (size_t)page * p.heads + head);
+                    if (ks > 0.0f) k_bits = max(k_bits, __float_as_uint(ks));
+                    if (vs > 0.0f) v_bits = max(v_bits, __float_as_uint(vs));
+                    if (vs != vs) nan_page = min(nan_page, (uint32_t)i);
                 }
             }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
-                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
-            }
+            k_bits = __reduce_max_sync(0xffffffffu, k_bits);
+            v_bits = __reduce_max_sync(0xffffffffu, v_bits);
+            nan_page = __reduce_min_sync(0xffffffffu, nan_page);
             if (lane == 0) {
-                top_k[warp] = mk;
-                top_v[warp] = mv;
+                top_k[warp] = k_bits;
+                top_v[warp] = v_bits;
+                first_nan[warp] = nan_page;
             }
             there = __syncthreads_and(there);
 #pragma unroll
             for (int w = 0; w < kImageThreads / 32; ++w) {
-                mk = fmaxf(mk, top_k[w]);
-                mv = fmaxf(mv, top_v[w]);
+                k_bits = max(k_bits, top_k[w]);
+                v_bits = max(v_bits, top_v[w]);
+                nan_page = min(nan_page, first_nan[w]);
             }
+            const float mk = __uint_as_float(k_bits), mv = __uint_as_float(v_bits);
             const int first = (int)(at - (int64_t)head * n);
             if (first == 0 && tid == 0) {
                 if (head == 0) {
                     a.ok[s] = there;
                     a.image_base[s] = there ? (int)base : 0;
                 }
-                if (there) a.norm[(size_t)base * p.heads + head] = make_float2(mk, mv);
+                if (there) a.units[(size_t)base * p.heads + head] = HeadUnits{mk, mv, nan_page < (uint32_t)pages ? (int)nan_page << shift : 0x7fffffff, 0};
             }
             const int last = (int)min((int64_t)n, first + (hi - x));
             x += last - first;
@@ -403,9 +410,9 @@ __global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p
                         const int64_t row = (int64_t)page_at(p, s, pos >> shift) * p.heads + head;
                         const float ks = __ldg(p.k_scale + row), vs = __ldg(p.v_scale + row);
                         part.at = (row * p.page + (pos & (p.page - 1))) * D;
-                        // (a scale of 0 may meet a largest one of 0; NaN scales stay NaN)
+                        // (a scale of 0 may meet a largest one of 0; a NaN k scale stays NaN)
                         part.k = (ks == 0.0f ? 0.0f : BF16 ? ks : ks / mk * kUp<E4M3>) * sign;
-                        part.v = vs == 0.0f ? 0.0f : vs / mv * kUp<E4M3>;
+                        part.v = vs > 0.0f ? vs / mv * kUp<E4M3> : 0.0f;
                     }
                     parts[tid] = part;
                 }
@@ -434,7 +441,7 @@ __global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p
                 }
                 __syncthreads();  // parts read
             }
-            __syncthreads();  // top_k, top_v read
+            __syncthreads();  // top_k, top_v, first_nan read
         }
         at = 0;
     }
@@ -606,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 const int tiles = unit_tiles(w.first, w.n, span, w.i);
                 const int to = (int)min((int64_t)tiles + kPromptUnitCost, w.from + w.left);
                 const int j0 = max(w.from - kPromptUnitCost, 0), count = to - kPromptUnitCost - j0;
-                const float2 norm = a.norm[(size_t)w.image * p.heads + w.head];
+                const HeadUnits of = a.units[(size_t)w.image * p.heads + w.head];
                 if (count > 0 && w.ok) {  // (a range may end within a unit's constant)
                     if (x >= kUnits) GDN_KV_WAIT(&sm.unit_empty[x % kUnits], (x / kUnits - 1) & 1);
                     const int token = w.i * span;
@@ -623,8 +630,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                         u.whole = count == tiles;
                         u.slot = 2 * blockIdx.x + (first_unit ? 0 : 1);  // (the range's first, were it one without images)
                         // (above 0, so that a masked score of -infinity stays one whatever the scale)
-                        u.score_unit = fmaxf(fabsf(p.scale) * kLog2e * (BF16 ? 1.0f : norm.x * (1.0f / kUp<E4M3>)), 1e-35f);
-                        u.v_unit = norm.y * (1.0f / kUp<E4M3>);
+                        u.score_unit = fmaxf(fabsf(p.scale) * kLog2e * (BF16 ? 1.0f : of.k * (1.0f / kUp<E4M3>)), 1e-35f);
+                        u.v_unit = of.v * (1.0f / kUp<E4M3>);
+                        u.nan_from = of.nan_from;
                         umma::mbar_arrive(&sm.unit_full[x % kUnits]);
                     }
                     for (int h = 0; h < 2; ++h) {
@@ -877,7 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 const int i_tok = r / group, tok = token0 + i_tok, qh = r - i_tok * group;
                 const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 31) == 0, whole = u.whole, valid = i_tok < tokens && tok < u.n;
                 const int slot = u.slot, row = 128 * h + r;
-                const float scale = whole ? (l == 0.0f ? 0.0f : u.v_unit / l) : u.v_unit;
+                float scale = whole ? (l == 0.0f ? 0.0f : u.v_unit / l) : u.v_unit;
+                if (u.first + tok >= u.nan_from) scale = __uint_as_float(0x7fffffffu);
                 uint16_t* const dst = p.y + ((int64_t)(u.t0 + tok) * p.hq + u.head * group + qh) * D + part * (D / 2);
                 if (!whole && part == 0) a.prompt_stat[(size_t)slot * kUnitRows + row] = make_float2(m, l);
 #pragma unroll

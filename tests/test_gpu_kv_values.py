@@ -43,3 +43,71 @@ def test_append_reads_the_rotation_of_its_own_positions(new, past, page, dim, ro
         t[used] = kept
     assert torch.equal(a.append(), b.append())
     same_cache(a, b)
+
+
+# ---- the attention of prompts ----------------------------------------------------------------------------
+
+def check_with_nan(b, q=None):
+    """Every row against the definition: NaN where it sees a value that is, within the bound elsewhere."""
+    import kv_util as u
+    y = u.values(b.attend(q))
+    ref, wabs, xabs = b.reference(q)
+    nan = np.isnan(ref)
+    assert nan.any() and not nan.all()
+    assert np.array_equal(np.isnan(y), nan)
+    bound = u.attention_bound(ref, wabs, xabs, b.dtype)
+    assert np.all(np.abs(y - ref)[~nan] <= bound[~nan])
+
+
+PROMPTS = [  # new, past, hq, heads, dim, page
+    ([200], [0], 4, 2, 128, 32),
+    ([300], [100], 2, 2, 64, 16),                     # one query head a kv head: units of 256 tokens
+    ([150, 130], [0, 60], 32, 8, 64, 64),
+    ([130, 1, 200], [50, 70, 0], 128, 32, 64, 16),    # more units than CTAs: handed out one by one
+    ([70, 1, 90], [3000, 5, 2000], 8, 2, 128, 64),    # a few long units: cut
+]
+
+
+@pytest.mark.parametrize("new,past,hq,heads,dim,page", PROMPTS)
+@pytest.mark.parametrize("fmt,dtype", [("int8", "fp16"), ("int8", "bf16"), ("e4m3", "fp16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_prompt_rows_before_a_value_that_is_not_finite(new, past, hq, heads, dim, page, fmt, dtype, which):
+    """An infinity among a prompt's new values reaches the rows that see its page, and no other."""
+    b = batch(new, past, hq, heads, dim, page, fmt, dtype, seed=len(new) + page, rot=0)
+    b.fill_past()
+    x = b.kn if which == "k" else b.vn
+    last = len(new) - 1
+    x[int(b.cu_h[last]) + new[last] // 2, heads - 1, 7] = float("inf")
+    x[int(b.cu_h[1]) - 1, 0, 1] = float("nan")        # the first prompt's last token
+    b.append()
+    check_with_nan(b)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("e4m3", "fp16")])
+def test_prompt_with_several_pages_that_are_not_finite(fmt, dtype):
+    """The first of a head's NaN pages decides; the other heads and sequences keep their own."""
+    b = batch([180, 160], [20, 300], 8, 4, 64, 16, fmt, dtype, seed=1)
+    b.fill_past()
+    b.append()
+    for s, head, at in ((0, 1, 9), (0, 1, 4), (0, 3, 12), (1, 0, 25), (1, 2, 20), (1, 2, 28)):
+        b.vs[int(b.table_h[s, at]), head] = float("nan")
+    b.ks[int(b.table_h[1, 22]), 0] = float("nan")
+    check_with_nan(b)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "fp16"), ("e4m3", "bf16")])
+def test_prompt_ignores_what_no_query_sees(fmt, dtype):
+    b = batch([120, 90], [37, 130], 4, 1, 128, 64, fmt, dtype, seed=8)
+    b.fill_past()
+    b.append()
+    y0 = b.attend().clone()
+    used = {int(b.table_h[s, at]) for s in range(2) for at in range(-(-(b.past_h[s] + b.new[s]) // 64))}
+    for pg in range(b.k.shape[0]):
+        if pg not in used:
+            b.ks[pg], b.vs[pg] = float("inf"), float("nan")
+    for s in range(2):
+        held = b.past_h[s] + b.new[s]
+        pg, rows = int(b.table_h[s, (held - 1) // 64]), (held - 1) % 64 + 1
+        for codes in (b.k, b.v):
+            codes.view(torch.uint8)[pg, :, rows:] = 0x7F
+    assert torch.equal(b.attend(), y0)
