@@ -50,6 +50,7 @@ constexpr int kThreads = 608;
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kQueryWarp = 18;
 constexpr float kWeightShift = 7.0f;
 constexpr float kLazy = 8.0f;
+constexpr float kLargeScore = 1048576.0f;  // 2^20: a step of 2^-3
 
 // images hold codes times kUp: up to 127 x 2^8 and 448 x 2^6
 template <bool E4M3> constexpr float kUp = E4M3 ? 64.0f : 256.0f;
@@ -807,7 +808,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                     const int i_tok = r / group;
                     if (i_tok < tokens && token0 + i_tok < u.n) last = u.first + token0 + i_tok - (u.j0 * kKeys + 64 * part);
                 }
-                float m = -INFINITY, l = 0.0f;
+                float m = -INFINITY, l = 0.0f;  // m: the reference in units of the scores as they come
+                // A weight's exponent is x coef + off, one fused operation with off = kWeightShift - m coef.  The
+                // products lie up to half a step of theirs beside the rounded one in off: where that is not small (a
+                // row of scores past 2^28 would leave fp16's range) m is subtracted from the scores themselves.
+                float off = kWeightShift;
+                bool large = false;
                 const int count = u.count;
 #pragma unroll 1
                 for (int j = 0; j < count; ++j, last -= kKeys) {
@@ -822,16 +828,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
                     }
-                    top *= coef;
-                    if (pair_any(pair, top > m + kLazy)) {
+                    if (pair_any(pair, (top - m) * coef > kLazy)) {
                         sm.other[h][part][r] = top;
                         pair_sync(pair);
                         top = fmaxf(top, sm.other[h][part ^ 1][r]);
                         float f = 1.0f;
-                        if (top > m + kLazy) {
-                            f = ex2(m - top);
+                        if ((top - m) * coef > kLazy) {
+                            f = ex2((m - top) * coef);
                             m = top;
                             l *= f;
+                            large = fabsf(m * coef) >= kLargeScore;
+                            off = large ? kWeightShift : kWeightShift - m * coef;
                         }
                         // O holds the products up to tile j - 1, which ended before this tile's scores
                         if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
@@ -847,7 +854,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                             }
                         }
                     }
-                    const float off = kWeightShift - (m == -INFINITY ? 0.0f : m);
+                    auto settle = [&] {
+                        if (large)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) unpair2(add2(pair2(x[e], x[e + 1]), pair2(-m, -m)), x[e], x[e + 1]);
+                    };
                     const uint64_t coef2 = pair2(coef, coef), off2 = pair2(off, off);
                     uint64_t sum[2] = {0, 0};
                     uint32_t u0[16], u1[16];
@@ -863,8 +874,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                         }
                     };
                     // the second 32 are still there; the first ones come again, then both go where those were
+                    settle();
                     weights(u1);
                     scores(0, last, x);
+                    settle();
                     umma::tmem_st16(t_s + 16, u1);
                     weights(u0);
                     umma::tmem_st16(t_s, u0);
@@ -888,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 float scale = whole ? (l == 0.0f ? 0.0f : u.v_unit / l) : u.v_unit;
                 if (u.first + tok >= u.nan_from) scale = __uint_as_float(0x7fffffffu);
                 uint16_t* const dst = p.y + ((int64_t)(u.t0 + tok) * p.hq + u.head * group + qh) * D + part * (D / 2);
-                if (!whole && part == 0) a.prompt_stat[(size_t)slot * kUnitRows + row] = make_float2(m, l);
+                if (!whole && part == 0) a.prompt_stat[(size_t)slot * kUnitRows + row] = make_float2(m * u.score_unit, l);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     float o[32];

@@ -111,3 +111,24 @@ def test_prompt_ignores_what_no_query_sees(fmt, dtype):
         for codes in (b.k, b.v):
             codes.view(torch.uint8)[pg, :, rows:] = 0x7F
     assert torch.equal(b.attend(), y0)
+
+
+@pytest.mark.parametrize("new,past,hq,heads,dim,page", [([150], [100], 4, 2, 128, 32), ([70, 1, 90], [3000, 5, 2000], 8, 2, 64, 64),
+                                                        ([3, 1], [900, 40], 8, 2, 128, 16)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("size", [1e7, 1e8, 1e9, 1e12, 1e30])
+def test_scores_beyond_the_steps_of_fp32(new, past, hq, heads, dim, page, fmt, size):
+    """Scores so large that neighbouring fp32 values lie apart by more than the weights' range: one position
+    takes all the weight, and nothing is NaN."""
+    b = batch(new, past, hq, heads, dim, page, fmt, "bf16", seed=5, rot=0)
+    b.fill_past()
+    b.append()
+    q = (b.q.float() * size).to(b.q.dtype)
+    y = b.attend(q).float()
+    assert not bool(y.isnan().any())
+    # an average of the values of its head: none larger than the largest of them, its weights rounded to fp16
+    for s in range(len(new)):
+        pages = [int(b.table_h[s, at]) for at in range(-(-(past[s] + new[s]) // page))]
+        largest = (b.v[pages].float() * b.vs[pages][..., None, None])[:, :, :].nan_to_num(0).abs().amax((0, 2))
+        rows = y[int(b.cu_h[s]):int(b.cu_h[s + 1])].view(new[s], heads, hq // heads, dim).abs().amax((0, 2))
+        assert bool((rows <= largest * 1.01).all())
