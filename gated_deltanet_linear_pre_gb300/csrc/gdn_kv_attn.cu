@@ -37,7 +37,7 @@ size_t layout(const KvBatch& b, void* ws, AttnSpace& a)
     if (tiles == 0) return at;
     a.image_tiles = (int)tiles;
     a.most_rows = kLongRows;
-    a.ok = reinterpret_cast<int*>(take(n * 4));
+    a.ok = take(n * ok_stride(b.heads));
     a.image_base = reinterpret_cast<int*>(take(n * 4));
     a.units = reinterpret_cast<HeadUnits*>(take(tiles * b.heads * sizeof(HeadUnits)));
     a.prompt_cut = reinterpret_cast<Cut*>(take(kPromptMaxWorkers * sizeof(Cut)));

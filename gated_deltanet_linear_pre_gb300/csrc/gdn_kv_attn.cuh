@@ -4,7 +4,8 @@
 // Two ways through the cache.  Sequences with few query rows (tokens times query heads per kv head, up
 // to kLongRows) go to the step kernel, which reads the codes themselves; the others are long: their
 // cache is unpacked once to fp16 operand images, which the prompt kernel then reads for every 256 query
-// rows.  The choice is made per sequence on the device, so one call serves a batch that mixes prompts
+// rows.  A long sequence whose images would not be exact (exact_ratio), have no room or lack a page takes the
+// step kernel too.  The choice is made per sequence on the device, so one call serves a batch that mixes prompts
 // and single tokens, and a captured call follows its lengths.
 //
 // Work is counted in key tiles: a unit is (sequence, kv head, group of query rows) and costs the tiles
@@ -90,7 +91,7 @@ struct AttnSpace {
     float2* step_stat;     // [2 kStepMaxWorkers][kStepMaxRows]: maximum (base 2), sum; two per worker, the
     float* step_out;       //   range's first unit and its last;  [..][kStepMaxRows][dim]
     // the rest is there only where the batch may hold a long sequence (image_tiles > 0)
-    int* ok;               // [n_seq] a candidate whose images are written
+    uint8_t* ok;           // [n_seq][ok_stride(heads)] 1: the images of that head are written (1 behind the last)
     int* image_base;       // [n_seq] its first image tile
     HeadUnits* units;      // [image_tiles][heads], at the sequence's first tile
     Cut* prompt_cut;       // [kPromptMaxWorkers]
@@ -107,7 +108,16 @@ __device__ __forceinline__ bool candidate(const KvBatch& p, const AttnSpace& a, 
     // (negative positions and positions past the table take the step kernel, which sees to them)
     return (int64_t)v.n * (p.hq / p.heads) > a.most_rows && v.first >= 0 && v.first + v.n <= p.max_pages * p.page;
 }
-__device__ __forceinline__ bool is_long(const KvBatch& p, const AttnSpace& a, int s, const SeqView& v) { return candidate(p, a, v) && a.ok[s]; }
+__host__ __device__ constexpr int ok_stride(int heads) { return (heads + 15) & ~15; }
+// whether the images of all heads of a candidate are written
+__device__ __forceinline__ bool images_there(const KvBatch& p, const AttnSpace& a, int s)
+{
+    const uint4* row = reinterpret_cast<const uint4*>(a.ok + (size_t)s * ok_stride(p.heads));
+    uint32_t all = 0x01010101u;
+    for (int i = 0; i < ok_stride(p.heads) / 16; ++i) all &= row[i].x & row[i].y & row[i].z & row[i].w;
+    return all == 0x01010101u;
+}
+__device__ __forceinline__ bool is_long(const KvBatch& p, const AttnSpace& a, int s, const SeqView& v) { return candidate(p, a, v) && images_there(p, a, s); }
 
 // the cut of `total` tiles into `workers` ranges: start of range w, and the range that holds tile x
 __device__ __forceinline__ int64_t cut_start(int64_t total, int workers, int w) { return total * w / workers; }

@@ -24,7 +24,7 @@ __device__ __forceinline__ void join_prompt(const AttnParams& p, const AttnSpace
     if (w >= workers || a.head->prompt_whole) return;
     const Cut cut = a.prompt_cut[w];
     const int64_t total = a.head->prompt_total, begin = cut.lo - cut.from, prev = a.prompt_cut[w - 1].lo;
-    if (cut.j0 == 0 || prev > begin + kPromptUnitCost || !a.ok[cut.s]) return;
+    if (cut.j0 == 0 || prev > begin + kPromptUnitCost || !images_there(p, a, cut.s)) return;
     const int last = cut_of(total, workers, begin + kPromptUnitCost + cut.tiles - 1);
     const int row = eighth * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
     const int h = row >> 7, r = row & 127, i_tok = r / group, qh = r - i_tok * group;

@@ -14,8 +14,9 @@
 // in: 4 bytes moved per code byte, some 5% of a prompt's time (16 us of 72 with its launch at 2048 tokens).  K takes the activations' type (both
 // operands of a product have one), so queries go to shared memory as they are.  A bf16 image holds code *
 // scale, exactly.  An fp16 image (V always) holds code * (page scale / largest scale of the sequence and
-// head) * kUp, exact for pages whose scale is at least 2^-21 (e4m3) or 2^-32 (int8) of the largest; the
-// largest scale itself goes into the scores' unit and the outputs'.  A page whose v scale is NaN has an image of
+// head) * kUp, exact for pages whose scale is at least exact_ratio of the largest, which goes into the scores'
+// unit and the outputs'.  A sequence with smaller ones takes the step kernel: rows that see only those must
+// not lose bits to pages that they do not see.  A page whose v scale is NaN has an image of
 // zeros, since a weight of 0 times NaN would reach the rows that do not see it: the output code makes the rows
 // that do see it NaN.  (A NaN k scale makes a column of scores NaN, which the mask replaces.)
 //
@@ -54,6 +55,10 @@ constexpr float kLargeScore = 1048576.0f;  // 2^20: a step of 2^-3
 
 // images hold codes times kUp: up to 127 x 2^8 and 448 x 2^6
 template <bool E4M3> constexpr float kUp = E4M3 ? 64.0f : 256.0f;
+
+// the smallest quotient of two scales that leaves a code times kUp a whole number of fp16's least steps, 2^-24:
+// int8 codes are multiples of 1, e4m3 ones of 2^-9
+template <bool E4M3> constexpr float exact_ratio = 1.0f / (E4M3 ? 2097152.0f : 4294967296.0f);
 
 template <int D> constexpr uint32_t kTileBytes = kKeys * D * 2;
 
@@ -244,7 +249,7 @@ struct Walk {
             n = v.n;
             first = v.first;
             units = (n + span - 1) / span;
-            ok = a.ok[s];
+            ok = images_there(p, a, s);
             image = ok ? a.image_base[s] : 0;
             return true;
         }
@@ -283,7 +288,7 @@ struct Walk {
             n = v.n;
             first = v.first;
             units = (n + span - 1) / span;
-            ok = a.ok[s];
+            ok = images_there(p, a, s);
             image = ok ? a.image_base[s] : 0;
         }
         const int64_t in = job - jobs;
@@ -329,6 +334,7 @@ __global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p
 {
     __shared__ ScanSmem<kImageThreads> scan;
     __shared__ uint32_t top_k[kImageThreads / 32], top_v[kImageThreads / 32], first_nan[kImageThreads / 32];
+    __shared__ uint32_t low_k[kImageThreads / 32], low_v[kImageThreads / 32];
     struct Part {
         int64_t at;  // byte of its first code
         float k, v;
@@ -360,9 +366,9 @@ __global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p
         const int64_t base = before / p.heads;         // image tiles before the sequence's
         before += (int64_t)p.heads * n;
         for (int head = (int)(at / n); head < p.heads && x < hi; ++head) {
-            // whether the sequence's images fit and every page is there; its largest scales (NaN ones apart, as
-            // bits: they are not below 0) and the first page whose v scale is NaN
-            uint32_t k_bits = 0u, v_bits = 0u, nan_page = 0x7fffffffu;
+            // whether the sequence's images fit and every page is there; its largest and smallest scales (0 and NaN
+            // apart, as bits: they are not below 0) and the first page whose v scale is NaN
+            uint32_t k_bits = 0u, v_bits = 0u, k_low = 0x7f800000u, v_low = 0x7f800000u, nan_page = 0x7fffffffu;
             bool there = base + n <= a.image_tiles;
             for (int i = tid; i < pages; i += kImageThreads) {
                 const int page = page_at(p, s, i);
@@ -370,15 +376,25 @@ __global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p
                     there = false;
                 } else {
                     const float ks = __ldg(p.k_scale + (size_t)page * p.heads + head), vs = __ldg(p.v_scale + (size_t)page * p.heads + head);
-                    if (ks > 0.0f) k_bits = max(k_bits, __float_as_uint(ks));
-                    if (vs > 0.0f) v_bits = max(v_bits, __float_as_uint(vs));
+                    if (ks > 0.0f) {
+                        k_bits = max(k_bits, __float_as_uint(ks));
+                        k_low = min(k_low, __float_as_uint(ks));
+                    }
+                    if (vs > 0.0f) {
+                        v_bits = max(v_bits, __float_as_uint(vs));
+                        v_low = min(v_low, __float_as_uint(vs));
+                    }
                     if (vs != vs) nan_page = min(nan_page, (uint32_t)i);
                 }
             }
             k_bits = __reduce_max_sync(0xffffffffu, k_bits);
             v_bits = __reduce_max_sync(0xffffffffu, v_bits);
+            k_low = __reduce_min_sync(0xffffffffu, k_low);
+            v_low = __reduce_min_sync(0xffffffffu, v_low);
             nan_page = __reduce_min_sync(0xffffffffu, nan_page);
             if (lane == 0) {
+                low_k[warp] = k_low;
+                low_v[warp] = v_low;
                 top_k[warp] = k_bits;
                 top_v[warp] = v_bits;
                 first_nan[warp] = nan_page;
@@ -388,15 +404,18 @@ __global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p
             for (int w = 0; w < kImageThreads / 32; ++w) {
                 k_bits = max(k_bits, top_k[w]);
                 v_bits = max(v_bits, top_v[w]);
+                k_low = min(k_low, low_k[w]);
+                v_low = min(v_low, low_v[w]);
                 nan_page = min(nan_page, first_nan[w]);
             }
             const float mk = __uint_as_float(k_bits), mv = __uint_as_float(v_bits);
+            there = there && (BF16 || __uint_as_float(k_low) >= mk * exact_ratio<E4M3>) && __uint_as_float(v_low) >= mv * exact_ratio<E4M3>;
             const int first = (int)(at - (int64_t)head * n);
+            const int behind = ok_stride(p.heads) - p.heads;
+            if (first == 0 && head == 0 && tid < behind) a.ok[(size_t)s * ok_stride(p.heads) + p.heads + tid] = 1;
             if (first == 0 && tid == 0) {
-                if (head == 0) {
-                    a.ok[s] = there;
-                    a.image_base[s] = there ? (int)base : 0;
-                }
+                a.ok[(size_t)s * ok_stride(p.heads) + head] = there;
+                if (head == 0) a.image_base[s] = there ? (int)base : 0;
                 if (there) a.units[(size_t)base * p.heads + head] = HeadUnits{mk, mv, nan_page < (uint32_t)pages ? (int)nan_page << shift : 0x7fffffff, 0};
             }
             const int last = (int)min((int64_t)n, first + (hi - x));
@@ -442,7 +461,7 @@ __global__ void __launch_bounds__(kImageThreads, 3) kv_image_kernel(AttnParams p
                 }
                 __syncthreads();  // parts read
             }
-            __syncthreads();  // top_k, top_v, first_nan read
+            __syncthreads();  // the warps' extremes read
         }
         at = 0;
     }
@@ -604,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 w.n = c.n;
                 w.first = c.first;
                 w.units = (c.n + span - 1) / span;
-                w.ok = a.ok[c.s];
+                w.ok = images_there(p, a, c.s);
                 w.image = min(c.image, a.image_tiles - 1);
                 w.from = c.from;
                 w.left = handed ? (int64_t)1 << 62 : ((int)blockIdx.x + 1 < workers ? next_lo : total) - c.lo;

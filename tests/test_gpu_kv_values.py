@@ -132,3 +132,22 @@ def test_scores_beyond_the_steps_of_fp32(new, past, hq, heads, dim, page, fmt, s
         largest = (b.v[pages].float() * b.vs[pages][..., None, None])[:, :, :].nan_to_num(0).abs().amax((0, 2))
         rows = y[int(b.cu_h[s]):int(b.cu_h[s + 1])].view(new[s], heads, hq // heads, dim).abs().amax((0, 2))
         assert bool((rows <= largest * 1.01).all())
+
+
+@pytest.mark.parametrize("new,past,hq,heads,dim,page", [([150], [100], 4, 2, 128, 32), ([170, 1, 140], [90, 40, 200], 8, 4, 64, 16)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_prompt_rows_before_much_larger_pages(new, past, hq, heads, dim, page, fmt, dtype, which):
+    """Later pages of one head are 2^36 times as large as those before them: rows that see only the small
+    ones keep all of their bits."""
+    import test_gpu_kv_attention as t
+    b = batch(new, past, hq, heads, dim, page, fmt, dtype, seed=5, rot=0)
+    b.fill_past()
+    b.append()
+    scales, small, large = (b.ks, -3, 33) if which == "k" else (b.vs, -22, 14) if dtype == "fp16" else (b.vs, 0, 36)
+    for s in range(len(new)):
+        for at in range(-(-(past[s] + new[s]) // page)):
+            behind = at >= (past[s] + new[s] // 2) // page
+            scales[int(b.table_h[s, at]), heads - 1] *= 2.0 ** (large if behind else small)
+    t.check_attention(b)
