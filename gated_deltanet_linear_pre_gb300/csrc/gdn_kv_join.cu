@@ -53,7 +53,7 @@ __device__ __forceinline__ void join_prompt(const AttnParams& p, const AttnSpace
         }
         top = next;
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = 1.0f / sum;  // (0: every score is -infinity, and 0 x inv NaN)
     uint2* dst = reinterpret_cast<uint2*>(p.y + ((int64_t)(t0 + tok) * p.hq + cut.head * group + qh) * D) + part * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) dst[e] = make_uint2(narrow2<BF16>(acc[e].x * inv, acc[e].y * inv), narrow2<BF16>(acc[e].z * inv, acc[e].w * inv));

@@ -917,7 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 const int i_tok = r / group, tok = token0 + i_tok, qh = r - i_tok * group;
                 const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 31) == 0, whole = u.whole, valid = i_tok < tokens && tok < u.n;
                 const int slot = u.slot, row = 128 * h + r;
-                float scale = whole ? (l == 0.0f ? 0.0f : u.v_unit / l) : u.v_unit;
+                // (every row sees its own position: l is 0 only where all scores are -infinity, and y is NaN)
+                float scale = whole ? u.v_unit / l : u.v_unit;
                 if (u.first + tok >= u.nan_from) scale = __uint_as_float(0x7fffffffu);
                 uint16_t* const dst = p.y + ((int64_t)(u.t0 + tok) * p.hq + u.head * group + qh) * D + part * (D / 2);
                 if (!whole && part == 0) a.prompt_stat[(size_t)slot * kUnitRows + row] = make_float2(m * u.score_unit, l);

@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(8 * NT)) kv_step_kerne
                 for (int ks = 0; ks < KS; ++ks)
                     sm.q[nt][ks][lane] = make_uint2(narrow2<false>(f[ks][0] * mul, f[ks][1] * mul), narrow2<false>(f[ks][2] * mul, f[ks][3] * mul));
                 if (t == 0) {
-                    sm.coef[8 * nt + g] = back * (p.scale * kLog2e);
+                    // a row that is not finite has no softmax; its scores alone might all be -infinity, as if masked
+                    sm.coef[8 * nt + g] = amax < 0x7f800000u ? back * (p.scale * kLog2e) : __uint_as_float(0x7fffffffu);
                     sm.limit[8 * nt + g] = row < rows ? v.first + i : -1;
                 }
             }

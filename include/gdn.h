@@ -414,7 +414,7 @@ GDN_API size_t gdn_kv_attn_workspace_bytes(const gdn_kv_cache* cache, int32_t n_
  *   j <= past[s] + i.
  * A position whose table entry is outside [0, n_pages), or past the table row,
  * is not seen; a token that sees none (past[s] + i < 0, say, for an idle slot
- * of a captured batch) gives zeros.
+ * of a captured batch) gives zeros.  A query that is not finite gives NaN.
  *
  * In:  q        [T][hq][head_dim] of `dtype`, tokens q_stride elements apart (a
  *               multiple of 8); hq a multiple of heads, at most 64 per kv head

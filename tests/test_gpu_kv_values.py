@@ -151,3 +151,39 @@ def test_prompt_rows_before_much_larger_pages(new, past, hq, heads, dim, page, f
             behind = at >= (past[s] + new[s] // 2) // page
             scales[int(b.table_h[s, at]), heads - 1] *= 2.0 ** (large if behind else small)
     t.check_attention(b)
+
+
+@pytest.mark.parametrize("new,past,hq,heads,dim,page", [([1], [0], 2, 1, 128, 16), ([1, 1], [70, 900], 8, 2, 64, 16), ([5, 3], [0, 40], 6, 2, 128, 32),
+                                                        ([150], [0], 4, 2, 128, 32), ([60, 1, 70], [3000, 5, 2000], 8, 2, 64, 64)])
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("e4m3", "fp16")])
+@pytest.mark.parametrize("value", [float("-inf"), float("inf"), float("nan")])
+def test_queries_that_are_not_finite(new, past, hq, heads, dim, page, fmt, dtype, value):
+    """A query that is not finite has no softmax: NaN, also where every score is minus infinity; the other
+    rows are what they are without it."""
+    b = batch(new, past, hq, heads, dim, page, fmt, dtype, seed=2, rot=0)
+    b.fill_past()
+    b.k.view(torch.uint8)[..., 3] = 0x40              # 64 or 2: channel 3 of every key is above 0
+    b.kn[:, :, 3] = 2.0
+    b.append()
+    q = b.q.clone()
+    q[..., 3] = -1.0
+    y0 = b.attend(q).clone()
+    rows = [(int(b.cu_h[s + 1]) - 1, (3 * s) % hq) for s in range(len(new))]
+    for tok, head in rows:
+        q[tok, head, 3] = value
+    y = b.attend(q)
+    bad = torch.zeros(y.shape[:2], dtype=torch.bool, device="cuda")
+    for tok, head in rows:
+        bad[tok, head] = True
+    assert bool(y[bad].isnan().all())
+    assert torch.equal(y[~bad], y0[~bad])
+
+
+def test_rows_that_see_nothing_stay_zero_whatever_their_query():
+    b = batch([2, 1], [-2, 5], 4, 2, 64, 16, "int8", "fp16", rot=0)
+    b.fill_past()
+    b.append()
+    q = b.q.clone()
+    q[:2] = float("nan")
+    y = b.attend(q)
+    assert not bool(y[:2].any()) and not bool(y.isnan().any())
