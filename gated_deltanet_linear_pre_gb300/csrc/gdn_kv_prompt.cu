@@ -649,8 +649,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                         u.token = token;
                         u.whole = count == tiles;
                         u.slot = 2 * blockIdx.x + (first_unit ? 0 : 1);  // (the range's first, were it one without images)
-                        // (above 0, so that a masked score of -infinity stays one whatever the scale)
-                        u.score_unit = fmaxf(fabsf(p.scale) * kLog2e * (BF16 ? 1.0f : of.k * (1.0f / kUp<E4M3>)), 1e-35f);
+                        // (above 0, so that a masked score of -infinity stays one whatever the scale; the least fp32
+                        // above it, so that bf16 scores of up to 2^127 times a softmax_scale of 0 are nothing)
+                        u.score_unit = fmaxf(fabsf(p.scale) * kLog2e * (BF16 ? 1.0f : of.k * (1.0f / kUp<E4M3>)), __uint_as_float(1u));
                         u.v_unit = of.v * (1.0f / kUp<E4M3>);
                         u.nan_from = of.nan_from;
                         umma::mbar_arrive(&sm.unit_full[x % kUnits]);

@@ -187,3 +187,14 @@ def test_rows_that_see_nothing_stay_zero_whatever_their_query():
     q[:2] = float("nan")
     y = b.attend(q)
     assert not bool(y[:2].any()) and not bool(y.isnan().any())
+
+
+@pytest.mark.parametrize("size", [1e30, 1e34, 1e36])
+def test_prompt_of_large_queries_and_a_scale_of_zero(size):
+    """Scores that count for nothing: every row is the mean of what it sees."""
+    import test_gpu_kv_attention as t
+    b = batch([130], [40], 4, 2, 64, 16, "e4m3", "bf16", seed=6, rot=0)
+    b.fill_past()
+    b.append()
+    q = torch.randn(b.q.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).clamp(-2, 2)
+    t.check_attention(b, q=(q * size).to(b.q.dtype), softmax_scale=0.0)
