@@ -6,7 +6,9 @@
 // code is x / S to nearest even.  Powers of two make three things exact: the division, the
 // dequantisation, and the growth S / S_old by which earlier codes of the page are shifted when a larger
 // value arrives; since every growth at least doubles S, the half steps lost at each of them add up to
-// less than one step of the final S.
+// less than one step of the final S.  A value that is not finite makes the page's scale NaN, whose bits keep
+// S (of the finite values; their codes are as they would be without it) and the first row that holds one: an
+// append that starts at or in front of that row, as after rejected drafts, finds the page as it was.
 //
 // Layout.  The unit of work is (page touched by a sequence, kv head, k or v): its scale is one maximum
 // over the unit's rows, so no unit needs another's result and the call is one launch without
@@ -94,16 +96,24 @@ struct Angles {
     }
 };
 
-// Smallest power of two not below amax / qmax, at least 2^-100; 0 for 0 and NaN for an infinity or NaN.
+// Smallest power of two not below amax / qmax, at least 2^-100; 0 for 0.
 // 127 = 1.984375 x 2^6 and 448 = 1.75 x 2^8: the exponent is amax's less 6 or 8, one more where amax's
 // mantissa exceeds qmax's.
 template <bool E4M3>
 __device__ __forceinline__ float scale_for(uint32_t amax_bits)
 {
     if (amax_bits == 0) return 0.0f;
-    if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
     const int e = (int)(amax_bits >> 23) - (E4M3 ? 8 : 6) + ((amax_bits & 0x7fffffu) > (E4M3 ? 0x600000u : 0x7e0000u) ? 1 : 0);
     return __uint_as_float((uint32_t)max(e, 27) << 23);
+}
+
+// The scale of a page that holds a value that is not finite: a NaN of 17 fixed bits, the exponent of the finite
+// values' scale (8 bits) and the first such row (7).  Any other NaN says nothing of either.
+constexpr uint32_t kNanScale = 0x7fd50000u, kNanScaleMask = 0xffff8000u;
+constexpr int kNoRow = 1 << 30;
+__device__ __forceinline__ float nan_scale(float scale, int row)
+{
+    return __uint_as_float(scale == scale ? kNanScale | ((__float_as_uint(scale) >> 23) << 7) | (uint32_t)row : 0x7fc00000u);
 }
 
 // 8 values times inv (a power of two) to codes, nearest even; |x inv| <= qmax
@@ -166,7 +176,7 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
     const uint16_t* const src = (is_v ? p.v_new : p.k_new) + (int64_t)(t0 + at * p.page - first) * stride + head * D + 8 * c;
     const bool rotated = !is_v && p.rot > 0;
-    const float before = lo > 0 ? *scale_at : 0.0f;
+    float before = lo > 0 ? *scale_at : 0.0f;
 
     auto fetch = [&](int row) {
         return row >= lo && row < hi ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * stride)) : make_uint4(0u, 0u, 0u, 0u);
@@ -182,6 +192,11 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
         return amax;
+    };
+    auto drop = [](float (&x)[8]) {  // values that are not finite, as 0
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if ((__float_as_uint(x[e]) & 0x7fffffffu) >= 0x7f800000u) x[e] = 0.0f;
     };
 
     float held[kTwice ? 1 : HELD][8];
@@ -210,8 +225,55 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
 #pragma unroll
         for (int w = 0; w < THREADS / 32; ++w) amax = max(amax, part[w]);
     }
+    // the first row with a value that is not finite: an earlier call's, unless this one stores it anew, or this call's
+    int bad = kNoRow;
+    if (before != before) {
+        const uint32_t bits = __float_as_uint(before);
+        if ((bits & kNanScaleMask) == kNanScale) {
+            before = __uint_as_float(((bits >> 7) & 0xffu) << 23);
+            if ((int)(bits & 127u) < lo) bad = bits & 127u;
+        }
+    }
+    const bool clean = amax < 0x7f800000u;  // uniform over the unit
+    if (!clean) {  // once more, over the finite values
+        amax = 0;
+        int mine = kNoRow;
+        auto finite = [&](int row, float (&x)[8]) {
+            if (row < lo || row >= hi) return;
+            if (largest(0, row, x) >= 0x7f800000u) mine = min(mine, row);
+            drop(x);
+            amax = largest(amax, row, x);
+        };
+        if constexpr (kTwice) {
+            for (int row = lo + r0; row - r0 < hi; row += kRows) {
+                float x[8];
+                value(row, fetch(row), x);
+                finite(row, x);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) finite(i * kRows + r0, held[i]);
+        }
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        mine = __reduce_min_sync(0xffffffffu, mine);
+        if constexpr (THREADS > 32) {
+            __shared__ uint32_t part[THREADS / 32];
+            __shared__ int row_part[THREADS / 32];
+            if ((threadIdx.x & 31) == 0) {
+                part[threadIdx.x >> 5] = amax;
+                row_part[threadIdx.x >> 5] = mine;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < THREADS / 32; ++w) {
+                amax = max(amax, part[w]);
+                mine = min(mine, row_part[w]);
+            }
+        }
+        bad = min(bad, mine);
+    }
     const float need = scale_for<E4M3>(amax);
-    const float scale = (before != before || need != need) ? __uint_as_float(0x7fc00000u) : fmaxf(before, need);
+    const float scale = before != before ? before : fmaxf(before, need);
     const float inv = scale > 0.0f ? __frcp_rn(scale) : 0.0f;  // exact: a power of two
     if (scale > before) {  // earlier rows move to the larger scale (before = 0: all their values are 0)
         const float ratio = before * inv;
@@ -230,13 +292,14 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, int unit)
         for (int row = lo + r0; row - r0 < hi; row += kRows) {
             float x[8];
             value(row, fetch(row), x);
+            if (!clean) drop(x);
             put(row, x);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < HELD; ++i) put(i * kRows + r0, held[i]);
     }
-    if (tid == 0) *scale_at = scale;
+    if (tid == 0) *scale_at = bad == kNoRow ? scale : nan_scale(scale, bad);
 }
 
 // (token, kQueryHeads heads) by D / 8 lanes

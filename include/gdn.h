@@ -342,8 +342,10 @@ typedef enum gdn_kv_format { GDN_KV_INT8 = 0, GDN_KV_E4M3 = 1 } gdn_kv_format;
  * A value is its code times the scale of its (page, head), one scale for k and
  * one for v.  Scales are 0 (every value 0), a power of two, or NaN (a value
  * that was not finite was stored: everything read from that page and head is
- * NaN).  Fresh pages need no initialisation: the call that stores a page's
- * first position ignores what the page held.
+ * NaN, until an append starts at or in front of the first such position; the
+ * NaN's bits say what the append needs to know for that, so scales are to be
+ * copied as bits).  Fresh pages need no initialisation: the call that stores a
+ * page's first position ignores what the page held.
  */
 typedef struct gdn_kv_cache {
     int32_t heads;       /* kv heads, 1..1024                              */
@@ -387,8 +389,13 @@ typedef struct gdn_kv_cache {
  *      of its page, however its page was filled.
  * A position that is negative, past the table row or whose entry is outside
  * [0, n_pages) is not stored (its query is still rotated).  Going back to an
- * earlier length needs no call: append again from there.  Two sequences of
- * one call must not store into the same page.
+ * earlier length needs no call: append again from there.  What was stored
+ * behind that length and is given up leaves one mark, on the page that the
+ * length ends in: a larger value among it has grown the page's scale, which
+ * does not fall again, so the page's kept values have been rounded to the
+ * coarser steps.  Values that are not finite leave none: they count as 0 in
+ * max|x|, and the page's other codes are what they would be without them.  Two
+ * sequences of one call must not store into the same page.
  */
 GDN_API gdn_status gdn_kv_append(const gdn_kv_cache* cache, int32_t dtype, int32_t n_seq,
                                  int32_t total_tokens, const int32_t* cu_seqlens, const int32_t* past,

@@ -198,3 +198,78 @@ def test_prompt_of_large_queries_and_a_scale_of_zero(size):
     b.append()
     q = torch.randn(b.q.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).clamp(-2, 2)
     t.check_attention(b, q=(q * size).to(b.q.dtype), softmax_scale=0.0)
+
+
+def roll_back(b, past, new):
+    """The same sequences from `past` tokens on, with `new` further ones of b's rows."""
+    import gated_deltanet_linear_pre_gb300 as gdn
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    T = int(sum(new))
+    rows = torch.cat([torch.arange(int(b.cu_h[s]), int(b.cu_h[s]) + n, device="cuda") for s, n in enumerate(new)])
+    gdn.gdn_kv_append(b.cache, cu, T, torch.tensor(past, dtype=torch.int32, device="cuda"), b.table, None, b.kn[rows].contiguous(),
+                      b.vn[rows].contiguous(), None, None, False, None)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim,page,n_seq,past,new", [
+    (128, 16, 1, 5, 9), (64, 32, 3, 20, 3), (128, 64, 2, 40, 40), (64, 128, 1, 30, 90), (128, 128, 2, 3, 120),
+    (64, 16, 60, 5, 11), (128, 16, 80, 2, 14), (128, 16, 40, 2, 14), (64, 64, 50, 3, 61)])
+def test_rejected_values_that_are_not_finite_do_not_cost_what_was_kept(fmt, dim, page, n_seq, past, new):
+    """Drafts of which one is not finite, then an append from in front of it: the page is what it would be
+    had that value been 0."""
+    heads = 4
+    a, b = (batch([new] * n_seq, [past] * n_seq, 4, heads, dim, page, fmt, "bf16", seed=n_seq, rot=0) for _ in range(2))
+    kept = new // 2                                   # tokens in front of the one that is not finite
+    for x in (a, b):
+        x.fill_past()
+        for s in range(n_seq):
+            row = int(x.cu_h[s]) + kept
+            for t, head, c, bad in ((x.kn, 1, 9, float("inf")), (x.vn, 2, 0, float("nan")), (x.vn, 2, 5, float("-inf"))):
+                t[row, head, c] = bad if x is b else 0.0
+        x.append()
+    first = [int(b.table_h[s, (past + kept) // page]) for s in range(n_seq)]
+    assert bool(b.ks[first, 1].isnan().all()) and bool(b.vs[first, 2].isnan().all())
+    assert not bool(b.ks[first][:, [0, 2, 3]].isnan().any()) and not bool(b.vs[first][:, [0, 1, 3]].isnan().any())
+    for codes in ("k", "v"):                          # the finite values of the page are kept beside it
+        assert torch.equal(getattr(a, codes).view(torch.uint8), getattr(b, codes).view(torch.uint8))
+    # behind the bad value: it stays
+    for x in (a, b):
+        roll_back(x, [past + kept + 1] * n_seq, [1] * n_seq)
+    assert bool(b.ks[first, 1].isnan().all()) and bool(b.vs[first, 2].isnan().all())
+    # in front of it: it is gone
+    for x in (a, b):
+        roll_back(x, [past + kept] * n_seq, [1] * n_seq)
+    assert not bool(b.ks[first].isnan().any()) and not bool(b.vs[first].isnan().any())
+    same_cache(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_rows_attend_to_kept_values_after_a_rejected_one(fmt):
+    """The kept tokens of a page whose draft was not finite are attended to within their error again."""
+    import test_gpu_kv_attention as t
+    b = batch([9, 4], [30, 5], 4, 2, 64, 32, fmt, "fp16", seed=4, rot=0)
+    b.fill_past()
+    b.vn[6, 1, 3] = float("inf")                      # position 36 of the first sequence
+    b.kn[11, 0, 3] = float("nan")                     # position 7 of the second
+    b.append()
+    assert bool(b.attend()[6:9, 2:].isnan().all())
+    roll_back(b, [36, 7], [1, 1])
+    b.new, b.past_h, b.cu_h, b.T = [1, 1], [36, 7], np.array([0, 1, 2]), 2
+    b.cu, b.past = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 1, 2], [36, 7]))
+    b.q = b.q[:2]
+    t.check_attention(b)
+
+
+def test_a_nan_scale_of_another_hand_stays_until_its_page_begins_afresh():
+    """Only the append's own NaN says what the page's scale was."""
+    for nan in (0x7FC00000, 0x7FFFFFFF, -1):
+        b = batch([3], [4], 2, 2, 64, 16, "int8", "fp16", seed=4, rot=0)
+        b.fill_past()
+        pg = int(b.table_h[0, 0])
+        b.ks.view(torch.int32)[pg, 1] = nan
+        b.append()
+        assert bool(b.ks[pg, 1].isnan()) and not bool(b.ks[pg, 0].isnan())
+        roll_back(b, [1], [2])
+        assert bool(b.ks[pg, 1].isnan())
+        roll_back(b, [0], [3])
+        assert not bool(b.ks[pg].isnan().any())
