@@ -513,6 +513,14 @@ __device__ __forceinline__ bool wait_for(uint64_t* mbar, uint32_t parity, const 
     return __all_sync(0xffffffffu, umma::mbar_try_wait(mbar, parity)) || wait_long(mbar, parity, abort_flag);
 }
 
+// Whatever completes phase `parity` has ended (bounded, about half a second of SM clock; copies and products end by
+// themselves).
+__device__ __forceinline__ void drain(uint64_t* mbar, uint32_t parity)
+{
+    const long long start = clock64();
+    while (!umma::mbar_try_wait_suspend(mbar, parity, 20000u) && clock64() - start < (1ll << 30)) {}
+}
+
 // 32 bytes, on a boundary of 32
 __device__ __forceinline__ void store8(void* to, const uint32_t* w)
 {
@@ -613,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
             const Cut c = a.prompt_cut[blockIdx.x];  // (all these loads at once: what lies past the workers is not used)
             const int64_t next_lo = a.prompt_cut[min(blockIdx.x + 1, kPromptMaxWorkers - 1)].lo;
             uint32_t x = 0, q_use[2] = {0, 0};  // units, and queries of each half, brought in
+            uint32_t q_armed[2] = {0, 0};       // units whose q_full of each half completes by itself
             bool more = (int)blockIdx.x < workers, first_unit = true;
             Walk w;
             if (more) {
@@ -635,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 const int j0 = max(w.from - kPromptUnitCost, 0), count = to - kPromptUnitCost - j0;
                 const HeadUnits of = a.units[(size_t)w.image * p.heads + w.head];
                 if (count > 0 && w.ok) {  // (a range may end within a unit's constant)
-                    if (x >= kUnits) GDN_KV_WAIT(&sm.unit_empty[x % kUnits], (x / kUnits - 1) & 1);
+                    if (x >= kUnits && !await(&sm.unit_empty[x % kUnits], (x / kUnits - 1) & 1)) goto queries_done;
                     const int token = w.i * span;
                     if (lane == 0) {
                         Unit& u = sm.unit[x % kUnits];
@@ -660,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                         const int token0 = token + h * tokens;
                         const bool rows = token0 < w.n;  // (else a second half without rows)
                         if (rows) {
-                            if (q_use[h] > 0) GDN_KV_WAIT(&sm.q_empty[h], (q_use[h] - 1) & 1);
+                            if (q_use[h] > 0 && !await(&sm.q_empty[h], (q_use[h] - 1) & 1)) goto queries_done;
                             ++q_use[h];
                         }
                         if (lane == 0) {
@@ -674,24 +683,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                                 umma::mbar_arrive(full);
                             }
                         }
+                        q_armed[h] = x + 1;
                     }
                     ++x;
                 }
                 first_unit = false;
                 if (handed) {
                     // the next one once the last scores of this are under way: sooner would leave it to a busy CTA
-                    if (q_use[0] > 0) GDN_KV_WAIT(&sm.q_empty[0], (q_use[0] - 1) & 1);
+                    if (q_use[0] > 0 && !await(&sm.q_empty[0], (q_use[0] - 1) & 1)) goto queries_done;
                     int job = lane == 0 ? atomicAdd(&a.head->prompt_next, 1) : 0;
                     more = w.take(p, a, span, __shfl_sync(0xffffffffu, job, 0));
                 } else {
                     more = w.next(p, a, span, to - w.from);
                 }
             }
-            if (x >= kUnits) GDN_KV_WAIT(&sm.unit_empty[x % kUnits], (x / kUnits - 1) & 1);
+            if (x >= kUnits && !await(&sm.unit_empty[x % kUnits], (x / kUnits - 1) & 1)) goto queries_done;
             if (lane == 0) {
                 sm.unit[x % kUnits].count = 0;
                 umma::mbar_arrive(&sm.unit_full[x % kUnits]);
             }
+        queries_done:
+            // no copy may be in flight when the CTA leaves: after an expired wait nobody else has waited for these
+            for (int h = 0; h < 2; ++h)
+                for (uint32_t i = q_armed[h] > kUnits ? q_armed[h] - kUnits : 0; i < q_armed[h]; ++i) drain(&sm.q_full[i % kUnits][h], (i / kUnits) & 1);
         } else if (warp == kLoadWarp) {
             // ---- copies: K and V of each tile in turn through the ring ----
             uint32_t n = 0;  // copies issued
@@ -705,7 +719,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 for (int j = 2 * count; j > 0; --j, ++n) {
                     const uint32_t slot = n % kSlots;
                     if (n >= kSlots && !await(&sm.kv_empty[slot], (n / kSlots - 1) & 1)) goto copies_done;
+#ifdef GDN_KV_SELFTEST_WITHHOLD_COPY  // the failure report's test builds a library without each CTA's first copy
+                    if (lane == 0 && n > 0) {
+#else
                     if (lane == 0) {
+#endif
                         umma::mbar_arrive_expect_tx(&sm.kv_full[slot], kTile);
                         umma::bulk_g2s(sm.kv[slot], j & 1 ? src + kTile : src, kTile, &sm.kv_full[slot]);
                     }
@@ -713,9 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                 }
             }
         copies_done:
-            // no copy may be in flight when the CTA leaves (copies end by themselves; the limit is a formality)
-            for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i)
-                for (int k = 0; k < 1 << 20 && !umma::mbar_try_wait(&sm.kv_full[i % kSlots], (i / kSlots) & 1); ++k) {}
+            for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i) drain(&sm.kv_full[i % kSlots], (i / kSlots) & 1);
         } else {
             // ---- products, issued by one lane ----
             constexpr uint32_t id_s = BF16 ? umma::idesc_bf16(128, kKeys, false, false) : umma::idesc_f16(128, kKeys, false, false);
@@ -961,7 +977,7 @@ done:
     if (warp == kMmaWarp) {
         if (umma::elect_one()) {  // (the lane that issued them)
             umma::commit(&sm.drain);
-            for (int k = 0; k < 1 << 20 && !umma::mbar_try_wait(&sm.drain, 0); ++k) {}
+            drain(&sm.drain, 0);
         }
         __syncwarp();
     }
