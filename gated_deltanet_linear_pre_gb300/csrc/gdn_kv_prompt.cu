@@ -51,7 +51,8 @@ constexpr int kThreads = 608;
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kQueryWarp = 18;
 constexpr float kWeightShift = 7.0f;
 constexpr float kLazy = 8.0f;
-constexpr float kLargeScore = 1048576.0f;  // 2^20: a step of 2^-3
+constexpr float kLargeScore = 1048576.0f;   // 2^20: fp32 steps of 2^-3
+constexpr float kHugeScore = 67108864.0f;   // 2^26: steps of 4 to 8
 
 // images hold codes times kUp: up to 127 x 2^8 and 448 x 2^6
 template <bool E4M3> constexpr float kUp = E4M3 ? 64.0f : 256.0f;
@@ -844,12 +845,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                     const int i_tok = r / group;
                     if (i_tok < tokens && token0 + i_tok < u.n) last = u.first + token0 + i_tok - (u.j0 * kKeys + 64 * part);
                 }
-                float m = -INFINITY, l = 0.0f;  // m: the reference in units of the scores as they come
-                // A weight's exponent is x coef + off, one fused operation with off = kWeightShift - m coef.  The
-                // products lie up to half a step of theirs beside the rounded one in off: where that is not small (a
-                // row of scores past 2^28 would leave fp16's range) m is subtracted from the scores themselves.
+                float m = -INFINITY, l = 0.0f;  // m: the reference, in units of the scores as they come
+                // A weight's exponent is x mul + off, one fused operation with mul = coef and off = kWeightShift - m coef;
+                // m moves where a score passes `most`.  The products lie up to half a step of theirs beside the
+                // rounded ones in off, which for large scores would take a weight out of fp16's range.  So from
+                // kLargeScore on m is the maximum itself, and from kHugeScore on, where the steps of fp32 scores and the
+                // errors of their sums are far above a weight's range, mul is a power of two and the products exact.
+                float most = -INFINITY, mul = coef;
+                const float lazy = kLazy / coef;
                 float off = kWeightShift;
-                bool large = false;
                 const int count = u.count;
 #pragma unroll 1
                 for (int j = 0; j < count; ++j, last -= kKeys) {
@@ -864,17 +868,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
                     }
-                    if (pair_any(pair, (top - m) * coef > kLazy)) {
+                    if (pair_any(pair, top > most)) {
                         sm.other[h][part][r] = top;
                         pair_sync(pair);
                         top = fmaxf(top, sm.other[h][part ^ 1][r]);
                         float f = 1.0f;
-                        if ((top - m) * coef > kLazy) {
+                        if (top > most) {
                             f = ex2((m - top) * coef);
                             m = top;
                             l *= f;
-                            large = fabsf(m * coef) >= kLargeScore;
-                            off = large ? kWeightShift : kWeightShift - m * coef;
+                            const float size = fabsf(m * coef);
+                            mul = size < kHugeScore ? coef : __uint_as_float(__float_as_uint(coef) & 0x7f800000u);
+                            off = kWeightShift - m * mul;
+                            most = size < kLargeScore ? m + lazy : m;
                         }
                         // O holds the products up to tile j - 1, which ended before this tile's scores
                         if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
@@ -890,12 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                             }
                         }
                     }
-                    auto settle = [&] {
-                        if (large)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) unpair2(add2(pair2(x[e], x[e + 1]), pair2(-m, -m)), x[e], x[e + 1]);
-                    };
-                    const uint64_t coef2 = pair2(coef, coef), off2 = pair2(off, off);
+                    const uint64_t coef2 = pair2(mul, mul), off2 = pair2(off, off);
                     uint64_t sum[2] = {0, 0};
                     uint32_t u0[16], u1[16];
                     auto weights = [&](uint32_t (&to)[16]) {
@@ -910,10 +911,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(AttnParams p, At
                         }
                     };
                     // the second 32 are still there; the first ones come again, then both go where those were
-                    settle();
                     weights(u1);
                     scores(0, last, x);
-                    settle();
                     umma::tmem_st16(t_s + 16, u1);
                     weights(u0);
                     umma::tmem_st16(t_s, u0);
