@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, UNIT == 32 ? 1 : 1024 / THREADS) kv_a
 
 int64_t unit_count(const AppendParams& p) { return ((int64_t)p.T / p.page + 2 * (int64_t)p.n_seq) * p.heads * 2; }
 
-constexpr int64_t kFewUnits = 8 * 152;  // a wave of blocks
+constexpr int64_t kFewUnits = 8 * 152;  // two waves of four blocks on each of this GPU's 152 SMs
 
 template <bool BF16, bool E4M3, int D, int THREADS, int UNIT, int HELD>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream)
@@ -369,8 +369,7 @@ cudaError_t launch(const AppendParams& p, cudaStream_t stream)
 template <bool BF16, bool E4M3, int D>
 cudaError_t launch_page(const AppendParams& p, cudaStream_t stream)
 {
-    // Up to kFewUnits the units fit the SMs at once as blocks of 256, and a call takes as long as one unit;
-    // above, as long as all units together.
+    // Up to kFewUnits a call takes as long as a unit or two, above as long as all units together.
     //   Sequences that bring a few tokens: a warp per unit, which looks at those rows only.  64 sequences of 12
     //   tokens (pages of 64, 8 heads of 128) took 9.5 us by warps and 11.2 by blocks, of 16 11.8 and 12.0, of 32
     //   17.2 and 18.3; 8 sequences of 1 token 3.2 and 4.2, of 4 the same, of 8 5.5 and 4.0.

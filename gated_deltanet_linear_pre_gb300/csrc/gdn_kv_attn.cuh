@@ -40,7 +40,7 @@ constexpr int kLongRows = 96;
 // the (sequence, kv head) pairs are few (kWholeUnits): 16 sequences of 900 positions, 4 heads, 12.8 us whole and
 // 16.7 cut, 38 of 1000 15.5 and 18.5; but 64 of lengths up to 1000 20.4 and 18.6.
 constexpr int kWholePositions = 512;
-constexpr int kWholeUnits = 152;
+constexpr int kWholeUnits = 152;  // (one for each SM of this GPU)
 constexpr size_t kImageCap = (size_t)2 << 30;  // bytes of images; sequences past it take the step kernel
 
 constexpr uint32_t kAttnTimeout = 1u;  // failure record: a bounded wait expired
