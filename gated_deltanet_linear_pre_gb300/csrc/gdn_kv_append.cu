@@ -335,9 +335,10 @@ __device__ __forceinline__ void rotate_queries(const AppendParams& p, int64_t it
             if (h0 + i < p.hq) __stcs(reinterpret_cast<uint4*>(dst + (h0 + i) * D), raw[i]);
 }
 
-// blocks [0, unit_blocks) store pages, the others rotate queries
+// blocks [0, unit_blocks) store pages, the others rotate queries.  Two blocks an SM at least where a lane holds 8
+// rows: at its own choice of 134 registers one fits (64 sequences of 1024 tokens, pages of 16, 8 heads: 356 us for 203).
 template <bool BF16, bool E4M3, int D, int THREADS, int UNIT, int HELD>
-__global__ void __launch_bounds__(THREADS, UNIT == 32 ? 1 : 1024 / THREADS) kv_append_kernel(AppendParams p, int units, int unit_blocks)
+__global__ void __launch_bounds__(THREADS, UNIT == 32 ? 2 : 1024 / THREADS) kv_append_kernel(AppendParams p, int units, int unit_blocks)
 {
     pdl_wait();
     pdl_launch_dependents();
