@@ -19,7 +19,7 @@
 // floor(T / P) + 2 n_seq slots hold any batch without a prefix sum on the host.
 //
 // Bound and measured.  Large calls by HBM: every value is read once and written once.  8 prompts of 1 to 4096
-// tokens (48 query and 16 kv heads of 128, fp16 to e4m3, pages of 64) take 186 us for 951 MB at the DRAM, 5.1
+// tokens (48 query and 16 kv heads of 128, fp16 to e4m3, pages of 64) take 189 us for 950 MB at the DRAM, 5.0
 // TB/s; the bytes' floor is 150 us at 6.8 TB/s.  (Eight query heads a lane in place of four: 192 to 200 us.)  Small calls by
 // one chain of loads (lengths, table entry, scale, values): a token for each of 64 sequences takes 3.7 us.
 #include "gdn_kv.cuh"

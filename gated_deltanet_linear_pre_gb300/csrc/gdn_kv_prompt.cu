@@ -34,7 +34,7 @@
 // Bound and measured.  By the tensor cores and what feeds them together: a tile of both halves is 2048 cycles of
 // products, reads shared memory at its full 128 bytes a cycle for as long, and has 1024 cycles of exponentials a
 // half.  A 4001-token chunk behind 16500 tokens (32 query heads over 4 of 128, beside three single tokens) takes
-// 745 us, 1.6 PFLOP/s, 83% of the measured dense rate; 2048 tokens from nothing (48 over 16) 60 us, of which a
+// 745 us, 1.6 PFLOP/s, 83% of the measured dense rate; 2048 tokens from nothing (48 over 16) 61 us, of which a
 // CTA's start takes 6 and each of its units 3 between the last tile of one and the first of the next.  Tried and
 // left out: 8 softmax warps of 208 registers (1090 us for the chunk's call, 790), a warp of products for each
 // half (830), waits that spin (829 and more).

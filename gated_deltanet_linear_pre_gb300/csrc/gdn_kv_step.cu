@@ -20,9 +20,10 @@
 // interleaves.  (Codes held in registers from load to use took 98 us where the ring took 72; eight warps a CTA
 // no less than four.)
 //
-// Measured, on cold caches: 64 sequences of 1 to 8192 positions (32 query heads over 4 of 128, e4m3) 66 us for
-// 282 MB, 3 of 131001 (16 over 4 of 64, int8) 43 us for 201 MB: 4.2 and 4.7 TB/s of 6.8.  In between a range's
-// first codes, some 7 us after the launch, and the first CTAs' ends HBM is busy; SMs then end up to 10 us apart.
+// Measured, on cold caches: 64 sequences of 1 to 8192 positions (32 query heads over 4 of 128, e4m3) 63 us for
+// 282 MB, 3 of 131001 (16 over 4 of 64, int8) 43 us for 201 MB: 4.5 and 4.7 TB/s of 6.8.  In between a range's
+// first codes, some 6 us after the launch, and the first CTAs' ends HBM is busy; the last end 12 and 4 us behind
+// the mean.
 // (Long ranges first and short ones after them, for the SMs that end early: 70.0 for 71.0 us, and drafted
 // tokens' 98 for 88, as a late CTA's start costs what the balance brings.)  37 sequences of up to 6 drafted
 // tokens over 4100 positions (48 over 16) 71 us for 299 MB.

@@ -429,8 +429,9 @@ GDN_API size_t gdn_kv_attn_workspace_bytes(const gdn_kv_cache* cache, int32_t n_
  * workspace: device scratch of at least gdn_kv_attn_workspace_bytes() bytes;
  *            contents on entry are ignored.  Calls sharing one must not overlap
  *            on the GPU.
- * Scores, softmax statistics and sums are fp32; the softmax weights are
- * rounded to fp16 for their product with v.  A call may be captured into a CUDA
+ * Scores, softmax statistics and sums are fp32, exponentials the hardware's;
+ * the softmax weights are rounded to fp16 for their product with v (11 bits, in
+ * steps of 2^-31 of the largest weight below).  A call may be captured into a CUDA
  * graph; the lengths in `past` may change between replays.
  */
 GDN_API gdn_status gdn_kv_attn(const gdn_kv_cache* cache, int32_t dtype, int32_t n_seq,
