@@ -118,6 +118,9 @@ def lib():
             L.gdn_kv_attn_check.argtypes = [_p, _p]
             L.gdn_draft_verify.restype = ctypes.c_int
             L.gdn_draft_verify.argtypes = [_i32, _i32, _i32, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p]
+            L.gdn_block_norm.restype = ctypes.c_int
+            L.gdn_block_norm.argtypes = ([_i32] * 4 + [_p, _i64] * 3 + [_i32, ctypes.c_float, _p, _p, ctypes.c_float] +
+                                         [_p] * 3)
             _lib = L
     return _lib
 
@@ -528,3 +531,67 @@ def gdn_draft_verify(p, q, draft, n_draft, u, accepted, next_token, stream=None)
                                 _dense(next_token, "next_token", _I32, per_seq), _stream(stream))
     if st:
         _check("gdn_draft_verify", st)
+
+
+# ---- around the layers: the residual stream between blocks ----
+_GATES = {"none": 0, "linear": 1, "sigmoid": 2, "silu": 3}
+_X_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _here(t, name: str, device):
+    """The tensor is on the current device, whose stream the call goes to."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+
+
+def _rows2(t, name: str, dtype, shape):
+    """Device pointer and row stride of a tensor [T, width] with contiguous rows."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda:
+            st, one = t.stride()
+            if one == 1 or shape[1] == 1:
+                return (t.data_ptr() if t.numel() else None), (st if shape[0] > 1 else shape[1])
+            raise ValueError(f"{name}'s rows must be contiguous")
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape)
+
+
+def gdn_block_norm(x, y, gate, gate_kind: str, scale: float, post_weight, pre_weight, eps: float, x_out, h,
+                   stream=None):
+    """x' = x + scale * act(gate) * norm(y); h = norm(x') (see include/gdn.h).  x [T, width] float16, bfloat16 or
+    float32; y, gate [T, width] 16-bit or None (gate expanded from one row or [1, width]: shared by all tokens);
+    gate_kind "none", "linear", "sigmoid" or "silu"; weights float32 [width] or None; x_out, h or None."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _X_TYPES:
+        raise TypeError("x must be a torch.float16, torch.bfloat16 or torch.float32 tensor [T, width]")
+    act = y if y is not None else h
+    dt = getattr(act, "dtype", None)
+    if dt not in _ACT_TYPES:
+        raise TypeError("y, or h where there is no y, must be torch.float16 or torch.bfloat16")
+    kind = _GATES.get(gate_kind)
+    if kind is None:
+        raise ValueError(f"gate_kind must be one of {sorted(_GATES)}")
+    device = torch.cuda.current_device()
+    shape = T, width = x.shape
+    xp, xs = _rows2(x, "x", x.dtype, shape)
+    yp = gp = None
+    ys = gs = 0
+    if y is not None:
+        yp, ys = _rows2(y, "y", dt, shape)
+    if gate is not None:
+        one = gate.shape == (1, width)
+        gp, gs = _rows2(gate, "gate", dt, (1, width) if one else shape)
+        if one:
+            gs = 0
+    post = None if post_weight is None else _dense(post_weight, "post_weight", _F32, (width,))
+    pre = None if pre_weight is None else _dense(pre_weight, "pre_weight", _F32, (width,))
+    xo = None if x_out is None else _dense(x_out, "x_out", x.dtype, shape)
+    ho = None if h is None else _dense(h, "h", dt, shape)
+    for t, name in ((x, "x"), (y, "y"), (gate, "gate"), (post_weight, "post_weight"), (pre_weight, "pre_weight"),
+                    (x_out, "x_out"), (h, "h")):
+        if t is not None:
+            _here(t, name, device)
+    st = lib().gdn_block_norm(_X_TYPES[x.dtype], _ACT_TYPES[dt], T, width, xp, xs, yp, ys, gp, gs, kind, scale, post,
+                              pre, eps, xo, ho, _stream(stream))
+    if st:
+        _check("gdn_block_norm", st)

@@ -142,6 +142,25 @@ struct VerifyParams {
     int32_t* next;
 };
 
+// the residual stream between two blocks
+struct BlockNormParams {
+    int T, width;
+    int x32, bf16;  // the stream in fp32; activations (and a 16-bit stream) in bf16, else fp16
+    const void* x;
+    int64_t x_stride;
+    const uint16_t* y;  // nullptr: h from x alone
+    int64_t y_stride;
+    const uint16_t* gate;
+    int64_t gate_stride;
+    int gate_kind;
+    float scale, eps;
+    const float* post_weight;
+    const float* pre_weight;
+    void* x_out;   // nullptr: not wanted
+    uint16_t* h;   // nullptr: not wanted
+};
+
+cudaError_t launch_block_norm(const BlockNormParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 size_t kv_attn_workspace_bytes(const KvBatch& b);
 cudaError_t launch_kv_attn(const AttnParams& p, cudaStream_t stream);

@@ -14,10 +14,8 @@ namespace {
 constexpr int kMaxGroup = 64;       // query heads per kv head
 constexpr int kMaxVocab = 1 << 19;  // 2^19 weights of at most 2^43 stay below 2^63
 
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 // bytes from the first element of a strided [T][row] array of 16-bit values to its last
-size_t span16(int32_t T, int64_t stride, size_t row) { return T > 0 ? ((size_t)(T - 1) * (size_t)stride + row) * 2 : 0; }
+size_t span16(int32_t T, int64_t stride, size_t row) { return span(T, stride, row, 2); }
 
 bool known_dim(const gdn_kv_cache* c) { return c->head_dim == 64 || c->head_dim == 128; }
 
@@ -57,13 +55,6 @@ gdn_status check_kv_batch(const gdn_kv_cache* c, int32_t dtype, int32_t n_seq, i
     if (n_seq > 0 && !past) return fail(GDN_ERR_INVALID_ARG, "past is NULL");
     if (n_seq > 0 && max_pages > 0 && !table) return fail(GDN_ERR_INVALID_ARG, "page_table is NULL");
     if (!aligned4(past) || !aligned4(table)) return fail(GDN_ERR_ALIGNMENT, "past or page_table not 4-byte aligned");
-    return GDN_OK;
-}
-
-gdn_status check_stride(const char* name, int64_t stride, size_t row)
-{
-    if (stride < (int64_t)row) return fail(GDN_ERR_INVALID_ARG, "%s_stride=%lld is shorter than a row of %zu", name, (long long)stride, row);
-    if (stride % 8) return fail(GDN_ERR_ALIGNMENT, "%s_stride=%lld is not a multiple of 8", name, (long long)stride);
     return GDN_OK;
 }
 

@@ -325,8 +325,9 @@ GDN_API gdn_status gdn_step(const gdn_dims* dims, int32_t n_seq, const uint16_t*
  * check of drafted tokens.  The pages have no counterpart to these.
  * ------------------------------------------------------------------------ */
 
-/* activation type of q, k, v and the attention's output */
-typedef enum gdn_dtype { GDN_FP16 = 0, GDN_BF16 = 1 } gdn_dtype;
+/* activation type of q, k, v and the attention's output; fp32 is for the
+ * residual stream of gdn_block_norm alone */
+typedef enum gdn_dtype { GDN_FP16 = 0, GDN_BF16 = 1, GDN_FP32 = 2 } gdn_dtype;
 
 /* what a cache byte holds: a two's complement integer in [-127, 127], or a
  * 4-bit-exponent, 3-bit-mantissa float (largest value 448, no infinities) */
@@ -479,6 +480,46 @@ GDN_API gdn_status gdn_draft_verify(int32_t n_seq, int32_t max_draft, int32_t vo
                                     int64_t p_stride, const float* q, int64_t q_stride,
                                     const int32_t* draft, const int32_t* n_draft, const float* u,
                                     int32_t* accepted, int32_t* next, struct CUstream_st* stream);
+
+/* ------------------------------------------------------------------------
+ * Around the layers, for a server of many requests: the residual stream
+ * between blocks.  The pages have no counterpart.
+ * ------------------------------------------------------------------------ */
+
+/* what a block's output is multiplied with: nothing, the gate as it is, its
+ * sigmoid, or gate * sigmoid(gate) */
+typedef enum gdn_gate { GDN_GATE_NONE = 0, GDN_GATE_LINEAR = 1, GDN_GATE_SIGMOID = 2, GDN_GATE_SILU = 3 } gdn_gate;
+
+/*
+ * gdn_block_norm -- a block's output joins the residual stream, which is
+ * normalised for the next block:
+ *   u  = y, or y / sqrt(mean(y^2) + eps) * post_weight where that is given
+ *   x' = x + scale * act(gate) * u          (act(gate) = 1 for GDN_GATE_NONE)
+ *   h  = x' / sqrt(mean(x'^2) + eps) * pre_weight
+ * token by token over `width` channels, in fp32 throughout: x' and h are each
+ * rounded once, h from x' before its rounding.
+ *
+ * In:  x       [T][width] of x_dtype: `dtype`, or GDN_FP32
+ *      y       [T][width] of `dtype` (GDN_FP16 or GDN_BF16), or NULL: x' = x
+ *              (in front of the first block; gate, post_weight and x_out NULL)
+ *      gate    [T][width] of `dtype`; gate_stride 0: one row for all tokens;
+ *              NULL with GDN_GATE_NONE
+ *      post_weight, pre_weight  fp32 [width]; post_weight NULL: y is taken as
+ *              it is; pre_weight NULL with h NULL
+ *      Tokens are x_stride, y_stride, gate_stride elements apart (multiples of
+ *      8; y may be a slice of a wider row).
+ * Out: x_out   [T][width] dense, of x_dtype; NULL: x' is not wanted (behind the
+ *              last block).  May be x itself where x_stride == width; overlaps
+ *              nothing else.
+ *      h       [T][width] dense, of `dtype`, or NULL: not wanted (not both)
+ * width: a multiple of 8 up to 16384.  eps > 0.  Squares are summed in fp32, so
+ * rows with values beyond 1e19 have a norm of infinity.
+ */
+GDN_API gdn_status gdn_block_norm(int32_t x_dtype, int32_t dtype, int32_t total_tokens, int32_t width,
+                                  const void* x, int64_t x_stride, const uint16_t* y, int64_t y_stride,
+                                  const uint16_t* gate, int64_t gate_stride, int32_t gate_kind,
+                                  float scale, const float* post_weight, const float* pre_weight,
+                                  float eps, void* x_out, uint16_t* h, struct CUstream_st* stream);
 
 #ifdef __cplusplus
 }
