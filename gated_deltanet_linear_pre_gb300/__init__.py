@@ -7,6 +7,7 @@ its thin ctypes binding under the ABI's names:
     gdn_pre, gdn_scan, gdn_scan_fast, gdn_scan_noalloc, gdn_post, gdn_layer, gdn_layer_fast, gdn_step,
     gdn_scan_workspace_bytes, gdn_layer_workspace_bytes, dims, GdnError
     gdn_kv_append, gdn_kv_attn, gdn_kv_attn_check, gdn_kv_attn_workspace_bytes, kv_cache, gdn_draft_verify
+    gdn_kv_remap, gdn_kv_remap_workspace_bytes, gdn_kv_compact, gdn_kv_compact_workspace_bytes, gdn_kv_copy, kv_caches
     gdn_block_norm
 
 ``inputs`` draws the seeded synthetic workloads.  Nothing here computes the
@@ -15,6 +16,7 @@ method on the CPU.
 _BINDING = ("gdn_pre", "gdn_scan", "gdn_scan_fast", "gdn_layer_fast", "gdn_scan_noalloc", "gdn_post", "gdn_layer", "gdn_step", "gdn_scan_check", "gdn_layer_check", "gdn_scan_noalloc_check", "gdn_last_async_error",
             "gdn_scan_selftest_timeout", "gdn_scan_selftest_one_taker", "gdn_scan_selftest_withhold_flag", "gdn_layer_selftest_stages", "gdn_scan_workspace_bytes",
             "gdn_kv_append", "gdn_kv_attn", "gdn_kv_attn_check", "gdn_kv_attn_workspace_bytes", "gdn_kv_cache", "kv_cache", "gdn_draft_verify",
+            "gdn_kv_remap", "gdn_kv_remap_workspace_bytes", "gdn_kv_compact", "gdn_kv_compact_workspace_bytes", "gdn_kv_copy", "kv_caches",
             "gdn_block_norm",
             "gdn_layer_workspace_bytes", "dims", "gdn_dims", "GdnError", "lib", "library_path")
 

@@ -118,6 +118,13 @@ def lib():
             L.gdn_kv_attn_check.argtypes = [_p, _p]
             L.gdn_draft_verify.restype = ctypes.c_int
             L.gdn_draft_verify.argtypes = [_i32, _i32, _i32, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p]
+            L.gdn_kv_remap_workspace_bytes.restype = L.gdn_kv_compact_workspace_bytes.restype = _sz
+            L.gdn_kv_remap_workspace_bytes.argtypes = [_i32] * 3
+            L.gdn_kv_compact_workspace_bytes.argtypes = [_i32]
+            L.gdn_kv_remap.restype = L.gdn_kv_compact.restype = L.gdn_kv_copy.restype = ctypes.c_int
+            L.gdn_kv_remap.argtypes = [_i32] * 4 + [_p, _i64, _i32, _p, _p, _p, _p, _i64] + [_p] * 4 + [_sz, _p]
+            L.gdn_kv_compact.argtypes = [_i32] * 3 + [_p, _i64, _p, _i64] + [_p] * 4 + [_sz, _p]
+            L.gdn_kv_copy.argtypes = [K, _i32, _i32, _p, _p, _p]
             L.gdn_block_norm.restype = ctypes.c_int
             L.gdn_block_norm.argtypes = ([_i32] * 4 + [_p, _i64] * 3 + [_i32, ctypes.c_float, _p, _p, ctypes.c_float] +
                                          [_p] * 3)
@@ -533,15 +540,132 @@ def gdn_draft_verify(p, q, draft, n_draft, u, accepted, next_token, stream=None)
         _check("gdn_draft_verify", st)
 
 
-# ---- around the layers: the residual stream between blocks ----
-_GATES = {"none": 0, "linear": 1, "sigmoid": 2, "silu": 3}
-_X_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-
-
+# ---- the pages that a batch's sequences hold ----
 def _here(t, name: str, device):
     """The tensor is on the current device, whose stream the call goes to."""
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+
+
+def _table(t, name: str):
+    """Device pointer and row stride of an int32 table [rows, max_pages] with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.dim() != 2 or not t.is_cuda:
+        raise TypeError(f"{name} must be an int32 CUDA tensor [rows, max_pages]")
+    rows, width = t.shape
+    stride, one = t.stride()
+    if one != 1 and width > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return (t.data_ptr() if rows and width else None), (stride if rows > 1 else width)
+
+
+def _scratch(t, device):
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or t.dtype is not _U8 or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, "workspace", _U8, None)
+        raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
+    _here(t, "workspace", device)
+    return t.data_ptr(), t.numel()
+
+
+def gdn_kv_remap_workspace_bytes(n_pages: int, n_rows: int, max_pages: int) -> int:
+    return int(lib().gdn_kv_remap_workspace_bytes(n_pages, n_rows, max_pages))
+
+
+def gdn_kv_remap(page_table, page_tokens: int, n_pages: int, parent, keep, need, table_out, copy_from, copy_to, info,
+                 workspace, stream=None):
+    """The next step's page table: row r keeps the first keep[r] tokens of row parent[r] of page_table [n_old,
+    max_pages] and gets room for need[r].  Writes table_out [n_rows, max_pages], the pages that gdn_kv_copy is to
+    copy (copy_from, copy_to [n_rows], -1 where there is none) and info [2]: pages named, pages missing."""
+    device = torch.cuda.current_device()
+    tp, ts = _table(page_table, "page_table")
+    op, os_ = _table(table_out, "table_out")
+    n_old, width = page_table.shape
+    n = table_out.shape[0]
+    if table_out.shape[1] != width:
+        raise ValueError(f"table_out has {table_out.shape[1]} entries a row, page_table {width}")
+    per_row = (n,)
+    args = [_dense(t, name, _I32, shape) for t, name, shape in (
+        (parent, "parent", per_row), (keep, "keep", per_row), (need, "need", per_row), (copy_from, "copy_from", per_row),
+        (copy_to, "copy_to", per_row), (info, "info", (2,)))]
+    wp, wb = _scratch(workspace, device)
+    for t, name in ((page_table, "page_table"), (parent, "parent"), (keep, "keep"), (need, "need"),
+                    (table_out, "table_out"), (copy_from, "copy_from"), (copy_to, "copy_to"), (info, "info")):
+        _here(t, name, device)
+    st = lib().gdn_kv_remap(page_tokens, n_pages, width, n_old, tp, ts, n, *args[:3], op, os_, *args[3:], wp, wb,
+                            _stream(stream))
+    if st:
+        _check("gdn_kv_remap", st)
+
+
+def gdn_kv_compact_workspace_bytes(n_pages: int) -> int:
+    return int(lib().gdn_kv_compact_workspace_bytes(n_pages))
+
+
+def gdn_kv_compact(page_table, n_pages: int, table_out, copy_from, copy_to, info, workspace, stream=None):
+    """Rename pages so that those in use are the pool's first: writes table_out (page_table itself will do), the
+    moves for gdn_kv_copy (copy_from, copy_to [n_pages // 2], -1 behind them) and info [2]: pages in use, moves."""
+    device = torch.cuda.current_device()
+    tp, ts = _table(page_table, "page_table")
+    op, os_ = _table(table_out, "table_out")
+    n, width = shape = page_table.shape
+    if table_out.shape != shape:
+        raise ValueError(f"table_out has shape {tuple(table_out.shape)}, expected {tuple(shape)}")
+    lists = (n_pages // 2,)
+    a, b = _dense(copy_from, "copy_from", _I32, lists), _dense(copy_to, "copy_to", _I32, lists)
+    ip = _dense(info, "info", _I32, (2,))
+    wp, wb = _scratch(workspace, device)
+    for t, name in ((page_table, "page_table"), (table_out, "table_out"), (copy_from, "copy_from"),
+                    (copy_to, "copy_to"), (info, "info")):
+        _here(t, name, device)
+    st = lib().gdn_kv_compact(n_pages, width, n, tp, ts, op, os_, a, b, ip, wp, wb, _stream(stream))
+    if st:
+        _check("gdn_kv_compact", st)
+
+
+class _KvCaches:
+    """Caches of the layers that share a page table, as gdn_kv_copy takes them."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        for c in caches:
+            if not isinstance(c, gdn_kv_cache) or not hasattr(c, "tensors"):
+                raise TypeError("each cache must come from kv_cache()")
+        self.caches = caches           # keeps the tensors alive
+        self.array = (gdn_kv_cache * len(caches))(*caches)
+        self.device = caches[0].tensors[0].get_device() if caches else None
+        for c in caches:
+            for t in c.tensors:
+                _here(t, "a cache's tensor", self.device)
+
+
+def kv_caches(caches) -> _KvCaches:
+    """Several layers' caches (from kv_cache), held for gdn_kv_copy."""
+    return _KvCaches(caches)
+
+
+def gdn_kv_copy(caches, copy_from, copy_to, stream=None):
+    """Copy pages copy_from[i] to copy_to[i] (int32 [n]; pairs with an index outside the pool are passed over)
+    within each of `caches`: from kv_caches(), one kv_cache() or a sequence of them."""
+    if not isinstance(caches, _KvCaches):
+        caches = _KvCaches([caches] if isinstance(caches, gdn_kv_cache) else caches)
+    device = torch.cuda.current_device()
+    if caches.device is not None and caches.device != device:
+        raise ValueError(f"the caches are on cuda:{caches.device}, the current device is cuda:{device}")
+    if not isinstance(copy_from, torch.Tensor) or copy_from.dim() != 1:
+        raise TypeError("copy_from must be an int32 CUDA tensor [n]")
+    shape = copy_from.shape
+    a, b = _dense(copy_from, "copy_from", _I32, shape), _dense(copy_to, "copy_to", _I32, shape)
+    _here(copy_from, "copy_from", device)
+    _here(copy_to, "copy_to", device)
+    st = lib().gdn_kv_copy(caches.array, len(caches.caches), shape[0], a, b, _stream(stream))
+    if st:
+        _check("gdn_kv_copy", st)
+
+
+# ---- around the layers: the residual stream between blocks ----
+_GATES = {"none": 0, "linear": 1, "sigmoid": 2, "silu": 3}
+_X_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
 def _rows2(t, name: str, dtype, shape):

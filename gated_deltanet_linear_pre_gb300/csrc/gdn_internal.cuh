@@ -160,6 +160,56 @@ struct BlockNormParams {
     uint16_t* h;   // nullptr: not wanted
 };
 
+// the next step's page table from the last one's
+struct RemapParams {
+    int n_old, n_rows, max_pages, page_shift, n_pages;
+    const int32_t* table;
+    int64_t table_stride, out_stride;
+    const int32_t* parent;
+    const int32_t* keep;
+    const int32_t* need;
+    int32_t* table_out;
+    int32_t* copy_from;
+    int32_t* copy_to;
+    int32_t* info;
+    // workspace: the free pages' number; per page, who names it; the free pages; per row, its place among them
+    int32_t* header;
+    int32_t* owner;
+    int32_t* free_list;
+    int32_t* first;
+};
+
+// pages renamed to the front of the pool
+struct CompactParams {
+    int n_rows, max_pages, n_pages;
+    const int32_t* table;
+    int64_t table_stride, out_stride;
+    int32_t* table_out;
+    int32_t* copy_from;  // [n_pages / 2]
+    int32_t* copy_to;
+    int32_t* info;
+    int32_t* name;  // workspace: per page, its new number
+};
+
+constexpr int kCopyCaches = 64;  // caches of one launch
+
+struct CopyParams {
+    struct Cache {
+        uint8_t* k;
+        uint8_t* v;
+        uint32_t* k_scale;
+        uint32_t* v_scale;
+    };
+    int n_caches, n, n_pages, heads;
+    size_t page_bytes;  // of k, and of v
+    const int32_t* from;
+    const int32_t* to;
+    Cache cache[kCopyCaches];
+};
+
+cudaError_t launch_kv_remap(const RemapParams& p, cudaStream_t stream);
+cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t stream);
+cudaError_t launch_kv_copy(const CopyParams& p, cudaStream_t stream);
 cudaError_t launch_block_norm(const BlockNormParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 size_t kv_attn_workspace_bytes(const KvBatch& b);

@@ -481,6 +481,91 @@ GDN_API gdn_status gdn_draft_verify(int32_t n_seq, int32_t max_draft, int32_t vo
                                     const int32_t* draft, const int32_t* n_draft, const float* u,
                                     int32_t* accepted, int32_t* next, struct CUstream_st* stream);
 
+/*
+ * gdn_kv_remap -- the page table of a batch's next step from that of its last:
+ * rows forked, cut, dropped and grown in one call, with their pages shared
+ * where they can be.  Row r of the new table
+ *   keeps   the first keep[r] tokens of row parent[r] of the old table (r itself
+ *           to go on; another's to fork it; keep[r] = 0 or a parent outside
+ *           [0, n_old): nothing), that is its first ceil(keep[r] / page_tokens)
+ *           entries;
+ *   gets    room for need[r] tokens: new pages up to
+ *           ceil(need[r] / page_tokens) entries (never fewer than it keeps).
+ * Pages that no row of the new table keeps are free, whoever had them.  A row
+ * with need[r] > keep[r] whose kept tokens end inside a page will write into
+ * that page.  Where another row keeps the page too it takes a new page in its
+ * place and the pair is listed for gdn_kv_copy; of rows that all write into the
+ * page the lowest keeps it.  (A row that keeps a page without writing into it
+ * never loses it.)  New pages go to the rows in order, a row's copy first, then
+ * its other entries in order, and are the free pages in order.
+ * If there are too few, the last to ask get none: their entries are -1 (what
+ * is appended there is not stored), and info says how many.
+ *
+ * In:  page_table  int32 [n_old] rows of max_pages entries, page_table_stride
+ *                  apart; an entry outside [0, n_pages) names no page and is
+ *                  kept as -1 (nothing is copied for it)
+ *      parent, keep, need  int32 [n_rows]; lengths below 0 count as 0, and
+ *                  past the row's end as its end
+ * Out: table_out   int32 [n_rows] rows of max_pages entries, table_out_stride
+ *                  apart, -1 behind what a row has; overlaps no input
+ *      copy_from, copy_to  int32 [n_rows]: the page that row r's last kept
+ *                  page is to be copied from and to, or -1.  A page that is
+ *                  copied from is never copied to, so gdn_kv_copy may follow
+ *                  at once, and the append behind it.
+ *      info        int32 [2]: pages that the new table names, and pages that
+ *                  were wanted and not there
+ * Nothing is kept between calls: what a row does not name is free.  To hold
+ * pages for later (a shared prompt, say) keep a row for them.
+ * page_tokens as in gdn_kv_cache; n_pages up to 2^28; n_rows * max_pages and
+ * max_pages * page_tokens up to 2^30.  The int32 arrays need 4-byte alignment
+ * only.  workspace: at least gdn_kv_remap_workspace_bytes() bytes (0 for a
+ * shape that is refused); contents on entry are ignored, calls sharing one must
+ * not overlap on the GPU.  May be captured into a CUDA graph.
+ */
+GDN_API size_t gdn_kv_remap_workspace_bytes(int32_t n_pages, int32_t n_rows, int32_t max_pages);
+GDN_API gdn_status gdn_kv_remap(int32_t page_tokens, int32_t n_pages, int32_t max_pages, int32_t n_old,
+                                const int32_t* page_table, int64_t page_table_stride, int32_t n_rows,
+                                const int32_t* parent, const int32_t* keep, const int32_t* need,
+                                int32_t* table_out, int64_t table_out_stride, int32_t* copy_from,
+                                int32_t* copy_to, int32_t* info, void* workspace, size_t workspace_bytes,
+                                struct CUstream_st* stream);
+
+/*
+ * gdn_kv_compact -- renames pages so that those in use are the pool's first
+ * ones: with U pages named by the table, those at or behind U move, in order, to
+ * the free ones in front of U, in order.
+ *
+ * In:  page_table  int32 [n_rows] rows of max_pages entries, page_table_stride
+ *                  apart; entries outside [0, n_pages) name no page
+ * Out: table_out   the same with the new names, -1 where an entry names no
+ *                  page; table_out_stride apart; may be page_table itself with
+ *                  the same stride, else overlaps it nowhere
+ *      copy_from, copy_to  int32 [n_pages / 2]: the moves, -1 behind them.  No
+ *                  page is in both lists: gdn_kv_copy may follow at once.
+ *      info        int32 [2]: U, and the number of moves
+ * Limits, alignment, workspace and capture as for gdn_kv_remap.
+ */
+GDN_API size_t gdn_kv_compact_workspace_bytes(int32_t n_pages);
+GDN_API gdn_status gdn_kv_compact(int32_t n_pages, int32_t max_pages, int32_t n_rows, const int32_t* page_table,
+                                  int64_t page_table_stride, int32_t* table_out, int64_t table_out_stride,
+                                  int32_t* copy_from, int32_t* copy_to, int32_t* info, void* workspace,
+                                  size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * gdn_kv_copy -- copies pages (codes and scales, as bits) within the caches of
+ * all layers that share a page table: page copy_from[i] to copy_to[i] for
+ * i < n, in each cache.  A pair with an index outside [0, n_pages), or twice
+ * the same, is passed over.  A page may be copied from more than once; a page
+ * that is copied to is in the lists once (twice, or as a source too: its
+ * contents are then some mixture of the pages named).
+ *
+ * In:  caches      host array of n_caches caches with the same heads, head_dim,
+ *                  page_tokens, n_pages and format, none overlapping another
+ *      copy_from, copy_to  int32 [n] (device, 4-byte aligned)
+ */
+GDN_API gdn_status gdn_kv_copy(const gdn_kv_cache* caches, int32_t n_caches, int32_t n, const int32_t* copy_from,
+                               const int32_t* copy_to, struct CUstream_st* stream);
+
 /* ------------------------------------------------------------------------
  * Around the layers, for a server of many requests: the residual stream
  * between blocks.  The pages have no counterpart.
