@@ -128,6 +128,11 @@ def lib():
             L.gdn_block_norm.restype = ctypes.c_int
             L.gdn_block_norm.argtypes = ([_i32] * 4 + [_p, _i64] * 3 + [_i32, ctypes.c_float, _p, _p, ctypes.c_float] +
                                          [_p] * 3)
+            L.gdn_adapter_workspace_bytes.restype = _sz
+            L.gdn_adapter_workspace_bytes.argtypes = [_i32] * 4
+            L.gdn_adapter_add.restype = ctypes.c_int
+            L.gdn_adapter_add.argtypes = ([_i32] * 3 + [_p, _p, _i32, _i32, _p, _p, _p, _p, _i32, _p, _i64, _i32, _p, _i64, _p,
+                                                        _i64, _p, _sz, _p])
             _lib = L
     return _lib
 
@@ -663,7 +668,7 @@ def gdn_kv_copy(caches, copy_from, copy_to, stream=None):
         _check("gdn_kv_copy", st)
 
 
-# ---- around the layers: the residual stream between blocks ----
+# ---- around the layers: the residual stream between blocks, adapters beside the projections ----
 _GATES = {"none": 0, "linear": 1, "sigmoid": 2, "silu": 3}
 _X_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
@@ -719,3 +724,35 @@ def gdn_block_norm(x, y, gate, gate_kind: str, scale: float, post_weight, pre_we
                               pre, eps, xo, ho, _stream(stream))
     if st:
         _check("gdn_block_norm", st)
+
+
+def gdn_adapter_workspace_bytes(n_seq: int, total_tokens: int, rank: int, d_in: int) -> int:
+    return int(lib().gdn_adapter_workspace_bytes(n_seq, total_tokens, rank, d_in))
+
+
+def gdn_adapter_add(cu_seqlens, total_tokens, ids, down, up, ranks, scales, x, y, y_out, workspace, stream=None):
+    """y_out = y + scales[a] * (x down[a]^T) up[a] with a = ids[s], the adapter of each token's sequence (outside
+    the adapters: none).  down [n, rank, d_in], up [n, rank, d_out], x [T, d_in], y [T, d_out] of one 16-bit type,
+    ids int32 [n_seq], ranks int32 [n] or None, scales float32 [n]; y_out may be y."""
+    device = torch.cuda.current_device()
+    T, n_seq = int(total_tokens), ids.shape[0]
+    dt = down.dtype
+    if dt not in _ACT_TYPES or down.dim() != 3 or up.dim() != 3:
+        raise TypeError("down and up must be torch.float16 or torch.bfloat16 tensors [n, rank, d_in] and [n, rank, d_out]")
+    n, rank, d_in = down.shape
+    d_out = up.shape[2]
+    dp, upp = _dense(down, "down", dt, (n, rank, d_in)), _dense(up, "up", dt, (n, rank, d_out))
+    xp, xs = _rows2(x, "x", dt, (T, d_in))
+    yp, ys = _rows2(y, "y", dt, (T, d_out))
+    op, os_ = _rows2(y_out, "y_out", dt, (T, d_out))
+    wp, wb = _scratch(workspace, device)
+    rp = None if ranks is None else _dense(ranks, "ranks", _I32, (n,))
+    for t, name in ((cu_seqlens, "cu_seqlens"), (ids, "ids"), (down, "down"), (up, "up"), (ranks, "ranks"), (scales, "scales"),
+                    (x, "x"), (y, "y"), (y_out, "y_out")):
+        if t is not None:
+            _here(t, name, device)
+    st = lib().gdn_adapter_add(_ACT_TYPES[dt], n_seq, T, _dense(cu_seqlens, "cu_seqlens", _I32, (n_seq + 1,)),
+                               _dense(ids, "ids", _I32, (n_seq,)), n, rank, rp, dp, upp, _dense(scales, "scales", _F32, (n,)),
+                               d_in, xp, xs, d_out, yp, ys, op, os_, wp, wb, _stream(stream))
+    if st:
+        _check("gdn_adapter_add", st)

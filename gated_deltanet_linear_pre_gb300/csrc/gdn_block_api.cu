@@ -8,6 +8,13 @@
 
 using namespace gdn::host;
 
+namespace {
+
+bool known_rank(int32_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
+bool known_width(int32_t d) { return d >= 8 && d <= 65536 && d % 8 == 0; }
+
+}  // namespace
+
 extern "C" {
 
 gdn_status gdn_block_norm(int32_t x_dtype, int32_t dtype, int32_t T, int32_t width, const void* x, int64_t x_stride,
@@ -49,6 +56,52 @@ gdn_status gdn_block_norm(int32_t x_dtype, int32_t dtype, int32_t T, int32_t wid
     p.post_weight = post_weight; p.pre_weight = pre_weight; p.x_out = x_out; p.h = h;
     cudaError_t e = gdn::launch_block_norm(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_block_norm launch");
+}
+
+size_t gdn_adapter_workspace_bytes(int32_t n_seq, int32_t T, int32_t rank, int32_t d_in)
+{
+    if (n_seq < 0 || n_seq > 65535 || T < 0 || (n_seq == 0 && T > 0) || !known_rank(rank) || !known_width(d_in)) return 0;
+    return T > 0 ? align256(gdn::adapter_workspace_bytes(n_seq, T, rank, d_in)) : 0;
+}
+
+gdn_status gdn_adapter_add(int32_t dtype, int32_t n_seq, int32_t T, const int32_t* cu_seqlens, const int32_t* ids, int32_t n_adapters,
+                           int32_t rank, const int32_t* ranks, const uint16_t* down, const uint16_t* up, const float* scales, int32_t d_in,
+                           const uint16_t* x, int64_t x_stride, int32_t d_out, const uint16_t* y, int64_t y_stride, uint16_t* y_out,
+                           int64_t y_out_stride, void* workspace, size_t workspace_bytes, struct CUstream_st* stream)
+{
+    gdn_status st;
+    if (dtype != GDN_FP16 && dtype != GDN_BF16) return fail(GDN_ERR_INVALID_ARG, "unknown activation type %d", dtype);
+    if ((st = check_batch(n_seq, T, cu_seqlens)) != GDN_OK) return st;
+    if (n_adapters < 0) return fail(GDN_ERR_INVALID_ARG, "negative n_adapters");
+    if (!known_rank(rank)) return fail(GDN_ERR_UNSUPPORTED, "rank=%d must be a multiple of 8 up to 128", rank);
+    if (!known_width(d_in) || !known_width(d_out)) return fail(GDN_ERR_UNSUPPORTED, "d_in=%d and d_out=%d must be multiples of 8 up to 65536", d_in, d_out);
+    if ((st = check_stride("x", x_stride, d_in)) != GDN_OK) return st;
+    if ((st = check_stride("y", y_stride, d_out)) != GDN_OK) return st;
+    if ((st = check_stride("y_out", y_out_stride, d_out)) != GDN_OK) return st;
+    if (T == 0) return GDN_OK;  // empty arrays may be NULL
+    const size_t n = (size_t)n_adapters, need = gdn_adapter_workspace_bytes(n_seq, T, rank, d_in);
+    const Buf lists[] = {{ids, (size_t)n_seq * 4, "ids"}, {ranks, ranks ? n * 4 : 0, "ranks"}, {scales, n * 4, "scales"}};
+    for (const Buf& b : lists) {
+        if (b.bytes && !b.p) return fail(GDN_ERR_INVALID_ARG, "%s is NULL", b.name);
+        if (b.bytes && !aligned4(b.p)) return fail(GDN_ERR_ALIGNMENT, "%s is not 4-byte aligned", b.name);
+    }
+    const Buf y_in{y, span(T, y_stride, d_out, 2), "y"}, out{y_out, span(T, y_out_stride, d_out, 2), "y_out"}, ws{workspace, need, "workspace"};
+    const Buf arrays[] = {{x, span(T, x_stride, d_in, 2), "x"}, {down, n * rank * d_in * 2, "down"}, {up, n * rank * d_out * 2, "up"}, y_in, out};
+    if ((st = check_bufs(arrays, 5)) != GDN_OK) return st;
+    if (workspace_bytes < need || !workspace) return fail(GDN_ERR_WORKSPACE, "adapter workspace %zu bytes, need %zu", workspace_bytes, need);
+    if ((st = check_bufs(&ws, 1)) != GDN_OK) return st;
+    const Buf outs[] = {out, ws}, ins[] = {arrays[0], arrays[1], arrays[2], lists[0], lists[1], lists[2], y_in};
+    // y_out may be y itself: a block has read what it writes
+    const bool in_place = y_out == y && y_out_stride == y_stride;
+    if ((st = check_disjoint(outs, 2, ins, in_place ? 6 : 7)) != GDN_OK) return st;
+    if (in_place && overlap(ws, y_in)) return fail(GDN_ERR_INVALID_ARG, "workspace overlaps y");
+    gdn::AdapterParams p{};
+    p.n_seq = n_seq; p.T = T; p.n_adapters = n_adapters; p.rank = rank; p.d_in = d_in; p.d_out = d_out; p.bf16 = dtype == GDN_BF16;
+    p.cu_seqlens = cu_seqlens; p.ids = ids; p.ranks = ranks; p.down = down; p.up = up; p.scales = scales;
+    p.x = x; p.y = y; p.y_out = y_out; p.x_stride = x_stride; p.y_stride = y_stride; p.out_stride = y_out_stride;
+    p.h = static_cast<float*>(workspace);
+    cudaError_t e = gdn::launch_adapter(p, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_adapter_add launch");
 }
 
 }  // extern "C"

@@ -210,6 +210,25 @@ struct CopyParams {
 cudaError_t launch_kv_remap(const RemapParams& p, cudaStream_t stream);
 cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t stream);
 cudaError_t launch_kv_copy(const CopyParams& p, cudaStream_t stream);
+// the sequences' adapters added to a shared projection's output
+struct AdapterParams {
+    int n_seq, T, n_adapters, rank, d_in, d_out, bf16;
+    const int32_t* cu_seqlens;
+    const int32_t* ids;
+    const int32_t* ranks;   // nullptr: all `rank`
+    const uint16_t* down;   // [n_adapters][rank][d_in]
+    const uint16_t* up;     // [n_adapters][rank][d_out]
+    const float* scales;
+    const uint16_t* x;
+    const uint16_t* y;
+    uint16_t* y_out;
+    int64_t x_stride, y_stride, out_stride;
+    float* h;               // workspace: [splits][T][rank]
+    int split_k, splits, split_o;  // set by launch_adapter
+};
+
+size_t adapter_workspace_bytes(int n_seq, int T, int rank, int d_in);
+cudaError_t launch_adapter(AdapterParams p, cudaStream_t stream);
 cudaError_t launch_block_norm(const BlockNormParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 size_t kv_attn_workspace_bytes(const KvBatch& b);

@@ -568,7 +568,8 @@ GDN_API gdn_status gdn_kv_copy(const gdn_kv_cache* caches, int32_t n_caches, int
 
 /* ------------------------------------------------------------------------
  * Around the layers, for a server of many requests: the residual stream
- * between blocks.  The pages have no counterpart.
+ * between blocks, and adapters beside the projections.  The pages have no
+ * counterpart to these.
  * ------------------------------------------------------------------------ */
 
 /* what a block's output is multiplied with: nothing, the gate as it is, its
@@ -605,6 +606,42 @@ GDN_API gdn_status gdn_block_norm(int32_t x_dtype, int32_t dtype, int32_t total_
                                   const uint16_t* gate, int64_t gate_stride, int32_t gate_kind,
                                   float scale, const float* post_weight, const float* pre_weight,
                                   float eps, void* x_out, uint16_t* h, struct CUstream_st* stream);
+
+/*
+ * gdn_adapter_add -- the low-rank adapter of each sequence added to the output
+ * of a projection that all share: for token t of sequence s, a = ids[s],
+ *   h     = down[a] x[t]                      (ranks[a] values)
+ *   y_out[t] = y[t] + scales[a] * up[a]^T h
+ * A sequence whose id is outside [0, n_adapters), or whose adapter's rank is 0,
+ * has none: y_out = y.
+ *
+ * In:  ids     int32 [n_seq] (device)
+ *      ranks   int32 [n_adapters], clamped to [0, rank], or NULL: all `rank`.
+ *              What down and up hold behind an adapter's rank is not read.
+ *      down    [n_adapters][rank][d_in], up [n_adapters][rank][d_out], of `dtype`
+ *      scales  fp32 [n_adapters]
+ *      x       [T][d_in], y [T][d_out] of `dtype` (GDN_FP16 or GDN_BF16); tokens
+ *              are x_stride, y_stride elements apart (multiples of 8: y may be
+ *              the q slice of a packed projection, say)
+ * Out: y_out   [T][d_out] of `dtype`, y_out_stride apart; may be y itself with
+ *              the same stride, else overlaps no input
+ * rank: a multiple of 8 up to 128; d_in, d_out: multiples of 8 up to 65536.
+ * ids and ranks need 4-byte alignment only.  Sums are fp32; h enters its
+ * product in two pieces of the weights' type (16 bits or more), and y_out is
+ * rounded once.  Values of x and of the weights that are not finite reach the
+ * tokens, and the channels, that their products reach.
+ * workspace: device scratch of at least gdn_adapter_workspace_bytes() bytes (0
+ * for a shape that is refused, and for no tokens); contents on entry are
+ * ignored, calls sharing one must not overlap on the GPU.  May be captured into
+ * a CUDA graph; ids and lengths may change between replays.
+ */
+GDN_API size_t gdn_adapter_workspace_bytes(int32_t n_seq, int32_t total_tokens, int32_t rank, int32_t d_in);
+GDN_API gdn_status gdn_adapter_add(int32_t dtype, int32_t n_seq, int32_t total_tokens, const int32_t* cu_seqlens,
+                                   const int32_t* ids, int32_t n_adapters, int32_t rank, const int32_t* ranks,
+                                   const uint16_t* down, const uint16_t* up, const float* scales, int32_t d_in,
+                                   const uint16_t* x, int64_t x_stride, int32_t d_out, const uint16_t* y,
+                                   int64_t y_stride, uint16_t* y_out, int64_t y_out_stride, void* workspace,
+                                   size_t workspace_bytes, struct CUstream_st* stream);
 
 #ifdef __cplusplus
 }

@@ -50,3 +50,38 @@ def test_binding_refusals():
         N.gdn_block_norm(x, x.float(), None, "none", 1.0, None, None, 1e-6, x, None)
     with pytest.raises(ValueError):
         N.gdn_block_norm(x, x, None, "tanh", 1.0, None, None, 1e-6, x, None)
+
+
+def adapter(L, **over):
+    a = dict(dtype=1, n=3, T=100, cu=F, ids=2 * F, n_adapters=4, rank=16, ranks=3 * F, down=4 * F, up=5 * F, scales=6 * F, d_in=256, x=7 * F, xs=256,
+             d_out=512, y=8 * F, ys=1024, out=9 * F, os=512, ws=10 * F, wb=None)
+    a.update(over)
+    if a["wb"] is None:
+        a["wb"] = L.gdn_adapter_workspace_bytes(a["n"], a["T"], a["rank"], a["d_in"])
+    return L.gdn_adapter_add(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=2), 1), (dict(dtype=-1), 1), (dict(n=-1), 1), (dict(T=-1), 1), (dict(n=0), 1), (dict(n=65536), 2), (dict(cu=None), 1),
+    (dict(cu=F + 2), 3), (dict(n_adapters=-1), 1), (dict(rank=0), 2), (dict(rank=12), 2), (dict(rank=136), 2), (dict(d_in=0, xs=256), 2),
+    (dict(d_in=252, xs=256), 2), (dict(d_in=65544, xs=1 << 17), 2), (dict(d_out=508), 2), (dict(xs=248), 1), (dict(xs=260), 3), (dict(ys=511), 1),
+    (dict(ys=1 << 31), 2), (dict(os=504), 1), (dict(os=516), 3), (dict(ids=None), 1), (dict(ids=2 * F + 1), 3), (dict(ranks=3 * F + 2), 3),
+    (dict(down=None), 1), (dict(down=4 * F + 8), 3), (dict(up=None), 1), (dict(scales=None), 1), (dict(x=None), 1), (dict(x=7 * F + 8), 3),
+    (dict(y=None), 1), (dict(out=None), 1), (dict(ws=None), 4), (dict(wb=100), 4), (dict(ws=10 * F + 8), 3), (dict(out=8 * F), 1),
+    (dict(out=8 * F + 16, os=1024), 1), (dict(out=7 * F), 1), (dict(out=5 * F, os=512), 1), (dict(ws=7 * F), 1), (dict(ws=9 * F + 256), 1),
+    (dict(out=8 * F, os=1024, ws=8 * F + 4096), 1), (dict(out=6 * F), 1)])
+def test_adapter_refusals(L, over, status):
+    assert adapter(L, **over) == status
+    assert L.gdn_last_error_string().decode()
+
+
+def test_adapter_without_tokens(L):
+    assert adapter(L, T=0) == 0
+    assert adapter(L, T=0, n=0, x=None, y=None, out=None, ids=None, ws=None, wb=0) == 0
+
+
+def test_adapter_workspace(L):
+    assert L.gdn_adapter_workspace_bytes(3, 100, 16, 256) >= 100 * 16 * 4
+    for a in ((3, 0, 16, 256), (-1, 100, 16, 256), (0, 100, 16, 256), (65536, 100, 16, 256), (3, -1, 16, 256), (3, 100, 0, 256), (3, 100, 20, 256),
+              (3, 100, 136, 256), (3, 100, 16, 0), (3, 100, 16, 260), (3, 100, 16, 70000)):
+        assert L.gdn_adapter_workspace_bytes(*a) == 0, a
