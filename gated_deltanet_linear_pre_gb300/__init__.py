@@ -8,7 +8,7 @@ its thin ctypes binding under the ABI's names:
     gdn_scan_workspace_bytes, gdn_layer_workspace_bytes, dims, GdnError
     gdn_kv_append, gdn_kv_attn, gdn_kv_attn_check, gdn_kv_attn_workspace_bytes, kv_cache, gdn_draft_verify
     gdn_kv_remap, gdn_kv_remap_workspace_bytes, gdn_kv_compact, gdn_kv_compact_workspace_bytes, gdn_kv_copy, kv_caches
-    gdn_block_norm, gdn_adapter_add, gdn_adapter_workspace_bytes
+    gdn_block_norm, gdn_adapter_add, gdn_adapter_check, gdn_adapter_workspace_bytes
 
 ``inputs`` draws the seeded synthetic workloads.  Nothing here computes the
 method on the CPU.
@@ -17,7 +17,7 @@ _BINDING = ("gdn_pre", "gdn_scan", "gdn_scan_fast", "gdn_layer_fast", "gdn_scan_
             "gdn_scan_selftest_timeout", "gdn_scan_selftest_one_taker", "gdn_scan_selftest_withhold_flag", "gdn_layer_selftest_stages", "gdn_scan_workspace_bytes",
             "gdn_kv_append", "gdn_kv_attn", "gdn_kv_attn_check", "gdn_kv_attn_workspace_bytes", "gdn_kv_cache", "kv_cache", "gdn_draft_verify",
             "gdn_kv_remap", "gdn_kv_remap_workspace_bytes", "gdn_kv_compact", "gdn_kv_compact_workspace_bytes", "gdn_kv_copy", "kv_caches",
-            "gdn_block_norm", "gdn_adapter_add", "gdn_adapter_workspace_bytes",
+            "gdn_block_norm", "gdn_adapter_add", "gdn_adapter_check", "gdn_adapter_workspace_bytes",
             "gdn_layer_workspace_bytes", "dims", "gdn_dims", "GdnError", "lib", "library_path")
 
 __all__ = list(_BINDING) + ["inputs", "build"]

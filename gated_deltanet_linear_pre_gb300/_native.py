@@ -130,7 +130,8 @@ def lib():
                                          [_p] * 3)
             L.gdn_adapter_workspace_bytes.restype = _sz
             L.gdn_adapter_workspace_bytes.argtypes = [_i32] * 4
-            L.gdn_adapter_add.restype = ctypes.c_int
+            L.gdn_adapter_add.restype = L.gdn_adapter_check.restype = ctypes.c_int
+            L.gdn_adapter_check.argtypes = [_p, _p]
             L.gdn_adapter_add.argtypes = ([_i32] * 3 + [_p, _p, _i32, _i32, _p, _p, _p, _p, _i32, _p, _i64, _i32, _p, _i64, _p,
                                                         _i64, _p, _sz, _p])
             _lib = L
@@ -756,3 +757,9 @@ def gdn_adapter_add(cu_seqlens, total_tokens, ids, down, up, ranks, scales, x, y
                                d_in, xp, xs, d_out, yp, ys, op, os_, wp, wb, _stream(stream))
     if st:
         _check("gdn_adapter_add", st)
+
+
+def gdn_adapter_check(workspace, stream=None):
+    """Raise GdnError (GDN_ERR_TIMEOUT) if the last gdn_adapter_add on this workspace reported an expired wait;
+    synchronises the stream."""
+    _check("gdn_adapter_check", lib().gdn_adapter_check(_ptr(workspace, "workspace", torch.uint8), _stream(stream)))

@@ -99,9 +99,21 @@ gdn_status gdn_adapter_add(int32_t dtype, int32_t n_seq, int32_t T, const int32_
     p.n_seq = n_seq; p.T = T; p.n_adapters = n_adapters; p.rank = rank; p.d_in = d_in; p.d_out = d_out; p.bf16 = dtype == GDN_BF16;
     p.cu_seqlens = cu_seqlens; p.ids = ids; p.ranks = ranks; p.down = down; p.up = up; p.scales = scales;
     p.x = x; p.y = y; p.y_out = y_out; p.x_stride = x_stride; p.y_stride = y_stride; p.out_stride = y_out_stride;
-    p.h = static_cast<float*>(workspace);
-    cudaError_t e = gdn::launch_adapter(p, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = gdn::launch_adapter(p, workspace, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_adapter_add launch");
+}
+
+gdn_status gdn_adapter_check(const void* workspace, struct CUstream_st* stream)
+{
+    if (!workspace) return fail(GDN_ERR_INVALID_ARG, "workspace is NULL");
+    int32_t status[2 * gdn::kAdapterCtas] = {};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(status, workspace, sizeof status, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "reading the failure record");
+    for (int32_t w : status)
+        if (w) return fail(GDN_ERR_TIMEOUT, "a bounded wait in the kernels expired; outputs are invalid");
+    return GDN_OK;
 }
 
 }  // extern "C"

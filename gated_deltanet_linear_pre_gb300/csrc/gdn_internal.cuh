@@ -223,12 +223,18 @@ struct AdapterParams {
     const uint16_t* y;
     uint16_t* y_out;
     int64_t x_stride, y_stride, out_stride;
-    float* h;               // workspace: [splits][T][rank]
-    int split_k, splits, split_o;  // set by launch_adapter
+    // workspace: a word for each CTA of either kernel, 0 or a wait that has expired; [parts][T][rank]
+    int32_t* status;
+    float* h;
+    // set by launch_adapter: tiles; units of a tile and of a CTA, for x's channels and for y's
+    int slots, chunks_in, chunks_out;
+    int64_t share_in, share_out;
 };
 
+constexpr int kAdapterCtas = 304;
+
 size_t adapter_workspace_bytes(int n_seq, int T, int rank, int d_in);
-cudaError_t launch_adapter(AdapterParams p, cudaStream_t stream);
+cudaError_t launch_adapter(AdapterParams p, void* workspace, cudaStream_t stream);
 cudaError_t launch_block_norm(const BlockNormParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 size_t kv_attn_workspace_bytes(const KvBatch& b);

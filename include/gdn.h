@@ -643,6 +643,15 @@ GDN_API gdn_status gdn_adapter_add(int32_t dtype, int32_t n_seq, int32_t total_t
                                    int64_t y_stride, uint16_t* y_out, int64_t y_out_stride, void* workspace,
                                    size_t workspace_bytes, struct CUstream_st* stream);
 
+/*
+ * gdn_adapter_check -- the failure report of the last gdn_adapter_add with
+ * tokens on this workspace: every wait inside its kernels is bounded, and one
+ * that expires is recorded (that call's outputs are invalid).  Enqueues a small
+ * device-to-host copy on `stream`, SYNCHRONISES it and returns GDN_OK or
+ * GDN_ERR_TIMEOUT.
+ */
+GDN_API gdn_status gdn_adapter_check(const void* workspace, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif

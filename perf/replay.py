@@ -1,5 +1,5 @@
 #!/usr/bin/env python3
-"""Times the cases of perf/operators.py through the package's operators.
+"""Times the cases of perf/operators.py and perf/more_operators.py through the package's operators.
 
   python perf/replay.py [CASE ...]      microseconds a call: from Python (calls one after another) and replayed
                                         from a CUDA graph, two input sets in turn
@@ -13,7 +13,7 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from perf import operators  # noqa: E402
+from perf import more_operators, operators  # noqa: E402
 
 CALLS = 20
 
@@ -30,7 +30,7 @@ def microseconds(fn, calls):
     return start.elapsed_time(end) * 1e3 / calls
 
 
-def time_case(case):
+def time_case(operators, case):
     states = [operators.prepare(case, seed) for seed in (1, 2)]
 
     def run():
@@ -49,17 +49,20 @@ def main():
     ap.add_argument("--twice", action="store_true")
     ap.add_argument("case", nargs="*")
     args = ap.parse_args()
-    operators.own = True
-    cases = {c["name"]: c for c in operators.listed()}
+    cases = {}
+    for module in (operators, more_operators):
+        module.own = True
+        cases.update((c["name"], (module, c)) for c in module.listed())
     for name in args.case or cases:
+        module, case = cases[name]
         if args.twice:
-            state = operators.prepare(cases[name], 1)
-            operators.run(state)
+            state = module.prepare(case, 1)
+            module.run(state)
             torch.empty(300 << 20, dtype=torch.uint8, device="cuda").zero_()
-            operators.run(state)
+            module.run(state)
             torch.cuda.synchronize()
         else:
-            print("%-18s call %8.2f us   graph %8.2f us" % (name, *time_case(cases[name])), flush=True)
+            print("%-18s call %8.2f us   graph %8.2f us" % (name, *time_case(module, case)), flush=True)
 
 
 if __name__ == "__main__":
