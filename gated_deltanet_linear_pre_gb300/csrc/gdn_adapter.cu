@@ -5,14 +5,20 @@
 //
 // Bound by HBM: x and y are read and y_out written once, an adapter's weights
 // once for every 128 tokens that use them (from L2 after the first).  Two launches:
-//   adapter_down  partial sums of h over ranges of x's channels, fp32, to the workspace
-//   adapter_up    the partial sums added in order, the product with up, the sum with y
+//   adapter_down  h, fp32, to the workspace
+//   adapter_up    the product of h with up, and the sum with y
 // A unit of work is 64 channels (of x, of y) for one tile of up to 128 tokens of
-// one sequence; each of two CTAs an SM takes an equal range of all units, and cuts
-// a tile where its range ends.  Tiles of more than 8 tokens go through the tensor
-// cores (tcgen05, 16-bit operands, fp32 sums in TMEM), 64 channels a stage of a
-// ring of 128-byte swizzled rows that cp.async fills; the others are sums on the
-// CUDA cores straight from global memory, as their weights are read once.
+// one sequence.  Each of 152 CTAs, one an SM, takes a range of all units of equal
+// cost (bytes, nearly), cutting a tile where its range ends: sequences of one
+// token and prompts share a batch, and may lie in any order.  A tile that lies in
+// several ranges has its h in several sums, which adapter_up adds in order.
+//
+// Four warps copy (cp.async, into a ring of stages of 128-byte swizzled rows), far
+// ahead of the others.  Tiles of more than 8 tokens go through the tensor cores:
+// tcgen05, 16-bit operands, fp32 sums in TMEM; one warp issues the products, eight
+// take what comes of them on.  Smaller tiles would leave those instructions mostly
+// empty: those eight warps take them by mma.sync with the tokens as its 8 columns,
+// several units a stage.
 // h enters its product as hi + lo in the weights' type: 16 bits of it in bf16, 21
 // of its row's largest in fp16, far below the rounding of y_out.
 #include <algorithm>
@@ -24,75 +30,224 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 128;              // tokens
-constexpr int kFew = 8;                 // tokens up to which a tile is summed on the CUDA cores, 4 at a time
-constexpr int kK = 64;                  // channels of a unit: rows of 128 bytes in shared memory
+constexpr int kWorkers = 8, kCopiers = 4;            // warps
+constexpr int kProduct = kWorkers + kCopiers;        // the warp that issues products
+constexpr int kThreads = (kProduct + 1) * 32;
+constexpr int kTile = 128;                           // tokens
+constexpr int kFew = 8;                              // tokens up to which a tile goes through mma.sync
+constexpr int kK = 64;                               // channels of a unit: rows of 128 bytes in shared memory
 constexpr int kRow = kK * 2;
-constexpr int kCtas = kAdapterCtas;     // two on each of 152 SMs
-constexpr int kLeast = 4;               // units that are worth a CTA
+constexpr int kCtas = kAdapterCtas;
 constexpr int kTokenBytes = kTile * kRow;
+constexpr int kParts = 16;                           // ranges that a tile is cut into at most, but for the one it begins in
+constexpr int kRing = 4;                             // chunks' products in TMEM
+constexpr int kColumnD = 256;                        // adapter_up's TMEM: h in the first R columns, products from here on
 
-template <int R> constexpr int kStages = R > 64 ? 3 : 4;
+template <int R> constexpr int kStages = R > 64 ? 6 : 8;
 template <int R> constexpr int kStageBytes = kTokenBytes + R * kRow;
-// two CTAs an SM hold all of its TMEM: never room for a third
-template <int R> constexpr size_t kSmem = 1024 + (kStages<R> * kStageBytes<R> < 80 << 10 ? 80 << 10 : kStages<R> * kStageBytes<R>);
+template <int R> constexpr size_t kSmem = 1024 + kStages<R> * kStageBytes<R>;
 
 // 16 bytes to shared memory, or zeros where there is nothing to read
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
 {
     const int bytes = there ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// one of the barrier's arrivals, when this thread's copies so far are there
+__device__ __forceinline__ void copies_arrive(uint64_t* mbar) { asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(umma::smem_u32(mbar)) : "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers * 32) : "memory"); }
 
 // byte offset of 16-byte piece `piece` of a row in a tile swizzled over 128 bytes
 __device__ __forceinline__ uint32_t place(int row, int piece) { return row * kRow + ((piece ^ (row & 7)) << 4); }
 
-// Up to kTile tokens of one sequence.  Sequence s owns the slots from cu[s] / kTile + s on; T / kTile + n_seq
-// slots cover any batch.
-struct Tile {
-    int start, n;   // first token, tokens (0: an empty slot)
-    int id, rank;   // adapter (-1: none) and its rank
-};
+// ---- who does what --------------------------------------------------------------
 
-__device__ __forceinline__ Tile tile_of(const AdapterParams& p, int slot)
+// What a unit costs, in steps of 128 bytes of HBM and a little for its hand-offs.  The weights of tiles of many tokens
+// come from L2 (several tiles of a sequence, or of an adapter, read them), a few tokens' from HBM.
+__host__ __device__ __forceinline__ int weight_cost(int n, int rank) { return n > kFew ? rank / 4 + 16 : rank + 8; }
+__host__ __device__ __forceinline__ int cost_in(int n, int rank) { return n > 0 && rank > 0 ? n + weight_cost(n, rank) : 0; }
+__host__ __device__ __forceinline__ int cost_out(int n, int rank, bool copied) { return n > 0 && (rank > 0 || copied) ? 2 * n + weight_cost(n, rank) : 0; }
+
+template <bool IN>
+__device__ __forceinline__ int unit_cost(const AdapterParams& p, int n, int rank) { return IN ? cost_in(n, rank) : cost_out(n, rank, p.y_out != p.y); }
+
+__device__ __forceinline__ int rank_of(const AdapterParams& p, int s, int& id)
 {
-    const auto base = [&](int s) { return (int64_t)(cu_at(p.cu_seqlens, s, p.T) / kTile + s); };
-    const int s = warp_find(p.n_seq, slot, base);
-    const int first = cu_at(p.cu_seqlens, s, p.T), end = cu_at(p.cu_seqlens, s + 1, p.T);
-    Tile t;
-    const int64_t start = first + (slot - base(s)) * kTile;
-    t.n = (int)max((int64_t)0, min((int64_t)kTile, end - start));
-    t.start = t.n > 0 ? (int)start : 0;
-    t.id = __ldg(p.ids + s);
-    if (t.id < 0 || t.id >= p.n_adapters) t.id = -1;
-    t.rank = t.id < 0 ? 0 : p.ranks ? min(max(__ldg(p.ranks + t.id), 0), p.rank) : p.rank;
-    return t;
+    id = __ldg(p.ids + s);
+    if (id < 0 || id >= p.n_adapters) {
+        id = -1;
+        return 0;
+    }
+    return p.ranks ? min(max(__ldg(p.ranks + id), 0), p.rank) : p.rank;
 }
 
-// What the CTA's threads share for the tensor cores.  Every wait is bounded; after one that has expired the
-// rest of the call's waits are passed over and its outputs are invalid, which the CTA records.
+template <bool IN>
+__device__ __forceinline__ int64_t sequence_cost(const AdapterParams& p, int s)
+{
+    const int n = cu_at(p.cu_seqlens, s + 1, p.T) - cu_at(p.cu_seqlens, s, p.T);
+    int id;
+    const int rank = rank_of(p, s, id);
+    return n <= 0 ? 0 : (IN ? p.chunks_in : p.chunks_out) * ((int64_t)(n / kTile) * unit_cost<IN>(p, kTile, rank) + unit_cost<IN>(p, n % kTile, rank));
+}
+
+// units [c_lo, c_hi) of one tile
+struct Piece {
+    int start, n, id, rank;
+    int slot;               // the tile's own number, below T / kTile + n_seq
+    int c_lo, c_hi;
+    int cost;               // of a unit
+    int64_t before;         // cost of all units in front of the tile
+};
+
+// Walks the tiles of a range of costs [lo, hi).  A whole warp, in step.
+template <bool IN>
+struct Walk {
+    int s, k;               // the next sequence and its next tile
+    int64_t at, lo, hi;     // cost of all units in front of that tile; the range
+
+    __device__ bool next(const AdapterParams& p, Piece& t)
+    {
+        const int chunks = IN ? p.chunks_in : p.chunks_out;
+        while (at < hi && s < p.n_seq) {
+            if (k == 0) {   // pass over sequences that cost nothing, 32 at a time
+                const int mine = s + (threadIdx.x & 31);
+                const uint32_t some = __ballot_sync(0xffffffffu, mine < p.n_seq && sequence_cost<IN>(p, min(mine, p.n_seq - 1)) > 0);
+                if (some == 0) {
+                    s += 32;
+                    continue;
+                }
+                s += __ffs(some) - 1;
+            }
+            const int first = cu_at(p.cu_seqlens, s, p.T), end = cu_at(p.cu_seqlens, s + 1, p.T);
+            t.start = first + k * kTile;
+            t.n = min(kTile, end - t.start);
+            t.rank = rank_of(p, s, t.id);
+            t.slot = first / kTile + s + k;
+            t.cost = unit_cost<IN>(p, t.n, t.rank);
+            t.before = at;
+            if (t.start + t.n >= end) {
+                ++s;
+                k = 0;
+            } else {
+                ++k;
+            }
+            const int whole = t.cost * chunks;  // below 2^20
+            at += whole;
+            t.c_lo = ((int)min(max(lo - t.before, (int64_t)0), (int64_t)whole) + t.cost - 1) / t.cost;
+            t.c_hi = ((int)min(hi - t.before, (int64_t)whole) + t.cost - 1) / t.cost;
+            if (t.c_lo < t.c_hi) return true;
+        }
+        return false;
+    }
+};
+
+struct PlanSmem {
+    int64_t warp_sum[2][kThreads / 32];
+    AdapterStart start;
+};
+
+// Sum over the threads in front of this one, and over all
+__device__ __forceinline__ int64_t block_exclusive(int64_t (&warp_sum)[kThreads / 32], int64_t v, int64_t& all)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
+    }
+    return before + incl - v;
+}
+
+// Where this CTA's ranges of x's and of y's units begin; every CTA goes over all sequences, a run of them a thread.
+// All threads.
+__device__ __forceinline__ void find_starts(const AdapterParams& p, PlanSmem& sm, AdapterStart& out)
+{
+    const int each = (p.n_seq + kThreads - 1) / kThreads, first = min(p.n_seq, (int)threadIdx.x * each), last = min(p.n_seq, first + each);
+    int64_t mine[2] = {0, 0}, total[2], at[2];
+    for (int s = first; s < last; ++s) {
+        mine[0] += sequence_cost<true>(p, s);
+        mine[1] += sequence_cost<false>(p, s);
+    }
+    at[0] = block_exclusive(sm.warp_sum[0], mine[0], total[0]);
+    at[1] = block_exclusive(sm.warp_sum[1], mine[1], total[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        AdapterStart& start = i ? out : sm.start;
+        // a CTA is worth 4 units of the largest tiles, and a tile is cut into at most kParts + 1
+        const int chunks = i ? p.chunks_out : p.chunks_in;
+        const int most = i ? cost_out(kTile, p.rank, true) : cost_in(kTile, p.rank);
+        const int64_t share = max((total[i] + kCtas - 1) / kCtas, (int64_t)most * max(4, (chunks + kParts - 1) / kParts)), lo = share * blockIdx.x;
+        if (threadIdx.x == 0) {
+            start.share = share;
+            if (lo >= total[i]) start.s = p.n_seq;  // no work
+        }
+        if (lo < at[i] || lo >= at[i] + mine[i]) continue;
+        for (int s = first; s < last; ++s) {
+            const int64_t c = i ? sequence_cost<false>(p, s) : sequence_cost<true>(p, s);
+            if (lo < at[i] + c) {
+                int id;
+                const int rank = rank_of(p, s, id);
+                const int tile = chunks * (i ? unit_cost<false>(p, kTile, rank) : unit_cost<true>(p, kTile, rank));
+                start.s = s;
+                start.k = (int)((lo - at[i]) / tile);
+                start.before = at[i] + (int64_t)start.k * tile;
+                break;
+            }
+            at[i] += c;
+        }
+    }
+}
+
+// ---- hand-offs ------------------------------------------------------------------
+
+// Every wait is bounded; after one that has expired the rest of the call's waits are passed over and its
+// outputs are invalid, which the CTA records.
+// A barrier's parity tells two turns apart, no more.  So whoever waits for a ring's stages waits for all of them, in
+// order, also those that are another role's, and is among those who free them: nobody falls a turn behind.
+// (adapter_down's workers pass over the tensor cores' stages, but only once all of them are done.)
 struct Shared {
-    uint64_t done[4];  // products of a chunk
+    uint64_t full[8], empty[8];           // stages of the ring
+    uint64_t d_full[kRing], d_empty[kRing];
+    uint64_t h_full;                      // h is in TMEM (adapter_up)
     uint32_t tmem;
     int expired;
     float factor[kTile];
-    float most[2][kTile];
+    union {
+        float most[2][kTile];
+        float sums[kWorkers][4][32];
+    };
 };
 
-__device__ __forceinline__ void wait_done(Shared& sm, uint32_t chunk)
+__device__ __forceinline__ void wait(Shared& sm, uint64_t* mbar, uint32_t parity)
 {
-    if (*(volatile int*)&sm.expired) return;
-    if (!umma::mbar_wait(&sm.done[chunk & 3], (chunk >> 2) & 1)) *(volatile int*)&sm.expired = 1;
+    volatile int* expired = &sm.expired;
+    for (uint32_t i = 0; i < 1u << 22; ++i)
+        if (umma::mbar_try_wait(mbar, parity) || *expired) return;
+    *expired = 1;
 }
 
-__device__ __forceinline__ void shared_begin(Shared& sm, int columns)
+__device__ __forceinline__ void shared_begin(Shared& sm, int columns, int empty_count)
 {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 4; ++i) umma::mbar_init(&sm.done[i], 1);
+        for (int i = 0; i < 8; ++i) {
+            umma::mbar_init(&sm.full[i], kCopiers * 32);
+            umma::mbar_init(&sm.empty[i], empty_count);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            umma::mbar_init(&sm.d_full[i], 1);
+            umma::mbar_init(&sm.d_empty[i], kWorkers);
+        }
+        umma::mbar_init(&sm.h_full, kWorkers);
         sm.expired = 0;
     }
     if (threadIdx.x < 32) umma::tmem_alloc(&sm.tmem, columns);
@@ -101,15 +256,64 @@ __device__ __forceinline__ void shared_begin(Shared& sm, int columns)
     umma::fence_after_sync();
 }
 
-// the CTA's record, and clean ones for CTAs that this call does not have
 __device__ __forceinline__ void shared_end(Shared& sm, int columns, int32_t* status)
 {
     umma::fence_before_sync();
     __syncthreads();
     if (threadIdx.x < 32) umma::tmem_dealloc(sm.tmem, columns);
-    if (threadIdx.x == 0) status[blockIdx.x] = sm.expired;
-    if (blockIdx.x == 0)
-        for (int i = gridDim.x + threadIdx.x; i < kCtas; i += kThreads) status[i] = 0;
+    if (threadIdx.x == 0) *status = sm.expired;
+}
+
+// A position in the ring of stages
+template <int R>
+struct Ring {
+    uint32_t stage = 0, phase = 0;
+    __device__ void next()
+    {
+        if (++stage == kStages<R>) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Tiles of few tokens: 2^units_shift units a stage, as many as fit, at most 8
+template <int R>
+__device__ __forceinline__ int units_shift(const Piece& t)
+{
+    const int fit = kStageBytes<R> / ((t.rank + t.n) * kRow);
+    return fit >= 8 ? 3 : fit >= 4 ? 2 : fit >= 2 ? 1 : 0;
+}
+
+// The copying warps: the tokens' and the weights' rows, `width` channels from channel `at` on, of 2^shift units
+// side by side; unit u's rows lie behind one another from u * unit_bytes on, weights first.
+__device__ __forceinline__ void copy_few(const Piece& t, int shift, int at, int width, const uint16_t* w, const uint16_t* x, int64_t x_stride, uint32_t stage)
+{
+    const int pieces = 8 << shift, all = (t.rank + t.n) * pieces, unit_bytes = (t.rank + t.n) * kRow;
+    for (int i = threadIdx.x - kWorkers * 32; i < all; i += kCopiers * 32) {
+        const int row = i >> (shift + 3), col = i & (pieces - 1), c = at + col * 8;
+        const uint16_t* src = row < t.rank ? w + (size_t)row * width + c : x + (size_t)(row - t.rank) * x_stride + c;
+        copy16(stage + (col >> 3) * unit_bytes + place(row, col & 7), c < width ? src : x, c < width);
+    }
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void* at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(umma::smem_u32(at)));
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], const void* at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(umma::smem_u32(at)));
+}
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 template <bool BF16, int M, int N>
@@ -117,194 +321,195 @@ constexpr uint32_t idesc(bool b_mn_major) { return BF16 ? umma::idesc_bf16(M, N,
 
 // ---- down -----------------------------------------------------------------------
 
-// h of up to NT tokens, channels [k_lo, k_hi): each warp two rows of `down` at a time
-template <bool BF16, int NT>
-__device__ __forceinline__ void down_few(const AdapterParams& p, const Tile& t, int k_lo, int k_hi, float* h)
+// h of a tile of up to 8 tokens: 16 rows of `down` by 8 tokens a product.  A warp takes 16 rows and, where there are
+// fewer rows than warps, every so many of a stage's units; the warps of the same rows add up at the end, in order.
+template <bool BF16, int R>
+__device__ __forceinline__ void down_few(const AdapterParams& p, const Piece& t, float* h, Shared& sm, const unsigned char* ring, Ring<R>& at)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kAhead = NT > 2 ? 2 : 4;  // steps of 256 channels loaded ahead: what 128 registers hold
-    const uint16_t* x = p.x + (size_t)t.start * p.x_stride;
-    for (int j = warp * 2; j < t.rank; j += kThreads / 16) {
-        const uint16_t* w0 = p.down + ((size_t)t.id * p.rank + j) * p.d_in;
-        const uint16_t* w1 = j + 1 < t.rank ? w0 + p.d_in : w0;
-        float acc[2][NT] = {};
-        for (int k0 = k_lo + lane * 8; k0 < k_hi; k0 += kAhead * 256) {
-            uint4 a[kAhead], b[kAhead];
+    const int blocks = (t.rank + 15) / 16, groups = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks;  // of 16 rows; warps that take different ones
+    const int block = warp % groups, unit = warp / groups, step = kWorkers / groups;
+    const int shift = units_shift<R>(t), unit_bytes = (t.rank + t.n) * kRow;
+    // a lane's row of either operand; rows that are not there are others again, and what comes of them goes nowhere
+    const int row = min(block * 16 + (lane & 15), t.rank - 1), token = t.rank + min(lane & 7, t.n - 1);
+    float acc[4] = {};
+    for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
+        wait(sm, &sm.full[at.stage], at.phase);
+        const int units = block < blocks ? min(1 << shift, t.c_hi - c) : 0;
+        for (int u = unit; u < units; u += step) {
+            const unsigned char* rows = ring + at.stage * kStageBytes<R> + u * unit_bytes;
+            uint32_t b[2][4];
+            ldmatrix4(b[0], rows + place(token, lane >> 3));
+            ldmatrix4(b[1], rows + place(token, 4 + (lane >> 3)));
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (k0 + i * 256 < k_hi) {
-                    a[i] = __ldg(reinterpret_cast<const uint4*>(w0 + k0 + i * 256));
-                    b[i] = __ldg(reinterpret_cast<const uint4*>(w1 + k0 + i * 256));
-                }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (k0 + i * 256 < k_hi) {
-                    float wa[8], wb[8];
-                    widen8<BF16>(a[i], wa);
-                    widen8<BF16>(b[i], wb);
-#pragma unroll
-                    for (int q = 0; q < NT; ++q) {
-                        float v[8];
-                        widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(x + (size_t)min(q, t.n - 1) * p.x_stride + k0 + i * 256)), v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            acc[0][q] = fmaf(wa[e], v[e], acc[0][q]);
-                            acc[1][q] = fmaf(wb[e], v[e], acc[1][q]);
-                        }
-                    }
-                }
-        }
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float sum = warp_sum(acc[i][q]);
-                if (lane == 0 && q < t.n && j + i < t.rank) h[(size_t)q * p.rank + j + i] = sum;
+            for (int k = 0; k < 4; ++k) {
+                uint32_t a[4];
+                ldmatrix4(a, rows + place(row, 2 * k + (lane >> 4)));
+                mma<BF16>(acc, a, b[k >> 1][2 * (k & 1)], b[k >> 1][2 * (k & 1) + 1]);
             }
+        }
+        workers_sync();
+        if (threadIdx.x == 0) umma::mbar_arrive(&sm.empty[at.stage]);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sm.sums[warp][e][lane] = acc[e];
+    workers_sync();
+    if (unit == 0 && block < blocks) {
+        for (int w = warp + groups; w < kWorkers; w += groups)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] += sm.sums[w][e][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = block * 16 + (lane >> 2) + (e >> 1) * 8, q = (lane & 3) * 2 + (e & 1);
+            if (j < t.rank && q < t.n) h[(size_t)q * p.rank + j] = acc[e];
+        }
+    }
+    workers_sync();  // the sums are read
 }
 
 template <bool BF16, int R>
-__device__ __forceinline__ void down_tile(const AdapterParams& p, const Tile& t, int c_lo, int c_hi, float* h, Shared& sm, uint32_t ring, uint32_t& at)
-{
-    constexpr int kS = kStages<R>;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint16_t* x = p.x + (size_t)t.start * p.x_stride;
-    const uint16_t* w = p.down + (size_t)t.id * p.rank * p.d_in;
-    const uint32_t first = at;
-    const auto load = [&](int c) {
-        if (c < c_hi) {
-            const uint32_t stage = ring + (first + c - c_lo) % kS * kStageBytes<R>;
-            const int k = c * kK + (tid & 7) * 8;
-            const bool there = k < p.d_in;
-            for (int row = tid >> 3; row < t.n; row += kThreads / 8)
-                copy16(stage + place(row, tid & 7), there ? x + (size_t)row * p.x_stride + k : p.x, there);
-            for (int row = tid >> 3; row < t.rank; row += kThreads / 8)
-                copy16(stage + kTokenBytes + place(row, tid & 7), there ? w + (size_t)row * p.d_in + k : p.x, there);
-        }
-        copies_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kS - 1; ++i) load(c_lo + i);
-    for (int c = c_lo; c < c_hi; ++c, ++at) {
-        copies_wait<kS - 2>();
-        umma::fence_proxy_async();
-        __syncthreads();
-        if (warp == 0) {
-            umma::fence_after_sync();
-            if (umma::elect_one()) {
-                const uint32_t stage = ring + at % kS * kStageBytes<R>;
-                const uint64_t da = umma::desc_sw128(stage, 16, 1024), db = umma::desc_sw128(stage + kTokenBytes, 16, 1024);
-#pragma unroll
-                for (int k = 0; k < kK / 16; ++k) umma::mma_bf16(sm.tmem, da + 2 * k, db + 2 * k, idesc<BF16, 128, R>(false), c > c_lo || k > 0);
-                umma::commit(&sm.done[at & 3]);
-            }
-            __syncwarp();
-        }
-        // the stage of the chunk before this one is free once its products are done
-        if (c > c_lo) wait_done(sm, at - 1);
-        load(c + kS - 1);
-    }
-    wait_done(sm, at - 1);
-    copies_wait<0>();
-    umma::fence_after_sync();
-    const int row = (warp & 3) * 32 + lane;
-#pragma unroll
-    for (int j = 0; j < R / 16; ++j)
-        if ((j & 1) == warp >> 2 && j * 16 < t.rank) {
-            float v[16];
-            umma::tmem_ld16(sm.tmem + ((warp & 3) * 32 << 16) + j * 16, v);
-            umma::tmem_wait_ld();
-            float4* to = reinterpret_cast<float4*>(h + (size_t)row * p.rank + j * 16);
-            if (row < t.n) {
-                to[0] = make_float4(v[0], v[1], v[2], v[3]);
-                to[1] = make_float4(v[4], v[5], v[6], v[7]);
-                if (j * 16 + 8 < p.rank) {  // a row holds a multiple of 8
-                    to[2] = make_float4(v[8], v[9], v[10], v[11]);
-                    to[3] = make_float4(v[12], v[13], v[14], v[15]);
-                }
-            }
-        }
-    umma::fence_before_sync();
-    __syncthreads();  // TMEM and the ring are free
-}
-
-template <bool BF16, int R>
-__global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_constant__ AdapterParams p)
+__global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_constant__ AdapterParams p)
 {
     extern __shared__ unsigned char smem[];
     __shared__ Shared sm;
-    constexpr int kColumns = R < 32 ? 32 : R;
-    const uint32_t ring = (umma::smem_u32(smem) + 1023) & ~1023u;
+    __shared__ PlanSmem plan;
+    constexpr int kColumns = R * 2 < 32 ? 32 : R * 2;
+    unsigned char* ring = smem + ((1024 - (umma::smem_u32(smem) & 1023)) & 1023);
+    const uint32_t base = umma::smem_u32(ring);
     // In this order.  Nobody waits here for another kernel while it holds TMEM that the other has yet to get, and
     // the kernel behind this one, which starts when all CTAs have come by, may read what earlier launches wrote.
     pdl_wait();
-    shared_begin(sm, kColumns);
+    shared_begin(sm, kColumns, 2);  // a stage is free: its products are done, or the workers are; the product warp is past it
     pdl_launch_dependents();
-    uint32_t at = 0;  // chunks so far
-    const int64_t total = (int64_t)p.slots * p.chunks_in, end = min(total, (int64_t)(blockIdx.x + 1) * p.share_in);
-    for (int64_t u = (int64_t)blockIdx.x * p.share_in; u < end;) {
-        const int slot = (int)(u / p.chunks_in), c_lo = (int)(u - (int64_t)slot * p.chunks_in);
-        const int c_hi = (int)min((int64_t)p.chunks_in, c_lo + end - u);
-        u += c_hi - c_lo;
-        const Tile t = tile_of(p, slot);
-        if (t.n == 0 || t.rank == 0) continue;
-        const int part = blockIdx.x - (int)((int64_t)slot * p.chunks_in / p.share_in);
-        float* h = p.h + ((size_t)part * p.T + t.start) * p.rank;
-        if (t.n <= kFew) {
-            const int k_lo = c_lo * kK, k_hi = min(p.d_in, c_hi * kK);
-            for (Tile q = t; q.n > 0; q.start += 4, q.n -= 4, h += 4 * p.rank) {
-                if (q.n == 1) down_few<BF16, 1>(p, q, k_lo, k_hi, h);
-                else if (q.n == 2) down_few<BF16, 2>(p, q, k_lo, k_hi, h);
-                else down_few<BF16, 4>(p, q, k_lo, k_hi, h);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    find_starts(p, plan, p.starts[blockIdx.x]);
+    __syncthreads();
+    const int64_t share = plan.start.share;
+    Walk<true> walk{plan.start.s, plan.start.k, plan.start.before, share * blockIdx.x, share * (blockIdx.x + 1)};
+    if (walk.s >= p.n_seq) walk.hi = walk.at;
+    Piece t;
+    if (warp < kWorkers) {
+        Ring<R> at;
+        uint32_t tiles = 0;
+        while (walk.next(p, t)) {
+            // the range that a tile begins in has its sums in the tokens' places, every other its own
+            float* h = t.before >= walk.lo ? p.h + (size_t)t.start * p.rank : p.h + ((size_t)p.T + (size_t)blockIdx.x * kTile) * p.rank;
+            if (tid == 0 && t.c_lo == 0) {
+                const int64_t at_last = t.before + (int64_t)(p.chunks_in - 1) * t.cost;
+                int ends = blockIdx.x;
+                for (int64_t hi = walk.hi; hi <= at_last; hi += share) ++ends;
+                p.parts[t.slot] = make_int2(blockIdx.x, ends);
             }
-        } else {
-            down_tile<BF16, R>(p, t, c_lo, c_hi, h, sm, ring, at);
+            if (t.n <= kFew) {
+                down_few<BF16, R>(p, t, h, sm, ring, at);
+                continue;
+            }
+            // the ring goes on under the products
+            for (int c = t.c_lo; c < t.c_hi; ++c) at.next();
+            const uint32_t d = tiles & 1;
+            wait(sm, &sm.d_full[d], (tiles >> 1) & 1);
+            umma::fence_after_sync();
+            const int row = (warp & 3) * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < R / 16; ++j)
+                if ((j & 1) == warp >> 2 && j * 16 < t.rank) {
+                    float v[16];
+                    umma::tmem_ld16(sm.tmem + ((warp & 3) * 32 << 16) + d * R + j * 16, v);
+                    umma::tmem_wait_ld();
+                    float4* to = reinterpret_cast<float4*>(h + (size_t)row * p.rank + j * 16);
+                    if (row < t.n) {
+                        to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                        if (j * 16 + 8 < p.rank) {  // a row holds a multiple of 8
+                            to[2] = make_float4(v[8], v[9], v[10], v[11]);
+                            to[3] = make_float4(v[12], v[13], v[14], v[15]);
+                        }
+                    }
+                }
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&sm.d_empty[d]);
+            ++tiles;
         }
+    } else if (warp < kProduct) {
+        Ring<R> at;
+        // this thread's piece of every 16th row; rows 16 apart are swizzled alike
+        const int row0 = (tid - kWorkers * 32) >> 3, piece = tid & 7;
+        const uint32_t spot = place(row0, piece);
+        while (walk.next(p, t)) {
+            const uint16_t* x = p.x + (size_t)t.start * p.x_stride;
+            const uint16_t* w = p.down + (size_t)t.id * p.rank * p.d_in;
+            if (t.n <= kFew) {
+                const int shift = units_shift<R>(t);
+                for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
+                    wait(sm, &sm.empty[at.stage], at.phase ^ 1);
+                    copy_few(t, shift, c * kK, p.d_in, w, x, p.x_stride, base + at.stage * kStageBytes<R>);
+                    copies_arrive(&sm.full[at.stage]);
+                }
+                continue;
+            }
+            x += (size_t)row0 * p.x_stride + t.c_lo * kK + piece * 8;
+            w += (size_t)row0 * p.d_in + t.c_lo * kK + piece * 8;
+            for (int c = t.c_lo; c < t.c_hi; ++c, x += kK, w += kK, at.next()) {
+                wait(sm, &sm.empty[at.stage], at.phase ^ 1);
+                const uint32_t stage = base + at.stage * kStageBytes<R> + spot;
+                const bool there = c * kK + piece * 8 < p.d_in;
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i)
+                    if (row0 + i * 16 < t.n) copy16(stage + i * 16 * kRow, there ? x + (size_t)(i * 16) * p.x_stride : p.x, there);
+#pragma unroll
+                for (int i = 0; i < R / 16; ++i)
+                    if (row0 + i * 16 < t.rank) copy16(stage + kTokenBytes + i * 16 * kRow, there ? w + (size_t)(i * 16) * p.d_in : p.x, there);
+                copies_arrive(&sm.full[at.stage]);
+            }
+        }
+        copies_wait();
+    } else {
+        Ring<R> at;
+        uint32_t tiles = 0;
+        while (walk.next(p, t)) {
+            if (t.n <= kFew) {
+                const int step = 1 << units_shift<R>(t);
+                for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
+                    wait(sm, &sm.full[at.stage], at.phase);
+                    if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
+                }
+                continue;
+            }
+            const uint32_t d = tiles & 1;
+            if (tiles >= 2) wait(sm, &sm.d_empty[d], ((tiles >> 1) - 1) & 1);
+            for (int c = t.c_lo; c < t.c_hi; ++c, at.next()) {
+                wait(sm, &sm.full[at.stage], at.phase);
+                umma::fence_proxy_async();  // the copies are generic writes
+                umma::fence_after_sync();
+                __syncwarp();
+                if (umma::elect_one()) {
+                    const uint32_t stage = base + at.stage * kStageBytes<R>;
+                    const uint64_t da = umma::desc_sw128(stage, 16, 1024), db = umma::desc_sw128(stage + kTokenBytes, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < kK / 16; ++k) umma::mma_bf16(sm.tmem + d * R, da + 2 * k, db + 2 * k, idesc<BF16, 128, R>(false), c > t.c_lo || k > 0);
+                    umma::commit(&sm.empty[at.stage]);
+                    umma::mbar_arrive(&sm.empty[at.stage]);
+                    if (c + 1 == t.c_hi) umma::commit(&sm.d_full[d]);
+                }
+                __syncwarp();
+            }
+            ++tiles;
+        }
+        // no product may be under way when the CTA leaves
+        if (tiles > 0) wait(sm, &sm.d_full[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
     }
-    shared_end(sm, kColumns, p.status);
+    shared_end(sm, kColumns, p.status + blockIdx.x);
 }
 
 // ---- up -------------------------------------------------------------------------
 
-constexpr int kColumnD = 128;  // TMEM: h in the first R columns, the products of two chunks from here on
-
-// y_out of up to NT tokens, channels [o_lo, o_hi): each thread 8 channels at a time
-template <bool BF16, int NT>
-__device__ __forceinline__ void up_few(const AdapterParams& p, const Tile& t, int o_lo, int o_hi, const float* h, float scale)
+// h of a token's column `col`, over all parts of its tile: `b` the ranges that the tile begins and ends in
+__device__ __forceinline__ float h_at(const AdapterParams& p, const Piece& t, int2 b, int row, int col)
 {
-    constexpr int kAhead = NT > 2 ? 4 : 8;  // rows of `up` loaded ahead: what 128 registers hold
-    const uint16_t* w = p.up + (size_t)t.id * p.rank * p.d_out;
-    for (int o = o_lo + threadIdx.x * 8; o < o_hi; o += kThreads * 8) {
-        uint4 y[NT];
-#pragma unroll
-        for (int q = 0; q < NT; ++q) y[q] = __ldcs(reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + min(q, t.n - 1)) * p.y_stride + o));
-        float acc[NT][8] = {};
-        for (int j = 0; j < t.rank; j += kAhead) {
-            uint4 v[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) v[i] = j + i < t.rank ? __ldg(reinterpret_cast<const uint4*>(w + (size_t)(j + i) * p.d_out + o)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                float f[8];
-                widen8<BF16>(v[i], f);
-#pragma unroll
-                for (int q = 0; q < NT; ++q)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[q][e] = fmaf(h[q * p.rank + j + i], f[e], acc[q][e]);
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-            if (q < t.n) {
-                float f[8];
-                widen8<BF16>(y[q], f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = fmaf(scale, acc[q][e], f[e]);
-                __stcs(reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o),
-                       make_uint4(narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]), narrow2<BF16>(f[4], f[5]), narrow2<BF16>(f[6], f[7])));
-            }
-    }
+    float v = p.h[(size_t)(t.start + row) * p.rank + col];
+    for (int r = b.x + 1; r <= b.y; ++r) v += p.h[((size_t)p.T + (size_t)r * kTile + row) * p.rank + col];
+    return v;
 }
 
 // two values as hi + lo in the weights' type; what is not finite goes into hi alone
@@ -324,6 +529,79 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     lo = narrow2<BF16>(isfinite(ha) ? a - ha : 0.0f, isfinite(hb) ? b - hb : 0.0f);
 }
 
+// y_out of a tile of up to 8 tokens; h[8][rank] in shared memory (zeros behind the tokens and the rank).  16 channels
+// by 8 tokens a product; the warps share a stage's blocks of 16 channels.
+template <bool BF16, int R>
+__device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, const float* h, Shared& sm, unsigned char* ring, Ring<R>& at)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, steps = (t.rank + 15) / 16;
+    const int shift = units_shift<R>(t), unit_bytes = (t.rank + t.n) * kRow;
+    // h as the products' second operand: column lane / 4, rows 16 k + 2 (lane & 3) + {0, 1, 8, 9}
+    uint32_t hi[R / 16][2], lo[R / 16][2];
+    float factor[2];  // of tokens 2 (lane & 3) and the next
+    {
+        const float* mine = h + (lane >> 2) * p.rank + (lane & 3) * 2;
+        float inv = 1.0f, scale = t.id < 0 ? 0.0f : __ldg(p.scales + t.id);
+        if (!BF16) {
+            // a token's largest value to [1, 2), as in operand()
+            float most = 0.0f;
+            for (int k = 0; k < steps * 2; ++k)
+                if (k * 8 < t.rank) most = fmaxf(most, fmaxf(fabsf(mine[k * 8]), fabsf(mine[k * 8 + 1])));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            const int exponent = min(max((int)(__float_as_uint(most) >> 23) - 127, -126), 126);
+            inv = __uint_as_float((uint32_t)(127 - exponent) << 23);
+            scale *= __uint_as_float((uint32_t)(127 + exponent) << 23);
+        }
+#pragma unroll
+        for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bool there = k * 16 + e * 8 < t.rank;  // (h's rows are a multiple of 8 long)
+                split2<BF16>(there ? mine[k * 16 + e * 8] * inv : 0.0f, there ? mine[k * 16 + e * 8 + 1] * inv : 0.0f, hi[k][e], lo[k][e]);
+            }
+        factor[0] = __shfl_sync(0xffffffffu, scale, (lane & 3) * 8);
+        factor[1] = __shfl_sync(0xffffffffu, scale, (lane & 3) * 8 + 4);
+    }
+    for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
+        wait(sm, &sm.full[at.stage], at.phase);
+        const int blocks = min(1 << shift, t.c_hi - c) * 4;
+        for (int b = warp; b < blocks; b += kWorkers) {
+            unsigned char* rows = ring + at.stage * kStageBytes<R> + (b >> 2) * unit_bytes;
+            const int piece = (b & 3) * 2;  // the first of the block's two 16-byte pieces
+            if (t.rank > 0) {
+                float acc[4] = {};
+#pragma unroll
+                for (int k = 0; k < R / 16; ++k)
+                    if (k < steps) {
+                        // rows behind the rank are the last one again: their h is 0, and what follows a tile's rows in its
+                        // stage may not be finite
+                        uint32_t a[4];
+                        ldmatrix4_t(a, rows + place(min(k * 16 + (lane & 7) + (lane >> 4 << 3), t.rank - 1), piece + (lane >> 3 & 1)));
+                        mma<BF16>(acc, a, hi[k][0], hi[k][1]);
+                        mma<BF16>(acc, a, lo[k][0], lo[k][1]);
+                    }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int q = (lane & 3) * 2 + (e & 1), channel = (lane >> 2) + (e >> 1) * 8;
+                    if (q < t.n) {
+                        uint16_t* y = reinterpret_cast<uint16_t*>(rows + place(t.rank + q, piece + (channel >> 3))) + (channel & 7);
+                        const float v = BF16 ? __uint_as_float((uint32_t)*y << 16) : __half2float(*reinterpret_cast<const __half*>(y));
+                        *y = (uint16_t)narrow2<BF16>(fmaf(factor[e & 1], acc[e], v), 0.0f);
+                    }
+                }
+                __syncwarp();
+            }
+            const int q = lane >> 1, o = (c + (b >> 2)) * kK + (piece + (lane & 1)) * 8;
+            if (q < t.n && o < p.d_out)
+                __stcs(reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o),
+                       *reinterpret_cast<const uint4*>(rows + place(t.rank + q, piece + (lane & 1))));
+        }
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N])
 {
@@ -338,9 +616,9 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N])
 }
 
 // h of a tile as the products' first operand: hi in TMEM columns [0, R / 2), lo behind it, two values a column.
-// Two threads a row, each half of its columns.
+// The workers: two threads a row, each half of its columns.
 template <bool BF16, int R>
-__device__ __forceinline__ void operand(const AdapterParams& p, const Tile& t, int parts, Shared& sm)
+__device__ __forceinline__ void operand(const AdapterParams& p, const Piece& t, int2 b, Shared& sm)
 {
     constexpr int kMine = R / 2, kAtOnce = kMine < 32 ? kMine : 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -349,8 +627,9 @@ __device__ __forceinline__ void operand(const AdapterParams& p, const Tile& t, i
 #pragma unroll
     for (int j = 0; j < kMine; ++j) v[j] = 0.0f;
     if (row < t.n)
-        for (int s = 0; s < parts; ++s) {
-            const float4* src = reinterpret_cast<const float4*>(p.h + ((size_t)s * p.T + t.start + row) * p.rank + col);
+        for (int r = b.x; r <= b.y; ++r) {
+            const size_t from = r == b.x ? (size_t)t.start : (size_t)p.T + (size_t)r * kTile;
+            const float4* src = reinterpret_cast<const float4*>(p.h + (from + row) * p.rank + col);
 #pragma unroll
             for (int j = 0; j < kMine; j += 4)
                 if (col + j < t.rank) {  // a row holds a multiple of 8 values
@@ -371,7 +650,7 @@ __device__ __forceinline__ void operand(const AdapterParams& p, const Tile& t, i
 #pragma unroll
         for (int j = 0; j < kMine; ++j) most = fmaxf(most, fabsf(v[j]));
         sm.most[half][row] = most;
-        __syncthreads();
+        workers_sync();
         most = fmaxf(sm.most[0][row], sm.most[1][row]);
         const int exponent = min(max((int)(__float_as_uint(most) >> 23) - 127, -126), 126);
         inv = __uint_as_float((uint32_t)(127 - exponent) << 23);
@@ -389,192 +668,219 @@ __device__ __forceinline__ void operand(const AdapterParams& p, const Tile& t, i
     }
     umma::tmem_wait_st();
     umma::fence_before_sync();
-    __syncthreads();
+    workers_sync();  // the factors
+    if (lane == 0) umma::mbar_arrive(&sm.h_full);
 }
 
-template <bool BF16, int R>
-__device__ __forceinline__ void up_tile(const AdapterParams& p, const Tile& t, int parts, int c_lo, int c_hi, Shared& sm, unsigned char* ring, uint32_t& at,
-                                        bool& waited)
+// A warp's part of a chunk from its stage to y_out, 64 bytes of 8 rows at a time
+__device__ __forceinline__ void store_rows(const AdapterParams& p, const Piece& t, int c, const unsigned char* tile, uint16_t* out, int row, int piece)
 {
-    constexpr int kS = kStages<R>;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = warp >> 2;
-    const int steps = (t.rank + 15) / 16;
-    const uint32_t base = umma::smem_u32(ring);
-    const uint16_t* w = p.up + (size_t)t.id * p.rank * p.d_out;
-    const uint16_t* y = p.y + (size_t)t.start * p.y_stride;
-    uint16_t* out = p.y_out + (size_t)t.start * p.out_stride;
-    const uint32_t first = at;
-    const auto load = [&](int c) {
-        if (c < c_hi) {
-            const uint32_t stage = base + (first + c - c_lo) % kS * kStageBytes<R>;
-            const int o = c * kK + (tid & 7) * 8;
-            const bool there = o < p.d_out;
-            for (int row = tid >> 3; row < t.n; row += kThreads / 8)
-                copy16(stage + place(row, tid & 7), there ? y + (size_t)row * p.y_stride + o : p.y, there);
-            // rows behind the rank: zeros, as what was there may not be finite
-            for (int row = tid >> 3; row < steps * 16; row += kThreads / 8) {
-                const bool mine = there && row < t.rank;
-                copy16(stage + kTokenBytes + place(row, tid & 7), mine ? w + (size_t)row * p.d_out + o : p.y, mine);
-            }
-        }
-        copies_commit();
-    };
-    // y plus the products of chunk c, the `n`th of all: this warp's 32 rows and 32 channels
-    const auto finish = [&](int c, uint32_t n) {
-        wait_done(sm, n);
-        umma::fence_after_sync();
-        float v[32];
-        umma::tmem_ld32(sm.tmem + ((warp & 3) * 32 << 16) + kColumnD + (n & 1) * kK + half * 32, v);
-        umma::tmem_wait_ld();
-        unsigned char* tile = ring + n % kS * kStageBytes<R>;
-        const int row = (warp & 3) * 32 + lane;
-        const float factor = sm.factor[row];
+    if (c * kK + piece * 8 >= p.d_out) return;
+    const unsigned char* mine = tile + place(row, piece);  // rows 8 apart are swizzled alike
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint4* q = reinterpret_cast<uint4*>(tile + place(row, half * 4 + i));
-            float f[8];
-            widen8<BF16>(*q, f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = fmaf(factor, v[i * 8 + e], f[e]);
-            *q = make_uint4(narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]), narrow2<BF16>(f[4], f[5]), narrow2<BF16>(f[6], f[7]));
-        }
-        __syncwarp();
-        const int piece = half * 4 + (lane & 3), o = c * kK + piece * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (warp & 3) * 32 + i * 8 + (lane >> 2);
-            if (r < t.n && o < p.d_out) __stcs(reinterpret_cast<uint4*>(out + (size_t)r * p.out_stride + o), *reinterpret_cast<const uint4*>(tile + place(r, piece)));
-        }
-        umma::fence_before_sync();
-    };
-#pragma unroll
-    for (int i = 0; i < kS - 2; ++i) load(c_lo + i);
-    if (!waited) pdl_wait();
-    waited = true;
-    operand<BF16, R>(p, t, parts, sm);
-    for (int c = c_lo; c < c_hi; ++c, ++at) {
-        copies_wait<kS - 3>();
-        umma::fence_proxy_async();
-        __syncthreads();
-        if (warp == 0) {
-            umma::fence_after_sync();
-            if (umma::elect_one()) {
-                const uint32_t d = sm.tmem + kColumnD + (at & 1) * kK;
-                const uint64_t db = umma::desc_sw128(base + at % kS * kStageBytes<R> + kTokenBytes, 16, 1024);
-                for (int k = 0; k < steps; ++k) umma::mma_ts(d, sm.tmem + 8 * k, db + k * (2048 >> 4), idesc<BF16, 128, kK>(true), k > 0);
-                for (int k = 0; k < steps; ++k) umma::mma_ts(d, sm.tmem + R / 2 + 8 * k, db + k * (2048 >> 4), idesc<BF16, 128, kK>(true), 1);
-                umma::commit(&sm.done[at & 3]);
-            }
-            __syncwarp();
-        }
-        // every warp is past the chunk before the last one: its stage is free
-        load(c + kS - 2);
-        if (c > c_lo) finish(c - 1, at - 1);
-    }
-    finish(c_hi - 1, at - 1);
-    copies_wait<0>();
-    __syncthreads();  // TMEM and the ring are free
+    for (int i = 0; i < 4; ++i)
+        if (row + i * 8 < t.n) __stcs(reinterpret_cast<uint4*>(out + (size_t)(i * 8) * p.out_stride), *reinterpret_cast<const uint4*>(mine + i * 8 * kRow));
 }
 
 template <bool BF16, int R>
-__global__ void __launch_bounds__(kThreads, 2) adapter_up_kernel(const __grid_constant__ AdapterParams p)
+__global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_constant__ AdapterParams p)
 {
     extern __shared__ unsigned char smem[];
     __shared__ Shared sm;
     __shared__ float few[kFew * R];
-    constexpr int kColumns = 256;
+    constexpr int kColumns = 512;
     unsigned char* ring = smem + ((1024 - (umma::smem_u32(smem) & 1023)) & 1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // all of adapter_down's CTAs have their TMEM, as those of this kernel when the next one starts
-    shared_begin(sm, kColumns);
+    shared_begin(sm, kColumns, kWorkers + 1);  // a stage is free: every worker is done with it, the product warp is past it
     pdl_launch_dependents();
-    // y, up and the batch were there before adapter_down began; only its own sums have to be waited for
-    bool waited = false;
-    uint32_t at = 0;
-    const int64_t total = (int64_t)p.slots * p.chunks_out, end = min(total, (int64_t)(blockIdx.x + 1) * p.share_out);
-    for (int64_t u = (int64_t)blockIdx.x * p.share_out; u < end;) {
-        const int slot = (int)(u / p.chunks_out), c_lo = (int)(u - (int64_t)slot * p.chunks_out);
-        const int c_hi = (int)min((int64_t)p.chunks_out, c_lo + end - u);
-        u += c_hi - c_lo;
-        const Tile t = tile_of(p, slot);
-        const int64_t first = (int64_t)slot * p.chunks_in;
-        const int parts = (int)((first + p.chunks_in - 1) / p.share_in - first / p.share_in) + 1;
-        const int o_lo = c_lo * kK, o_hi = min(p.d_out, c_hi * kK);
-        if (t.rank > 0 && t.n > kFew) {
-            up_tile<BF16, R>(p, t, parts, c_lo, c_hi, sm, ring, at, waited);
-            continue;
+    pdl_wait();
+    const AdapterStart start = p.starts[blockIdx.x];
+    const int64_t share = p.starts[0].share;
+    Walk<false> walk{start.s, start.k, start.before, share * blockIdx.x, share * (blockIdx.x + 1)};
+    if (walk.s >= p.n_seq) walk.hi = walk.at;
+    Piece t;
+    if (warp < kWorkers) {
+        const int half = warp >> 2, row0 = (warp & 3) * 32, row = row0 + lane, spot = row0 + (lane >> 2), piece = half * 4 + (lane & 3);
+        Ring<R> at;
+        uint32_t m = 0;  // chunks of products
+        while (walk.next(p, t)) {
+            const int2 b = t.rank > 0 ? p.parts[t.slot] : make_int2(0, 0);
+            if (t.n <= kFew) {
+                workers_sync();  // the last tile's h is read
+                for (int i = tid; i < t.n * p.rank; i += kWorkers * 32)
+                    few[i] = i % p.rank < t.rank ? h_at(p, t, b, i / p.rank, i % p.rank) : 0.0f;
+                for (int i = t.n * p.rank + tid; i < kFew * p.rank; i += kWorkers * 32) few[i] = 0.0f;
+                workers_sync();
+                up_few<BF16, R>(p, t, few, sm, ring, at);
+                continue;
+            }
+            if (t.rank == 0) {  // y as it is
+                uint16_t* out = p.y_out + (size_t)(t.start + spot) * p.out_stride + t.c_lo * kK + piece * 8;
+                for (int c = t.c_lo; c < t.c_hi; ++c, out += kK, at.next()) {
+                    wait(sm, &sm.full[at.stage], at.phase);
+                    store_rows(p, t, c, ring + at.stage * kStageBytes<R>, out, spot, piece);
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
+                }
+                continue;
+            }
+            workers_sync();  // the last tile's factors are read
+            operand<BF16, R>(p, t, b, sm);
+            uint16_t* out = p.y_out + (size_t)(t.start + spot) * p.out_stride + t.c_lo * kK + piece * 8;
+            const float factor = sm.factor[row];
+            for (int c = t.c_lo; c < t.c_hi; ++c, ++m, out += kK, at.next()) {
+                const uint32_t d = m % kRing;
+                wait(sm, &sm.d_full[d], (m / kRing) & 1);
+                if (row0 < t.n) {
+                    wait(sm, &sm.full[at.stage], at.phase);  // long since; y was copied by other threads
+                    umma::fence_after_sync();
+                    float v[32];
+                    umma::tmem_ld32(sm.tmem + (row0 << 16) + kColumnD + d * kK + half * 32, v);
+                    umma::tmem_wait_ld();
+                    unsigned char* tile = ring + at.stage * kStageBytes<R>;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4* q = reinterpret_cast<uint4*>(tile + place(row, half * 4 + i));
+                        float f[8];
+                        widen8<BF16>(*q, f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = fmaf(factor, v[i * 8 + e], f[e]);
+                        *q = make_uint4(narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]), narrow2<BF16>(f[4], f[5]), narrow2<BF16>(f[6], f[7]));
+                    }
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(&sm.d_empty[d]);
+                    store_rows(p, t, c, tile, out, spot, piece);
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
+                } else if (lane == 0) {
+                    umma::mbar_arrive(&sm.d_empty[d]);
+                    umma::mbar_arrive(&sm.empty[at.stage]);
+                }
+            }
         }
-        if (!waited) pdl_wait();
-        waited = true;
-        if (t.rank > 0 && t.n > 0) {
-            for (int i = threadIdx.x; i < t.n * p.rank; i += kThreads) {
-                float v = 0.0f;
-                if (i % p.rank < t.rank)
-                    for (int s = 0; s < parts; ++s) v += p.h[((size_t)s * p.T + t.start) * p.rank + i];
-                few[i] = v;
+    } else if (warp < kProduct) {
+        Ring<R> at;
+        const uint32_t base = umma::smem_u32(ring);
+        // this thread's piece of every 16th row; rows 16 apart are swizzled alike
+        const int row0 = (tid - kWorkers * 32) >> 3, piece = tid & 7;
+        const uint32_t spot = place(row0, piece);
+        while (walk.next(p, t)) {
+            const int rows = (t.rank + 15) / 16 * 16;
+            const uint16_t* y = p.y + (size_t)t.start * p.y_stride;
+            const uint16_t* w = p.up + (size_t)max(t.id, 0) * p.rank * p.d_out;
+            if (t.n <= kFew) {
+                const int shift = units_shift<R>(t);
+                for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
+                    wait(sm, &sm.empty[at.stage], at.phase ^ 1);
+                    copy_few(t, shift, c * kK, p.d_out, w, y, p.y_stride, base + at.stage * kStageBytes<R>);
+                    copies_arrive(&sm.full[at.stage]);
+                }
+                continue;
             }
-            for (int i = t.n * p.rank + threadIdx.x; i < kFew * p.rank; i += kThreads) few[i] = 0.0f;
-            __syncthreads();
-            const float scale = __ldg(p.scales + t.id);
-            const float* h = few;
-            for (Tile q = t; q.n > 0; q.start += 4, q.n -= 4, h += 4 * p.rank) {
-                if (q.n == 1) up_few<BF16, 1>(p, q, o_lo, o_hi, h, scale);
-                else if (q.n == 2) up_few<BF16, 2>(p, q, o_lo, o_hi, h, scale);
-                else up_few<BF16, 4>(p, q, o_lo, o_hi, h, scale);
-            }
-            __syncthreads();
-        } else if (p.y_out != p.y) {
-            const int vectors = (o_hi - o_lo) / 8;
-            for (int i = threadIdx.x; i < t.n * vectors; i += kThreads) {
-                const int row = t.start + i / vectors, o = o_lo + i % vectors * 8;
-                __stcs(reinterpret_cast<uint4*>(p.y_out + (size_t)row * p.out_stride + o), __ldcs(reinterpret_cast<const uint4*>(p.y + (size_t)row * p.y_stride + o)));
+            y += (size_t)row0 * p.y_stride + t.c_lo * kK + piece * 8;
+            w += (size_t)row0 * p.d_out + t.c_lo * kK + piece * 8;
+            for (int c = t.c_lo; c < t.c_hi; ++c, y += kK, w += kK, at.next()) {
+                wait(sm, &sm.empty[at.stage], at.phase ^ 1);
+                const uint32_t stage = base + at.stage * kStageBytes<R> + spot;
+                const bool there = c * kK + piece * 8 < p.d_out;
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i)
+                    if (row0 + i * 16 < t.n) copy16(stage + i * 16 * kRow, there ? y + (size_t)(i * 16) * p.y_stride : p.y, there);
+                // rows behind the rank: zeros, as what was there may not be finite
+#pragma unroll
+                for (int i = 0; i < R / 16; ++i)
+                    if (row0 + i * 16 < rows) {
+                        const bool mine = there && row0 + i * 16 < t.rank;
+                        copy16(stage + kTokenBytes + i * 16 * kRow, mine ? w + (size_t)(i * 16) * p.d_out : p.y, mine);
+                    }
+                copies_arrive(&sm.full[at.stage]);
             }
         }
+        copies_wait();
+    } else {
+        const uint32_t base = umma::smem_u32(ring);
+        Ring<R> at;
+        uint32_t m = 0, tiles = 0;
+        while (walk.next(p, t)) {
+            if (t.n <= kFew || t.rank == 0) {
+                const int step = t.n <= kFew ? 1 << units_shift<R>(t) : 1;
+                for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
+                    wait(sm, &sm.full[at.stage], at.phase);
+                    if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
+                }
+                continue;
+            }
+            const int steps = (t.rank + 15) / 16;
+            wait(sm, &sm.h_full, tiles & 1);
+            ++tiles;
+            for (int c = t.c_lo; c < t.c_hi; ++c, ++m, at.next()) {
+                const uint32_t slot = m % kRing;
+                wait(sm, &sm.full[at.stage], at.phase);
+                if (m >= kRing) wait(sm, &sm.d_empty[slot], (m / kRing - 1) & 1);
+                umma::fence_proxy_async();  // the copies are generic writes
+                umma::fence_after_sync();
+                __syncwarp();
+                if (umma::elect_one()) {
+                    const uint32_t d = sm.tmem + kColumnD + slot * kK;
+                    const uint64_t db = umma::desc_sw128(base + at.stage * kStageBytes<R> + kTokenBytes, 16, 1024);
+                    for (int k = 0; k < steps; ++k) umma::mma_ts(d, sm.tmem + 8 * k, db + k * (2048 >> 4), idesc<BF16, 128, kK>(true), k > 0);
+                    for (int k = 0; k < steps; ++k) umma::mma_ts(d, sm.tmem + R / 2 + 8 * k, db + k * (2048 >> 4), idesc<BF16, 128, kK>(true), 1);
+                    umma::commit(&sm.d_full[slot]);
+                    umma::mbar_arrive(&sm.empty[at.stage]);
+                }
+                __syncwarp();
+            }
+        }
+        // no product may be under way when the CTA leaves
+        if (m > 0) wait(sm, &sm.d_full[(m - 1) % kRing], ((m - 1) / kRing) & 1);
     }
-    if (!waited) pdl_wait();
-    shared_end(sm, kColumns, p.status + kCtas);
+    shared_end(sm, kColumns, p.status + kCtas + blockIdx.x);
 }
 
 template <bool BF16, int R>
-cudaError_t launch_rank(const AdapterParams& p, unsigned ctas_in, unsigned ctas_out, cudaStream_t stream)
+cudaError_t launch_rank(const AdapterParams& p, cudaStream_t stream)
 {
     cudaError_t e = cudaFuncSetAttribute(adapter_down_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(adapter_up_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
-    if (e == cudaSuccess) e = launch_k(adapter_down_kernel<BF16, R>, dim3(ctas_in), dim3(kThreads), kSmem<R>, stream, true, p);
-    if (e == cudaSuccess) e = launch_k(adapter_up_kernel<BF16, R>, dim3(ctas_out), dim3(kThreads), kSmem<R>, stream, true, p);
+    if (e == cudaSuccess) e = launch_k(adapter_down_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p);
+    if (e == cudaSuccess) e = launch_k(adapter_up_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p);
     return e;
 }
 
-int64_t slots_of(int n_seq, int T) { return (int64_t)T / kTile + n_seq; }
-int chunks_of(int width) { return (width + kK - 1) / kK; }
-int64_t share_of(int64_t units) { return std::max<int64_t>(kLeast, (units + kCtas - 1) / kCtas); }
-constexpr size_t kHeader = (2 * kCtas * 4 + 255) / 256 * 256;
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-size_t adapter_workspace_bytes(int n_seq, int T, int rank, int d_in)
+// status words, where the ranges of adapter_up begin, which ranges a tile's h is in, h
+size_t adapter_workspace(AdapterParams& p, void* workspace)
 {
-    // consecutive units of a tile lie in at most so many shares
-    const int64_t chunks = chunks_of(d_in), share = share_of(slots_of(n_seq, T) * chunks), parts = (chunks + share - 2) / share + 1;
-    return kHeader + (size_t)parts * T * rank * 4;
+    char* at = static_cast<char*>(workspace);
+    size_t used = 0;
+    const auto take = [&](size_t bytes) {
+        char* mine = at + used;
+        used += align256(bytes);
+        return mine;
+    };
+    p.status = reinterpret_cast<int32_t*>(take(2 * kCtas * 4));
+    p.starts = reinterpret_cast<AdapterStart*>(take(kCtas * sizeof(AdapterStart)));
+    p.parts = reinterpret_cast<int2*>(take(((size_t)p.T / kTile + p.n_seq) * sizeof(int2)));
+    p.h = reinterpret_cast<float*>(take(((size_t)p.T + kCtas * kTile) * p.rank * 4));
+    return used;
 }
 
 cudaError_t launch_adapter(AdapterParams p, void* workspace, cudaStream_t stream)
 {
-    p.slots = (int)slots_of(p.n_seq, p.T);
-    p.chunks_in = chunks_of(p.d_in);
-    p.chunks_out = chunks_of(p.d_out);
-    const int64_t units_in = (int64_t)p.slots * p.chunks_in, units_out = (int64_t)p.slots * p.chunks_out;
-    p.share_in = share_of(units_in);
-    p.share_out = share_of(units_out);
-    p.status = static_cast<int32_t*>(workspace);
-    p.h = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader);
-    const unsigned ctas_in = (unsigned)((units_in + p.share_in - 1) / p.share_in), ctas_out = (unsigned)((units_out + p.share_out - 1) / p.share_out);
+    adapter_workspace(p, workspace);
+    p.chunks_in = (p.d_in + kK - 1) / kK;
+    p.chunks_out = (p.d_out + kK - 1) / kK;
     const auto launch = [&](auto bf16) {
         constexpr bool kBf16 = decltype(bf16)::value;
-        if (p.rank <= 16) return launch_rank<kBf16, 16>(p, ctas_in, ctas_out, stream);
-        if (p.rank <= 32) return launch_rank<kBf16, 32>(p, ctas_in, ctas_out, stream);
-        if (p.rank <= 64) return launch_rank<kBf16, 64>(p, ctas_in, ctas_out, stream);
-        return launch_rank<kBf16, 128>(p, ctas_in, ctas_out, stream);
+        if (p.rank <= 16) return launch_rank<kBf16, 16>(p, stream);
+        if (p.rank <= 32) return launch_rank<kBf16, 32>(p, stream);
+        if (p.rank <= 64) return launch_rank<kBf16, 64>(p, stream);
+        return launch_rank<kBf16, 128>(p, stream);
     };
     return p.bf16 ? launch(std::true_type{}) : launch(std::false_type{});
 }

@@ -61,7 +61,10 @@ gdn_status gdn_block_norm(int32_t x_dtype, int32_t dtype, int32_t T, int32_t wid
 size_t gdn_adapter_workspace_bytes(int32_t n_seq, int32_t T, int32_t rank, int32_t d_in)
 {
     if (n_seq < 0 || n_seq > 65535 || T < 0 || (n_seq == 0 && T > 0) || !known_rank(rank) || !known_width(d_in)) return 0;
-    return T > 0 ? align256(gdn::adapter_workspace_bytes(n_seq, T, rank, d_in)) : 0;
+    if (T == 0) return 0;
+    gdn::AdapterParams p{};
+    p.n_seq = n_seq; p.T = T; p.rank = rank;
+    return gdn::adapter_workspace(p, nullptr);
 }
 
 gdn_status gdn_adapter_add(int32_t dtype, int32_t n_seq, int32_t T, const int32_t* cu_seqlens, const int32_t* ids, int32_t n_adapters,

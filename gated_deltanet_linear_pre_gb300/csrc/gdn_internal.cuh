@@ -210,6 +210,15 @@ struct CopyParams {
 cudaError_t launch_kv_remap(const RemapParams& p, cudaStream_t stream);
 cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t stream);
 cudaError_t launch_kv_copy(const CopyParams& p, cudaStream_t stream);
+constexpr int kAdapterCtas = 152;
+
+// where a CTA's range of units begins: a sequence (n_seq: no work), its tile, the cost of all units in front of that
+// tile; the cost of a range (in the first CTA's)
+struct AdapterStart {
+    int64_t before, share;
+    int s, k;
+};
+
 // the sequences' adapters added to a shared projection's output
 struct AdapterParams {
     int n_seq, T, n_adapters, rank, d_in, d_out, bf16;
@@ -223,17 +232,18 @@ struct AdapterParams {
     const uint16_t* y;
     uint16_t* y_out;
     int64_t x_stride, y_stride, out_stride;
-    // workspace: a word for each CTA of either kernel, 0 or a wait that has expired; [parts][T][rank]
+    int chunks_in, chunks_out;  // units of a tile (set by launch_adapter)
+    // workspace (set by launch_adapter): a word for each CTA of either kernel, 0 or a wait that has expired; per CTA, where
+    // its range of y's units begins; per tile, the first and the last range of x's units that it lies in;
+    // h [T + ranges * 128][rank]: what the range that a tile begins in summed, then what each of the others did
     int32_t* status;
+    AdapterStart* starts;
+    int2* parts;
     float* h;
-    // set by launch_adapter: tiles; units of a tile and of a CTA, for x's channels and for y's
-    int slots, chunks_in, chunks_out;
-    int64_t share_in, share_out;
 };
 
-constexpr int kAdapterCtas = 304;
-
-size_t adapter_workspace_bytes(int n_seq, int T, int rank, int d_in);
+// lays the workspace out (p: n_seq, T, rank) and returns its bytes
+size_t adapter_workspace(AdapterParams& p, void* workspace);
 cudaError_t launch_adapter(AdapterParams p, void* workspace, cudaStream_t stream);
 cudaError_t launch_block_norm(const BlockNormParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);

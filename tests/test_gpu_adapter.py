@@ -259,7 +259,7 @@ def test_another_stream_and_a_graph(gdn, lengths):
 
 def test_refusals(gdn):
     c = Case([4, 5], [0, 1], 2, 16, 128, 192, "bf16")
-    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(gdn.gdn_adapter_workspace_bytes(2, 9, 16, 128), dtype=torch.uint8, device="cuda")
     good = dict(cu=i32(c.cu), T=9, ids=i32(c.ids), down=c.down, up=c.up, ranks=None, scales=c.scales, x=c.x, y=c.y, out=torch.empty_like(c.y), ws=ws)
     gdn.gdn_adapter_add(*good.values())
     for over in [dict(cu=i32([0, 4])), dict(cu=i32(c.cu).cpu()), dict(ids=i32([0, 1, 2])), dict(ids=torch.zeros(2, device="cuda")), dict(down=c.down.half()),
