@@ -13,8 +13,8 @@
 // token and prompts share a batch, and may lie in any order.  A tile that lies in
 // several ranges has its h in several sums, which adapter_up adds in order.
 //
-// Four warps copy (cp.async, into a ring of stages of 128-byte swizzled rows), far
-// ahead of the others.  Tiles of more than 8 tokens go through the tensor cores:
+// One warp copies (TMA boxes of 64 channels, into a ring of stages of 128-byte
+// swizzled rows), far ahead of the others.  Tiles of more than 8 tokens go through the tensor cores:
 // tcgen05, 16-bit operands, fp32 sums in TMEM; one warp issues the products, eight
 // take what comes of them on.  Smaller tiles would leave those instructions mostly
 // empty: those eight warps take them by mma.sync with the tokens as its 8 columns,
@@ -25,13 +25,15 @@
 #include <type_traits>
 
 #include "gdn_kv.cuh"
+#include "gdn_tensor_map.cuh"
 #include "umma.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kWorkers = 8, kCopiers = 4;            // warps
-constexpr int kProduct = kWorkers + kCopiers;        // the warp that issues products
+constexpr int kWorkers = 8;                          // warps
+constexpr int kCopier = kWorkers;                    // the warp that copies
+constexpr int kProduct = kWorkers + 1;               // the warp that issues products
 constexpr int kThreads = (kProduct + 1) * 32;
 constexpr int kTile = 128;                           // tokens
 constexpr int kFew = 8;                              // tokens up to which a tile goes through mma.sync
@@ -45,17 +47,14 @@ constexpr int kColumnD = 256;                        // adapter_up's TMEM: h in 
 
 template <int R> constexpr int kStages = R > 64 ? 6 : 8;
 template <int R> constexpr int kStageBytes = kTokenBytes + R * kRow;
-template <int R> constexpr size_t kSmem = 1024 + kStages<R> * kStageBytes<R>;
+constexpr int kResultBytes = 32 * 64;                // a worker's part of a chunk of y_out, on its way out
+template <int R> constexpr size_t kSmem = 1024 + kStages<R> * kStageBytes<R> + kWorkers * kResultBytes;
 
-// 16 bytes to shared memory, or zeros where there is nothing to read
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
-{
-    const int bytes = there ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// one of the barrier's arrivals, when this thread's copies so far are there
-__device__ __forceinline__ void copies_arrive(uint64_t* mbar) { asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(umma::smem_u32(mbar)) : "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// tensor maps of the tokens (x or y): boxes of kTile and of kFew rows; and of the weights: boxes of `rank` and of 8 rows
+struct Maps {
+    CUtensorMap tokens, few, weights, weights8;
+};
+
 __device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers * 32) : "memory"); }
 
 // byte offset of 16-byte piece `piece` of a row in a tile swizzled over 128 bytes
@@ -63,11 +62,15 @@ __device__ __forceinline__ uint32_t place(int row, int piece) { return row * kRo
 
 // ---- who does what --------------------------------------------------------------
 
-// What a unit costs, in steps of 128 bytes of HBM and a little for its hand-offs.  The weights of tiles of many tokens
-// come from L2 (several tiles of a sequence, or of an adapter, read them), a few tokens' from HBM.
-__host__ __device__ __forceinline__ int weight_cost(int n, int rank) { return n > kFew ? rank / 4 + 16 : rank + 8; }
-__host__ __device__ __forceinline__ int cost_in(int n, int rank) { return n > 0 && rank > 0 ? n + weight_cost(n, rank) : 0; }
-__host__ __device__ __forceinline__ int cost_out(int n, int rank, bool copied) { return n > 0 && (rank > 0 || copied) ? 2 * n + weight_cost(n, rank) : 0; }
+// What a unit costs, in steps of some 2 ns: rows of 128 bytes copied and written, fitted to the time that a CTA took for
+// ranges of one kind (8 prompts with rank 64, a prompt with rank 72 beside drafts of ranks 8 to 112).  A tile of more
+// than a few tokens copies the rows of a whole one.
+__host__ __device__ __forceinline__ int cost_few(int rank) { return 24 + (rank + 8) * 3 / 2; }
+__host__ __device__ __forceinline__ int cost_in(int n, int rank) { return n <= 0 || rank <= 0 ? 0 : n <= kFew ? cost_few(rank) : 144 + rank; }
+__host__ __device__ __forceinline__ int cost_out(int n, int rank, bool copied)
+{
+    return n <= 0 || (rank <= 0 && !copied) ? 0 : n <= kFew ? cost_few(rank) + 2 * n : rank > 0 ? 160 + 2 * rank : 192;
+}
 
 template <bool IN>
 __device__ __forceinline__ int unit_cost(const AdapterParams& p, int n, int rank) { return IN ? cost_in(n, rank) : cost_out(n, rank, p.y_out != p.y); }
@@ -240,7 +243,7 @@ __device__ __forceinline__ void shared_begin(Shared& sm, int columns, int empty_
 {
     if (threadIdx.x == 0) {
         for (int i = 0; i < 8; ++i) {
-            umma::mbar_init(&sm.full[i], kCopiers * 32);
+            umma::mbar_init(&sm.full[i], 1);
             umma::mbar_init(&sm.empty[i], empty_count);
         }
         for (int i = 0; i < kRing; ++i) {
@@ -277,23 +280,49 @@ struct Ring {
     }
 };
 
-// Tiles of few tokens: 2^units_shift units a stage, as many as fit, at most 8
+// Tiles of few tokens: 2^units_shift units a stage, as many as fit, at most 8.  A unit is `rank` rows of weights and
+// kFew of tokens behind them.
+__device__ __forceinline__ int unit_bytes(const AdapterParams& p) { return (p.rank + kFew) * kRow; }
+
 template <int R>
-__device__ __forceinline__ int units_shift(const Piece& t)
+__device__ __forceinline__ int units_shift(const AdapterParams& p)
 {
-    const int fit = kStageBytes<R> / ((t.rank + t.n) * kRow);
+    const int fit = kStageBytes<R> / unit_bytes(p);
     return fit >= 8 ? 3 : fit >= 4 ? 2 : fit >= 2 ? 1 : 0;
 }
 
-// The copying warps: the tokens' and the weights' rows, `width` channels from channel `at` on, of 2^shift units
-// side by side; unit u's rows lie behind one another from u * unit_bytes on, weights first.
-__device__ __forceinline__ void copy_few(const Piece& t, int shift, int at, int width, const uint16_t* w, const uint16_t* x, int64_t x_stride, uint32_t stage)
+// The copying warp: the stages of a piece, in order.  Rows of tokens behind the tile's own are its neighbours', and
+// what comes of them goes nowhere.
+template <int R>
+__device__ __forceinline__ void copy_piece(const AdapterParams& p, const Piece& t, const Maps& maps, Shared& sm, uint32_t base, Ring<R>& at)
 {
-    const int pieces = 8 << shift, all = (t.rank + t.n) * pieces, unit_bytes = (t.rank + t.n) * kRow;
-    for (int i = threadIdx.x - kWorkers * 32; i < all; i += kCopiers * 32) {
-        const int row = i >> (shift + 3), col = i & (pieces - 1), c = at + col * 8;
-        const uint16_t* src = row < t.rank ? w + (size_t)row * width + c : x + (size_t)(row - t.rank) * x_stride + c;
-        copy16(stage + (col >> 3) * unit_bytes + place(row, col & 7), c < width ? src : x, c < width);
+    const bool few = t.n <= kFew;
+    const int step = few ? 1 << units_shift<R>(p) : 1, rows = (t.rank + 7) & ~7, row = t.rank > 0 ? t.id * p.rank : 0;
+    const auto weights = [&](uint32_t to, int c, uint64_t* full) {
+        if (rows == p.rank) umma::tensor_g2s_2d(to, &maps.weights, c * kK, row, full);
+        else
+            for (int r = 0; r < rows; r += 8) umma::tensor_g2s_2d(to + r * kRow, &maps.weights8, c * kK, row + r, full);
+    };
+    for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
+        wait(sm, &sm.empty[at.stage], at.phase ^ 1);
+        __syncwarp();
+        if (umma::elect_one()) {
+            uint32_t to = base + at.stage * kStageBytes<R>;
+            uint64_t* full = &sm.full[at.stage];
+            if (few) {
+                const int units = min(step, t.c_hi - c);
+                umma::mbar_arrive_expect_tx(full, units * (rows + kFew) * kRow);
+                for (int u = 0; u < units; ++u, to += unit_bytes(p)) {
+                    weights(to, c + u, full);
+                    umma::tensor_g2s_2d(to + p.rank * kRow, &maps.few, (c + u) * kK, t.start, full);
+                }
+            } else {
+                umma::mbar_arrive_expect_tx(full, kTokenBytes + rows * kRow);
+                umma::tensor_g2s_2d(to, &maps.tokens, c * kK, t.start, full);
+                weights(to + kTokenBytes, c, full);
+            }
+        }
+        __syncwarp();
     }
 }
 
@@ -329,15 +358,15 @@ __device__ __forceinline__ void down_few(const AdapterParams& p, const Piece& t,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int blocks = (t.rank + 15) / 16, groups = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks;  // of 16 rows; warps that take different ones
     const int block = warp % groups, unit = warp / groups, step = kWorkers / groups;
-    const int shift = units_shift<R>(t), unit_bytes = (t.rank + t.n) * kRow;
+    const int shift = units_shift<R>(p), bytes = unit_bytes(p);
     // a lane's row of either operand; rows that are not there are others again, and what comes of them goes nowhere
-    const int row = min(block * 16 + (lane & 15), t.rank - 1), token = t.rank + min(lane & 7, t.n - 1);
+    const int row = min(block * 16 + (lane & 15), t.rank - 1), token = p.rank + min(lane & 7, t.n - 1);
     float acc[4] = {};
     for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
         wait(sm, &sm.full[at.stage], at.phase);
         const int units = block < blocks ? min(1 << shift, t.c_hi - c) : 0;
         for (int u = unit; u < units; u += step) {
-            const unsigned char* rows = ring + at.stage * kStageBytes<R> + u * unit_bytes;
+            const unsigned char* rows = ring + at.stage * kStageBytes<R> + u * bytes;
             uint32_t b[2][4];
             ldmatrix4(b[0], rows + place(token, lane >> 3));
             ldmatrix4(b[1], rows + place(token, 4 + (lane >> 3)));
@@ -368,7 +397,7 @@ __device__ __forceinline__ void down_few(const AdapterParams& p, const Piece& t,
 }
 
 template <bool BF16, int R>
-__global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_constant__ AdapterParams p)
+__global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_constant__ AdapterParams p, const __grid_constant__ Maps maps)
 {
     extern __shared__ unsigned char smem[];
     __shared__ Shared sm;
@@ -431,45 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
             if (lane == 0) umma::mbar_arrive(&sm.d_empty[d]);
             ++tiles;
         }
-    } else if (warp < kProduct) {
+    } else if (warp == kCopier) {
         Ring<R> at;
-        // this thread's piece of every 16th row; rows 16 apart are swizzled alike
-        const int row0 = (tid - kWorkers * 32) >> 3, piece = tid & 7;
-        const uint32_t spot = place(row0, piece);
-        while (walk.next(p, t)) {
-            const uint16_t* x = p.x + (size_t)t.start * p.x_stride;
-            const uint16_t* w = p.down + (size_t)t.id * p.rank * p.d_in;
-            if (t.n <= kFew) {
-                const int shift = units_shift<R>(t);
-                for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
-                    wait(sm, &sm.empty[at.stage], at.phase ^ 1);
-                    copy_few(t, shift, c * kK, p.d_in, w, x, p.x_stride, base + at.stage * kStageBytes<R>);
-                    copies_arrive(&sm.full[at.stage]);
-                }
-                continue;
-            }
-            x += (size_t)row0 * p.x_stride + t.c_lo * kK + piece * 8;
-            w += (size_t)row0 * p.d_in + t.c_lo * kK + piece * 8;
-            for (int c = t.c_lo; c < t.c_hi; ++c, x += kK, w += kK, at.next()) {
-                wait(sm, &sm.empty[at.stage], at.phase ^ 1);
-                const uint32_t stage = base + at.stage * kStageBytes<R> + spot;
-                const bool there = c * kK + piece * 8 < p.d_in;
-#pragma unroll
-                for (int i = 0; i < kTile / 16; ++i)
-                    if (row0 + i * 16 < t.n) copy16(stage + i * 16 * kRow, there ? x + (size_t)(i * 16) * p.x_stride : p.x, there);
-#pragma unroll
-                for (int i = 0; i < R / 16; ++i)
-                    if (row0 + i * 16 < t.rank) copy16(stage + kTokenBytes + i * 16 * kRow, there ? w + (size_t)(i * 16) * p.d_in : p.x, there);
-                copies_arrive(&sm.full[at.stage]);
-            }
-        }
-        copies_wait();
+        while (walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at);
     } else {
         Ring<R> at;
         uint32_t tiles = 0;
         while (walk.next(p, t)) {
             if (t.n <= kFew) {
-                const int step = 1 << units_shift<R>(t);
+                const int step = 1 << units_shift<R>(p);
                 for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
                     wait(sm, &sm.full[at.stage], at.phase);
                     if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
@@ -480,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
             if (tiles >= 2) wait(sm, &sm.d_empty[d], ((tiles >> 1) - 1) & 1);
             for (int c = t.c_lo; c < t.c_hi; ++c, at.next()) {
                 wait(sm, &sm.full[at.stage], at.phase);
-                umma::fence_proxy_async();  // the copies are generic writes
                 umma::fence_after_sync();
                 __syncwarp();
                 if (umma::elect_one()) {
@@ -529,29 +527,29 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     lo = narrow2<BF16>(isfinite(ha) ? a - ha : 0.0f, isfinite(hb) ? b - hb : 0.0f);
 }
 
-// y_out of a tile of up to 8 tokens; h[8][rank] in shared memory (zeros behind the tokens and the rank).  16 channels
-// by 8 tokens a product; the warps share a stage's blocks of 16 channels.
+// y_out of a tile of up to 8 tokens; h[8][rank] in shared memory (zeros behind the tokens and the rank).  The tokens are
+// 8 of a product's 16 rows, by 8 channels.  A stage is one warp's, so that eight of them are under way at a time.
 template <bool BF16, int R>
-__device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, const float* h, Shared& sm, unsigned char* ring, Ring<R>& at)
+__device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, const float* h, Shared& sm, const unsigned char* ring, unsigned char* result,
+                                       Ring<R>& at, uint32_t& turn)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, steps = (t.rank + 15) / 16;
-    const int shift = units_shift<R>(t), unit_bytes = (t.rank + t.n) * kRow;
-    // h as the products' second operand: column lane / 4, rows 16 k + 2 (lane & 3) + {0, 1, 8, 9}
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, steps = (t.rank + 15) / 16, q = lane >> 2;
+    const int shift = units_shift<R>(p), bytes = unit_bytes(p);
+    // h as the products' first operand: row lane / 4, columns 16 k + 2 (lane & 3) + {0, 1, 8, 9}
     uint32_t hi[R / 16][2], lo[R / 16][2];
-    float factor[2];  // of tokens 2 (lane & 3) and the next
+    float factor = t.id < 0 ? 0.0f : __ldg(p.scales + t.id);
     {
-        const float* mine = h + (lane >> 2) * p.rank + (lane & 3) * 2;
-        float inv = 1.0f, scale = t.id < 0 ? 0.0f : __ldg(p.scales + t.id);
+        const float* mine = h + q * p.rank + (lane & 3) * 2;
+        float inv = 1.0f;
         if (!BF16) {
             // a token's largest value to [1, 2), as in operand()
             float most = 0.0f;
-            for (int k = 0; k < steps * 2; ++k)
-                if (k * 8 < t.rank) most = fmaxf(most, fmaxf(fabsf(mine[k * 8]), fabsf(mine[k * 8 + 1])));
+            for (int k = 0; k * 8 < t.rank; ++k) most = fmaxf(most, fmaxf(fabsf(mine[k * 8]), fabsf(mine[k * 8 + 1])));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
             const int exponent = min(max((int)(__float_as_uint(most) >> 23) - 127, -126), 126);
             inv = __uint_as_float((uint32_t)(127 - exponent) << 23);
-            scale *= __uint_as_float((uint32_t)(127 + exponent) << 23);
+            factor *= __uint_as_float((uint32_t)(127 + exponent) << 23);
         }
 #pragma unroll
         for (int k = 0; k < R / 16; ++k)
@@ -560,44 +558,52 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
                 const bool there = k * 16 + e * 8 < t.rank;  // (h's rows are a multiple of 8 long)
                 split2<BF16>(there ? mine[k * 16 + e * 8] * inv : 0.0f, there ? mine[k * 16 + e * 8 + 1] * inv : 0.0f, hi[k][e], lo[k][e]);
             }
-        factor[0] = __shfl_sync(0xffffffffu, scale, (lane & 3) * 8);
-        factor[1] = __shfl_sync(0xffffffffu, scale, (lane & 3) * 8 + 4);
     }
     for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
+        // every warp waits for every stage and hands it back: none is ever a whole turn of the ring from another
         wait(sm, &sm.full[at.stage], at.phase);
-        const int blocks = min(1 << shift, t.c_hi - c) * 4;
-        for (int b = warp; b < blocks; b += kWorkers) {
-            unsigned char* rows = ring + at.stage * kStageBytes<R> + (b >> 2) * unit_bytes;
-            const int piece = (b & 3) * 2;  // the first of the block's two 16-byte pieces
-            if (t.rank > 0) {
-                float acc[4] = {};
+        const int units = turn++ % kWorkers == warp ? min(1 << shift, t.c_hi - c) : 0;
+        const unsigned char* rows = ring + at.stage * kStageBytes<R>;
+        for (int u = 0; u < units; ++u, rows += bytes) {
+            float acc[8][4] = {};
 #pragma unroll
-                for (int k = 0; k < R / 16; ++k)
-                    if (k < steps) {
-                        // rows behind the rank are the last one again: their h is 0, and what follows a tile's rows in its
-                        // stage may not be finite
-                        uint32_t a[4];
-                        ldmatrix4_t(a, rows + place(min(k * 16 + (lane & 7) + (lane >> 4 << 3), t.rank - 1), piece + (lane >> 3 & 1)));
-                        mma<BF16>(acc, a, hi[k][0], hi[k][1]);
-                        mma<BF16>(acc, a, lo[k][0], lo[k][1]);
-                    }
+            for (int k = 0; k < R / 16; ++k)
+                if (k < steps) {
+                    // rows behind the rank are the last one again: their h is 0, and what lies there may not be finite
+                    const int row = min(k * 16 + (lane & 15), t.rank - 1);
+                    const uint32_t a[4] = {hi[k][0], 0, hi[k][1], 0}, a2[4] = {lo[k][0], 0, lo[k][1], 0};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int q = (lane & 3) * 2 + (e & 1), channel = (lane >> 2) + (e >> 1) * 8;
-                    if (q < t.n) {
-                        uint16_t* y = reinterpret_cast<uint16_t*>(rows + place(t.rank + q, piece + (channel >> 3))) + (channel & 7);
-                        const float v = BF16 ? __uint_as_float((uint32_t)*y << 16) : __half2float(*reinterpret_cast<const __half*>(y));
-                        *y = (uint16_t)narrow2<BF16>(fmaf(factor[e & 1], acc[e], v), 0.0f);
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t b[4];
+                        ldmatrix4_t(b, rows + place(row, 2 * j + (lane >> 4)));
+                        mma<BF16>(acc[2 * j], a, b[0], b[1]);
+                        mma<BF16>(acc[2 * j + 1], a, b[2], b[3]);
+                        mma<BF16>(acc[2 * j], a2, b[0], b[1]);
+                        mma<BF16>(acc[2 * j + 1], a2, b[2], b[3]);
                     }
                 }
-                __syncwarp();
+            if (q < t.n) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t y = *reinterpret_cast<const uint32_t*>(rows + place(p.rank + q, j) + (lane & 3) * 4);
+                    float2 v;
+                    if (BF16) v = make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+                    else v = __half22float2(*reinterpret_cast<const __half2*>(&y));
+                    *reinterpret_cast<uint32_t*>(result + place(q, j) + (lane & 3) * 4) =
+                        t.rank > 0 ? narrow2<BF16>(fmaf(factor, acc[j][0], v.x), fmaf(factor, acc[j][1], v.y)) : y;
+                }
             }
-            const int q = lane >> 1, o = (c + (b >> 2)) * kK + (piece + (lane & 1)) * 8;
-            if (q < t.n && o < p.d_out)
-                __stcs(reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o),
-                       *reinterpret_cast<const uint4*>(rows + place(t.rank + q, piece + (lane & 1))));
+            __syncwarp();
+            const int o = (c + u) * kK + (lane & 7) * 8;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int token = i * 4 + (lane >> 3);
+                if (token < t.n && o < p.d_out)
+                    __stcs(reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + token) * p.out_stride + o),
+                           *reinterpret_cast<const uint4*>(result + place(token, lane & 7)));
+            }
+            __syncwarp();  // the results are read
         }
-        __syncwarp();
         if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
     }
 }
@@ -683,13 +689,14 @@ __device__ __forceinline__ void store_rows(const AdapterParams& p, const Piece& 
 }
 
 template <bool BF16, int R>
-__global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_constant__ AdapterParams p)
+__global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_constant__ AdapterParams p, const __grid_constant__ Maps maps)
 {
     extern __shared__ unsigned char smem[];
     __shared__ Shared sm;
     __shared__ float few[kFew * R];
     constexpr int kColumns = 512;
     unsigned char* ring = smem + ((1024 - (umma::smem_u32(smem) & 1023)) & 1023);
+    const uint32_t base = umma::smem_u32(ring);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // all of adapter_down's CTAs have their TMEM, as those of this kernel when the next one starts
     shared_begin(sm, kColumns, kWorkers + 1);  // a stage is free: every worker is done with it, the product warp is past it
@@ -701,9 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
     if (walk.s >= p.n_seq) walk.hi = walk.at;
     Piece t;
     if (warp < kWorkers) {
+        unsigned char* result = ring + kStages<R> * kStageBytes<R> + warp * kResultBytes;
         const int half = warp >> 2, row0 = (warp & 3) * 32, row = row0 + lane, spot = row0 + (lane >> 2), piece = half * 4 + (lane & 3);
         Ring<R> at;
-        uint32_t m = 0;  // chunks of products
+        uint32_t m = 0, turn = 0;  // chunks of products; stages of few tokens
         while (walk.next(p, t)) {
             const int2 b = t.rank > 0 ? p.parts[t.slot] : make_int2(0, 0);
             if (t.n <= kFew) {
@@ -712,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
                     few[i] = i % p.rank < t.rank ? h_at(p, t, b, i / p.rank, i % p.rank) : 0.0f;
                 for (int i = t.n * p.rank + tid; i < kFew * p.rank; i += kWorkers * 32) few[i] = 0.0f;
                 workers_sync();
-                up_few<BF16, R>(p, t, few, sm, ring, at);
+                up_few<BF16, R>(p, t, few, sm, ring, result, at, turn);
                 continue;
             }
             if (t.rank == 0) {  // y as it is
@@ -738,74 +746,48 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
                     float v[32];
                     umma::tmem_ld32(sm.tmem + (row0 << 16) + kColumnD + d * kK + half * 32, v);
                     umma::tmem_wait_ld();
-                    unsigned char* tile = ring + at.stage * kStageBytes<R>;
+                    const unsigned char* tile = ring + at.stage * kStageBytes<R>;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint4* q = reinterpret_cast<uint4*>(tile + place(row, half * 4 + i));
                         float f[8];
-                        widen8<BF16>(*q, f);
+                        widen8<BF16>(*reinterpret_cast<const uint4*>(tile + place(row, half * 4 + i)), f);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) f[e] = fmaf(factor, v[i * 8 + e], f[e]);
-                        *q = make_uint4(narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]), narrow2<BF16>(f[4], f[5]), narrow2<BF16>(f[6], f[7]));
+                        *reinterpret_cast<uint4*>(result + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) =
+                            make_uint4(narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]), narrow2<BF16>(f[4], f[5]), narrow2<BF16>(f[6], f[7]));
                     }
                     umma::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) umma::mbar_arrive(&sm.d_empty[d]);
-                    store_rows(p, t, c, tile, out, spot, piece);
-                    __syncwarp();
-                    if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
+                    if (lane == 0) {
+                        umma::mbar_arrive(&sm.d_empty[d]);
+                        umma::mbar_arrive(&sm.empty[at.stage]);
+                    }
+                    // 64 bytes of 8 rows at a time
+                    if (c * kK + piece * 8 < p.d_out) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = i * 8 + (lane >> 2);
+                            if (row0 + r < t.n)
+                                __stcs(reinterpret_cast<uint4*>(out + (size_t)(i * 8) * p.out_stride),
+                                       *reinterpret_cast<const uint4*>(result + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4)));
+                        }
+                    }
+                    __syncwarp();  // the results are read
                 } else if (lane == 0) {
                     umma::mbar_arrive(&sm.d_empty[d]);
                     umma::mbar_arrive(&sm.empty[at.stage]);
                 }
             }
         }
-    } else if (warp < kProduct) {
+    } else if (warp == kCopier) {
         Ring<R> at;
-        const uint32_t base = umma::smem_u32(ring);
-        // this thread's piece of every 16th row; rows 16 apart are swizzled alike
-        const int row0 = (tid - kWorkers * 32) >> 3, piece = tid & 7;
-        const uint32_t spot = place(row0, piece);
-        while (walk.next(p, t)) {
-            const int rows = (t.rank + 15) / 16 * 16;
-            const uint16_t* y = p.y + (size_t)t.start * p.y_stride;
-            const uint16_t* w = p.up + (size_t)max(t.id, 0) * p.rank * p.d_out;
-            if (t.n <= kFew) {
-                const int shift = units_shift<R>(t);
-                for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
-                    wait(sm, &sm.empty[at.stage], at.phase ^ 1);
-                    copy_few(t, shift, c * kK, p.d_out, w, y, p.y_stride, base + at.stage * kStageBytes<R>);
-                    copies_arrive(&sm.full[at.stage]);
-                }
-                continue;
-            }
-            y += (size_t)row0 * p.y_stride + t.c_lo * kK + piece * 8;
-            w += (size_t)row0 * p.d_out + t.c_lo * kK + piece * 8;
-            for (int c = t.c_lo; c < t.c_hi; ++c, y += kK, w += kK, at.next()) {
-                wait(sm, &sm.empty[at.stage], at.phase ^ 1);
-                const uint32_t stage = base + at.stage * kStageBytes<R> + spot;
-                const bool there = c * kK + piece * 8 < p.d_out;
-#pragma unroll
-                for (int i = 0; i < kTile / 16; ++i)
-                    if (row0 + i * 16 < t.n) copy16(stage + i * 16 * kRow, there ? y + (size_t)(i * 16) * p.y_stride : p.y, there);
-                // rows behind the rank: zeros, as what was there may not be finite
-#pragma unroll
-                for (int i = 0; i < R / 16; ++i)
-                    if (row0 + i * 16 < rows) {
-                        const bool mine = there && row0 + i * 16 < t.rank;
-                        copy16(stage + kTokenBytes + i * 16 * kRow, mine ? w + (size_t)(i * 16) * p.d_out : p.y, mine);
-                    }
-                copies_arrive(&sm.full[at.stage]);
-            }
-        }
-        copies_wait();
+        while (walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at);
     } else {
-        const uint32_t base = umma::smem_u32(ring);
         Ring<R> at;
         uint32_t m = 0, tiles = 0;
         while (walk.next(p, t)) {
             if (t.n <= kFew || t.rank == 0) {
-                const int step = t.n <= kFew ? 1 << units_shift<R>(t) : 1;
+                const int step = t.n <= kFew ? 1 << units_shift<R>(p) : 1;
                 for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
                     wait(sm, &sm.full[at.stage], at.phase);
                     if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
@@ -819,7 +801,12 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
                 const uint32_t slot = m % kRing;
                 wait(sm, &sm.full[at.stage], at.phase);
                 if (m >= kRing) wait(sm, &sm.d_empty[slot], (m / kRing - 1) & 1);
-                umma::fence_proxy_async();  // the copies are generic writes
+                if (t.rank & 15) {
+                    // rows behind the rank that the last step takes in: zeros, as what is there may not be finite
+                    uint4* rows = reinterpret_cast<uint4*>(ring + at.stage * kStageBytes<R> + kTokenBytes + t.rank * kRow);
+                    for (int i = lane; i < (steps * 16 - t.rank) * (kRow / 16); i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+                    umma::fence_proxy_async();
+                }
                 umma::fence_after_sync();
                 __syncwarp();
                 if (umma::elect_one()) {
@@ -839,13 +826,35 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
     shared_end(sm, kColumns, p.status + kCtas + blockIdx.x);
 }
 
+// rows of `width` 16-bit values, `stride` apart, in boxes of 64 of them by `box_rows` rows, swizzled over 128 bytes
+bool encode_map(CUtensorMap& map, const void* rows, bool bf16, int width, int64_t n_rows, int64_t stride, int box_rows)
+{
+    const auto encode = tensor_map_encoder();
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)n_rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {kK, (cuuint32_t)box_rows}, ones[2] = {1, 1};
+    return encode && encode(&map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(rows), dims, strides, box,
+                            ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_maps(Maps& maps, const AdapterParams& p, const uint16_t* tokens, int64_t stride, const uint16_t* weights, int width)
+{
+    const int64_t rows = (int64_t)p.n_adapters * p.rank;
+    return encode_map(maps.tokens, tokens, p.bf16, width, p.T, stride, kTile) && encode_map(maps.few, tokens, p.bf16, width, p.T, stride, kFew) &&
+           // without adapters nothing is read through these
+           encode_map(maps.weights, rows ? weights : tokens, p.bf16, width, rows ? rows : 1, rows ? width : stride, p.rank) &&
+           encode_map(maps.weights8, rows ? weights : tokens, p.bf16, width, rows ? rows : 1, rows ? width : stride, 8);
+}
+
 template <bool BF16, int R>
 cudaError_t launch_rank(const AdapterParams& p, cudaStream_t stream)
 {
+    Maps in, out;
+    if (!encode_maps(in, p, p.x, p.x_stride, p.down, p.d_in) || !encode_maps(out, p, p.y, p.y_stride, p.up, p.d_out)) return cudaErrorNotSupported;
     cudaError_t e = cudaFuncSetAttribute(adapter_down_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(adapter_up_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
-    if (e == cudaSuccess) e = launch_k(adapter_down_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p);
-    if (e == cudaSuccess) e = launch_k(adapter_up_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p);
+    if (e == cudaSuccess) e = launch_k(adapter_down_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p, in);
+    if (e == cudaSuccess) e = launch_k(adapter_up_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p, out);
     return e;
 }
 

@@ -76,6 +76,7 @@ gdn_status gdn_adapter_add(int32_t dtype, int32_t n_seq, int32_t T, const int32_
     if (dtype != GDN_FP16 && dtype != GDN_BF16) return fail(GDN_ERR_INVALID_ARG, "unknown activation type %d", dtype);
     if ((st = check_batch(n_seq, T, cu_seqlens)) != GDN_OK) return st;
     if (n_adapters < 0) return fail(GDN_ERR_INVALID_ARG, "negative n_adapters");
+    if (n_adapters > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "n_adapters=%d above 2^20", n_adapters);
     if (!known_rank(rank)) return fail(GDN_ERR_UNSUPPORTED, "rank=%d must be a multiple of 8 up to 128", rank);
     if (!known_width(d_in) || !known_width(d_out)) return fail(GDN_ERR_UNSUPPORTED, "d_in=%d and d_out=%d must be multiples of 8 up to 65536", d_in, d_out);
     if ((st = check_stride("x", x_stride, d_in)) != GDN_OK) return st;

@@ -38,10 +38,8 @@
 // CTA's start takes 6 and each of its units 3 between the last tile of one and the first of the next.  Tried and
 // left out: 8 softmax warps of 208 registers (1090 us for the chunk's call, 790), a warp of products for each
 // half (830), waits that spin (829 and more).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "gdn_kv_attn.cuh"
+#include "gdn_tensor_map.cuh"
 #include "umma.cuh"
 
 namespace gdn {
@@ -985,18 +983,6 @@ done:
     __syncthreads();
     if (warp == kMmaWarp) umma::tmem_dealloc(tmem, kTmemCols);
 #undef GDN_KV_WAIT
-}
-
-// the driver's tensor map encoder, looked up once (the library links the runtime alone)
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
-{
-    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(e == cudaSuccess && found == cudaDriverEntryPointSuccess ? f : nullptr);
-    }();
-    return encode;
 }
 
 template <int D, bool BF16, bool E4M3>

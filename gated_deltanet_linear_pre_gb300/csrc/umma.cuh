@@ -273,6 +273,16 @@ __device__ __forceinline__ void tensor_g2s_3d(void* dst, const void* map, int x,
         : "memory");
 }
 
+// the same of a 2-D tensor map
+__device__ __forceinline__ void tensor_g2s_2d(uint32_t dst, const void* map, int x, int y, uint64_t* mbar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        :
+        : "r"(dst), "l"(map), "r"(x), "r"(y), "r"(smem_u32(mbar))
+        : "memory");
+}
+
 // global -> L2 only (no completion tracking); src 16-byte aligned, bytes a multiple of 16
 __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes)
 {
