@@ -50,9 +50,10 @@ template <int R> constexpr int kStageBytes = kTokenBytes + R * kRow;
 constexpr int kResultBytes = 32 * 64;                // a worker's part of a chunk of y_out, on its way out
 template <int R> constexpr size_t kSmem = 1024 + kStages<R> * kStageBytes<R> + kWorkers * kResultBytes;
 
-// tensor maps of the tokens (x or y): boxes of kTile and of kFew rows; and of the weights: boxes of `rank` and of 8 rows
+// Tensor maps of the tokens (x or y) and of the weights: boxes of 64 channels by kTile or kFew tokens, by `rank` or 8 rows
+// of weights; and the last three for several units at once (a copy has its price, whatever its size).
 struct Maps {
-    CUtensorMap tokens, few, weights, weights8;
+    CUtensorMap tokens, few, weights, weights8, few_units, weights_units, weights8_units;
 };
 
 __device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers * 32) : "memory"); }
@@ -280,46 +281,67 @@ struct Ring {
     }
 };
 
-// Tiles of few tokens: 2^units_shift units a stage, as many as fit, at most 8.  A unit is `rank` rows of weights and
-// kFew of tokens behind them.
-__device__ __forceinline__ int unit_bytes(const AdapterParams& p) { return (p.rank + kFew) * kRow; }
+// Tiles of few tokens: 2^units_shift units a stage, as many as fit, at most 8: the units' rows of weights, `rank` each,
+// then their rows of tokens, kFew each.
+template <int R>
+__host__ __device__ __forceinline__ int units_shift(int rank)
+{
+    const int fit = kStageBytes<R> / ((rank + kFew) * kRow);
+    return fit >= 8 ? 3 : fit >= 4 ? 2 : fit >= 2 ? 1 : 0;
+}
+
+// Where a stage of few tokens holds its rows: row r of unit u's weights at u * unit + (r / 8) * group + place(r & 7, .),
+// row q of its tokens at tokens + u * kFew rows + place(q, .).
+struct FewLayout {
+    int unit, group, tokens;
+    bool low;  // the adapter's rank is far below the others': its rows are copied 8 at a time
+    int step;  // units of a stage
+};
 
 template <int R>
-__device__ __forceinline__ int units_shift(const AdapterParams& p)
+__device__ __forceinline__ FewLayout few_layout(const AdapterParams& p, const Piece& t)
 {
-    const int fit = kStageBytes<R> / unit_bytes(p);
-    return fit >= 8 ? 3 : fit >= 4 ? 2 : fit >= 2 ? 1 : 0;
+    const int step = 1 << units_shift<R>(p.rank);
+    const bool low = t.rank * 2 <= p.rank;
+    return {low ? 8 * kRow : p.rank * kRow, low ? step * 8 * kRow : 8 * kRow, step * p.rank * kRow, low, step};
 }
 
 // The copying warp: the stages of a piece, in order.  Rows of tokens behind the tile's own are its neighbours', and
 // what comes of them goes nowhere.
 template <int R>
-__device__ __forceinline__ void copy_piece(const AdapterParams& p, const Piece& t, const Maps& maps, Shared& sm, uint32_t base, Ring<R>& at)
+__device__ __forceinline__ void copy_piece(const AdapterParams& p, const Piece& t, int width, const Maps& maps, Shared& sm, uint32_t base, Ring<R>& at)
 {
     const bool few = t.n <= kFew;
-    const int step = few ? 1 << units_shift<R>(p) : 1, rows = (t.rank + 7) & ~7, row = t.rank > 0 ? t.id * p.rank : 0;
-    const auto weights = [&](uint32_t to, int c, uint64_t* full) {
-        if (rows == p.rank) umma::tensor_g2s_2d(to, &maps.weights, c * kK, row, full);
-        else
-            for (int r = 0; r < rows; r += 8) umma::tensor_g2s_2d(to + r * kRow, &maps.weights8, c * kK, row + r, full);
-    };
+    const FewLayout layout = few_layout<R>(p, t);
+    const int step = few ? layout.step : 1, whole = width / kK, row = t.rank > 0 ? t.id * p.rank : 0;
+    const int rows = t.rank == 0 ? 0 : few && layout.low ? (t.rank + 7) & ~7 : p.rank;
     for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
         wait(sm, &sm.empty[at.stage], at.phase ^ 1);
         __syncwarp();
         if (umma::elect_one()) {
-            uint32_t to = base + at.stage * kStageBytes<R>;
+            const uint32_t to = base + at.stage * kStageBytes<R>, tokens = to + layout.tokens;
             uint64_t* full = &sm.full[at.stage];
-            if (few) {
-                const int units = min(step, t.c_hi - c);
-                umma::mbar_arrive_expect_tx(full, units * (rows + kFew) * kRow);
-                for (int u = 0; u < units; ++u, to += unit_bytes(p)) {
-                    weights(to, c + u, full);
-                    umma::tensor_g2s_2d(to + p.rank * kRow, &maps.few, (c + u) * kK, t.start, full);
-                }
-            } else {
+            if (!few) {
                 umma::mbar_arrive_expect_tx(full, kTokenBytes + rows * kRow);
                 umma::tensor_g2s_2d(to, &maps.tokens, c * kK, t.start, full);
-                weights(to + kTokenBytes, c, full);
+                if (rows) umma::tensor_g2s_2d(to + kTokenBytes, &maps.weights, c * kK, row, full);
+            } else if (c + step <= whole || t.c_hi <= whole) {
+                umma::mbar_arrive_expect_tx(full, step * (rows + kFew) * kRow);
+                if (layout.low)
+                    for (int r = 0; r < rows; r += 8) umma::tensor_g2s_3d(to + r / 8 * layout.group, &maps.weights8_units, 0, row + r, c, full);
+                else
+                    umma::tensor_g2s_3d(to, &maps.weights_units, 0, row, c, full);
+                umma::tensor_g2s_3d(tokens, &maps.few_units, 0, t.start, c, full);
+            } else {  // the last channels are fewer than 64
+                const int units = min(step, t.c_hi - c);
+                umma::mbar_arrive_expect_tx(full, units * (rows + kFew) * kRow);
+                for (int u = 0; u < units; ++u) {
+                    if (layout.low)
+                        for (int r = 0; r < rows; r += 8) umma::tensor_g2s_2d(to + u * layout.unit + r / 8 * layout.group, &maps.weights8, (c + u) * kK, row + r, full);
+                    else
+                        umma::tensor_g2s_2d(to + u * layout.unit, &maps.weights, (c + u) * kK, row, full);
+                    umma::tensor_g2s_2d(tokens + u * kFew * kRow, &maps.few, (c + u) * kK, t.start, full);
+                }
             }
         }
         __syncwarp();
@@ -358,22 +380,23 @@ __device__ __forceinline__ void down_few(const AdapterParams& p, const Piece& t,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int blocks = (t.rank + 15) / 16, groups = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks;  // of 16 rows; warps that take different ones
     const int block = warp % groups, unit = warp / groups, step = kWorkers / groups;
-    const int shift = units_shift<R>(p), bytes = unit_bytes(p);
+    const FewLayout layout = few_layout<R>(p, t);
     // a lane's row of either operand; rows that are not there are others again, and what comes of them goes nowhere
-    const int row = min(block * 16 + (lane & 15), t.rank - 1), token = p.rank + min(lane & 7, t.n - 1);
+    const int row = min(block * 16 + (lane & 15), t.rank - 1), token = min(lane & 7, t.n - 1);
     float acc[4] = {};
-    for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
+    for (int c = t.c_lo; c < t.c_hi; c += layout.step, at.next()) {
         wait(sm, &sm.full[at.stage], at.phase);
-        const int units = block < blocks ? min(1 << shift, t.c_hi - c) : 0;
+        const int units = block < blocks ? min(layout.step, t.c_hi - c) : 0;
         for (int u = unit; u < units; u += step) {
-            const unsigned char* rows = ring + at.stage * kStageBytes<R> + u * bytes;
+            const unsigned char *stage = ring + at.stage * kStageBytes<R>, *tokens = stage + layout.tokens + u * kFew * kRow;
+            const unsigned char* rows = stage + u * layout.unit + (row >> 3) * layout.group;
             uint32_t b[2][4];
-            ldmatrix4(b[0], rows + place(token, lane >> 3));
-            ldmatrix4(b[1], rows + place(token, 4 + (lane >> 3)));
+            ldmatrix4(b[0], tokens + place(token, lane >> 3));
+            ldmatrix4(b[1], tokens + place(token, 4 + (lane >> 3)));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 uint32_t a[4];
-                ldmatrix4(a, rows + place(row, 2 * k + (lane >> 4)));
+                ldmatrix4(a, rows + place(row & 7, 2 * k + (lane >> 4)));
                 mma<BF16>(acc, a, b[k >> 1][2 * (k & 1)], b[k >> 1][2 * (k & 1) + 1]);
             }
         }
@@ -462,13 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
         }
     } else if (warp == kCopier) {
         Ring<R> at;
-        while (walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at);
+        while (walk.next(p, t)) copy_piece<R>(p, t, p.d_in, maps, sm, base, at);
     } else {
         Ring<R> at;
         uint32_t tiles = 0;
         while (walk.next(p, t)) {
             if (t.n <= kFew) {
-                const int step = 1 << units_shift<R>(p);
+                const int step = 1 << units_shift<R>(p.rank);
                 for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
                     wait(sm, &sm.full[at.stage], at.phase);
                     if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
@@ -534,7 +557,7 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
                                        Ring<R>& at, uint32_t& turn)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, steps = (t.rank + 15) / 16, q = lane >> 2;
-    const int shift = units_shift<R>(p), bytes = unit_bytes(p);
+    const FewLayout layout = few_layout<R>(p, t);
     // h as the products' first operand: row lane / 4, columns 16 k + 2 (lane & 3) + {0, 1, 8, 9}
     uint32_t hi[R / 16][2], lo[R / 16][2];
     float factor = t.id < 0 ? 0.0f : __ldg(p.scales + t.id);
@@ -559,12 +582,12 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
                 split2<BF16>(there ? mine[k * 16 + e * 8] * inv : 0.0f, there ? mine[k * 16 + e * 8 + 1] * inv : 0.0f, hi[k][e], lo[k][e]);
             }
     }
-    for (int c = t.c_lo; c < t.c_hi; c += 1 << shift, at.next()) {
+    for (int c = t.c_lo; c < t.c_hi; c += layout.step, at.next()) {
         // every warp waits for every stage and hands it back: none is ever a whole turn of the ring from another
         wait(sm, &sm.full[at.stage], at.phase);
-        const int units = turn++ % kWorkers == warp ? min(1 << shift, t.c_hi - c) : 0;
-        const unsigned char* rows = ring + at.stage * kStageBytes<R>;
-        for (int u = 0; u < units; ++u, rows += bytes) {
+        const int units = turn++ % kWorkers == warp ? min(layout.step, t.c_hi - c) : 0;
+        const unsigned char *rows = ring + at.stage * kStageBytes<R>, *tokens = rows + layout.tokens;
+        for (int u = 0; u < units; ++u, rows += layout.unit, tokens += kFew * kRow) {
             float acc[8][4] = {};
 #pragma unroll
             for (int k = 0; k < R / 16; ++k)
@@ -575,7 +598,7 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t b[4];
-                        ldmatrix4_t(b, rows + place(row, 2 * j + (lane >> 4)));
+                        ldmatrix4_t(b, rows + (row >> 3) * layout.group + place(row & 7, 2 * j + (lane >> 4)));
                         mma<BF16>(acc[2 * j], a, b[0], b[1]);
                         mma<BF16>(acc[2 * j + 1], a, b[2], b[3]);
                         mma<BF16>(acc[2 * j], a2, b[0], b[1]);
@@ -585,7 +608,7 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
             if (q < t.n) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint32_t y = *reinterpret_cast<const uint32_t*>(rows + place(p.rank + q, j) + (lane & 3) * 4);
+                    const uint32_t y = *reinterpret_cast<const uint32_t*>(tokens + place(q, j) + (lane & 3) * 4);
                     float2 v;
                     if (BF16) v = make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
                     else v = __half22float2(*reinterpret_cast<const __half2*>(&y));
@@ -781,13 +804,13 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
         }
     } else if (warp == kCopier) {
         Ring<R> at;
-        while (walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at);
+        while (walk.next(p, t)) copy_piece<R>(p, t, p.d_out, maps, sm, base, at);
     } else {
         Ring<R> at;
         uint32_t m = 0, tiles = 0;
         while (walk.next(p, t)) {
             if (t.n <= kFew || t.rank == 0) {
-                const int step = t.n <= kFew ? 1 << units_shift<R>(p) : 1;
+                const int step = t.n <= kFew ? 1 << units_shift<R>(p.rank) : 1;
                 for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
                     wait(sm, &sm.full[at.stage], at.phase);
                     if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
@@ -826,31 +849,34 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
     shared_end(sm, kColumns, p.status + kCtas + blockIdx.x);
 }
 
-// rows of `width` 16-bit values, `stride` apart, in boxes of 64 of them by `box_rows` rows, swizzled over 128 bytes
-bool encode_map(CUtensorMap& map, const void* rows, bool bf16, int width, int64_t n_rows, int64_t stride, int box_rows)
+// Rows of `width` 16-bit values, `stride` apart, in boxes of 64 of them by `box_rows` rows, swizzled over 128 bytes; with
+// `units` the whole units of 64 as a dimension of their own, so many to a box.
+bool encode_map(CUtensorMap& map, const void* rows, bool bf16, int width, int64_t n_rows, int64_t stride, int box_rows, int units = 0)
 {
     const auto encode = tensor_map_encoder();
-    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)n_rows}, strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {kK, (cuuint32_t)box_rows}, ones[2] = {1, 1};
-    return encode && encode(&map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(rows), dims, strides, box,
-                            ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t dims[3] = {(cuuint64_t)(units ? kK : width), (cuuint64_t)n_rows, (cuuint64_t)(width / kK)}, strides[2] = {(cuuint64_t)stride * 2, kRow};
+    const cuuint32_t box[3] = {kK, (cuuint32_t)box_rows, (cuuint32_t)units}, ones[3] = {1, 1, 1};
+    return encode && encode(&map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, units ? 3 : 2, const_cast<void*>(rows), dims,
+                            strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_maps(Maps& maps, const AdapterParams& p, const uint16_t* tokens, int64_t stride, const uint16_t* weights, int width)
+bool encode_maps(Maps& maps, const AdapterParams& p, const uint16_t* tokens, int64_t stride, const uint16_t* weights, int width, int units)
 {
     const int64_t rows = (int64_t)p.n_adapters * p.rank;
-    return encode_map(maps.tokens, tokens, p.bf16, width, p.T, stride, kTile) && encode_map(maps.few, tokens, p.bf16, width, p.T, stride, kFew) &&
-           // without adapters nothing is read through these
-           encode_map(maps.weights, rows ? weights : tokens, p.bf16, width, rows ? rows : 1, rows ? width : stride, p.rank) &&
-           encode_map(maps.weights8, rows ? weights : tokens, p.bf16, width, rows ? rows : 1, rows ? width : stride, 8);
+    const auto of_tokens = [&](CUtensorMap& map, int box, int u = 0) { return encode_map(map, tokens, p.bf16, width, p.T, stride, box, u); };
+    // without adapters nothing is read through these
+    const auto of_weights = [&](CUtensorMap& map, int box, int u = 0) { return rows == 0 || encode_map(map, weights, p.bf16, width, rows, width, box, u); };
+    return of_tokens(maps.tokens, kTile) && of_tokens(maps.few, kFew) && of_weights(maps.weights, p.rank) && of_weights(maps.weights8, 8) &&
+           (width < kK || (of_tokens(maps.few_units, kFew, units) && of_weights(maps.weights_units, p.rank, units) && of_weights(maps.weights8_units, 8, units)));
 }
 
 template <bool BF16, int R>
 cudaError_t launch_rank(const AdapterParams& p, cudaStream_t stream)
 {
-    Maps in, out;
-    if (!encode_maps(in, p, p.x, p.x_stride, p.down, p.d_in) || !encode_maps(out, p, p.y, p.y_stride, p.up, p.d_out)) return cudaErrorNotSupported;
+    Maps in{}, out{};
+    const int units = 1 << units_shift<R>(p.rank);
+    if (!encode_maps(in, p, p.x, p.x_stride, p.down, p.d_in, units) || !encode_maps(out, p, p.y, p.y_stride, p.up, p.d_out, units)) return cudaErrorNotSupported;
     cudaError_t e = cudaFuncSetAttribute(adapter_down_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(adapter_up_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = launch_k(adapter_down_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p, in);
