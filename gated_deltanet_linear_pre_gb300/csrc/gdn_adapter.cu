@@ -45,15 +45,15 @@ constexpr int kParts = 16;                           // ranges that a tile is cu
 constexpr int kRing = 4;                             // chunks' products in TMEM
 constexpr int kColumnD = 256;                        // adapter_up's TMEM: h in the first R columns, products from here on
 
-template <int R> constexpr int kStages = R > 64 ? 6 : 8;
+template <int R> constexpr int kStages = R > 64 ? 5 : 8;  // (6 for R of 128 leave too little L1: 110 us for 102, 8192 tokens, 2048 to 10240)
 template <int R> constexpr int kStageBytes = kTokenBytes + R * kRow;
 constexpr int kResultBytes = 32 * 64;                // a worker's part of a chunk of y_out, on its way out
 template <int R> constexpr size_t kSmem = 1024 + kStages<R> * kStageBytes<R> + kWorkers * kResultBytes;
 
 // Tensor maps of the tokens (x or y) and of the weights: boxes of 64 channels by kTile or kFew tokens, by `rank` or 8 rows
-// of weights; and the last three for several units at once (a copy has its price, whatever its size).
+// of weights; and the last four for several units at once (a copy has its price, whatever its size).
 struct Maps {
-    CUtensorMap tokens, few, weights, weights8, few_units, weights_units, weights8_units;
+    CUtensorMap tokens, few, weights, weights8, few_units, weights_units, few_low, weights8_low;
 };
 
 __device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers * 32) : "memory"); }
@@ -63,18 +63,55 @@ __device__ __forceinline__ uint32_t place(int row, int piece) { return row * kRo
 
 // ---- who does what --------------------------------------------------------------
 
-// What a unit costs, in steps of some 2 ns: rows of 128 bytes copied and written, fitted to the time that a CTA took for
-// ranges of one kind (8 prompts with rank 64, a prompt with rank 72 beside drafts of ranks 8 to 112).  A tile of more
-// than a few tokens copies the rows of a whole one.
-__host__ __device__ __forceinline__ int cost_few(int rank) { return 24 + (rank + 8) * 3 / 2; }
-__host__ __device__ __forceinline__ int cost_in(int n, int rank) { return n <= 0 || rank <= 0 ? 0 : n <= kFew ? cost_few(rank) : 144 + rank; }
-__host__ __device__ __forceinline__ int cost_out(int n, int rank, bool copied)
+// Tiles of few tokens: several units a stage.  Row r of unit u's weights lies at u * unit + (r / 8) * group +
+// place(r & 7, .), row q of its tokens at tokens + u * kFew rows + place(q, .).
+struct FewLayout {
+    int step;   // units of a stage
+    bool low;   // an adapter of a lower rank than the others', whose rows are copied 8 at a time, kLowUnits units at once
+    int rows;   // of weights that are copied
+    int unit, group, tokens;
+};
+
+constexpr int kLowUnits = 4;
+
+// the rank that the kernels are built for, and units of full rank that fit a stage
+__host__ __device__ __forceinline__ int built_rank(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+__host__ __device__ __forceinline__ int full_units(int rank)
 {
-    return n <= 0 || (rank <= 0 && !copied) ? 0 : n <= kFew ? cost_few(rank) + 2 * n : rank > 0 ? 160 + 2 * rank : 192;
+    const int fit = (kTile + built_rank(rank)) / (rank + kFew);
+    return fit >= 8 ? 8 : fit >= 4 ? 4 : fit >= 2 ? 2 : 1;
 }
 
+__device__ __forceinline__ FewLayout few_layout(const AdapterParams& p, int rank)
+{
+    FewLayout f;
+    const int rows = (rank + 7) & ~7, full = full_units(p.rank);
+    f.low = (rows + kFew) * kLowUnits <= kTile + built_rank(p.rank) && (full < kLowUnits || rows * 2 <= p.rank);
+    f.step = f.low ? kLowUnits : full;
+    f.rows = f.low || rank == 0 ? rows : p.rank;
+    f.unit = f.low ? 8 * kRow : p.rank * kRow;
+    f.group = f.low ? kLowUnits * 8 * kRow : 8 * kRow;
+    f.tokens = f.step * f.rows * kRow;
+    return f;
+}
+
+// What a unit costs, in steps of some 2 ns, fitted to the time that CTAs took for ranges of one kind (8 prompts with
+// rank 64; a prompt with rank 72 beside drafts of ranks 8 to 112).  A tile of more than a few tokens copies the rows of a
+// whole one.  Few tokens' units take their weights from HBM, and the ring's turn where they are small.
+__device__ __forceinline__ int cost_few(const AdapterParams& p, int rank)
+{
+    const FewLayout f = few_layout(p, rank);
+    return max(184 / f.step, (f.rows + kFew) * 3 / 2);
+}
+__host__ __device__ __forceinline__ int cost_in_tile(int rank) { return 144 + rank; }
+__host__ __device__ __forceinline__ int cost_out_tile(int rank) { return rank > 0 ? 160 + 2 * rank : 192; }
+
 template <bool IN>
-__device__ __forceinline__ int unit_cost(const AdapterParams& p, int n, int rank) { return IN ? cost_in(n, rank) : cost_out(n, rank, p.y_out != p.y); }
+__device__ __forceinline__ int unit_cost(const AdapterParams& p, int n, int rank)
+{
+    if (n <= 0 || (rank == 0 && (IN || p.y_out == p.y))) return 0;
+    return n <= kFew ? cost_few(p, rank) : IN ? cost_in_tile(rank) : cost_out_tile(rank);
+}
 
 __device__ __forceinline__ int rank_of(const AdapterParams& p, int s, int& id)
 {
@@ -189,7 +226,7 @@ __device__ __forceinline__ void find_starts(const AdapterParams& p, PlanSmem& sm
         AdapterStart& start = i ? out : sm.start;
         // a CTA is worth 4 units of the largest tiles, and a tile is cut into at most kParts + 1
         const int chunks = i ? p.chunks_out : p.chunks_in;
-        const int most = i ? cost_out(kTile, p.rank, true) : cost_in(kTile, p.rank);
+        const int most = i ? cost_out_tile(p.rank) : cost_in_tile(p.rank);
         const int64_t share = max((total[i] + kCtas - 1) / kCtas, (int64_t)most * max(4, (chunks + kParts - 1) / kParts)), lo = share * blockIdx.x;
         if (threadIdx.x == 0) {
             start.share = share;
@@ -281,40 +318,15 @@ struct Ring {
     }
 };
 
-// Tiles of few tokens: 2^units_shift units a stage, as many as fit, at most 8: the units' rows of weights, `rank` each,
-// then their rows of tokens, kFew each.
-template <int R>
-__host__ __device__ __forceinline__ int units_shift(int rank)
-{
-    const int fit = kStageBytes<R> / ((rank + kFew) * kRow);
-    return fit >= 8 ? 3 : fit >= 4 ? 2 : fit >= 2 ? 1 : 0;
-}
-
-// Where a stage of few tokens holds its rows: row r of unit u's weights at u * unit + (r / 8) * group + place(r & 7, .),
-// row q of its tokens at tokens + u * kFew rows + place(q, .).
-struct FewLayout {
-    int unit, group, tokens;
-    bool low;  // the adapter's rank is far below the others': its rows are copied 8 at a time
-    int step;  // units of a stage
-};
-
-template <int R>
-__device__ __forceinline__ FewLayout few_layout(const AdapterParams& p, const Piece& t)
-{
-    const int step = 1 << units_shift<R>(p.rank);
-    const bool low = t.rank * 2 <= p.rank;
-    return {low ? 8 * kRow : p.rank * kRow, low ? step * 8 * kRow : 8 * kRow, step * p.rank * kRow, low, step};
-}
-
 // The copying warp: the stages of a piece, in order.  Rows of tokens behind the tile's own are its neighbours', and
 // what comes of them goes nowhere.
 template <int R>
 __device__ __forceinline__ void copy_piece(const AdapterParams& p, const Piece& t, int width, const Maps& maps, Shared& sm, uint32_t base, Ring<R>& at)
 {
     const bool few = t.n <= kFew;
-    const FewLayout layout = few_layout<R>(p, t);
+    const FewLayout layout = few_layout(p, t.rank);
     const int step = few ? layout.step : 1, whole = width / kK, row = t.rank > 0 ? t.id * p.rank : 0;
-    const int rows = t.rank == 0 ? 0 : few && layout.low ? (t.rank + 7) & ~7 : p.rank;
+    const int rows = few ? layout.rows : t.rank == 0 ? 0 : t.rank <= 8 ? 8 : p.rank;
     for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
         wait(sm, &sm.empty[at.stage], at.phase ^ 1);
         __syncwarp();
@@ -324,14 +336,14 @@ __device__ __forceinline__ void copy_piece(const AdapterParams& p, const Piece& 
             if (!few) {
                 umma::mbar_arrive_expect_tx(full, kTokenBytes + rows * kRow);
                 umma::tensor_g2s_2d(to, &maps.tokens, c * kK, t.start, full);
-                if (rows) umma::tensor_g2s_2d(to + kTokenBytes, &maps.weights, c * kK, row, full);
+                if (rows) umma::tensor_g2s_2d(to + kTokenBytes, rows == 8 ? &maps.weights8 : &maps.weights, c * kK, row, full);
             } else if (c + step <= whole || t.c_hi <= whole) {
                 umma::mbar_arrive_expect_tx(full, step * (rows + kFew) * kRow);
                 if (layout.low)
-                    for (int r = 0; r < rows; r += 8) umma::tensor_g2s_3d(to + r / 8 * layout.group, &maps.weights8_units, 0, row + r, c, full);
+                    for (int r = 0; r < rows; r += 8) umma::tensor_g2s_3d(to + r / 8 * layout.group, &maps.weights8_low, 0, row + r, c, full);
                 else
                     umma::tensor_g2s_3d(to, &maps.weights_units, 0, row, c, full);
-                umma::tensor_g2s_3d(tokens, &maps.few_units, 0, t.start, c, full);
+                umma::tensor_g2s_3d(tokens, layout.low ? &maps.few_low : &maps.few_units, 0, t.start, c, full);
             } else {  // the last channels are fewer than 64
                 const int units = min(step, t.c_hi - c);
                 umma::mbar_arrive_expect_tx(full, units * (rows + kFew) * kRow);
@@ -380,7 +392,7 @@ __device__ __forceinline__ void down_few(const AdapterParams& p, const Piece& t,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int blocks = (t.rank + 15) / 16, groups = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks;  // of 16 rows; warps that take different ones
     const int block = warp % groups, unit = warp / groups, step = kWorkers / groups;
-    const FewLayout layout = few_layout<R>(p, t);
+    const FewLayout layout = few_layout(p, t.rank);
     // a lane's row of either operand; rows that are not there are others again, and what comes of them goes nowhere
     const int row = min(block * 16 + (lane & 15), t.rank - 1), token = min(lane & 7, t.n - 1);
     float acc[4] = {};
@@ -491,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
         uint32_t tiles = 0;
         while (walk.next(p, t)) {
             if (t.n <= kFew) {
-                const int step = 1 << units_shift<R>(p.rank);
+                const int step = few_layout(p, t.rank).step;
                 for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
                     wait(sm, &sm.full[at.stage], at.phase);
                     if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
@@ -557,7 +569,7 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
                                        Ring<R>& at, uint32_t& turn)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, steps = (t.rank + 15) / 16, q = lane >> 2;
-    const FewLayout layout = few_layout<R>(p, t);
+    const FewLayout layout = few_layout(p, t.rank);
     // h as the products' first operand: row lane / 4, columns 16 k + 2 (lane & 3) + {0, 1, 8, 9}
     uint32_t hi[R / 16][2], lo[R / 16][2];
     float factor = t.id < 0 ? 0.0f : __ldg(p.scales + t.id);
@@ -588,32 +600,35 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
         const int units = turn++ % kWorkers == warp ? min(layout.step, t.c_hi - c) : 0;
         const unsigned char *rows = ring + at.stage * kStageBytes<R>, *tokens = rows + layout.tokens;
         for (int u = 0; u < units; ++u, rows += layout.unit, tokens += kFew * kRow) {
-            float acc[8][4] = {};
+#pragma unroll 1
+            for (int part = 0; part < 8; part += 4) {  // 32 channels at a time: what the registers hold beside h
+                float acc[4][4] = {};
 #pragma unroll
-            for (int k = 0; k < R / 16; ++k)
-                if (k < steps) {
-                    // rows behind the rank are the last one again: their h is 0, and what lies there may not be finite
-                    const int row = min(k * 16 + (lane & 15), t.rank - 1);
-                    const uint32_t a[4] = {hi[k][0], 0, hi[k][1], 0}, a2[4] = {lo[k][0], 0, lo[k][1], 0};
+                for (int k = 0; k < R / 16; ++k)
+                    if (k < steps) {
+                        // rows behind the rank are the last one again: their h is 0, and what lies there may not be finite
+                        const int row = min(k * 16 + (lane & 15), t.rank - 1);
+                        const uint32_t a[4] = {hi[k][0], 0, hi[k][1], 0}, a2[4] = {lo[k][0], 0, lo[k][1], 0};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t b[4];
+                            ldmatrix4_t(b, rows + (row >> 3) * layout.group + place(row & 7, part + 2 * j + (lane >> 4)));
+                            mma<BF16>(acc[2 * j], a, b[0], b[1]);
+                            mma<BF16>(acc[2 * j + 1], a, b[2], b[3]);
+                            mma<BF16>(acc[2 * j], a2, b[0], b[1]);
+                            mma<BF16>(acc[2 * j + 1], a2, b[2], b[3]);
+                        }
+                    }
+                if (q < t.n) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        uint32_t b[4];
-                        ldmatrix4_t(b, rows + (row >> 3) * layout.group + place(row & 7, 2 * j + (lane >> 4)));
-                        mma<BF16>(acc[2 * j], a, b[0], b[1]);
-                        mma<BF16>(acc[2 * j + 1], a, b[2], b[3]);
-                        mma<BF16>(acc[2 * j], a2, b[0], b[1]);
-                        mma<BF16>(acc[2 * j + 1], a2, b[2], b[3]);
+                        const uint32_t y = *reinterpret_cast<const uint32_t*>(tokens + place(q, part + j) + (lane & 3) * 4);
+                        float2 v;
+                        if (BF16) v = make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+                        else v = __half22float2(*reinterpret_cast<const __half2*>(&y));
+                        *reinterpret_cast<uint32_t*>(result + place(q, part + j) + (lane & 3) * 4) =
+                            t.rank > 0 ? narrow2<BF16>(fmaf(factor, acc[j][0], v.x), fmaf(factor, acc[j][1], v.y)) : y;
                     }
-                }
-            if (q < t.n) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t y = *reinterpret_cast<const uint32_t*>(tokens + place(q, j) + (lane & 3) * 4);
-                    float2 v;
-                    if (BF16) v = make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
-                    else v = __half22float2(*reinterpret_cast<const __half2*>(&y));
-                    *reinterpret_cast<uint32_t*>(result + place(q, j) + (lane & 3) * 4) =
-                        t.rank > 0 ? narrow2<BF16>(fmaf(factor, acc[j][0], v.x), fmaf(factor, acc[j][1], v.y)) : y;
                 }
             }
             __syncwarp();
@@ -644,6 +659,25 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N])
         umma::tmem_st16(at, v);
 }
 
+// A tile's products take 16 rows of `up` a step.  Where the last step has only 8 rows of its own (the rank rounded up to
+// 8s) it takes the 8 in front of them again, with zeros for their h: rows behind the rank may not be finite.
+struct Steps {
+    int count, last;  // steps; the first row of the last one
+    __device__ explicit Steps(int rank)
+    {
+        const int rows = (rank + 7) & ~7;
+        count = (rows + 15) / 16;
+        last = rows > 8 ? rows - 16 : 0;
+    }
+    __device__ int first_row(int step) const { return step == count - 1 ? last : step * 16; }
+    // the row whose h stands in column j of the operand; -1: none
+    __device__ int row_of(int j) const
+    {
+        if (j < (count - 1) * 16 || last == (count - 1) * 16) return j;
+        return j >= count * 16 ? -1 : j >= count * 16 - 8 ? j - 8 : -1;
+    }
+};
+
 // h of a tile as the products' first operand: hi in TMEM columns [0, R / 2), lo behind it, two values a column.
 // The workers: two threads a row, each half of its columns.
 template <bool BF16, int R>
@@ -655,23 +689,27 @@ __device__ __forceinline__ void operand(const AdapterParams& p, const Piece& t, 
     float v[kMine];
 #pragma unroll
     for (int j = 0; j < kMine; ++j) v[j] = 0.0f;
+    const Steps steps(t.rank);
     if (row < t.n)
         for (int r = b.x; r <= b.y; ++r) {
             const size_t from = r == b.x ? (size_t)t.start : (size_t)p.T + (size_t)r * kTile;
-            const float4* src = reinterpret_cast<const float4*>(p.h + (from + row) * p.rank + col);
+            const float* src = p.h + (from + row) * p.rank;
 #pragma unroll
-            for (int j = 0; j < kMine; j += 4)
-                if (col + j < t.rank) {  // a row holds a multiple of 8 values
-                    const float4 f = src[j / 4];
+            for (int j = 0; j < kMine; j += 4) {
+                const int at = steps.row_of(col + j);
+                if (at >= 0 && at < t.rank) {  // a row holds a multiple of 8 values
+                    const float4 f = *reinterpret_cast<const float4*>(src + at);
                     v[j] += f.x;
                     v[j + 1] += f.y;
                     v[j + 2] += f.z;
                     v[j + 3] += f.w;
                 }
+            }
         }
+    if (t.rank & 3)
 #pragma unroll
-    for (int j = 0; j < kMine; ++j)
-        if (col + j >= t.rank) v[j] = 0.0f;
+        for (int j = 0; j < kMine; ++j)
+            if (steps.row_of(col + j) >= t.rank) v[j] = 0.0f;
     float inv = 1.0f, factor = __ldg(p.scales + t.id);
     if (!BF16) {
         // a row's largest value to [1, 2): fp16 has 5 bits of exponent
@@ -810,24 +848,25 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
         uint32_t m = 0, tiles = 0;
         while (walk.next(p, t)) {
             if (t.n <= kFew || t.rank == 0) {
-                const int step = t.n <= kFew ? 1 << units_shift<R>(p.rank) : 1;
+                const int step = t.n <= kFew ? few_layout(p, t.rank).step : 1;
                 for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
                     wait(sm, &sm.full[at.stage], at.phase);
                     if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
                 }
                 continue;
             }
-            const int steps = (t.rank + 15) / 16;
+            const Steps steps(t.rank);
+            const int zeros = t.rank <= 8 ? 16 - t.rank : -t.rank & 7;  // rows behind the rank that a step takes in all the same
             wait(sm, &sm.h_full, tiles & 1);
             ++tiles;
             for (int c = t.c_lo; c < t.c_hi; ++c, ++m, at.next()) {
                 const uint32_t slot = m % kRing;
                 wait(sm, &sm.full[at.stage], at.phase);
                 if (m >= kRing) wait(sm, &sm.d_empty[slot], (m / kRing - 1) & 1);
-                if (t.rank & 15) {
-                    // rows behind the rank that the last step takes in: zeros, as what is there may not be finite
+                // (rows 8 to 15 of an adapter of 8 are copied by nobody: once a stage is enough)
+                if (zeros > 0 && ((t.rank & 7) || c - t.c_lo < kStages<R>)) {
                     uint4* rows = reinterpret_cast<uint4*>(ring + at.stage * kStageBytes<R> + kTokenBytes + t.rank * kRow);
-                    for (int i = lane; i < (steps * 16 - t.rank) * (kRow / 16); i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+                    for (int i = lane; i < zeros * (kRow / 16); i += 32) rows[i] = make_uint4(0, 0, 0, 0);
                     umma::fence_proxy_async();
                 }
                 umma::fence_after_sync();
@@ -835,8 +874,11 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
                 if (umma::elect_one()) {
                     const uint32_t d = sm.tmem + kColumnD + slot * kK;
                     const uint64_t db = umma::desc_sw128(base + at.stage * kStageBytes<R> + kTokenBytes, 16, 1024);
-                    for (int k = 0; k < steps; ++k) umma::mma_ts(d, sm.tmem + 8 * k, db + k * (2048 >> 4), idesc<BF16, 128, kK>(true), k > 0);
-                    for (int k = 0; k < steps; ++k) umma::mma_ts(d, sm.tmem + R / 2 + 8 * k, db + k * (2048 >> 4), idesc<BF16, 128, kK>(true), 1);
+                    for (int k = 0; k < steps.count; ++k) {
+                        const uint64_t rows = db + steps.first_row(k) * (kRow >> 4);
+                        umma::mma_ts(d, sm.tmem + 8 * k, rows, idesc<BF16, 128, kK>(true), k > 0);
+                        umma::mma_ts(d, sm.tmem + R / 2 + 8 * k, rows, idesc<BF16, 128, kK>(true), 1);
+                    }
                     umma::commit(&sm.d_full[slot]);
                     umma::mbar_arrive(&sm.empty[at.stage]);
                 }
@@ -868,14 +910,15 @@ bool encode_maps(Maps& maps, const AdapterParams& p, const uint16_t* tokens, int
     // without adapters nothing is read through these
     const auto of_weights = [&](CUtensorMap& map, int box, int u = 0) { return rows == 0 || encode_map(map, weights, p.bf16, width, rows, width, box, u); };
     return of_tokens(maps.tokens, kTile) && of_tokens(maps.few, kFew) && of_weights(maps.weights, p.rank) && of_weights(maps.weights8, 8) &&
-           (width < kK || (of_tokens(maps.few_units, kFew, units) && of_weights(maps.weights_units, p.rank, units) && of_weights(maps.weights8_units, 8, units)));
+           (width < kK || (of_tokens(maps.few_units, kFew, units) && of_weights(maps.weights_units, p.rank, units) && of_tokens(maps.few_low, kFew, kLowUnits) &&
+                         of_weights(maps.weights8_low, 8, kLowUnits)));
 }
 
 template <bool BF16, int R>
 cudaError_t launch_rank(const AdapterParams& p, cudaStream_t stream)
 {
     Maps in{}, out{};
-    const int units = 1 << units_shift<R>(p.rank);
+    const int units = full_units(p.rank);
     if (!encode_maps(in, p, p.x, p.x_stride, p.down, p.d_in, units) || !encode_maps(out, p, p.y, p.y_stride, p.up, p.d_out, units)) return cudaErrorNotSupported;
     cudaError_t e = cudaFuncSetAttribute(adapter_down_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(adapter_up_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
