@@ -600,9 +600,10 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
         const int units = turn++ % kWorkers == warp ? min(layout.step, t.c_hi - c) : 0;
         const unsigned char *rows = ring + at.stage * kStageBytes<R>, *tokens = rows + layout.tokens;
         for (int u = 0; u < units; ++u, rows += layout.unit, tokens += kFew * kRow) {
+            constexpr int kPart = R > 64 ? 4 : 8;  // pieces at a time: what the registers hold beside h
 #pragma unroll 1
-            for (int part = 0; part < 8; part += 4) {  // 32 channels at a time: what the registers hold beside h
-                float acc[4][4] = {};
+            for (int part = 0; part < 8; part += kPart) {
+                float acc[kPart][4] = {};
 #pragma unroll
                 for (int k = 0; k < R / 16; ++k)
                     if (k < steps) {
@@ -610,7 +611,7 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
                         const int row = min(k * 16 + (lane & 15), t.rank - 1);
                         const uint32_t a[4] = {hi[k][0], 0, hi[k][1], 0}, a2[4] = {lo[k][0], 0, lo[k][1], 0};
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
+                        for (int j = 0; j < kPart / 2; ++j) {
                             uint32_t b[4];
                             ldmatrix4_t(b, rows + (row >> 3) * layout.group + place(row & 7, part + 2 * j + (lane >> 4)));
                             mma<BF16>(acc[2 * j], a, b[0], b[1]);
@@ -621,7 +622,7 @@ __device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, c
                     }
                 if (q < t.n) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < kPart; ++j) {
                         const uint32_t y = *reinterpret_cast<const uint32_t*>(tokens + place(q, part + j) + (lane & 3) * 4);
                         float2 v;
                         if (BF16) v = make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
