@@ -553,10 +553,22 @@ def _here(t, name: str, device):
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _table(t, name: str):
+def _on(t, name, dtype, shape, device):
+    """As _dense, of a tensor on `device`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dense(t, name, dtype, shape)
+    _here(t, name, device)
+
+
+def _table(t, name: str, device):
     """Device pointer and row stride of an int32 table [rows, max_pages] with contiguous rows."""
     if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.dim() != 2 or not t.is_cuda:
         raise TypeError(f"{name} must be an int32 CUDA tensor [rows, max_pages]")
+    _here(t, name, device)
     rows, width = t.shape
     stride, one = t.stride()
     if one != 1 and width > 1:
@@ -584,21 +596,19 @@ def gdn_kv_remap(page_table, page_tokens: int, n_pages: int, parent, keep, need,
     max_pages] and gets room for need[r].  Writes table_out [n_rows, max_pages], the pages that gdn_kv_copy is to
     copy (copy_from, copy_to [n_rows], -1 where there is none) and info [2]: pages named, pages missing."""
     device = torch.cuda.current_device()
-    tp, ts = _table(page_table, "page_table")
-    op, os_ = _table(table_out, "table_out")
+    tp, ts = _table(page_table, "page_table", device)
+    op, os_ = _table(table_out, "table_out", device)
     n_old, width = page_table.shape
     n = table_out.shape[0]
     if table_out.shape[1] != width:
         raise ValueError(f"table_out has {table_out.shape[1]} entries a row, page_table {width}")
     per_row = (n,)
-    args = [_dense(t, name, _I32, shape) for t, name, shape in (
-        (parent, "parent", per_row), (keep, "keep", per_row), (need, "need", per_row), (copy_from, "copy_from", per_row),
-        (copy_to, "copy_to", per_row), (info, "info", (2,)))]
+    pp, kp, np_ = (_on(parent, "parent", _I32, per_row, device), _on(keep, "keep", _I32, per_row, device),
+                   _on(need, "need", _I32, per_row, device))
+    a, b = _on(copy_from, "copy_from", _I32, per_row, device), _on(copy_to, "copy_to", _I32, per_row, device)
+    ip = _on(info, "info", _I32, (2,), device)
     wp, wb = _scratch(workspace, device)
-    for t, name in ((page_table, "page_table"), (parent, "parent"), (keep, "keep"), (need, "need"),
-                    (table_out, "table_out"), (copy_from, "copy_from"), (copy_to, "copy_to"), (info, "info")):
-        _here(t, name, device)
-    st = lib().gdn_kv_remap(page_tokens, n_pages, width, n_old, tp, ts, n, *args[:3], op, os_, *args[3:], wp, wb,
+    st = lib().gdn_kv_remap(page_tokens, n_pages, width, n_old, tp, ts, n, pp, kp, np_, op, os_, a, b, ip, wp, wb,
                             _stream(stream))
     if st:
         _check("gdn_kv_remap", st)
@@ -612,18 +622,15 @@ def gdn_kv_compact(page_table, n_pages: int, table_out, copy_from, copy_to, info
     """Rename pages so that those in use are the pool's first: writes table_out (page_table itself will do), the
     moves for gdn_kv_copy (copy_from, copy_to [n_pages // 2], -1 behind them) and info [2]: pages in use, moves."""
     device = torch.cuda.current_device()
-    tp, ts = _table(page_table, "page_table")
-    op, os_ = _table(table_out, "table_out")
+    tp, ts = _table(page_table, "page_table", device)
+    op, os_ = _table(table_out, "table_out", device)
     n, width = shape = page_table.shape
     if table_out.shape != shape:
         raise ValueError(f"table_out has shape {tuple(table_out.shape)}, expected {tuple(shape)}")
     lists = (n_pages // 2,)
-    a, b = _dense(copy_from, "copy_from", _I32, lists), _dense(copy_to, "copy_to", _I32, lists)
-    ip = _dense(info, "info", _I32, (2,))
+    a, b = _on(copy_from, "copy_from", _I32, lists, device), _on(copy_to, "copy_to", _I32, lists, device)
+    ip = _on(info, "info", _I32, (2,), device)
     wp, wb = _scratch(workspace, device)
-    for t, name in ((page_table, "page_table"), (table_out, "table_out"), (copy_from, "copy_from"),
-                    (copy_to, "copy_to"), (info, "info")):
-        _here(t, name, device)
     st = lib().gdn_kv_compact(n_pages, width, n, tp, ts, op, os_, a, b, ip, wp, wb, _stream(stream))
     if st:
         _check("gdn_kv_compact", st)
@@ -661,9 +668,7 @@ def gdn_kv_copy(caches, copy_from, copy_to, stream=None):
     if not isinstance(copy_from, torch.Tensor) or copy_from.dim() != 1:
         raise TypeError("copy_from must be an int32 CUDA tensor [n]")
     shape = copy_from.shape
-    a, b = _dense(copy_from, "copy_from", _I32, shape), _dense(copy_to, "copy_to", _I32, shape)
-    _here(copy_from, "copy_from", device)
-    _here(copy_to, "copy_to", device)
+    a, b = _on(copy_from, "copy_from", _I32, shape, device), _on(copy_to, "copy_to", _I32, shape, device)
     st = lib().gdn_kv_copy(caches.array, len(caches.caches), shape[0], a, b, _stream(stream))
     if st:
         _check("gdn_kv_copy", st)
@@ -674,16 +679,23 @@ _GATES = {"none": 0, "linear": 1, "sigmoid": 2, "silu": 3}
 _X_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _rows2(t, name: str, dtype, shape):
-    """Device pointer and row stride of a tensor [T, width] with contiguous rows."""
+def _rows2(t, name: str, dtype, shape, device):
+    """Device pointer and row stride of a tensor [T, width] on `device` with contiguous rows."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.is_cuda:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device:
             st, one = t.stride()
             if one == 1 or shape[1] == 1:
-                return (t.data_ptr() if t.numel() else None), (st if shape[0] > 1 else shape[1])
+                return (t.data_ptr() if shape[0] else None), (st if shape[0] > 1 else shape[1])
             raise ValueError(f"{name}'s rows must be contiguous")
     except AttributeError:
         pass
+    _refuse_rows(t, name, dtype, shape, device)
+
+
+def _refuse_rows(t, name, dtype, shape, device):
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        _here(t, name, device)
+        t = t.contiguous()
     _refuse(t, name, dtype, shape)
 
 
@@ -703,24 +715,20 @@ def gdn_block_norm(x, y, gate, gate_kind: str, scale: float, post_weight, pre_we
         raise ValueError(f"gate_kind must be one of {sorted(_GATES)}")
     device = torch.cuda.current_device()
     shape = T, width = x.shape
-    xp, xs = _rows2(x, "x", x.dtype, shape)
+    xp, xs = _rows2(x, "x", x.dtype, shape, device)
     yp = gp = None
     ys = gs = 0
     if y is not None:
-        yp, ys = _rows2(y, "y", dt, shape)
+        yp, ys = _rows2(y, "y", dt, shape, device)
     if gate is not None:
         one = gate.shape == (1, width)
-        gp, gs = _rows2(gate, "gate", dt, (1, width) if one else shape)
+        gp, gs = _rows2(gate, "gate", dt, (1, width) if one else shape, device)
         if one:
             gs = 0
-    post = None if post_weight is None else _dense(post_weight, "post_weight", _F32, (width,))
-    pre = None if pre_weight is None else _dense(pre_weight, "pre_weight", _F32, (width,))
-    xo = None if x_out is None else _dense(x_out, "x_out", x.dtype, shape)
-    ho = None if h is None else _dense(h, "h", dt, shape)
-    for t, name in ((x, "x"), (y, "y"), (gate, "gate"), (post_weight, "post_weight"), (pre_weight, "pre_weight"),
-                    (x_out, "x_out"), (h, "h")):
-        if t is not None:
-            _here(t, name, device)
+    post = None if post_weight is None else _on(post_weight, "post_weight", _F32, (width,), device)
+    pre = None if pre_weight is None else _on(pre_weight, "pre_weight", _F32, (width,), device)
+    xo = None if x_out is None else _on(x_out, "x_out", x.dtype, shape, device)
+    ho = None if h is None else _on(h, "h", dt, shape, device)
     st = lib().gdn_block_norm(_X_TYPES[x.dtype], _ACT_TYPES[dt], T, width, xp, xs, yp, ys, gp, gs, kind, scale, post,
                               pre, eps, xo, ho, _stream(stream))
     if st:
@@ -742,19 +750,16 @@ def gdn_adapter_add(cu_seqlens, total_tokens, ids, down, up, ranks, scales, x, y
         raise TypeError("down and up must be torch.float16 or torch.bfloat16 tensors [n, rank, d_in] and [n, rank, d_out]")
     n, rank, d_in = down.shape
     d_out = up.shape[2]
-    dp, upp = _dense(down, "down", dt, (n, rank, d_in)), _dense(up, "up", dt, (n, rank, d_out))
-    xp, xs = _rows2(x, "x", dt, (T, d_in))
-    yp, ys = _rows2(y, "y", dt, (T, d_out))
-    op, os_ = _rows2(y_out, "y_out", dt, (T, d_out))
+    dp, upp = _on(down, "down", dt, (n, rank, d_in), device), _on(up, "up", dt, (n, rank, d_out), device)
+    xp, xs = _rows2(x, "x", dt, (T, d_in), device)
+    yp, ys = _rows2(y, "y", dt, (T, d_out), device)
+    op, os_ = _rows2(y_out, "y_out", dt, (T, d_out), device)
     wp, wb = _scratch(workspace, device)
-    rp = None if ranks is None else _dense(ranks, "ranks", _I32, (n,))
-    for t, name in ((cu_seqlens, "cu_seqlens"), (ids, "ids"), (down, "down"), (up, "up"), (ranks, "ranks"), (scales, "scales"),
-                    (x, "x"), (y, "y"), (y_out, "y_out")):
-        if t is not None:
-            _here(t, name, device)
-    st = lib().gdn_adapter_add(_ACT_TYPES[dt], n_seq, T, _dense(cu_seqlens, "cu_seqlens", _I32, (n_seq + 1,)),
-                               _dense(ids, "ids", _I32, (n_seq,)), n, rank, rp, dp, upp, _dense(scales, "scales", _F32, (n,)),
-                               d_in, xp, xs, d_out, yp, ys, op, os_, wp, wb, _stream(stream))
+    rp = None if ranks is None else _on(ranks, "ranks", _I32, (n,), device)
+    st = lib().gdn_adapter_add(_ACT_TYPES[dt], n_seq, T, _on(cu_seqlens, "cu_seqlens", _I32, (n_seq + 1,), device),
+                               _on(ids, "ids", _I32, (n_seq,), device), n, rank, rp, dp, upp,
+                               _on(scales, "scales", _F32, (n,), device), d_in, xp, xs, d_out, yp, ys, op, os_, wp, wb,
+                               _stream(stream))
     if st:
         _check("gdn_adapter_add", st)
 

@@ -177,6 +177,7 @@ struct RemapParams {
     int32_t* owner;
     int32_t* free_list;
     int32_t* first;
+    int32_t* sums;  // [remap_sums]
 };
 
 // pages renamed to the front of the pool
@@ -189,6 +190,7 @@ struct CompactParams {
     int32_t* copy_to;
     int32_t* info;
     int32_t* name;  // workspace: per page, its new number
+    int32_t* sums;  // workspace: [compact_sums]
 };
 
 constexpr int kCopyCaches = 64;  // caches of one launch
@@ -207,6 +209,9 @@ struct CopyParams {
     Cache cache[kCopyCaches];
 };
 
+// words of the workspace for the counts of a large batch's blocks
+size_t remap_sums(int n_pages, int n_rows);
+size_t compact_sums(int n_pages);
 cudaError_t launch_kv_remap(const RemapParams& p, cudaStream_t stream);
 cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t stream);
 cudaError_t launch_kv_copy(const CopyParams& p, cudaStream_t stream);

@@ -192,7 +192,7 @@ size_t words(size_t n) { return align256(n * 4); }
 size_t gdn_kv_remap_workspace_bytes(int32_t n_pages, int32_t n_rows, int32_t max_pages)
 {
     if (n_pages < 1 || n_pages > kMaxPages || n_rows < 0 || max_pages < 0 || (int64_t)n_rows * max_pages > (1 << 30)) return 0;
-    return words(1) + 2 * words(n_pages) + words(n_rows);
+    return words(1) + 2 * words(n_pages) + words(n_rows) + words(gdn::remap_sums(n_pages, n_rows));
 }
 
 gdn_status gdn_kv_remap(int32_t page_tokens, int32_t n_pages, int32_t max_pages, int32_t n_old, const int32_t* page_table,
@@ -227,11 +227,15 @@ gdn_status gdn_kv_remap(int32_t page_tokens, int32_t n_pages, int32_t max_pages,
     p.owner = reinterpret_cast<int32_t*>(ws + words(1));
     p.free_list = reinterpret_cast<int32_t*>(ws + words(1) + words(n_pages));
     p.first = reinterpret_cast<int32_t*>(ws + words(1) + 2 * words(n_pages));
+    p.sums = reinterpret_cast<int32_t*>(ws + words(1) + 2 * words(n_pages) + words(n_rows));
     cudaError_t e = gdn::launch_kv_remap(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_kv_remap launch");
 }
 
-size_t gdn_kv_compact_workspace_bytes(int32_t n_pages) { return n_pages < 1 || n_pages > kMaxPages ? 0 : words(n_pages); }
+size_t gdn_kv_compact_workspace_bytes(int32_t n_pages)
+{
+    return n_pages < 1 || n_pages > kMaxPages ? 0 : words(n_pages) + words(gdn::compact_sums(n_pages));
+}
 
 gdn_status gdn_kv_compact(int32_t n_pages, int32_t max_pages, int32_t n_rows, const int32_t* page_table, int64_t page_table_stride,
                           int32_t* table_out, int64_t table_out_stride, int32_t* copy_from, int32_t* copy_to, int32_t* info,
@@ -258,6 +262,7 @@ gdn_status gdn_kv_compact(int32_t n_pages, int32_t max_pages, int32_t n_rows, co
     p.table = page_table; p.table_stride = page_table_stride; p.out_stride = table_out_stride;
     p.table_out = table_out; p.copy_from = copy_from; p.copy_to = copy_to; p.info = info;
     p.name = static_cast<int32_t*>(workspace);
+    p.sums = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + words(n_pages));
     cudaError_t e = gdn::launch_kv_compact(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_kv_compact launch");
 }

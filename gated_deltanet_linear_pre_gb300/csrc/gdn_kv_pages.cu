@@ -7,12 +7,13 @@
 //   clear  no page has a word
 //   mark   every table entry leaves its word at its page (scattered stores, or a
 //          minimum where rows compete for a page)
-//   scan   running counts over the pages (and, for remap, over the rows): a
-//          cluster's CTAs take equal ranges and exchange their totals
+//   scan   running counts over the pages (and, for remap, over the rows)
 //   fill   the new table, entry by entry
-// A small batch's phases run in one launch of one cluster, with a cluster barrier
-// between them; a large one's in a launch each over the whole GPU, as scattered
-// accesses of 8 SMs would bound them (kOneLaunch).
+// A small batch's phases run in one launch of one cluster, whose CTAs exchange
+// their counts: what bounds it is the chain of loads and barriers.  A large one's
+// run in a launch each over the whole GPU, the scan in two: every block's count,
+// then each block adds up those in front of it.  500 rows of 2048 entries over
+// 914k pages take 31 us (90 with the scan by one cluster of 8).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -30,12 +31,14 @@ constexpr int kNone = 0x7fffffff;  // a page that no entry names
 constexpr int kReader = -1;        // a page that some row reads on
 constexpr int kSegment = 256;      // table entries a warp takes at a time
 constexpr int kPer = kSegment / 32;
-// table entries and pages from which on each phase is a launch of its own
-constexpr int64_t kOneLaunch = 1 << 16;
+// Table entries and pages from which on each phase is a launch of its own.  256 rows of 128 entries take 13.0 us in one
+// launch and 10.0 in five, 512 of 512 32 and 14 (replayed); a call from Python 29 and 40, 34 and 39.
+constexpr int64_t kOneLaunch = 1 << 17;
 
 struct Phases {
-    static constexpr int kClear = 1, kMark = 2, kScan = 4, kFill = 8, kAll = 15;
+    static constexpr int kClear = 0, kMark = 1, kFill = 2;
 };
+constexpr int kBlockPages = kThreads * 4;  // of a large scan's block; of rows, kThreads
 
 // this CTA's place among those that share a phase's work
 struct Share {
@@ -108,6 +111,21 @@ __device__ __forceinline__ int4 words_at(const int* words, int at, int hi)
     if (at + 2 >= hi) w.z = kNone - 1;
     if (at + 3 >= hi) w.w = kNone - 1;
     return w;
+}
+
+// Sum of sums[0 .. block) and of all n, kThreads threads
+__device__ __forceinline__ int sums_exclusive(ScanSmem& sm, const int* sums, int n, int block, int& turn, int& all)
+{
+    int before = 0, total = 0, mine, part;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int v = __ldcg(sums + i);
+        total += v;
+        if (i < block) before += v;
+    }
+    block_exclusive(sm, before, turn++, part);
+    mine = part;
+    block_exclusive(sm, total, turn++, all);
+    return mine;
 }
 
 __device__ __forceinline__ void clear_words(int* words, int n, Share s)
@@ -222,6 +240,56 @@ __device__ __forceinline__ void remap_scan(const RemapParams& p, ScanSmem& sm)
     }
 }
 
+// the scan of a large batch: blocks of pages, then blocks of rows
+__device__ __forceinline__ int page_blocks(int n_pages) { return (n_pages + kBlockPages - 1) / kBlockPages; }
+
+__device__ __forceinline__ void remap_count(const RemapParams& p, ScanSmem& sm)
+{
+    const int pages = page_blocks(p.n_pages), block = blockIdx.x;
+    int mine = 0, all;
+    bool copied;
+    if (block < pages) {
+        mine = frees(words_at(p.owner, block * kBlockPages + (int)threadIdx.x * 4, p.n_pages));
+    } else {
+        const int64_t r = (int64_t)(block - pages) * kThreads + threadIdx.x;
+        if (r < p.n_rows) mine = wanted(p, (int)r, copied);
+    }
+    block_exclusive(sm, mine, 0, all);
+    if (threadIdx.x == 0) p.sums[block] = all;
+}
+
+__device__ __forceinline__ void remap_list(const RemapParams& p, ScanSmem& sm)
+{
+    const int pages = page_blocks(p.n_pages), block = blockIdx.x;
+    int turn = 0, all, total;
+    if (block < pages) {
+        int k = sums_exclusive(sm, p.sums, pages, block, turn, total);
+        const int at = block * kBlockPages + (int)threadIdx.x * 4;
+        const int4 w = words_at(p.owner, at, p.n_pages);
+        k += block_exclusive(sm, frees(w), turn++, all);
+        if (w.x == kNone) p.free_list[k++] = at;
+        if (w.y == kNone) p.free_list[k++] = at + 1;
+        if (w.z == kNone) p.free_list[k++] = at + 2;
+        if (w.w == kNone) p.free_list[k++] = at + 3;
+        if (block == 0) {
+            int n_wanted;
+            sums_exclusive(sm, p.sums + pages, (int)gridDim.x - pages, 0, turn, n_wanted);
+            if (threadIdx.x == 0) {
+                p.header[0] = total;
+                p.info[0] = p.n_pages - total + min(n_wanted, total);
+                p.info[1] = max(n_wanted - total, 0);
+            }
+        }
+    } else {
+        const int first = sums_exclusive(sm, p.sums + pages, (int)gridDim.x - pages, block - pages, turn, total);
+        const int64_t r = (int64_t)(block - pages) * kThreads + threadIdx.x;
+        bool copied = false;
+        const int mine = r < p.n_rows ? wanted(p, (int)r, copied) : 0;
+        const int at = first + block_exclusive(sm, mine, turn++, all);
+        if (r < p.n_rows) p.first[r] = copied ? ~at : at;
+    }
+}
+
 __device__ __forceinline__ void remap_fill(const RemapParams& p, Share s)
 {
     const int lane = threadIdx.x & 31;
@@ -286,6 +354,12 @@ __device__ __forceinline__ void compact_entries(const CompactParams& p, Share s)
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 if (e[i] >= 0) e[i] = __ldcg(p.name + e[i]);
+            // (a large batch's moved pages: their place in the list)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int at = at0 + i * 32 + lane;
+                if (at < p.max_pages && e[i] < -1) e[i] = __ldcg(p.copy_to + (-2 - e[i]));
+            }
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -369,6 +443,52 @@ __device__ __forceinline__ void compact_scan(const CompactParams& p, ScanSmem& s
     }
 }
 
+__device__ __forceinline__ void compact_count(const CompactParams& p, ScanSmem& sm)
+{
+    int all;
+    const int at = blockIdx.x * kBlockPages + (int)threadIdx.x * 4;
+    block_exclusive(sm, min(4, max(0, p.n_pages - at)) - frees(words_at(p.name, at, p.n_pages)), 0, all);
+    if (threadIdx.x == 0) p.sums[blockIdx.x] = all;
+}
+
+__device__ __forceinline__ void compact_list(const CompactParams& p, ScanSmem& sm)
+{
+    const int tid = threadIdx.x, block = blockIdx.x;
+    int turn = 0, all, used;
+    const int before = sums_exclusive(sm, p.sums, (int)gridDim.x, block, turn, used);
+    // pages in use in front of `used`: the blocks there, and the block that it falls into up to it
+    int below, unused, cut = 0;
+    const int edge = used / kBlockPages;
+    below = sums_exclusive(sm, p.sums, (int)gridDim.x, edge, turn, unused);
+    {
+        const int at = edge * kBlockPages + tid * 4;
+        const int4 w = words_at(p.name, at, min(used, p.n_pages));
+        if (at < used) cut = min(4, used - at) - frees(w);
+        block_exclusive(sm, cut, turn++, all);
+        below += all;
+    }
+    const int n_moved = used - below, lo = block * kBlockPages, at = lo + tid * 4;
+    const int4 w = words_at(p.name, at, p.n_pages);
+    const int c[4] = {moved_or_hole(w.x, at, used), moved_or_hole(w.y, at + 1, used), moved_or_hole(w.z, at + 2, used), moved_or_hole(w.w, at + 3, used)};
+    const int k = block_exclusive(sm, c[0] + c[1] + c[2] + c[3], turn++, all);
+    // pages to move in front of this block, and holes
+    int f = max(before - below, 0) + (k & 0xffff), t = min(lo, used) - min(before, below) + (k >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (c[i] & 0xffff) {
+            p.copy_from[f] = at + i;
+            p.name[at + i] = -2 - f++;
+        }
+        if (c[i] >> 16) p.copy_to[t++] = at + i;
+    }
+    for (int64_t i = (int64_t)block * kThreads + tid; i < p.n_pages / 2; i += (int64_t)gridDim.x * kThreads)
+        if (i >= n_moved) p.copy_from[i] = p.copy_to[i] = -1;
+    if (block == 0 && tid == 0) {
+        p.info[0] = used;
+        p.info[1] = n_moved;
+    }
+}
+
 // ---- launches -------------------------------------------------------------------
 
 __device__ __forceinline__ void clear(const RemapParams& p, Share s) { clear_words(p.owner, p.n_pages, s); }
@@ -380,8 +500,13 @@ __device__ __forceinline__ void mark(const CompactParams& p, Share s) { compact_
 __device__ __forceinline__ void scan(const CompactParams& p, ScanSmem& sm) { compact_scan(p, sm); }
 __device__ __forceinline__ void fill(const CompactParams& p, Share s) { compact_entries<true>(p, s); }
 
-// all phases, or the scan alone, in one cluster
-template <typename Params, int PHASES>
+__device__ __forceinline__ void count(const RemapParams& p, ScanSmem& sm) { remap_count(p, sm); }
+__device__ __forceinline__ void list(const RemapParams& p, ScanSmem& sm) { remap_list(p, sm); }
+__device__ __forceinline__ void count(const CompactParams& p, ScanSmem& sm) { compact_count(p, sm); }
+__device__ __forceinline__ void list(const CompactParams& p, ScanSmem& sm) { compact_list(p, sm); }
+
+// all phases in one cluster
+template <typename Params>
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) pages_cluster_kernel(Params p)
 {
     __shared__ ScanSmem sm;
@@ -389,17 +514,13 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) pages_clu
     pdl_wait();
     cg::cluster_group cluster = cg::this_cluster();
     const Share s{(int)cluster.block_rank(), kCluster};
-    if (PHASES & Phases::kClear) {
-        clear(p, s);
-        cluster.sync();
-    }
-    if (PHASES & Phases::kMark) {
-        mark(p, s);
-        cluster.sync();
-    }
+    clear(p, s);
+    cluster.sync();
+    mark(p, s);
+    cluster.sync();
     scan(p, sm);
     cluster.sync();  // also: no CTA leaves before its totals have been read
-    if (PHASES & Phases::kFill) fill(p, s);
+    fill(p, s);
 }
 
 // one phase over the whole GPU
@@ -414,23 +535,41 @@ __global__ void __launch_bounds__(256) pages_phase_kernel(Params p)
     if (PHASE == Phases::kFill) fill(p, s);
 }
 
+// the scan's two halves, a block for every kBlockPages pages and, for remap, kThreads rows
+template <typename Params, bool LIST>
+__global__ void __launch_bounds__(kThreads) pages_scan_kernel(Params p)
+{
+    __shared__ ScanSmem sm;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (LIST) list(p, sm);
+    else count(p, sm);
+}
+
+int row_blocks(const RemapParams& p) { return (p.n_rows + kThreads - 1) / kThreads; }
+int row_blocks(const CompactParams&) { return 0; }
+
 template <typename Params>
 cudaError_t launch_pages(const Params& p, cudaStream_t stream)
 {
     const int64_t cells = (int64_t)p.n_rows * p.max_pages;
-    if (cells + p.n_pages < kOneLaunch)
-        return launch_k(pages_cluster_kernel<Params, Phases::kAll>, dim3(kCluster), dim3(kThreads), 0, stream, true, p);
+    if (cells + p.n_pages < kOneLaunch) return launch_k(pages_cluster_kernel<Params>, dim3(kCluster), dim3(kThreads), 0, stream, true, p);
     // a warp for every kSegment entries of a row, or every 512 words, and at most 8 blocks of 8 warps on an SM
     const int64_t units = (int64_t)p.n_rows * ((p.max_pages + kSegment - 1) / kSegment), most = 152 * 8;
     const auto blocks = [&](int64_t warps) { return dim3((unsigned)std::min(most, std::max<int64_t>(1, (warps + 7) / 8))); };
+    const dim3 scans((unsigned)(((int64_t)p.n_pages + kBlockPages - 1) / kBlockPages + row_blocks(p)));
     cudaError_t e = launch_k(pages_phase_kernel<Params, Phases::kClear>, blocks(p.n_pages / 512), dim3(256), 0, stream, true, p);
     if (e == cudaSuccess) e = launch_k(pages_phase_kernel<Params, Phases::kMark>, blocks(units), dim3(256), 0, stream, true, p);
-    if (e == cudaSuccess) e = launch_k(pages_cluster_kernel<Params, Phases::kScan>, dim3(kCluster), dim3(kThreads), 0, stream, true, p);
+    if (e == cudaSuccess) e = launch_k(pages_scan_kernel<Params, false>, scans, dim3(kThreads), 0, stream, true, p);
+    if (e == cudaSuccess) e = launch_k(pages_scan_kernel<Params, true>, scans, dim3(kThreads), 0, stream, true, p);
     if (e == cudaSuccess) e = launch_k(pages_phase_kernel<Params, Phases::kFill>, blocks(units), dim3(256), 0, stream, true, p);
     return e;
 }
 
 }  // namespace
+
+size_t remap_sums(int n_pages, int n_rows) { return ((size_t)n_pages + kBlockPages - 1) / kBlockPages + ((size_t)n_rows + kThreads - 1) / kThreads; }
+size_t compact_sums(int n_pages) { return ((size_t)n_pages + kBlockPages - 1) / kBlockPages; }
 
 cudaError_t launch_kv_remap(const RemapParams& p, cudaStream_t stream) { return launch_pages(p, stream); }
 cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t stream) { return launch_pages(p, stream); }
