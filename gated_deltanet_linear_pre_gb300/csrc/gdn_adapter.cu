@@ -915,6 +915,184 @@ bool encode_maps(Maps& maps, const AdapterParams& p, const uint16_t* tokens, int
                          of_weights(maps.weights8_low, 8, kLowUnits)));
 }
 
+// ---- batches of single tokens, mostly ---------------------------------------------
+//
+// Where the sequences hold one or two tokens each, what counts is the chain from the batch's lengths to the last
+// store, and neither rings nor equal ranges shorten it.  Such batches (by their average: kDirectTokens) take two kernels
+// without any: a block for 4 tokens of a sequence and some channels, on the CUDA cores, each thread's loads all under way
+// at once, and in the second kernel before the first has ended.  64 single tokens with 48 adapters of rank 16, 4096 to
+// 10240: @DIRECT@ us, 25 by the ring.  Any lengths are right here, long ones only slow.
+constexpr int kDirectThreads = 256, kDirectTile = 4;
+constexpr int kDirectTokens = 8;     // tokens a sequence, on average, up to which a batch goes this way
+constexpr int kDirectIn = 1024;      // x's channels of a block
+constexpr int kDirectOut = kDirectThreads * 8;
+
+// up to kDirectTile tokens of one sequence; n 0: an empty slot.  Slots as in adapter_down, of kDirectTile tokens.
+__device__ __forceinline__ Piece direct_tile(const AdapterParams& p, int slot)
+{
+    const auto base = [&](int s) { return (int64_t)(cu_at(p.cu_seqlens, s, p.T) / kDirectTile + s); };
+    const int s = warp_find(p.n_seq, slot, base);
+    const int first = cu_at(p.cu_seqlens, s, p.T), end = cu_at(p.cu_seqlens, s + 1, p.T);
+    Piece t{};
+    const int64_t start = first + (slot - base(s)) * kDirectTile;
+    t.n = (int)max((int64_t)0, min((int64_t)kDirectTile, end - start));
+    t.start = t.n > 0 ? (int)start : 0;
+    t.rank = rank_of(p, s, t.id);
+    return t;
+}
+
+// h of up to NT tokens, channels [k_lo, k_hi): each warp two rows of `down` at a time
+template <bool BF16, int NT>
+__device__ __forceinline__ void direct_down(const AdapterParams& p, const Piece& t, int k_lo, int k_hi, float* h)
+{
+    constexpr int kSteps = kDirectIn / 256;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k0 = k_lo + lane * 8;
+    const uint16_t* x = p.x + (size_t)t.start * p.x_stride;
+    for (int j = warp * 2; j < t.rank; j += kDirectThreads / 16) {
+        const uint16_t* w0 = p.down + ((size_t)t.id * p.rank + j) * p.d_in;
+        const uint16_t* w1 = j + 1 < t.rank ? w0 + p.d_in : w0;
+        uint4 a[kSteps][2];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            a[i][0] = a[i][1] = make_uint4(0, 0, 0, 0);
+            if (k0 + i * 256 < k_hi) {
+                a[i][0] = __ldg(reinterpret_cast<const uint4*>(w0 + k0 + i * 256));
+                a[i][1] = __ldg(reinterpret_cast<const uint4*>(w1 + k0 + i * 256));
+            }
+        }
+        float acc[2][NT] = {};
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+            if (k0 + i * 256 < k_hi) {
+                float f[2][8];
+                widen8<BF16>(a[i][0], f[0]);
+                widen8<BF16>(a[i][1], f[1]);
+#pragma unroll
+                for (int q = 0; q < NT; ++q) {
+                    float v[8];
+                    widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(x + (size_t)min(q, t.n - 1) * p.x_stride + k0 + i * 256)), v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        acc[0][q] = fmaf(f[0][e], v[e], acc[0][q]);
+                        acc[1][q] = fmaf(f[1][e], v[e], acc[1][q]);
+                    }
+                }
+            }
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float sum = warp_sum(acc[r][q]);
+                if (lane == 0 && q < t.n && j + r < t.rank) h[(size_t)q * p.rank + j + r] = sum;
+            }
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kDirectThreads) adapter_direct_down_kernel(const __grid_constant__ AdapterParams p)
+{
+    pdl_wait();
+    // behind the wait: the kernel behind this one may read what earlier launches wrote
+    pdl_launch_dependents();
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < 2 * kCtas; i += kDirectThreads) p.status[i] = 0;  // nobody waits here
+    const Piece t = direct_tile(p, blockIdx.x);
+    if (t.n == 0 || t.rank == 0) return;
+    const int k_lo = blockIdx.y * kDirectIn, k_hi = min(p.d_in, k_lo + kDirectIn);
+    float* h = p.h + ((size_t)blockIdx.y * p.T + t.start) * p.rank;
+    if (t.n == 1) direct_down<BF16, 1>(p, t, k_lo, k_hi, h);
+    else if (t.n == 2) direct_down<BF16, 2>(p, t, k_lo, k_hi, h);
+    else direct_down<BF16, 4>(p, t, k_lo, k_hi, h);
+}
+
+template <bool BF16, int NT>
+__device__ __forceinline__ void direct_up(const AdapterParams& p, const Piece& t, int o, float* h)
+{
+    constexpr int kAhead = NT > 2 ? 8 : 16;  // rows of `up` loaded ahead
+    const bool mine = o < p.d_out;
+    const uint16_t* w = p.up + (size_t)t.id * p.rank * p.d_out + (mine ? o : 0);
+    uint4 y[NT], v[kAhead];
+    const auto load = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) v[i] = mine && j + i < t.rank ? __ldg(reinterpret_cast<const uint4*>(w + (size_t)(j + i) * p.d_out)) : make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+        y[q] = mine ? __ldcs(reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + min(q, t.n - 1)) * p.y_stride + o)) : make_uint4(0, 0, 0, 0);
+    load(0);
+    pdl_wait();
+    const int splits = (p.d_in + kDirectIn - 1) / kDirectIn;
+    for (int i = threadIdx.x; i < kDirectTile * 128; i += kDirectThreads) {
+        float sum = 0.0f;
+        const int q = i >> 7, j = i & 127;
+        if (q < t.n && j < t.rank)
+            for (int s = 0; s < splits; ++s) sum += p.h[((size_t)s * p.T + t.start + q) * p.rank + j];
+        h[i] = sum;
+    }
+    __syncthreads();
+    float acc[NT][8] = {};
+    for (int j = 0; j < t.rank; j += kAhead) {
+        if (j > 0) load(j);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            float f[8];
+            widen8<BF16>(v[i], f);
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+                const float x = h[q * 128 + min(j + i, 127)];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[q][e] = fmaf(x, f[e], acc[q][e]);
+            }
+        }
+    }
+    const float scale = __ldg(p.scales + t.id);
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+        if (mine && q < t.n) {
+            float f[8];
+            widen8<BF16>(y[q], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = fmaf(scale, acc[q][e], f[e]);
+            __stcs(reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o),
+                   make_uint4(narrow2<BF16>(f[0], f[1]), narrow2<BF16>(f[2], f[3]), narrow2<BF16>(f[4], f[5]), narrow2<BF16>(f[6], f[7])));
+        }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kDirectThreads) adapter_direct_up_kernel(const __grid_constant__ AdapterParams p)
+{
+    __shared__ float h[kDirectTile * 128];
+    pdl_launch_dependents();
+    // y, up and the batch were there before the first kernel began: only its sums are waited for
+    const Piece t = direct_tile(p, blockIdx.x);
+    const int o = blockIdx.y * kDirectOut + threadIdx.x * 8;
+    if (t.n == 0 || t.rank == 0) {
+        pdl_wait();
+        if (p.y_out == p.y || o >= p.d_out) return;
+        for (int q = 0; q < t.n; ++q)
+            *reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o) = *reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + q) * p.y_stride + o);
+        return;
+    }
+    if (t.n == 1) direct_up<BF16, 1>(p, t, o, h);
+    else if (t.n == 2) direct_up<BF16, 2>(p, t, o, h);
+    else direct_up<BF16, 4>(p, t, o, h);
+}
+
+// by the batch's average, where the sums fit the workspace
+bool goes_direct(const AdapterParams& p)
+{
+    const int64_t splits = (p.d_in + kDirectIn - 1) / kDirectIn;
+    return p.T <= (int64_t)kDirectTokens * p.n_seq && p.T * (splits - 1) <= kCtas * kTile;
+}
+
+template <bool BF16>
+cudaError_t launch_direct(const AdapterParams& p, cudaStream_t stream)
+{
+    const unsigned slots = (unsigned)((int64_t)p.T / kDirectTile + p.n_seq);
+    const cudaError_t e = launch_k(adapter_direct_down_kernel<BF16>, dim3(slots, (unsigned)((p.d_in + kDirectIn - 1) / kDirectIn)), dim3(kDirectThreads), 0, stream, true, p);
+    return e != cudaSuccess ? e : launch_k(adapter_direct_up_kernel<BF16>, dim3(slots, (unsigned)((p.d_out + kDirectOut - 1) / kDirectOut)), dim3(kDirectThreads), 0, stream, true, p);
+}
+
 template <bool BF16, int R>
 cudaError_t launch_rank(const AdapterParams& p, cudaStream_t stream)
 {
@@ -956,6 +1134,7 @@ cudaError_t launch_adapter(AdapterParams p, void* workspace, cudaStream_t stream
     p.chunks_out = (p.d_out + kK - 1) / kK;
     const auto launch = [&](auto bf16) {
         constexpr bool kBf16 = decltype(bf16)::value;
+        if (goes_direct(p)) return launch_direct<kBf16>(p, stream);
         if (p.rank <= 16) return launch_rank<kBf16, 16>(p, stream);
         if (p.rank <= 32) return launch_rank<kBf16, 32>(p, stream);
         if (p.rank <= 64) return launch_rank<kBf16, 64>(p, stream);
