@@ -4,23 +4,25 @@
 //   y_out[t] = y[t] + scale[a] * up[a]^T h[t]        a = the adapter of t's sequence
 //
 // Bound by HBM: x and y are read and y_out written once, an adapter's weights
-// once for every 128 tokens that use them (from L2 after the first).  Two launches:
-//   adapter_down  h, fp32, to the workspace
-//   adapter_up    the product of h with up, and the sum with y
-// A unit of work is 64 channels (of x, of y) for one tile of up to 128 tokens of
-// one sequence.  Each of 152 CTAs, one an SM, takes a range of all units of equal
-// cost (bytes, nearly), cutting a tile where its range ends: sequences of one
-// token and prompts share a batch, and may lie in any order.  A tile that lies in
-// several ranges has its h in several sums, which adapter_up adds in order.
+// once for every 128 tokens that use them (from L2 after the first).
 //
-// One warp copies (TMA boxes of 64 channels, into a ring of stages of 128-byte
-// swizzled rows), far ahead of the others.  Tiles of more than 8 tokens go through the tensor cores:
-// tcgen05, 16-bit operands, fp32 sums in TMEM; one warp issues the products, eight
-// take what comes of them on.  Smaller tiles would leave those instructions mostly
-// empty: those eight warps take them by mma.sync with the tokens as its 8 columns,
-// several units a stage.
-// h enters its product as hi + lo in the weights' type: 16 bits of it in bf16, 21
-// of its row's largest in fp16, far below the rounding of y_out.
+// Tiles of 9 to 128 tokens of a sequence go through the tensor cores, in two
+// launches: adapter_down (h, fp32, to the workspace) and adapter_up (its product with
+// up, and the sum with y).  A unit of work is 64 channels (of x, of y) of a tile.
+// Each of 152 CTAs, one an SM, takes a range of all units of equal cost, cutting a
+// tile where its range ends; a tile that lies in several ranges has its h in several
+// sums, which adapter_up adds in order.  One warp copies (TMA boxes of 64 channels,
+// into a ring of stages of 128-byte swizzled rows), far ahead of the others; one
+// issues the products (tcgen05, 16-bit operands, fp32 sums in TMEM); eight take what
+// comes of them on.  h enters its product as hi + lo in the weights' type: 16 bits of
+// it in bf16, 21 of its row's largest in fp16, far below the rounding of y_out.
+//
+// Smaller tiles (single tokens, drafts) read weights that nobody shares; what counts
+// for them is the chain from the batch's lengths to the last store.  They take two
+// kernels of their own, without rings or ranges, that run beside the others; a batch
+// with few tokens a sequence on average goes that way alone.
+//
+// Measured (of what a plain copy reaches): @MEASURED@
 #include <algorithm>
 #include <type_traits>
 
@@ -36,7 +38,7 @@ constexpr int kCopier = kWorkers;                    // the warp that copies
 constexpr int kProduct = kWorkers + 1;               // the warp that issues products
 constexpr int kThreads = (kProduct + 1) * 32;
 constexpr int kTile = 128;                           // tokens
-constexpr int kFew = 8;                              // tokens up to which a tile goes through mma.sync
+constexpr int kFew = 8;                              // tokens up to which a tile is left to the kernels of few tokens
 constexpr int kK = 64;                               // channels of a unit: rows of 128 bytes in shared memory
 constexpr int kRow = kK * 2;
 constexpr int kCtas = kAdapterCtas;
@@ -50,10 +52,9 @@ template <int R> constexpr int kStageBytes = kTokenBytes + R * kRow;
 constexpr int kResultBytes = 32 * 64;                // a worker's part of a chunk of y_out, on its way out
 template <int R> constexpr size_t kSmem = 1024 + kStages<R> * kStageBytes<R> + kWorkers * kResultBytes;
 
-// Tensor maps of the tokens (x or y) and of the weights: boxes of 64 channels by kTile or kFew tokens, by `rank` or 8 rows
-// of weights; and the last four for several units at once (a copy has its price, whatever its size).
+// tensor maps of the tokens (x or y): boxes of kTile rows; and of the weights: boxes of `rank` and of 8 rows
 struct Maps {
-    CUtensorMap tokens, few, weights, weights8, few_units, weights_units, few_low, weights8_low;
+    CUtensorMap tokens, weights, weights8;
 };
 
 __device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers * 32) : "memory"); }
@@ -63,54 +64,15 @@ __device__ __forceinline__ uint32_t place(int row, int piece) { return row * kRo
 
 // ---- who does what --------------------------------------------------------------
 
-// Tiles of few tokens: several units a stage.  Row r of unit u's weights lies at u * unit + (r / 8) * group +
-// place(r & 7, .), row q of its tokens at tokens + u * kFew rows + place(q, .).
-struct FewLayout {
-    int step;   // units of a stage
-    bool low;   // an adapter of a lower rank than the others', whose rows are copied 8 at a time, kLowUnits units at once
-    int rows;   // of weights that are copied
-    int unit, group, tokens;
-};
-
-constexpr int kLowUnits = 4;
-
-// the rank that the kernels are built for, and units of full rank that fit a stage
-__host__ __device__ __forceinline__ int built_rank(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
-__host__ __device__ __forceinline__ int full_units(int rank)
-{
-    const int fit = (kTile + built_rank(rank)) / (rank + kFew);
-    return fit >= 8 ? 8 : fit >= 4 ? 4 : fit >= 2 ? 2 : 1;
-}
-
-__device__ __forceinline__ FewLayout few_layout(const AdapterParams& p, int rank)
-{
-    FewLayout f;
-    const int rows = (rank + 7) & ~7, full = full_units(p.rank);
-    f.low = (rows + kFew) * kLowUnits <= kTile + built_rank(p.rank) && (full < kLowUnits || rows * 2 <= p.rank);
-    f.step = f.low ? kLowUnits : full;
-    f.rows = f.low || rank == 0 ? rows : p.rank;
-    f.unit = f.low ? 8 * kRow : p.rank * kRow;
-    f.group = f.low ? kLowUnits * 8 * kRow : 8 * kRow;
-    f.tokens = f.step * f.rows * kRow;
-    return f;
-}
-
-// What a unit costs, in steps of some 2 ns, fitted to the time that CTAs took for ranges of one kind (8 prompts with
-// rank 64; a prompt with rank 72 beside drafts of ranks 8 to 112).  A tile of more than a few tokens copies the rows of a
-// whole one.  Few tokens' units take their weights from HBM, and the ring's turn where they are small.
-__device__ __forceinline__ int cost_few(const AdapterParams& p, int rank)
-{
-    const FewLayout f = few_layout(p, rank);
-    return max(184 / f.step, (f.rows + kFew) * 3 / 2);
-}
-__host__ __device__ __forceinline__ int cost_in_tile(int rank) { return 144 + rank; }
-__host__ __device__ __forceinline__ int cost_out_tile(int rank) { return rank > 0 ? 160 + 2 * rank : 192; }
+// What a unit costs, in steps of some 2 ns: rows of 128 bytes copied and written, fitted to the time that a CTA took for
+// ranges of one kind (8 prompts with rank 64, one with rank 72).  A tile copies the rows of a whole one.
+__device__ __forceinline__ int cost_in(int rank) { return rank > 0 ? 144 + rank : 0; }
+__device__ __forceinline__ int cost_out(int rank, bool copied) { return rank > 0 ? 160 + 2 * rank : copied ? 192 : 0; }
 
 template <bool IN>
 __device__ __forceinline__ int unit_cost(const AdapterParams& p, int n, int rank)
 {
-    if (n <= 0 || (rank == 0 && (IN || p.y_out == p.y))) return 0;
-    return n <= kFew ? cost_few(p, rank) : IN ? cost_in_tile(rank) : cost_out_tile(rank);
+    return n <= kFew ? 0 : IN ? cost_in(rank) : cost_out(rank, p.y_out != p.y);
 }
 
 __device__ __forceinline__ int rank_of(const AdapterParams& p, int s, int& id)
@@ -173,6 +135,7 @@ struct Walk {
             } else {
                 ++k;
             }
+            if (t.cost == 0) continue;
             const int whole = t.cost * chunks;  // below 2^20
             at += whole;
             t.c_lo = ((int)min(max(lo - t.before, (int64_t)0), (int64_t)whole) + t.cost - 1) / t.cost;
@@ -226,7 +189,7 @@ __device__ __forceinline__ void find_starts(const AdapterParams& p, PlanSmem& sm
         AdapterStart& start = i ? out : sm.start;
         // a CTA is worth 4 units of the largest tiles, and a tile is cut into at most kParts + 1
         const int chunks = i ? p.chunks_out : p.chunks_in;
-        const int most = i ? cost_out_tile(p.rank) : cost_in_tile(p.rank);
+        const int most = i ? cost_out(p.rank, true) : cost_in(p.rank);
         const int64_t share = max((total[i] + kCtas - 1) / kCtas, (int64_t)most * max(4, (chunks + kParts - 1) / kParts)), lo = share * blockIdx.x;
         if (threadIdx.x == 0) {
             start.share = share;
@@ -254,8 +217,7 @@ __device__ __forceinline__ void find_starts(const AdapterParams& p, PlanSmem& sm
 // Every wait is bounded; after one that has expired the rest of the call's waits are passed over and its
 // outputs are invalid, which the CTA records.
 // A barrier's parity tells two turns apart, no more.  So whoever waits for a ring's stages waits for all of them, in
-// order, also those that are another role's, and is among those who free them: nobody falls a turn behind.
-// (adapter_down's workers pass over the tensor cores' stages, but only once all of them are done.)
+// order, and is among those who free them: nobody falls a turn behind.
 struct Shared {
     uint64_t full[8], empty[8];           // stages of the ring
     uint64_t d_full[kRing], d_empty[kRing];
@@ -263,10 +225,7 @@ struct Shared {
     uint32_t tmem;
     int expired;
     float factor[kTile];
-    union {
-        float most[2][kTile];
-        float sums[kWorkers][4][32];
-    };
+    float most[2][kTile];
 };
 
 __device__ __forceinline__ void wait(Shared& sm, uint64_t* mbar, uint32_t parity)
@@ -321,115 +280,27 @@ struct Ring {
 // The copying warp: the stages of a piece, in order.  Rows of tokens behind the tile's own are its neighbours', and
 // what comes of them goes nowhere.
 template <int R>
-__device__ __forceinline__ void copy_piece(const AdapterParams& p, const Piece& t, int width, const Maps& maps, Shared& sm, uint32_t base, Ring<R>& at)
+__device__ __forceinline__ void copy_piece(const AdapterParams& p, const Piece& t, const Maps& maps, Shared& sm, uint32_t base, Ring<R>& at)
 {
-    const bool few = t.n <= kFew;
-    const FewLayout layout = few_layout(p, t.rank);
-    const int step = few ? layout.step : 1, whole = width / kK, row = t.rank > 0 ? t.id * p.rank : 0;
-    const int rows = few ? layout.rows : t.rank == 0 ? 0 : t.rank <= 8 ? 8 : p.rank;
-    for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
+    const int rows = t.rank == 0 ? 0 : t.rank <= 8 ? 8 : p.rank, row = t.rank > 0 ? t.id * p.rank : 0;
+    for (int c = t.c_lo; c < t.c_hi; ++c, at.next()) {
         wait(sm, &sm.empty[at.stage], at.phase ^ 1);
         __syncwarp();
         if (umma::elect_one()) {
-            const uint32_t to = base + at.stage * kStageBytes<R>, tokens = to + layout.tokens;
+            const uint32_t to = base + at.stage * kStageBytes<R>;
             uint64_t* full = &sm.full[at.stage];
-            if (!few) {
-                umma::mbar_arrive_expect_tx(full, kTokenBytes + rows * kRow);
-                umma::tensor_g2s_2d(to, &maps.tokens, c * kK, t.start, full);
-                if (rows) umma::tensor_g2s_2d(to + kTokenBytes, rows == 8 ? &maps.weights8 : &maps.weights, c * kK, row, full);
-            } else if (c + step <= whole || t.c_hi <= whole) {
-                umma::mbar_arrive_expect_tx(full, step * (rows + kFew) * kRow);
-                if (layout.low)
-                    for (int r = 0; r < rows; r += 8) umma::tensor_g2s_3d(to + r / 8 * layout.group, &maps.weights8_low, 0, row + r, c, full);
-                else
-                    umma::tensor_g2s_3d(to, &maps.weights_units, 0, row, c, full);
-                umma::tensor_g2s_3d(tokens, layout.low ? &maps.few_low : &maps.few_units, 0, t.start, c, full);
-            } else {  // the last channels are fewer than 64
-                const int units = min(step, t.c_hi - c);
-                umma::mbar_arrive_expect_tx(full, units * (rows + kFew) * kRow);
-                for (int u = 0; u < units; ++u) {
-                    if (layout.low)
-                        for (int r = 0; r < rows; r += 8) umma::tensor_g2s_2d(to + u * layout.unit + r / 8 * layout.group, &maps.weights8, (c + u) * kK, row + r, full);
-                    else
-                        umma::tensor_g2s_2d(to + u * layout.unit, &maps.weights, (c + u) * kK, row, full);
-                    umma::tensor_g2s_2d(tokens + u * kFew * kRow, &maps.few, (c + u) * kK, t.start, full);
-                }
-            }
+            umma::mbar_arrive_expect_tx(full, kTokenBytes + rows * kRow);
+            umma::tensor_g2s_2d(to, &maps.tokens, c * kK, t.start, full);
+            if (rows) umma::tensor_g2s_2d(to + kTokenBytes, rows == 8 ? &maps.weights8 : &maps.weights, c * kK, row, full);
         }
         __syncwarp();
     }
-}
-
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void* at)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(umma::smem_u32(at)));
-}
-__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], const void* at)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(umma::smem_u32(at)));
-}
-template <bool BF16>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    if (BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 template <bool BF16, int M, int N>
 constexpr uint32_t idesc(bool b_mn_major) { return BF16 ? umma::idesc_bf16(M, N, false, b_mn_major) : umma::idesc_f16(M, N, false, b_mn_major); }
 
 // ---- down -----------------------------------------------------------------------
-
-// h of a tile of up to 8 tokens: 16 rows of `down` by 8 tokens a product.  A warp takes 16 rows and, where there are
-// fewer rows than warps, every so many of a stage's units; the warps of the same rows add up at the end, in order.
-template <bool BF16, int R>
-__device__ __forceinline__ void down_few(const AdapterParams& p, const Piece& t, float* h, Shared& sm, const unsigned char* ring, Ring<R>& at)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int blocks = (t.rank + 15) / 16, groups = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks;  // of 16 rows; warps that take different ones
-    const int block = warp % groups, unit = warp / groups, step = kWorkers / groups;
-    const FewLayout layout = few_layout(p, t.rank);
-    // a lane's row of either operand; rows that are not there are others again, and what comes of them goes nowhere
-    const int row = min(block * 16 + (lane & 15), t.rank - 1), token = min(lane & 7, t.n - 1);
-    float acc[4] = {};
-    for (int c = t.c_lo; c < t.c_hi; c += layout.step, at.next()) {
-        wait(sm, &sm.full[at.stage], at.phase);
-        const int units = block < blocks ? min(layout.step, t.c_hi - c) : 0;
-        for (int u = unit; u < units; u += step) {
-            const unsigned char *stage = ring + at.stage * kStageBytes<R>, *tokens = stage + layout.tokens + u * kFew * kRow;
-            const unsigned char* rows = stage + u * layout.unit + (row >> 3) * layout.group;
-            uint32_t b[2][4];
-            ldmatrix4(b[0], tokens + place(token, lane >> 3));
-            ldmatrix4(b[1], tokens + place(token, 4 + (lane >> 3)));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t a[4];
-                ldmatrix4(a, rows + place(row & 7, 2 * k + (lane >> 4)));
-                mma<BF16>(acc, a, b[k >> 1][2 * (k & 1)], b[k >> 1][2 * (k & 1) + 1]);
-            }
-        }
-        workers_sync();
-        if (threadIdx.x == 0) umma::mbar_arrive(&sm.empty[at.stage]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sm.sums[warp][e][lane] = acc[e];
-    workers_sync();
-    if (unit == 0 && block < blocks) {
-        for (int w = warp + groups; w < kWorkers; w += groups)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] += sm.sums[w][e][lane];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int j = block * 16 + (lane >> 2) + (e >> 1) * 8, q = (lane & 3) * 2 + (e & 1);
-            if (j < t.rank && q < t.n) h[(size_t)q * p.rank + j] = acc[e];
-        }
-    }
-    workers_sync();  // the sums are read
-}
 
 template <bool BF16, int R>
 __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_constant__ AdapterParams p, const __grid_constant__ Maps maps)
@@ -443,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
     // In this order.  Nobody waits here for another kernel while it holds TMEM that the other has yet to get, and
     // the kernel behind this one, which starts when all CTAs have come by, may read what earlier launches wrote.
     pdl_wait();
-    shared_begin(sm, kColumns, 2);  // a stage is free: its products are done, or the workers are; the product warp is past it
+    shared_begin(sm, kColumns, 1);  // a stage is free when its products are done
     pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     find_starts(p, plan, p.starts[blockIdx.x]);
@@ -453,7 +324,6 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
     if (walk.s >= p.n_seq) walk.hi = walk.at;
     Piece t;
     if (warp < kWorkers) {
-        Ring<R> at;
         uint32_t tiles = 0;
         while (walk.next(p, t)) {
             // the range that a tile begins in has its sums in the tokens' places, every other its own
@@ -464,12 +334,6 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
                 for (int64_t hi = walk.hi; hi <= at_last; hi += share) ++ends;
                 p.parts[t.slot] = make_int2(blockIdx.x, ends);
             }
-            if (t.n <= kFew) {
-                down_few<BF16, R>(p, t, h, sm, ring, at);
-                continue;
-            }
-            // the ring goes on under the products
-            for (int c = t.c_lo; c < t.c_hi; ++c) at.next();
             const uint32_t d = tiles & 1;
             wait(sm, &sm.d_full[d], (tiles >> 1) & 1);
             umma::fence_after_sync();
@@ -497,19 +361,11 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
         }
     } else if (warp == kCopier) {
         Ring<R> at;
-        while (walk.next(p, t)) copy_piece<R>(p, t, p.d_in, maps, sm, base, at);
+        while (walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at);
     } else {
         Ring<R> at;
         uint32_t tiles = 0;
         while (walk.next(p, t)) {
-            if (t.n <= kFew) {
-                const int step = few_layout(p, t.rank).step;
-                for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
-                    wait(sm, &sm.full[at.stage], at.phase);
-                    if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
-                }
-                continue;
-            }
             const uint32_t d = tiles & 1;
             if (tiles >= 2) wait(sm, &sm.d_empty[d], ((tiles >> 1) - 1) & 1);
             for (int c = t.c_lo; c < t.c_hi; ++c, at.next()) {
@@ -522,7 +378,6 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
 #pragma unroll
                     for (int k = 0; k < kK / 16; ++k) umma::mma_bf16(sm.tmem + d * R, da + 2 * k, db + 2 * k, idesc<BF16, 128, R>(false), c > t.c_lo || k > 0);
                     umma::commit(&sm.empty[at.stage]);
-                    umma::mbar_arrive(&sm.empty[at.stage]);
                     if (c + 1 == t.c_hi) umma::commit(&sm.d_full[d]);
                 }
                 __syncwarp();
@@ -536,14 +391,6 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
 }
 
 // ---- up -------------------------------------------------------------------------
-
-// h of a token's column `col`, over all parts of its tile: `b` the ranges that the tile begins and ends in
-__device__ __forceinline__ float h_at(const AdapterParams& p, const Piece& t, int2 b, int row, int col)
-{
-    float v = p.h[(size_t)(t.start + row) * p.rank + col];
-    for (int r = b.x + 1; r <= b.y; ++r) v += p.h[((size_t)p.T + (size_t)r * kTile + row) * p.rank + col];
-    return v;
-}
 
 // two values as hi + lo in the weights' type; what is not finite goes into hi alone
 template <bool BF16>
@@ -560,91 +407,6 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
         hb = f.y;
     }
     lo = narrow2<BF16>(isfinite(ha) ? a - ha : 0.0f, isfinite(hb) ? b - hb : 0.0f);
-}
-
-// y_out of a tile of up to 8 tokens; h[8][rank] in shared memory (zeros behind the tokens and the rank).  The tokens are
-// 8 of a product's 16 rows, by 8 channels.  A stage is one warp's, so that eight of them are under way at a time.
-template <bool BF16, int R>
-__device__ __forceinline__ void up_few(const AdapterParams& p, const Piece& t, const float* h, Shared& sm, const unsigned char* ring, unsigned char* result,
-                                       Ring<R>& at, uint32_t& turn)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, steps = (t.rank + 15) / 16, q = lane >> 2;
-    const FewLayout layout = few_layout(p, t.rank);
-    // h as the products' first operand: row lane / 4, columns 16 k + 2 (lane & 3) + {0, 1, 8, 9}
-    uint32_t hi[R / 16][2], lo[R / 16][2];
-    float factor = t.id < 0 ? 0.0f : __ldg(p.scales + t.id);
-    {
-        const float* mine = h + q * p.rank + (lane & 3) * 2;
-        float inv = 1.0f;
-        if (!BF16) {
-            // a token's largest value to [1, 2), as in operand()
-            float most = 0.0f;
-            for (int k = 0; k * 8 < t.rank; ++k) most = fmaxf(most, fmaxf(fabsf(mine[k * 8]), fabsf(mine[k * 8 + 1])));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            const int exponent = min(max((int)(__float_as_uint(most) >> 23) - 127, -126), 126);
-            inv = __uint_as_float((uint32_t)(127 - exponent) << 23);
-            factor *= __uint_as_float((uint32_t)(127 + exponent) << 23);
-        }
-#pragma unroll
-        for (int k = 0; k < R / 16; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const bool there = k * 16 + e * 8 < t.rank;  // (h's rows are a multiple of 8 long)
-                split2<BF16>(there ? mine[k * 16 + e * 8] * inv : 0.0f, there ? mine[k * 16 + e * 8 + 1] * inv : 0.0f, hi[k][e], lo[k][e]);
-            }
-    }
-    for (int c = t.c_lo; c < t.c_hi; c += layout.step, at.next()) {
-        // every warp waits for every stage and hands it back: none is ever a whole turn of the ring from another
-        wait(sm, &sm.full[at.stage], at.phase);
-        const int units = turn++ % kWorkers == warp ? min(layout.step, t.c_hi - c) : 0;
-        const unsigned char *rows = ring + at.stage * kStageBytes<R>, *tokens = rows + layout.tokens;
-        for (int u = 0; u < units; ++u, rows += layout.unit, tokens += kFew * kRow) {
-            constexpr int kPart = R > 64 ? 4 : 8;  // pieces at a time: what the registers hold beside h
-#pragma unroll 1
-            for (int part = 0; part < 8; part += kPart) {
-                float acc[kPart][4] = {};
-#pragma unroll
-                for (int k = 0; k < R / 16; ++k)
-                    if (k < steps) {
-                        // rows behind the rank are the last one again: their h is 0, and what lies there may not be finite
-                        const int row = min(k * 16 + (lane & 15), t.rank - 1);
-                        const uint32_t a[4] = {hi[k][0], 0, hi[k][1], 0}, a2[4] = {lo[k][0], 0, lo[k][1], 0};
-#pragma unroll
-                        for (int j = 0; j < kPart / 2; ++j) {
-                            uint32_t b[4];
-                            ldmatrix4_t(b, rows + (row >> 3) * layout.group + place(row & 7, part + 2 * j + (lane >> 4)));
-                            mma<BF16>(acc[2 * j], a, b[0], b[1]);
-                            mma<BF16>(acc[2 * j + 1], a, b[2], b[3]);
-                            mma<BF16>(acc[2 * j], a2, b[0], b[1]);
-                            mma<BF16>(acc[2 * j + 1], a2, b[2], b[3]);
-                        }
-                    }
-                if (q < t.n) {
-#pragma unroll
-                    for (int j = 0; j < kPart; ++j) {
-                        const uint32_t y = *reinterpret_cast<const uint32_t*>(tokens + place(q, part + j) + (lane & 3) * 4);
-                        float2 v;
-                        if (BF16) v = make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
-                        else v = __half22float2(*reinterpret_cast<const __half2*>(&y));
-                        *reinterpret_cast<uint32_t*>(result + place(q, part + j) + (lane & 3) * 4) =
-                            t.rank > 0 ? narrow2<BF16>(fmaf(factor, acc[j][0], v.x), fmaf(factor, acc[j][1], v.y)) : y;
-                    }
-                }
-            }
-            __syncwarp();
-            const int o = (c + u) * kK + (lane & 7) * 8;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int token = i * 4 + (lane >> 3);
-                if (token < t.n && o < p.d_out)
-                    __stcs(reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + token) * p.out_stride + o),
-                           *reinterpret_cast<const uint4*>(result + place(token, lane & 7)));
-            }
-            __syncwarp();  // the results are read
-        }
-        if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
-    }
 }
 
 template <int N>
@@ -755,15 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
 {
     extern __shared__ unsigned char smem[];
     __shared__ Shared sm;
-    __shared__ float few[kFew * R];
     constexpr int kColumns = 512;
     unsigned char* ring = smem + ((1024 - (umma::smem_u32(smem) & 1023)) & 1023);
     const uint32_t base = umma::smem_u32(ring);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // all of adapter_down's CTAs have their TMEM, as those of this kernel when the next one starts
+    // all of adapter_down's CTAs have their TMEM, as those of this kernel when the next one starts, and the next one (the
+    // few tokens' second kernel) may read what both first kernels wrote
     shared_begin(sm, kColumns, kWorkers + 1);  // a stage is free: every worker is done with it, the product warp is past it
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const AdapterStart start = p.starts[blockIdx.x];
     const int64_t share = p.starts[0].share;
     Walk<false> walk{start.s, start.k, start.before, share * blockIdx.x, share * (blockIdx.x + 1)};
@@ -773,18 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
         unsigned char* result = ring + kStages<R> * kStageBytes<R> + warp * kResultBytes;
         const int half = warp >> 2, row0 = (warp & 3) * 32, row = row0 + lane, spot = row0 + (lane >> 2), piece = half * 4 + (lane & 3);
         Ring<R> at;
-        uint32_t m = 0, turn = 0;  // chunks of products; stages of few tokens
+        uint32_t m = 0;  // chunks of products
         while (walk.next(p, t)) {
-            const int2 b = t.rank > 0 ? p.parts[t.slot] : make_int2(0, 0);
-            if (t.n <= kFew) {
-                workers_sync();  // the last tile's h is read
-                for (int i = tid; i < t.n * p.rank; i += kWorkers * 32)
-                    few[i] = i % p.rank < t.rank ? h_at(p, t, b, i / p.rank, i % p.rank) : 0.0f;
-                for (int i = t.n * p.rank + tid; i < kFew * p.rank; i += kWorkers * 32) few[i] = 0.0f;
-                workers_sync();
-                up_few<BF16, R>(p, t, few, sm, ring, result, at, turn);
-                continue;
-            }
             if (t.rank == 0) {  // y as it is
                 uint16_t* out = p.y_out + (size_t)(t.start + spot) * p.out_stride + t.c_lo * kK + piece * 8;
                 for (int c = t.c_lo; c < t.c_hi; ++c, out += kK, at.next()) {
@@ -795,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
                 }
                 continue;
             }
+            const int2 b = p.parts[t.slot];
             workers_sync();  // the last tile's factors are read
             operand<BF16, R>(p, t, b, sm);
             uint16_t* out = p.y_out + (size_t)(t.start + spot) * p.out_stride + t.c_lo * kK + piece * 8;
@@ -843,14 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
         }
     } else if (warp == kCopier) {
         Ring<R> at;
-        while (walk.next(p, t)) copy_piece<R>(p, t, p.d_out, maps, sm, base, at);
+        while (walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at);
     } else {
         Ring<R> at;
         uint32_t m = 0, tiles = 0;
         while (walk.next(p, t)) {
-            if (t.n <= kFew || t.rank == 0) {
-                const int step = t.n <= kFew ? few_layout(p, t.rank).step : 1;
-                for (int c = t.c_lo; c < t.c_hi; c += step, at.next()) {
+            if (t.rank == 0) {
+                for (int c = t.c_lo; c < t.c_hi; ++c, at.next()) {
                     wait(sm, &sm.full[at.stage], at.phase);
                     if (lane == 0) umma::mbar_arrive(&sm.empty[at.stage]);
                 }
@@ -892,75 +644,83 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
     shared_end(sm, kColumns, p.status + kCtas + blockIdx.x);
 }
 
-// Rows of `width` 16-bit values, `stride` apart, in boxes of 64 of them by `box_rows` rows, swizzled over 128 bytes; with
-// `units` the whole units of 64 as a dimension of their own, so many to a box.
-bool encode_map(CUtensorMap& map, const void* rows, bool bf16, int width, int64_t n_rows, int64_t stride, int box_rows, int units = 0)
+// rows of `width` 16-bit values, `stride` apart, in boxes of 64 of them by `box_rows` rows, swizzled over 128 bytes
+bool encode_map(CUtensorMap& map, const void* rows, bool bf16, int width, int64_t n_rows, int64_t stride, int box_rows)
 {
     const auto encode = tensor_map_encoder();
-    const cuuint64_t dims[3] = {(cuuint64_t)(units ? kK : width), (cuuint64_t)n_rows, (cuuint64_t)(width / kK)}, strides[2] = {(cuuint64_t)stride * 2, kRow};
-    const cuuint32_t box[3] = {kK, (cuuint32_t)box_rows, (cuuint32_t)units}, ones[3] = {1, 1, 1};
-    return encode && encode(&map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, units ? 3 : 2, const_cast<void*>(rows), dims,
-                            strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)n_rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {kK, (cuuint32_t)box_rows}, ones[2] = {1, 1};
+    return encode && encode(&map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(rows), dims, strides, box,
+                            ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_maps(Maps& maps, const AdapterParams& p, const uint16_t* tokens, int64_t stride, const uint16_t* weights, int width, int units)
+bool encode_maps(Maps& maps, const AdapterParams& p, const uint16_t* tokens, int64_t stride, const uint16_t* weights, int width)
 {
     const int64_t rows = (int64_t)p.n_adapters * p.rank;
-    const auto of_tokens = [&](CUtensorMap& map, int box, int u = 0) { return encode_map(map, tokens, p.bf16, width, p.T, stride, box, u); };
-    // without adapters nothing is read through these
-    const auto of_weights = [&](CUtensorMap& map, int box, int u = 0) { return rows == 0 || encode_map(map, weights, p.bf16, width, rows, width, box, u); };
-    return of_tokens(maps.tokens, kTile) && of_tokens(maps.few, kFew) && of_weights(maps.weights, p.rank) && of_weights(maps.weights8, 8) &&
-           (width < kK || (of_tokens(maps.few_units, kFew, units) && of_weights(maps.weights_units, p.rank, units) && of_tokens(maps.few_low, kFew, kLowUnits) &&
-                         of_weights(maps.weights8_low, 8, kLowUnits)));
+    // (without adapters nothing is read through the weights')
+    return encode_map(maps.tokens, tokens, p.bf16, width, p.T, stride, kTile) &&
+           (rows == 0 || (encode_map(maps.weights, weights, p.bf16, width, rows, width, p.rank) && encode_map(maps.weights8, weights, p.bf16, width, rows, width, 8)));
 }
 
-// ---- batches of single tokens, mostly ---------------------------------------------
+// ---- few tokens -------------------------------------------------------------------
 //
-// Where the sequences hold one or two tokens each, what counts is the chain from the batch's lengths to the last
-// store, and neither rings nor equal ranges shorten it.  Such batches (by their average: kDirectTokens) take two kernels
-// without any: a block for 4 tokens of a sequence and some channels, on the CUDA cores, each thread's loads all under way
-// at once, and in the second kernel before the first has ended.  64 single tokens with 48 adapters of rank 16, 4096 to
-// 10240: @DIRECT@ us, 25 by the ring.  Any lengths are right here, long ones only slow.
-constexpr int kDirectThreads = 256, kDirectTile = 4;
-constexpr int kDirectTokens = 8;     // tokens a sequence, on average, up to which a batch goes this way
-constexpr int kDirectIn = 1024;      // x's channels of a block
-constexpr int kDirectOut = kDirectThreads * 8;
+// A block takes 4 tokens of a sequence and some channels, on the CUDA cores, each thread's loads all under way at once,
+// the second kernel's before the first has ended.  Alone (ALONE, a batch with few tokens a sequence) they take every
+// token, and split x's channels among blocks; any lengths are right there, long ones only slow.  Beside the tensor
+// cores' kernels they take the tiles that those leave, and neither waits for nor holds up the kernel that it runs beside:
+// the order is adapter_down, few_down, adapter_up, few_up; each is there to read what the ones in front of the last
+// wrote, and its first block waits for the last at the end, so that whoever comes next has them all behind it.
+constexpr int kFewThreads = 128, kFewTile = 4;
+constexpr int kFewRows = kFewThreads / 16;   // of `down`, two a warp
+constexpr int kFewIn = 1024;                 // x's channels at a time
+constexpr int kFewOut = kFewThreads * 8;
+// Tokens a sequence, on average, up to which a batch goes this way alone.  64 sequences of up to 8 tokens, rank 16,
+// 4096 to 10240: 14 us, 25 with the others' kernels (replayed).
+constexpr int kAloneTokens = 8;
 
-// up to kDirectTile tokens of one sequence; n 0: an empty slot.  Slots as in adapter_down, of kDirectTile tokens.
-__device__ __forceinline__ Piece direct_tile(const AdapterParams& p, int slot)
+// up to kFewTile tokens of one sequence; n 0: an empty slot
+template <bool ALONE>
+__device__ __forceinline__ Piece few_tile(const AdapterParams& p, int slot)
 {
-    const auto base = [&](int s) { return (int64_t)(cu_at(p.cu_seqlens, s, p.T) / kDirectTile + s); };
-    const int s = warp_find(p.n_seq, slot, base);
-    const int first = cu_at(p.cu_seqlens, s, p.T), end = cu_at(p.cu_seqlens, s + 1, p.T);
     Piece t{};
-    const int64_t start = first + (slot - base(s)) * kDirectTile;
-    t.n = (int)max((int64_t)0, min((int64_t)kDirectTile, end - start));
+    int s = slot >> 1, end;
+    int64_t start;
+    if (ALONE) {  // sequence s owns the slots from cu[s] / kFewTile + s on
+        const auto base = [&](int i) { return (int64_t)(cu_at(p.cu_seqlens, i, p.T) / kFewTile + i); };
+        s = warp_find(p.n_seq, slot, base);
+        end = cu_at(p.cu_seqlens, s + 1, p.T);
+        start = cu_at(p.cu_seqlens, s, p.T) + (slot - base(s)) * kFewTile;
+    } else {      // two slots a sequence, for its last tokens
+        const int first = cu_at(p.cu_seqlens, s, p.T);
+        end = cu_at(p.cu_seqlens, s + 1, p.T);
+        const int rest = max(end - first, 0) % kTile;
+        start = rest > kFew ? end : end - rest + (slot & 1) * kFewTile;
+    }
+    t.n = (int)max((int64_t)0, min((int64_t)kFewTile, end - start));
     t.start = t.n > 0 ? (int)start : 0;
     t.rank = rank_of(p, s, t.id);
     return t;
 }
 
-// h of up to NT tokens, channels [k_lo, k_hi): each warp two rows of `down` at a time
+// two rows of `down` with up to NT tokens, channels [k_lo, k_hi)
 template <bool BF16, int NT>
-__device__ __forceinline__ void direct_down(const AdapterParams& p, const Piece& t, int k_lo, int k_hi, float* h)
+__device__ __forceinline__ void few_down(const AdapterParams& p, const Piece& t, int j, int k_lo, int k_hi, float* h)
 {
-    constexpr int kSteps = kDirectIn / 256;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k0 = k_lo + lane * 8;
+    constexpr int kSteps = kFewIn / 256;
+    const int lane = threadIdx.x & 31;
     const uint16_t* x = p.x + (size_t)t.start * p.x_stride;
-    for (int j = warp * 2; j < t.rank; j += kDirectThreads / 16) {
-        const uint16_t* w0 = p.down + ((size_t)t.id * p.rank + j) * p.d_in;
-        const uint16_t* w1 = j + 1 < t.rank ? w0 + p.d_in : w0;
+    const uint16_t* w0 = p.down + ((size_t)t.id * p.rank + j) * p.d_in;
+    const uint16_t* w1 = j + 1 < t.rank ? w0 + p.d_in : w0;
+    float acc[2][NT] = {};
+    for (int k0 = k_lo + lane * 8; k0 < k_hi; k0 += kFewIn) {
         uint4 a[kSteps][2];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            a[i][0] = a[i][1] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kSteps; ++i)
             if (k0 + i * 256 < k_hi) {
                 a[i][0] = __ldg(reinterpret_cast<const uint4*>(w0 + k0 + i * 256));
                 a[i][1] = __ldg(reinterpret_cast<const uint4*>(w1 + k0 + i * 256));
             }
-        }
-        float acc[2][NT] = {};
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
             if (k0 + i * 256 < k_hi) {
@@ -978,35 +738,39 @@ __device__ __forceinline__ void direct_down(const AdapterParams& p, const Piece&
                     }
                 }
             }
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float sum = warp_sum(acc[r][q]);
-                if (lane == 0 && q < t.n && j + r < t.rank) h[(size_t)q * p.rank + j + r] = sum;
-            }
     }
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float sum = warp_sum(acc[r][q]);
+            if (lane == 0 && q < t.n && j + r < t.rank) h[(size_t)q * p.rank + j + r] = sum;
+        }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kDirectThreads) adapter_direct_down_kernel(const __grid_constant__ AdapterParams p)
+// grid: slots, groups of kFewRows rows, (alone) ranges of kFewIn channels
+template <bool BF16, bool ALONE>
+__global__ void __launch_bounds__(kFewThreads) few_down_kernel(const __grid_constant__ AdapterParams p)
 {
-    pdl_wait();
-    // behind the wait: the kernel behind this one may read what earlier launches wrote
+    if (ALONE) pdl_wait();
     pdl_launch_dependents();
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int i = threadIdx.x; i < 2 * kCtas; i += kDirectThreads) p.status[i] = 0;  // nobody waits here
-    const Piece t = direct_tile(p, blockIdx.x);
-    if (t.n == 0 || t.rank == 0) return;
-    const int k_lo = blockIdx.y * kDirectIn, k_hi = min(p.d_in, k_lo + kDirectIn);
-    float* h = p.h + ((size_t)blockIdx.y * p.T + t.start) * p.rank;
-    if (t.n == 1) direct_down<BF16, 1>(p, t, k_lo, k_hi, h);
-    else if (t.n == 2) direct_down<BF16, 2>(p, t, k_lo, k_hi, h);
-    else direct_down<BF16, 4>(p, t, k_lo, k_hi, h);
+    const bool first = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+    if (ALONE && first)
+        for (int i = threadIdx.x; i < 2 * kCtas; i += kFewThreads) p.status[i] = 0;  // nobody waits here
+    const Piece t = few_tile<ALONE>(p, blockIdx.x);
+    const int j = blockIdx.y * kFewRows + (threadIdx.x >> 5) * 2;
+    if (t.n > 0 && j < t.rank) {
+        const int k_lo = ALONE ? blockIdx.z * kFewIn : 0, k_hi = ALONE ? min(p.d_in, k_lo + kFewIn) : p.d_in;
+        float* h = p.h + ((size_t)blockIdx.z * p.T + t.start) * p.rank;
+        if (t.n == 1) few_down<BF16, 1>(p, t, j, k_lo, k_hi, h);
+        else if (t.n == 2) few_down<BF16, 2>(p, t, j, k_lo, k_hi, h);
+        else few_down<BF16, 4>(p, t, j, k_lo, k_hi, h);
+    }
+    if (!ALONE && first) pdl_wait();
 }
 
-template <bool BF16, int NT>
-__device__ __forceinline__ void direct_up(const AdapterParams& p, const Piece& t, int o, float* h)
+template <bool BF16, bool ALONE, int NT>
+__device__ __forceinline__ void few_up(const AdapterParams& p, const Piece& t, int o, float* h)
 {
     constexpr int kAhead = NT > 2 ? 8 : 16;  // rows of `up` loaded ahead
     const bool mine = o < p.d_out;
@@ -1020,9 +784,9 @@ __device__ __forceinline__ void direct_up(const AdapterParams& p, const Piece& t
     for (int q = 0; q < NT; ++q)
         y[q] = mine ? __ldcs(reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + min(q, t.n - 1)) * p.y_stride + o)) : make_uint4(0, 0, 0, 0);
     load(0);
-    pdl_wait();
-    const int splits = (p.d_in + kDirectIn - 1) / kDirectIn;
-    for (int i = threadIdx.x; i < kDirectTile * 128; i += kDirectThreads) {
+    if (ALONE) pdl_wait();
+    const int splits = ALONE ? (p.d_in + kFewIn - 1) / kFewIn : 1;
+    for (int i = threadIdx.x; i < kFewTile * 128; i += kFewThreads) {
         float sum = 0.0f;
         const int q = i >> 7, j = i & 127;
         if (q < t.n && j < t.rank)
@@ -1039,7 +803,7 @@ __device__ __forceinline__ void direct_up(const AdapterParams& p, const Piece& t
             widen8<BF16>(v[i], f);
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
-                const float x = h[q * 128 + min(j + i, 127)];
+                const float x = h[q * 128 + min(j + i, 127)];  // (zero behind the rank, as v is)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[q][e] = fmaf(x, f[e], acc[q][e]);
             }
@@ -1058,51 +822,69 @@ __device__ __forceinline__ void direct_up(const AdapterParams& p, const Piece& t
         }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kDirectThreads) adapter_direct_up_kernel(const __grid_constant__ AdapterParams p)
+// grid: slots, ranges of kFewOut channels
+template <bool BF16, bool ALONE>
+__global__ void __launch_bounds__(kFewThreads) few_up_kernel(const __grid_constant__ AdapterParams p)
 {
-    __shared__ float h[kDirectTile * 128];
+    __shared__ float h[kFewTile * 128];
     pdl_launch_dependents();
-    // y, up and the batch were there before the first kernel began: only its sums are waited for
-    const Piece t = direct_tile(p, blockIdx.x);
-    const int o = blockIdx.y * kDirectOut + threadIdx.x * 8;
-    if (t.n == 0 || t.rank == 0) {
-        pdl_wait();
-        if (p.y_out == p.y || o >= p.d_out) return;
-        for (int q = 0; q < t.n; ++q)
-            *reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o) = *reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + q) * p.y_stride + o);
-        return;
+    // y, up and the batch were there before the first of the call's kernels began; alone, that one's sums are waited for
+    const Piece t = few_tile<ALONE>(p, blockIdx.x);
+    const int o = blockIdx.y * kFewOut + threadIdx.x * 8;
+    if (t.n > 0 && t.rank > 0) {
+        if (t.n == 1) few_up<BF16, ALONE, 1>(p, t, o, h);
+        else if (t.n == 2) few_up<BF16, ALONE, 2>(p, t, o, h);
+        else few_up<BF16, ALONE, 4>(p, t, o, h);
+    } else {
+        if (ALONE) pdl_wait();
+        if (p.y_out != p.y && o < p.d_out)
+            for (int q = 0; q < t.n; ++q)
+                *reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o) =
+                    *reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + q) * p.y_stride + o);
     }
-    if (t.n == 1) direct_up<BF16, 1>(p, t, o, h);
-    else if (t.n == 2) direct_up<BF16, 2>(p, t, o, h);
-    else direct_up<BF16, 4>(p, t, o, h);
+    if (!ALONE && blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
 }
 
-// by the batch's average, where the sums fit the workspace
-bool goes_direct(const AdapterParams& p)
+template <bool BF16, bool ALONE>
+cudaError_t launch_few_down(const AdapterParams& p, unsigned slots, cudaStream_t stream)
 {
-    const int64_t splits = (p.d_in + kDirectIn - 1) / kDirectIn;
-    return p.T <= (int64_t)kDirectTokens * p.n_seq && p.T * (splits - 1) <= kCtas * kTile;
+    const dim3 grid(slots, (unsigned)((p.rank + kFewRows - 1) / kFewRows), ALONE ? (unsigned)((p.d_in + kFewIn - 1) / kFewIn) : 1);
+    return launch_k(few_down_kernel<BF16, ALONE>, grid, dim3(kFewThreads), 0, stream, true, p);
+}
+
+template <bool BF16, bool ALONE>
+cudaError_t launch_few_up(const AdapterParams& p, unsigned slots, cudaStream_t stream)
+{
+    return launch_k(few_up_kernel<BF16, ALONE>, dim3(slots, (unsigned)((p.d_out + kFewOut - 1) / kFewOut)), dim3(kFewThreads), 0, stream, true, p);
+}
+
+// by the batch's average, where the ranges' sums fit the workspace
+bool goes_alone(const AdapterParams& p)
+{
+    const int64_t splits = (p.d_in + kFewIn - 1) / kFewIn;
+    return p.T <= (int64_t)kAloneTokens * p.n_seq && p.T * (splits - 1) <= kCtas * kTile;
 }
 
 template <bool BF16>
-cudaError_t launch_direct(const AdapterParams& p, cudaStream_t stream)
+cudaError_t launch_alone(const AdapterParams& p, cudaStream_t stream)
 {
-    const unsigned slots = (unsigned)((int64_t)p.T / kDirectTile + p.n_seq);
-    const cudaError_t e = launch_k(adapter_direct_down_kernel<BF16>, dim3(slots, (unsigned)((p.d_in + kDirectIn - 1) / kDirectIn)), dim3(kDirectThreads), 0, stream, true, p);
-    return e != cudaSuccess ? e : launch_k(adapter_direct_up_kernel<BF16>, dim3(slots, (unsigned)((p.d_out + kDirectOut - 1) / kDirectOut)), dim3(kDirectThreads), 0, stream, true, p);
+    const unsigned slots = (unsigned)((int64_t)p.T / kFewTile + p.n_seq);
+    const cudaError_t e = launch_few_down<BF16, true>(p, slots, stream);
+    return e != cudaSuccess ? e : launch_few_up<BF16, true>(p, slots, stream);
 }
 
 template <bool BF16, int R>
 cudaError_t launch_rank(const AdapterParams& p, cudaStream_t stream)
 {
     Maps in{}, out{};
-    const int units = full_units(p.rank);
-    if (!encode_maps(in, p, p.x, p.x_stride, p.down, p.d_in, units) || !encode_maps(out, p, p.y, p.y_stride, p.up, p.d_out, units)) return cudaErrorNotSupported;
+    if (!encode_maps(in, p, p.x, p.x_stride, p.down, p.d_in) || !encode_maps(out, p, p.y, p.y_stride, p.up, p.d_out)) return cudaErrorNotSupported;
+    const unsigned slots = (unsigned)p.n_seq * 2;
     cudaError_t e = cudaFuncSetAttribute(adapter_down_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(adapter_up_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = launch_k(adapter_down_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p, in);
+    if (e == cudaSuccess) e = launch_few_down<BF16, false>(p, slots, stream);
     if (e == cudaSuccess) e = launch_k(adapter_up_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p, out);
+    if (e == cudaSuccess) e = launch_few_up<BF16, false>(p, slots, stream);
     return e;
 }
 
@@ -1134,7 +916,7 @@ cudaError_t launch_adapter(AdapterParams p, void* workspace, cudaStream_t stream
     p.chunks_out = (p.d_out + kK - 1) / kK;
     const auto launch = [&](auto bf16) {
         constexpr bool kBf16 = decltype(bf16)::value;
-        if (goes_direct(p)) return launch_direct<kBf16>(p, stream);
+        if (goes_alone(p)) return launch_alone<kBf16>(p, stream);
         if (p.rank <= 16) return launch_rank<kBf16, 16>(p, stream);
         if (p.rank <= 32) return launch_rank<kBf16, 32>(p, stream);
         if (p.rank <= 64) return launch_rank<kBf16, 64>(p, stream);
