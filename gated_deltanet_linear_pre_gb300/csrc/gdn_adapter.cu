@@ -45,6 +45,7 @@ constexpr int kCtas = kAdapterCtas;
 constexpr int kTokenBytes = kTile * kRow;
 constexpr int kParts = 16;                           // ranges that a tile is cut into at most, but for the one it begins in
 constexpr int kRing = 4;                             // chunks' products in TMEM
+constexpr uint32_t kPolls = 1u << 18;                // of a wait: some two seconds
 constexpr int kColumnD = 256;                        // adapter_up's TMEM: h in the first R columns, products from here on
 
 template <int R> constexpr int kStages = R > 64 ? 5 : 8;  // (6 for R of 128 leave too little L1: 110 us for 102, 8192 tokens, 2048 to 10240)
@@ -214,14 +215,15 @@ __device__ __forceinline__ void find_starts(const AdapterParams& p, PlanSmem& sm
 
 // ---- hand-offs ------------------------------------------------------------------
 
-// Every wait is bounded; after one that has expired the rest of the call's waits are passed over and its
-// outputs are invalid, which the CTA records.
+// Every wait is bounded; after one that has expired the rest of the CTA's waits are passed over, no copy or product is
+// begun any more, those under way are waited for, and the CTA records that the call's outputs are invalid.
 // A barrier's parity tells two turns apart, no more.  So whoever waits for a ring's stages waits for all of them, in
 // order, and is among those who free them: nobody falls a turn behind.
 struct Shared {
     uint64_t full[8], empty[8];           // stages of the ring
     uint64_t d_full[kRing], d_empty[kRing];
     uint64_t h_full;                      // h is in TMEM (adapter_up)
+    uint64_t last;                        // every product is done
     uint32_t tmem;
     int expired;
     float factor[kTile];
@@ -231,9 +233,17 @@ struct Shared {
 __device__ __forceinline__ void wait(Shared& sm, uint64_t* mbar, uint32_t parity)
 {
     volatile int* expired = &sm.expired;
-    for (uint32_t i = 0; i < 1u << 22; ++i)
+    for (uint32_t i = 0; i < kPolls; ++i)
         if (umma::mbar_try_wait(mbar, parity) || *expired) return;
     *expired = 1;
+}
+
+__device__ __forceinline__ bool expired(Shared& sm) { return *(volatile int*)&sm.expired; }
+
+// a wait for what this CTA has under way, which no other expired wait cuts short
+__device__ __forceinline__ void drain(uint64_t* mbar, uint32_t parity)
+{
+    umma::mbar_wait(mbar, parity, kPolls);
 }
 
 __device__ __forceinline__ void shared_begin(Shared& sm, int columns, int empty_count)
@@ -248,6 +258,7 @@ __device__ __forceinline__ void shared_begin(Shared& sm, int columns, int empty_
             umma::mbar_init(&sm.d_empty[i], kWorkers);
         }
         umma::mbar_init(&sm.h_full, kWorkers);
+        umma::mbar_init(&sm.last, 1);
         sm.expired = 0;
     }
     if (threadIdx.x < 32) umma::tmem_alloc(&sm.tmem, columns);
@@ -280,13 +291,20 @@ struct Ring {
 // The copying warp: the stages of a piece, in order.  Rows of tokens behind the tile's own are its neighbours', and
 // what comes of them goes nowhere.
 template <int R>
-__device__ __forceinline__ void copy_piece(const AdapterParams& p, const Piece& t, const Maps& maps, Shared& sm, uint32_t base, Ring<R>& at)
+__device__ __forceinline__ void copy_piece(const AdapterParams& p, const Piece& t, const Maps& maps, Shared& sm, uint32_t base, Ring<R>& at, uint32_t& issued)
 {
     const int rows = t.rank == 0 ? 0 : t.rank <= 8 ? 8 : p.rank, row = t.rank > 0 ? t.id * p.rank : 0;
     for (int c = t.c_lo; c < t.c_hi; ++c, at.next()) {
         wait(sm, &sm.empty[at.stage], at.phase ^ 1);
         __syncwarp();
+        if (__any_sync(0xffffffffu, expired(sm))) return;
+#ifdef GDN_ADAPTER_SELFTEST_WITHHOLD_COPY
+        if (issued++ == 0) continue;  // tests: the CTA's first copy is left out
         if (umma::elect_one()) {
+#else
+        ++issued;
+        if (umma::elect_one()) {
+#endif
             const uint32_t to = base + at.stage * kStageBytes<R>;
             uint64_t* full = &sm.full[at.stage];
             umma::mbar_arrive_expect_tx(full, kTokenBytes + rows * kRow);
@@ -361,7 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
         }
     } else if (warp == kCopier) {
         Ring<R> at;
-        while (walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at);
+        uint32_t issued = 0;
+        while (!__any_sync(0xffffffffu, expired(sm)) && walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at, issued);
+        // no copy may be under way when the CTA leaves
+        if (expired(sm))
+            for (uint32_t i = issued > kStages<R> ? issued - kStages<R> : 0; i < issued; ++i) drain(&sm.full[i % kStages<R>], (i / kStages<R>) & 1);
     } else {
         Ring<R> at;
         uint32_t tiles = 0;
@@ -372,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
                 wait(sm, &sm.full[at.stage], at.phase);
                 umma::fence_after_sync();
                 __syncwarp();
+                if (__any_sync(0xffffffffu, expired(sm))) break;
                 if (umma::elect_one()) {
                     const uint32_t stage = base + at.stage * kStageBytes<R>;
                     const uint64_t da = umma::desc_sw128(stage, 16, 1024), db = umma::desc_sw128(stage + kTokenBytes, 16, 1024);
@@ -385,7 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
             ++tiles;
         }
         // no product may be under way when the CTA leaves
-        if (tiles > 0) wait(sm, &sm.d_full[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1);
+        if (umma::elect_one()) umma::commit(&sm.last);
+        __syncwarp();
+        drain(&sm.last, 0);
     }
     shared_end(sm, kColumns, p.status + blockIdx.x);
 }
@@ -596,7 +621,11 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
         }
     } else if (warp == kCopier) {
         Ring<R> at;
-        while (walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at);
+        uint32_t issued = 0;
+        while (!__any_sync(0xffffffffu, expired(sm)) && walk.next(p, t)) copy_piece<R>(p, t, maps, sm, base, at, issued);
+        // no copy may be under way when the CTA leaves
+        if (expired(sm))
+            for (uint32_t i = issued > kStages<R> ? issued - kStages<R> : 0; i < issued; ++i) drain(&sm.full[i % kStages<R>], (i / kStages<R>) & 1);
     } else {
         Ring<R> at;
         uint32_t m = 0, tiles = 0;
@@ -624,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
                 }
                 umma::fence_after_sync();
                 __syncwarp();
+                if (__any_sync(0xffffffffu, expired(sm))) break;
                 if (umma::elect_one()) {
                     const uint32_t d = sm.tmem + kColumnD + slot * kK;
                     const uint64_t db = umma::desc_sw128(base + at.stage * kStageBytes<R> + kTokenBytes, 16, 1024);
@@ -639,7 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_up_kernel(const __grid_co
             }
         }
         // no product may be under way when the CTA leaves
-        if (m > 0) wait(sm, &sm.d_full[(m - 1) % kRing], ((m - 1) / kRing) & 1);
+        if (umma::elect_one()) umma::commit(&sm.last);
+        __syncwarp();
+        drain(&sm.last, 0);
     }
     shared_end(sm, kColumns, p.status + kCtas + blockIdx.x);
 }

@@ -257,6 +257,38 @@ def test_another_stream_and_a_graph(gdn, lengths):
     c.check(out)
 
 
+@pytest.mark.parametrize("rank,d_in,d_out,dt", [(16, 1992, 3080, "fp16"), (32, 520, 5000, "bf16"), (64, 1992, 3080, "bf16"), (128, 1032, 2056, "fp16"),
+                                                (72, 2048, 1288, "bf16")])
+def test_many_tiles(gdn, rank, d_in, d_out, dt):
+    """Prompts and drafts of any length side by side, adapters of any rank and none: ranges that begin and end inside
+    tiles, rings that turn many times."""
+    rng = np.random.default_rng(rank)
+    lengths = [int(x) for x in rng.choice([0, 1, 3, 8, 9, 10, 60, 127, 128, 129, 136, 137, 300, 700], 40)]
+    ranks = [rank, 1, rank - 3, 8, rank // 2, 7, 0, rank]
+    c = Case(lengths, [int(x) for x in rng.integers(-1, 8, 40)], 8, rank, d_in, d_out, dt, ranks=ranks, strided=True)
+    out = c.run(gdn)
+    c.check(out)
+    assert torch.equal(out, c.run(gdn))
+    assert torch.equal(c.run(gdn, out=c.y), out)      # in place
+
+
+def test_two_calls_at_once(gdn):
+    """Two streams, each with its workspace, several calls each."""
+    cases = [Case([500, 3, 260], [0, 1, 1], 2, 64, 1024, 2048, "bf16", seed=1), Case([1] * 200, [i % 2 for i in range(200)], 2, 64, 1024, 2048, "bf16", seed=2),
+             Case([130, 900, 1, 1], [1, 0, 1, 0], 2, 64, 1024, 2048, "bf16", seed=3)]
+    want = [c.run(gdn).clone() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(5):
+        for c, s, g in zip(cases, streams, got):
+            with torch.cuda.stream(s):
+                g.append(c.run(gdn))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(x, w) for x in g)
+
+
 def test_refusals(gdn):
     c = Case([4, 5], [0, 1], 2, 16, 128, 192, "bf16")
     ws = torch.empty(gdn.gdn_adapter_workspace_bytes(2, 9, 16, 128), dtype=torch.uint8, device="cuda")
