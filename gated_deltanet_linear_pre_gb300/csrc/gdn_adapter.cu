@@ -6,7 +6,7 @@
 // Bound by HBM: x and y are read and y_out written once, an adapter's weights
 // once for every 128 tokens that use them (from L2 after the first).
 //
-// Tiles of 9 to 128 tokens of a sequence go through the tensor cores, in two
+// Tiles of a good many of up to 128 tokens go through the tensor cores, in two
 // launches: adapter_down (h, fp32, to the workspace) and adapter_up (its product with
 // up, and the sum with y).  A unit of work is 64 channels (of x, of y) of a tile.
 // Each of 152 CTAs, one an SM, takes a range of all units of equal cost, cutting a
@@ -38,13 +38,12 @@ constexpr int kCopier = kWorkers;                    // the warp that copies
 constexpr int kProduct = kWorkers + 1;               // the warp that issues products
 constexpr int kThreads = (kProduct + 1) * 32;
 constexpr int kTile = 128;                           // tokens
-constexpr int kFew = 8;                              // tokens up to which a tile is left to the kernels of few tokens
 constexpr int kK = 64;                               // channels of a unit: rows of 128 bytes in shared memory
 constexpr int kRow = kK * 2;
 constexpr int kCtas = kAdapterCtas;
 constexpr int kTokenBytes = kTile * kRow;
-constexpr int kParts = 16;                           // ranges that a tile is cut into at most, but for the one it begins in
 constexpr int kRing = 4;                             // chunks' products in TMEM
+constexpr int kPartsOut = 16;
 constexpr uint32_t kPolls = 1u << 18;                // of a wait: some two seconds
 constexpr int kColumnD = 256;                        // adapter_up's TMEM: h in the first R columns, products from here on
 
@@ -73,7 +72,7 @@ __device__ __forceinline__ int cost_out(int rank, bool copied) { return rank > 0
 template <bool IN>
 __device__ __forceinline__ int unit_cost(const AdapterParams& p, int n, int rank)
 {
-    return n <= kFew ? 0 : IN ? cost_in(rank) : cost_out(rank, p.y_out != p.y);
+    return n <= p.few ? 0 : IN ? cost_in(rank) : cost_out(rank, p.y_out != p.y);
 }
 
 __device__ __forceinline__ int rank_of(const AdapterParams& p, int s, int& id)
@@ -188,10 +187,10 @@ __device__ __forceinline__ void find_starts(const AdapterParams& p, PlanSmem& sm
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         AdapterStart& start = i ? out : sm.start;
-        // a CTA is worth 4 units of the largest tiles, and a tile is cut into at most kParts + 1
-        const int chunks = i ? p.chunks_out : p.chunks_in;
+        // a CTA is worth 4 units of the largest tiles, and a tile is cut into `parts` + 1 at most
+        const int chunks = i ? p.chunks_out : p.chunks_in, parts = i ? kPartsOut : p.parts_in;
         const int most = i ? cost_out(p.rank, true) : cost_in(p.rank);
-        const int64_t share = max((total[i] + kCtas - 1) / kCtas, (int64_t)most * max(4, (chunks + kParts - 1) / kParts)), lo = share * blockIdx.x;
+        const int64_t share = max((total[i] + kCtas - 1) / kCtas, (int64_t)most * max(4, (chunks + parts - 1) / parts)), lo = share * blockIdx.x;
         if (threadIdx.x == 0) {
             start.share = share;
             if (lo >= total[i]) start.s = p.n_seq;  // no work
@@ -707,27 +706,29 @@ constexpr int kFewThreads = 128, kFewTile = 4;
 constexpr int kFewRows = kFewThreads / 16;   // of `down`, two a warp
 constexpr int kFewIn = 1024;                 // x's channels at a time
 constexpr int kFewOut = kFewThreads * 8;
-// Tokens a sequence, on average, up to which a batch goes this way alone.  64 sequences of up to 8 tokens, rank 16,
-// 4096 to 10240: 14 us, 25 with the others' kernels (replayed).
-constexpr int kAloneTokens = 8;
+// Tokens up to which a tile goes this way, and a batch's average up to which all of it does: the weights are read for
+// every 4 tokens, and the others' kernels copy whole tiles.  128 sequences of 12 tokens, 4096 to 10240: rank 16 52 us, 99
+// by the others; of 24 98 and 102; rank 64, of 12 138 and 107 (replayed).
+int few_tokens(int rank) { return rank <= 16 ? 24 : rank <= 32 ? 16 : 8; }
 
 // up to kFewTile tokens of one sequence; n 0: an empty slot
 template <bool ALONE>
 __device__ __forceinline__ Piece few_tile(const AdapterParams& p, int slot)
 {
     Piece t{};
-    int s = slot >> 1, end;
+    const int slots = p.few / kFewTile;
+    int s = slot / slots, end;
     int64_t start;
     if (ALONE) {  // sequence s owns the slots from cu[s] / kFewTile + s on
         const auto base = [&](int i) { return (int64_t)(cu_at(p.cu_seqlens, i, p.T) / kFewTile + i); };
         s = warp_find(p.n_seq, slot, base);
         end = cu_at(p.cu_seqlens, s + 1, p.T);
         start = cu_at(p.cu_seqlens, s, p.T) + (slot - base(s)) * kFewTile;
-    } else {      // two slots a sequence, for its last tokens
+    } else {      // p.few tokens' slots a sequence, for its last ones
         const int first = cu_at(p.cu_seqlens, s, p.T);
         end = cu_at(p.cu_seqlens, s + 1, p.T);
         const int rest = max(end - first, 0) % kTile;
-        start = rest > kFew ? end : end - rest + (slot & 1) * kFewTile;
+        start = rest > p.few ? end : end - rest + slot % slots * kFewTile;
     }
     t.n = (int)max((int64_t)0, min((int64_t)kFewTile, end - start));
     t.start = t.n > 0 ? (int)start : 0;
@@ -894,7 +895,7 @@ cudaError_t launch_few_up(const AdapterParams& p, unsigned slots, cudaStream_t s
 bool goes_alone(const AdapterParams& p)
 {
     const int64_t splits = (p.d_in + kFewIn - 1) / kFewIn;
-    return p.T <= (int64_t)kAloneTokens * p.n_seq && p.T * (splits - 1) <= kCtas * kTile;
+    return p.T <= (int64_t)p.few * p.n_seq && p.T * (splits - 1) <= kCtas * kTile;
 }
 
 template <bool BF16>
@@ -910,7 +911,7 @@ cudaError_t launch_rank(const AdapterParams& p, cudaStream_t stream)
 {
     Maps in{}, out{};
     if (!encode_maps(in, p, p.x, p.x_stride, p.down, p.d_in) || !encode_maps(out, p, p.y, p.y_stride, p.up, p.d_out)) return cudaErrorNotSupported;
-    const unsigned slots = (unsigned)p.n_seq * 2;
+    const unsigned slots = (unsigned)p.n_seq * (unsigned)(p.few / kFewTile);
     cudaError_t e = cudaFuncSetAttribute(adapter_down_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(adapter_up_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = launch_k(adapter_down_kernel<BF16, R>, dim3(kCtas), dim3(kThreads), kSmem<R>, stream, true, p, in);
@@ -944,8 +945,13 @@ size_t adapter_workspace(AdapterParams& p, void* workspace)
 cudaError_t launch_adapter(AdapterParams p, void* workspace, cudaStream_t stream)
 {
     adapter_workspace(p, workspace);
+    p.few = few_tokens(p.rank);
     p.chunks_in = (p.d_in + kK - 1) / kK;
     p.chunks_out = (p.d_out + kK - 1) / kK;
+    // Each part of a tile's h takes adapter_up over a microsecond to add, each unit of a range adapter_down half of one:
+    // about sqrt(units) / 2 parts are best where there are more CTAs than tiles (one prompt of 3001 tokens, rank 128, 2048
+    // to 10240: 63.6 us, 78.9 with up to 16).
+    for (p.parts_in = 2; 4 * p.parts_in * p.parts_in < p.chunks_in; ++p.parts_in) {}
     const auto launch = [&](auto bf16) {
         constexpr bool kBf16 = decltype(bf16)::value;
         if (goes_alone(p)) return launch_alone<kBf16>(p, stream);

@@ -237,7 +237,8 @@ struct AdapterParams {
     const uint16_t* y;
     uint16_t* y_out;
     int64_t x_stride, y_stride, out_stride;
-    int chunks_in, chunks_out;  // units of a tile (set by launch_adapter)
+    int few;                    // tokens up to which a tile is not the tensor cores' (set by launch_adapter)
+    int chunks_in, chunks_out, parts_in;  // units of a tile; ranges that one is cut into (set by launch_adapter)
     // workspace (set by launch_adapter): a word for each CTA of either kernel, 0 or a wait that has expired; per CTA, where
     // its range of y's units begins; per tile, the first and the last range of x's units that it lies in;
     // h [T + ranges * 128][rank]: what the range that a tile begins in summed, then what each of the others did
