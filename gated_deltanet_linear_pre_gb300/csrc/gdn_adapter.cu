@@ -711,33 +711,40 @@ constexpr int kFewOut = kFewThreads * 8;
 // by the others; of 24 98 and 102; rank 64, of 12 138 and 107 (replayed).
 int few_tokens(int rank) { return rank <= 16 ? 24 : rank <= 32 ? 16 : 8; }
 
+// A load in front of the kernel's wait (EARLY) comes from L2, as only the wait lets it trust what an SM's L1 holds.
+template <bool EARLY, class V>
+__device__ __forceinline__ V fetch(const V* at) { return EARLY ? __ldcg(at) : __ldg(at); }
+
 // up to kFewTile tokens of one sequence; n 0: an empty slot
-template <bool ALONE>
+template <bool ALONE, bool EARLY>
 __device__ __forceinline__ Piece few_tile(const AdapterParams& p, int slot)
 {
     Piece t{};
     const int slots = p.few / kFewTile;
+    const auto cu = [&](int i) { return min(max(fetch<EARLY>(p.cu_seqlens + i), 0), p.T); };
     int s = slot / slots, end;
     int64_t start;
     if (ALONE) {  // sequence s owns the slots from cu[s] / kFewTile + s on
-        const auto base = [&](int i) { return (int64_t)(cu_at(p.cu_seqlens, i, p.T) / kFewTile + i); };
+        const auto base = [&](int i) { return (int64_t)(cu(i) / kFewTile + i); };
         s = warp_find(p.n_seq, slot, base);
-        end = cu_at(p.cu_seqlens, s + 1, p.T);
-        start = cu_at(p.cu_seqlens, s, p.T) + (slot - base(s)) * kFewTile;
+        end = cu(s + 1);
+        start = cu(s) + (slot - base(s)) * kFewTile;
     } else {      // p.few tokens' slots a sequence, for its last ones
-        const int first = cu_at(p.cu_seqlens, s, p.T);
-        end = cu_at(p.cu_seqlens, s + 1, p.T);
+        const int first = cu(s);
+        end = cu(s + 1);
         const int rest = max(end - first, 0) % kTile;
         start = rest > p.few ? end : end - rest + slot % slots * kFewTile;
     }
     t.n = (int)max((int64_t)0, min((int64_t)kFewTile, end - start));
     t.start = t.n > 0 ? (int)start : 0;
-    t.rank = rank_of(p, s, t.id);
+    t.id = fetch<EARLY>(p.ids + s);
+    if (t.id < 0 || t.id >= p.n_adapters) t.id = -1;
+    t.rank = t.id < 0 ? 0 : p.ranks ? min(max(fetch<EARLY>(p.ranks + t.id), 0), p.rank) : p.rank;
     return t;
 }
 
 // two rows of `down` with up to NT tokens, channels [k_lo, k_hi)
-template <bool BF16, int NT>
+template <bool BF16, bool EARLY, int NT>
 __device__ __forceinline__ void few_down(const AdapterParams& p, const Piece& t, int j, int k_lo, int k_hi, float* h)
 {
     constexpr int kSteps = kFewIn / 256;
@@ -751,8 +758,8 @@ __device__ __forceinline__ void few_down(const AdapterParams& p, const Piece& t,
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
             if (k0 + i * 256 < k_hi) {
-                a[i][0] = __ldg(reinterpret_cast<const uint4*>(w0 + k0 + i * 256));
-                a[i][1] = __ldg(reinterpret_cast<const uint4*>(w1 + k0 + i * 256));
+                a[i][0] = fetch<EARLY>(reinterpret_cast<const uint4*>(w0 + k0 + i * 256));
+                a[i][1] = fetch<EARLY>(reinterpret_cast<const uint4*>(w1 + k0 + i * 256));
             }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
@@ -763,7 +770,7 @@ __device__ __forceinline__ void few_down(const AdapterParams& p, const Piece& t,
 #pragma unroll
                 for (int q = 0; q < NT; ++q) {
                     float v[8];
-                    widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(x + (size_t)min(q, t.n - 1) * p.x_stride + k0 + i * 256)), v);
+                    widen8<BF16>(fetch<EARLY>(reinterpret_cast<const uint4*>(x + (size_t)min(q, t.n - 1) * p.x_stride + k0 + i * 256)), v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         acc[0][q] = fmaf(f[0][e], v[e], acc[0][q]);
@@ -790,14 +797,14 @@ __global__ void __launch_bounds__(kFewThreads) few_down_kernel(const __grid_cons
     const bool first = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
     if (ALONE && first)
         for (int i = threadIdx.x; i < 2 * kCtas; i += kFewThreads) p.status[i] = 0;  // nobody waits here
-    const Piece t = few_tile<ALONE>(p, blockIdx.x);
+    const Piece t = few_tile<ALONE, !ALONE>(p, blockIdx.x);
     const int j = blockIdx.y * kFewRows + (threadIdx.x >> 5) * 2;
     if (t.n > 0 && j < t.rank) {
         const int k_lo = ALONE ? blockIdx.z * kFewIn : 0, k_hi = ALONE ? min(p.d_in, k_lo + kFewIn) : p.d_in;
         float* h = p.h + ((size_t)blockIdx.z * p.T + t.start) * p.rank;
-        if (t.n == 1) few_down<BF16, 1>(p, t, j, k_lo, k_hi, h);
-        else if (t.n == 2) few_down<BF16, 2>(p, t, j, k_lo, k_hi, h);
-        else few_down<BF16, 4>(p, t, j, k_lo, k_hi, h);
+        if (t.n == 1) few_down<BF16, !ALONE, 1>(p, t, j, k_lo, k_hi, h);
+        else if (t.n == 2) few_down<BF16, !ALONE, 2>(p, t, j, k_lo, k_hi, h);
+        else few_down<BF16, !ALONE, 4>(p, t, j, k_lo, k_hi, h);
     }
     if (!ALONE && first) pdl_wait();
 }
@@ -811,11 +818,11 @@ __device__ __forceinline__ void few_up(const AdapterParams& p, const Piece& t, i
     uint4 y[NT], v[kAhead];
     const auto load = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) v[i] = mine && j + i < t.rank ? __ldg(reinterpret_cast<const uint4*>(w + (size_t)(j + i) * p.d_out)) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kAhead; ++i) v[i] = mine && j + i < t.rank ? __ldcg(reinterpret_cast<const uint4*>(w + (size_t)(j + i) * p.d_out)) : make_uint4(0, 0, 0, 0);
     };
 #pragma unroll
     for (int q = 0; q < NT; ++q)
-        y[q] = mine ? __ldcs(reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + min(q, t.n - 1)) * p.y_stride + o)) : make_uint4(0, 0, 0, 0);
+        y[q] = mine ? __ldcg(reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + min(q, t.n - 1)) * p.y_stride + o)) : make_uint4(0, 0, 0, 0);
     load(0);
     if (ALONE) pdl_wait();
     const int splits = ALONE ? (p.d_in + kFewIn - 1) / kFewIn : 1;
@@ -823,7 +830,7 @@ __device__ __forceinline__ void few_up(const AdapterParams& p, const Piece& t, i
         float sum = 0.0f;
         const int q = i >> 7, j = i & 127;
         if (q < t.n && j < t.rank)
-            for (int s = 0; s < splits; ++s) sum += p.h[((size_t)s * p.T + t.start + q) * p.rank + j];
+            for (int s = 0; s < splits; ++s) sum += __ldcg(p.h + ((size_t)s * p.T + t.start + q) * p.rank + j);
         h[i] = sum;
     }
     __syncthreads();
@@ -842,7 +849,7 @@ __device__ __forceinline__ void few_up(const AdapterParams& p, const Piece& t, i
             }
         }
     }
-    const float scale = __ldg(p.scales + t.id);
+    const float scale = __ldcg(p.scales + t.id);
 #pragma unroll
     for (int q = 0; q < NT; ++q)
         if (mine && q < t.n) {
@@ -862,7 +869,7 @@ __global__ void __launch_bounds__(kFewThreads) few_up_kernel(const __grid_consta
     __shared__ float h[kFewTile * 128];
     pdl_launch_dependents();
     // y, up and the batch were there before the first of the call's kernels began; alone, that one's sums are waited for
-    const Piece t = few_tile<ALONE>(p, blockIdx.x);
+    const Piece t = few_tile<ALONE, true>(p, blockIdx.x);
     const int o = blockIdx.y * kFewOut + threadIdx.x * 8;
     if (t.n > 0 && t.rank > 0) {
         if (t.n == 1) few_up<BF16, ALONE, 1>(p, t, o, h);
@@ -873,7 +880,7 @@ __global__ void __launch_bounds__(kFewThreads) few_up_kernel(const __grid_consta
         if (p.y_out != p.y && o < p.d_out)
             for (int q = 0; q < t.n; ++q)
                 *reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o) =
-                    *reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + q) * p.y_stride + o);
+                    __ldcg(reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + q) * p.y_stride + o));
     }
     if (!ALONE && blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
 }

@@ -272,6 +272,29 @@ def test_many_tiles(gdn, rank, d_in, d_out, dt):
     assert torch.equal(c.run(gdn, out=c.y), out)      # in place
 
 
+@pytest.mark.parametrize("lengths", [[1, 3, 2, 1], [300, 2, 1, 5], [200]])
+def test_inputs_written_right_before_the_call(gdn, lengths):
+    """Every input is new, written by the kernels in front of the call, over buffers that the last call has read."""
+    n = len(lengths)
+    c = Case(lengths, [i % 3 for i in range(n)], 3, 16, 136, 264, "bf16", ranks=None)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    cu, ids = i32(c.cu), i32(c.ids)
+    ws = torch.empty(gdn.gdn_adapter_workspace_bytes(n, c.T, 16, 136), dtype=torch.uint8, device="cuda")
+    news = [[torch.randn(t.shape, generator=g, device="cuda").to(c.dt) for t in (c.x, c.y, c.down, c.up)] for _ in range(40)]
+    orders = [torch.randint(-1, 3, (n,), generator=g, device="cuda", dtype=torch.int32) for _ in range(40)]
+    out, outs = torch.empty_like(c.y), []
+    for new, order in zip(news, orders):
+        for t, v in zip((c.x, c.y, c.down, c.up), new):
+            t.copy_(v)
+        ids.copy_(order)
+        gdn.gdn_adapter_add(cu, c.T, ids, c.down, c.up, None, c.scales, c.x, c.y, out, ws)
+        outs.append(out.clone())
+    for new, order, got in zip(news, orders, outs):
+        c.x, c.y, c.down, c.up = new
+        c.ids = order.tolist()
+        c.check(got)
+
+
 def test_two_calls_at_once(gdn):
     """Two streams, each with its workspace, several calls each."""
     cases = [Case([500, 3, 260], [0, 1, 1], 2, 64, 1024, 2048, "bf16", seed=1), Case([1] * 200, [i % 2 for i in range(200)], 2, 64, 1024, 2048, "bf16", seed=2),
