@@ -19,8 +19,8 @@
 //
 // Smaller tiles (single tokens, drafts) read weights that nobody shares; what counts
 // for them is the chain from the batch's lengths to the last store.  They take two
-// kernels of their own, without rings or ranges, that run beside the others; a batch
-// with few tokens a sequence on average goes that way alone.
+// kernels of their own, without rings or ranges, that run beside the others; a small
+// batch goes that way alone.
 //
 // Measured (of what a plain copy reaches): @MEASURED@
 #include <algorithm>
@@ -43,7 +43,7 @@ constexpr int kRow = kK * 2;
 constexpr int kCtas = kAdapterCtas;
 constexpr int kTokenBytes = kTile * kRow;
 constexpr int kRing = 4;                             // chunks' products in TMEM
-constexpr int kPartsOut = 16;
+constexpr int kPartsOut = 16;                        // ranges of a tile's y at most, less one
 constexpr uint32_t kPolls = 1u << 18;                // of a wait: some two seconds
 constexpr int kColumnD = 256;                        // adapter_up's TMEM: h in the first R columns, products from here on
 
@@ -697,8 +697,8 @@ bool encode_maps(Maps& maps, const AdapterParams& p, const uint16_t* tokens, int
 // ---- few tokens -------------------------------------------------------------------
 //
 // A block takes 4 tokens of a sequence and some channels, on the CUDA cores, each thread's loads all under way at once,
-// the second kernel's before the first has ended.  Alone (ALONE, a batch with few tokens a sequence) they take every
-// token, and split x's channels among blocks; any lengths are right there, long ones only slow.  Beside the tensor
+// the second kernel's before the first has ended.  Alone (ALONE, a small batch) they take every
+// token, and split x's channels among blocks.  Beside the tensor
 // cores' kernels they take the tiles that those leave, and neither waits for nor holds up the kernel that it runs beside:
 // the order is adapter_down, few_down, adapter_up, few_up; each is there to read what the ones in front of the last
 // wrote, and its first block waits for the last at the end, so that whoever comes next has them all behind it.
@@ -706,9 +706,9 @@ constexpr int kFewThreads = 128, kFewTile = 4;
 constexpr int kFewRows = kFewThreads / 16;   // of `down`, two a warp
 constexpr int kFewIn = 1024;                 // x's channels at a time
 constexpr int kFewOut = kFewThreads * 8;
-// Tokens up to which a tile goes this way, and a batch's average up to which all of it does: the weights are read for
-// every 4 tokens, and the others' kernels copy whole tiles.  128 sequences of 12 tokens, 4096 to 10240: rank 16 52 us, 99
-// by the others; of 24 98 and 102; rank 64, of 12 138 and 107 (replayed).
+// Tokens up to which a tile goes this way: the weights are read for every 4 tokens, and the others' kernels copy whole
+// tiles.  128 sequences of 12 tokens, 4096 to 10240: rank 16 52 us, 99 by the others; of 24 98 and 102; rank 64, of 12 138
+// and 107 (replayed).
 int few_tokens(int rank) { return rank <= 16 ? 24 : rank <= 32 ? 16 : 8; }
 
 // A load in front of the kernel's wait (EARLY) comes from L2, as only the wait lets it trust what an SM's L1 holds.
@@ -898,11 +898,19 @@ cudaError_t launch_few_up(const AdapterParams& p, unsigned slots, cudaStream_t s
     return launch_k(few_up_kernel<BF16, ALONE>, dim3(slots, (unsigned)((p.d_out + kFewOut - 1) / kFewOut)), dim3(kFewThreads), 0, stream, true, p);
 }
 
-// by the batch's average, where the ranges' sums fit the workspace
+// Whether a batch goes this way alone, long sequences too, by the products that it takes: the other kernels cost some 10 us
+// whatever they do, and 2^27 products are about as much.  Replayed, alone and beside, us: 8 single tokens (rank 16, 5120 to
+// 5120) 4.6 and 13; 64 with rank 64 17.6 and 21; a prompt of 400 tokens, rank 16, 12.6 and 22.4, of 800 21.6 and 19.9; 128
+// single tokens, rank 64, 28.5 and 28.5; 64 and a chunk of 400, rank 128, 84 and 38; 255 and one of 1500, 290 and 101.
+#ifdef GDN_ADAPTER_SELFTEST_NEVER_ALONE
+constexpr int64_t kAloneWork = -1;  // tests: small batches through all kernels
+#else
+constexpr int64_t kAloneWork = 1 << 27;
+#endif
 bool goes_alone(const AdapterParams& p)
 {
     const int64_t splits = (p.d_in + kFewIn - 1) / kFewIn;
-    return p.T <= (int64_t)p.few * p.n_seq && p.T * (splits - 1) <= kCtas * kTile;
+    return (int64_t)p.T * p.rank * (p.d_in + p.d_out) <= kAloneWork && p.T * (splits - 1) <= kCtas * kTile;
 }
 
 template <bool BF16>

@@ -264,15 +264,14 @@ __device__ __forceinline__ void prefetch_map(const void* map) { asm volatile("pr
 
 // one box of a 3-D tensor map -> shared memory (dst on a 1024-byte boundary for a 128-byte swizzle); x times
 // the element size a multiple of 16 bytes; places outside the tensor are zeros
-__device__ __forceinline__ void tensor_g2s_3d(uint32_t dst, const void* map, int x, int y, int z, uint64_t* mbar)
+__device__ __forceinline__ void tensor_g2s_3d(void* dst, const void* map, int x, int y, int z, uint64_t* mbar)
 {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         :
-        : "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(mbar))
+        : "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(mbar))
         : "memory");
 }
-__device__ __forceinline__ void tensor_g2s_3d(void* dst, const void* map, int x, int y, int z, uint64_t* mbar) { tensor_g2s_3d(smem_u32(dst), map, x, y, z, mbar); }
 
 // the same of a 2-D tensor map
 __device__ __forceinline__ void tensor_g2s_2d(uint32_t dst, const void* map, int x, int y, uint64_t* mbar)

@@ -14,14 +14,20 @@ S = 2.0 ** -23
 DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
 
 
-@pytest.fixture(scope="module", autouse=True)
-def gdn():
+@pytest.fixture(scope="module", autouse=True, params=["as_chosen", "never_alone"])
+def gdn(request, tmp_path_factory):
+    """The package, and with a library whose small batches go through the tensor cores' kernels too."""
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
-    from gated_deltanet_linear_pre_gb300 import build
+    from gated_deltanet_linear_pre_gb300 import _native, build
     build.build()
     import gated_deltanet_linear_pre_gb300 as g
-    return g
+    with pytest.MonkeyPatch.context() as m:
+        if request.param == "never_alone":
+            from selftest_lib import adapter_library
+            m.setattr(_native, "_lib", None)
+            m.setattr(_native._build, "LIB", adapter_library(str(tmp_path_factory.mktemp("adapter")), "GDN_ADAPTER_SELFTEST_NEVER_ALONE"))
+        yield g
 
 
 def f64(t):

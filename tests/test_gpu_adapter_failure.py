@@ -5,10 +5,6 @@ A library of its own is built here in which every CTA of those kernels leaves ou
 wait for it runs out (seconds), and with it the waits of the CTA's other warps; the CTA begins nothing more, waits for
 what it has under way, frees its tensor memory and ends.  gdn_adapter_check then reports GDN_ERR_TIMEOUT, and the same
 context, workspace and buffers go on to compute right results."""
-import glob
-import os
-import subprocess
-
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -21,17 +17,8 @@ def withholding(tmp_path_factory):
     """Path of the library without those kernels' first copies."""
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
-    from gated_deltanet_linear_pre_gb300 import build
-    build.build()
-    out = tmp_path_factory.mktemp("withholding")
-    obj, lib = str(out / "adapter.o"), str(out / "libgdn_withholding.so")
-    nvcc = build._nvcc()
-    src = os.path.join(build.CSRC, "gdn_adapter.cu")
-    subprocess.run([nvcc, *build.ARCH, *build.NVCC_FLAGS, "-DGDN_ADAPTER_SELFTEST_WITHHOLD_COPY", "-c", src, "-o", obj], check=True)
-    others = [o for o in glob.glob(os.path.join(build.BUILD, "*.o")) if not o.endswith("gdn_adapter.o")]
-    libs = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "lib64")
-    subprocess.run([nvcc, *build.ARCH, "-shared", "-cudart", "shared", "-o", lib, obj, *others, "-Xlinker", f"-rpath,{libs}"], check=True)
-    return lib
+    from selftest_lib import adapter_library
+    return adapter_library(str(tmp_path_factory.mktemp("withholding")), "GDN_ADAPTER_SELFTEST_WITHHOLD_COPY")
 
 
 @pytest.mark.parametrize("lengths,rank", [([3000, 5, 700, 1], 64), ([40, 900], 128)])
