@@ -215,6 +215,7 @@ size_t compact_sums(int n_pages);
 cudaError_t launch_kv_remap(const RemapParams& p, cudaStream_t stream);
 cudaError_t launch_kv_compact(const CompactParams& p, cudaStream_t stream);
 cudaError_t launch_kv_copy(const CopyParams& p, cudaStream_t stream);
+
 constexpr int kAdapterCtas = 152;
 
 // where a CTA's range of units begins: a sequence (n_seq: no work), its tile, the cost of all units in front of that

@@ -1,6 +1,8 @@
 // gdn_kv_copy.cu -- pages copied within the caches of all layers in one launch.
 //
-// HBM-bound.  A warp moves 4 KB at a time, 8 independent 16-byte loads a lane.
+// HBM-bound.  A warp moves 4 KB at a time, 8 independent 16-byte loads a lane: 705 MB
+// read and written in 110 us, 6.4 TB/s, 94% of what a plain copy reaches (12 layers,
+// pages of 128 KB for keys and for values, 112 pairs among 125); 179 MB in 29 us, 6.2 TB/s.
 // Lists may be mostly empty (gdn_kv_remap has an entry for every row): each
 // block gathers the entries that name two pages, and all warps of the grid share
 // the pieces of those pages, layer by layer.

@@ -559,8 +559,9 @@ GDN_API gdn_status gdn_kv_compact(int32_t n_pages, int32_t max_pages, int32_t n_
  * that is copied to is in the lists once (twice, or as a source too: its
  * contents are then some mixture of the pages named).
  *
- * In:  caches      host array of n_caches caches with the same heads, head_dim,
- *                  page_tokens, n_pages and format, none overlapping another
+ * In:  caches      host array of n_caches caches (up to 1024) with the same heads,
+ *                  head_dim, page_tokens, n_pages and format, none overlapping
+ *                  another
  *      copy_from, copy_to  int32 [n] (device, 4-byte aligned)
  */
 GDN_API gdn_status gdn_kv_copy(const gdn_kv_cache* caches, int32_t n_caches, int32_t n, const int32_t* copy_from,
@@ -625,10 +626,10 @@ GDN_API gdn_status gdn_block_norm(int32_t x_dtype, int32_t dtype, int32_t total_
  *              the q slice of a packed projection, say)
  * Out: y_out   [T][d_out] of `dtype`, y_out_stride apart; may be y itself with
  *              the same stride, else overlaps no input
- * rank: a multiple of 8 up to 128; d_in, d_out: multiples of 8 up to 65536.
- * ids and ranks need 4-byte alignment only.  Sums are fp32; h enters its
- * product in two pieces of the weights' type (16 bits or more), and y_out is
- * rounded once.  Values of x and of the weights that are not finite reach the
+ * rank: a multiple of 8 up to 128; d_in, d_out: multiples of 8 up to 65536;
+ * n_adapters up to 2^20.  ids, ranks and scales need 4-byte alignment only.
+ * Sums are fp32; h enters its product in fp32 or in two pieces of the weights'
+ * type (16 bits or more), and y_out is rounded once.  Values of x and of the weights that are not finite reach the
  * tokens, and the channels, that their products reach.
  * workspace: device scratch of at least gdn_adapter_workspace_bytes() bytes (0
  * for a shape that is refused, and for no tokens); contents on entry are
