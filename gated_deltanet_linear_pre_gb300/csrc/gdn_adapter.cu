@@ -733,7 +733,7 @@ __device__ __forceinline__ Piece few_tile(const AdapterParams& p, int slot)
         const auto base = [&](int i) { return (int64_t)(cu(i) / kFewTile + i); };
         s = warp_find(p.n_seq, slot, base);
         end = cu(s + 1);
-        start = cu(s) + (slot - base(s)) * kFewTile;
+        start = cu(s) + max((int64_t)0, slot - base(s)) * kFewTile;
     } else {      // p.few tokens' slots a sequence, for its last ones
         const int first = cu(s);
         end = cu(s + 1);
