@@ -242,7 +242,8 @@ struct AdapterParams {
     int chunks_in, chunks_out, parts_in;  // units of a tile; ranges that one is cut into (set by launch_adapter)
     // workspace (set by launch_adapter): a word for each CTA of either kernel, 0 or a wait that has expired; per CTA, where
     // its range of y's units begins; per tile, the first and the last range of x's units that it lies in;
-    // h [T + ranges * 128][rank]: what the range that a tile begins in summed, then what each of the others did
+    // h [T + ranges * 128][rank]: what the range that a tile begins in summed, then what each of the others did (a tile's
+    // tokens change places with its rank; the few tokens' do not)
     int32_t* status;
     AdapterStart* starts;
     int2* parts;
