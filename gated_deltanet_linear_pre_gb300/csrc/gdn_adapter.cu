@@ -13,8 +13,8 @@
 // tile where its range ends; a tile that lies in several ranges has its h in several
 // sums, which adapter_up adds in order.  One warp copies (TMA boxes of 64 channels,
 // into a ring of stages of 128-byte swizzled rows), far ahead of the others; one
-// issues the products (tcgen05, 16-bit operands, fp32 sums in TMEM); eight take what
-// comes of them on.  h enters its product there as hi + lo in the weights' type: 16 bits of
+// issues the products (tcgen05, 16-bit operands, fp32 sums in TMEM); eight, or in
+// adapter_up two teams of eight in turn, take what comes of them on.  h enters its product there as hi + lo in the weights' type: 16 bits of
 // it in bf16, 21 of its row's largest in fp16, far below the rounding of y_out.
 //
 // Smaller tiles (single tokens, drafts) read weights that nobody shares; what counts
@@ -23,11 +23,12 @@
 // batch goes that way alone.
 //
 // Measured (one GB300; the floor is the bytes that have to move, at a plain copy's rate): 8 prompts of 1 to 4096 tokens,
-// rank 64, 4096 to 6144, fp16 143 us, 75% of the floor's rate (298 in the first form, by mma.sync in tiles of 64 tokens);
+// rank 64, 4096 to 6144, fp16 137 us, 78% of the floor's rate (298 in the first form, by mma.sync in tiles of 64 tokens);
 // one token of 64 sequences, rank 16, 4096 to 10240, 9.3 us replayed (floor 2.8); a 3001-token prompt beside 39 drafts,
-// ranks of 8 to 128, 2048 to 10240, 69 us (floor 25; 181 in the first form); 8192 tokens, 2048 to 10240, rank 16 73 us,
-// 64 89, 128 102 (floor 55).  What is left is the workers' part of adapter_up: TMEM, y and y_out of a unit one after the
-// other, with the warps of one CTA to cover for one another (167 registers, 16% of the SM's warps).
+// ranks of 8 to 128, 2048 to 10240, 69 us (floor 25; 181 in the first form); 8192 tokens, 2048 to 10240, rank 16 72 us,
+// 64 77, 128 96 (floor 55).  What is left: the start of either kernel (some 5 us: lengths, ranges, the first copies; h), and
+// reads and writes mixed, 5.5 TB/s in adapter_up; where few tokens stand beside a prompt, few_up, which gets the SMs when
+// adapter_up leaves them (its registers are taken; with fewer for either kernel 71 to 81 us for 69).
 #include <algorithm>
 #include <type_traits>
 
