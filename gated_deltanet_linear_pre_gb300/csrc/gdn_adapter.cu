@@ -58,7 +58,8 @@ constexpr int kPartsOut = 16;                        // ranges of a tile's y at 
 constexpr uint32_t kPolls = 1u << 18;                // of a wait: some two seconds
 constexpr int kColumnD = 256;                        // adapter_up's TMEM: h in the first R columns, products from here on
 
-// Stages leave some L1: 8192 tokens, rank 64, 2048 to 10240, 6 stages 80.5 us, 7 84.3; rank 128, 4 100.5, 3 106.5
+// Stages leave some L1: 8192 tokens, rank 64, 2048 to 10240, 6 stages 77.4 us, 7 80.4; 255 single tokens beside 1500, rank
+// 128, 5120 to 5120, 4 99.5, 5 105 (8192 tokens 97.8 and 97.2, with 3 106)
 template <int R> constexpr int kStages = R > 64 ? 4 : R > 32 ? 6 : 7;
 template <int R> constexpr int kStageBytes = kTokenBytes + R * kRow;
 constexpr int kResultBytes = 32 * 64;                // a worker's part of a chunk of y_out, on its way out
@@ -741,8 +742,8 @@ constexpr int kFewRows = kFewThreads / 16;   // of `down`, two a warp
 constexpr int kFewIn = 1024;                 // x's channels at a time
 constexpr int kFewOut = kFewThreads * 8;
 // Tokens up to which a tile goes this way: the weights are read for every 4 tokens, and the others' kernels copy whole
-// tiles.  128 sequences of 12 tokens, 4096 to 10240: rank 16 52 us, 99 by the others; of 24 98 and 102; rank 64, of 12 138
-// and 107 (replayed).
+// tiles.  128 sequences of 12 tokens, 4096 to 10240: rank 16 54 us, 100 by the others; of 24 97 and 103; rank 64, of 12 135
+// and 110 (replayed).
 int few_tokens(int rank) { return rank <= 16 ? 24 : rank <= 32 ? 16 : 8; }
 
 // A load in front of the kernel's wait (EARLY) comes from L2, as only the wait lets it trust what an SM's L1 holds.
@@ -934,8 +935,8 @@ cudaError_t launch_few_up(const AdapterParams& p, unsigned slots, cudaStream_t s
 
 // Whether a batch goes this way alone, long sequences too, by the products that it takes: the other kernels cost some 10 us
 // whatever they do, and 2^27 products are about as much.  Replayed, alone and beside, us: 8 single tokens (rank 16, 5120 to
-// 5120) 4.6 and 13; 64 with rank 64 17.6 and 21; a prompt of 400 tokens, rank 16, 12.6 and 22.4, of 800 21.6 and 19.9; 128
-// single tokens, rank 64, 28.5 and 28.5; 64 and a chunk of 400, rank 128, 84 and 38; 255 and one of 1500, 290 and 101.
+// 5120) 4.6 and 11; 64 with rank 64 17.4 and 21.7; a prompt of 400 tokens, rank 16, 12.5 and 20.8, of 800 21.6 and 20.1; 128
+// single tokens, rank 64, 28.6 and 28.6; 64 and a chunk of 400, rank 128, 85 and 35; 255 and one of 1500, 292 and 100.
 #ifdef GDN_ADAPTER_SELFTEST_NEVER_ALONE
 constexpr int64_t kAloneWork = -1;  // tests: small batches through all kernels
 #else
@@ -962,8 +963,8 @@ cudaError_t launch_rank(const AdapterParams& p, cudaStream_t stream)
     if (!encode_maps(in, p, p.x, p.x_stride, p.down, p.d_in) || !encode_maps(out, p, p.y, p.y_stride, p.up, p.d_out)) return cudaErrorNotSupported;
     const unsigned slots = (unsigned)p.n_seq * (unsigned)(p.few / kFewTile);
     // adapter_up may start while the kernels in front of it end, but not in a batch of prompts.  Replayed, so and so, us: 8192
-    // tokens, rank 64, 2048 to 10240, 80.5 and 77.0; 4 prompts of 90 to 1200 40.4 and 37.3; 3001 beside 40 drafts of 3 53.3
-    // and 55.1; 255 single tokens beside 1500 65.7 and 66.2.
+    // tokens, rank 64, 2048 to 10240, 80.0 and 77.3; 4 prompts of 90 to 1200 39.1 and 37.3; 3001 beside 40 drafts of 3 53.5
+    // and 55.5; 255 single tokens beside 1500 66.1 and 67.2.
     const bool early = p.T < (int64_t)kTile * p.n_seq;
     cudaError_t e = cudaFuncSetAttribute(adapter_down_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(adapter_up_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
@@ -1003,7 +1004,7 @@ cudaError_t launch_adapter(AdapterParams p, void* workspace, cudaStream_t stream
     p.chunks_out = (p.d_out + kK - 1) / kK;
     // Each part of a tile's h takes adapter_up over a microsecond to add, each unit of a range adapter_down half of one:
     // about sqrt(units) / 2 parts are best where there are more CTAs than tiles (one prompt of 3001 tokens, rank 128, 2048
-    // to 10240: 63.6 us, 78.9 with up to 16).
+    // to 10240: 56.6 us, 64.1 with up to 16).
     for (p.parts_in = 2; 4 * p.parts_in * p.parts_in < p.chunks_in; ++p.parts_in) {}
     const auto launch = [&](auto bf16) {
         constexpr bool kBf16 = decltype(bf16)::value;
