@@ -505,20 +505,15 @@ __device__ __forceinline__ void operand(const AdapterParams& p, const Piece& t, 
             const float* src = p.h + (r + i == b.x ? (size_t)t.start : (size_t)p.T + (size_t)(r + i) * kTile) * p.rank + row;
 #pragma unroll
             for (int j = 0; j < kMine; j += kBlock) {
-                const float* at = src + max(steps.row_of(col + j), 0) * t.n;  // (a tile has room for all of p.rank)
+                const int at = steps.row_of(col + j), left = row < t.n && r + i <= b.y && at >= 0 ? t.rank - at : 0;
 #pragma unroll
-                for (int e = 0; e < kBlock; ++e) f[i][j + e] = load_now(at + e * t.n, row < t.n && r + i <= b.y);
+                for (int e = 0; e < kBlock; ++e) f[i][j + e] = load_now(src + (at + e) * t.n, e < left);
             }
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
 #pragma unroll
             for (int j = 0; j < kMine; ++j) v[j] += f[i][j];
-    }
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int at = steps.row_of(col + j);
-        if (at < 0 || at >= t.rank) v[j] = 0.0f;
     }
     float inv = 1.0f, factor = __ldg(p.scales + t.id);
     if (!BF16) {

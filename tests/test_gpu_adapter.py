@@ -278,6 +278,15 @@ def test_many_tiles(gdn, rank, d_in, d_out, dt):
     assert torch.equal(c.run(gdn, out=c.y), out)      # in place
 
 
+@pytest.mark.parametrize("rank", [24, 40, 72, 104])
+def test_low_ranks_among_high_ones(gdn, rank):
+    """Prompts cut into ranges by all CTAs, whose adapters use few of the ranks that there is room for."""
+    c = Case([4000, 700, 130, 2000], [0, 1, 2, 3], 4, rank, 1024, 2056, "bf16", ranks=[16, 1, 8, 17])
+    out = c.run(gdn)
+    c.check(out)
+    assert torch.equal(out, c.run(gdn))
+
+
 @pytest.mark.parametrize("lengths", [[1, 3, 2, 1], [300, 2, 1, 5], [200]])
 def test_inputs_written_right_before_the_call(gdn, lengths):
     """Every input is new, written by the kernels in front of the call, over buffers that the last call has read."""
