@@ -14,8 +14,9 @@
 // sums, which adapter_up adds in order.  One warp copies (TMA boxes of 64 channels,
 // into a ring of stages of 128-byte swizzled rows), far ahead of the others; one
 // issues the products (tcgen05, 16-bit operands, fp32 sums in TMEM); eight, or in
-// adapter_up two teams of eight in turn, take what comes of them on.  h enters its product there as hi + lo in the weights' type: 16 bits of
-// it in bf16, 21 of its row's largest in fp16, far below the rounding of y_out.
+// adapter_up two teams of eight in turn, take what comes of them on.  h enters its
+// product there as hi + lo in the weights' type: 16 bits of it in bf16, 21 of its
+// row's largest in fp16, far below the rounding of y_out.
 //
 // Smaller tiles (single tokens, drafts) read weights that nobody shares; what counts
 // for them is the chain from the batch's lengths to the last store.  They take two
