@@ -518,7 +518,9 @@ __device__ __forceinline__ void operand(const AdapterParams& p, const Piece& t, 
     }
     float inv = 1.0f, factor = __ldg(p.scales + t.id);
     if (!BF16) {
-        // a row's largest value to [1, 2): fp16 has 5 bits of exponent
+        // A row's largest value to [2^14, 2^15): fp16 has 5 bits of exponent.  A value keeps 22 bits, or is off by half the
+        // type's least step, 2^-25, which is 2^-39 of that largest (with the largest in [1, 2) values 2^14 below it came
+        // out with the bits of the output, those 2^23 below with two).
         float most = 0.0f;
 #pragma unroll
         for (int j = 0; j < kMine; ++j) most = fmaxf(most, fabsf(v[j]));
@@ -526,7 +528,7 @@ __device__ __forceinline__ void operand(const AdapterParams& p, const Piece& t, 
         workers_sync();
 #pragma unroll
         for (int i = 0; i < kParts; ++i) most = fmaxf(most, sm.most[i][row]);
-        const int exponent = min(max((int)(__float_as_uint(most) >> 23) - 127, -126), 126);
+        const int exponent = max((int)(__float_as_uint(most) >> 23) - 127 - 14, -126);  // up to 114
         inv = __uint_as_float((uint32_t)(127 - exponent) << 23);
         factor *= __uint_as_float((uint32_t)(127 + exponent) << 23);
     }

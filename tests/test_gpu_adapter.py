@@ -185,6 +185,37 @@ def test_sizes_far_apart(gdn, dt):
     c.check(c.run(gdn))
 
 
+@pytest.mark.parametrize("apart", [6, 12, 18, 23])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_small_values_of_h_that_decide(gdn, dt, apart):
+    """A token's h whose largest value meets small weights, and its small ones, 2^apart below, large weights: what
+    counts is the bits of each value, not those of the largest.
+
+    Tolerances.  h itself is exact here (sums of whole multiples of 2^-apart).  In bf16 its two pieces leave 2^-17 of a
+    value; in fp16, scaled to below 2^15, 2^-23 of it or 2^-25, half of the type's least step, which is 2^-39 of the row's
+    largest.  The sum over the ranks and the output's rounding as above."""
+    c = Case([40, 130, 3], [0, 1, 0], 2, 16, 128, 192, dt, seed=apart)
+    c.x.copy_(c.x.float().sign())
+    c.down[:, 0] = 64.0
+    odd = 65.0 + 2 * torch.arange(15, device="cuda")[:, None]     # 7 bits
+    c.down[:, 1:] = (c.down[:, 1:].float().sign() * odd * 2.0 ** -apart).to(c.dt)
+    c.up[:, 0] = 2.0 ** -14
+    c.up[:, 1:] = (c.up[:, 1:].float().clamp(-1, 1) * 128).to(c.dt)
+    c.y.zero_()
+    got, eps = f64(c.run(gdn)), torch.finfo(c.dt).eps / 2
+    tiny = float(torch.finfo(c.dt).smallest_normal) * eps
+    for s, a in enumerate(c.ids):
+        rows = slice(c.cu[s], c.cu[s + 1])
+        up, scale = f64(c.up[a]), f64(c.scales)[a]
+        h = f64(c.x[rows]) @ f64(c.down[a]).T
+        dh = np.maximum(2.0 ** -23 * np.abs(h), 2.0 ** -39 * np.abs(h).max(1, keepdims=True)) if dt == "fp16" else 2.0 ** -17 * np.abs(h)
+        ref = scale * (h @ up)
+        bound = abs(scale) * (dh @ np.abs(up) + (16 / 8 + 32) * S * (np.abs(h) @ np.abs(up)))
+        limit = bound + eps * (np.abs(ref) + bound) + 2 * tiny
+        off = np.abs(got[rows] - ref)
+        assert (off <= limit).all(), (s, float((off / limit).max()))
+
+
 @pytest.mark.parametrize("dt", ["fp16", "bf16"])
 def test_values_that_are_not_finite(gdn, dt):
     c = Case([5, 20, 70], [0, 1, 0], 2, 16, 136, 200, dt)
