@@ -172,6 +172,31 @@ def test_gates_at_their_ends(gdn):
     assert torch.isfinite(xo).all()
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "silu"])
+@pytest.mark.parametrize("xt,dt", [("fp16", "fp16"), ("bf16", "bf16"), ("fp32", "fp16"), ("fp32", "bf16")])
+def test_the_gates_range(gdn, xt, dt, kind):
+    """The gated term alone (x is 0), from gates whose sigmoid a large y makes visible to those that leave y as it is.
+
+    Tolerances, e = 2^-24.  expf is off by 2 units (4 e), the hardware's exponential by 2 + 1.173 |g| units; 1 + exp(-|g|) by e,
+    the quotient by 2 units, the products with g, y and scale and the sum by e each: 12 e and the exponential.  An
+    exponential below 2^-126 is a multiple of 2^-149, as is its quotient: two of those."""
+    big = 60000.0 if dt == "fp16" else 1e38
+    ends = [-88.5, -88.0, -87.5, -87.25, -86.0, -40.0, -20.0, -17.0, -9.0, -3.0, -0.5, -1e-3, 0.0, 1e-3, 0.5, 3.0, 9.0, 20.0, 88.0, 200.0, 60000.0, -60000.0]
+    g = torch.tensor((ends * 3)[:64], device="cuda").to(DT[dt]).expand(3, 64)
+    x = torch.zeros((3, 64), dtype=DT[xt], device="cuda")
+    y = torch.full((3, 64), big, dtype=DT[dt], device="cuda")
+    y[1], y[2] = 1.0, -big
+    if kind == "silu":      # g * y stays in the type's range
+        y = torch.where(g > 0.5, torch.full_like(y, 0.5), y)
+    xo, _ = call(gdn, x, y, g, kind, 1.0, None, torch.ones(64, device="cuda"))
+    gate, u = f64(g), f64(y)
+    s = np.where(gate < 0, np.exp(np.minimum(gate, 0)), 1.0) / (1.0 + np.exp(-np.abs(gate)))
+    factor = gate if kind == "silu" else 1.0
+    ref = u * s * factor
+    units = 2.0 if xt == "fp32" else 2.0 + 1.173 * np.abs(gate)
+    close(xo, ref, (12 + 2 * units) * E * np.abs(ref) + 2 * 2.0 ** -149 * np.abs(u * factor), kind)
+
+
 def test_no_tokens(gdn):
     x = torch.empty((0, 128), dtype=torch.float16, device="cuda")
     w = torch.ones(128, device="cuda")
