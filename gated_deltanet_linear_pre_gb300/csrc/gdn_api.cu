@@ -112,12 +112,13 @@ gdn_status check_disjoint(const Buf* outs, int n_out, const Buf* ins, int n_in)
     return GDN_OK;
 }
 
-gdn_status check_stride(const char* name, int64_t stride, size_t row)
+gdn_status check_stride(const char* name, int64_t stride, size_t row, int32_t T)
 {
     if (stride < (int64_t)row) return fail(GDN_ERR_INVALID_ARG, "%s_stride=%lld is shorter than a row of %zu", name, (long long)stride, row);
     if (stride % 8) return fail(GDN_ERR_ALIGNMENT, "%s_stride=%lld is not a multiple of 8", name, (long long)stride);
-    // an array's length in bytes stays in 63 bits
-    if (stride > (1 << 30)) return fail(GDN_ERR_UNSUPPORTED, "%s_stride=%lld above 2^30", name, (long long)stride);
+    // what an array spans is counted in 64 bits; no address space holds this much
+    if (T > 1 && stride > ((int64_t)1 << 58) / (T - 1))
+        return fail(GDN_ERR_UNSUPPORTED, "%d tokens %s_stride=%lld apart span more than 2^58 elements", T, name, (long long)stride);
     return GDN_OK;
 }
 

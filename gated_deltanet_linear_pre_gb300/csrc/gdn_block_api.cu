@@ -13,6 +13,14 @@ namespace {
 bool known_rank(int32_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
 bool known_width(int32_t d) { return d >= 8 && d <= 65536 && d % 8 == 0; }
 
+// rows that stand no further apart than these entries take them
+gdn_status check_near(const char* name, int64_t stride, size_t row, int32_t T)
+{
+    const gdn_status st = check_stride(name, stride, row, T);
+    if (st == GDN_OK && stride > (1 << 30)) return fail(GDN_ERR_UNSUPPORTED, "%s_stride=%lld above 2^30", name, (long long)stride);
+    return st;
+}
+
 }  // namespace
 
 extern "C" {
@@ -35,9 +43,9 @@ gdn_status gdn_block_norm(int32_t x_dtype, int32_t dtype, int32_t T, int32_t wid
     if (!gate != (gate_kind == GDN_GATE_NONE)) return fail(GDN_ERR_INVALID_ARG, "gate and gate_kind=%d do not go together", gate_kind);
     if (!y && (gate || post_weight || x_out)) return fail(GDN_ERR_INVALID_ARG, "without y there is no gate, post_weight or x_out");
     gdn_status st;
-    if ((st = check_stride("x", x_stride, width)) != GDN_OK) return st;
-    if (y && (st = check_stride("y", y_stride, width)) != GDN_OK) return st;
-    if (gate && gate_stride != 0 && (st = check_stride("gate", gate_stride, width)) != GDN_OK) return st;
+    if ((st = check_near("x", x_stride, width, T)) != GDN_OK) return st;
+    if (y && (st = check_near("y", y_stride, width, T)) != GDN_OK) return st;
+    if (gate && gate_stride != 0 && (st = check_near("gate", gate_stride, width, T)) != GDN_OK) return st;
     const size_t row = (size_t)width, x_bytes = x_dtype == GDN_FP32 ? 4 : 2, weight = row * 4;
     const Buf ins[] = {{x, span(T, x_stride, row, x_bytes), "x"}, {y, y ? span(T, y_stride, row, 2) : 0, "y"},
                        {gate, gate ? span(T, gate_stride, row, 2) : 0, "gate"}, {post_weight, post_weight ? weight : 0, "post_weight"},
@@ -79,9 +87,9 @@ gdn_status gdn_adapter_add(int32_t dtype, int32_t n_seq, int32_t T, const int32_
     if (n_adapters > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "n_adapters=%d above 2^20", n_adapters);
     if (!known_rank(rank)) return fail(GDN_ERR_UNSUPPORTED, "rank=%d must be a multiple of 8 up to 128", rank);
     if (!known_width(d_in) || !known_width(d_out)) return fail(GDN_ERR_UNSUPPORTED, "d_in=%d and d_out=%d must be multiples of 8 up to 65536", d_in, d_out);
-    if ((st = check_stride("x", x_stride, d_in)) != GDN_OK) return st;
-    if ((st = check_stride("y", y_stride, d_out)) != GDN_OK) return st;
-    if ((st = check_stride("y_out", y_out_stride, d_out)) != GDN_OK) return st;
+    if ((st = check_near("x", x_stride, d_in, T)) != GDN_OK) return st;
+    if ((st = check_near("y", y_stride, d_out, T)) != GDN_OK) return st;
+    if ((st = check_near("y_out", y_out_stride, d_out, T)) != GDN_OK) return st;
     if (T == 0) return GDN_OK;  // empty arrays may be NULL
     const size_t n = (size_t)n_adapters, need = gdn_adapter_workspace_bytes(n_seq, T, rank, d_in);
     const Buf lists[] = {{ids, (size_t)n_seq * 4, "ids"}, {ranks, ranks ? n * 4 : 0, "ranks"}, {scales, n * 4, "scales"}};

@@ -33,8 +33,8 @@ bool overlap(const Buf& a, const Buf& b);
 // no output may overlap another output or any input
 gdn_status check_disjoint(const Buf* outs, int n_out, const Buf* ins, int n_in);
 
-// token rows of `row` elements, `stride` apart, read in 16-byte pieces
-gdn_status check_stride(const char* name, int64_t stride, size_t row);
+// T token rows of `row` elements, `stride` apart, read in 16-byte pieces
+gdn_status check_stride(const char* name, int64_t stride, size_t row, int32_t T);
 // bytes from the first element of a strided [T][row] array to its last
 inline size_t span(int32_t T, int64_t stride, size_t row, size_t element)
 {

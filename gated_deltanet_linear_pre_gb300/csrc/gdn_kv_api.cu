@@ -86,9 +86,9 @@ gdn_status gdn_kv_append(const gdn_kv_cache* cache, int32_t dtype, int32_t n_seq
     const size_t d = cache->head_dim, rowq = (size_t)hq * d, rowk = (size_t)cache->heads * d;
     if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16) return fail(GDN_ERR_UNSUPPORTED, "rot_dim=%d must be a multiple of 16 up to head_dim", rot_dim);
     if (rot_dim > 0 && n_pos < 1) return fail(GDN_ERR_INVALID_ARG, "n_pos=%d: the rotation table is empty", n_pos);
-    if (hq > 0 && (st = check_stride("q", q_stride, rowq)) != GDN_OK) return st;
-    if ((st = check_stride("k", k_stride, rowk)) != GDN_OK) return st;
-    if ((st = check_stride("v", v_stride, rowk)) != GDN_OK) return st;
+    if (hq > 0 && (st = check_stride("q", q_stride, rowq, T)) != GDN_OK) return st;
+    if ((st = check_stride("k", k_stride, rowk, T)) != GDN_OK) return st;
+    if ((st = check_stride("v", v_stride, rowk, T)) != GDN_OK) return st;
     const size_t tt = (size_t)T, table_bytes = rot_dim > 0 && T > 0 ? (size_t)n_pos * (rot_dim / 2) * 4 : 0;
     const size_t codes = (size_t)cache->n_pages * rowk * cache->page_tokens, scales = (size_t)cache->n_pages * cache->heads * 4;
     const Buf ins[] = {{q, hq ? span16(T, q_stride, rowq) : 0, "q"}, {k, span16(T, k_stride, rowk), "k"}, {v, span16(T, v_stride, rowk), "v"},
@@ -129,7 +129,7 @@ gdn_status gdn_kv_attn(const gdn_kv_cache* cache, int32_t dtype, int32_t n_seq, 
     if (hq > 65535) return fail(GDN_ERR_UNSUPPORTED, "hq=%d above 65535", hq);
     if (!std::isfinite(softmax_scale)) return fail(GDN_ERR_INVALID_ARG, "softmax_scale is not finite");
     const size_t row = (size_t)hq * cache->head_dim, tt = (size_t)T;
-    if ((st = check_stride("q", q_stride, row)) != GDN_OK) return st;
+    if ((st = check_stride("q", q_stride, row, T)) != GDN_OK) return st;
     const size_t need = gdn_kv_attn_workspace_bytes(cache, n_seq, T, hq, max_pages);
     if (workspace_bytes < need || (need && !workspace)) return fail(GDN_ERR_WORKSPACE, "attention workspace %zu bytes, need %zu", workspace_bytes, need);
     const size_t codes = (size_t)cache->n_pages * cache->heads * cache->page_tokens * cache->head_dim;

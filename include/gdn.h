@@ -370,8 +370,9 @@ typedef struct gdn_kv_cache {
  * In:  past     int32 [n_seq] (device)
  *      q        [T][hq][head_dim], k, v [T][heads][head_dim] of `dtype`; tokens
  *               are q_stride, k_stride, v_stride elements apart (multiples of
- *               8: the three may be slices of one packed projection).  q may be
- *               NULL (hq 0): only k and v are stored.
+ *               8: the three may be slices of one packed projection, or lie
+ *               further apart; arrays that span more than 2^58 elements are
+ *               refused).  q may be NULL (hq 0): only k and v are stored.
  *      cos, sin fp32 [n_pos][rot_dim / 2], the rotation of each position
  *               (positions past the table take its last row); NULL with
  *               rot_dim 0 for none.  rot_dim: a multiple of 16 up to head_dim;
@@ -516,8 +517,8 @@ GDN_API gdn_status gdn_draft_verify(int32_t n_seq, int32_t max_draft, int32_t vo
  *                  were wanted and not there
  * Nothing is kept between calls: what a row does not name is free.  To hold
  * pages for later (a shared prompt, say) keep a row for them.
- * page_tokens as in gdn_kv_cache; n_pages up to 2^28; n_rows * max_pages and
- * max_pages * page_tokens up to 2^30.  The int32 arrays need 4-byte alignment
+ * page_tokens as in gdn_kv_cache; n_pages up to 2^28; n_rows * max_pages,
+ * max_pages * page_tokens and the tables' strides up to 2^30.  The int32 arrays need 4-byte alignment
  * only.  workspace: at least gdn_kv_remap_workspace_bytes() bytes (0 for a
  * shape that is refused); contents on entry are ignored, calls sharing one must
  * not overlap on the GPU.  May be captured into a CUDA graph.
@@ -594,7 +595,7 @@ typedef enum gdn_gate { GDN_GATE_NONE = 0, GDN_GATE_LINEAR = 1, GDN_GATE_SIGMOID
  *      post_weight, pre_weight  fp32 [width]; post_weight NULL: y is taken as
  *              it is; pre_weight NULL with h NULL
  *      Tokens are x_stride, y_stride, gate_stride elements apart (multiples of
- *      8; y may be a slice of a wider row).
+ *      8 up to 2^30; y may be a slice of a wider row).
  * Out: x_out   [T][width] dense, of x_dtype; NULL: x' is not wanted (behind the
  *              last block).  May be x itself where x_stride == width; overlaps
  *              nothing else.
@@ -622,8 +623,8 @@ GDN_API gdn_status gdn_block_norm(int32_t x_dtype, int32_t dtype, int32_t total_
  *      down    [n_adapters][rank][d_in], up [n_adapters][rank][d_out], of `dtype`
  *      scales  fp32 [n_adapters]
  *      x       [T][d_in], y [T][d_out] of `dtype` (GDN_FP16 or GDN_BF16); tokens
- *              are x_stride, y_stride elements apart (multiples of 8: y may be
- *              the q slice of a packed projection, say)
+ *              are x_stride, y_stride elements apart (multiples of 8 up to 2^30:
+ *              y may be the q slice of a packed projection, say)
  * Out: y_out   [T][d_out] of `dtype`, y_out_stride apart; may be y itself with
  *              the same stride, else overlaps no input
  * rank: a multiple of 8 up to 128; d_in, d_out: multiples of 8 up to 65536;

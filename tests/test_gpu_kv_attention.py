@@ -531,6 +531,29 @@ def test_strided_and_cut_inputs():
     b.table = kept
 
 
+@pytest.mark.parametrize("hq,heads", [(6, 2), (64, 1)])
+def test_tokens_far_apart(hq, heads):
+    """Two tokens 2^30 elements and more apart, as single rows and as rows enough for the prompts' kernels, give what
+    dense ones give."""
+    b = Batch([2], [100], hq, heads, 128, 16, "int8", "bf16", seed=3)
+    b.fill_past()
+    codes = [t.clone() for t in (b.k, b.v, b.ks, b.vs)]
+    q = b.append()
+    y, stored = b.attend(q=q).clone(), [t.clone() for t in (b.k, b.v, b.ks, b.vs)]
+    for t, was in zip((b.k, b.v, b.ks, b.vs), codes):
+        t.copy_(was)
+    row, far = (hq + 2 * heads) * 128, (1 << 30) + 64
+    wide = torch.empty(far + row, dtype=b.q.dtype, device="cuda").as_strided((2, hq + 2 * heads, 128), (far, 128, 1))
+    wide.copy_(b.qkv)
+    b.q, b.kn, b.vn = wide[:, :hq], wide[:, hq:hq + heads], wide[:, hq + heads:]
+    assert torch.equal(b.append(q_out=torch.empty_like(q)), q)
+    for t, was in zip((b.ks, b.vs), stored[2:]):
+        assert torch.equal(t.nan_to_num(-1.0), was.nan_to_num(-1.0))
+    assert torch.equal(b.k, stored[0]) and torch.equal(b.v, stored[1])
+    wide[:, :hq] = q
+    assert torch.equal(b.attend(q=wide[:, :hq]), y)
+
+
 def test_long_cache_offsets_past_32_bits():
     """Pages whose byte offset does not fit 32 bits."""
     import kv_util as u

@@ -47,6 +47,18 @@ BATCH_FAULTS = [(dict(n=-1), 1), (dict(T=-1), 1), (dict(n=0), 1), (dict(n=70000)
                 (dict(width=1 << 25, stride=1 << 25), 2)]
 
 
+@pytest.mark.parametrize("call,strides", [(append, ("qs", "ks", "vs")), (attn, ("qs",))], ids=["append", "attn"])
+def test_tokens_far_apart(L, call, strides):
+    """Any distance between tokens is taken whose rows can lie in memory: one token's has no meaning, two may be 2^58
+    elements apart."""
+    for name in strides:
+        for far in ((1 << 30) + 8, 1 << 31, 1 << 40, 1 << 58):
+            assert call(L, cache(), T=0, **{name: far}) == 0, (name, far)
+        assert call(L, cache(), T=2, **{name: (1 << 58) + 8}) == 2, name
+        assert call(L, cache(), T=9, **{name: (1 << 55) + 8}) == 2, name
+        assert call(L, cache(), T=6, **{name: (1 << 62)}) == 2, name
+
+
 @pytest.mark.parametrize("call", [append, attn], ids=["append", "attn"])
 def test_shared_refusals(L, call):
     assert call(L, None) == 1
