@@ -15,6 +15,7 @@ namespace {
 constexpr int kMaxGroup = 64;       // query heads per kv head
 constexpr int kMaxPages = 1 << 28;  // a pool whose lists of pages are counted in 31 bits
 constexpr int kMaxCaches = 1024;    // layers that share a page table
+constexpr int kMaxList = 1 << 30;   // entries of a list that kernels step through with 32-bit numbers
 constexpr int kMaxVocab = 1 << 19;  // 2^19 weights of at most 2^43 stay below 2^63
 
 // bytes from the first element of a strided [T][row] array of 16-bit values to its last
@@ -273,6 +274,7 @@ gdn_status gdn_kv_copy(const gdn_kv_cache* caches, int32_t n_caches, int32_t n, 
     gdn_status st;
     if (n_caches < 0 || n < 0) return fail(GDN_ERR_INVALID_ARG, "negative n_caches or n");
     if (n_caches > kMaxCaches) return fail(GDN_ERR_UNSUPPORTED, "n_caches=%d above %d", n_caches, kMaxCaches);
+    if (n > kMaxList) return fail(GDN_ERR_UNSUPPORTED, "n=%d above 2^30", n);
     if (n_caches > 0 && !caches) return fail(GDN_ERR_INVALID_ARG, "caches is NULL");
     const Buf lists[] = {{copy_from, (size_t)n * 4, "copy_from"}, {copy_to, (size_t)n * 4, "copy_to"}};
     if ((st = check_lists(lists, 2)) != GDN_OK) return st;

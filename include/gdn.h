@@ -563,7 +563,7 @@ GDN_API gdn_status gdn_kv_compact(int32_t n_pages, int32_t max_pages, int32_t n_
  * In:  caches      host array of n_caches caches (up to 1024) with the same heads,
  *                  head_dim, page_tokens, n_pages and format, none overlapping
  *                  another
- *      copy_from, copy_to  int32 [n] (device, 4-byte aligned)
+ *      copy_from, copy_to  int32 [n] (device, 4-byte aligned), n up to 2^30
  */
 GDN_API gdn_status gdn_kv_copy(const gdn_kv_cache* caches, int32_t n_caches, int32_t n, const int32_t* copy_from,
                                const int32_t* copy_to, struct CUstream_st* stream);

@@ -81,6 +81,13 @@ def test_copy_refusals(L):
     assert copy(L, two, n=0, a=None, b=None) == 0
 
 
+def test_lists_past_what_the_kernels_count(L):
+    two = [cache(0), cache(1)]
+    for n in ((1 << 30) + 1, (1 << 31) - 1024, (1 << 31) - 1):
+        assert copy(L, two, n=n) == 2, n
+        assert copy(L, [], n=n) == 2, n
+
+
 def test_workspaces(L):
     assert L.gdn_kv_remap_workspace_bytes(100, 5, 8) > 0 and L.gdn_kv_compact_workspace_bytes(100) >= 400
     for a in ((0, 5, 8), (-1, 5, 8), (100, -1, 8), (100, 5, -1), ((1 << 28) + 1, 5, 8), (100, 1 << 20, 1 << 20)):
