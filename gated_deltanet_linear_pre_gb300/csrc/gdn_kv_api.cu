@@ -192,7 +192,7 @@ size_t words(size_t n) { return align256(n * 4); }
 
 size_t gdn_kv_remap_workspace_bytes(int32_t n_pages, int32_t n_rows, int32_t max_pages)
 {
-    if (n_pages < 1 || n_pages > kMaxPages || n_rows < 0 || max_pages < 0 || (int64_t)n_rows * max_pages > (1 << 30)) return 0;
+    if (n_pages < 1 || n_pages > kMaxPages || n_rows < 0 || n_rows > kMaxList || max_pages < 0 || (int64_t)n_rows * max_pages > (1 << 30)) return 0;
     return words(1) + 2 * words(n_pages) + words(n_rows) + words(gdn::remap_sums(n_pages, n_rows));
 }
 
@@ -205,6 +205,7 @@ gdn_status gdn_kv_remap(int32_t page_tokens, int32_t n_pages, int32_t max_pages,
     if (!known_page(page_tokens)) return fail(GDN_ERR_UNSUPPORTED, "page_tokens must be 16, 32, 64 or 128 (got %d)", page_tokens);
     if ((st = check_pool(n_pages, max_pages)) != GDN_OK) return st;
     if ((int64_t)max_pages * page_tokens > (1 << 30)) return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_tokens above 2^30");
+    if (n_rows > kMaxList) return fail(GDN_ERR_UNSUPPORTED, "n_rows=%d above 2^30", n_rows);
     if ((st = check_table("page_table", n_old, page_table_stride, max_pages)) != GDN_OK) return st;
     if ((st = check_table("table_out", n_rows, table_out_stride, max_pages)) != GDN_OK) return st;
     const size_t rows = (size_t)n_rows * 4, need_ws = gdn_kv_remap_workspace_bytes(n_pages, n_rows, max_pages);

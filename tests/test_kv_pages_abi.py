@@ -86,6 +86,8 @@ def test_lists_past_what_the_kernels_count(L):
     for n in ((1 << 30) + 1, (1 << 31) - 1024, (1 << 31) - 1):
         assert copy(L, two, n=n) == 2, n
         assert copy(L, [], n=n) == 2, n
+        assert L.gdn_kv_remap_workspace_bytes(100, n, 0) == 0, n
+        assert remap(L, n=n, width=0, wb=1 << 40) == 2, n
 
 
 def test_workspaces(L):
