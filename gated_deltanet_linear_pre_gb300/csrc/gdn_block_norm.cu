@@ -199,7 +199,7 @@ cudaError_t launch_typed(const BlockNormParams& p, cudaStream_t stream)
 {
     const int vectors = p.width / 8;
     const auto row_warps = [&](auto kernel) {
-        return launch_k(kernel, dim3((unsigned)((p.T + kRowWarps - 1) / kRowWarps)), dim3(kRowWarps * 32), 0, stream, true, p);
+        return launch_k(kernel, dim3((unsigned)(((int64_t)p.T + kRowWarps - 1) / kRowWarps)), dim3(kRowWarps * 32), 0, stream, true, p);
     };
     const auto row_blocks = [&](auto kernel, int vpt) {
         const int threads = ((vectors + vpt - 1) / vpt + 31) / 32 * 32;

@@ -220,6 +220,22 @@ def test_rows_past_32_bits(gdn):
     close(h[rows], hh, eh)
 
 
+def test_as_many_rows_as_there_can_be(gdn):
+    """2^31 - 1 tokens: four rows a block, whose number is counted past 32 bits on the way."""
+    T, width = (1 << 31) - 1, 8
+    x = torch.zeros((T, width), dtype=torch.bfloat16, device="cuda")
+    h = torch.empty_like(x)
+    rows = [0, 3, (1 << 30) + 1, T - 4, T - 1]
+    for i, r in enumerate(rows):
+        x[r] = torch.arange(width, device="cuda") + i - 3
+    w = torch.linspace(0.5, 2.0, width, device="cuda")
+    gdn.gdn_block_norm(x, None, None, "none", 1.0, None, w, EPS, None, h)
+    at = torch.tensor(rows, device="cuda")
+    _, _, ref, eh = reference(f64(x[at]), None, None, "none", 1.0, None, f64(w))
+    close(h[at], ref, eh)
+    assert not h[T - 1000:T - 4].any() and not h[4:1000].any()
+
+
 @pytest.mark.parametrize("T,width", [(37, 1016), (3000, 2560)])
 def test_another_stream_and_a_graph(gdn, T, width):
     x, y, g, po, pr = inputs(T, width, "bf16", "bf16", "silu", False, True, False)
