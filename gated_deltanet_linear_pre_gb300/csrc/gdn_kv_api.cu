@@ -3,6 +3,7 @@
 // synchronisation.
 #include <algorithm>
 #include <cmath>
+#include <functional>
 
 #include "gdn.h"
 #include "gdn_host.cuh"
@@ -290,7 +291,13 @@ gdn_status gdn_kv_copy(const gdn_kv_cache* caches, int32_t n_caches, int32_t n, 
         const Buf b[] = {{c.k, codes, "cache k"}, {c.v, codes, "cache v"}, {c.k_scale, scales, "k_scale"}, {c.v_scale, scales, "v_scale"}};
         std::copy(b, b + 4, bufs + 4 * i);
     }
-    if ((st = check_disjoint(bufs, n_caches * 4, lists, 2)) != GDN_OK) return st;
+    for (int i = 0; i < n_caches * 4; ++i)
+        for (const Buf& list : lists)
+            if (overlap(bufs[i], list)) return fail(GDN_ERR_INVALID_ARG, "%s overlaps %s", list.name, bufs[i].name);
+    // of buffers in the order of their addresses, if any two overlap then two neighbours do (all pairs of 1024 caches: 19 ms)
+    std::sort(bufs, bufs + n_caches * 4, [](const Buf& a, const Buf& b) { return std::less<const void*>()(a.p, b.p); });
+    for (int i = 0; i + 1 < n_caches * 4; ++i)
+        if (overlap(bufs[i], bufs[i + 1])) return fail(GDN_ERR_INVALID_ARG, "%s overlaps %s", bufs[i].name, bufs[i + 1].name);
     if (n_caches == 0 || n == 0) return GDN_OK;
     gdn::CopyParams p{};
     p.n = n; p.n_pages = caches[0].n_pages; p.heads = caches[0].heads; p.from = copy_from; p.to = copy_to;

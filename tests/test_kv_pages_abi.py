@@ -1,6 +1,8 @@
 """Host-side argument checks of the entries that move pages (no GPU: every call fails before a launch, or has
 nothing to do)."""
 import ctypes
+import random
+import timeit
 
 import pytest
 
@@ -79,6 +81,27 @@ def test_copy_refusals(L):
         assert copy(L, [cache(0), cache(1, **over)]) == status, over
     assert copy(L, []) == 0
     assert copy(L, two, n=0, a=None, b=None) == 0
+
+
+def test_copy_of_many_caches(L):
+    """An overlap is found wherever the two caches stand, and the search takes no time that a call would notice (a
+    comparison of all pairs took 19 ms)."""
+    at = random.Random(0).sample(range(1024), 1024)
+    many = [cache(i) for i in at]
+    lists = dict(a=5000 * F, b=5001 * F)
+    assert copy(L, many, n=0, **lists) == 0
+    best = min(timeit.repeat(lambda: copy(L, many, n=0, **lists), number=1, repeat=7))
+    assert best < 6e-3, best
+    for i, j in ((0, 1023), (1023, 0), (511, 512), (3, 700)):
+        for mine, theirs in (("k", "v"), ("v", "v_scale"), ("k_scale", "k"), ("v_scale", "v_scale")):
+            size, own = (163840 if name in ("k", "v") else 80 for name in (theirs, mine))
+            for off, status in ((0, 1), (16, 1), (-16, 1), (size - 16, 1), (16 - own, 1), (size, 0), (-own, 0)):
+                bad = list(many)
+                bad[i] = cache(at[i], **{mine: getattr(many[j], theirs) + off})
+                assert copy(L, bad, n=0, **lists) == status, (i, j, mine, theirs, off)
+                assert status == 0 or b"overlaps" in L.gdn_last_error_string()
+    assert copy(L, many, a=many[7].v + 64, b=5001 * F) == 1
+    assert copy(L, many, a=5000 * F, b=many[900].k_scale) == 1
 
 
 def test_lists_past_what_the_kernels_count(L):
