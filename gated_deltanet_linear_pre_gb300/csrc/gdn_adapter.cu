@@ -20,16 +20,16 @@
 //
 // Smaller tiles (single tokens, drafts) read weights that nobody shares; what counts
 // for them is the chain from the batch's lengths to the last store.  They take two
-// kernels of their own, without rings or ranges, that run beside the others; a small
-// batch goes that way alone.
+// kernels of their own, without rings or ranges, behind the others'; a small batch goes
+// that way alone.
 //
 // Measured (one GB300; the floor is the bytes that have to move, at a plain copy's rate): 8 prompts of 1 to 4096 tokens,
-// rank 64, 4096 to 6144, fp16 137 us, 78% of the floor's rate (298 in the first form, by mma.sync in tiles of 64 tokens);
-// one token of 64 sequences, rank 16, 4096 to 10240, 9.3 us replayed (floor 2.8); a 3001-token prompt beside 39 drafts,
-// ranks of 8 to 128, 2048 to 10240, 69 us (floor 25; 181 in the first form); 8192 tokens, 2048 to 10240, rank 16 72 us,
-// 64 77, 128 96 (floor 55).  What is left: the start of either kernel (some 5 us: lengths, ranges, the first copies; h), and
-// reads and writes mixed, 5.5 TB/s in adapter_up; where few tokens stand beside a prompt, few_up, which gets the SMs when
-// adapter_up leaves them (its registers are taken; with fewer for either kernel 71 to 81 us for 69).
+// rank 64, 4096 to 6144, fp16 139 us, 77% of the floor's rate (298 in the first form, by mma.sync in tiles of 64 tokens);
+// one token of 64 sequences, rank 16, 4096 to 10240, 8.7 us replayed (floor 2.8); a 3001-token prompt beside 39 drafts,
+// ranks of 8 to 128, 2048 to 10240, 82 us (floor 25; 181 in the first form); 8192 tokens, 2048 to 10240, rank 16 74 us,
+// 64 80, 128 95 (floor 55).  What is left: the start of either kernel (some 5 us: lengths, ranges, the first copies; h), and
+// reads and writes mixed, 5.5 TB/s in adapter_up; where few tokens stand beside a prompt, few_down and few_up, which wait
+// for the kernel in front of them.
 #include <algorithm>
 #include <type_traits>
 
@@ -45,7 +45,7 @@ constexpr int kCopier = kWorkers;                    // the warp that copies
 constexpr int kProduct = kWorkers + 1;               // the warp that issues products
 constexpr int kThreads = (kProduct + 1) * 32;
 // adapter_up has two teams of workers, which take its units in turn: a unit is a chain (product, TMEM, y, y_out).  One team:
-// 8192 tokens, 2048 to 10240, rank 64 88.9 us for 86.0, rank 128 106.1 for 100.5.
+// 8192 tokens, 2048 to 10240, rank 16 75.2 us for 73.6, rank 64 81.9 for 80.2, rank 128 96.3 for 95.3.
 constexpr int kTeams = 2;
 constexpr int kUpWorkers = kWorkers * kTeams;
 constexpr int kUpThreads = (kUpWorkers + 2) * 32;
@@ -59,8 +59,8 @@ constexpr int kPartsOut = 16;                        // ranges of a tile's y at 
 constexpr uint32_t kPolls = 1u << 18;                // of a wait: some two seconds
 constexpr int kColumnD = 256;                        // adapter_up's TMEM: h in the first R columns, products from here on
 
-// Stages leave some L1: 8192 tokens, rank 64, 2048 to 10240, 6 stages 77.4 us, 7 80.4; 255 single tokens beside 1500, rank
-// 128, 5120 to 5120, 4 99.5, 5 105 (8192 tokens 97.8 and 97.2, with 3 106)
+// Stages leave some L1: 8192 tokens, 2048 to 10240, rank 64, 6 stages 80.2 us, 5 81.6, 7 82.6; rank 128, 4 and 5 95.3, 3 102.9;
+// 255 single tokens beside 1500, rank 128, 5120 to 5120, 4 114.1, 5 120.5
 template <int R> constexpr int kStages = R > 64 ? 4 : R > 32 ? 6 : 7;
 template <int R> constexpr int kStageBytes = kTokenBytes + R * kRow;
 constexpr int kResultBytes = 32 * 64;                // a worker's part of a chunk of y_out, on its way out
@@ -342,8 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
     constexpr int kColumns = R * 2 < 32 ? 32 : R * 2;
     unsigned char* ring = smem + ((1024 - (umma::smem_u32(smem) & 1023)) & 1023);
     const uint32_t base = umma::smem_u32(ring);
-    // In this order.  Nobody waits here for another kernel while it holds TMEM that the other has yet to get, and
-    // the kernel behind this one, which starts when all CTAs have come by, may read what earlier launches wrote.
+    // In this order: nobody waits here for another kernel while it holds TMEM that the other has yet to get.
     pdl_wait();
     shared_begin(sm, kColumns, 1, kWorkers);  // a stage is free when its products are done
     pdl_launch_dependents();
@@ -567,8 +566,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) adapter_up_kernel(const __grid_
     unsigned char* ring = smem + ((1024 - (umma::smem_u32(smem) & 1023)) & 1023);
     const uint32_t base = umma::smem_u32(ring);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // all of adapter_down's CTAs have their TMEM, as those of this kernel when the next one starts, and the next one (the
-    // few tokens' second kernel) may read what both first kernels wrote
+    // nobody waits for TMEM that this kernel holds in front of its wait: adapter_down has ended when few_down lets it start
     shared_begin(sm, kColumns, kWorkers + 1, kUpWorkers);  // a stage is free: its team is done with it, the product warp is past it
     pdl_wait();
     pdl_launch_dependents();
@@ -729,32 +727,29 @@ bool encode_maps(Maps& maps, const AdapterParams& p, const uint16_t* tokens, int
 
 // ---- few tokens -------------------------------------------------------------------
 //
-// A block takes 4 tokens of a sequence and some channels, on the CUDA cores, each thread's loads all under way at once,
-// the second kernel's before the first has ended.  Alone (ALONE, a small batch) they take every
-// token, and split x's channels among blocks.  Beside the tensor
-// cores' kernels they take the tiles that those leave, and neither waits for nor holds up the kernel that it runs beside:
-// the order is adapter_down, few_down, adapter_up, few_up; each is there to read what the ones in front of the last
-// wrote, and its first block waits for the last at the end, so that whoever comes next has them all behind it.
+// A block takes 4 tokens of a sequence and some channels, on the CUDA cores, each thread's loads all under way at once.
+// Alone (ALONE, a small batch) they take every token, and split x's channels among blocks.  Beside the tensor
+// cores' kernels they take the tiles that those leave: the order is adapter_down, few_down, adapter_up, few_up, each
+// behind the end of the one before it.  (A few_down beside adapter_down, which did not wait for it, and a few_up that read
+// y, `up` and h in front of its wait took 69 us for 82, a 3001-token prompt beside 39 drafts; but only a grid that waits is
+// promised to see what was written before.  few_down by adapter_down's workers, idle until their first product: 81, and 78
+// for 53 for 128 sequences of 12 tokens, rank 16.)
 constexpr int kFewThreads = 128, kFewTile = 4;
 constexpr int kFewRows = kFewThreads / 16;   // of `down`, two a warp
 constexpr int kFewIn = 1024;                 // x's channels at a time
 constexpr int kFewOut = kFewThreads * 8;
 // Tokens up to which a tile goes this way: the weights are read for every 4 tokens, and the others' kernels copy whole
-// tiles.  128 sequences of 12 tokens, 4096 to 10240: rank 16 54 us, 100 by the others; of 24 97 and 103; rank 64, of 12 135
-// and 110 (replayed).
+// tiles.  128 sequences of 12 tokens, 4096 to 10240: rank 16 53 us, 102 by the others; of 24 96 and 106; rank 64, of 12 134
+// and 114 (replayed).
 int few_tokens(int rank) { return rank <= 16 ? 24 : rank <= 32 ? 16 : 8; }
 
-// A load in front of the kernel's wait (EARLY) comes from L2, as only the wait lets it trust what an SM's L1 holds.
-template <bool EARLY, class V>
-__device__ __forceinline__ V fetch(const V* at) { return EARLY ? __ldcg(at) : __ldg(at); }
-
 // up to kFewTile tokens of one sequence; n 0: an empty slot
-template <bool ALONE, bool EARLY>
+template <bool ALONE>
 __device__ __forceinline__ Piece few_tile(const AdapterParams& p, int slot)
 {
     Piece t{};
     const int slots = p.few / kFewTile;
-    const auto cu = [&](int i) { return min(max(fetch<EARLY>(p.cu_seqlens + i), 0), p.T); };
+    const auto cu = [&](int i) { return cu_at(p.cu_seqlens, i, p.T); };
     int s = slot / slots, end;
     int64_t start;
     if (ALONE) {  // sequence s owns the slots from cu[s] / kFewTile + s on
@@ -770,14 +765,12 @@ __device__ __forceinline__ Piece few_tile(const AdapterParams& p, int slot)
     }
     t.n = (int)max((int64_t)0, min((int64_t)kFewTile, end - start));
     t.start = t.n > 0 ? (int)start : 0;
-    t.id = fetch<EARLY>(p.ids + s);
-    if (t.id < 0 || t.id >= p.n_adapters) t.id = -1;
-    t.rank = t.id < 0 ? 0 : p.ranks ? min(max(fetch<EARLY>(p.ranks + t.id), 0), p.rank) : p.rank;
+    t.rank = rank_of(p, s, t.id);
     return t;
 }
 
 // two rows of `down` with up to NT tokens, channels [k_lo, k_hi)
-template <bool BF16, bool EARLY, int NT>
+template <bool BF16, int NT>
 __device__ __forceinline__ void few_down(const AdapterParams& p, const Piece& t, int j, int k_lo, int k_hi, float* h)
 {
     constexpr int kSteps = kFewIn / 256;
@@ -791,8 +784,8 @@ __device__ __forceinline__ void few_down(const AdapterParams& p, const Piece& t,
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
             if (k0 + i * 256 < k_hi) {
-                a[i][0] = fetch<EARLY>(reinterpret_cast<const uint4*>(w0 + k0 + i * 256));
-                a[i][1] = fetch<EARLY>(reinterpret_cast<const uint4*>(w1 + k0 + i * 256));
+                a[i][0] = __ldg(reinterpret_cast<const uint4*>(w0 + k0 + i * 256));
+                a[i][1] = __ldg(reinterpret_cast<const uint4*>(w1 + k0 + i * 256));
             }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
@@ -803,7 +796,7 @@ __device__ __forceinline__ void few_down(const AdapterParams& p, const Piece& t,
 #pragma unroll
                 for (int q = 0; q < NT; ++q) {
                     float v[8];
-                    widen8<BF16>(fetch<EARLY>(reinterpret_cast<const uint4*>(x + (size_t)min(q, t.n - 1) * p.x_stride + k0 + i * 256)), v);
+                    widen8<BF16>(__ldg(reinterpret_cast<const uint4*>(x + (size_t)min(q, t.n - 1) * p.x_stride + k0 + i * 256)), v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         acc[0][q] = fmaf(f[0][e], v[e], acc[0][q]);
@@ -825,21 +818,19 @@ __device__ __forceinline__ void few_down(const AdapterParams& p, const Piece& t,
 template <bool BF16, bool ALONE>
 __global__ void __launch_bounds__(kFewThreads) few_down_kernel(const __grid_constant__ AdapterParams p)
 {
-    if (ALONE) pdl_wait();
+    pdl_wait();
     pdl_launch_dependents();
-    const bool first = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
-    if (ALONE && first)
+    if (ALONE && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
         for (int i = threadIdx.x; i < 2 * kCtas; i += kFewThreads) p.status[i] = 0;  // nobody waits here
-    const Piece t = few_tile<ALONE, !ALONE>(p, blockIdx.x);
+    const Piece t = few_tile<ALONE>(p, blockIdx.x);
     const int j = blockIdx.y * kFewRows + (threadIdx.x >> 5) * 2;
     if (t.n > 0 && j < t.rank) {
         const int k_lo = ALONE ? blockIdx.z * kFewIn : 0, k_hi = ALONE ? min(p.d_in, k_lo + kFewIn) : p.d_in;
         float* h = p.h + ((size_t)blockIdx.z * p.T + t.start) * p.rank;
-        if (t.n == 1) few_down<BF16, !ALONE, 1>(p, t, j, k_lo, k_hi, h);
-        else if (t.n == 2) few_down<BF16, !ALONE, 2>(p, t, j, k_lo, k_hi, h);
-        else few_down<BF16, !ALONE, 4>(p, t, j, k_lo, k_hi, h);
+        if (t.n == 1) few_down<BF16, 1>(p, t, j, k_lo, k_hi, h);
+        else if (t.n == 2) few_down<BF16, 2>(p, t, j, k_lo, k_hi, h);
+        else few_down<BF16, 4>(p, t, j, k_lo, k_hi, h);
     }
-    if (!ALONE && first) pdl_wait();
 }
 
 template <bool BF16, bool ALONE, int NT>
@@ -857,7 +848,6 @@ __device__ __forceinline__ void few_up(const AdapterParams& p, const Piece& t, i
     for (int q = 0; q < NT; ++q)
         y[q] = mine ? __ldcg(reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + min(q, t.n - 1)) * p.y_stride + o)) : make_uint4(0, 0, 0, 0);
     load(0);
-    if (ALONE) pdl_wait();
     const int splits = ALONE ? (p.d_in + kFewIn - 1) / kFewIn : 1;
     for (int i = threadIdx.x; i < kFewTile * 128; i += kFewThreads) {
         float sum = 0.0f;
@@ -900,22 +890,19 @@ template <bool BF16, bool ALONE>
 __global__ void __launch_bounds__(kFewThreads) few_up_kernel(const __grid_constant__ AdapterParams p)
 {
     __shared__ float h[kFewTile * 128];
+    pdl_wait();
     pdl_launch_dependents();
-    // y, up and the batch were there before the first of the call's kernels began; alone, that one's sums are waited for
-    const Piece t = few_tile<ALONE, true>(p, blockIdx.x);
+    const Piece t = few_tile<ALONE>(p, blockIdx.x);
     const int o = blockIdx.y * kFewOut + threadIdx.x * 8;
     if (t.n > 0 && t.rank > 0) {
         if (t.n == 1) few_up<BF16, ALONE, 1>(p, t, o, h);
         else if (t.n == 2) few_up<BF16, ALONE, 2>(p, t, o, h);
         else few_up<BF16, ALONE, 4>(p, t, o, h);
-    } else {
-        if (ALONE) pdl_wait();
-        if (p.y_out != p.y && o < p.d_out)
-            for (int q = 0; q < t.n; ++q)
-                *reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o) =
-                    __ldcg(reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + q) * p.y_stride + o));
+    } else if (p.y_out != p.y && o < p.d_out) {
+        for (int q = 0; q < t.n; ++q)
+            *reinterpret_cast<uint4*>(p.y_out + (size_t)(t.start + q) * p.out_stride + o) =
+                __ldcg(reinterpret_cast<const uint4*>(p.y + (size_t)(t.start + q) * p.y_stride + o));
     }
-    if (!ALONE && blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
 }
 
 template <bool BF16, bool ALONE>
@@ -933,8 +920,8 @@ cudaError_t launch_few_up(const AdapterParams& p, unsigned slots, cudaStream_t s
 
 // Whether a batch goes this way alone, long sequences too, by the products that it takes: the other kernels cost some 10 us
 // whatever they do, and 2^27 products are about as much.  Replayed, alone and beside, us: 8 single tokens (rank 16, 5120 to
-// 5120) 4.6 and 11; 64 with rank 64 17.4 and 21.7; a prompt of 400 tokens, rank 16, 12.5 and 20.8, of 800 21.6 and 20.1; 128
-// single tokens, rank 64, 28.6 and 28.6; 64 and a chunk of 400, rank 128, 85 and 35; 255 and one of 1500, 292 and 100.
+// 5120) 5.5 and 13.5; 64 with rank 64 17.5 and 20.8; a prompt of 400 tokens, rank 16, 13.0 and 31.5, of 800 21.7 and 21.3; 128
+// single tokens, rank 64, 28.4 and 29.4; 64 and a chunk of 400, rank 128, 84 and 53; 255 and one of 1500, 288 and 114.
 #ifdef GDN_ADAPTER_SELFTEST_NEVER_ALONE
 constexpr int64_t kAloneWork = -1;  // tests: small batches through all kernels
 #else
@@ -960,9 +947,9 @@ cudaError_t launch_rank(const AdapterParams& p, cudaStream_t stream)
     Maps in{}, out{};
     if (!encode_maps(in, p, p.x, p.x_stride, p.down, p.d_in) || !encode_maps(out, p, p.y, p.y_stride, p.up, p.d_out)) return cudaErrorNotSupported;
     const unsigned slots = (unsigned)p.n_seq * (unsigned)(p.few / kFewTile);
-    // adapter_up may start while the kernels in front of it end, but not in a batch of prompts.  Replayed, so and so, us: 8192
-    // tokens, rank 64, 2048 to 10240, 80.0 and 77.3; 4 prompts of 90 to 1200 39.1 and 37.3; 3001 beside 40 drafts of 3 53.5
-    // and 55.5; 255 single tokens beside 1500 66.1 and 67.2.
+    // adapter_up may start while few_down ends, but not in a batch of prompts.  Replayed, so and so, us: 8 prompts of 1 to 4096
+    // tokens, rank 64, 4096 to 6144, 142 and 139; 3001 beside 40 drafts of 3, 2048 to 10240, 65.6 and 67.1; 255 single tokens
+    // beside 1500 76.8 and 77.8.
     const bool early = p.T < (int64_t)kTile * p.n_seq;
     cudaError_t e = cudaFuncSetAttribute(adapter_down_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(adapter_up_kernel<BF16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<R>);
@@ -1002,7 +989,7 @@ cudaError_t launch_adapter(AdapterParams p, void* workspace, cudaStream_t stream
     p.chunks_out = (p.d_out + kK - 1) / kK;
     // Each part of a tile's h takes adapter_up over a microsecond to add, each unit of a range adapter_down half of one:
     // about sqrt(units) / 2 parts are best where there are more CTAs than tiles (one prompt of 3001 tokens, rank 128, 2048
-    // to 10240: 56.6 us, 64.1 with up to 16).
+    // to 10240: 56.1 us, 66.0 with up to 16).
     for (p.parts_in = 2; 4 * p.parts_in * p.parts_in < p.chunks_in; ++p.parts_in) {}
     const auto launch = [&](auto bf16) {
         constexpr bool kBf16 = decltype(bf16)::value;

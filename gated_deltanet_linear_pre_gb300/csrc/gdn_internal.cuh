@@ -271,10 +271,12 @@ void set_last_error(const char* msg);
 
 // ---- programmatic dependent launch ---------------------------------------------
 // Kernels launched with launch_k(..., pdl = true) may start while the previous
-// kernel on the stream is still draining.  Every kernel calls pdl_wait() before
-// its first read of global memory (a no-op when launched without the
-// attribute) and pdl_launch_dependents() early, which lets the next kernel's
-// CTAs be scheduled once every CTA of this one has started.
+// kernel on the stream is still draining.  Every block of every kernel calls
+// pdl_wait() before its first read of global memory (a no-op when launched
+// without the attribute), whoever wrote what it reads: only the grid that waits is
+// promised to see earlier writes.  (scan_chain_kernel takes each chunk by its flag
+// instead, and waits at its end.)  pdl_launch_dependents() comes early, which lets the
+// next kernel's CTAs be scheduled once every CTA of this one has started.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
