@@ -33,6 +33,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "gdn_adapter_index.cuh"
 #include "gdn_kv.cuh"
 #include "gdn_tensor_map.cuh"
 #include "umma.cuh"
@@ -46,10 +47,10 @@ constexpr int kProduct = kWorkers + 1;               // the warp that issues pro
 constexpr int kThreads = (kProduct + 1) * 32;
 // adapter_up has two teams of workers, which take its units in turn: a unit is a chain (product, TMEM, y, y_out).  One team:
 // 8192 tokens, 2048 to 10240, rank 16 75.2 us for 73.6, rank 64 81.9 for 80.2, rank 128 96.3 for 95.3.
-constexpr int kTeams = 2;
+constexpr int kTeams = kAdapterTeams;
 constexpr int kUpWorkers = kWorkers * kTeams;
 constexpr int kUpThreads = (kUpWorkers + 2) * 32;
-constexpr int kTile = 128;                           // tokens
+constexpr int kTile = kAdapterTile;
 constexpr int kK = 64;                               // channels of a unit: rows of 128 bytes in shared memory
 constexpr int kRow = kK * 2;
 constexpr int kCtas = kAdapterCtas;
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
         while (walk.next(p, t)) {
             // the range that a tile begins in has its sums in the tokens' places, every other its own; [rank][tokens],
             // as a warp has a row a lane here and where it reads them (rows of `rank`: 89.9 us for 86.0, 8192 tokens, rank 64)
-            float* h = t.before >= walk.lo ? p.h + (size_t)t.start * p.rank : p.h + ((size_t)p.T + (size_t)blockIdx.x * kTile) * p.rank;
+            float* h = p.h + h_place(p.T, p.rank, blockIdx.x, t.start, t.before >= walk.lo);
             if (tid == 0 && t.c_lo == 0) {
                 const int64_t at_last = t.before + (int64_t)(p.chunks_in - 1) * t.cost;
                 int ends = blockIdx.x;
@@ -457,25 +458,6 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&v)[N])
         umma::tmem_st16(at, v);
 }
 
-// A tile's products take 16 rows of `up` a step.  Where the last step has only 8 rows of its own (the rank rounded up to
-// 8s) it takes the 8 in front of them again, with zeros for their h: rows behind the rank may not be finite.
-struct Steps {
-    int count, last;  // steps; the first row of the last one
-    __device__ explicit Steps(int rank)
-    {
-        const int rows = (rank + 7) & ~7;
-        count = (rows + 15) / 16;
-        last = rows > 8 ? rows - 16 : 0;
-    }
-    __device__ int first_row(int step) const { return step == count - 1 ? last : step * 16; }
-    // the row whose h stands in column j of the operand; -1: none
-    __device__ int row_of(int j) const
-    {
-        if (j < (count - 1) * 16 || last == (count - 1) * 16) return j;
-        return j >= count * 16 ? -1 : j >= count * 16 - 8 ? j - 8 : -1;
-    }
-};
-
 // a load that stays in front of the next one, so that a batch of them is under way at once
 // (else the compiler waits for each: 79 us for 70, a 3001-token prompt of rank 72 beside drafts); 0 where it is not wanted
 __device__ __forceinline__ float load_now(const float* from, bool wanted)
@@ -490,7 +472,7 @@ __device__ __forceinline__ float load_now(const float* from, bool wanted)
 template <bool BF16, int R>
 __device__ __forceinline__ void operand(const AdapterParams& p, const Piece& t, int2 b, Shared& sm)
 {
-    constexpr int kParts = kTeams * 2, kMine = R / kParts, kAtOnce = kMine < 32 ? kMine : 32, kBlock = kMine < 8 ? kMine : 8;
+    constexpr int kParts = kAdapterParts, kMine = R / kParts, kAtOnce = kMine < 32 ? kMine : 32, kBlock = kMine < 8 ? kMine : 8;
     constexpr int kAhead = kMine >= 32 ? 1 : kMine >= 16 ? 2 : 4;  // ranges
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp >> 2, row = (warp & 3) * 32 + lane;
     const int col = part * kMine;
@@ -502,12 +484,13 @@ __device__ __forceinline__ void operand(const AdapterParams& p, const Piece& t, 
         float f[kAhead][kMine];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const float* src = p.h + (r + i == b.x ? (size_t)t.start : (size_t)p.T + (size_t)(r + i) * kTile) * p.rank + row;
+            const float* src = p.h + h_place(p.T, p.rank, r + i, t.start, r + i == b.x) + row;
 #pragma unroll
             for (int j = 0; j < kMine; j += kBlock) {
-                const int at = steps.row_of(col + j), left = row < t.n && r + i <= b.y && at >= 0 ? t.rank - at : 0;
+                const OperandRows rows(steps, t.rank, col + j);
+                const int left = row < t.n && r + i <= b.y ? rows.left : 0;
 #pragma unroll
-                for (int e = 0; e < kBlock; ++e) f[i][j + e] = load_now(src + (at + e) * t.n, e < left);
+                for (int e = 0; e < kBlock; ++e) f[i][j + e] = load_now(src + (rows.at + e) * t.n, e < left);
             }
         }
 #pragma unroll
