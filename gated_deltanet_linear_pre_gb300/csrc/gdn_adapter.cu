@@ -55,7 +55,8 @@ constexpr int kK = 64;                               // channels of a unit: rows
 constexpr int kRow = kK * 2;
 constexpr int kCtas = kAdapterCtas;
 constexpr int kTokenBytes = kTile * kRow;
-constexpr int kRing = 4;                             // chunks' products in TMEM; a multiple of the teams
+constexpr int kRing = 4;                             // slots of chunks' products in TMEM
+static_assert(kRing % kTeams == 0, "a slot is always the same team's");
 constexpr int kPartsOut = 16;                        // ranges of a tile's y at most, less one
 constexpr uint32_t kPolls = 1u << 18;                // of a wait: some two seconds
 constexpr int kColumnD = 256;                        // adapter_up's TMEM: h in the first R columns, products from here on
@@ -231,8 +232,13 @@ __device__ __forceinline__ void find_starts(const AdapterParams& p, PlanSmem& sm
 
 // Every wait is bounded; after one that has expired the rest of the CTA's waits are passed over, no copy or product is
 // begun any more, those under way are waited for, and the CTA records that the call's outputs are invalid.
-// A barrier's parity tells two turns apart, no more.  So whoever waits for a ring's stages waits for all of them, in
-// order, and is among those who free them: nobody falls a turn behind.
+// A barrier's parity tells two turns apart, no more, so nobody may fall a turn behind or run one ahead.  The copier and the
+// product warp wait for every stage, in order; the product warp for every slot of products too.  A worker passes over
+// the other team's units without a wait, and is held by its own: slots go to units in turn and kRing is a multiple of the
+// teams, so a slot is always the same team's; a slot's next product waits for its 8 arrivals (d_empty), and a stage's
+// next copy for those of the team whose unit it held (empty, with the product warp's).  A worker waits for its slot (d_full)
+// before it looks at the stage, which was full before that product began and stays so until the worker's own arrival.
+// adapter_down's workers wait for every tile's slot; its stages are freed by their products.
 struct Shared {
     uint64_t full[8], empty[8];           // stages of the ring
     uint64_t d_full[kRing], d_empty[kRing];
