@@ -118,6 +118,12 @@ def test_widths(gdn, d_in, d_out, dt, lengths):
     c.check(c.run(gdn))
 
 
+@pytest.mark.parametrize("d_in,d_out,rank", [(65536, 72, 16), (72, 65536, 128), (65528, 65536, 8)])
+def test_the_widest(gdn, d_in, d_out, rank):
+    c = Case([40, 3, 200], [0, 1, 0], 2, rank, d_in, d_out, "bf16", seed=rank)
+    c.check(c.run(gdn))
+
+
 @pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 127, 129, 300])
 def test_one_sequence(gdn, n):
     for rank in (16, 64):
