@@ -81,7 +81,8 @@ __device__ __forceinline__ uint32_t place(int row, int piece) { return row * kRo
 // ---- who does what --------------------------------------------------------------
 
 // What a unit costs, in steps of some 2 ns: rows of 128 bytes copied and written, fitted to the time that a CTA took for
-// ranges of one kind (8 prompts with rank 64, one with rank 72).  A tile copies the rows of a whole one.
+// ranges of one kind (8 prompts with rank 64, one with rank 72), with one team of workers; not fitted again since there are
+// two.  A tile copies the rows of a whole one.
 __device__ __forceinline__ int cost_in(int rank) { return rank > 0 ? 144 + rank : 0; }
 __device__ __forceinline__ int cost_out(int rank, bool copied) { return rank > 0 ? 160 + 2 * rank : copied ? 192 : 0; }
 
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
         uint32_t tiles = 0;
         while (walk.next(p, t)) {
             // the range that a tile begins in has its sums in the tokens' places, every other its own; [rank][tokens],
-            // as a warp has a row a lane here and where it reads them (rows of `rank`: 89.9 us for 86.0, 8192 tokens, rank 64)
+            // as a warp has a row a lane here and where it reads them (rows of `rank`, when there was one team: 89.9 us for 86.0, 8192 tokens, rank 64)
             float* h = p.h + h_place(p.T, p.rank, blockIdx.x, t.start, t.before >= walk.lo);
             if (tid == 0 && t.c_lo == 0) {
                 const int64_t at_last = t.before + (int64_t)(p.chunks_in - 1) * t.cost;

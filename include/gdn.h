@@ -629,9 +629,12 @@ GDN_API gdn_status gdn_block_norm(int32_t x_dtype, int32_t dtype, int32_t total_
  *              the same stride, else overlaps no input
  * rank: a multiple of 8 up to 128; d_in, d_out: multiples of 8 up to 65536;
  * n_adapters up to 2^20.  ids, ranks and scales need 4-byte alignment only.
- * Sums are fp32; h enters its product in fp32 or in two pieces of the weights'
- * type (16 bits or more), and y_out is rounded once.  Values of x and of the weights that are not finite reach the
- * tokens, and the channels, that their products reach.
+ * Sums are fp32, and y_out is rounded once.  h enters its product in fp32, or, in
+ * tiles of many tokens, in two pieces of the weights' type: 17 bits or more in
+ * bf16; 22 in fp16, or 2^-39 of the token's largest.  So the last bits in fp32 of
+ * what is added may differ with the batch that a token comes in.  Values of x and
+ * of the weights that are not finite reach the tokens, and the channels, that
+ * their products reach (an infinity in `up` as infinity or NaN).
  * workspace: device scratch of at least gdn_adapter_workspace_bytes() bytes (0
  * for a shape that is refused, and for no tokens); contents on entry are
  * ignored, calls sharing one must not overlap on the GPU.  May be captured into
