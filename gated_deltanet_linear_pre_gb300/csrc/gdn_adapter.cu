@@ -24,7 +24,7 @@
 // that way alone.
 //
 // Measured (one GB300; the floor is the bytes that have to move, at a plain copy's rate): 8 prompts of 1 to 4096 tokens,
-// rank 64, 4096 to 6144, fp16 139 us, 77% of the floor's rate (298 in the first form, by mma.sync in tiles of 64 tokens);
+// rank 64, 4096 to 6144, fp16 137 us, 78% of the floor's rate (298 in the first form, by mma.sync in tiles of 64 tokens);
 // one token of 64 sequences, rank 16, 4096 to 10240, 8.7 us replayed (floor 2.8); a 3001-token prompt beside 39 drafts,
 // ranks of 8 to 128, 2048 to 10240, 82 us (floor 25; 181 in the first form); 8192 tokens, 2048 to 10240, rank 16 74 us,
 // 64 80, 128 95 (floor 55).  What is left: the start of either kernel (some 5 us: lengths, ranges, the first copies; h), and
@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) adapter_down_kernel(const __grid_
         uint32_t tiles = 0;
         while (walk.next(p, t)) {
             // the range that a tile begins in has its sums in the tokens' places, every other its own; [rank][tokens],
-            // as a warp has a row a lane here and where it reads them (rows of `rank`, when there was one team: 89.9 us for 86.0, 8192 tokens, rank 64)
+            // as a warp has a row a lane here and where it reads them (rows of `rank`, when there was one team: 89.9 us for
+            // 86.0, 8192 tokens, rank 64)
             float* h = p.h + h_place(p.T, p.rank, blockIdx.x, t.start, t.before >= walk.lo);
             if (tid == 0 && t.c_lo == 0) {
                 const int64_t at_last = t.before + (int64_t)(p.chunks_in - 1) * t.cost;

@@ -521,7 +521,8 @@ GDN_API gdn_status gdn_draft_verify(int32_t n_seq, int32_t max_draft, int32_t vo
  * max_pages, max_pages * page_tokens and the tables' strides up to 2^30.  The
  * int32 arrays need 4-byte alignment only.  workspace: at least
  * gdn_kv_remap_workspace_bytes() bytes (0 for a shape that is refused); contents
- * on entry are ignored, calls sharing one must not overlap on the GPU.  May be captured into a CUDA graph.
+ * on entry are ignored, calls sharing one must not overlap on the GPU.  May be
+ * captured into a CUDA graph.
  */
 GDN_API size_t gdn_kv_remap_workspace_bytes(int32_t n_pages, int32_t n_rows, int32_t max_pages);
 GDN_API gdn_status gdn_kv_remap(int32_t page_tokens, int32_t n_pages, int32_t max_pages, int32_t n_old,
